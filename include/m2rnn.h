@@ -307,6 +307,136 @@ int m2rnn_decode_step(float* H, const void* q, const void* k, const void* v,
                       int64_t V, m2rnn_dtype dtype, void* workspace,
                       size_t workspace_bytes, void* cuda_stream);
 
+/* ---------------------------------------------------------------------------
+ * The layer around the scans: the short causal convolution that makes q, k, v
+ * from their projections, a selective state space scan on the same matrix
+ * state for hybrid models, and the global gradient norm of a training step.
+ *
+ * Activations (y, and their upstream gradients where noted) have the element
+ * type `dtype`, as the next layer takes them; states of the scan and every
+ * gradient returned are fp32.  x, q, k, v, dt may be column slices of a wider
+ * row-major tensor: rows (tokens) lie `*_stride` elements apart, sequences
+ * T rows apart, and those pointers need the alignment of an element only
+ * (rows on 16-byte boundaries take the vector path).  `lengths` [B] int32
+ * (NULL = all T) cuts each sequence to its first lengths[b] steps, clamped to
+ * [0, T]: steps behind it are not read, their outputs and gradients are 0, and
+ * the final state is the one at lengths[b].  None of these calls uses a
+ * status block.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Short causal depthwise convolution (reading notes, section 2.3; Eq. 14-23:
+ * width 4 with SiLU).  With xs = [x0 | x] along time:
+ *     pre_t = bias + sum_w w[:, w] xs[t + w],   y_t = silu(pre_t) or pre_t.
+ *   x [B,T,C] (rows x_stride apart); w [C,W]; bias [C] (may be NULL);
+ *   x0 [B,W-1,C] (may be NULL = zero): the W - 1 inputs before the sequence;
+ *   y [B,T,C]; x_T [B,W-1,C] (may be NULL): the last W - 1 inputs, which are
+ *   the x0 of the sequence's next piece and the state of
+ *   m2rnn_causal_conv_step.  All in `dtype`.  1 <= W <= 8.  y, x_T must not
+ *   overlap x, x0 (M2RNN_ERR_INVALID_ARG).  silu: 1, or 0 for none.
+ */
+int m2rnn_causal_conv(const void* x, int64_t x_stride, const void* w, const void* bias, const void* x0,
+                      const int32_t* lengths, void* y, void* x_T, int64_t B, int64_t T, int64_t C, int64_t W,
+                      int silu, m2rnn_dtype dtype, void* cuda_stream);
+
+/* Bytes of device workspace m2rnn_causal_conv_backward needs, 0 for an
+ * unsupported shape. */
+size_t m2rnn_causal_conv_backward_workspace_size(int64_t B, int64_t T, int64_t C, int64_t W);
+
+/*
+ * Backward of m2rnn_causal_conv.  dy [B,T,C] fp32 (the scans' dq, dk, dv are
+ * fp32); dx_T [B,W-1,C] fp32 (may be NULL): gradient of x_T;  out, all fp32:
+ * dx [B,T,C], dw [C,W], db [C] (may be NULL), dx0 [B,W-1,C] (may be NULL).
+ * dw and db are summed over b and t in a fixed order.
+ */
+int m2rnn_causal_conv_backward(const void* x, int64_t x_stride, const void* w, const void* bias, const void* x0,
+                               const int32_t* lengths, const float* dy, const float* dx_T, float* dx, float* dw,
+                               float* db, float* dx0, int64_t B, int64_t T, int64_t C, int64_t W, int silu,
+                               m2rnn_dtype dtype, void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/* One token: state [B,W-1,C] (the last W - 1 inputs) is shifted in place and
+ * takes x [B,C] (rows x_stride apart) in; y [B,C]. */
+int m2rnn_causal_conv_step(void* state, const void* x, int64_t x_stride, const void* w, const void* bias, void* y,
+                           int64_t B, int64_t C, int64_t W, int silu, m2rnn_dtype dtype, void* cuda_stream);
+
+/*
+ * Selective state space scan (no counterpart in the paper; its hybrid models
+ * mix the recurrence with linear layers of this form), per batch element and
+ * head, from H_0:
+ *     D_t = softplus(dt_t + dt_bias),  a_t = exp(D_t A)
+ *     H_t = a_t H_{t-1} + D_t k_t v_t^T
+ *     y_t = H_t^T q_t + w_r (*) v_t
+ *   q, k [B,T,G,K], v [B,T,N,V], dt [B,T,N], w_r [N,V] (may be NULL) in
+ *   `dtype`; value head n reads q, k of head n / (N / G), G divides N;
+ *   A [N] fp32 (negative for a decaying state); dt_bias [N] fp32 (may be
+ *   NULL); H_0 [B,N,K,V] fp32 (may be NULL = zero); K, V in [1, 128].
+ *   out: y [B,T,N,V] in `dtype`; H_T [B,N,K,V] fp32 (may be NULL; may be H_0).
+ * A step whose v is not finite may also leave non-finite y at earlier steps
+ * of the same 64-step chunk.
+ */
+size_t m2rnn_ssm_workspace_size(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V,
+                                m2rnn_dtype dtype);
+int m2rnn_ssm_scan(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                   int64_t v_stride, const void* dt, int64_t dt_stride, const float* A, const float* dt_bias,
+                   const void* w_r, const float* H_0, const int32_t* lengths, void* y, float* H_T, int64_t B,
+                   int64_t T, int64_t N, int64_t G, int64_t K, int64_t V, m2rnn_dtype dtype, void* workspace,
+                   size_t workspace_bytes, void* cuda_stream);
+
+/*
+ * Backward of m2rnn_ssm_scan for L = sum(dy * y) + <dH_T, H_T>.
+ *   dy [B,T,N,V] in `dtype`; dH_T [B,N,K,V] fp32 (may be NULL = zero).
+ *   out, all fp32: dq, dk [B,T,G,K] (summed over the heads that share them),
+ *   dv [B,T,N,V], ddt [B,T,N], dA [N], ddt_bias [N] (may be NULL), dw_r [N,V]
+ *   (may be NULL), dH_0 [B,N,K,V] (may be NULL; may be dH_T).
+ * Sums in a fixed order: results are bitwise reproducible.
+ */
+size_t m2rnn_ssm_backward_workspace_size(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V,
+                                         m2rnn_dtype dtype);
+int m2rnn_ssm_scan_backward(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                            int64_t v_stride, const void* dt, int64_t dt_stride, const float* A,
+                            const float* dt_bias, const void* w_r, const float* H_0, const int32_t* lengths,
+                            const void* dy, const float* dH_T, float* dq, float* dk, float* dv, float* ddt,
+                            float* dA, float* ddt_bias, float* dw_r, float* dH_0, int64_t B, int64_t T,
+                            int64_t N, int64_t G, int64_t K, int64_t V, m2rnn_dtype dtype, void* workspace,
+                            size_t workspace_bytes, void* cuda_stream);
+
+/* One token: H [B,N,K,V] fp32 advances in place; q, k [B,G,K], v, y [B,N,V],
+ * dt [B,N]; strides lie between sequences.  No workspace. */
+int m2rnn_ssm_step(float* H, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                   int64_t v_stride, const void* dt, int64_t dt_stride, const float* A, const float* dt_bias,
+                   const void* w_r, void* y, int64_t B, int64_t N, int64_t G, int64_t K, int64_t V,
+                   m2rnn_dtype dtype, void* cuda_stream);
+
+/*
+ * Global gradient norm and clipping (reading notes, section 2.3: the recipe
+ * clips the whole model's gradient at 1) over any number of tensors:
+ *     norm = sqrt(sum over all tensors of x^2)
+ *     out  = x min(1, max_norm / (norm + 1e-6)), rounded to the tensor's type.
+ * A NaN anywhere makes the norm and every output NaN; an infinity makes the
+ * norm infinite and the factor 0.  The norm is right over the whole fp32
+ * range (squares that leave it are summed in fp64).
+ *
+ * A plan lists the tensors.  m2rnn_grad_plan_build fills `plan` (HOST memory,
+ * m2rnn_grad_plan_size bytes) from n device pointers, element counts and
+ * dtypes (host arrays); outs[i] may be grads[i] (clipped in place), outs may
+ * be NULL (a plan for m2rnn_grad_norm, or in place); outputs must not overlap
+ * other tensors.  The caller copies it to the device and keeps it while the
+ * tensors stay where they are.  Tensors need the alignment of an element; a
+ * count of 0 is allowed.  The size is 0 on bad arguments, else a multiple of
+ * 32 and at least 32.
+ */
+size_t m2rnn_grad_plan_size(int64_t n, const int64_t* counts);
+int m2rnn_grad_plan_build(int64_t n, const void* const* grads, void* const* outs, const int64_t* counts,
+                          const int32_t* dtypes, void* plan, size_t plan_bytes);
+/* plan: the DEVICE copy; norm: one fp32 on the device; max_norm > 0 (NaN and
+ * negative values are M2RNN_ERR_INVALID_ARG); workspace:
+ * m2rnn_grad_workspace_size() bytes. */
+size_t m2rnn_grad_workspace_size(void);
+int m2rnn_grad_norm(const void* plan, size_t plan_bytes, float* norm, void* workspace, size_t workspace_bytes,
+                    void* cuda_stream);
+int m2rnn_grad_clip(const void* plan, size_t plan_bytes, float max_norm, float* norm, void* workspace,
+                    size_t workspace_bytes, void* cuda_stream);
+
 /*
  * Synchronises `cuda_stream`, then reads and clears the workspace status
  * block that the last call on this workspace wrote.  Returns M2RNN_OK,

@@ -39,6 +39,11 @@ EXPORTS = (
     "m2rnn_backward_gated", "m2rnn_output_norm", "m2rnn_output_norm_backward_workspace_size",
     "m2rnn_output_norm_backward", "m2rnn_z_stash_size", "m2rnn_set_option",
     "m2rnn_backward_noalloc", "m2rnn_backward_noalloc_status",
+    "m2rnn_causal_conv", "m2rnn_causal_conv_backward_workspace_size", "m2rnn_causal_conv_backward",
+    "m2rnn_causal_conv_step", "m2rnn_ssm_workspace_size", "m2rnn_ssm_scan",
+    "m2rnn_ssm_backward_workspace_size", "m2rnn_ssm_scan_backward", "m2rnn_ssm_step",
+    "m2rnn_grad_plan_size", "m2rnn_grad_plan_build", "m2rnn_grad_workspace_size", "m2rnn_grad_norm",
+    "m2rnn_grad_clip",
 )
 
 _lib = None
@@ -102,6 +107,35 @@ def load() -> ctypes.CDLL:
     lib.m2rnn_output_norm_backward_workspace_size.argtypes = [i64] * 4
     lib.m2rnn_output_norm_backward.restype = ci
     lib.m2rnn_output_norm_backward.argtypes = [vp] * 4 + [fl] + [vp] * 3 + [i64] * 4 + [ci, vp, sz, vp]
+    lib.m2rnn_causal_conv.restype = ci
+    lib.m2rnn_causal_conv.argtypes = [vp, i64] + [vp] * 6 + [i64] * 4 + [ci, ci, vp]
+    lib.m2rnn_causal_conv_backward_workspace_size.restype = sz
+    lib.m2rnn_causal_conv_backward_workspace_size.argtypes = [i64] * 4
+    lib.m2rnn_causal_conv_backward.restype = ci
+    lib.m2rnn_causal_conv_backward.argtypes = [vp, i64] + [vp] * 10 + [i64] * 4 + [ci, ci, vp, sz, vp]
+    lib.m2rnn_causal_conv_step.restype = ci
+    lib.m2rnn_causal_conv_step.argtypes = [vp, vp, i64] + [vp] * 3 + [i64] * 3 + [ci, ci, vp]
+    rows = [vp, i64] * 4
+    lib.m2rnn_ssm_workspace_size.restype = sz
+    lib.m2rnn_ssm_workspace_size.argtypes = [i64] * 6 + [ci]
+    lib.m2rnn_ssm_scan.restype = ci
+    lib.m2rnn_ssm_scan.argtypes = rows + [vp] * 7 + [i64] * 6 + [ci, vp, sz, vp]
+    lib.m2rnn_ssm_backward_workspace_size.restype = sz
+    lib.m2rnn_ssm_backward_workspace_size.argtypes = [i64] * 6 + [ci]
+    lib.m2rnn_ssm_scan_backward.restype = ci
+    lib.m2rnn_ssm_scan_backward.argtypes = rows + [vp] * 15 + [i64] * 6 + [ci, vp, sz, vp]
+    lib.m2rnn_ssm_step.restype = ci
+    lib.m2rnn_ssm_step.argtypes = [vp] + rows + [vp] * 4 + [i64] * 5 + [ci, vp]
+    lib.m2rnn_grad_plan_size.restype = sz
+    lib.m2rnn_grad_plan_size.argtypes = [i64, vp]
+    lib.m2rnn_grad_plan_build.restype = ci
+    lib.m2rnn_grad_plan_build.argtypes = [i64] + [vp] * 5 + [sz]
+    lib.m2rnn_grad_workspace_size.restype = sz
+    lib.m2rnn_grad_workspace_size.argtypes = []
+    lib.m2rnn_grad_norm.restype = ci
+    lib.m2rnn_grad_norm.argtypes = [vp, sz, vp, vp, sz, vp]
+    lib.m2rnn_grad_clip.restype = ci
+    lib.m2rnn_grad_clip.argtypes = [vp, sz, fl, vp, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -508,3 +542,331 @@ def m2rnn_backward_noalloc_status(stream):
     detail = ctypes.c_uint32(0)
     st = fn(stream, ctypes.byref(detail))
     return st, detail.value
+
+
+# ---------------------------------------------------------------------------
+# The hybrid layer: short causal convolution, selective state space scan,
+# gradient clipping (raw wrappers, then torch conveniences)
+# ---------------------------------------------------------------------------
+def m2rnn_causal_conv(*args) -> int:
+    return load().m2rnn_causal_conv(*args)
+
+
+def m2rnn_causal_conv_backward_workspace_size(B, T, C, W) -> int:
+    return load().m2rnn_causal_conv_backward_workspace_size(B, T, C, W)
+
+
+def m2rnn_causal_conv_backward(*args) -> int:
+    return load().m2rnn_causal_conv_backward(*args)
+
+
+def m2rnn_causal_conv_step(*args) -> int:
+    return load().m2rnn_causal_conv_step(*args)
+
+
+def m2rnn_ssm_workspace_size(B, T, N, G, K, V, dtype) -> int:
+    return load().m2rnn_ssm_workspace_size(B, T, N, G, K, V, dtype)
+
+
+def m2rnn_ssm_scan(*args) -> int:
+    return load().m2rnn_ssm_scan(*args)
+
+
+def m2rnn_ssm_backward_workspace_size(B, T, N, G, K, V, dtype) -> int:
+    return load().m2rnn_ssm_backward_workspace_size(B, T, N, G, K, V, dtype)
+
+
+def m2rnn_ssm_scan_backward(*args) -> int:
+    return load().m2rnn_ssm_scan_backward(*args)
+
+
+def m2rnn_ssm_step(*args) -> int:
+    return load().m2rnn_ssm_step(*args)
+
+
+def m2rnn_grad_plan_size(n, counts) -> int:
+    return load().m2rnn_grad_plan_size(n, counts)
+
+
+def m2rnn_grad_plan_build(n, grads, outs, counts, dtypes, plan, plan_bytes) -> int:
+    return load().m2rnn_grad_plan_build(n, grads, outs, counts, dtypes, plan, plan_bytes)
+
+
+def m2rnn_grad_workspace_size() -> int:
+    return load().m2rnn_grad_workspace_size()
+
+
+def m2rnn_grad_norm(plan, plan_bytes, norm, workspace, workspace_bytes, stream) -> int:
+    return load().m2rnn_grad_norm(plan, plan_bytes, norm, workspace, workspace_bytes, stream)
+
+
+def m2rnn_grad_clip(plan, plan_bytes, max_norm, norm, workspace, workspace_bytes, stream) -> int:
+    return load().m2rnn_grad_clip(plan, plan_bytes, max_norm, norm, workspace, workspace_bytes, stream)
+
+
+def _need(t, name: str, shape, dtype, device):
+    """Address of an optional dense operand (None for None), checked."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous on {device}")
+    return t.data_ptr()
+
+
+def _rows(t, name: str, shape, inner: int, dtype, device):
+    """Address and row stride of an input that may be a column slice of a
+    wider tensor: its last ``inner`` dimensions (one token's values) dense,
+    the tokens of [B,T,...] evenly spaced through all sequences."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    width, stride, n = 1, t.stride(), len(shape) - inner
+    for i in range(len(shape) - 1, n - 1, -1):
+        if shape[i] != 1 and stride[i] != width:
+            raise ValueError(f"{name}: the values of one token must be dense")
+        width *= shape[i]
+    if n == 2 and shape[1] > 1:
+        if shape[0] > 1 and stride[0] != shape[1] * stride[1]:
+            raise ValueError(f"{name}: sequences must lie T rows apart")
+        return t.data_ptr(), stride[1]
+    return t.data_ptr(), stride[0] if shape[0] > 1 else width
+
+
+def _alloc(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream it is used on."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out(out, name, shape, dtype, device, stream):
+    t = out.get(name) if out else None
+    if t is None:
+        return _alloc(shape, dtype, device, stream)
+    _need(t, name, shape, dtype, device)
+    return t
+
+
+def _scratch(workspace, nbytes: int, device, stream, what: str):
+    import torch
+    if nbytes == 0:
+        raise M2RNNError(M2RNN_ERR_UNSUPPORTED, what)
+    if workspace is None or workspace.numel() < nbytes:
+        workspace = _alloc((nbytes,), torch.uint8, device, stream)
+    return workspace
+
+
+def causal_conv(x, w, bias=None, *, x0=None, lengths=None, silu: bool = True, want_state: bool = False,
+                out=None, stream=None):
+    """Short causal depthwise convolution, with SiLU.  ``x`` [B,T,C] (may be a
+    column slice of a wider projection), ``w`` [C,W], ``bias`` [C], ``x0``
+    [B,W-1,C] the inputs before the sequence (None = zero), ``lengths`` [B]
+    int32.  Returns dict(y[, x_T]); x_T [B,W-1,C] continues the sequence, as
+    ``x0`` of the next piece or as the state of ``causal_conv_step``.  ``out``
+    may hold preallocated y / x_T."""
+    import torch
+    B, T, C = x.shape
+    W, dev, dt = w.shape[1], x.device, x.dtype
+    code = _dtype_code(x)
+    xp, xs = _rows(x, "x", (B, T, C), 1, dt, dev)
+    y = _out(out, "y", (B, T, C), dt, dev, stream)
+    x_T = _out(out, "x_T", (B, W - 1, C), dt, dev, stream) if want_state or (out and "x_T" in out) else None
+    st = load().m2rnn_causal_conv(xp, xs, _need(w, "w", (C, W), dt, dev), _need(bias, "bias", (C,), dt, dev),
+                                  _need(x0, "x0", (B, W - 1, C), dt, dev),
+                                  _need(lengths, "lengths", (B,), torch.int32, dev), y.data_ptr(), _ptr(x_T), B, T, C,
+                                  W, int(silu), code, _stream_handle(stream))
+    _check(st, "m2rnn_causal_conv")
+    return dict(y=y) if x_T is None else dict(y=y, x_T=x_T)
+
+
+def causal_conv_backward(x, w, bias, dy, *, x0=None, dx_T=None, lengths=None, silu: bool = True,
+                         want_dx0: bool = False, out=None, workspace=None, stream=None):
+    """Backward of ``causal_conv``: ``dy`` [B,T,C] and ``dx_T`` [B,W-1,C] fp32.
+    Returns dict(dx, dw[, db][, dx0]), fp32 (db when there is a bias)."""
+    import torch
+    B, T, C = x.shape
+    W, dev, dt, f32 = w.shape[1], x.device, x.dtype, torch.float32
+    code = _dtype_code(x)
+    xp, xs = _rows(x, "x", (B, T, C), 1, dt, dev)
+    res = dict(dx=_out(out, "dx", (B, T, C), f32, dev, stream), dw=_out(out, "dw", (C, W), f32, dev, stream))
+    if bias is not None:
+        res["db"] = _out(out, "db", (C,), f32, dev, stream)
+    if want_dx0:
+        res["dx0"] = _out(out, "dx0", (B, W - 1, C), f32, dev, stream)
+    ws = _scratch(workspace, m2rnn_causal_conv_backward_workspace_size(B, T, C, W), dev, stream,
+                  "m2rnn_causal_conv_backward_workspace_size")
+    st = load().m2rnn_causal_conv_backward(
+        xp, xs, _need(w, "w", (C, W), dt, dev), _need(bias, "bias", (C,), dt, dev),
+        _need(x0, "x0", (B, W - 1, C), dt, dev), _need(lengths, "lengths", (B,), torch.int32, dev),
+        _need(dy, "dy", (B, T, C), f32, dev), _need(dx_T, "dx_T", (B, W - 1, C), f32, dev), res["dx"].data_ptr(),
+        res["dw"].data_ptr(), _ptr(res.get("db")), _ptr(res.get("dx0")), B, T, C, W, int(silu), code, ws.data_ptr(),
+        ws.numel(), _stream_handle(stream))
+    _check(st, "m2rnn_causal_conv_backward")
+    return res
+
+
+def causal_conv_step(state, x, w, bias=None, *, silu: bool = True, y=None, stream=None):
+    """One token: ``state`` [B,W-1,C] is shifted in place and takes ``x`` [B,C]
+    in.  Returns y [B,C]."""
+    B, C = x.shape
+    W, dev, dt = w.shape[1], x.device, x.dtype
+    code = _dtype_code(x)
+    xp, xs = _rows(x, "x", (B, C), 1, dt, dev)
+    if y is None:
+        y = _alloc((B, C), dt, dev, stream)
+    st = load().m2rnn_causal_conv_step(_need(state, "state", (B, W - 1, C), dt, dev), xp, xs,
+                                       _need(w, "w", (C, W), dt, dev), _need(bias, "bias", (C,), dt, dev),
+                                       _need(y, "y", (B, C), dt, dev), B, C, W, int(silu), code,
+                                       _stream_handle(stream))
+    _check(st, "m2rnn_causal_conv_step")
+    return y
+
+
+def ssm_scan(q, k, v, dt, A, *, dt_bias=None, w_r=None, H_0=None, lengths=None, want_state: bool = True, out=None,
+             workspace=None, stream=None):
+    """Selective state space scan (see m2rnn_ssm_scan): q, k [B,T,G,K], v
+    [B,T,N,V], dt [B,T,N] (column slices of wider tensors are fine), A [N]
+    fp32, dt_bias [N] fp32, w_r [N,V], H_0 [B,N,K,V] fp32, lengths [B] int32.
+    Returns dict(y, H_T, workspace): y in the inputs' type, H_T fp32."""
+    import torch
+    B, T, G, K = q.shape
+    N, V = v.shape[2:]
+    dev, ty, f32 = v.device, v.dtype, torch.float32
+    code = _dtype_code(v)
+    qp, qs = _rows(q, "q", (B, T, G, K), 2, ty, dev)
+    kp, ks = _rows(k, "k", (B, T, G, K), 2, ty, dev)
+    vp, vs = _rows(v, "v", (B, T, N, V), 2, ty, dev)
+    dp, ds = _rows(dt, "dt", (B, T, N), 1, ty, dev)
+    y = _out(out, "y", (B, T, N, V), ty, dev, stream)
+    H_T = _out(out, "H_T", (B, N, K, V), f32, dev, stream) if want_state else None
+    ws = _scratch(workspace, m2rnn_ssm_workspace_size(B, T, N, G, K, V, code), dev, stream,
+                  "m2rnn_ssm_workspace_size")
+    st = load().m2rnn_ssm_scan(qp, qs, kp, ks, vp, vs, dp, ds, _need(A, "A", (N,), f32, dev),
+                               _need(dt_bias, "dt_bias", (N,), f32, dev), _need(w_r, "w_r", (N, V), ty, dev),
+                               _need(H_0, "H_0", (B, N, K, V), f32, dev),
+                               _need(lengths, "lengths", (B,), torch.int32, dev), y.data_ptr(), _ptr(H_T), B, T, N, G,
+                               K, V, code, ws.data_ptr(), ws.numel(), _stream_handle(stream))
+    _check(st, "m2rnn_ssm_scan")
+    return dict(y=y, H_T=H_T, workspace=ws)
+
+
+def ssm_scan_backward(q, k, v, dt, A, dy, *, dt_bias=None, w_r=None, H_0=None, dH_T=None, lengths=None,
+                      want_dH0: bool = False, out=None, workspace=None, stream=None):
+    """Backward of ``ssm_scan``: ``dy`` [B,T,N,V] in the inputs' type, ``dH_T``
+    [B,N,K,V] fp32.  Returns dict(dq, dk, dv, ddt, dA[, ddt_bias][, dw_r]
+    [, dH_0], workspace), all fp32."""
+    import torch
+    B, T, G, K = q.shape
+    N, V = v.shape[2:]
+    dev, ty, f32 = v.device, v.dtype, torch.float32
+    code = _dtype_code(v)
+    qp, qs = _rows(q, "q", (B, T, G, K), 2, ty, dev)
+    kp, ks = _rows(k, "k", (B, T, G, K), 2, ty, dev)
+    vp, vs = _rows(v, "v", (B, T, N, V), 2, ty, dev)
+    dp, ds = _rows(dt, "dt", (B, T, N), 1, ty, dev)
+    shapes = dict(dq=(B, T, G, K), dk=(B, T, G, K), dv=(B, T, N, V), ddt=(B, T, N), dA=(N,))
+    if dt_bias is not None:
+        shapes["ddt_bias"] = (N,)
+    if w_r is not None:
+        shapes["dw_r"] = (N, V)
+    if want_dH0:
+        shapes["dH_0"] = (B, N, K, V)
+    res = {n: _out(out, n, sh, f32, dev, stream) for n, sh in shapes.items()}
+    ws = _scratch(workspace, m2rnn_ssm_backward_workspace_size(B, T, N, G, K, V, code), dev, stream,
+                  "m2rnn_ssm_backward_workspace_size")
+    st = load().m2rnn_ssm_scan_backward(
+        qp, qs, kp, ks, vp, vs, dp, ds, _need(A, "A", (N,), f32, dev), _need(dt_bias, "dt_bias", (N,), f32, dev),
+        _need(w_r, "w_r", (N, V), ty, dev), _need(H_0, "H_0", (B, N, K, V), f32, dev),
+        _need(lengths, "lengths", (B,), torch.int32, dev), _need(dy, "dy", (B, T, N, V), ty, dev),
+        _need(dH_T, "dH_T", (B, N, K, V), f32, dev),
+        *(_ptr(res.get(n)) for n in ("dq", "dk", "dv", "ddt", "dA", "ddt_bias", "dw_r", "dH_0")), B, T, N, G, K, V,
+        code, ws.data_ptr(), ws.numel(), _stream_handle(stream))
+    _check(st, "m2rnn_ssm_scan_backward")
+    res["workspace"] = ws
+    return res
+
+
+def ssm_step(H, q, k, v, dt, A, *, dt_bias=None, w_r=None, y=None, stream=None):
+    """One token of ``ssm_scan``: ``H`` [B,N,K,V] fp32 advances in place; q, k
+    [B,G,K], v [B,N,V], dt [B,N].  Returns y [B,N,V]."""
+    import torch
+    B, G, K = q.shape
+    N, V = v.shape[1:]
+    dev, ty, f32 = v.device, v.dtype, torch.float32
+    code = _dtype_code(v)
+    qp, qs = _rows(q, "q", (B, G, K), 2, ty, dev)
+    kp, ks = _rows(k, "k", (B, G, K), 2, ty, dev)
+    vp, vs = _rows(v, "v", (B, N, V), 2, ty, dev)
+    dp, ds = _rows(dt, "dt", (B, N), 1, ty, dev)
+    if y is None:
+        y = _alloc((B, N, V), ty, dev, stream)
+    st = load().m2rnn_ssm_step(_need(H, "H", (B, N, K, V), f32, dev), qp, qs, kp, ks, vp, vs, dp, ds,
+                               _need(A, "A", (N,), f32, dev), _need(dt_bias, "dt_bias", (N,), f32, dev),
+                               _need(w_r, "w_r", (N, V), ty, dev), _need(y, "y", (B, N, V), ty, dev), B, N, G, K, V,
+                               code, _stream_handle(stream))
+    _check(st, "m2rnn_ssm_step")
+    return y
+
+
+class GradPlan:
+    """The gradient tensors of a program, listed once for ``grad_norm`` and
+    ``grad_clip``.  It holds their addresses (and keeps them alive): build a new
+    one when a tensor is replaced.  Calls that share a plan must not overlap."""
+
+    def __init__(self, grads, out=None):
+        import torch
+        grads = list(grads)
+        outs = grads if out is None else list(out)
+        if len(outs) != len(grads):
+            raise ValueError(f"{len(grads)} gradients, {len(outs)} outputs")
+        if not grads:
+            raise ValueError("no gradients")
+        self.device = grads[0].device
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            for t, name in ((g, f"grads[{i}]"), (o, f"out[{i}]")):
+                _need(t, name, g.shape, g.dtype, self.device)
+        n = len(grads)
+        counts = (ctypes.c_int64 * n)(*(g.numel() for g in grads))
+        codes = (ctypes.c_int32 * n)(*(_dtype_code(g) for g in grads))
+        ptrs = (ctypes.c_void_p * n)(*(g.data_ptr() for g in grads))
+        optrs = (ctypes.c_void_p * n)(*(o.data_ptr() for o in outs))
+        size = m2rnn_grad_plan_size(n, counts)
+        host = torch.empty(size, dtype=torch.uint8)
+        _check(m2rnn_grad_plan_build(n, ptrs, optrs, counts, codes, host.data_ptr(), size), "m2rnn_grad_plan_build")
+        self.table = host.to(self.device)
+        self.workspace = torch.empty(m2rnn_grad_workspace_size(), dtype=torch.uint8, device=self.device)
+        self.grads, self.outs = grads, outs
+
+
+def grad_plan(grads, out=None) -> GradPlan:
+    """Lists gradient tensors (contiguous, bf16 or fp32) for ``grad_clip``;
+    ``out``: where the clipped ones go (None = in place)."""
+    return GradPlan(grads, out)
+
+
+def grad_norm(plan: GradPlan, *, norm=None, stream=None):
+    """Global norm of the plan's tensors: a 0-dim fp32 tensor on the device."""
+    import torch
+    if norm is None:
+        norm = _alloc((), torch.float32, plan.device, stream)
+    st = load().m2rnn_grad_norm(plan.table.data_ptr(), plan.table.numel(), norm.data_ptr(), plan.workspace.data_ptr(),
+                                plan.workspace.numel(), _stream_handle(stream))
+    _check(st, "m2rnn_grad_norm")
+    return norm
+
+
+def grad_clip(plan: GradPlan, max_norm: float, *, norm=None, stream=None):
+    """Scales the plan's tensors by min(1, max_norm / (norm + 1e-6)) into its
+    outputs.  Returns the norm before clipping, a 0-dim fp32 tensor."""
+    import torch
+    if norm is None:
+        norm = _alloc((), torch.float32, plan.device, stream)
+    st = load().m2rnn_grad_clip(plan.table.data_ptr(), plan.table.numel(), float(max_norm), norm.data_ptr(),
+                                plan.workspace.data_ptr(), plan.workspace.numel(), _stream_handle(stream))
+    _check(st, "m2rnn_grad_clip")
+    return norm

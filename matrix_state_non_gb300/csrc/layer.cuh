@@ -1,0 +1,121 @@
+// Shared by the hybrid layer's kernels (short convolution, selective state
+// space scan, gradient clipping): element access in the input type, the
+// argument blocks that the C-ABI layer fills, and the launchers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/m2rnn.h"
+#include "ptx.cuh"
+
+namespace m2rnn {
+
+// Element type tags: bf16 as raw bits, fp32 as float.
+__device__ __forceinline__ float to_f32(uint16_t x) { return bf16_bits_to_f32(x); }
+__device__ __forceinline__ float to_f32(float x) { return x; }
+template <typename T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ uint16_t from_f32<uint16_t>(float x) {
+  return static_cast<uint16_t>(pack_bf16x2(x, 0.f) & 0xFFFFu);
+}
+
+// ---------------------------------------------------------------------------
+// Short causal convolution
+// ---------------------------------------------------------------------------
+constexpr int kConvMaxWidth = 8;
+
+struct ConvArgs {
+  const void* x;       // [B,T,C], rows x_stride elements apart
+  const void* w;       // [C,W]
+  const void* bias;    // [C] or null
+  const void* x0;      // [B,W-1,C] or null (zero)
+  const int* lengths;  // [B] or null (all T)
+  void* y;             // forward: [B,T,C]
+  void* x_T;           // forward: [B,W-1,C] or null
+  const float* dy;     // backward: [B,T,C]
+  const float* dx_T;   // backward: [B,W-1,C] or null
+  float* dx;           // backward: [B,T,C]
+  float* dw;           // backward: [C,W]
+  float* db;           // backward: [C] or null
+  float* dx0;          // backward: [B,W-1,C] or null
+  float* part;         // backward: [parts][W+1][C]
+  int64_t x_stride;
+  int B, T, C, W;
+  bool silu, bf16;
+};
+
+int conv_backward_parts(int64_t B, int64_t T);
+cudaError_t launch_conv_forward(const ConvArgs& a, cudaStream_t s);
+cudaError_t launch_conv_backward(const ConvArgs& a, cudaStream_t s);
+// state [B,W-1,C] in place; x, y [B,C].
+cudaError_t launch_conv_step(void* state, const void* x, int64_t x_stride, const void* w, const void* bias, void* y,
+                             int B, int C, int W, bool silu, bool bf16, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Selective state space scan
+// ---------------------------------------------------------------------------
+struct SsmArgs {
+  const void* q;         // [B,T,G,K], tokens q_stride elements apart
+  const void* k;         // [B,T,G,K]
+  const void* v;         // [B,T,N,V]
+  const void* dt;        // [B,T,N]
+  const float* A;        // [N]
+  const float* dt_bias;  // [N] or null
+  const void* w_r;       // [N,V] or null
+  const float* H_0;      // [B,N,K,V] or null
+  const int* lengths;    // [B] or null
+  void* y;               // forward: [B,T,N,V] in the input type
+  float* H_T;            // forward: [B,N,K,V] or null
+  const void* dy;        // backward: [B,T,N,V] in the input type
+  const float* dH_T;     // backward: or null
+  float* dq;             // backward: [B,T,G,K]
+  float* dk;
+  float* dv;             // [B,T,N,V]
+  float* ddt;            // [B,T,N]
+  float* dA;             // [N]
+  float* ddt_bias;       // [N] or null
+  float* dw_r;           // [N,V] or null
+  float* dH_0;           // [B,N,K,V] or null
+  void* ws;              // scratch behind the status block
+  int64_t q_stride, k_stride, v_stride, dt_stride;
+  int B, T, N, G, K, V;
+  bool bf16;
+};
+
+size_t ssm_forward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V, bool bf16);
+size_t ssm_backward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V, bool bf16);
+cudaError_t launch_ssm_forward(const SsmArgs& a, cudaStream_t s);
+cudaError_t launch_ssm_backward(const SsmArgs& a, cudaStream_t s);
+// One token: H [B,N,K,V] in place; q, k [B,G,K], v, y [B,N,V], dt [B,N]
+// (strides between sequences in the *_stride fields; T is ignored).
+cudaError_t launch_ssm_step(float* H, const SsmArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Gradient norm and clipping
+// ---------------------------------------------------------------------------
+// One piece of one tensor, the unit of work of a block.
+struct GradChunk {
+  const void* in;
+  void* out;
+  int32_t count;  // elements
+  int32_t bf16;
+  int64_t pad;
+};
+static_assert(sizeof(GradChunk) == 32, "plan entries are 32 bytes");
+
+constexpr int kGradChunk = 16384;  // elements of a piece
+
+size_t grad_clip_scratch_bytes();
+// clip false: only the norm.
+cudaError_t launch_grad_clip(const GradChunk* plan, int64_t chunks, float max_norm, bool clip, float* norm, void* ws,
+                             cudaStream_t s);
+
+}  // namespace m2rnn
