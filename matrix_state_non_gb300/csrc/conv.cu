@@ -16,160 +16,500 @@
 namespace m2rnn {
 namespace {
 
-// x sigmoid(x); __expf and __fdividef are good to a few units of fp32 here.
-__device__ __forceinline__ float silu_f(float x) { return __fdividef(x, 1.f + __expf(-x)); }
+struct Yes { static constexpr bool value = true; };
+struct No { static constexpr bool value = false; };
 
-// One thread per (b, t, c): the plain kernel.
-template <typename T>
-__global__ void conv_forward_kernel(ConvArgs A) {
-  const int64_t n = static_cast<int64_t>(A.B) * A.T * A.C;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= n) return;
-  const int c = static_cast<int>(i % A.C);
-  const int64_t bt = i / A.C;
-  const int t = static_cast<int>(bt % A.T), b = static_cast<int>(bt / A.T);
-  const int len = A.lengths ? min(max(A.lengths[b], 0), A.T) : A.T;
-  const T* x = static_cast<const T*>(A.x) + static_cast<int64_t>(b) * A.T * A.x_stride + c;
-  const T* x0 = static_cast<const T*>(A.x0);
-  auto at = [&](int s) -> float {  // xs at x index s >= -(W - 1)
-    if (s >= 0) return to_f32(x[s * A.x_stride]);
-    return x0 ? to_f32(x0[(static_cast<int64_t>(b) * (A.W - 1) + s + A.W - 1) * A.C + c]) : 0.f;
-  };
-  float r = 0.f;
-  if (t < len) {
-    float p = A.bias ? to_f32(static_cast<const T*>(A.bias)[c]) : 0.f;
-    for (int w = 0; w < A.W; ++w) p += to_f32(static_cast<const T*>(A.w)[c * A.W + w]) * at(t + w - (A.W - 1));
-    r = A.silu ? silu_f(p) : p;
+// kVec consecutive elements of a row: one load or store of kVec elements
+// (16 or 8 bytes on the vector paths).
+template <typename T, int kVec>
+struct Row {
+  alignas(sizeof(T) * kVec) T e[kVec];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (sizeof(T) * kVec == 16) {
+      *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
+    } else if constexpr (sizeof(T) * kVec == 8) {
+      *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
+    } else if constexpr (sizeof(T) * kVec == 4) {
+      *reinterpret_cast<uint32_t*>(e) = *reinterpret_cast<const uint32_t*>(p);
+    } else {
+      static_assert(kVec == 1, "vectors of 4, 8 or 16 bytes");
+      e[0] = *p;
+    }
   }
-  static_cast<T*>(A.y)[i] = from_f32<T>(r);
-  if (A.x_T != nullptr && t == 0)
-    for (int j = 0; j < A.W - 1; ++j)
-      static_cast<T*>(A.x_T)[(static_cast<int64_t>(b) * (A.W - 1) + j) * A.C + c] = from_f32<T>(at(len + j - (A.W - 1)));
+  __device__ __forceinline__ void store(T* p) const {
+    if constexpr (sizeof(T) * kVec == 16) {
+      *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(e);
+    } else if constexpr (sizeof(T) * kVec == 8) {
+      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
+    } else if constexpr (sizeof(T) * kVec == 4) {
+      *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(e);
+    } else {
+      *p = e[0];
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[kVec]) const {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) f[i] = to_f32(e[i]);
+  }
+  __device__ __forceinline__ void set(const float (&f)[kVec]) {
+    if constexpr (sizeof(T) == 2 && kVec % 2 == 0) {
+      uint32_t* o = reinterpret_cast<uint32_t*>(e);
+#pragma unroll
+      for (int i = 0; i < kVec; i += 2) o[i / 2] = pack_bf16x2(f[i], f[i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) e[i] = from_f32<T>(f[i]);
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) e[i] = T(0);
+  }
+};
+
+// One sequence's inputs at its channels: xs at x index s >= -(W - 1), zero
+// where there is none.
+template <typename T, int kVec>
+struct Source {
+  const T* x;
+  const T* x0;  // null: zero
+  int64_t stride;
+  int C, W;
+  __device__ __forceinline__ void at(int s, int len, Row<T, kVec>& r) const {
+    if (s >= len || s < -(W - 1) || (s < 0 && x0 == nullptr))
+      r.zero();
+    else
+      r.load(s >= 0 ? x + s * stride : x0 + static_cast<int64_t>(s + W - 1) * C);
+  }
+};
+
+template <typename T, int kVec>
+__device__ __forceinline__ Source<T, kVec> source(const ConvArgs& A, int b, int c) {
+  return {static_cast<const T*>(A.x) + static_cast<int64_t>(b) * A.T * A.x_stride + c,
+          A.x0 ? static_cast<const T*>(A.x0) + static_cast<int64_t>(b) * (A.W - 1) * A.C + c : nullptr, A.x_stride, A.C,
+          A.W};
 }
 
-constexpr int kBwdStrip = 64;  // steps of one partial sum of dw, db
-
-// One thread per (channel, strip of kBwdStrip steps).
-template <typename T>
-__global__ void conv_backward_kernel(ConvArgs A) {
-  const int c = blockIdx.x * blockDim.x + threadIdx.x;
-  if (c >= A.C) return;
-  const int strips = (A.T + kBwdStrip - 1) / kBwdStrip;
-  const int b = blockIdx.y / strips, strip = blockIdx.y % strips;
-  const int t0 = strip * kBwdStrip, t1 = min(A.T, t0 + kBwdStrip);
-  const int len = A.lengths ? min(max(A.lengths[b], 0), A.T) : A.T;
-  const int W = A.W;
-  const T* x = static_cast<const T*>(A.x) + static_cast<int64_t>(b) * A.T * A.x_stride + c;
-  const T* x0 = static_cast<const T*>(A.x0);
-  const float* dy = A.dy + static_cast<int64_t>(b) * A.T * A.C + c;
-  float w[kConvMaxWidth], dw[kConvMaxWidth], db = 0.f;
-  for (int j = 0; j < W; ++j) {
-    w[j] = to_f32(static_cast<const T*>(A.w)[c * W + j]);
-    dw[j] = 0.f;
-  }
-  const float bias = A.bias ? to_f32(static_cast<const T*>(A.bias)[c]) : 0.f;
-  auto at = [&](int s) -> float {
-    if (s >= 0) return to_f32(x[s * A.x_stride]);
-    return x0 ? to_f32(x0[(static_cast<int64_t>(b) * (W - 1) + s + W - 1) * A.C + c]) : 0.f;
-  };
-  auto grad = [&](int t, bool add) -> float {
-    if (t < 0 || t >= len) return 0.f;
-    float p = bias;
-    for (int j = 0; j < W; ++j) p += w[j] * at(t + j - (W - 1));
-    float g = dy[static_cast<int64_t>(t) * A.C];
-    if (A.silu) {
-      const float sg = 1.f / (1.f + __expf(-p));
-      g *= sg * (1.f + p * (1.f - sg));
+// The channels' weights, right-aligned to kW taps (zero in front).  With W =
+// kW they are consecutive and come as a few 16-byte loads: 40 single loads
+// per thread cost as much as the strip's own rows.
+template <typename T, int kVec, int kW>
+__device__ __forceinline__ void load_weights(const ConvArgs& A, int c, float (&w)[kW][kVec], float (&bias)[kVec]) {
+  const T* p = static_cast<const T*>(A.w) + static_cast<int64_t>(c) * A.W;
+  constexpr int kPer = 16 / sizeof(T);
+  if (kVec * kW % kPer == 0 && A.W == kW) {
+#pragma unroll
+    for (int i = 0; i < kVec * kW / kPer; ++i) {
+      Row<T, kPer> r;
+      r.load(p + i * kPer);
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) w[(i * kPer + e) % kW][(i * kPer + e) / kW] = to_f32(r.e[e]);
     }
-    if (add) {
-      db += g;
-      for (int j = 0; j < W; ++j) dw[j] += g * at(t + j - (W - 1));
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+#pragma unroll
+      for (int j = 0; j < kW; ++j) {
+        const int k = j - (kW - A.W);
+        w[j][i] = k >= 0 ? to_f32(p[i * A.W + k]) : 0.f;
+      }
     }
-    return g;
-  };
-  // x index s gets sum over t = s .. s + W - 1 of g_t w[s - t + W - 1].
-  for (int s = strip == 0 ? -(W - 1) : t0; s < t1; ++s) {
-    float d = 0.f;
-    for (int t = s; t < s + W; ++t) d += grad(t, t == s) * w[s - t + W - 1];
-    if (A.dx_T != nullptr && s < len && s >= len - (W - 1))
-      d += A.dx_T[(static_cast<int64_t>(b) * (W - 1) + s - len + W - 1) * A.C + c];
-    if (s >= 0)
-      A.dx[(static_cast<int64_t>(b) * A.T + s) * A.C + c] = d;
-    else if (A.dx0 != nullptr)
-      A.dx0[(static_cast<int64_t>(b) * (W - 1) + s + W - 1) * A.C + c] = d;
   }
-  float* part = A.part + static_cast<int64_t>(blockIdx.y) * (W + 1) * A.C + c;
-  for (int j = 0; j < W; ++j) part[static_cast<int64_t>(j) * A.C] = dw[j];
-  part[static_cast<int64_t>(W) * A.C] = db;
+  Row<T, kVec> r;
+  r.zero();
+  if (A.bias != nullptr) r.load(static_cast<const T*>(A.bias) + c);
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) bias[i] = to_f32(r.e[i]);
 }
 
-// Fixed-order sum of the partials: thread (j, c) of [W + 1][C].
-__global__ void conv_sum_parts_kernel(const float* part, float* dw, float* db, int parts, int C, int W) {
-  const int c = blockIdx.x * blockDim.x + threadIdx.x, j = blockIdx.y;
-  if (c >= C) return;
+__device__ __forceinline__ int seq_len(const ConvArgs& A, int b) {
+  return A.lengths ? min(max(A.lengths[b], 0), A.T) : A.T;
+}
+
+// Forward.  A thread takes kVec channels of a strip of `steps` steps (a
+// multiple of kAhead) and keeps the last kW - 1 inputs in registers, so every
+// input is loaded once but for the W - 1 rows before each strip; the next
+// kAhead rows are in flight while it computes on the last.  kEdge: the strip
+// may reach behind its sequence's end.
+constexpr int kFwdThreads = 256, kFwdBlocks = 2, kAhead = 4;
+
+template <typename T, int kVec, int kW, bool kEdge>
+__device__ __forceinline__ void forward_strip(const ConvArgs& A, const Source<T, kVec>& src, T* y, int c, int t0,
+                                              int t1, int len) {
+  float w[kW][kVec], bias[kVec], h[kW][kVec];
+  Row<T, kVec> in[kAhead], next[kAhead];
+  const T* px = src.x + t0 * src.stride;
+  T* py = y + static_cast<int64_t>(t0) * A.C;
+  auto load = [&](int t, Row<T, kVec>(&r)[kAhead]) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (!kEdge || t + u < len)
+        r[u].load(px + u * src.stride);
+      else
+        r[u].zero();
+    }
+    px += kAhead * src.stride;
+  };
+  load(t0, in);
+#pragma unroll
+  for (int j = 1; j < kW; ++j) {  // h[j] = xs at t - kW + j
+    Row<T, kVec> r;
+    src.at(t0 - kW + j, len, r);
+    r.get(h[j]);
+  }
+  load_weights<T, kVec, kW>(A, c, w, bias);
+  for (int t = t0; t < t1; t += kAhead) {
+    if (t + kAhead < t1) load(t + kAhead, next);
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      float p[kVec];
+      Row<T, kVec> out;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) p[e] = bias[e];
+#pragma unroll
+      for (int j = 0; j < kW - 1; ++j) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) h[j][e] = h[j + 1][e];
+        fma_row<kVec>(p, w[j], h[j]);
+      }
+      in[u].get(h[kW - 1]);
+      fma_row<kVec>(p, w[kW - 1], h[kW - 1]);
+      if (A.silu) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) p[e] *= sigmoid_fast(p[e]);
+      }
+      out.set(p);
+      if (kEdge && t + u >= len) out.zero();
+      if (!kEdge || t + u < t1) out.store(py + static_cast<int64_t>(u) * A.C);
+      in[u] = next[u];
+    }
+    py += static_cast<int64_t>(kAhead) * A.C;
+  }
+}
+
+template <typename T, int kVec, int kW>
+__global__ void __launch_bounds__(kFwdThreads, kFwdBlocks)
+    conv_forward_kernel(ConvArgs A, int steps, int strips) {
+  const int groups = A.C / kVec;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kFwdThreads + threadIdx.x;
+  if (i >= static_cast<int64_t>(A.B) * strips * groups) return;
+  const int c = static_cast<int>(i % groups) * kVec;
+  const int bs = static_cast<int>(i / groups), b = bs / strips, strip = bs % strips;
+  const int len = seq_len(A, b), t0 = strip * steps, t1 = min(A.T, t0 + steps);
+  const Source<T, kVec> src = source<T, kVec>(A, b, c);
+  T* y = static_cast<T*>(A.y) + static_cast<int64_t>(b) * A.T * A.C + c;
+  if (strip == 0 && A.x_T != nullptr) {
+    for (int j = 0; j < A.W - 1; ++j) {
+      Row<T, kVec> r;
+      src.at(len + j - (A.W - 1), len, r);
+      r.store(static_cast<T*>(A.x_T) + (static_cast<int64_t>(b) * (A.W - 1) + j) * A.C + c);
+    }
+  }
+  if (t0 + steps <= len)
+    forward_strip<T, kVec, kW, false>(A, src, y, c, t0, t1, len);
+  else
+    forward_strip<T, kVec, kW, true>(A, src, y, c, t0, t1, len);
+}
+
+// Backward.  A warp takes 32 kVec channels of a strip of kStrip steps: it
+// walks the steps with the last kW - 1 inputs and gradients g in registers,
+// so that dxs comes out kW - 1 steps behind; the strip's last gradients are
+// those of the kW - 1 steps behind it.  The block's warps are consecutive
+// strips; their sums of dw, db are added in warp order through shared memory
+// into one partial per block.  Bound by HBM (10 bytes per bf16 element).
+constexpr int kBwdWarps = 8, kStrip = 64, kBwdAhead = 4, kBwdBlocks = 4;
+
+// kEdge: the strip is its sequence's first or reaches its end.
+template <typename T, int kVec, int kW, bool kEdge>
+__device__ __forceinline__ void backward_strip(const ConvArgs& A, int b, int c, int t0, int t1, int len,
+                                               float (&dw)[kW][kVec], float (&db)[kVec]) {
+  const Source<T, kVec> src = source<T, kVec>(A, b, c);
+  float w[kW][kVec], bias[kVec], h[kW][kVec], g[kW][kVec];
+  const T* px = src.x + t0 * src.stride;
+  const float* pu = A.dy + (static_cast<int64_t>(b) * A.T + t0) * A.C + c;
+  float* pd = A.dx + (static_cast<int64_t>(b) * A.T + t0 - (kW - 1)) * A.C + c;
+#pragma unroll
+  for (int j = 1; j < kW; ++j) {
+    Row<T, kVec> r;
+    src.at(t0 - kW + j, len, r);
+    r.get(h[j]);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) g[j][e] = 0.f;  // gradients before the strip belong to the strip before
+  }
+  load_weights<T, kVec, kW>(A, c, w, bias);
+  const int end = t0 + kStrip + kW - 1;  // g is wanted up to the last input's kW - 1 steps later
+  // One group of kBwdAhead steps; kMine: all of them belong to the strip.
+  auto group = [&](int t, auto mine_tag) {
+    constexpr bool kMine = decltype(mine_tag)::value;
+    Row<T, kVec> in[kBwdAhead];
+    Row<float, kVec> up[kBwdAhead];
+#pragma unroll
+    for (int u = 0; u < kBwdAhead; ++u) {
+      if ((!kEdge && kMine) || t + u < (kEdge ? min(len, end) : end)) {
+        in[u].load(px + u * src.stride);
+        up[u].load(pu + static_cast<int64_t>(u) * A.C);
+      } else {
+        in[u].zero();
+        up[u].zero();
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBwdAhead; ++u) {
+      float p[kVec], x[kVec], r[kVec];
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        p[e] = bias[e];
+        r[e] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < kW - 1; ++j) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          h[j][e] = h[j + 1][e];
+          g[j][e] = g[j + 1][e];
+        }
+        fma_row<kVec>(p, w[j], h[j]);
+      }
+      in[u].get(h[kW - 1]);
+      fma_row<kVec>(p, w[kW - 1], h[kW - 1]);
+      up[u].get(x);
+      if (A.silu) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          const float sg = sigmoid_fast(p[e]);
+          x[e] *= fmaf(p[e] * sg, 1.f - sg, sg);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) g[kW - 1][e] = kEdge && t + u >= len ? 0.f : x[e];
+      if (kMine || t + u < t1) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) db[e] += g[kW - 1][e];
+#pragma unroll
+        for (int j = 0; j < kW; ++j) fma_row<kVec>(dw[j], g[kW - 1], h[j]);
+      }
+      // x index s = t - (kW - 1) gets sum over j of g at s + j times w[kW - 1 - j].
+#pragma unroll
+      for (int j = 0; j < kW; ++j) fma_row<kVec>(r, g[j], w[kW - 1 - j]);
+      const int s = t + u - (kW - 1);
+      Row<float, kVec> out;
+      out.set(r);
+      if (!kEdge) {
+        if (s >= t0 && (kMine || s < t1)) out.store(pd + static_cast<int64_t>(u) * A.C);
+      } else if (s >= t0 ? s < t1 : t0 == 0 && s >= -(A.W - 1)) {
+        if (A.dx_T != nullptr && s < len && s >= len - (A.W - 1)) {
+          Row<float, kVec> last;
+          last.load(A.dx_T + (static_cast<int64_t>(b) * (A.W - 1) + s - len + A.W - 1) * A.C + c);
+#pragma unroll
+          for (int e = 0; e < kVec; ++e) out.e[e] += last.e[e];
+        }
+        if (s >= 0)
+          out.store(pd + static_cast<int64_t>(u) * A.C);
+        else if (A.dx0 != nullptr)
+          out.store(A.dx0 + (static_cast<int64_t>(b) * (A.W - 1) + s + A.W - 1) * A.C + c);
+      }
+    }
+    px += kBwdAhead * src.stride;
+    pu += static_cast<int64_t>(kBwdAhead) * A.C;
+    pd += static_cast<int64_t>(kBwdAhead) * A.C;
+  };
+  int t = t0;
+  if (!kEdge)
+    for (; t < t0 + kStrip; t += kBwdAhead) group(t, Yes{});
+  for (; t < end; t += kBwdAhead) group(t, No{});
+}
+
+template <typename T, int kVec, int kW>
+__global__ void __launch_bounds__(32 * kBwdWarps, kW == 4 ? kBwdBlocks : 2)
+    conv_backward_kernel(ConvArgs A, int blocks_c, int blocks_t) {
+  __shared__ float red[kBwdWarps][kW + 1][32 * kVec];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int bc = blockIdx.x % blocks_c, bt = blockIdx.x / blocks_c;
+  const int b = bt / blocks_t, c = (bc * 32 + lane) * kVec;
+  const int t0 = ((bt % blocks_t) * kBwdWarps + warp) * kStrip, t1 = min(A.T, t0 + kStrip);
+  const int len = seq_len(A, b);
+  float dw[kW][kVec], db[kVec];
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) {
+    db[e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < kW; ++j) dw[j][e] = 0.f;
+  }
+  if (c < A.C && t0 < A.T) {
+    // The last kW steps of a sequence may take dx_T in.
+    if (t0 > 0 && t0 + kStrip + kW - 1 <= len - kW)
+      backward_strip<T, kVec, kW, false>(A, b, c, t0, t1, len, dw, db);
+    else
+      backward_strip<T, kVec, kW, true>(A, b, c, t0, t1, len, dw, db);
+  }
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) {
+#pragma unroll
+    for (int j = 0; j < kW; ++j) red[warp][j][lane * kVec + e] = dw[j][e];
+    red[warp][kW][lane * kVec + e] = db[e];
+  }
+  __syncthreads();
+  // Partials are [block of steps][A.W taps, then the bias][C].
+  for (int i = threadIdx.x; i < (kW + 1) * 32 * kVec; i += 32 * kBwdWarps) {
+    const int j = i / (32 * kVec) - (kW - A.W), x = i % (32 * kVec), cc = bc * 32 * kVec + x;
+    if (j < 0 || cc >= A.C) continue;
+    float s = 0.f;
+#pragma unroll
+    for (int v = 0; v < kBwdWarps; ++v) s += red[v][i / (32 * kVec)][x];
+    A.part[(static_cast<int64_t>(bt) * (A.W + 1) + j) * A.C + cc] = s;
+  }
+}
+
+// Sum of the partials over the blocks of steps: block (32 channels, tap j),
+// 8 warps taking every eighth partial, added in warp order.
+__global__ void __launch_bounds__(256) conv_sum_parts_kernel(const float* part, float* dw, float* db, int parts, int C,
+                                                             int W) {
+  __shared__ float red[8][32];
+  const int lane = threadIdx.x & 31, v = threadIdx.x >> 5, c = blockIdx.x * 32 + lane, j = blockIdx.y;
   float t = 0.f;
-  for (int p = 0; p < parts; ++p) t += part[(static_cast<int64_t>(p) * (W + 1) + j) * C + c];
+  if (c < C) {
+#pragma unroll 4
+    for (int p = v; p < parts; p += 8) t += part[(static_cast<int64_t>(p) * (W + 1) + j) * C + c];
+  }
+  red[v][lane] = t;
+  __syncthreads();
+  if (v != 0 || c >= C) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) t += red[i][lane];
   if (j < W)
     dw[static_cast<int64_t>(c) * W + j] = t;
   else if (db != nullptr)
     db[c] = t;
 }
 
-template <typename T>
-__global__ void conv_step_kernel(T* state, const T* x, int64_t x_stride, const T* w, const T* bias, T* y, int B, int C,
-                                 int W, bool silu) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (i >= static_cast<int64_t>(B) * C) return;
-  const int c = static_cast<int>(i % C), b = static_cast<int>(i / C);
-  T* st = state + static_cast<int64_t>(b) * (W - 1) * C + c;
-  const T xn = x[b * x_stride + c];
-  float p = bias ? to_f32(bias[c]) : 0.f;
-  for (int j = 0; j < W - 1; ++j) p += to_f32(w[c * W + j]) * to_f32(st[static_cast<int64_t>(j) * C]);
-  p += to_f32(w[c * W + W - 1]) * to_f32(xn);
-  for (int j = 0; j + 1 < W - 1; ++j) st[static_cast<int64_t>(j) * C] = st[static_cast<int64_t>(j + 1) * C];
-  if (W > 1) st[static_cast<int64_t>(W - 2) * C] = xn;
-  y[i] = from_f32<T>(silu ? silu_f(p) : p);
+// One token: a thread takes kVec channels of one sequence.
+template <typename T, int kVec, int kW>
+__global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs A, T* state) {
+  const int groups = A.C / kVec;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
+  if (i >= static_cast<int64_t>(A.B) * groups) return;
+  const int c = static_cast<int>(i % groups) * kVec, b = static_cast<int>(i / groups), W = A.W;
+  T* st = state + static_cast<int64_t>(b) * (W - 1) * A.C + c;
+  Row<T, kVec> r[kW], out;
+  r[kW - 1].load(static_cast<const T*>(A.x) + b * A.x_stride + c);
+#pragma unroll
+  for (int j = 0; j < kW - 1; ++j) {
+    const int k = j - (kW - W);
+    if (k >= 0)
+      r[j].load(st + static_cast<int64_t>(k) * A.C);
+    else
+      r[j].zero();
+  }
+  float w[kW][kVec], bias[kVec];
+  load_weights<T, kVec, kW>(A, c, w, bias);
+#pragma unroll
+  for (int j = 1; j < kW; ++j) {
+    const int k = j - 1 - (kW - W);
+    if (k >= 0) r[j].store(st + static_cast<int64_t>(k) * A.C);
+  }
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) {
+    float p = bias[e];
+#pragma unroll
+    for (int j = 0; j < kW; ++j) p = fmaf(w[j][e], to_f32(r[j].e[e]), p);
+    out.e[e] = from_f32<T>(A.silu ? p * sigmoid_fast(p) : p);
+  }
+  out.store(static_cast<T*>(A.y) + static_cast<int64_t>(b) * A.C + c);
 }
+
+// Rows that can be moved in vectors of v elements.
+bool rows_of(const ConvArgs& a, int v) {
+  const size_t bytes = (a.bf16 ? 2 : 4) * v;
+  return a.C % v == 0 && a.x_stride % v == 0 && reinterpret_cast<uintptr_t>(a.x) % bytes == 0;
+}
+
+template <typename T, int kVec, int kW>
+void forward(const ConvArgs& a, cudaStream_t s) {
+  // Strips as short as it takes to fill every SM once (each strip loads W - 1 rows twice), at most 64 steps.
+  const int64_t groups = a.C / kVec, room = 152ll * kFwdBlocks * kFwdThreads;
+  int steps = static_cast<int>((static_cast<int64_t>(a.B) * a.T * groups + room - 1) / room);
+  steps = steps > 64 ? 64 : (steps + kAhead - 1) / kAhead * kAhead;
+  const int strips = (a.T + steps - 1) / steps;
+  const int64_t n = static_cast<int64_t>(a.B) * strips * groups;
+  conv_forward_kernel<T, kVec, kW>
+      <<<static_cast<unsigned>((n + kFwdThreads - 1) / kFwdThreads), kFwdThreads, 0, s>>>(a, steps, strips);
+}
+
+template <typename T, int kVec, int kW>
+void backward(const ConvArgs& a, cudaStream_t s) {
+  const int blocks_c = (a.C + 32 * kVec - 1) / (32 * kVec), blocks_t = conv_backward_parts(1, a.T);
+  conv_backward_kernel<T, kVec, kW><<<static_cast<unsigned>(static_cast<int64_t>(blocks_c) * blocks_t * a.B),
+                                      32 * kBwdWarps, 0, s>>>(a, blocks_c, blocks_t);
+}
+
+template <typename T, int kVec, int kW>
+void step(const ConvArgs& a, void* state, cudaStream_t s) {
+  const int64_t n = static_cast<int64_t>(a.B) * (a.C / kVec);
+  conv_step_kernel<T, kVec, kW><<<static_cast<unsigned>((n + 127) / 128), 128, 0, s>>>(a, static_cast<T*>(state));
+}
+
+// Widths 1-4 run as 4 taps, 5-8 as 8 (those with fewer channels a thread: 8
+// taps of 8 channels spill).
+#define M2RNN_CONV(CALL, T, VEC, VEC8, ...) \
+  do {                                      \
+    if (a.W <= 4)                           \
+      CALL<T, VEC, 4>(__VA_ARGS__);         \
+    else                                    \
+      CALL<T, VEC8, 8>(__VA_ARGS__);        \
+  } while (0)
 
 }  // namespace
 
-int conv_backward_parts(int64_t B, int64_t T) { return static_cast<int>(B * ((T + kBwdStrip - 1) / kBwdStrip)); }
+int conv_backward_parts(int64_t B, int64_t T) {
+  return static_cast<int>(B * ((T + kBwdWarps * kStrip - 1) / (kBwdWarps * kStrip)));
+}
 
 cudaError_t launch_conv_forward(const ConvArgs& a, cudaStream_t s) {
-  const int64_t n = static_cast<int64_t>(a.B) * a.T * a.C;
-  const unsigned grid = static_cast<unsigned>((n + 255) / 256);
-  if (a.bf16)
-    conv_forward_kernel<uint16_t><<<grid, 256, 0, s>>>(a);
-  else
-    conv_forward_kernel<float><<<grid, 256, 0, s>>>(a);
+  if (a.bf16) {
+    if (rows_of(a, 8))
+      M2RNN_CONV(forward, uint16_t, 8, 4, a, s);
+    else
+      M2RNN_CONV(forward, uint16_t, 1, 1, a, s);
+  } else {
+    if (rows_of(a, 4))
+      M2RNN_CONV(forward, float, 4, 4, a, s);
+    else
+      M2RNN_CONV(forward, float, 1, 1, a, s);
+  }
   return cudaGetLastError();
 }
 
 cudaError_t launch_conv_backward(const ConvArgs& a, cudaStream_t s) {
-  const int parts = conv_backward_parts(a.B, a.T);
-  const dim3 grid((a.C + 127) / 128, parts);
-  if (a.bf16)
-    conv_backward_kernel<uint16_t><<<grid, 128, 0, s>>>(a);
-  else
-    conv_backward_kernel<float><<<grid, 128, 0, s>>>(a);
+  if (a.bf16) {
+    if (rows_of(a, 2))
+      M2RNN_CONV(backward, uint16_t, 2, 1, a, s);
+    else
+      M2RNN_CONV(backward, uint16_t, 1, 1, a, s);
+  } else {
+    if (rows_of(a, 2))
+      M2RNN_CONV(backward, float, 2, 1, a, s);
+    else
+      M2RNN_CONV(backward, float, 1, 1, a, s);
+  }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  conv_sum_parts_kernel<<<dim3((a.C + 127) / 128, a.W + 1), 128, 0, s>>>(a.part, a.dw, a.db, parts, a.C, a.W);
+  conv_sum_parts_kernel<<<dim3((a.C + 31) / 32, a.W + 1), 256, 0, s>>>(a.part, a.dw, a.db,
+                                                                      conv_backward_parts(a.B, a.T), a.C, a.W);
   return cudaGetLastError();
 }
 
-cudaError_t launch_conv_step(void* state, const void* x, int64_t x_stride, const void* w, const void* bias, void* y,
-                             int B, int C, int W, bool silu, bool bf16, cudaStream_t s) {
-  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(B) * C + 127) / 128);
-  if (bf16)
-    conv_step_kernel<uint16_t><<<grid, 128, 0, s>>>(static_cast<uint16_t*>(state), static_cast<const uint16_t*>(x),
-                                                    x_stride, static_cast<const uint16_t*>(w),
-                                                    static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(y), B, C,
-                                                    W, silu);
-  else
-    conv_step_kernel<float><<<grid, 128, 0, s>>>(static_cast<float*>(state), static_cast<const float*>(x), x_stride,
-                                                 static_cast<const float*>(w), static_cast<const float*>(bias),
-                                                 static_cast<float*>(y), B, C, W, silu);
+cudaError_t launch_conv_step(void* state, const ConvArgs& a, cudaStream_t s) {
+  if (a.bf16) {
+    if (rows_of(a, 8))
+      M2RNN_CONV(step, uint16_t, 8, 4, a, state, s);
+    else
+      M2RNN_CONV(step, uint16_t, 1, 1, a, state, s);
+  } else {
+    if (rows_of(a, 4))
+      M2RNN_CONV(step, float, 4, 4, a, state, s);
+    else
+      M2RNN_CONV(step, float, 1, 1, a, state, s);
+  }
   return cudaGetLastError();
 }
 

@@ -27,6 +27,36 @@ __device__ __forceinline__ uint16_t from_f32<uint16_t>(float x) {
   return static_cast<uint16_t>(pack_bf16x2(x, 0.f) & 0xFFFFu);
 }
 
+// 2^x and 1 / x by the hardware's approximations (a few units of fp32).
+__device__ __forceinline__ float ex2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float sigmoid_fast(float x) { return rcp_fast(1.f + ex2_fast(-1.44269504f * x)); }
+
+// Two fp32 fused multiply-adds in one instruction.
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 d, {%0, %1};\n\t"
+      "fma.rn.f32x2 d, a, b, d;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+// d += a * b over kN elements, in pairs.
+template <int kN>
+__device__ __forceinline__ void fma_row(float (&d)[kN], const float (&a)[kN], const float (&b)[kN]) {
+#pragma unroll
+  for (int i = 0; i + 1 < kN; i += 2) fma2(d[i], d[i + 1], a[i], a[i + 1], b[i], b[i + 1]);
+  if constexpr (kN % 2 == 1) d[kN - 1] = fmaf(a[kN - 1], b[kN - 1], d[kN - 1]);
+}
+
 // ---------------------------------------------------------------------------
 // Short causal convolution
 // ---------------------------------------------------------------------------
@@ -55,9 +85,8 @@ struct ConvArgs {
 int conv_backward_parts(int64_t B, int64_t T);
 cudaError_t launch_conv_forward(const ConvArgs& a, cudaStream_t s);
 cudaError_t launch_conv_backward(const ConvArgs& a, cudaStream_t s);
-// state [B,W-1,C] in place; x, y [B,C].
-cudaError_t launch_conv_step(void* state, const void* x, int64_t x_stride, const void* w, const void* bias, void* y,
-                             int B, int C, int W, bool silu, bool bf16, cudaStream_t s);
+// One token: state [B,W-1,C] in place; a.x, a.y [B,C].
+cudaError_t launch_conv_step(void* state, const ConvArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
 // Selective state space scan

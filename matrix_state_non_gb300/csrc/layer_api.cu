@@ -150,9 +150,11 @@ int m2rnn_causal_conv_step(void* state, const void* x, int64_t x_stride, const v
     return M2RNN_ERR_INVALID_ARG;
   const uint64_t nx = span(B, x_stride, C, e), ny = static_cast<uint64_t>(B * C) * e, ns = ny * (W - 1);
   if (overlap(state, ns, x, nx) || overlap(state, ns, y, ny) || overlap(x, nx, y, ny)) return M2RNN_ERR_INVALID_ARG;
-  return cuda_status(launch_conv_step(state, x, x_stride, w, bias, y, static_cast<int>(B), static_cast<int>(C),
-                                      static_cast<int>(W), silu != 0, dtype == M2RNN_BF16,
-                                      static_cast<cudaStream_t>(cuda_stream)));
+  ConvArgs a{};
+  a.x = x; a.w = w; a.bias = bias; a.y = y; a.x_stride = x_stride;
+  a.B = static_cast<int>(B); a.T = 1; a.C = static_cast<int>(C); a.W = static_cast<int>(W);
+  a.silu = silu != 0; a.bf16 = dtype == M2RNN_BF16;
+  return cuda_status(launch_conv_step(state, a, static_cast<cudaStream_t>(cuda_stream)));
 }
 
 size_t m2rnn_ssm_workspace_size(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V, m2rnn_dtype dtype) {

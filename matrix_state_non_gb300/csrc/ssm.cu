@@ -86,10 +86,6 @@ __device__ void load_rows(const void* p, int64_t base, int64_t stride, int width
   }
 }
 
-__device__ __forceinline__ int seq_len(const SsmArgs& A, int b) {
-  return A.lengths ? min(max(A.lengths[b], 0), A.T) : A.T;
-}
-
 // kRev false: sum_j exp(l_L - l_j) D_j k_j v_j^T;  true: sum_i exp(l_i) q_i u_i^T.
 template <typename T, bool kRev>
 __global__ void __launch_bounds__(kThreads) ssm_chunk_sum_kernel(SsmArgs A, float* states, float* tot, int nc) {
@@ -97,7 +93,7 @@ __global__ void __launch_bounds__(kThreads) ssm_chunk_sum_kernel(SsmArgs A, floa
   __shared__ Decays dc;
   const int64_t id = blockIdx.x;
   const int c = static_cast<int>(id % nc), bn = static_cast<int>(id / nc), b = bn / A.N, n = bn % A.N;
-  const int g = n / (A.N / A.G), len = seq_len(A, b), t0 = c * kL, K = A.K, V = A.V;
+  const int g = n / (A.N / A.G), len = ssm_len(A, b), t0 = c * kL, K = A.K, V = A.V;
   float *ra = sm, *rb = sm + kL * K;
   load_decays<T>(A, b, n, t0, len, dc);
   const int64_t row = static_cast<int64_t>(b) * A.T;
@@ -151,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) ssm_chunk_out_kernel(SsmArgs A, cons
   __shared__ float P[kL][kL + 1];
   const int64_t id = blockIdx.x;
   const int c = static_cast<int>(id % nc), bn = static_cast<int>(id / nc), b = bn / A.N, n = bn % A.N;
-  const int g = n / (A.N / A.G), len = seq_len(A, b), t0 = c * kL, K = A.K, V = A.V, ld = K + 1;
+  const int g = n / (A.N / A.G), len = ssm_len(A, b), t0 = c * kL, K = A.K, V = A.V, ld = K + 1;
   float *sq = sm, *sk = sq + kL * ld, *sv = sk + kL * ld;
   const int64_t row = static_cast<int64_t>(b) * A.T;
   load_decays<T>(A, b, n, t0, len, dc);
@@ -193,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) ssm_chunk_grad_kernel(SsmArgs A, con
   __shared__ float P[kL][kL + 1], dP[kL][kL + 1], qd[kL], ck[kL], ci[kL], red[kThreads / 32];
   const int64_t id = blockIdx.x;
   const int c = static_cast<int>(id % nc), bn = static_cast<int>(id / nc), b = bn / A.N, n = bn % A.N;
-  const int g = n / (A.N / A.G), len = seq_len(A, b), t0 = c * kL, K = A.K, V = A.V, lk = K + 1, lv = V + 1;
+  const int g = n / (A.N / A.G), len = ssm_len(A, b), t0 = c * kL, K = A.K, V = A.V, lk = K + 1, lv = V + 1;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float *sq = sm, *sk = sq + kL * lk, *sv = sk + kL * lk, *su = sv + kL * lv, *sS = su + kL * lv, *sX = sS + K * lv,
         *sY = sX + kL * lk;
@@ -386,33 +382,73 @@ __global__ void __launch_bounds__(kThreads) ssm_sum_heads_kernel(const float* dq
   dk[i] = b;
 }
 
-// One token: block (b, n); thread (x, y) owns column x (+ multiples) of rows y, y + rows, ...
-template <typename T>
+// One token.  Block (b, n) streams its state through registers once: thread
+// (x, y) takes kVec columns of rows y, y + rows, ..., kAhead rows' loads in
+// flight; y_t is summed over a thread's rows, then over the y in order.  Bound
+// by HBM (8 bytes per state element) at large batches, by latency at small.
+template <typename T, int kVec>
 __global__ void __launch_bounds__(kThreads) ssm_step_kernel(float* H, SsmArgs A) {
-  __shared__ float red[kThreads];
+  constexpr int kAhead = 4;
+  __shared__ float red[kThreads * kVec];
   const int64_t bn = blockIdx.x;
   const int b = static_cast<int>(bn / A.N), n = static_cast<int>(bn % A.N), g = n / (A.N / A.G), K = A.K, V = A.V;
-  const int rows = kThreads / V, x = threadIdx.x % V, y = threadIdx.x / V;
-  const float s = to_f32(static_cast<const T*>(A.dt)[b * A.dt_stride + n]) + (A.dt_bias ? A.dt_bias[n] : 0.f);
-  const float D = softplus_f(s), a = expf(D * A.A[n]);
+  const int cols = V / kVec, rows = kThreads / cols, x = threadIdx.x % cols, y = threadIdx.x / cols;
   const T* q = static_cast<const T*>(A.q) + b * A.q_stride + static_cast<int64_t>(g) * K;
   const T* k = static_cast<const T*>(A.k) + b * A.k_stride + static_cast<int64_t>(g) * K;
-  float acc = 0.f, vx = 0.f;
+  const T* v = static_cast<const T*>(A.v) + b * A.v_stride + static_cast<int64_t>(n) * V + x * kVec;
+  const float s = to_f32(static_cast<const T*>(A.dt)[b * A.dt_stride + n]) + (A.dt_bias ? A.dt_bias[n] : 0.f);
+  const float An = A.A[n];
+  float acc[kVec], vx[kVec], D = 0.f, a = 0.f;
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) acc[e] = vx[e] = 0.f;
   if (y < rows) {
-    vx = to_f32(static_cast<const T*>(A.v)[b * A.v_stride + static_cast<int64_t>(n) * V + x]);
-    float* h = H + bn * K * V + x;
-    for (int r = y; r < K; r += rows) {
-      const float hn = fmaf(a, h[static_cast<int64_t>(r) * V], D * to_f32(k[r]) * vx);
-      h[static_cast<int64_t>(r) * V] = hn;
-      acc = fmaf(to_f32(q[r]), hn, acc);
+    float* h = H + bn * K * V + x * kVec;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) vx[e] = to_f32(v[e]);
+    for (int r0 = y; r0 < K; r0 += kAhead * rows) {
+      float st[kAhead][kVec], kr[kAhead], qr[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int r = r0 + u * rows;
+        if (r >= K) continue;
+        if constexpr (kVec == 4)
+          *reinterpret_cast<float4*>(st[u]) = *reinterpret_cast<const float4*>(h + r * V);
+        else
+          st[u][0] = h[r * V];
+        kr[u] = to_f32(k[r]);
+        qr[u] = to_f32(q[r]);
+      }
+      if (r0 == y) {  // behind the first loads
+        D = softplus_f(s);
+        a = expf(D * An);
+      }
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        const int r = r0 + u * rows;
+        if (r >= K) continue;
+        const float kd = D * kr[u];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+          st[u][e] = fmaf(a, st[u][e], kd * vx[e]);
+          acc[e] = fmaf(qr[u], st[u][e], acc[e]);
+        }
+        if constexpr (kVec == 4)
+          *reinterpret_cast<float4*>(h + r * V) = *reinterpret_cast<const float4*>(st[u]);
+        else
+          h[r * V] = st[u][0];
+      }
     }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) red[y * V + x * kVec + e] = acc[e];
   }
-  red[threadIdx.x] = acc;
   __syncthreads();
-  if (y == 0) {
-    for (int r = 1; r < rows; ++r) acc += red[r * V + x];
-    if (A.w_r) acc = fmaf(to_f32(static_cast<const T*>(A.w_r)[n * V + x]), vx, acc);
-    static_cast<T*>(A.y)[bn * V + x] = from_f32<T>(acc);
+  for (int c = threadIdx.x; c < V; c += kThreads) {
+    float t = 0.f;
+    for (int r = 0; r < min(rows, K); ++r) t += red[r * V + c];
+    if (A.w_r)
+      t = fmaf(to_f32(static_cast<const T*>(A.w_r)[n * V + c]),
+               to_f32(static_cast<const T*>(A.v)[b * A.v_stride + static_cast<int64_t>(n) * V + c]), t);
+    static_cast<T*>(A.y)[bn * V + c] = from_f32<T>(t);
   }
 }
 
@@ -478,7 +514,18 @@ cudaError_t backward_simt(const SsmArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-size_t ssm_forward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V, bool) {
+cudaError_t launch_ssm_piece_scan(float* states, const float* tot, const float* from, float* to, int nc, int KV,
+                                  int64_t chains, bool rev, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(chains), (KV + kThreads - 1) / kThreads);
+  if (rev)
+    ssm_chunk_scan_kernel<true><<<grid, kThreads, 0, s>>>(states, tot, from, to, nc, KV);
+  else
+    ssm_chunk_scan_kernel<false><<<grid, kThreads, 0, s>>>(states, tot, from, to, nc, KV);
+  return cudaGetLastError();
+}
+
+size_t ssm_forward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V, bool bf16) {
+  if (bf16) return align256(ssm_mma_forward_scratch_bytes(B, T, N, K, V));
   const size_t blocks = static_cast<size_t>(B) * N * ((T + kL - 1) / kL);
   return align256(sizeof(float) * blocks * (static_cast<size_t>(K) * V + 1));
 }
@@ -490,7 +537,7 @@ size_t ssm_backward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t G, in
 }
 
 cudaError_t launch_ssm_forward(const SsmArgs& a, cudaStream_t s) {
-  return a.bf16 ? forward_simt<uint16_t>(a, s) : forward_simt<float>(a, s);
+  return a.bf16 ? launch_ssm_mma_forward(a, s) : forward_simt<float>(a, s);
 }
 
 cudaError_t launch_ssm_backward(const SsmArgs& a, cudaStream_t s) {
@@ -499,10 +546,14 @@ cudaError_t launch_ssm_backward(const SsmArgs& a, cudaStream_t s) {
 
 cudaError_t launch_ssm_step(float* H, const SsmArgs& a, cudaStream_t s) {
   const unsigned grid = static_cast<unsigned>(a.B * a.N);
-  if (a.bf16)
-    ssm_step_kernel<uint16_t><<<grid, kThreads, 0, s>>>(H, a);
+  if (a.bf16 && a.V % 4 == 0)
+    ssm_step_kernel<uint16_t, 4><<<grid, kThreads, 0, s>>>(H, a);
+  else if (a.bf16)
+    ssm_step_kernel<uint16_t, 1><<<grid, kThreads, 0, s>>>(H, a);
+  else if (a.V % 4 == 0)
+    ssm_step_kernel<float, 4><<<grid, kThreads, 0, s>>>(H, a);
   else
-    ssm_step_kernel<float><<<grid, kThreads, 0, s>>>(H, a);
+    ssm_step_kernel<float, 1><<<grid, kThreads, 0, s>>>(H, a);
   return cudaGetLastError();
 }
 
