@@ -127,15 +127,26 @@ __global__ void __launch_bounds__(kThreads) ssm_chunk_scan_kernel(float* states,
   const int e = blockIdx.y * kThreads + threadIdx.x;
   const int64_t bn = blockIdx.x;
   if (e >= KV) return;
+  constexpr int kAhead = 8;  // pieces' loads in flight: the walk itself is one FMA a piece
   float cur = from ? from[bn * KV + e] : 0.f;
   float* st = states + bn * nc * KV + e;
   const float* tt = tot + bn * nc;
-#pragma unroll 4
-  for (int i = 0; i < nc; ++i) {
-    const int c = kRev ? nc - 1 - i : i;
-    const float u = st[static_cast<int64_t>(c) * KV];
-    st[static_cast<int64_t>(c) * KV] = cur;
-    cur = fmaf(tt[c], cur, u);
+  for (int i = 0; i < nc; i += kAhead) {
+    float u[kAhead], a[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (i + j >= nc) continue;
+      const int c = kRev ? nc - 1 - i - j : i + j;
+      u[j] = st[static_cast<int64_t>(c) * KV];
+      a[j] = tt[c];
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (i + j >= nc) continue;
+      const int c = kRev ? nc - 1 - i - j : i + j;
+      st[static_cast<int64_t>(c) * KV] = cur;
+      cur = fmaf(a[j], cur, u[j]);
+    }
   }
   if (to != nullptr) to[bn * KV + e] = cur;
 }

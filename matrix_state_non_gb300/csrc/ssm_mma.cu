@@ -1,20 +1,25 @@
 // Forward of the selective state space scan on tensor cores (bf16 inputs; the
-// mathematics in ssm.cu).  A sequence is cut into segments, enough of them to
-// fill the GPU; a block walks the chunks (64 steps) of one segment of one
-// head, on up to 64 value columns, with the state in the accumulators of its
-// warps:
-//   1. every segment but the last: the state its own steps leave, from zero;
-//   2. a scan over the segments gives the state before each;
-//   3. every segment again from there, with the outputs.
-// With one segment (enough heads) only 3 runs.  Per chunk a warp holds 16 of
-// the 64 steps as rows of Q K^T, the outputs and Q S, and a quarter of the
-// state's rows:
-//   y = diag(first) Q S + (Q K^T (*) decays) V     S, decayed scores: one bf16
-//   S = tot S + K^T diag(last D) V                 rounding each, as y has
-// The state has to stay good to fp32: the rows of K^T diag(last D) are split
-// into three bf16 parts (K, V themselves are exact), their products summed
-// from the smallest part up, and the chunk's sum added to the state by an
-// fp32 FMA, so that the tensor core's truncating adds never see the state.
+// mathematics in ssm.cu), in chunks of 64 steps.  A sequence is cut into
+// segments of chunks, enough of them to fill the GPU:
+//   1. decays of every chunk;
+//   2. a block per (head, value slice, segment) walks the segment's chunks
+//      with the state in its warps' accumulators, from zero (the first segment
+//      from H_0), and leaves the state before each chunk as bf16 operands;
+//   3. a scan over the segments: the state before each, and H_T;
+//   4. a block per (head, value slice, chunk), all independent: the outputs
+//        y_i = first_i (S^T q_i + (decay since the segment's start) S0^T q_i)
+//              + sum_j P_ij v_j + w_r (*) v_i,
+//      S the segment's own state before the chunk, S0 the state before the
+//      segment, P the decayed scores.
+// S, S0 and P take one rounding to bf16 each, as y does.  The states
+// themselves stay good to fp32: k_j exp(l_63 - l_j) D_j is split into three
+// bf16 parts (v is exact), their products are summed from the smallest part
+// up, and the chunk's sum is added to the state by an fp32 FMA, so that the
+// tensor core's truncating adds never see the running state.
+//
+// The state is held transposed, V rows by K columns: an accumulator fragment
+// of it, packed to bf16, is as it stands the B operand of Q S, so states go
+// from the walk to the outputs as fragments, without a transposition.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -26,369 +31,560 @@ namespace {
 
 constexpr int kThreads = 128;  // four warps
 
-struct WalkArgs {
+// One warp per (chain, chunk), two steps a lane; a block takes the same chunk
+// of eight heads, whose dt lie side by side.  Sums run within a block of 16
+// steps first and only from there over the blocks, each from its own end: no
+// two long sums are ever subtracted, so fp32 is enough.
+__global__ void __launch_bounds__(256) ssm_decay_kernel(SsmArgs A, ChunkDecay* out, float* tot, int nc) {
+  const int lane = threadIdx.x & 31, heads = (A.N + 7) / 8, own = lane >> 3;
+  const int n = static_cast<int>(blockIdx.x % heads) * 8 + (threadIdx.x >> 5);
+  const int64_t bc = blockIdx.x / heads;
+  const int b = static_cast<int>(bc / nc), c = static_cast<int>(bc % nc);
+  if (n >= A.N) return;
+  const int64_t id = (static_cast<int64_t>(b) * A.N + n) * nc + c;
+  const int len = ssm_len(A, b), t = c * kChunk + 2 * lane;
+  const uint16_t* p = static_cast<const uint16_t*>(A.dt) + (static_cast<int64_t>(b) * A.T + t) * A.dt_stride + n;
+  const float bias = A.dt_bias ? A.dt_bias[n] : 0.f, An = A.A[n];
+  const float D0 = t < len ? softplus_f(to_f32(p[0]) + bias) : 0.f;
+  const float D1 = t + 1 < len ? softplus_f(to_f32(p[A.dt_stride]) + bias) : 0.f;
+  const float a0 = D0 * An, a1 = D1 * An;
+  // Within the block of 16 steps: r = sum up to a step, s = sum behind it.
+  float up = a0 + a1, down = up;
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) {
+    const float x = __shfl_up_sync(0xffffffffu, up, o, 8), y = __shfl_down_sync(0xffffffffu, down, o, 8);
+    if ((lane & 7) >= o) up += x;
+    if ((lane & 7) + o < 8) down += y;
+  }
+  float before = __shfl_up_sync(0xffffffffu, up, 1, 8), behind = __shfl_down_sync(0xffffffffu, down, 1, 8);
+  if ((lane & 7) == 0) before = 0.f;
+  if ((lane & 7) == 7) behind = 0.f;
+  const float r0 = before + a0, r1 = up, s0 = behind + a1, s1 = behind;
+  float T[4];  // the blocks' sums
+#pragma unroll
+  for (int i = 0; i < 4; ++i) T[i] = __shfl_sync(0xffffffffu, up, 8 * i + 7);
+  const float base = own == 0 ? 0.f : own == 1 ? T[0] : own == 2 ? T[0] + T[1] : T[0] + T[1] + T[2];
+  const float rest = own == 3 ? 0.f : own == 2 ? T[3] : own == 1 ? T[3] + T[2] : T[3] + T[2] + T[1];
+  ChunkDecay& d = out[id];
+  const int i = 2 * lane;
+  auto put = [&](float* at, float x, float y) { *reinterpret_cast<float2*>(at + i) = make_float2(x, y); };
+  put(d.D, D0, D1);
+  put(d.rel, r0, r1);
+  put(d.row, expf(r0), expf(r1));
+  put(d.first, expf(base + r0), expf(base + r1));
+  put(d.wD, expf(s0 + rest) * D0, expf(s1 + rest) * D1);
+#pragma unroll
+  for (int ib = 1; ib < 4; ++ib) {
+    // From the end of the step's block to the start of block ib.
+    float mid = 0.f;
+#pragma unroll
+    for (int x = 1; x < ib; ++x) mid += own < x ? T[x] : 0.f;
+    const bool past = own < ib;
+    put(d.col[ib - 1], past ? expf(s0 + mid) * D0 : 0.f, past ? expf(s1 + mid) * D1 : 0.f);
+  }
+  if (lane == 0) tot[id] = expf(T[0] + T[1] + T[2] + T[3]);
+}
+
+struct ScanArgs {
   SsmArgs a;
-  const float* start;  // [B N][segs][K][V]: the state before each segment; null: H_0 (one segment)
-  float* sums;         // phase 1: [B N][segs][K][V]
-  float* tot;          // phase 1: [B N][segs]
-  int segs, per_seg;   // segments, chunks in each
-  int slices;          // of the value columns
-  bool vq, vk, vv;     // rows that asynchronous copies can take
+  const ChunkDecay* decay;  // [B N][chunks]
+  const float* tot;         // [B N][chunks]: exp(l_63)
+  float* since;             // [B N][chunks]: decay from the segment's start to the chunk's
+  uint4* local;             // [B N][slices][chunks][fragments]: a segment's own state before each chunk
+  float4* sums;             // [B N][slices][segs][2 x fragments]: the state each segment leaves
+  float* seg_tot;           // [B N][segs]
+  uint4* start;             // [B N][slices][segs][fragments]: the state before each segment
+  int nc, segs, per_seg, slices;
+  bool vq, vk, vv;          // rows that asynchronous copies can take
 };
 
-template <int KP, int VS, bool kOut>
-struct WalkSmem {
-  static constexpr int kQ = kOut ? Tile<KP>::kBytes(kChunk) : 0, kK = Tile<KP>::kBytes(kChunk),
-                       kV = Tile<VS>::kBytes(kChunk), kStage = kQ + kK + kV;
-  static constexpr int kS = kOut ? Tile<VS>::kBytes(KP) : 0;
-  static constexpr int kDecay = (sizeof(ChunkDecay) + 15) / 16 * 16;
-  static constexpr int kBytes = 2 * kStage + 2 * kS + 2 * kDecay;
+// A fragment: 16 state rows kt by 16 value columns vt, 32 lanes of 8 values
+// (k, v) = (16 kt + 8 b + 2 (lane % 4) + e, 16 vt + 8 h + lane / 4), in order
+// h, b, e: as bf16 pairs the B operands of value tiles 2 vt and 2 vt + 1.
+template <int KP, int VS>
+struct Frag {
+  static constexpr int kVt = VS / 16, kCount = (KP / 16) * kVt * 32;  // uint4 per state of a slice
+  static __device__ __forceinline__ int at(int kt, int vt, int lane) { return (kt * kVt + vt) * 32 + lane; }
 };
 
-// kOut false: phase 1.  KP: K padded to 32, 64 or 128; VS: columns of a slice.
-template <int KP, int VS, bool kOut>
-__global__ void __launch_bounds__(kThreads, KP * VS > 4096 ? 2 : 3) ssm_walk_kernel(WalkArgs W) {
-  using Sm = WalkSmem<KP, VS, kOut>;
-  constexpr int kKt = KP / 16;                                  // k-steps over the state's rows
-  constexpr int kMw = KP >= 64 ? 4 : KP / 16, kNw = 4 / kMw;    // warps along the state's rows, columns
-  constexpr int kMt = KP / 16 / kMw, kNt = VS / 8 / kNw;        // a warp's 16-row, 8-column tiles of the state
-  static_assert(kNt >= 1, "slice too narrow for the warps");
+template <int KP, int VS>
+struct WalkShape {
+  static constexpr int kNw = KP >= 64 ? 4 : KP / 16, kMw = 4 / kNw;  // warps along K (16 columns and more), V
+  static constexpr int kKt = KP / 16 / kNw;                          // a warp's 16-column tiles
+  static constexpr int kVt = VS / 16 >= kMw ? VS / 16 / kMw : 1;     // and its 16-row tiles
+  static constexpr int kK = Tile<KP>::kBytes(kChunk), kV = Tile<VS>::kBytes(kChunk), kStage = kK + kV + kChunk * 4;
+  static constexpr int kBytes = 2 * kStage;
+  static constexpr int kBlocks = KP * VS > 4096 ? 2 : 3;  // per SM (registers)
+};
+
+// Phase 2.
+template <int KP, int VS>
+__global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk_kernel(ScanArgs W) {
+  using Sh = WalkShape<KP, VS>;
+  using Fr = Frag<KP, VS>;
   extern __shared__ __align__(16) uint8_t smem[];
   const SsmArgs& A = W.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
-  const int mw = warp % kMw, nw = warp / kMw;
-  int64_t id = blockIdx.x;
-  const int seg = static_cast<int>(id % W.segs);
-  id /= W.segs;
-  const int slice = static_cast<int>(id % W.slices), bn = static_cast<int>(id / W.slices);
+  const int nw = warp % Sh::kNw, mw = warp / Sh::kNw;
+  const bool busy = mw * Sh::kVt < VS / 16;
+  const unsigned head = blockIdx.x / W.segs;  // (chain, slice)
+  const int seg = blockIdx.x - head * W.segs, bn = head / W.slices, slice = head - bn * W.slices;
   const int b = bn / A.N, n = bn % A.N, gq = n / (A.N / A.G), K = A.K, V = A.V, v0 = slice * VS;
-  if (!kOut && seg == W.segs - 1) return;
   const int len = ssm_len(A, b), width = min(VS, V - v0);
-  const int c0 = seg * W.per_seg, c1 = min((A.T + kChunk - 1) / kChunk, c0 + W.per_seg);
+  const int c0 = seg * W.per_seg, c1 = min(W.nc, c0 + W.per_seg);
   const int live = min(c1, (len + kChunk - 1) / kChunk);  // chunks with steps in them
 
-  const uint32_t base = smem_u32(smem), sS = base + 2 * Sm::kStage;
-  ChunkDecay* dec = reinterpret_cast<ChunkDecay*>(smem + 2 * Sm::kStage + 2 * Sm::kS);
-  auto decay_of = [&](int c) -> ChunkDecay& {
-    return *reinterpret_cast<ChunkDecay*>(reinterpret_cast<uint8_t*>(dec) + (c & 1) * Sm::kDecay);
-  };
+  const uint32_t base = smem_u32(smem);
   const int64_t row = static_cast<int64_t>(b) * A.T;
-  const uint16_t* pq = static_cast<const uint16_t*>(A.q) + row * A.q_stride + static_cast<int64_t>(gq) * K;
-  const uint16_t* pk = static_cast<const uint16_t*>(A.k) + row * A.k_stride + static_cast<int64_t>(gq) * K;
-  const uint16_t* pv = static_cast<const uint16_t*>(A.v) + row * A.v_stride + static_cast<int64_t>(n) * V + v0;
-  const uint16_t* pt = static_cast<const uint16_t*>(A.dt) + row * A.dt_stride + n;
-  const float An = A.A[n], bias = A.dt_bias ? A.dt_bias[n] : 0.f;
+  const TileLoader<KP, kThreads> lk{static_cast<const uint16_t*>(A.k) + row * A.k_stride + static_cast<int64_t>(gq) * K,
+                                    A.k_stride, K, W.vk};
+  const TileLoader<VS, kThreads> lv{
+      static_cast<const uint16_t*>(A.v) + row * A.v_stride + static_cast<int64_t>(n) * V + v0, A.v_stride, width, W.vv};
+  const ChunkDecay* pd = W.decay + static_cast<int64_t>(bn) * W.nc;
+  const float* ptot = W.tot + static_cast<int64_t>(bn) * W.nc;
   auto load_chunk = [&](int c) {
-    const uint32_t st = base + (c & 1) * Sm::kStage;
-    if (kOut) load_tile<KP, kThreads>(st, pq, A.q_stride, K, c * kChunk, len, W.vq);
-    load_tile<KP, kThreads>(st + Sm::kQ, pk, A.k_stride, K, c * kChunk, len, W.vk);
-    load_tile<VS, kThreads>(st + Sm::kQ + Sm::kK, pv, A.v_stride, width, c * kChunk, len, W.vv);
+    const uint32_t st = base + (c & 1) * Sh::kStage;
+    lk.load(st, c * kChunk, len);
+    lv.load(st + Sh::kK, c * kChunk, len);
+    if (tid < kChunk / 4) cp_async_16(st + Sh::kK + Sh::kV + tid * 16, pd[c].wD + tid * 4, true);
     cp_async_commit();
   };
-  // dt of a chunk, two steps a lane of warp 0 (whose row block has the fewest scores).
-  float x0 = 0.f, x1 = 0.f;
-  auto load_dt = [&](int c) {
-    const int t = c * kChunk + 2 * lane;
-    if (t < len) x0 = to_f32(pt[t * A.dt_stride]) + bias;
-    if (t + 1 < len) x1 = to_f32(pt[(t + 1) * A.dt_stride]) + bias;
-  };
-  auto make_decay = [&](int c) {
-    const int t = c * kChunk + 2 * lane;
-    chunk_decay(decay_of(c), x0, x1, t < len, t + 1 < len, An, lane);
-  };
 
-  // The state: rows (mw kMt + mt) 16 + g (+ 8), columns (nw kNt + nt) 8 + 2 q4 (+ 1).
-  float S[kMt][kNt][4];
-  const float* from = kOut ? (W.start ? W.start + (static_cast<int64_t>(bn) * W.segs + seg) * K * V
-                                      : (A.H_0 ? A.H_0 + static_cast<int64_t>(bn) * K * V : nullptr))
-                           : nullptr;
-  auto each_state = [&](auto f) {
+  // The state, transposed: rows (value columns) 16 (mw kVt + vt) + g (+ 8), columns (state
+  // rows) 16 (nw kKt + kt) + 8 b + 2 q4 (+ 1).
+  float S[Sh::kVt][Sh::kKt][2][4];
+  auto each = [&](auto f) {
 #pragma unroll
-    for (int mt = 0; mt < kMt; ++mt)
+    for (int vt = 0; vt < Sh::kVt; ++vt)
 #pragma unroll
-      for (int nt = 0; nt < kNt; ++nt)
+      for (int kt = 0; kt < Sh::kKt; ++kt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = (mw * kMt + mt) * 16 + g + (e >> 1) * 8, c = (nw * kNt + nt) * 8 + 2 * q4 + (e & 1);
-          f(S[mt][nt][e], r, c, r < K && c < width);
-        }
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int v = 16 * (mw * Sh::kVt + vt) + g + 8 * (e >> 1);
+            const int k = 16 * (nw * Sh::kKt + kt) + 8 * h + 2 * q4 + (e & 1);
+            f(S[vt][kt][h][e], k, v, busy && k < K && v < width);
+          }
   };
-  each_state([&](float& s, int r, int c, bool ok) { s = from != nullptr && ok ? from[r * V + v0 + c] : 0.f; });
-  auto store_operand = [&](int c) {  // the state before chunk c as bf16
-    const uint32_t t = sS + (c & 1) * Sm::kS;
-#pragma unroll
-    for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < kNt; ++nt) {
-        const uint32_t at = t + ((mw * kMt + mt) * 16 + g) * Tile<VS>::kPitch + ((nw * kNt + nt) * 8 + 2 * q4) * 2;
-        st_shared_b32(at, pack_bf16x2(S[mt][nt][0], S[mt][nt][1]));
-        st_shared_b32(at + 8 * Tile<VS>::kPitch, pack_bf16x2(S[mt][nt][2], S[mt][nt][3]));
-      }
-  };
+  const float* from = seg == 0 && A.H_0 ? A.H_0 + static_cast<int64_t>(bn) * K * V : nullptr;
+  each([&](float& s, int k, int v, bool ok) { s = from != nullptr && ok ? from[k * V + v0 + v] : 0.f; });
 
-  float decay = 1.f;  // over the whole segment
+  float tot = 0.f, decay = 1.f;  // of a chunk; since the segment's start
+  uint4* local = W.local + ((static_cast<int64_t>(bn) * W.slices + slice) * W.nc + c0) * Fr::kCount;
   if (c0 < live) {
     load_chunk(c0);
-    if (warp == 0) {
-      load_dt(c0);
-      make_decay(c0);
-    }
-    if (kOut) store_operand(c0);
+    tot = ptot[c0];
   }
   for (int c = c0; c < live; ++c) {
     cp_async_wait<0>();
     __syncthreads();
+    const float tot_c = tot;
     if (c + 1 < live) {
       load_chunk(c + 1);
-      if (warp == 0) load_dt(c + 1);
+      tot = ptot[c + 1];
     }
-    const uint32_t sQ = base + (c & 1) * Sm::kStage, sK = sQ + Sm::kQ, sV = sK + Sm::kK;
-    const ChunkDecay& d = decay_of(c);
-
-    uint32_t P[4][4];    // decayed scores as A operands, per 16 steps j
-    float O[VS / 8][4];  // outputs of the warp's rows
-    if (kOut) {
-      uint32_t qf[kKt][4];
+    if (slice == 0 && tid == 0) W.since[static_cast<int64_t>(bn) * W.nc + c] = decay;
+    decay *= tot_c;
+    const int stage = (c & 1) * Sh::kStage;
+    const uint32_t sK = base + stage, sV = sK + Sh::kK;
+    const float* wD = reinterpret_cast<const float*>(smem + stage + Sh::kK + Sh::kV);
+    if (busy) {
 #pragma unroll
-      for (int kt = 0; kt < kKt; ++kt) ldmatrix_x4(qf[kt], at_rows<KP>(sQ, 16 * warp, 16 * kt, lane));
-      const int i0 = 16 * warp + g, i1 = i0 + 8;
-      const float r0 = d.row[i0], r1 = d.row[i1];
+      for (int vt = 0; vt < Sh::kVt; ++vt)
+#pragma unroll
+        for (int kt = 0; kt < Sh::kKt; ++kt) {
+          const auto& s = S[vt][kt];
+          local[Fr::at(nw * Sh::kKt + kt, mw * Sh::kVt + vt, lane)] =
+              make_uint4(pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[0][2], s[0][3]),
+                         pack_bf16x2(s[1][2], s[1][3]));
+        }
+      local += Fr::kCount;
+      float U[Sh::kVt][Sh::kKt][2][4] = {};
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
-        if (jt > warp) continue;
-        float s[2][4] = {};
+        uint32_t vf[Sh::kVt][4];
 #pragma unroll
-        for (int kt = 0; kt < kKt; ++kt) {
-          uint32_t kf[4];
-          ldmatrix_x4(kf, at_cols<KP>(sK, 16 * jt, 16 * kt, lane));
-          mma_bf16_16816(s[0], qf[kt], kf[0], kf[1]);
-          mma_bf16_16816(s[1], qf[kt], kf[2], kf[3]);
-        }
+        for (int vt = 0; vt < Sh::kVt; ++vt)
+          ldmatrix_x4_trans(vf[vt], at_cols<VS>(sV, 16 * jt, 16 * (mw * Sh::kVt + vt), lane));
+        const int j = 16 * jt + 2 * q4;
+        const float2 wa = *reinterpret_cast<const float2*>(&wD[j]), wb = *reinterpret_cast<const float2*>(&wD[j + 8]);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int j = 16 * jt + 8 * h + 2 * q4;
-          const float2 D = *reinterpret_cast<const float2*>(&d.D[j]);
-          if (jt < warp) {
-            const float2 cf = *reinterpret_cast<const float2*>(&d.col[warp][j]);
-            const float f0 = cf.x * D.x, f1 = cf.y * D.y;
-            P[jt][2 * h] = pack_bf16x2(s[h][0] * (r0 * f0), s[h][1] * (r0 * f1));
-            P[jt][2 * h + 1] = pack_bf16x2(s[h][2] * (r1 * f0), s[h][3] * (r1 * f1));
-          } else {
-            const float2 hj = *reinterpret_cast<const float2*>(&d.hi[j]);
-            const float2 lj = *reinterpret_cast<const float2*>(&d.lo[j]);
-            const float h0 = d.hi[i0], l0 = d.lo[i0], h1 = d.hi[i1], l1 = d.lo[i1];
-            const float p0 = j <= i0 ? s[h][0] * (exp_diff(h0 - hj.x, l0 - lj.x) * D.x) : 0.f;
-            const float p1 = j + 1 <= i0 ? s[h][1] * (exp_diff(h0 - hj.y, l0 - lj.y) * D.y) : 0.f;
-            const float p2 = j <= i1 ? s[h][2] * (exp_diff(h1 - hj.x, l1 - lj.x) * D.x) : 0.f;
-            const float p3 = j + 1 <= i1 ? s[h][3] * (exp_diff(h1 - hj.y, l1 - lj.y) * D.y) : 0.f;
-            P[jt][2 * h] = pack_bf16x2(p0, p1);
-            P[jt][2 * h + 1] = pack_bf16x2(p2, p3);
+        for (int kt = 0; kt < Sh::kKt; ++kt) {
+          uint32_t kf[4], hi[4], mid[4], lo[4];
+          ldmatrix_x4_trans(kf, at_rows<KP>(sK, 16 * jt, 16 * (nw * Sh::kKt + kt), lane));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const float2 w = r & 1 ? wb : wa;
+            split3(bf16lo(kf[r]) * w.x, bf16hi(kf[r]) * w.y, hi[r], mid[r], lo[r]);
           }
+#pragma unroll
+          for (int vt = 0; vt < Sh::kVt; ++vt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) mma_bf16_16816(U[vt][kt][h], vf[vt], lo[2 * h], lo[2 * h + 1]);
+#pragma unroll
+          for (int vt = 0; vt < Sh::kVt; ++vt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) mma_bf16_16816(U[vt][kt][h], vf[vt], mid[2 * h], mid[2 * h + 1]);
+#pragma unroll
+          for (int vt = 0; vt < Sh::kVt; ++vt)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) mma_bf16_16816(U[vt][kt][h], vf[vt], hi[2 * h], hi[2 * h + 1]);
         }
       }
-      // Q S
-      const uint32_t st = sS + (c & 1) * Sm::kS;
 #pragma unroll
-      for (int nt = 0; nt < VS / 8; ++nt)
+      for (int vt = 0; vt < Sh::kVt; ++vt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) O[nt][e] = 0.f;
+        for (int kt = 0; kt < Sh::kKt; ++kt)
 #pragma unroll
-      for (int kt = 0; kt < kKt; ++kt)
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int np = 0; np < VS / 16; ++np) {
-          uint32_t sf[4];
-          ldmatrix_x4_trans(sf, at_rows<VS>(st, 16 * kt, 16 * np, lane));
-          mma_bf16_16816(O[2 * np], qf[kt], sf[0], sf[1]);
-          mma_bf16_16816(O[2 * np + 1], qf[kt], sf[2], sf[3]);
-        }
-      const float e0 = d.first[i0], e1 = d.first[i1];
-#pragma unroll
-      for (int nt = 0; nt < VS / 8; ++nt) {
-        O[nt][0] *= e0;
-        O[nt][1] *= e0;
-        O[nt][2] *= e1;
-        O[nt][3] *= e1;
-      }
-    }
-
-    // The scores times V, and the chunk's own state.
-    float U[kMt][kNt][4];
-#pragma unroll
-    for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) U[mt][nt][e] = 0.f;
-#pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-      uint32_t vf[VS / 16][4];
-#pragma unroll
-      for (int np = 0; np < VS / 16; ++np) ldmatrix_x4_trans(vf[np], at_rows<VS>(sV, 16 * jt, 16 * np, lane));
-      if (kOut && jt <= warp) {
-#pragma unroll
-        for (int np = 0; np < VS / 16; ++np) {
-          mma_bf16_16816(O[2 * np], P[jt], vf[np][0], vf[np][1]);
-          mma_bf16_16816(O[2 * np + 1], P[jt], vf[np][2], vf[np][3]);
-        }
-      }
-      const int j = 16 * jt + 2 * q4;
-      const float2 wa = *reinterpret_cast<const float2*>(&d.last[j]), wb = *reinterpret_cast<const float2*>(&d.last[j + 8]);
-      const float2 Da = *reinterpret_cast<const float2*>(&d.D[j]), Db = *reinterpret_cast<const float2*>(&d.D[j + 8]);
-      const float w0 = wa.x * Da.x, w1 = wa.y * Da.y, w2 = wb.x * Db.x, w3 = wb.y * Db.y;
-#pragma unroll
-      for (int mt = 0; mt < kMt; ++mt) {
-        uint32_t kf[4], hi[4], mid[4], lo[4];
-        ldmatrix_x4_trans(kf, at_cols<KP>(sK, 16 * jt, (mw * kMt + mt) * 16, lane));
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-          split3(bf16lo(kf[r]) * (r < 2 ? w0 : w2), bf16hi(kf[r]) * (r < 2 ? w1 : w3), hi[r], mid[r], lo[r]);
-#pragma unroll
-        for (int nt = 0; nt < kNt; ++nt) {
-          constexpr int kHalf = kNw == 1 ? 0 : kNt;  // the second column half's first tile
-          const int o = nt + kHalf;
-          const uint32_t b0 = kNw == 1 || nw == 0 ? vf[nt / 2][2 * (nt & 1)] : vf[o / 2][2 * (o & 1)];
-          const uint32_t b1 = kNw == 1 || nw == 0 ? vf[nt / 2][2 * (nt & 1) + 1] : vf[o / 2][2 * (o & 1) + 1];
-          mma_bf16_16816(U[mt][nt], lo, b0, b1);
-          mma_bf16_16816(U[mt][nt], mid, b0, b1);
-          mma_bf16_16816(U[mt][nt], hi, b0, b1);
-        }
-      }
-    }
-#pragma unroll
-    for (int mt = 0; mt < kMt; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < kNt; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) S[mt][nt][e] = fmaf(d.tot, S[mt][nt][e], U[mt][nt][e]);
-    if (!kOut) decay *= d.tot;
-
-    if (c + 1 < live) {
-      if (kOut) store_operand(c + 1);
-      if (warp == 0) make_decay(c + 1);
-    }
-    if (kOut) {
-      // y = O + w_r v, rounded to bf16
-      uint16_t* y = static_cast<uint16_t*>(A.y);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int i = 16 * warp + g + 8 * h, t = c * kChunk + i;
-        if (t >= A.T) continue;
-        uint16_t* yr = y + ((row + t) * A.N + n) * V + v0;
-#pragma unroll
-        for (int nt = 0; nt < VS / 8; ++nt) {
-          const int col = 8 * nt + 2 * q4;
-          float a0 = O[nt][2 * h], a1 = O[nt][2 * h + 1];
-          if (A.w_r != nullptr) {
-            const uint32_t vv = ld_shared_b32(sV + i * Tile<VS>::kPitch + col * 2);
-            const uint16_t* wr = static_cast<const uint16_t*>(A.w_r) + n * V + v0;
-            if (col < width) a0 = fmaf(to_f32(wr[col]), bf16lo(vv), a0);
-            if (col + 1 < width) a1 = fmaf(to_f32(wr[col + 1]), bf16hi(vv), a1);
-          }
-          uint32_t r = pack_bf16x2(a0, a1);
-          if (t >= len) r = 0u;
-          if (W.vv) {  // width a multiple of 8
-            if (col < width) *reinterpret_cast<uint32_t*>(yr + col) = r;
-          } else {
-            if (col < width) yr[col] = static_cast<uint16_t>(r);
-            if (col + 1 < width) yr[col + 1] = static_cast<uint16_t>(r >> 16);
-          }
-        }
-      }
+            for (int e = 0; e < 4; ++e) S[vt][kt][h][e] = fmaf(tot_c, S[vt][kt][h][e], U[vt][kt][h][e]);
     }
   }
-  if (kOut) {
-    // Chunks behind the sequence's end: zero outputs.
-    uint16_t* y = static_cast<uint16_t*>(A.y);
-    const int t0 = max(c0, live) * kChunk, t1 = min(A.T, c1 * kChunk);
-    for (int e = tid; e < (t1 - t0) * width; e += kThreads)
-      y[((row + t0 + e / width) * A.N + n) * V + v0 + e % width] = 0;
-    if (A.H_T != nullptr && seg == W.segs - 1)
-      each_state([&](float& s, int r, int c, bool ok) {
-        if (ok) A.H_T[static_cast<int64_t>(bn) * K * V + r * V + v0 + c] = s;
+  if (W.segs == 1) {
+    if (A.H_T != nullptr)
+      each([&](float& s, int k, int v, bool ok) {
+        if (ok) A.H_T[static_cast<int64_t>(bn) * K * V + k * V + v0 + v] = s;
       });
-  } else {
-    float* to = W.sums + (static_cast<int64_t>(bn) * W.segs + seg) * K * V;
-    each_state([&](float& s, int r, int c, bool ok) {
-      if (ok) to[r * V + v0 + c] = s;
-    });
-    if (tid == 0 && slice == 0) W.tot[static_cast<int64_t>(bn) * W.segs + seg] = decay;
+    return;
   }
+  if (busy) {
+    float4* to = W.sums + ((static_cast<int64_t>(bn) * W.slices + slice) * W.segs + seg) * (2 * Fr::kCount);
+#pragma unroll
+    for (int vt = 0; vt < Sh::kVt; ++vt)
+#pragma unroll
+      for (int kt = 0; kt < Sh::kKt; ++kt) {
+        const auto& s = S[vt][kt];
+        const int at = Fr::at(nw * Sh::kKt + kt, mw * Sh::kVt + vt, lane);
+        to[2 * at] = make_float4(s[0][0], s[0][1], s[1][0], s[1][1]);
+        to[2 * at + 1] = make_float4(s[0][2], s[0][3], s[1][2], s[1][3]);
+      }
+  }
+  if (tid == 0 && slice == 0) W.seg_tot[static_cast<int64_t>(bn) * W.segs + seg] = decay;
 }
 
-int padded_rows(int K) { return K <= 32 ? 32 : K <= 64 ? 64 : 128; }
-int slice_cols(int V) { return V <= 16 ? 16 : V <= 32 ? 32 : 64; }
-
-struct Plan {
-  int slices, segs, per_seg;
-};
-
-// Segments: as many as the GPU holds blocks at once, where that is two or
-// more per head; a single one costs no first phase.
-Plan make_plan(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
-  Plan p{};
-  const int vs = slice_cols(static_cast<int>(V));
-  p.slices = static_cast<int>((V + vs - 1) / vs);
-  const int64_t chains = B * N * p.slices, room = 152 * (padded_rows(static_cast<int>(K)) * vs > 4096 ? 2 : 3);
-  const int64_t nc = (T + kChunk - 1) / kChunk;
-  int64_t segs = room / chains;
-  segs = segs < 1 ? 1 : segs > nc ? nc : segs;
-  p.per_seg = static_cast<int>((nc + segs - 1) / segs);
-  p.segs = static_cast<int>((nc + p.per_seg - 1) / p.per_seg);
-  return p;
+// Phase 3: block (chain and slice, 256 halves of fragments); thread (fragment, h).
+template <int KP, int VS>
+__global__ void __launch_bounds__(256) ssm_segment_scan_kernel(ScanArgs W) {
+  using Fr = Frag<KP, VS>;
+  constexpr int kAhead = 8, kN = 2 * Fr::kCount;
+  const SsmArgs& A = W.a;
+  const int e = blockIdx.y * 256 + threadIdx.x;
+  if (e >= kN) return;
+  const int64_t bn = blockIdx.x / W.slices;
+  const int slice = blockIdx.x % W.slices;
+  const float4* sums = W.sums + static_cast<int64_t>(blockIdx.x) * W.segs * kN + e;
+  uint2* start = reinterpret_cast<uint2*>(W.start) + static_cast<int64_t>(blockIdx.x) * W.segs * kN + e;
+  const float* tot = W.seg_tot + bn * W.segs;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < W.segs; i += kAhead) {
+    float4 u[kAhead];
+    float a[kAhead];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (i + j >= W.segs) continue;
+      u[j] = sums[static_cast<int64_t>(i + j) * kN];
+      a[j] = tot[i + j];
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      if (i + j >= W.segs) continue;
+      start[static_cast<int64_t>(i + j) * kN] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+      s = make_float4(fmaf(a[j], s.x, u[j].x), fmaf(a[j], s.y, u[j].y), fmaf(a[j], s.z, u[j].z),
+                      fmaf(a[j], s.w, u[j].w));
+    }
+  }
+  if (A.H_T == nullptr) return;
+  const int lane = (e >> 1) & 31, tile = e >> 6, vt = tile % Fr::kVt, kt = tile / Fr::kVt;
+  const int v = slice * VS + 16 * vt + 8 * (e & 1) + (lane >> 2), k = 16 * kt + 2 * (lane & 3);
+  if (v >= A.V) return;
+  float* H = A.H_T + bn * A.K * A.V + v;
+  const float x[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int kk = k + 8 * (r >> 1) + (r & 1);
+    if (kk < A.K) H[kk * A.V] = x[r];
+  }
 }
 
 template <int KP, int VS>
-cudaError_t run(const WalkArgs& w, int64_t chains, cudaStream_t s) {
-  using Out = WalkSmem<KP, VS, true>;
-  using Sum = WalkSmem<KP, VS, false>;
-  cudaError_t e = cudaFuncSetAttribute(ssm_walk_kernel<KP, VS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Out::kBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(ssm_walk_kernel<KP, VS, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Sum::kBytes);
-  if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>(chains * w.slices * w.segs);
-  if (w.segs > 1) {
-    ssm_walk_kernel<KP, VS, false><<<grid, kThreads, Sum::kBytes, s>>>(w);
-    e = launch_ssm_piece_scan(w.sums, w.tot, w.a.H_0, nullptr, w.segs, w.a.K * w.a.V, chains, false, s);
-    if (e != cudaSuccess) return e;
+struct OutShape {
+  static constexpr int kQ = Tile<KP>::kBytes(kChunk), kV = Tile<VS>::kBytes(kChunk), kS = Frag<KP, VS>::kCount * 16;
+  static constexpr int kBytes = 2 * kQ + kV + static_cast<int>(sizeof(ChunkDecay)) + 2 * kS + VS * 4;
+  static constexpr int kBlocks = KP * VS > 4096 ? 2 : 4;
+};
+
+// Phase 4.
+template <int KP, int VS>
+__global__ void __launch_bounds__(kThreads, OutShape<KP, VS>::kBlocks) ssm_out_kernel(ScanArgs W) {
+  using Sh = OutShape<KP, VS>;
+  using Fr = Frag<KP, VS>;
+  static_assert(VS <= KP, "outputs pass through the q tile");
+  constexpr int kKt = KP / 16;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const SsmArgs& A = W.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
+  const unsigned head = blockIdx.x / W.nc;  // (chain, slice)
+  const int c = blockIdx.x - head * W.nc, bn = head / W.slices, slice = head - bn * W.slices;
+  const int b = bn / A.N, n = bn % A.N, gq = n / (A.N / A.G), K = A.K, V = A.V, v0 = slice * VS;
+  const int len = ssm_len(A, b), width = min(VS, V - v0), t0 = c * kChunk, seg = c / W.per_seg;
+  const int64_t row = static_cast<int64_t>(b) * A.T;
+  uint16_t* y = static_cast<uint16_t*>(A.y) + ((row + t0) * A.N + n) * V + v0;
+  const int64_t y_stride = static_cast<int64_t>(A.N) * V;
+  if (t0 >= len) {  // behind the sequence's end
+    for (int e = tid; e < min(kChunk, A.T - t0) * width; e += kThreads) y[(e / width) * y_stride + e % width] = 0;
+    return;
   }
-  ssm_walk_kernel<KP, VS, true><<<grid, kThreads, Out::kBytes, s>>>(w);
+  const uint32_t sQ = smem_u32(smem), sK = sQ + Sh::kQ, sV = sK + Sh::kQ, sD = sV + Sh::kV,
+                 sS = sD + static_cast<uint32_t>(sizeof(ChunkDecay));
+  const ChunkDecay& d = *reinterpret_cast<const ChunkDecay*>(smem + 2 * Sh::kQ + Sh::kV);
+  const uint4* fS = reinterpret_cast<const uint4*>(smem + 2 * Sh::kQ + Sh::kV + sizeof(ChunkDecay));
+  float* s_wr = reinterpret_cast<float*>(smem + 2 * Sh::kQ + Sh::kV + sizeof(ChunkDecay) + 2 * Sh::kS);
+  const TileLoader<KP, kThreads> lq{static_cast<const uint16_t*>(A.q) + row * A.q_stride + static_cast<int64_t>(gq) * K,
+                                    A.q_stride, K, W.vq};
+  const TileLoader<KP, kThreads> lk{static_cast<const uint16_t*>(A.k) + row * A.k_stride + static_cast<int64_t>(gq) * K,
+                                    A.k_stride, K, W.vk};
+  const TileLoader<VS, kThreads> lv{
+      static_cast<const uint16_t*>(A.v) + row * A.v_stride + static_cast<int64_t>(n) * V + v0, A.v_stride, width, W.vv};
+  const bool more = seg > 0;  // a state before the segment
+  lq.load(sQ, t0, len);
+  lk.load(sK, t0, len);
+  const int64_t at = static_cast<int64_t>(bn) * W.nc + c;
+  cp_async_16(sD + tid * 16, reinterpret_cast<const uint8_t*>(W.decay + at) + tid * 16, true);
+  cp_async_commit();
+  {
+    const uint4* l = W.local + ((static_cast<int64_t>(bn) * W.slices + slice) * W.nc + c) * Fr::kCount;
+    const uint4* s = W.start + ((static_cast<int64_t>(bn) * W.slices + slice) * W.segs + seg) * Fr::kCount;
+#pragma unroll
+    for (int e = tid; e < Fr::kCount; e += kThreads) cp_async_16(sS + e * 16, l + e, true);
+    if (more) {
+#pragma unroll
+      for (int e = tid; e < Fr::kCount; e += kThreads) cp_async_16(sS + Sh::kS + e * 16, s + e, true);
+    }
+  }
+  lv.load(sV, t0, len);
+  cp_async_commit();
+  const float since = more ? W.since[at] : 0.f;
+  for (int e = tid; e < VS; e += kThreads)
+    s_wr[e] = A.w_r != nullptr && e < width ? to_f32(static_cast<const uint16_t*>(A.w_r)[n * V + v0 + e]) : 0.f;
+  cp_async_wait<1>();
+  __syncthreads();
+
+  uint32_t qf[kKt][4], P[4][4];  // q; decayed scores as A operands, per 16 steps j
+#pragma unroll
+  for (int kt = 0; kt < kKt; ++kt) ldmatrix_x4(qf[kt], at_rows<KP>(sQ, 16 * warp, 16 * kt, lane));
+  const int i0 = 16 * warp + g, i1 = i0 + 8;
+  {
+    const float r0 = d.row[i0], r1 = d.row[i1], l0 = d.rel[i0], l1 = d.rel[i1];
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+      if (jt > warp) continue;
+      float s[2][4] = {};
+#pragma unroll
+      for (int kt = 0; kt < kKt; ++kt) {
+        uint32_t kf[4];
+        ldmatrix_x4(kf, at_cols<KP>(sK, 16 * jt, 16 * kt, lane));
+        mma_bf16_16816(s[0], qf[kt], kf[0], kf[1]);
+        mma_bf16_16816(s[1], qf[kt], kf[2], kf[3]);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int j = 16 * jt + 8 * h + 2 * q4;
+        if (jt < warp) {
+          const float2 cf = *reinterpret_cast<const float2*>(&d.col[warp - 1][j]);
+          P[jt][2 * h] = pack_bf16x2(s[h][0] * (r0 * cf.x), s[h][1] * (r0 * cf.y));
+          P[jt][2 * h + 1] = pack_bf16x2(s[h][2] * (r1 * cf.x), s[h][3] * (r1 * cf.y));
+        } else {
+          const float2 D = *reinterpret_cast<const float2*>(&d.D[j]);
+          const float2 lj = *reinterpret_cast<const float2*>(&d.rel[j]);
+          const float p0 = j <= i0 ? s[h][0] * (exp_fast(l0 - lj.x) * D.x) : 0.f;
+          const float p1 = j + 1 <= i0 ? s[h][1] * (exp_fast(l0 - lj.y) * D.y) : 0.f;
+          const float p2 = j <= i1 ? s[h][2] * (exp_fast(l1 - lj.x) * D.x) : 0.f;
+          const float p3 = j + 1 <= i1 ? s[h][3] * (exp_fast(l1 - lj.y) * D.y) : 0.f;
+          P[jt][2 * h] = pack_bf16x2(p0, p1);
+          P[jt][2 * h + 1] = pack_bf16x2(p2, p3);
+        }
+      }
+    }
+  }
+  cp_async_wait<0>();
+  __syncthreads();
+  float O[VS / 8][4] = {};
+  auto add_state = [&](const uint4* f) {
+#pragma unroll
+    for (int kt = 0; kt < kKt; ++kt)
+#pragma unroll
+      for (int vt = 0; vt < VS / 16; ++vt) {
+        const uint4 s = f[Fr::at(kt, vt, lane)];
+        mma_bf16_16816(O[2 * vt], qf[kt], s.x, s.y);
+        mma_bf16_16816(O[2 * vt + 1], qf[kt], s.z, s.w);
+      }
+  };
+  if (more) {
+    add_state(fS + Fr::kCount);
+#pragma unroll
+    for (int nt = 0; nt < VS / 8; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) O[nt][e] *= since;
+  }
+  add_state(fS);
+  const float e0 = d.first[i0], e1 = d.first[i1];
+#pragma unroll
+  for (int nt = 0; nt < VS / 8; ++nt) {
+    O[nt][0] *= e0;
+    O[nt][1] *= e0;
+    O[nt][2] *= e1;
+    O[nt][3] *= e1;
+  }
+#pragma unroll
+  for (int jt = 0; jt < 4; ++jt) {
+    if (jt > warp) continue;
+#pragma unroll
+    for (int vt = 0; vt < VS / 16; ++vt) {
+      uint32_t vf[4];
+      ldmatrix_x4_trans(vf, at_rows<VS>(sV, 16 * jt, 16 * vt, lane));
+      mma_bf16_16816(O[2 * vt], P[jt], vf[0], vf[1]);
+      mma_bf16_16816(O[2 * vt + 1], P[jt], vf[2], vf[3]);
+    }
+  }
+  // y = O + w_r v, rounded to bf16, by way of the warp's own rows of the q tile.
+  __syncwarp();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = 16 * warp + g + 8 * h;
+#pragma unroll
+    for (int nt = 0; nt < VS / 8; ++nt) {
+      const int col = 8 * nt + 2 * q4;
+      const uint32_t vv = ld_shared_b32(sV + i * Tile<VS>::kPitch + col * 2);
+      const float2 wr = *reinterpret_cast<const float2*>(&s_wr[col]);
+      st_shared_b32(sQ + i * Tile<KP>::kPitch + col * 2,
+                    pack_bf16x2(fmaf(wr.x, bf16lo(vv), O[nt][2 * h]), fmaf(wr.y, bf16hi(vv), O[nt][2 * h + 1])));
+    }
+  }
+  __syncwarp();
+  constexpr int kPer = VS / 8;  // 16-byte pieces of a row
+#pragma unroll
+  for (int e = lane; e < 16 * kPer; e += 32) {
+    const int i = 16 * warp + e / kPer, col = (e % kPer) * 8, t = t0 + i;
+    if (t >= A.T || col >= width) continue;
+    const uint4 r = t < len ? ld_shared_v4(sQ + i * Tile<KP>::kPitch + col * 2) : make_uint4(0u, 0u, 0u, 0u);
+    uint16_t* yr = y + i * y_stride + col;
+    if (V % 8 == 0) {
+      *reinterpret_cast<uint4*>(yr) = r;
+    } else {
+      const uint32_t x[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (col + u < width) yr[u] = static_cast<uint16_t>(x[u / 2] >> (16 * (u & 1)));
+    }
+  }
+}
+
+int padded_rows(int64_t K) { return K <= 32 ? 32 : K <= 64 ? 64 : 128; }
+int slice_cols(int64_t K, int64_t V) { return V <= 16 ? 16 : V <= 32 || K <= 32 ? 32 : 64; }
+
+struct Plan {
+  int kp, vs, slices, segs, per_seg, nc;
+};
+
+// Segments: as many as the GPU holds walking blocks at once.
+Plan make_plan(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
+  Plan p{};
+  p.kp = padded_rows(K);
+  p.vs = slice_cols(K, V);
+  p.slices = static_cast<int>((V + p.vs - 1) / p.vs);
+  p.nc = static_cast<int>((T + kChunk - 1) / kChunk);
+  const int64_t chains = B * N * p.slices, room = 152 * (p.kp * p.vs > 4096 ? 2 : 3);
+  int64_t segs = room / chains;
+  segs = segs < 1 ? 1 : segs > p.nc ? p.nc : segs;
+  p.per_seg = static_cast<int>((p.nc + segs - 1) / segs);
+  p.segs = (p.nc + p.per_seg - 1) / p.per_seg;
+  return p;
+}
+
+// Scratch, in bytes, each on a 16-byte boundary.
+struct Layout {
+  size_t decay, tot, since, local, sums, seg_tot, start, total;
+};
+
+Layout make_layout(const Plan& p, int64_t chains) {
+  Layout l{};
+  auto take = [&](size_t bytes) {
+    const size_t at = l.total;
+    l.total += (bytes + 15) / 16 * 16;
+    return at;
+  };
+  const size_t state = static_cast<size_t>(p.kp) * p.vs, chunks = static_cast<size_t>(chains) * p.nc,
+               segs = static_cast<size_t>(chains) * p.segs;
+  l.decay = take(chunks * sizeof(ChunkDecay));
+  l.tot = take(chunks * 4);
+  l.since = take(chunks * 4);
+  l.local = take(chunks * p.slices * state * 2);
+  if (p.segs > 1) {
+    l.sums = take(segs * p.slices * state * 4);
+    l.seg_tot = take(segs * 4);
+    l.start = take(segs * p.slices * state * 2);
+  }
+  return l;
+}
+
+template <int KP, int VS>
+cudaError_t run(const ScanArgs& w, int64_t chains, cudaStream_t s) {
+  using Walk = WalkShape<KP, VS>;
+  using Out = OutShape<KP, VS>;
+  cudaError_t e =
+      cudaFuncSetAttribute(ssm_walk_kernel<KP, VS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Walk::kBytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(ssm_out_kernel<KP, VS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Out::kBytes);
+  if (e != cudaSuccess) return e;
+  const int64_t heads = chains * w.slices;
+  ssm_walk_kernel<KP, VS><<<static_cast<unsigned>(heads * w.segs), kThreads, Walk::kBytes, s>>>(w);
+  if (w.segs > 1)
+    ssm_segment_scan_kernel<KP, VS>
+        <<<dim3(static_cast<unsigned>(heads), (2 * Frag<KP, VS>::kCount + 255) / 256), 256, 0, s>>>(w);
+  ssm_out_kernel<KP, VS><<<static_cast<unsigned>(heads * w.nc), kThreads, Out::kBytes, s>>>(w);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t ssm_mma_forward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
-  const Plan p = make_plan(B, T, N, K, V);
-  if (p.segs == 1) return 16;
-  return sizeof(float) * static_cast<size_t>(B) * N * p.segs * (static_cast<size_t>(K) * V + 1);
+  return make_layout(make_plan(B, T, N, K, V), B * N).total;
 }
 
 cudaError_t launch_ssm_mma_forward(const SsmArgs& a, cudaStream_t s) {
   const Plan p = make_plan(a.B, a.T, a.N, a.K, a.V);
   const int64_t chains = static_cast<int64_t>(a.B) * a.N;
-  WalkArgs w{};
+  const Layout l = make_layout(p, chains);
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  ChunkDecay* decay = reinterpret_cast<ChunkDecay*>(ws + l.decay);
+  float* tot = reinterpret_cast<float*>(ws + l.tot);
+  ScanArgs w{};
   w.a = a;
+  w.decay = decay;
+  w.tot = tot;
+  w.since = reinterpret_cast<float*>(ws + l.since);
+  w.local = reinterpret_cast<uint4*>(ws + l.local);
+  w.sums = reinterpret_cast<float4*>(ws + l.sums);
+  w.seg_tot = reinterpret_cast<float*>(ws + l.seg_tot);
+  w.start = reinterpret_cast<uint4*>(ws + l.start);
+  w.nc = p.nc;
   w.segs = p.segs;
   w.per_seg = p.per_seg;
   w.slices = p.slices;
-  if (p.segs > 1) {
-    w.sums = static_cast<float*>(a.ws);
-    w.tot = w.sums + chains * p.segs * a.K * a.V;
-    w.start = w.sums;
-  }
   auto vec = [](const void* p, int64_t stride, int width) {
     return width % 8 == 0 && stride % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
   };
   w.vq = vec(a.q, a.q_stride, a.K);
   w.vk = vec(a.k, a.k_stride, a.K);
   w.vv = vec(a.v, a.v_stride, a.V);
-  const int kp = padded_rows(a.K), vs = slice_cols(a.V);
+  const int64_t blocks = static_cast<int64_t>(a.B) * p.nc * ((a.N + 7) / 8);
+  ssm_decay_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(a, decay, tot, p.nc);
 #define M2RNN_SSM_CASE(KP, VS) \
-  if (kp == KP && vs == VS) return run<KP, VS>(w, chains, s);
+  if (p.kp == KP && p.vs == VS) return run<KP, VS>(w, chains, s);
   M2RNN_SSM_CASE(32, 16)
   M2RNN_SSM_CASE(32, 32)
-  M2RNN_SSM_CASE(32, 64)
   M2RNN_SSM_CASE(64, 16)
   M2RNN_SSM_CASE(64, 32)
   M2RNN_SSM_CASE(64, 64)

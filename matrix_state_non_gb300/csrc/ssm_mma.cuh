@@ -28,30 +28,40 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
-// Rows t0 .. t0 + 63 of one head into a tile: `width` columns of it are there,
-// steps behind `len` and columns behind `width` become zero.  vec: rows on
-// 16-byte boundaries and width a multiple of 8 (asynchronous copies);
-// otherwise element by element.
+// Copies the 64 rows of a chunk of one head into a tile, chunk after chunk:
+// `width` columns are there, steps behind `len` and columns behind `width`
+// become zero.  vec: rows on 16-byte boundaries and width a multiple of 8
+// (asynchronous copies); otherwise element by element.
 template <int kCols, int kThreads>
-__device__ __forceinline__ void load_tile(uint32_t tile, const uint16_t* p, int64_t stride, int width, int t0, int len,
-                                          bool vec) {
-  if (vec) {
-    constexpr int kPer = kCols / 8;
+struct TileLoader {
+  static constexpr int kPer = kCols / 8, kStep = kThreads / kPer;  // 16-byte pieces of a row; rows apart
+  const uint16_t* p;
+  int64_t stride;
+  int width;
+  bool vec;
+
+  __device__ __forceinline__ void load(uint32_t tile, int t0, int len) const {
+    if (vec) {
+      const int r = threadIdx.x / kPer, c = (threadIdx.x % kPer) * 8;
+      const uint16_t* src = p + static_cast<int64_t>(t0 + r) * stride + c;
+      uint32_t dst = tile + r * Tile<kCols>::kPitch + c * 2;
+      const int live = c < width ? len - t0 - r : 0;
 #pragma unroll
-    for (int i = 0; i < kChunk * kPer / kThreads; ++i) {
-      const int e = i * kThreads + threadIdx.x, r = e / kPer, c = (e % kPer) * 8;
-      const bool ok = t0 + r < len && c < width;
-      cp_async_16(tile + r * Tile<kCols>::kPitch + c * 2, ok ? p + (t0 + r) * stride + c : p, ok);
-    }
-  } else {
+      for (int i = 0; i < kChunk / kStep; ++i) {
+        const bool ok = i * kStep < live;
+        cp_async_16(dst + i * kStep * Tile<kCols>::kPitch, ok ? src : p, ok);
+        src += kStep * stride;
+      }
+    } else {
 #pragma unroll 4
-    for (int e = threadIdx.x; e < kChunk * kCols; e += kThreads) {
-      const int r = e / kCols, c = e % kCols;
-      const uint16_t x = t0 + r < len && c < width ? p[(t0 + r) * stride + c] : uint16_t(0);
-      asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile + r * Tile<kCols>::kPitch + c * 2), "h"(x) : "memory");
+      for (int e = threadIdx.x; e < kChunk * kCols; e += kThreads) {
+        const int r = e / kCols, c = e % kCols;
+        const uint16_t x = t0 + r < len && c < width ? p[static_cast<int64_t>(t0 + r) * stride + c] : uint16_t(0);
+        asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile + r * Tile<kCols>::kPitch + c * 2), "h"(x) : "memory");
+      }
     }
   }
-}
+};
 
 // ldmatrix addresses within a tile, block (r0, c0) of 16 x 16 elements:
 // in order (rows 0-7, cols 0-7), (rows 8-15, cols 0-7), (0-7, 8-15), (8-15, 8-15).
@@ -78,57 +88,22 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t& hi, uint32_t&
   lo = pack_bf16x2(x - bf16lo(mid), y - bf16hi(mid));
 }
 
-// The decays of one chunk, in shared memory.  l_i is the sum of D A over the
-// chunk's steps up to i; the factor exp(l_i - l_j) of row block ib and an
-// earlier step j is row[i] col[ib][j] with the sum before the block as the
-// reference, so a chunk takes a few hundred exponentials and not 64 x 64.
-struct ChunkDecay {
-  float hi[kChunk], lo[kChunk];  // l_i in two parts: differences of long sums keep their bits
-  float D[kChunk];               // step sizes (0 behind the sequence's end)
-  float first[kChunk];           // exp(l_i)
-  float last[kChunk];            // exp(l_63 - l_i)
-  float row[kChunk];             // exp(l_i - l_{16 ib - 1})
-  float col[4][kChunk];          // exp(l_{16 ib - 1} - l_j) for j < 16 ib
-  float tot;                     // exp(l_63)
+// The decays of one chunk.  l_i is the sum of D A over the chunk's steps up to
+// i; the factor exp(l_i - l_j) of row block ib and a step j before the block is
+// row[i] col[ib - 1][j] with the sum before the block as the reference, so a
+// chunk takes a few hundred exponentials and not 64 x 64.  Made once per call
+// for every (chain, chunk) and read by the chunk's blocks.
+struct __align__(16) ChunkDecay {
+  float wD[kChunk];      // exp(l_63 - l_j) D_j
+  float first[kChunk];   // exp(l_i)
+  float row[kChunk];     // exp(l_i - l before i's block)
+  float rel[kChunk];     // l_i - l before i's block
+  float D[kChunk];       // step sizes, 0 behind the sequence's end
+  float col[3][kChunk];  // exp(l before block ib - l_j) D_j for j < 16 ib, ib = 1 .. 3 (else 0)
 };
+static_assert(sizeof(ChunkDecay) == 2048, "128 copies of 16 bytes");
 
-__device__ __forceinline__ float exp_diff(float hi, float lo) { return ex2_fast(1.44269504f * hi + 1.44269504f * lo); }
-
-// By one warp; lane i holds dt of steps t0 + 2 i, t0 + 2 i + 1 (already with
-// the bias).  Sums in fp64: a chunk's sum reaches some hundreds and its
-// differences have to be good to 1e-7.
-__device__ __forceinline__ void chunk_decay(ChunkDecay& d, float x0, float x1, bool ok0, bool ok1, float A, int lane) {
-  const float D0 = ok0 ? softplus_f(x0) : 0.f, D1 = ok1 ? softplus_f(x1) : 0.f;
-  const double a0 = static_cast<double>(D0) * A, a1 = static_cast<double>(D1) * A;
-  double l1 = a0 + a1;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double p = __shfl_up_sync(0xffffffffu, l1, o);
-    if (lane >= o) l1 += p;
-  }
-  double before = __shfl_up_sync(0xffffffffu, l1, 1);
-  if (lane == 0) before = 0.;
-  const double l0 = before + a0;
-  const double end = __shfl_sync(0xffffffffu, l1, 31);
-  const int i = 2 * lane;
-  const float h0 = static_cast<float>(l0), h1 = static_cast<float>(l1);
-  *reinterpret_cast<float2*>(&d.hi[i]) = make_float2(h0, h1);
-  *reinterpret_cast<float2*>(&d.lo[i]) = make_float2(static_cast<float>(l0 - h0), static_cast<float>(l1 - h1));
-  *reinterpret_cast<float2*>(&d.D[i]) = make_float2(D0, D1);
-  *reinterpret_cast<float2*>(&d.first[i]) = make_float2(expf(h0), expf(h1));
-  *reinterpret_cast<float2*>(&d.last[i]) =
-      make_float2(expf(static_cast<float>(end - l0)), expf(static_cast<float>(end - l1)));
-#pragma unroll
-  for (int ib = 0; ib < 4; ++ib) {
-    const double ref = ib == 0 ? 0. : __shfl_sync(0xffffffffu, l1, 8 * ib - 1);
-    if ((lane >> 3) == ib)
-      *reinterpret_cast<float2*>(&d.row[i]) =
-          make_float2(expf(static_cast<float>(l0 - ref)), expf(static_cast<float>(l1 - ref)));
-    if ((lane >> 3) < ib)
-      *reinterpret_cast<float2*>(&d.col[ib][i]) =
-          make_float2(expf(static_cast<float>(ref - l0)), expf(static_cast<float>(ref - l1)));
-  }
-  if (lane == 0) d.tot = expf(static_cast<float>(end));
-}
+// exp(a) for a difference a of sums, by the hardware's 2^x.
+__device__ __forceinline__ float exp_fast(float a) { return ex2_fast(1.44269504f * a); }
 
 }  // namespace m2rnn
