@@ -334,9 +334,9 @@ __global__ void __launch_bounds__(kThreads) ssm_chunk_grad_kernel(SsmArgs A, con
 // Block (n): 256 threads; thread i takes chunks i, i + 256, ... of every b.
 __global__ void __launch_bounds__(kThreads) ssm_sum_ab_kernel(const float2* part, float* dA, float* ddt_bias, int B,
                                                               int N, int nc) {
-  __shared__ float2 red[kThreads];
+  __shared__ double2 red[kThreads];  // both sums cancel: fp64
   const int n = blockIdx.x;
-  float2 s = make_float2(0.f, 0.f);
+  double2 s = make_double2(0., 0.);
   for (int64_t i = threadIdx.x; i < static_cast<int64_t>(B) * nc; i += kThreads) {
     const int64_t b = i / nc, c = i % nc;
     const float2 p = part[(b * N + n) * nc + c];
@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(kThreads) ssm_sum_ab_kernel(const float2* part
     __syncthreads();
   }
   if (threadIdx.x == 0) {
-    dA[n] = red[0].x;
-    if (ddt_bias != nullptr) ddt_bias[n] = red[0].y;
+    dA[n] = static_cast<float>(red[0].x);
+    if (ddt_bias != nullptr) ddt_bias[n] = static_cast<float>(red[0].y);
   }
 }
 
@@ -512,15 +512,7 @@ cudaError_t backward_simt(const SsmArgs& a, cudaStream_t s) {
   ssm_chunk_scan_kernel<false><<<scan, kThreads, 0, s>>>(states, tot, a.H_0, nullptr, nc, KV);
   ssm_chunk_scan_kernel<true><<<scan, kThreads, 0, s>>>(rstates, tot, a.dH_T, a.dH_0, nc, KV);
   ssm_chunk_grad_kernel<T><<<static_cast<unsigned>(blocks), kThreads, sm2, s>>>(a, states, rstates, o, nc);
-  ssm_sum_ab_kernel<<<a.N, kThreads, 0, s>>>(ab, a.dA, a.ddt_bias, a.B, a.N, nc);
-  if (a.dw_r != nullptr)
-    ssm_sum_wr_kernel<<<dim3(a.N, (a.V + 31) / 32), kThreads, 0, s>>>(wr, a.dw_r, a.B, a.N, nc, a.V);
-  if (a.G != a.N) {
-    const int64_t n = static_cast<int64_t>(a.B) * a.T * a.G * a.K;
-    ssm_sum_heads_kernel<<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(
-        dqh, dkh, a.dq, a.dk, n, a.N, a.G, a.K);
-  }
-  return cudaGetLastError();
+  return launch_ssm_grad_sums(a, o, nc, s);
 }
 
 }  // namespace
@@ -535,13 +527,26 @@ cudaError_t launch_ssm_piece_scan(float* states, const float* tot, const float* 
   return cudaGetLastError();
 }
 
+cudaError_t launch_ssm_grad_sums(const SsmArgs& a, const SsmGradOut& o, int nc, cudaStream_t s) {
+  ssm_sum_ab_kernel<<<a.N, kThreads, 0, s>>>(o.ab_part, a.dA, a.ddt_bias, a.B, a.N, nc);
+  if (a.dw_r != nullptr)
+    ssm_sum_wr_kernel<<<dim3(a.N, (a.V + 31) / 32), kThreads, 0, s>>>(o.wr_part, a.dw_r, a.B, a.N, nc, a.V);
+  if (a.G != a.N) {
+    const int64_t n = static_cast<int64_t>(a.B) * a.T * a.G * a.K;
+    ssm_sum_heads_kernel<<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(
+        o.dq, o.dk, a.dq, a.dk, n, a.N, a.G, a.K);
+  }
+  return cudaGetLastError();
+}
+
 size_t ssm_forward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V, bool bf16) {
   if (bf16) return align256(ssm_mma_forward_scratch_bytes(B, T, N, K, V));
   const size_t blocks = static_cast<size_t>(B) * N * ((T + kL - 1) / kL);
   return align256(sizeof(float) * blocks * (static_cast<size_t>(K) * V + 1));
 }
 
-size_t ssm_backward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V, bool) {
+size_t ssm_backward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V, bool bf16) {
+  if (bf16) return align256(ssm_mma_backward_scratch_bytes(B, T, N, G, K, V));
   const size_t blocks = static_cast<size_t>(B) * N * ((T + kL - 1) / kL);
   const size_t heads = G == N ? 0 : 2 * static_cast<size_t>(B) * T * N * K;
   return align256(sizeof(float) * (blocks * (2 * static_cast<size_t>(K) * V + 3 + V) + heads));
@@ -552,7 +557,7 @@ cudaError_t launch_ssm_forward(const SsmArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_ssm_backward(const SsmArgs& a, cudaStream_t s) {
-  return a.bf16 ? backward_simt<uint16_t>(a, s) : backward_simt<float>(a, s);
+  return a.bf16 ? launch_ssm_mma_backward(a, s) : backward_simt<float>(a, s);
 }
 
 cudaError_t launch_ssm_step(float* H, const SsmArgs& a, cudaStream_t s) {

@@ -29,5 +29,11 @@ cudaError_t launch_ssm_piece_scan(float* states, const float* tot, const float* 
 // The tensor-core kernels (bf16 inputs).
 size_t ssm_mma_forward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V);
 cudaError_t launch_ssm_mma_forward(const SsmArgs& a, cudaStream_t s);
+size_t ssm_mma_backward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V);
+cudaError_t launch_ssm_mma_backward(const SsmArgs& a, cudaStream_t s);
+
+// The fixed-order sums behind the chunks' gradients: dA, ddt_bias, dw_r from
+// their partials over the chunks, dq, dk from the value heads' where G < N.
+cudaError_t launch_ssm_grad_sums(const SsmArgs& a, const SsmGradOut& o, int nc, cudaStream_t s);
 
 }  // namespace m2rnn

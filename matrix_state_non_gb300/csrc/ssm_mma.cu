@@ -35,29 +35,38 @@ constexpr int kThreads = 128;  // four warps
 // of eight heads, whose dt lie side by side.  Sums run within a block of 16
 // steps first and only from there over the blocks, each from its own end: no
 // two long sums are ever subtracted, so fp32 is enough.
-__global__ void __launch_bounds__(256) ssm_decay_kernel(SsmArgs A, ChunkDecay* out, float* tot, int nc) {
+template <bool kGrad>
+__global__ void __launch_bounds__(256) ssm_decay_kernel(SsmArgs A, void* out, float* tot, int nc) {
   const int lane = threadIdx.x & 31, heads = (A.N + 7) / 8, own = lane >> 3;
-  const int n = static_cast<int>(blockIdx.x % heads) * 8 + (threadIdx.x >> 5);
-  const int64_t bc = blockIdx.x / heads;
-  const int b = static_cast<int>(bc / nc), c = static_cast<int>(bc % nc);
+  const unsigned bc = blockIdx.x / heads;
+  const int n = (blockIdx.x - bc * heads) * 8 + (threadIdx.x >> 5), b = bc / nc, c = bc - b * nc;
   if (n >= A.N) return;
   const int64_t id = (static_cast<int64_t>(b) * A.N + n) * nc + c;
   const int len = ssm_len(A, b), t = c * kChunk + 2 * lane;
   const uint16_t* p = static_cast<const uint16_t*>(A.dt) + (static_cast<int64_t>(b) * A.T + t) * A.dt_stride + n;
   const float bias = A.dt_bias ? A.dt_bias[n] : 0.f, An = A.A[n];
-  const float D0 = t < len ? softplus_f(to_f32(p[0]) + bias) : 0.f;
-  const float D1 = t + 1 < len ? softplus_f(to_f32(p[A.dt_stride]) + bias) : 0.f;
+  const float x0 = t < len ? to_f32(p[0]) + bias : 0.f, x1 = t + 1 < len ? to_f32(p[A.dt_stride]) + bias : 0.f;
+  const float D0 = t < len ? softplus_f(x0) : 0.f, D1 = t + 1 < len ? softplus_f(x1) : 0.f;
   const float a0 = D0 * An, a1 = D1 * An;
-  // Within the block of 16 steps: r = sum up to a step, s = sum behind it.
-  float up = a0 + a1, down = up;
+  // Within the block of 16 steps: the sum up to a step, and the sum behind it.
+  float up = a0 + a1, down = up, low = kGrad ? (a0 - up) + a1 : 0.f;
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) {
     const float x = __shfl_up_sync(0xffffffffu, up, o, 8), y = __shfl_down_sync(0xffffffffu, down, o, 8);
-    if ((lane & 7) >= o) up += x;
+    const float z = kGrad ? __shfl_up_sync(0xffffffffu, low, o, 8) : 0.f;
+    if ((lane & 7) >= o) {
+      const float s = up + x;
+      if (kGrad) {  // the rounding of this sum, kept
+        const float w = s - up;
+        low += z + ((up - (s - w)) + (x - w));
+      }
+      up = s;
+    }
     if ((lane & 7) + o < 8) down += y;
   }
   float before = __shfl_up_sync(0xffffffffu, up, 1, 8), behind = __shfl_down_sync(0xffffffffu, down, 1, 8);
-  if ((lane & 7) == 0) before = 0.f;
+  float before_low = kGrad ? __shfl_up_sync(0xffffffffu, low, 1, 8) : 0.f;
+  if ((lane & 7) == 0) before = before_low = 0.f;
   if ((lane & 7) == 7) behind = 0.f;
   const float r0 = before + a0, r1 = up, s0 = behind + a1, s1 = behind;
   float T[4];  // the blocks' sums
@@ -65,14 +74,15 @@ __global__ void __launch_bounds__(256) ssm_decay_kernel(SsmArgs A, ChunkDecay* o
   for (int i = 0; i < 4; ++i) T[i] = __shfl_sync(0xffffffffu, up, 8 * i + 7);
   const float base = own == 0 ? 0.f : own == 1 ? T[0] : own == 2 ? T[0] + T[1] : T[0] + T[1] + T[2];
   const float rest = own == 3 ? 0.f : own == 2 ? T[3] : own == 1 ? T[3] + T[2] : T[3] + T[2] + T[1];
-  ChunkDecay& d = out[id];
+  ChunkDecay& d = kGrad ? static_cast<ChunkDecayGrad*>(out)[id].d : static_cast<ChunkDecay*>(out)[id];
   const int i = 2 * lane;
   auto put = [&](float* at, float x, float y) { *reinterpret_cast<float2*>(at + i) = make_float2(x, y); };
+  const float e0 = expf(s0 + rest), e1 = expf(s1 + rest);
   put(d.D, D0, D1);
   put(d.rel, r0, r1);
   put(d.row, expf(r0), expf(r1));
   put(d.first, expf(base + r0), expf(base + r1));
-  put(d.wD, expf(s0 + rest) * D0, expf(s1 + rest) * D1);
+  put(d.wD, e0 * D0, e1 * D1);
 #pragma unroll
   for (int ib = 1; ib < 4; ++ib) {
     // From the end of the step's block to the start of block ib.
@@ -80,7 +90,14 @@ __global__ void __launch_bounds__(256) ssm_decay_kernel(SsmArgs A, ChunkDecay* o
 #pragma unroll
     for (int x = 1; x < ib; ++x) mid += own < x ? T[x] : 0.f;
     const bool past = own < ib;
-    put(d.col[ib - 1], past ? expf(s0 + mid) * D0 : 0.f, past ? expf(s1 + mid) * D1 : 0.f);
+    put(d.col[ib - 1], past ? expf(s0 + mid) * (kGrad ? 1.f : D0) : 0.f, past ? expf(s1 + mid) * (kGrad ? 1.f : D1) : 0.f);
+  }
+  if (kGrad) {
+    ChunkDecayGrad& dg = static_cast<ChunkDecayGrad*>(out)[id];
+    const float w = r0 - before;
+    put(dg.last, e0, e1);
+    put(dg.rel_lo, before_low + ((before - (r0 - w)) + (a0 - w)), low);
+    put(dg.sg, 1.f / (1.f + expf(-x0)), 1.f / (1.f + expf(-x1)));
   }
   if (lane == 0) tot[id] = expf(T[0] + T[1] + T[2] + T[3]);
 }
@@ -549,6 +566,15 @@ cudaError_t run(const ScanArgs& w, int64_t chains, cudaStream_t s) {
 
 }  // namespace
 
+cudaError_t launch_ssm_decay(const SsmArgs& a, void* out, float* tot, int nc, bool grad, cudaStream_t s) {
+  const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.B) * nc * ((a.N + 7) / 8));
+  if (grad)
+    ssm_decay_kernel<true><<<blocks, 256, 0, s>>>(a, out, tot, nc);
+  else
+    ssm_decay_kernel<false><<<blocks, 256, 0, s>>>(a, out, tot, nc);
+  return cudaGetLastError();
+}
+
 size_t ssm_mma_forward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
   return make_layout(make_plan(B, T, N, K, V), B * N).total;
 }
@@ -579,8 +605,8 @@ cudaError_t launch_ssm_mma_forward(const SsmArgs& a, cudaStream_t s) {
   w.vq = vec(a.q, a.q_stride, a.K);
   w.vk = vec(a.k, a.k_stride, a.K);
   w.vv = vec(a.v, a.v_stride, a.V);
-  const int64_t blocks = static_cast<int64_t>(a.B) * p.nc * ((a.N + 7) / 8);
-  ssm_decay_kernel<<<static_cast<unsigned>(blocks), 256, 0, s>>>(a, decay, tot, p.nc);
+  const cudaError_t e = launch_ssm_decay(a, decay, tot, p.nc, false, s);
+  if (e != cudaSuccess) return e;
 #define M2RNN_SSM_CASE(KP, VS) \
   if (p.kp == KP && p.vs == VS) return run<KP, VS>(w, chains, s);
   M2RNN_SSM_CASE(32, 16)

@@ -99,9 +99,21 @@ struct __align__(16) ChunkDecay {
   float row[kChunk];     // exp(l_i - l before i's block)
   float rel[kChunk];     // l_i - l before i's block
   float D[kChunk];       // step sizes, 0 behind the sequence's end
-  float col[3][kChunk];  // exp(l before block ib - l_j) D_j for j < 16 ib, ib = 1 .. 3 (else 0)
+  float col[3][kChunk];  // exp(l before block ib - l_j) for j < 16 ib, ib = 1 .. 3 (else 0); the forward's times D_j
 };
 static_assert(sizeof(ChunkDecay) == 2048, "128 copies of 16 bytes");
+
+// What the backward reads besides.
+struct __align__(16) ChunkDecayGrad {
+  ChunkDecay d;
+  float last[kChunk];    // exp(l_63 - l_j)
+  float rel_lo[kChunk];  // the part of the sum that rel leaves out
+  float sg[kChunk];      // sigmoid(dt + dt_bias)
+};
+
+// Decays of every (chain, chunk) into `out` (ChunkDecay, or ChunkDecayGrad for
+// the backward), exp(l_63) into tot.
+cudaError_t launch_ssm_decay(const SsmArgs& a, void* out, float* tot, int nc, bool grad, cudaStream_t s);
 
 // exp(a) for a difference a of sums, by the hardware's 2^x.
 __device__ __forceinline__ float exp_fast(float a) { return ex2_fast(1.44269504f * a); }
