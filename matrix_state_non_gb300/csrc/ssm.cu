@@ -330,51 +330,53 @@ __global__ void __launch_bounds__(kThreads) ssm_chunk_grad_kernel(SsmArgs A, con
   }
 }
 
-// dA, ddt_bias [N] and dw_r [N,V]: fixed-order sums of the chunks' partials.
-// Block (n): 256 threads; thread i takes chunks i, i + 256, ... of every b.
-__global__ void __launch_bounds__(kThreads) ssm_sum_ab_kernel(const float2* part, float* dA, float* ddt_bias, int B,
-                                                              int N, int nc) {
-  __shared__ double2 red[kThreads];  // both sums cancel: fp64
-  const int n = blockIdx.x;
-  double2 s = make_double2(0., 0.);
-  for (int64_t i = threadIdx.x; i < static_cast<int64_t>(B) * nc; i += kThreads) {
-    const int64_t b = i / nc, c = i % nc;
-    const float2 p = part[(b * N + n) * nc + c];
-    s.x += p.x;
-    s.y += p.y;
-  }
-  red[threadIdx.x] = s;
-  __syncthreads();
-  for (int o = kThreads / 2; o > 0; o >>= 1) {
-    if (threadIdx.x < o) {
-      red[threadIdx.x].x += red[threadIdx.x + o].x;
-      red[threadIdx.x].y += red[threadIdx.x + o].y;
-    }
-    __syncthreads();
-  }
-  if (threadIdx.x == 0) {
-    dA[n] = static_cast<float>(red[0].x);
-    if (ddt_bias != nullptr) ddt_bias[n] = static_cast<float>(red[0].y);
-  }
-}
+// dA, ddt_bias [N] and dw_r [N,V]: fixed-order sums of the partials over the
+// chunks of every b, in one launch.  Block (n, 0): 512 threads take chunks i,
+// i + 512, ... (fp64: both sums cancel); block (n, 1 + x): 16 warps take every
+// sixteenth chunk of columns 32 x .., added in warp order.
+constexpr int kSumThreads = 512;
 
-// Block (n, 32 columns): 8 warps take interleaved chunks, added in warp order.
-__global__ void __launch_bounds__(kThreads) ssm_sum_wr_kernel(const float* part, float* dw_r, int B, int N, int nc,
-                                                              int V) {
-  __shared__ float red[kThreads / 32][32];
-  const int n = blockIdx.x, vv = blockIdx.y * 32 + (threadIdx.x & 31), w = threadIdx.x >> 5;
-  float s = 0.f;
-  if (vv < V)
-    for (int64_t i = w; i < static_cast<int64_t>(B) * nc; i += kThreads / 32) {
-      const int64_t b = i / nc, c = i % nc;
-      s += part[((b * N + n) * nc + c) * V + vv];
+__global__ void __launch_bounds__(kSumThreads) ssm_grad_sums_kernel(const float2* ab, const float* wr, float* dA,
+                                                                    float* ddt_bias, float* dw_r, int B, int N, int nc,
+                                                                    int V) {
+  __shared__ double2 red[kSumThreads / 32];
+  __shared__ float col[kSumThreads / 32][32];
+  const int n = blockIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5, chunks = B * nc;
+  auto at = [&](int i) { return (static_cast<int64_t>(i / nc) * N + n) * nc + i % nc; };
+  if (blockIdx.y == 0) {
+    double2 s = make_double2(0., 0.);
+    for (int i = threadIdx.x; i < chunks; i += kSumThreads) {
+      const float2 p = ab[at(i)];
+      s.x += p.x;
+      s.y += p.y;
     }
-  red[w][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (w == 0 && vv < V) {
-    for (int i = 1; i < kThreads / 32; ++i) s += red[i][threadIdx.x];
-    dw_r[static_cast<int64_t>(n) * V + vv] = s;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+      s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+    }
+    if (lane == 0) red[w] = s;
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    for (int i = 1; i < kSumThreads / 32; ++i) {
+      s.x += red[i].x;
+      s.y += red[i].y;
+    }
+    dA[n] = static_cast<float>(s.x);
+    if (ddt_bias != nullptr) ddt_bias[n] = static_cast<float>(s.y);
+    return;
   }
+  const int vv = (blockIdx.y - 1) * 32 + lane;
+  float s = 0.f;
+  if (vv < V) {
+#pragma unroll 8
+    for (int i = w; i < chunks; i += kSumThreads / 32) s += wr[at(i) * V + vv];
+  }
+  col[w][lane] = s;
+  __syncthreads();
+  if (w != 0 || vv >= V) return;
+  for (int i = 1; i < kSumThreads / 32; ++i) s += col[i][lane];
+  dw_r[static_cast<int64_t>(n) * V + vv] = s;
 }
 
 // dq, dk of the G shared heads: the per-head gradients summed in head order.
@@ -528,9 +530,8 @@ cudaError_t launch_ssm_piece_scan(float* states, const float* tot, const float* 
 }
 
 cudaError_t launch_ssm_grad_sums(const SsmArgs& a, const SsmGradOut& o, int nc, cudaStream_t s) {
-  ssm_sum_ab_kernel<<<a.N, kThreads, 0, s>>>(o.ab_part, a.dA, a.ddt_bias, a.B, a.N, nc);
-  if (a.dw_r != nullptr)
-    ssm_sum_wr_kernel<<<dim3(a.N, (a.V + 31) / 32), kThreads, 0, s>>>(o.wr_part, a.dw_r, a.B, a.N, nc, a.V);
+  ssm_grad_sums_kernel<<<dim3(a.N, a.dw_r != nullptr ? 1 + (a.V + 31) / 32 : 1), kSumThreads, 0, s>>>(
+      o.ab_part, o.wr_part, a.dA, a.ddt_bias, a.dw_r, a.B, a.N, nc, a.V);
   if (a.G != a.N) {
     const int64_t n = static_cast<int64_t>(a.B) * a.T * a.G * a.K;
     ssm_sum_heads_kernel<<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(

@@ -336,9 +336,9 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
       x[nt][2] *= f1;
       x[nt][3] *= f1;
     }
-#pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-      if (jt > warp) continue;
+    // Not unrolled, here and below: four copies of the body do not fit the instruction cache.
+#pragma unroll 1
+    for (int jt = 0; jt <= warp; ++jt) {
       float s[2][4] = {};
 #pragma unroll
       for (int vt = 0; vt < kVt; ++vt) {
@@ -392,43 +392,8 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
     }
   }
 
-  // <R, S> while both are at hand (the two larger parts: what the third adds
-  // to a sum over K V elements is far below fp32); then R takes S's place.
-  float rs = 0.f;
-  if (vec) {
-    for (int e = tid; e < K * (V / 8); e += kThreads) {
-      const int r = e / (V / 8), col = (e % (V / 8)) * 8;
-      const uint4 a0 = ld_shared_v4(sP + r * Tile<VP>::kPitch + col * 2);
-      const uint4 a1 = ld_shared_v4(sP + Sh::kP + r * Tile<VP>::kPitch + col * 2);
-      const uint4 b0 = *reinterpret_cast<const uint4*>(gR + r * V + col);
-      const uint4 b1 = *reinterpret_cast<const uint4*>(gR + KV + r * V + col);
-      const uint32_t x0[4] = {a0.x, a0.y, a0.z, a0.w}, x1[4] = {a1.x, a1.y, a1.z, a1.w};
-      const uint32_t y0[4] = {b0.x, b0.y, b0.z, b0.w}, y1[4] = {b1.x, b1.y, b1.z, b1.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        rs = fmaf(bf16lo(x0[i]) + bf16lo(x1[i]), bf16lo(y0[i]) + bf16lo(y1[i]), rs);
-        rs = fmaf(bf16hi(x0[i]) + bf16hi(x1[i]), bf16hi(y0[i]) + bf16hi(y1[i]), rs);
-      }
-    }
-  } else {
-    for (int e = tid; e < K * V; e += kThreads) {
-      const int r = e / V, col = e % V;
-      float x = 0.f, y = 0.f;
-#pragma unroll
-      for (int p = 1; p >= 0; --p) {
-        x += bf16_bits_to_f32(static_cast<uint16_t>(ld_shared_u16(sP + p * Sh::kP + r * Tile<VP>::kPitch + col * 2)));
-        y += bf16_bits_to_f32(gR[p * KV + e]);
-      }
-      rs = fmaf(x, y, rs);
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) rs += __shfl_xor_sync(0xffffffffu, rs, o);
-  if (lane == 0) red[warp] = rs;
   __syncthreads();
-  load_planes(gR);
-  cp_async_wait<0>();
-  __syncthreads();
+  load_planes(gR);  // in S's place, behind the first half of dk
 
   const float l0 = dg.last[m0], l1 = dg.last[m1], D0 = d.D[m0], D1 = d.D[m1];
   // Rows j of the transposed scores: factors exp(l_i - l_j), columns i of block it.
@@ -454,28 +419,8 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
     uint32_t vf[kVt][4];
 #pragma unroll
     for (int vt = 0; vt < kVt; ++vt) ldmatrix_x4(vf[vt], at_rows<VP>(sV, 16 * warp, 16 * vt, lane));
-#pragma unroll
-    for (int p = 2; p >= 0; --p)
-#pragma unroll
-      for (int vt = 0; vt < kVt; ++vt)
-#pragma unroll
-        for (int kt = 0; kt < kKt; ++kt) {
-          uint32_t f[4];
-          ldmatrix_x4(f, at_cols<VP>(sP + p * Sh::kP, 16 * kt, 16 * vt, lane));
-          mma_bf16_16816(x[2 * kt], vf[vt], f[0], f[1]);
-          mma_bf16_16816(x[2 * kt + 1], vf[vt], f[2], f[3]);
-        }
-#pragma unroll
-    for (int nt = 0; nt < KP / 8; ++nt) {
-      x[nt][0] *= l0;
-      x[nt][1] *= l0;
-      x[nt][2] *= l1;
-      x[nt][3] *= l1;
-    }
-    row_dots(sK, x, ci);
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      if (it < warp) continue;
+#pragma unroll 1
+    for (int it = warp; it < 4; ++it) {
       float s[2][4] = {};
 #pragma unroll
       for (int vt = 0; vt < kVt; ++vt) {
@@ -498,9 +443,48 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
         }
       }
     }
+    cp_async_wait<0>();
+    __syncthreads();
+    float z[KP / 8][4] = {};
+#pragma unroll
+    for (int p = 2; p >= 0; --p)
+#pragma unroll
+      for (int vt = 0; vt < kVt; ++vt)
+#pragma unroll
+        for (int kt = 0; kt < kKt; ++kt) {
+          uint32_t f[4];
+          ldmatrix_x4(f, at_cols<VP>(sP + p * Sh::kP, 16 * kt, 16 * vt, lane));
+          mma_bf16_16816(z[2 * kt], vf[vt], f[0], f[1]);
+          mma_bf16_16816(z[2 * kt + 1], vf[vt], f[2], f[3]);
+        }
+    row_dots(sK, z, ci);  // times last_j below
+#pragma unroll
+    for (int nt = 0; nt < KP / 8; ++nt) {
+      x[nt][0] = fmaf(l0, z[nt][0], x[nt][0]);
+      x[nt][1] = fmaf(l0, z[nt][1], x[nt][1]);
+      x[nt][2] = fmaf(l1, z[nt][2], x[nt][2]);
+      x[nt][3] = fmaf(l1, z[nt][3], x[nt][3]);
+    }
     row_dots(sK, x, ck);
 #pragma unroll
     for (int nt = 0; nt < KP / 8; ++nt) store_rows(dk, qk_stride, K, x[nt], nt, D0, D1);
+  }
+
+  // <R, S>: the thread's pieces of S are loaded here and used behind dv, with
+  // R from shared memory (the two larger parts of both: what the third adds to
+  // a sum over K V elements is far below fp32).
+  constexpr int kDot = KP * VP / 8 / kThreads < 4 ? KP * VP / 8 / kThreads : 4;
+  uint4 s_hi[kDot], s_mid[kDot];
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < kDot; ++i) {
+      const int e = i * kThreads + tid, r = e / (VP / 8), col = (e % (VP / 8)) * 8;
+      s_hi[i] = s_mid[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < K && col < V) {
+        s_hi[i] = *reinterpret_cast<const uint4*>(gS + r * V + col);
+        s_mid[i] = *reinterpret_cast<const uint4*>(gS + KV + r * V + col);
+      }
+    }
   }
 
   {  // zv_j = last_j R^T k_j + sum_i E_ij (q_i . k_j) u_i
@@ -526,9 +510,8 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
       x[nt][2] *= l1;
       x[nt][3] *= l1;
     }
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-      if (it < warp) continue;
+#pragma unroll 1
+    for (int it = warp; it < 4; ++it) {
       float s[2][4] = {};
 #pragma unroll
       for (int kt = 0; kt < kKt; ++kt) {
@@ -571,12 +554,51 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
       store_rows(dv, v_stride, V, x[nt], nt, 1.f, 1.f);
     }
   }
+  float rs = 0.f;
+  auto dot_piece = [&](const uint4& hi, const uint4& mid, int r, int col) {
+    const uint4 b0 = ld_shared_v4(sP + r * Tile<VP>::kPitch + col * 2);
+    const uint4 b1 = ld_shared_v4(sP + Sh::kP + r * Tile<VP>::kPitch + col * 2);
+    const uint32_t x0[4] = {hi.x, hi.y, hi.z, hi.w}, x1[4] = {mid.x, mid.y, mid.z, mid.w};
+    const uint32_t y0[4] = {b0.x, b0.y, b0.z, b0.w}, y1[4] = {b1.x, b1.y, b1.z, b1.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      rs = fmaf(bf16lo(x0[i]) + bf16lo(x1[i]), bf16lo(y0[i]) + bf16lo(y1[i]), rs);
+      rs = fmaf(bf16hi(x0[i]) + bf16hi(x1[i]), bf16hi(y0[i]) + bf16hi(y1[i]), rs);
+    }
+  };
+  if (vec) {
+#pragma unroll
+    for (int i = 0; i < kDot; ++i) {
+      const int e = i * kThreads + tid;
+      dot_piece(s_hi[i], s_mid[i], e / (VP / 8), (e % (VP / 8)) * 8);  // zeros where there is no S
+    }
+    for (int e = kDot * kThreads + tid; e < K * (VP / 8); e += kThreads) {
+      const int r = e / (VP / 8), col = (e % (VP / 8)) * 8;
+      if (col < V)
+        dot_piece(*reinterpret_cast<const uint4*>(gS + r * V + col),
+                  *reinterpret_cast<const uint4*>(gS + KV + r * V + col), r, col);
+    }
+  } else {
+    for (int e = tid; e < K * V; e += kThreads) {
+      const int r = e / V, col = e % V;
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int p = 1; p >= 0; --p) {
+        x += bf16_bits_to_f32(static_cast<uint16_t>(ld_shared_u16(sP + p * Sh::kP + r * Tile<VP>::kPitch + col * 2)));
+        y += bf16_bits_to_f32(gS[p * KV + e]);
+      }
+      rs = fmaf(x, y, rs);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) rs += __shfl_xor_sync(0xffffffffu, rs, o);
+  if (lane == 0) red[warp] = rs;
   __syncthreads();
 
   if (warp == 0) {  // two steps a lane
     const int i = 2 * lane;
     const float A_n = A.A[n];
-    float s = d.D[i] * ci[i] + d.D[i + 1] * ci[i + 1];
+    float s = d.wD[i] * ci[i] + d.wD[i + 1] * ci[i + 1];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     const float end = fmaf(W.tot[blockIdx.x], (red[0] + red[1]) + (red[2] + red[3]), s);  // <R, S'>
