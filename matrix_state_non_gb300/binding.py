@@ -604,30 +604,36 @@ def m2rnn_grad_clip(plan, plan_bytes, max_norm, norm, workspace, workspace_bytes
     return load().m2rnn_grad_clip(plan, plan_bytes, max_norm, norm, workspace, workspace_bytes, stream)
 
 
-def _need(t, name: str, shape, dtype, device):
+def _need(t, name: str, shape, dtype, gpu: int):
     """Address of an optional dense operand (None for None), checked."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape:
+    if t.dtype is dtype and t.shape == shape and t.get_device() == gpu and t.is_contiguous():
+        return t.data_ptr()
+    _refuse(t, name, shape, dtype, gpu)
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _refuse(t, name: str, shape, dtype, gpu: int):
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous on {device}")
-    return t.data_ptr()
+    if t.get_device() != gpu:
+        raise ValueError(f"{name} must be on cuda:{gpu}, is on {t.device}")
 
 
-def _rows(t, name: str, shape, inner: int, dtype, device):
+def _rows(t, name: str, shape, inner: int, width: int, dtype, gpu: int):
     """Address and row stride of an input that may be a column slice of a
-    wider tensor: its last ``inner`` dimensions (one token's values) dense,
-    the tokens of [B,T,...] evenly spaced through all sequences."""
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    width, stride, n = 1, t.stride(), len(shape) - inner
+    wider tensor: its last ``inner`` dimensions (the ``width`` values of one
+    token) dense, the tokens of [B,T,...] evenly spaced through all sequences."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != gpu:
+        _refuse(t, name, shape, dtype, gpu)
+    if t.is_contiguous():
+        return t.data_ptr(), width
+    dense, stride, n = 1, t.stride(), len(shape) - inner
     for i in range(len(shape) - 1, n - 1, -1):
-        if shape[i] != 1 and stride[i] != width:
+        if shape[i] != 1 and stride[i] != dense:
             raise ValueError(f"{name}: the values of one token must be dense")
-        width *= shape[i]
+        dense *= shape[i]
     if n == 2 and shape[1] > 1:
         if shape[0] > 1 and stride[0] != shape[1] * stride[1]:
             raise ValueError(f"{name}: sequences must lie T rows apart")
@@ -635,29 +641,44 @@ def _rows(t, name: str, shape, inner: int, dtype, device):
     return t.data_ptr(), stride[0] if shape[0] > 1 else width
 
 
-def _alloc(shape, dtype, device, stream):
+def _gpu(t) -> int:
+    gpu = t.get_device()
+    if gpu < 0:
+        raise ValueError(f"expected CUDA tensors, got one on {t.device}")
+    return gpu
+
+
+def _on(gpu: int, stream) -> int:
+    """Handle of the given stream, else of the GPU's current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    from torch._C import _cuda_getCurrentRawStream
+    return _cuda_getCurrentRawStream(gpu)
+
+
+def _alloc(like, shape, dtype, stream):
     """A new tensor that belongs to the stream it is used on."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
+    import torch
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _out(out, name, shape, dtype, device, stream):
+def _out(out, name, like, shape, dtype, stream):
     t = out.get(name) if out else None
     if t is None:
-        return _alloc(shape, dtype, device, stream)
-    _need(t, name, shape, dtype, device)
+        return _alloc(like, shape, dtype, stream)
+    _need(t, name, shape, dtype, like.get_device())
     return t
 
 
-def _scratch(workspace, nbytes: int, device, stream, what: str):
+def _scratch(workspace, nbytes: int, like, stream, what: str):
     import torch
     if nbytes == 0:
         raise M2RNNError(M2RNN_ERR_UNSUPPORTED, what)
     if workspace is None or workspace.numel() < nbytes:
-        workspace = _alloc((nbytes,), torch.uint8, device, stream)
+        return _alloc(like, (nbytes,), torch.uint8, stream)
     return workspace
 
 
@@ -671,15 +692,15 @@ def causal_conv(x, w, bias=None, *, x0=None, lengths=None, silu: bool = True, wa
     may hold preallocated y / x_T."""
     import torch
     B, T, C = x.shape
-    W, dev, dt = w.shape[1], x.device, x.dtype
+    W, gpu, dt = w.shape[1], _gpu(x), x.dtype
     code = _dtype_code(x)
-    xp, xs = _rows(x, "x", (B, T, C), 1, dt, dev)
-    y = _out(out, "y", (B, T, C), dt, dev, stream)
-    x_T = _out(out, "x_T", (B, W - 1, C), dt, dev, stream) if want_state or (out and "x_T" in out) else None
-    st = load().m2rnn_causal_conv(xp, xs, _need(w, "w", (C, W), dt, dev), _need(bias, "bias", (C,), dt, dev),
-                                  _need(x0, "x0", (B, W - 1, C), dt, dev),
-                                  _need(lengths, "lengths", (B,), torch.int32, dev), y.data_ptr(), _ptr(x_T), B, T, C,
-                                  W, int(silu), code, _stream_handle(stream))
+    xp, xs = _rows(x, "x", (B, T, C), 1, C, dt, gpu)
+    y = _out(out, "y", x, (B, T, C), dt, stream)
+    x_T = _out(out, "x_T", x, (B, W - 1, C), dt, stream) if want_state or (out and "x_T" in out) else None
+    st = load().m2rnn_causal_conv(xp, xs, _need(w, "w", (C, W), dt, gpu), _need(bias, "bias", (C,), dt, gpu),
+                                  _need(x0, "x0", (B, W - 1, C), dt, gpu),
+                                  _need(lengths, "lengths", (B,), torch.int32, gpu), y.data_ptr(), _ptr(x_T), B, T, C,
+                                  W, int(silu), code, _on(gpu, stream))
     _check(st, "m2rnn_causal_conv")
     return dict(y=y) if x_T is None else dict(y=y, x_T=x_T)
 
@@ -690,22 +711,22 @@ def causal_conv_backward(x, w, bias, dy, *, x0=None, dx_T=None, lengths=None, si
     Returns dict(dx, dw[, db][, dx0]), fp32 (db when there is a bias)."""
     import torch
     B, T, C = x.shape
-    W, dev, dt, f32 = w.shape[1], x.device, x.dtype, torch.float32
+    W, gpu, dt, f32 = w.shape[1], _gpu(x), x.dtype, torch.float32
     code = _dtype_code(x)
-    xp, xs = _rows(x, "x", (B, T, C), 1, dt, dev)
-    res = dict(dx=_out(out, "dx", (B, T, C), f32, dev, stream), dw=_out(out, "dw", (C, W), f32, dev, stream))
+    xp, xs = _rows(x, "x", (B, T, C), 1, C, dt, gpu)
+    res = dict(dx=_out(out, "dx", x, (B, T, C), f32, stream), dw=_out(out, "dw", x, (C, W), f32, stream))
     if bias is not None:
-        res["db"] = _out(out, "db", (C,), f32, dev, stream)
+        res["db"] = _out(out, "db", x, (C,), f32, stream)
     if want_dx0:
-        res["dx0"] = _out(out, "dx0", (B, W - 1, C), f32, dev, stream)
-    ws = _scratch(workspace, m2rnn_causal_conv_backward_workspace_size(B, T, C, W), dev, stream,
+        res["dx0"] = _out(out, "dx0", x, (B, W - 1, C), f32, stream)
+    ws = _scratch(workspace, m2rnn_causal_conv_backward_workspace_size(B, T, C, W), x, stream,
                   "m2rnn_causal_conv_backward_workspace_size")
     st = load().m2rnn_causal_conv_backward(
-        xp, xs, _need(w, "w", (C, W), dt, dev), _need(bias, "bias", (C,), dt, dev),
-        _need(x0, "x0", (B, W - 1, C), dt, dev), _need(lengths, "lengths", (B,), torch.int32, dev),
-        _need(dy, "dy", (B, T, C), f32, dev), _need(dx_T, "dx_T", (B, W - 1, C), f32, dev), res["dx"].data_ptr(),
+        xp, xs, _need(w, "w", (C, W), dt, gpu), _need(bias, "bias", (C,), dt, gpu),
+        _need(x0, "x0", (B, W - 1, C), dt, gpu), _need(lengths, "lengths", (B,), torch.int32, gpu),
+        _need(dy, "dy", (B, T, C), f32, gpu), _need(dx_T, "dx_T", (B, W - 1, C), f32, gpu), res["dx"].data_ptr(),
         res["dw"].data_ptr(), _ptr(res.get("db")), _ptr(res.get("dx0")), B, T, C, W, int(silu), code, ws.data_ptr(),
-        ws.numel(), _stream_handle(stream))
+        ws.numel(), _on(gpu, stream))
     _check(st, "m2rnn_causal_conv_backward")
     return res
 
@@ -714,15 +735,15 @@ def causal_conv_step(state, x, w, bias=None, *, silu: bool = True, y=None, strea
     """One token: ``state`` [B,W-1,C] is shifted in place and takes ``x`` [B,C]
     in.  Returns y [B,C]."""
     B, C = x.shape
-    W, dev, dt = w.shape[1], x.device, x.dtype
+    W, gpu, dt = w.shape[1], _gpu(x), x.dtype
     code = _dtype_code(x)
-    xp, xs = _rows(x, "x", (B, C), 1, dt, dev)
+    xp, xs = _rows(x, "x", (B, C), 1, C, dt, gpu)
     if y is None:
-        y = _alloc((B, C), dt, dev, stream)
-    st = load().m2rnn_causal_conv_step(_need(state, "state", (B, W - 1, C), dt, dev), xp, xs,
-                                       _need(w, "w", (C, W), dt, dev), _need(bias, "bias", (C,), dt, dev),
-                                       _need(y, "y", (B, C), dt, dev), B, C, W, int(silu), code,
-                                       _stream_handle(stream))
+        y = _alloc(x, (B, C), dt, stream)
+    st = load().m2rnn_causal_conv_step(_need(state, "state", (B, W - 1, C), dt, gpu), xp, xs,
+                                       _need(w, "w", (C, W), dt, gpu), _need(bias, "bias", (C,), dt, gpu),
+                                       _need(y, "y", (B, C), dt, gpu), B, C, W, int(silu), code,
+                                       _on(gpu, stream))
     _check(st, "m2rnn_causal_conv_step")
     return y
 
@@ -736,21 +757,21 @@ def ssm_scan(q, k, v, dt, A, *, dt_bias=None, w_r=None, H_0=None, lengths=None, 
     import torch
     B, T, G, K = q.shape
     N, V = v.shape[2:]
-    dev, ty, f32 = v.device, v.dtype, torch.float32
+    gpu, ty, f32 = _gpu(v), v.dtype, torch.float32
     code = _dtype_code(v)
-    qp, qs = _rows(q, "q", (B, T, G, K), 2, ty, dev)
-    kp, ks = _rows(k, "k", (B, T, G, K), 2, ty, dev)
-    vp, vs = _rows(v, "v", (B, T, N, V), 2, ty, dev)
-    dp, ds = _rows(dt, "dt", (B, T, N), 1, ty, dev)
-    y = _out(out, "y", (B, T, N, V), ty, dev, stream)
-    H_T = _out(out, "H_T", (B, N, K, V), f32, dev, stream) if want_state else None
-    ws = _scratch(workspace, m2rnn_ssm_workspace_size(B, T, N, G, K, V, code), dev, stream,
+    qp, qs = _rows(q, "q", (B, T, G, K), 2, G * K, ty, gpu)
+    kp, ks = _rows(k, "k", (B, T, G, K), 2, G * K, ty, gpu)
+    vp, vs = _rows(v, "v", (B, T, N, V), 2, N * V, ty, gpu)
+    dp, ds = _rows(dt, "dt", (B, T, N), 1, N, ty, gpu)
+    y = _out(out, "y", v, (B, T, N, V), ty, stream)
+    H_T = _out(out, "H_T", v, (B, N, K, V), f32, stream) if want_state else None
+    ws = _scratch(workspace, m2rnn_ssm_workspace_size(B, T, N, G, K, V, code), v, stream,
                   "m2rnn_ssm_workspace_size")
-    st = load().m2rnn_ssm_scan(qp, qs, kp, ks, vp, vs, dp, ds, _need(A, "A", (N,), f32, dev),
-                               _need(dt_bias, "dt_bias", (N,), f32, dev), _need(w_r, "w_r", (N, V), ty, dev),
-                               _need(H_0, "H_0", (B, N, K, V), f32, dev),
-                               _need(lengths, "lengths", (B,), torch.int32, dev), y.data_ptr(), _ptr(H_T), B, T, N, G,
-                               K, V, code, ws.data_ptr(), ws.numel(), _stream_handle(stream))
+    st = load().m2rnn_ssm_scan(qp, qs, kp, ks, vp, vs, dp, ds, _need(A, "A", (N,), f32, gpu),
+                               _need(dt_bias, "dt_bias", (N,), f32, gpu), _need(w_r, "w_r", (N, V), ty, gpu),
+                               _need(H_0, "H_0", (B, N, K, V), f32, gpu),
+                               _need(lengths, "lengths", (B,), torch.int32, gpu), y.data_ptr(), _ptr(H_T), B, T, N, G,
+                               K, V, code, ws.data_ptr(), ws.numel(), _on(gpu, stream))
     _check(st, "m2rnn_ssm_scan")
     return dict(y=y, H_T=H_T, workspace=ws)
 
@@ -763,12 +784,12 @@ def ssm_scan_backward(q, k, v, dt, A, dy, *, dt_bias=None, w_r=None, H_0=None, d
     import torch
     B, T, G, K = q.shape
     N, V = v.shape[2:]
-    dev, ty, f32 = v.device, v.dtype, torch.float32
+    gpu, ty, f32 = _gpu(v), v.dtype, torch.float32
     code = _dtype_code(v)
-    qp, qs = _rows(q, "q", (B, T, G, K), 2, ty, dev)
-    kp, ks = _rows(k, "k", (B, T, G, K), 2, ty, dev)
-    vp, vs = _rows(v, "v", (B, T, N, V), 2, ty, dev)
-    dp, ds = _rows(dt, "dt", (B, T, N), 1, ty, dev)
+    qp, qs = _rows(q, "q", (B, T, G, K), 2, G * K, ty, gpu)
+    kp, ks = _rows(k, "k", (B, T, G, K), 2, G * K, ty, gpu)
+    vp, vs = _rows(v, "v", (B, T, N, V), 2, N * V, ty, gpu)
+    dp, ds = _rows(dt, "dt", (B, T, N), 1, N, ty, gpu)
     shapes = dict(dq=(B, T, G, K), dk=(B, T, G, K), dv=(B, T, N, V), ddt=(B, T, N), dA=(N,))
     if dt_bias is not None:
         shapes["ddt_bias"] = (N,)
@@ -776,16 +797,16 @@ def ssm_scan_backward(q, k, v, dt, A, dy, *, dt_bias=None, w_r=None, H_0=None, d
         shapes["dw_r"] = (N, V)
     if want_dH0:
         shapes["dH_0"] = (B, N, K, V)
-    res = {n: _out(out, n, sh, f32, dev, stream) for n, sh in shapes.items()}
-    ws = _scratch(workspace, m2rnn_ssm_backward_workspace_size(B, T, N, G, K, V, code), dev, stream,
+    res = {n: _out(out, n, v, sh, f32, stream) for n, sh in shapes.items()}
+    ws = _scratch(workspace, m2rnn_ssm_backward_workspace_size(B, T, N, G, K, V, code), v, stream,
                   "m2rnn_ssm_backward_workspace_size")
     st = load().m2rnn_ssm_scan_backward(
-        qp, qs, kp, ks, vp, vs, dp, ds, _need(A, "A", (N,), f32, dev), _need(dt_bias, "dt_bias", (N,), f32, dev),
-        _need(w_r, "w_r", (N, V), ty, dev), _need(H_0, "H_0", (B, N, K, V), f32, dev),
-        _need(lengths, "lengths", (B,), torch.int32, dev), _need(dy, "dy", (B, T, N, V), ty, dev),
-        _need(dH_T, "dH_T", (B, N, K, V), f32, dev),
+        qp, qs, kp, ks, vp, vs, dp, ds, _need(A, "A", (N,), f32, gpu), _need(dt_bias, "dt_bias", (N,), f32, gpu),
+        _need(w_r, "w_r", (N, V), ty, gpu), _need(H_0, "H_0", (B, N, K, V), f32, gpu),
+        _need(lengths, "lengths", (B,), torch.int32, gpu), _need(dy, "dy", (B, T, N, V), ty, gpu),
+        _need(dH_T, "dH_T", (B, N, K, V), f32, gpu),
         *(_ptr(res.get(n)) for n in ("dq", "dk", "dv", "ddt", "dA", "ddt_bias", "dw_r", "dH_0")), B, T, N, G, K, V,
-        code, ws.data_ptr(), ws.numel(), _stream_handle(stream))
+        code, ws.data_ptr(), ws.numel(), _on(gpu, stream))
     _check(st, "m2rnn_ssm_scan_backward")
     res["workspace"] = ws
     return res
@@ -797,18 +818,18 @@ def ssm_step(H, q, k, v, dt, A, *, dt_bias=None, w_r=None, y=None, stream=None):
     import torch
     B, G, K = q.shape
     N, V = v.shape[1:]
-    dev, ty, f32 = v.device, v.dtype, torch.float32
+    gpu, ty, f32 = _gpu(v), v.dtype, torch.float32
     code = _dtype_code(v)
-    qp, qs = _rows(q, "q", (B, G, K), 2, ty, dev)
-    kp, ks = _rows(k, "k", (B, G, K), 2, ty, dev)
-    vp, vs = _rows(v, "v", (B, N, V), 2, ty, dev)
-    dp, ds = _rows(dt, "dt", (B, N), 1, ty, dev)
+    qp, qs = _rows(q, "q", (B, G, K), 2, G * K, ty, gpu)
+    kp, ks = _rows(k, "k", (B, G, K), 2, G * K, ty, gpu)
+    vp, vs = _rows(v, "v", (B, N, V), 2, N * V, ty, gpu)
+    dp, ds = _rows(dt, "dt", (B, N), 1, N, ty, gpu)
     if y is None:
-        y = _alloc((B, N, V), ty, dev, stream)
-    st = load().m2rnn_ssm_step(_need(H, "H", (B, N, K, V), f32, dev), qp, qs, kp, ks, vp, vs, dp, ds,
-                               _need(A, "A", (N,), f32, dev), _need(dt_bias, "dt_bias", (N,), f32, dev),
-                               _need(w_r, "w_r", (N, V), ty, dev), _need(y, "y", (B, N, V), ty, dev), B, N, G, K, V,
-                               code, _stream_handle(stream))
+        y = _alloc(v, (B, N, V), ty, stream)
+    st = load().m2rnn_ssm_step(_need(H, "H", (B, N, K, V), f32, gpu), qp, qs, kp, ks, vp, vs, dp, ds,
+                               _need(A, "A", (N,), f32, gpu), _need(dt_bias, "dt_bias", (N,), f32, gpu),
+                               _need(w_r, "w_r", (N, V), ty, gpu), _need(y, "y", (B, N, V), ty, gpu), B, N, G, K, V,
+                               code, _on(gpu, stream))
     _check(st, "m2rnn_ssm_step")
     return y
 
@@ -826,10 +847,10 @@ class GradPlan:
             raise ValueError(f"{len(grads)} gradients, {len(outs)} outputs")
         if not grads:
             raise ValueError("no gradients")
-        self.device = grads[0].device
+        self.gpu = _gpu(grads[0])
         for i, (g, o) in enumerate(zip(grads, outs)):
             for t, name in ((g, f"grads[{i}]"), (o, f"out[{i}]")):
-                _need(t, name, g.shape, g.dtype, self.device)
+                _need(t, name, g.shape, g.dtype, self.gpu)
         n = len(grads)
         counts = (ctypes.c_int64 * n)(*(g.numel() for g in grads))
         codes = (ctypes.c_int32 * n)(*(_dtype_code(g) for g in grads))
@@ -838,8 +859,8 @@ class GradPlan:
         size = m2rnn_grad_plan_size(n, counts)
         host = torch.empty(size, dtype=torch.uint8)
         _check(m2rnn_grad_plan_build(n, ptrs, optrs, counts, codes, host.data_ptr(), size), "m2rnn_grad_plan_build")
-        self.table = host.to(self.device)
-        self.workspace = torch.empty(m2rnn_grad_workspace_size(), dtype=torch.uint8, device=self.device)
+        self.table = host.to(grads[0].device)
+        self.workspace = self.table.new_empty(m2rnn_grad_workspace_size())
         self.grads, self.outs = grads, outs
 
 
@@ -853,9 +874,9 @@ def grad_norm(plan: GradPlan, *, norm=None, stream=None):
     """Global norm of the plan's tensors: a 0-dim fp32 tensor on the device."""
     import torch
     if norm is None:
-        norm = _alloc((), torch.float32, plan.device, stream)
+        norm = _alloc(plan.table, (), torch.float32, stream)
     st = load().m2rnn_grad_norm(plan.table.data_ptr(), plan.table.numel(), norm.data_ptr(), plan.workspace.data_ptr(),
-                                plan.workspace.numel(), _stream_handle(stream))
+                                plan.workspace.numel(), _on(plan.gpu, stream))
     _check(st, "m2rnn_grad_norm")
     return norm
 
@@ -865,8 +886,8 @@ def grad_clip(plan: GradPlan, max_norm: float, *, norm=None, stream=None):
     outputs.  Returns the norm before clipping, a 0-dim fp32 tensor."""
     import torch
     if norm is None:
-        norm = _alloc((), torch.float32, plan.device, stream)
+        norm = _alloc(plan.table, (), torch.float32, stream)
     st = load().m2rnn_grad_clip(plan.table.data_ptr(), plan.table.numel(), float(max_norm), norm.data_ptr(),
-                                plan.workspace.data_ptr(), plan.workspace.numel(), _stream_handle(stream))
+                                plan.workspace.data_ptr(), plan.workspace.numel(), _on(plan.gpu, stream))
     _check(st, "m2rnn_grad_clip")
     return norm

@@ -6,6 +6,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/m2rnn.h"
@@ -25,6 +26,19 @@ __device__ __forceinline__ float from_f32<float>(float x) {
 template <>
 __device__ __forceinline__ uint16_t from_f32<uint16_t>(float x) {
   return static_cast<uint16_t>(pack_bf16x2(x, 0.f) & 0xFFFFu);
+}
+
+// Allows `kernel` its dynamic shared memory, once per GPU: `done` is a static
+// of the caller, a bit for each device.
+inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // 2^x and 1 / x by the hardware's approximations (a few units of fp32).
@@ -140,7 +154,7 @@ struct GradChunk {
 };
 static_assert(sizeof(GradChunk) == 32, "plan entries are 32 bytes");
 
-constexpr int kGradChunk = 16384;  // elements of a piece
+constexpr int kGradChunk = 8192;  // elements of a piece
 
 size_t grad_clip_scratch_bytes();
 // clip false: only the norm.

@@ -400,50 +400,55 @@ __global__ void __launch_bounds__(kThreads) ssm_sum_heads_kernel(const float* dq
 // flight; y_t is summed over a thread's rows, then over the y in order.  Bound
 // by HBM (8 bytes per state element) at large batches, by latency at small.
 template <typename T, int kVec>
-__global__ void __launch_bounds__(kThreads) ssm_step_kernel(float* H, SsmArgs A) {
-  constexpr int kAhead = 4;
-  __shared__ float red[kThreads * kVec];
-  const int64_t bn = blockIdx.x;
-  const int b = static_cast<int>(bn / A.N), n = static_cast<int>(bn % A.N), g = n / (A.N / A.G), K = A.K, V = A.V;
-  const int cols = V / kVec, rows = kThreads / cols, x = threadIdx.x % cols, y = threadIdx.x / cols;
-  const T* q = static_cast<const T*>(A.q) + b * A.q_stride + static_cast<int64_t>(g) * K;
-  const T* k = static_cast<const T*>(A.k) + b * A.k_stride + static_cast<int64_t>(g) * K;
-  const T* v = static_cast<const T*>(A.v) + b * A.v_stride + static_cast<int64_t>(n) * V + x * kVec;
+__global__ void __launch_bounds__(kThreads, 3) ssm_step_kernel(float* H, SsmArgs A) {
+  constexpr int kAhead = kVec == 4 ? 8 : 4;
+  __shared__ float red[kThreads * kVec], sk[128], sq[128];
+  const int bn = blockIdx.x, b = bn / A.N, n = bn - b * A.N, g = n / (A.N / A.G), K = A.K, V = A.V;
+  const int cols = V / kVec, rows = kThreads / cols, y = threadIdx.x / cols, x = threadIdx.x - y * cols;
   const float s = to_f32(static_cast<const T*>(A.dt)[b * A.dt_stride + n]) + (A.dt_bias ? A.dt_bias[n] : 0.f);
   const float An = A.A[n];
-  float acc[kVec], vx[kVec], D = 0.f, a = 0.f;
+  float* h = H + static_cast<int64_t>(bn) * K * V + x * kVec;
+  const bool own = y < rows;
+  float st[kAhead][kVec];
+  auto load = [&](int r0) {
 #pragma unroll
-  for (int e = 0; e < kVec; ++e) acc[e] = vx[e] = 0.f;
-  if (y < rows) {
-    float* h = H + bn * K * V + x * kVec;
+    for (int u = 0; u < kAhead; ++u) {
+      const int r = r0 + u * rows;
+      if (!own || r >= K) continue;
+      if constexpr (kVec == 4)
+        *reinterpret_cast<float4*>(st[u]) = *reinterpret_cast<const float4*>(h + r * V);
+      else
+        st[u][0] = h[r * V];
+    }
+  };
+  load(y);  // before anything waits
+  float vx[kVec], acc[kVec];
+  {
+    const T* v = static_cast<const T*>(A.v) + b * A.v_stride + static_cast<int64_t>(n) * V + x * kVec;
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) vx[e] = to_f32(v[e]);
+    for (int e = 0; e < kVec; ++e) {
+      vx[e] = own ? to_f32(v[e]) : 0.f;
+      acc[e] = 0.f;
+    }
+  }
+  const float D = softplus_f(s), a = expf(D * An);
+  if (threadIdx.x < K) {
+    sk[threadIdx.x] = D * to_f32(static_cast<const T*>(A.k)[b * A.k_stride + static_cast<int64_t>(g) * K + threadIdx.x]);
+    sq[threadIdx.x] = to_f32(static_cast<const T*>(A.q)[b * A.q_stride + static_cast<int64_t>(g) * K + threadIdx.x]);
+  }
+  __syncthreads();
+  if (own) {
     for (int r0 = y; r0 < K; r0 += kAhead * rows) {
-      float st[kAhead][kVec], kr[kAhead], qr[kAhead];
+      if (r0 != y) load(r0);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const int r = r0 + u * rows;
         if (r >= K) continue;
-        if constexpr (kVec == 4)
-          *reinterpret_cast<float4*>(st[u]) = *reinterpret_cast<const float4*>(h + r * V);
-        else
-          st[u][0] = h[r * V];
-        kr[u] = to_f32(k[r]);
-        qr[u] = to_f32(q[r]);
-      }
-      if (r0 == y) {  // behind the first loads
-        D = softplus_f(s);
-        a = expf(D * An);
-      }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int r = r0 + u * rows;
-        if (r >= K) continue;
-        const float kd = D * kr[u];
+        const float kd = sk[r], qr = sq[r];
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
           st[u][e] = fmaf(a, st[u][e], kd * vx[e]);
-          acc[e] = fmaf(qr[u], st[u][e], acc[e]);
+          acc[e] = fmaf(qr, st[u][e], acc[e]);
         }
         if constexpr (kVec == 4)
           *reinterpret_cast<float4*>(h + r * V) = *reinterpret_cast<const float4*>(st[u]);
@@ -461,16 +466,15 @@ __global__ void __launch_bounds__(kThreads) ssm_step_kernel(float* H, SsmArgs A)
     if (A.w_r)
       t = fmaf(to_f32(static_cast<const T*>(A.w_r)[n * V + c]),
                to_f32(static_cast<const T*>(A.v)[b * A.v_stride + static_cast<int64_t>(n) * V + c]), t);
-    static_cast<T*>(A.y)[bn * V + c] = from_f32<T>(t);
+    static_cast<T*>(A.y)[static_cast<int64_t>(bn) * V + c] = from_f32<T>(t);
   }
 }
 
 inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
-}
+// Shared memory at K = V = 128.
+constexpr int kMaxOut = sizeof(float) * kL * (2 * 129 + 128);
+constexpr int kMaxGrad = sizeof(float) * (kL * (4 * 129 + 2 * 129) + 128 * 129);
 
 template <typename T>
 cudaError_t forward_simt(const SsmArgs& a, cudaStream_t s) {
@@ -479,7 +483,8 @@ cudaError_t forward_simt(const SsmArgs& a, cudaStream_t s) {
   float* states = static_cast<float*>(a.ws);
   float* tot = states + blocks * KV;
   const size_t sm1 = sizeof(float) * kL * (a.K + a.V), sm2 = sizeof(float) * kL * (2 * (a.K + 1) + a.V);
-  cudaError_t e = allow_smem(ssm_chunk_out_kernel<T>, sm2);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_chunk_out_kernel<T>), kMaxOut, done);
   if (e != cudaSuccess) return e;
   ssm_chunk_sum_kernel<T, false><<<static_cast<unsigned>(blocks), kThreads, sm1, s>>>(a, states, tot, nc);
   ssm_chunk_scan_kernel<false><<<dim3(a.B * a.N, (KV + kThreads - 1) / kThreads), kThreads, 0, s>>>(
@@ -506,7 +511,8 @@ cudaError_t backward_simt(const SsmArgs& a, cudaStream_t s) {
   }
   const size_t sm1 = sizeof(float) * kL * (a.K + a.V);
   const size_t sm2 = sizeof(float) * (kL * (4 * (a.K + 1) + 2 * (a.V + 1)) + a.K * (a.V + 1));
-  cudaError_t e = allow_smem(ssm_chunk_grad_kernel<T>, sm2);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_chunk_grad_kernel<T>), kMaxGrad, done);
   if (e != cudaSuccess) return e;
   const dim3 scan(a.B * a.N, (KV + kThreads - 1) / kThreads);
   ssm_chunk_sum_kernel<T, false><<<static_cast<unsigned>(blocks), kThreads, sm1, s>>>(a, states, tot, nc);

@@ -659,8 +659,8 @@ cudaError_t run(const GradArgs& w, cudaStream_t s) {
   constexpr int VS = VP < 64 ? VP : 64;
   using Sum = SumShape<KP, VS>;
   using Gr = GradShape<KP, VP>;
-  cudaError_t e =
-      cudaFuncSetAttribute(ssm_grad_kernel<KP, VP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Gr::kBytes);
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_grad_kernel<KP, VP>), Gr::kBytes, done);
   if (e != cudaSuccess) return e;
   const SsmArgs& a = w.a;
   const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.B) * a.N * w.nc);

@@ -550,10 +550,9 @@ template <int KP, int VS>
 cudaError_t run(const ScanArgs& w, int64_t chains, cudaStream_t s) {
   using Walk = WalkShape<KP, VS>;
   using Out = OutShape<KP, VS>;
-  cudaError_t e =
-      cudaFuncSetAttribute(ssm_walk_kernel<KP, VS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Walk::kBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(ssm_out_kernel<KP, VS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Out::kBytes);
+  static std::atomic<uint64_t> walk{0}, out{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_walk_kernel<KP, VS>), Walk::kBytes, walk);
+  if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(ssm_out_kernel<KP, VS>), Out::kBytes, out);
   if (e != cudaSuccess) return e;
   const int64_t heads = chains * w.slices;
   ssm_walk_kernel<KP, VS><<<static_cast<unsigned>(heads * w.segs), kThreads, Walk::kBytes, s>>>(w);
