@@ -86,9 +86,11 @@ __device__ void load_rows(const void* p, int64_t base, int64_t stride, int width
   }
 }
 
-// kRev false: sum_j exp(l_L - l_j) D_j k_j v_j^T;  true: sum_i exp(l_i) q_i u_i^T.
-template <typename T, bool kRev>
-__global__ void __launch_bounds__(kThreads) ssm_chunk_sum_kernel(SsmArgs A, float* states, float* tot, int nc) {
+// blockIdx.y = 0: sum_j exp(l_L - l_j) D_j k_j v_j^T;  1: sum_i exp(l_i) q_i u_i^T, `other` floats behind.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) ssm_chunk_sum_kernel(SsmArgs A, float* states, int64_t other, float* tot,
+                                                                 int nc) {
+  const bool rev = blockIdx.y == 1;
   extern __shared__ float sm[];
   __shared__ Decays dc;
   const int64_t id = blockIdx.x;
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) ssm_chunk_sum_kernel(SsmArgs A, floa
   float *ra = sm, *rb = sm + kL * K;
   load_decays<T>(A, b, n, t0, len, dc);
   const int64_t row = static_cast<int64_t>(b) * A.T;
-  if (kRev) {
+  if (rev) {
     load_rows<T>(A.q, row * A.q_stride + static_cast<int64_t>(g) * K, A.q_stride, K, t0, len, ra, K);
     load_rows<T>(A.dy, (row * A.N + n) * V, static_cast<int64_t>(A.N) * V, V, t0, len, rb, V);
   } else {
@@ -105,45 +107,49 @@ __global__ void __launch_bounds__(kThreads) ssm_chunk_sum_kernel(SsmArgs A, floa
     load_rows<T>(A.v, row * A.v_stride + static_cast<int64_t>(n) * V, A.v_stride, V, t0, len, rb, V);
   }
   __syncthreads();
-  float* out = states + id * K * V;
+  float* out = states + (rev ? other : 0) + id * K * V;
   for (int e = threadIdx.x; e < K * V; e += kThreads) {
     const int kk = e / V, vv = e % V;
     float s = 0.f;
 #pragma unroll 8
     for (int j = 0; j < kL; ++j) {
-      const float w = kRev ? dc.first[j] : dc.last[j] * dc.D[j];
+      const float w = rev ? dc.first[j] : dc.last[j] * dc.D[j];
       s = fmaf(ra[j * K + kk] * w, rb[j * V + vv], s);
     }
     out[e] = s;
   }
-  if (tot != nullptr && threadIdx.x == 0) tot[id] = dc.tot;
+  if (!rev && threadIdx.x == 0) tot[id] = dc.tot;
 }
 
-// In place: chunk sums -> the state before each chunk (kRev: the state
-// gradient behind each chunk), and the state (gradient) at the other end.
-template <bool kRev>
-__global__ void __launch_bounds__(kThreads) ssm_chunk_scan_kernel(float* states, const float* tot, const float* from,
-                                                                  float* to, int nc, int KV) {
+// In place: chunk sums -> the state before each chunk (blockIdx.z = 1, for
+// the sums `other` floats behind: the state gradient behind each chunk), and
+// the state (gradient) at the other end.
+__global__ void __launch_bounds__(kThreads) ssm_chunk_scan_kernel(float* states, int64_t other, const float* tot,
+                                                                  const float* H_0, float* H_T, const float* dH_T,
+                                                                  float* dH_0, int nc, int KV) {
+  constexpr int kAhead = 8;  // chunks' loads in flight: the walk itself is one FMA a chunk
+  const bool rev = blockIdx.z == 1;
   const int e = blockIdx.y * kThreads + threadIdx.x;
   const int64_t bn = blockIdx.x;
   if (e >= KV) return;
-  constexpr int kAhead = 8;  // pieces' loads in flight: the walk itself is one FMA a piece
+  const float* from = rev ? dH_T : H_0;
+  float* to = rev ? dH_0 : H_T;
   float cur = from ? from[bn * KV + e] : 0.f;
-  float* st = states + bn * nc * KV + e;
+  float* st = states + (rev ? other : 0) + bn * nc * KV + e;
   const float* tt = tot + bn * nc;
   for (int i = 0; i < nc; i += kAhead) {
     float u[kAhead], a[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (i + j >= nc) continue;
-      const int c = kRev ? nc - 1 - i - j : i + j;
+      const int c = rev ? nc - 1 - i - j : i + j;
       u[j] = st[static_cast<int64_t>(c) * KV];
       a[j] = tt[c];
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (i + j >= nc) continue;
-      const int c = kRev ? nc - 1 - i - j : i + j;
+      const int c = rev ? nc - 1 - i - j : i + j;
       st[static_cast<int64_t>(c) * KV] = cur;
       cur = fmaf(a[j], cur, u[j]);
     }
@@ -486,9 +492,9 @@ cudaError_t forward_simt(const SsmArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_chunk_out_kernel<T>), kMaxOut, done);
   if (e != cudaSuccess) return e;
-  ssm_chunk_sum_kernel<T, false><<<static_cast<unsigned>(blocks), kThreads, sm1, s>>>(a, states, tot, nc);
-  ssm_chunk_scan_kernel<false><<<dim3(a.B * a.N, (KV + kThreads - 1) / kThreads), kThreads, 0, s>>>(
-      states, tot, a.H_0, a.H_T, nc, KV);
+  ssm_chunk_sum_kernel<T><<<static_cast<unsigned>(blocks), kThreads, sm1, s>>>(a, states, 0, tot, nc);
+  ssm_chunk_scan_kernel<<<dim3(a.B * a.N, (KV + kThreads - 1) / kThreads), kThreads, 0, s>>>(
+      states, 0, tot, a.H_0, a.H_T, nullptr, nullptr, nc, KV);
   ssm_chunk_out_kernel<T><<<static_cast<unsigned>(blocks), kThreads, sm2, s>>>(a, states, nc);
   return cudaGetLastError();
 }
@@ -514,26 +520,14 @@ cudaError_t backward_simt(const SsmArgs& a, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_chunk_grad_kernel<T>), kMaxGrad, done);
   if (e != cudaSuccess) return e;
-  const dim3 scan(a.B * a.N, (KV + kThreads - 1) / kThreads);
-  ssm_chunk_sum_kernel<T, false><<<static_cast<unsigned>(blocks), kThreads, sm1, s>>>(a, states, tot, nc);
-  ssm_chunk_sum_kernel<T, true><<<static_cast<unsigned>(blocks), kThreads, sm1, s>>>(a, rstates, nullptr, nc);
-  ssm_chunk_scan_kernel<false><<<scan, kThreads, 0, s>>>(states, tot, a.H_0, nullptr, nc, KV);
-  ssm_chunk_scan_kernel<true><<<scan, kThreads, 0, s>>>(rstates, tot, a.dH_T, a.dH_0, nc, KV);
+  ssm_chunk_sum_kernel<T><<<dim3(static_cast<unsigned>(blocks), 2), kThreads, sm1, s>>>(a, states, blocks * KV, tot, nc);
+  ssm_chunk_scan_kernel<<<dim3(a.B * a.N, (KV + kThreads - 1) / kThreads, 2), kThreads, 0, s>>>(
+      states, blocks * KV, tot, a.H_0, nullptr, a.dH_T, a.dH_0, nc, KV);
   ssm_chunk_grad_kernel<T><<<static_cast<unsigned>(blocks), kThreads, sm2, s>>>(a, states, rstates, o, nc);
   return launch_ssm_grad_sums(a, o, nc, s);
 }
 
 }  // namespace
-
-cudaError_t launch_ssm_piece_scan(float* states, const float* tot, const float* from, float* to, int nc, int KV,
-                                  int64_t chains, bool rev, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(chains), (KV + kThreads - 1) / kThreads);
-  if (rev)
-    ssm_chunk_scan_kernel<true><<<grid, kThreads, 0, s>>>(states, tot, from, to, nc, KV);
-  else
-    ssm_chunk_scan_kernel<false><<<grid, kThreads, 0, s>>>(states, tot, from, to, nc, KV);
-  return cudaGetLastError();
-}
 
 cudaError_t launch_ssm_grad_sums(const SsmArgs& a, const SsmGradOut& o, int nc, cudaStream_t s) {
   ssm_grad_sums_kernel<<<dim3(a.N, a.dw_r != nullptr ? 1 + (a.V + 31) / 32 : 1), kSumThreads, 0, s>>>(

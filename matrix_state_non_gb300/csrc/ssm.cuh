@@ -20,12 +20,6 @@ __device__ __forceinline__ int ssm_len(const SsmArgs& A, int b) {
   return A.lengths ? min(max(A.lengths[b], 0), A.T) : A.T;
 }
 
-// In place over nc pieces of a sequence: the pieces' own sums become the
-// state before each piece (rev: the state gradient behind each), from `from`
-// (null = 0); `to` (may be null) receives the state at the other end.
-cudaError_t launch_ssm_piece_scan(float* states, const float* tot, const float* from, float* to, int nc, int KV,
-                                  int64_t chains, bool rev, cudaStream_t s);
-
 // The tensor-core kernels (bf16 inputs).
 size_t ssm_mma_forward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V);
 cudaError_t launch_ssm_mma_forward(const SsmArgs& a, cudaStream_t s);
