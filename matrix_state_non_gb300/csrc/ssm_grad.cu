@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_sum_kernel(GradArgs W, int 
   cp_async_commit();
   cp_async_wait<0>();
   __syncthreads();
-  float U[Sh::kMt][Sh::kNt][4] = {};
+  // The small parts on their own: four adds, not twelve, at the sum's full size are truncated.
+  float U[Sh::kMt][Sh::kNt][4] = {}, low[Sh::kMt][Sh::kNt][4] = {};
 #pragma unroll
   for (int jt = 0; jt < 4; ++jt) {
     constexpr int kPairs = Sh::kNt / 2;
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_sum_kernel(GradArgs W, int 
       for (int i = 0; i < 3; ++i)
 #pragma unroll
         for (int nt = 0; nt < Sh::kNt; ++nt)
-          mma_bf16_16816(U[mt][nt], p[i], vf[nt / 2][2 * (nt & 1)], vf[nt / 2][2 * (nt & 1) + 1]);
+          mma_bf16_16816(i < 2 ? low[mt][nt] : U[mt][nt], p[i], vf[nt / 2][2 * (nt & 1)], vf[nt / 2][2 * (nt & 1) + 1]);
     }
   }
   float* out = W.sums[rev] + static_cast<int64_t>(blockIdx.x) * K * V + v0;
@@ -109,11 +110,12 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_sum_kernel(GradArgs W, int 
         const int r = (mw * Sh::kMt + mt) * 16 + g + 8 * h, col = (nw * Sh::kNt + nt) * 8 + 2 * q4;
         if (r >= K || col >= width) continue;
         float* at = out + r * V + col;
+        const float x = U[mt][nt][2 * h] + low[mt][nt][2 * h], y = U[mt][nt][2 * h + 1] + low[mt][nt][2 * h + 1];
         if (V % 2 == 0) {
-          *reinterpret_cast<float2*>(at) = make_float2(U[mt][nt][2 * h], U[mt][nt][2 * h + 1]);
+          *reinterpret_cast<float2*>(at) = make_float2(x, y);
         } else {
-          at[0] = U[mt][nt][2 * h];
-          if (col + 1 < width) at[1] = U[mt][nt][2 * h + 1];
+          at[0] = x;
+          if (col + 1 < width) at[1] = y;
         }
       }
 }
@@ -188,6 +190,19 @@ __device__ __forceinline__ void split_scores(const float (&s)[2][4], uint32_t (&
     split3(s[h][0], s[h][1], p[2][2 * h], p[1][2 * h], p[0][2 * h]);
     split3(s[h][2], s[h][3], p[2][2 * h + 1], p[1][2 * h + 1], p[0][2 * h + 1]);
   }
+}
+
+// x += P f, P in three parts: the products are summed on their own, from the
+// smallest part up, and added in fp32.  The tensor core truncates its adds;
+// on the running sum itself that is a bias which dA and ddt_bias, differences
+// of sums over all steps, cannot take.
+__device__ __forceinline__ void add_split(float (&x)[4], const uint32_t (&p)[3][4], uint32_t f0, uint32_t f1) {
+  float t[4];
+  mma_bf16_16816_zc(t, p[0], f0, f1);
+  mma_bf16_16816(t, p[1], f0, f1);
+  mma_bf16_16816(t, p[2], f0, f1);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] += t[e];
 }
 
 // Phase 4: block (chain, chunk).  K padded to KP, V to VP.
@@ -368,11 +383,8 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
       for (int kt = 0; kt < kKt; ++kt) {
         uint32_t f[4];
         ldmatrix_x4_trans(f, at_rows<KP>(sK, 16 * jt, 16 * kt, lane));
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          mma_bf16_16816(x[2 * kt], p[i], f[0], f[1]);
-          mma_bf16_16816(x[2 * kt + 1], p[i], f[2], f[3]);
-        }
+        add_split(x[2 * kt], p, f[0], f[1]);
+        add_split(x[2 * kt + 1], p, f[2], f[3]);
       }
     }
     row_dots(sQ, x, qd);
@@ -436,11 +448,8 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
       for (int kt = 0; kt < kKt; ++kt) {
         uint32_t f[4];
         ldmatrix_x4_trans(f, at_rows<KP>(sQ, 16 * it, 16 * kt, lane));
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          mma_bf16_16816(x[2 * kt], p[i], f[0], f[1]);
-          mma_bf16_16816(x[2 * kt + 1], p[i], f[2], f[3]);
-        }
+        add_split(x[2 * kt], p, f[0], f[1]);
+        add_split(x[2 * kt + 1], p, f[2], f[3]);
       }
     }
     cp_async_wait<0>();
@@ -527,11 +536,8 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
       for (int vt = 0; vt < kVt; ++vt) {
         uint32_t f[4];
         ldmatrix_x4_trans(f, at_rows<VP>(sU, 16 * it, 16 * vt, lane));
-#pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          mma_bf16_16816(x[2 * vt], p[i], f[0], f[1]);
-          mma_bf16_16816(x[2 * vt + 1], p[i], f[2], f[3]);
-        }
+        add_split(x[2 * vt], p, f[0], f[1]);
+        add_split(x[2 * vt + 1], p, f[2], f[3]);
       }
     }
     const uint16_t* wr = A.w_r ? static_cast<const uint16_t*>(A.w_r) + n * V : nullptr;
