@@ -178,6 +178,113 @@ def test_ssm_scan_backward(B, T, N, G, K, V, dtype, lengths, h0):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_ssm_gradient_is_a_difference(dtype):
+    """The kernel's gradient along a random direction against the oracle's
+    forward in 64 bits: (L(x + h e) - L(x - h e)) / 2h, off by O(h^2)."""
+    from matrix_state_non_gb300 import binding as m
+    d = ssm_inputs(2, 70, 4, 2, 16, 32, dtype, seed=61)
+    g = ssm_dev(d, dtype)
+    a, kw = _scan_args(g)
+    r = m.ssm_scan_backward(*a, g["dy"], dH_T=g["dH_T"], want_dH0=True, **kw)
+    rng, h = np.random.default_rng(62), 1e-5
+    for n in SSM_IN + SSM_OPT:
+        e = rng.normal(size=d[n].shape)
+
+        def loss(s):
+            p = dict(d, **{n: d[n] + s * e})
+            y, H = o.ssm_scan(*(p[i] for i in SSM_IN), **{i: p[i] for i in SSM_OPT})
+            return (y * d["dy"]).sum() + (H * d["dH_T"]).sum()
+
+        want, got = (loss(h) - loss(-h)) / (2 * h), host(r["d" + n])
+        tol = TOL_STEP if n in ("dt", "A", "dt_bias") else TOL_GRAD
+        assert abs((got * e).sum() - want) <= tol * np.linalg.norm(got) * np.linalg.norm(e), n
+
+
+def test_ssm_nan_stays_behind_its_step():
+    """A NaN in q touches its own step, one in k or dt the steps from its own
+    on; earlier steps and other heads and sequences stay as they were."""
+    import torch
+    from matrix_state_non_gb300 import binding as m
+    for dtype in ("bf16", "f32"):
+        d = ssm_inputs(2, 150, 2, 2, 32, 32, dtype, seed=71)
+        base = ssm_dev(d, dtype)
+        a, kw = _scan_args(base)
+        ref = m.ssm_scan(*a, **kw)["y"]
+        for n, later in (("q", False), ("k", True), ("dt", True)):
+            g = {i: None if x is None else x.clone() for i, x in base.items()}
+            g[n][1, 77, 1] = float("nan")
+            a, kw = _scan_args(g)
+            y = m.ssm_scan(*a, **kw)["y"]
+            bad = torch.zeros_like(y, dtype=torch.bool)
+            bad[1, 77:(150 if later else 78), 1] = True
+            assert torch.equal(torch.isnan(y), bad), (dtype, n)
+            assert torch.equal(y[~bad], ref[~bad]), (dtype, n)
+
+
+def test_offsets_beyond_32_bits():
+    """Rows 2^20 elements apart: the last tokens lie beyond 2^32 elements."""
+    import torch
+    from matrix_state_non_gb300 import binding as m
+    T, wide = 4200, 1 << 20
+    d = ssm_inputs(1, T, 1, 1, 16, 16, "bf16", seed=81, h0=False)
+    g = ssm_dev(d, "bf16")
+    big = torch.empty((1, T, wide), dtype=torch.bfloat16, device="cuda")
+    s, at = {}, wide - 64
+    for n, w in (("v", 16), ("k", 16), ("q", 16), ("dt", 1)):
+        big[..., at:at + w] = g[n].flatten(2)
+        s[n] = big[..., at:at + w].unflatten(-1, g[n].shape[2:])
+        at += w
+    want, got = m.ssm_scan(*(g[n] for n in SSM_IN)), m.ssm_scan(s["q"], s["k"], s["v"], s["dt"], g["A"])
+    assert torch.equal(got["y"], want["y"]) and torch.equal(got["H_T"], want["H_T"])
+    a = m.ssm_scan_backward(*(g[n] for n in SSM_IN), g["dy"])
+    b = m.ssm_scan_backward(s["q"], s["k"], s["v"], s["dt"], g["A"], g["dy"])
+    assert all(torch.equal(a[n], b[n]) for n in ("dq", "dk", "dv", "ddt", "dA"))
+    c = conv_inputs(1, T, 16, 4, "bf16", seed=82)
+    w, bias, dy = dev(c["w"], "bf16"), dev(c["bias"], "bf16"), dev(c["dy"])
+    x = big[..., wide - 64:wide - 48]
+    assert torch.equal(m.causal_conv(x, w, bias)["y"], m.causal_conv(x.contiguous(), w, bias)["y"])
+    p, q = m.causal_conv_backward(x, w, bias, dy), m.causal_conv_backward(x.contiguous(), w, bias, dy)
+    assert all(torch.equal(p[n], q[n]) for n in p)
+    del big
+    # More than 2^31 elements in one dense tensor.
+    x = torch.empty((1, 70000, 32768), dtype=torch.bfloat16, device="cuda")
+    x[:, :100] = 1.0
+    x[:, -100:] = torch.randn((1, 100, 32768), device="cuda")
+    w = torch.randn((32768, 4), device="cuda").bfloat16()
+    y = m.causal_conv(x, w, silu=False)["y"]
+    assert torch.equal(y[:, -90:], m.causal_conv(x[:, -100:].contiguous(), w, silu=False)["y"][:, 10:])
+
+
+def test_torch_helpers_refuse():
+    import torch
+    from matrix_state_non_gb300 import binding as m
+    g = ssm_dev(ssm_inputs(2, 8, 2, 1, 16, 16, "bf16", seed=91), "bf16")
+    a, kw = _scan_args(g)
+    with pytest.raises(ValueError, match="k: expected"):
+        m.ssm_scan(a[0], a[1].float(), *a[2:])
+    with pytest.raises(ValueError, match="A: expected"):
+        m.ssm_scan(*a[:4], a[4].bfloat16())
+    with pytest.raises(ValueError, match="dense"):
+        m.ssm_scan(*a[:2], a[2].transpose(2, 3).contiguous().transpose(2, 3), *a[3:])
+    with pytest.raises(ValueError, match="T rows apart"):
+        m.ssm_scan(*a[:2], torch.cat([a[2], a[2]], 1)[:, :8], *a[3:])
+    with pytest.raises(ValueError, match="contiguous"):
+        m.ssm_scan(*a, H_0=g["H_0"].transpose(2, 3).contiguous().transpose(2, 3))
+    with pytest.raises(ValueError, match="lengths"):
+        m.ssm_scan(*a, lengths=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    with pytest.raises(TypeError, match="unsupported"):
+        m.ssm_scan(*(x.half() for x in a[:4]), a[4])
+    with pytest.raises(m.M2RNNError, match="unsupported"):
+        wide = torch.zeros((1, 2, 1, 130), dtype=torch.bfloat16, device="cuda")
+        m.ssm_scan(wide, wide, wide, wide[..., 0], torch.zeros(1, device="cuda"))
+    with pytest.raises(m.M2RNNError):
+        m.grad_clip(m.grad_plan([a[4]]), -1.0)
+    x = torch.zeros((1, 4, 8), device="cuda")
+    with pytest.raises(m.M2RNNError, match="invalid"):
+        m.causal_conv(x, torch.zeros((8, 4), device="cuda"), out=dict(y=x))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("decay", [0.0, -1e-3, -300.0, 0.5])
 def test_ssm_scan_extreme_decays(dtype, decay):
     """No decay, almost none, states forgotten within a step, growing states."""
