@@ -20,6 +20,12 @@ __device__ __forceinline__ int ssm_len(const SsmArgs& A, int b) {
   return A.lengths ? min(max(A.lengths[b], 0), A.T) : A.T;
 }
 
+// The CUDA-core kernels (fp32 inputs).
+size_t ssm_f32_forward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V);
+size_t ssm_f32_backward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V);
+cudaError_t launch_ssm_f32_forward(const SsmArgs& a, cudaStream_t s);
+cudaError_t launch_ssm_f32_backward(const SsmArgs& a, cudaStream_t s);
+
 // The tensor-core kernels (bf16 inputs).
 size_t ssm_mma_forward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V);
 cudaError_t launch_ssm_mma_forward(const SsmArgs& a, cudaStream_t s);
