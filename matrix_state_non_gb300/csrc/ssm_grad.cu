@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_sum_kernel(GradArgs W, int 
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const float2 x = r < 2 ? wa : wb;
-        split3(bf16lo(kf[r]) * x.x, bf16hi(kf[r]) * x.y, p[2][r], p[1][r], p[0][r]);
+        split3_weighted(kf[r], x.x, x.y, p[2][r], p[1][r], p[0][r]);
       }
 #pragma unroll
       for (int i = 0; i < 3; ++i)

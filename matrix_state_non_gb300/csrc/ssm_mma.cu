@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             const float2 w = r & 1 ? wb : wa;
-            split3(bf16lo(kf[r]) * w.x, bf16hi(kf[r]) * w.y, hi[r], mid[r], lo[r]);
+            split3_weighted(kf[r], w.x, w.y, hi[r], mid[r], lo[r]);
           }
 #pragma unroll
           for (int vt = 0; vt < Sh::kVt; ++vt)

@@ -44,13 +44,19 @@ struct TileLoader {
     if (vec) {
       const int r = threadIdx.x / kPer, c = (threadIdx.x % kPer) * 8;
       const uint16_t* src = p + static_cast<int64_t>(t0 + r) * stride + c;
-      uint32_t dst = tile + r * Tile<kCols>::kPitch + c * 2;
-      const int live = c < width ? len - t0 - r : 0;
+      const uint32_t dst = tile + r * Tile<kCols>::kPitch + c * 2;
+      const int64_t step = kStep * stride;
+      if (t0 + kChunk <= len && c < width) {
 #pragma unroll
-      for (int i = 0; i < kChunk / kStep; ++i) {
-        const bool ok = i * kStep < live;
-        cp_async_16(dst + i * kStep * Tile<kCols>::kPitch, ok ? src : p, ok);
-        src += kStep * stride;
+        for (int i = 0; i < kChunk / kStep; ++i, src += step)
+          cp_async_16(dst + i * kStep * Tile<kCols>::kPitch, src, true);
+      } else {
+        const int live = c < width ? len - t0 - r : 0;
+#pragma unroll
+        for (int i = 0; i < kChunk / kStep; ++i, src += step) {
+          const bool ok = i * kStep < live;
+          cp_async_16(dst + i * kStep * Tile<kCols>::kPitch, ok ? src : p, ok);
+        }
       }
     } else {
 #pragma unroll 4
@@ -82,10 +88,18 @@ __device__ __forceinline__ uint32_t at_cols(uint32_t tile, int r0, int c0, int l
 // A pair of fp32 values as three bf16 pairs whose sum is exact to 2^-24.
 __device__ __forceinline__ void split3(float x, float y, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
   hi = pack_bf16x2(x, y);
-  x -= bf16lo(hi);
-  y -= bf16hi(hi);
+  sub2(x, y, bf16lo(hi), bf16hi(hi));
   mid = pack_bf16x2(x, y);
-  lo = pack_bf16x2(x - bf16lo(mid), y - bf16hi(mid));
+  sub2(x, y, bf16lo(mid), bf16hi(mid));
+  lo = pack_bf16x2(x, y);
+}
+
+// The same of two bf16 values times two weights.
+__device__ __forceinline__ void split3_weighted(uint32_t k, float w0, float w1, uint32_t& hi, uint32_t& mid,
+                                                uint32_t& lo) {
+  float x, y;
+  mul2(x, y, bf16lo(k), bf16hi(k), w0, w1);
+  split3(x, y, hi, mid, lo);
 }
 
 // The decays of one chunk.  l_i is the sum of D A over the chunk's steps up to
