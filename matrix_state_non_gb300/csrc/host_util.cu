@@ -46,6 +46,21 @@ bool make_tensor_map_btnx(CUtensorMap* m, const void* base, CUtensorMapDataType 
   return r == CUDA_SUCCESS;
 }
 
+bool make_tensor_map_rows(CUtensorMap* m, const void* base, int X, int heads, int64_t row_stride, int T, int B, int bx,
+                          int bt) {
+  auto enc = encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t row = static_cast<cuuint64_t>(row_stride) * 2;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(X), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(T),
+                        static_cast<cuuint64_t>(B)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(X) * 2, row, row * T};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(bx), 1, static_cast<cuuint32_t>(bt), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 namespace {
 // -2 = not yet read from the environment.
 std::atomic<int> g_kernel_family{-2};

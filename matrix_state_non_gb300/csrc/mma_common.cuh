@@ -248,4 +248,10 @@ __device__ __forceinline__ bool mbar_wait_timed(uint32_t bar, uint32_t parity, S
 bool make_tensor_map_btnx(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int esize, int B,
                           int T, int N, int X, int bx, int by);
 
+// Host: 4-D bf16 tensor map {X, heads, T, B} of rows `row_stride` elements
+// apart (a column slice of a wider tensor), box {bx, 1, bt, 1} of 128-byte
+// rows, 128-byte swizzle, zero fill out of bounds.
+bool make_tensor_map_rows(CUtensorMap* m, const void* base, int X, int heads, int64_t row_stride, int T, int B, int bx,
+                          int bt);
+
 }  // namespace m2rnn

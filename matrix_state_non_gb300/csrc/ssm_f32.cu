@@ -205,6 +205,7 @@ __device__ __forceinline__ const float* u_rows(const SsmArgs& A, const Place& p)
 template <int L>
 __global__ void __launch_bounds__(kThreads) ssm_chunk_sum_kernel(SsmArgs A, float* states, int64_t other, float* tot,
                                                                  int nc) {
+  if (blockIdx.x == 0 && threadIdx.x < sizeof(StatusBlock) / 4) static_cast<unsigned*>(A.ws)[threadIdx.x] = 0u;
   extern __shared__ __align__(16) float sm[];
   __shared__ Decays<L> dc;
   const bool rev = blockIdx.y == 1;
@@ -490,18 +491,18 @@ int64_t chunks_of(int64_t B, int64_t T, int64_t N, int L) { return B * N * ((T +
 }  // namespace
 
 size_t ssm_f32_forward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
-  return sizeof(float) * static_cast<size_t>(chunks_of(B, T, N, kFwd)) * (static_cast<size_t>(K) * V + 1);
+  return sizeof(StatusBlock) + sizeof(float) * static_cast<size_t>(chunks_of(B, T, N, kFwd)) * (static_cast<size_t>(K) * V + 1);
 }
 
 size_t ssm_f32_backward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V) {
   const size_t heads = G == N ? 0 : 2 * static_cast<size_t>(B) * T * N * K;
-  return sizeof(float) * (static_cast<size_t>(chunks_of(B, T, N, kBwd)) * (2 * static_cast<size_t>(K) * V + 3 + V) + heads);
+  return sizeof(StatusBlock) + sizeof(float) * (static_cast<size_t>(chunks_of(B, T, N, kBwd)) * (2 * static_cast<size_t>(K) * V + 3 + V) + heads);
 }
 
 cudaError_t launch_ssm_f32_forward(const SsmArgs& a, cudaStream_t s) {
   const int nc = (a.T + kFwd - 1) / kFwd, KV = a.K * a.V;
   const int64_t blocks = chunks_of(a.B, a.T, a.N, kFwd);
-  float* states = static_cast<float*>(a.ws);
+  float* states = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + sizeof(StatusBlock));
   float* tot = states + blocks * KV;
   static std::atomic<uint64_t> sum{0}, out{0};
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_chunk_sum_kernel<kFwd>), 4 * sum_floats(kFwd, 128, 128), sum);
@@ -519,7 +520,7 @@ cudaError_t launch_ssm_f32_forward(const SsmArgs& a, cudaStream_t s) {
 cudaError_t launch_ssm_f32_backward(const SsmArgs& a, cudaStream_t s) {
   const int nc = (a.T + kBwd - 1) / kBwd, KV = a.K * a.V;
   const int64_t blocks = chunks_of(a.B, a.T, a.N, kBwd), heads = static_cast<int64_t>(a.B) * a.T * a.N * a.K;
-  float* states = static_cast<float*>(a.ws);
+  float* states = reinterpret_cast<float*>(static_cast<uint8_t*>(a.ws) + sizeof(StatusBlock));
   float* rstates = states + blocks * KV;
   float2* ab = reinterpret_cast<float2*>(rstates + blocks * KV);
   float* tot = reinterpret_cast<float*>(ab + blocks);

@@ -639,6 +639,7 @@ struct Layout {
 
 Layout make_layout(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V) {
   Layout l{};
+  l.total = sizeof(StatusBlock);
   auto take = [&](size_t bytes) {
     const size_t at = l.total;
     l.total += (bytes + 15) / 16 * 16;
@@ -711,7 +712,8 @@ cudaError_t launch_ssm_mma_backward(const SsmArgs& a, cudaStream_t s) {
   w.vk = vec(a.k, a.k_stride, a.K);
   w.vv = vec(a.v, a.v_stride, a.V);
   w.vu = vec(a.dy, static_cast<int64_t>(a.N) * a.V, a.V);
-  cudaError_t e = launch_ssm_decay(a, ws + l.decay, reinterpret_cast<float*>(ws + l.tot), w.nc, true, s);
+  cudaError_t e = launch_ssm_decay(a, ws + l.decay, reinterpret_cast<float*>(ws + l.tot), w.nc, true,
+                                  reinterpret_cast<StatusBlock*>(ws), s);
   if (e != cudaSuccess) return e;
   const int kp = padded(a.K), vp = padded(a.V);
   e = cudaErrorInvalidValue;

@@ -25,6 +25,7 @@
 #include <cstdint>
 
 #include "ssm_mma.cuh"
+#include "ssm_tc.cuh"
 
 namespace m2rnn {
 namespace {
@@ -36,7 +37,9 @@ constexpr int kThreads = 128;  // four warps
 // steps first and only from there over the blocks, each from its own end: no
 // two long sums are ever subtracted, so fp32 is enough.
 template <bool kGrad>
-__global__ void __launch_bounds__(256) ssm_decay_kernel(SsmArgs A, void* out, float* tot, int nc) {
+__global__ void __launch_bounds__(256) ssm_decay_kernel(SsmArgs A, void* out, float* tot, int nc,
+                                                        StatusBlock* status) {
+  if (blockIdx.x == 0 && threadIdx.x < sizeof(StatusBlock) / 4) reinterpret_cast<unsigned*>(status)[threadIdx.x] = 0u;
   const int lane = threadIdx.x & 31, heads = (A.N + 7) / 8, own = lane >> 3;
   const unsigned bc = blockIdx.x / heads;
   const int n = (blockIdx.x - bc * heads) * 8 + (threadIdx.x >> 5), b = bc / nc, c = bc - b * nc;
@@ -105,12 +108,16 @@ __global__ void __launch_bounds__(256) ssm_decay_kernel(SsmArgs A, void* out, fl
 struct ScanArgs {
   SsmArgs a;
   const ChunkDecay* decay;  // [B N][chunks]
+  const float* wD;          // of the first chunk: exp(l_63 - l_j) D_j; a chunk's wD_step floats apart
+  int64_t wD_step;
   const float* tot;         // [B N][chunks]: exp(l_63)
-  float* since;             // [B N][chunks]: decay from the segment's start to the chunk's
-  uint4* local;             // [B N][slices][chunks][fragments]: a segment's own state before each chunk
+  float* since;             // of the first chunk: decay from the segment's start to the chunk's; since_step apart
+  int64_t since_step;
+  uint4* local;             // [B N][slices][chunks][fragments]: a segment's own state before each chunk (kTile:
+                            // of every second chunk, in the order of tc_state_at)
   float4* sums;             // [B N][slices][segs][2 x fragments]: the state each segment leaves
   float* seg_tot;           // [B N][segs]
-  uint4* start;             // [B N][slices][segs][fragments]: the state before each segment
+  uint4* start;             // [B N][slices][segs][fragments]: the state before each segment (kTile: likewise)
   int nc, segs, per_seg, slices;
   bool vq, vk, vv;          // rows that asynchronous copies can take
 };
@@ -134,8 +141,8 @@ struct WalkShape {
   static constexpr int kBlocks = KP * VS > 4096 ? 2 : 3;  // per SM (registers)
 };
 
-// Phase 2.
-template <int KP, int VS>
+// Phase 2.  kTile: states for the tiles of ssm_tc.cu.
+template <int KP, int VS, bool kTile>
 __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk_kernel(ScanArgs W) {
   using Sh = WalkShape<KP, VS>;
   using Fr = Frag<KP, VS>;
@@ -157,13 +164,13 @@ __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk
                                     A.k_stride, K, W.vk};
   const TileLoader<VS, kThreads> lv{
       static_cast<const uint16_t*>(A.v) + row * A.v_stride + static_cast<int64_t>(n) * V + v0, A.v_stride, width, W.vv};
-  const ChunkDecay* pd = W.decay + static_cast<int64_t>(bn) * W.nc;
+  const float* pw = W.wD + static_cast<int64_t>(bn) * W.nc * W.wD_step;
   const float* ptot = W.tot + static_cast<int64_t>(bn) * W.nc;
   auto load_chunk = [&](int c) {
     const uint32_t st = base + (c & 1) * Sh::kStage;
     lk.load(st, c * kChunk, len);
     lv.load(st + Sh::kK, c * kChunk, len);
-    if (tid < kChunk / 4) cp_async_16(st + Sh::kK + Sh::kV + tid * 16, pd[c].wD + tid * 4, true);
+    if (tid < kChunk / 4) cp_async_16(st + Sh::kK + Sh::kV + tid * 16, pw + c * W.wD_step + tid * 4, true);
     cp_async_commit();
   };
 
@@ -188,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk
   each([&](float& s, int k, int v, bool ok) { s = from != nullptr && ok ? from[k * V + v0 + v] : 0.f; });
 
   float tot = 0.f, decay = 1.f;  // of a chunk; since the segment's start
-  uint4* local = W.local + ((static_cast<int64_t>(bn) * W.slices + slice) * W.nc + c0) * Fr::kCount;
+  uint4* local = W.local + (static_cast<int64_t>(head) * (kTile ? W.nc / 2 : W.nc) + (kTile ? c0 / 2 : c0)) * Fr::kCount;
   if (c0 < live) {
     load_chunk(c0);
     tot = ptot[c0];
@@ -201,22 +208,40 @@ __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk
       load_chunk(c + 1);
       tot = ptot[c + 1];
     }
-    if (slice == 0 && tid == 0) W.since[static_cast<int64_t>(bn) * W.nc + c] = decay;
+    if (slice == 0 && tid == 0) W.since[(static_cast<int64_t>(bn) * W.nc + c) * W.since_step] = decay;
     decay *= tot_c;
     const int stage = (c & 1) * Sh::kStage;
     const uint32_t sK = base + stage, sV = sK + Sh::kK;
     const float* wD = reinterpret_cast<const float*>(smem + stage + Sh::kK + Sh::kV);
     if (busy) {
+      if constexpr (kTile) {
+        if ((c & 1) == 0) {
+          uint8_t* out = reinterpret_cast<uint8_t*>(local);
 #pragma unroll
-      for (int vt = 0; vt < Sh::kVt; ++vt)
+          for (int vt = 0; vt < Sh::kVt; ++vt)
 #pragma unroll
-        for (int kt = 0; kt < Sh::kKt; ++kt) {
-          const auto& s = S[vt][kt];
-          local[Fr::at(nw * Sh::kKt + kt, mw * Sh::kVt + vt, lane)] =
-              make_uint4(pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[0][2], s[0][3]),
-                         pack_bf16x2(s[1][2], s[1][3]));
+            for (int kt = 0; kt < Sh::kKt; ++kt)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)  // a core matrix of 128 bytes to a store
+                  *reinterpret_cast<uint32_t*>(out + tc_state_at(16 * (nw * Sh::kKt + kt) + 8 * h + 2 * q4,
+                                                                 16 * (mw * Sh::kVt + vt) + 8 * e + g)) =
+                      pack_bf16x2(S[vt][kt][h][2 * e], S[vt][kt][h][2 * e + 1]);
+          local += Fr::kCount;
         }
-      local += Fr::kCount;
+      } else {
+#pragma unroll
+        for (int vt = 0; vt < Sh::kVt; ++vt)
+#pragma unroll
+          for (int kt = 0; kt < Sh::kKt; ++kt) {
+            const auto& s = S[vt][kt];
+            local[Fr::at(nw * Sh::kKt + kt, mw * Sh::kVt + vt, lane)] =
+                make_uint4(pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[0][2], s[0][3]),
+                           pack_bf16x2(s[1][2], s[1][3]));
+          }
+        local += Fr::kCount;
+      }
       float U[Sh::kVt][Sh::kKt][2][4] = {};
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
@@ -282,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk
 }
 
 // Phase 3: block (chain and slice, 256 halves of fragments); thread (fragment, h).
-template <int KP, int VS>
+template <int KP, int VS, bool kTile>
 __global__ void __launch_bounds__(256) ssm_segment_scan_kernel(ScanArgs W) {
   using Fr = Frag<KP, VS>;
   constexpr int kAhead = 8, kN = 2 * Fr::kCount;
@@ -291,6 +316,8 @@ __global__ void __launch_bounds__(256) ssm_segment_scan_kernel(ScanArgs W) {
   if (e >= kN) return;
   const int64_t bn = blockIdx.x / W.slices;
   const int slice = blockIdx.x % W.slices;
+  const int lane = (e >> 1) & 31, tile = e >> 6, vt = tile % Fr::kVt, kt = tile / Fr::kVt;
+  const int v = 16 * vt + 8 * (e & 1) + (lane >> 2), k = 16 * kt + 2 * (lane & 3);  // (and k + 1, k + 8, k + 9)
   const float4* sums = W.sums + static_cast<int64_t>(blockIdx.x) * W.segs * kN + e;
   uint2* start = reinterpret_cast<uint2*>(W.start) + static_cast<int64_t>(blockIdx.x) * W.segs * kN + e;
   const float* tot = W.seg_tot + bn * W.segs;
@@ -307,16 +334,20 @@ __global__ void __launch_bounds__(256) ssm_segment_scan_kernel(ScanArgs W) {
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
       if (i + j >= W.segs) continue;
-      start[static_cast<int64_t>(i + j) * kN] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+      if constexpr (kTile) {
+        uint8_t* out = reinterpret_cast<uint8_t*>(W.start) +
+                       (static_cast<int64_t>(blockIdx.x) * W.segs + i + j) * (Fr::kCount * 16) + tc_state_at(k, v);
+        *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(s.x, s.y);
+        *reinterpret_cast<uint32_t*>(out + tc_state_at(8, 0)) = pack_bf16x2(s.z, s.w);
+      } else {
+        start[static_cast<int64_t>(i + j) * kN] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+      }
       s = make_float4(fmaf(a[j], s.x, u[j].x), fmaf(a[j], s.y, u[j].y), fmaf(a[j], s.z, u[j].z),
                       fmaf(a[j], s.w, u[j].w));
     }
   }
-  if (A.H_T == nullptr) return;
-  const int lane = (e >> 1) & 31, tile = e >> 6, vt = tile % Fr::kVt, kt = tile / Fr::kVt;
-  const int v = slice * VS + 16 * vt + 8 * (e & 1) + (lane >> 2), k = 16 * kt + 2 * (lane & 3);
-  if (v >= A.V) return;
-  float* H = A.H_T + bn * A.K * A.V + v;
+  if (A.H_T == nullptr || slice * VS + v >= A.V) return;
+  float* H = A.H_T + bn * A.K * A.V + slice * VS + v;
   const float x[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
@@ -498,11 +529,14 @@ __global__ void __launch_bounds__(kThreads, OutShape<KP, VS>::kBlocks) ssm_out_k
   }
 }
 
+constexpr int64_t kMinTiles = 2 * 152;
+
 int padded_rows(int64_t K) { return K <= 32 ? 32 : K <= 64 ? 64 : 128; }
 int slice_cols(int64_t K, int64_t V) { return V <= 16 ? 16 : V <= 32 || K <= 32 ? 32 : 64; }
 
 struct Plan {
   int kp, vs, slices, segs, per_seg, nc;
+  bool tile;  // outputs on tcgen05 (ssm_tc.cu)
 };
 
 // Segments: as many as the GPU holds walking blocks at once.
@@ -513,20 +547,26 @@ Plan make_plan(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
   p.slices = static_cast<int>((V + p.vs - 1) / p.vs);
   p.nc = static_cast<int>((T + kChunk - 1) / kChunk);
   const int64_t chains = B * N * p.slices, room = 152 * (p.kp * p.vs > 4096 ? 2 : 3);
+  // The tcgen05 outputs are built for 64 x 64 states and want a few tiles for each SM: below that the
+  // blocks of ssm_out_kernel, four to an SM, are done sooner.
+  p.tile = p.kp == kTcK && p.vs == kTcV && chains * ((p.nc + 1) / 2) >= kMinTiles;
+  const int unit = p.tile ? 2 : 1;
+  if (p.tile) p.nc = (p.nc + 1) / 2 * 2;
   int64_t segs = room / chains;
-  segs = segs < 1 ? 1 : segs > p.nc ? p.nc : segs;
-  p.per_seg = static_cast<int>((p.nc + segs - 1) / segs);
+  segs = segs < 1 ? 1 : segs > p.nc / unit ? p.nc / unit : segs;
+  p.per_seg = static_cast<int>((p.nc / unit + segs - 1) / segs) * unit;
   p.segs = (p.nc + p.per_seg - 1) / p.per_seg;
   return p;
 }
 
-// Scratch, in bytes, each on a 16-byte boundary.
+// Scratch, in bytes, each on a 16-byte boundary; the status block first.
 struct Layout {
   size_t decay, tot, since, local, sums, seg_tot, start, total;
 };
 
 Layout make_layout(const Plan& p, int64_t chains) {
   Layout l{};
+  l.total = sizeof(StatusBlock);
   auto take = [&](size_t bytes) {
     const size_t at = l.total;
     l.total += (bytes + 15) / 16 * 16;
@@ -534,7 +574,8 @@ Layout make_layout(const Plan& p, int64_t chains) {
   };
   const size_t state = static_cast<size_t>(p.kp) * p.vs, chunks = static_cast<size_t>(chains) * p.nc,
                segs = static_cast<size_t>(chains) * p.segs;
-  l.decay = take(chunks * sizeof(ChunkDecay));
+  l.decay = take(chunks * sizeof(ChunkDecay));  // (the tiles' decays and states are smaller; rows that they
+  // cannot take fall back on the larger)
   l.tot = take(chunks * 4);
   l.since = take(chunks * 4);
   l.local = take(chunks * p.slices * state * 2);
@@ -546,31 +587,41 @@ Layout make_layout(const Plan& p, int64_t chains) {
   return l;
 }
 
+template <int KP, int VS, bool kTile>
+cudaError_t walk(const ScanArgs& w, int64_t heads, cudaStream_t s) {
+  using Walk = WalkShape<KP, VS>;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_walk_kernel<KP, VS, kTile>), Walk::kBytes, done);
+  if (e != cudaSuccess) return e;
+  ssm_walk_kernel<KP, VS, kTile><<<static_cast<unsigned>(heads * w.segs), kThreads, Walk::kBytes, s>>>(w);
+  if (w.segs > 1)
+    ssm_segment_scan_kernel<KP, VS, kTile>
+        <<<dim3(static_cast<unsigned>(heads), (2 * Frag<KP, VS>::kCount + 255) / 256), 256, 0, s>>>(w);
+  return cudaGetLastError();
+}
+
 template <int KP, int VS>
 cudaError_t run(const ScanArgs& w, int64_t chains, cudaStream_t s) {
-  using Walk = WalkShape<KP, VS>;
   using Out = OutShape<KP, VS>;
-  static std::atomic<uint64_t> walk{0}, out{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_walk_kernel<KP, VS>), Walk::kBytes, walk);
-  if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(ssm_out_kernel<KP, VS>), Out::kBytes, out);
-  if (e != cudaSuccess) return e;
   const int64_t heads = chains * w.slices;
-  ssm_walk_kernel<KP, VS><<<static_cast<unsigned>(heads * w.segs), kThreads, Walk::kBytes, s>>>(w);
-  if (w.segs > 1)
-    ssm_segment_scan_kernel<KP, VS>
-        <<<dim3(static_cast<unsigned>(heads), (2 * Frag<KP, VS>::kCount + 255) / 256), 256, 0, s>>>(w);
+  cudaError_t e = walk<KP, VS, false>(w, heads, s);
+  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> done{0};
+  e = allow_smem(reinterpret_cast<const void*>(ssm_out_kernel<KP, VS>), Out::kBytes, done);
+  if (e != cudaSuccess) return e;
   ssm_out_kernel<KP, VS><<<static_cast<unsigned>(heads * w.nc), kThreads, Out::kBytes, s>>>(w);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_ssm_decay(const SsmArgs& a, void* out, float* tot, int nc, bool grad, cudaStream_t s) {
+cudaError_t launch_ssm_decay(const SsmArgs& a, void* out, float* tot, int nc, bool grad, StatusBlock* status,
+                             cudaStream_t s) {
   const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.B) * nc * ((a.N + 7) / 8));
   if (grad)
-    ssm_decay_kernel<true><<<blocks, 256, 0, s>>>(a, out, tot, nc);
+    ssm_decay_kernel<true><<<blocks, 256, 0, s>>>(a, out, tot, nc, status);
   else
-    ssm_decay_kernel<false><<<blocks, 256, 0, s>>>(a, out, tot, nc);
+    ssm_decay_kernel<false><<<blocks, 256, 0, s>>>(a, out, tot, nc, status);
   return cudaGetLastError();
 }
 
@@ -583,13 +634,15 @@ cudaError_t launch_ssm_mma_forward(const SsmArgs& a, cudaStream_t s) {
   const int64_t chains = static_cast<int64_t>(a.B) * a.N;
   const Layout l = make_layout(p, chains);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
-  ChunkDecay* decay = reinterpret_cast<ChunkDecay*>(ws + l.decay);
-  float* tot = reinterpret_cast<float*>(ws + l.tot);
+  StatusBlock* status = reinterpret_cast<StatusBlock*>(ws);
+  auto vec = [](const void* p, int64_t stride, int width) {
+    return width % 8 == 0 && stride % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
+  };
   ScanArgs w{};
   w.a = a;
-  w.decay = decay;
-  w.tot = tot;
+  w.tot = reinterpret_cast<float*>(ws + l.tot);
   w.since = reinterpret_cast<float*>(ws + l.since);
+  w.since_step = 1;
   w.local = reinterpret_cast<uint4*>(ws + l.local);
   w.sums = reinterpret_cast<float4*>(ws + l.sums);
   w.seg_tot = reinterpret_cast<float*>(ws + l.seg_tot);
@@ -598,13 +651,30 @@ cudaError_t launch_ssm_mma_forward(const SsmArgs& a, cudaStream_t s) {
   w.segs = p.segs;
   w.per_seg = p.per_seg;
   w.slices = p.slices;
-  auto vec = [](const void* p, int64_t stride, int width) {
-    return width % 8 == 0 && stride % 8 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0;
-  };
   w.vq = vec(a.q, a.q_stride, a.K);
   w.vk = vec(a.k, a.k_stride, a.K);
   w.vv = vec(a.v, a.v_stride, a.V);
-  const cudaError_t e = launch_ssm_decay(a, decay, tot, p.nc, false, s);
+  float* tot = reinterpret_cast<float*>(ws + l.tot);
+  // TMA takes strides below 2^40 bytes.
+  const int64_t widest = a.q_stride > a.k_stride ? (a.q_stride > a.v_stride ? a.q_stride : a.v_stride)
+                                                 : (a.k_stride > a.v_stride ? a.k_stride : a.v_stride);
+  if (p.tile && w.vq && w.vk && w.vv && widest * a.T < (int64_t{1} << 39)) {
+    TileDecay* decay = reinterpret_cast<TileDecay*>(ws + l.decay);
+    w.wD = decay->wD;
+    w.since = &decay->T[2];
+    w.wD_step = w.since_step = sizeof(TileDecay) / sizeof(float);
+    cudaError_t e = launch_ssm_tile_decay(a, decay, tot, p.nc, status, s);
+    if (e == cudaSuccess) e = walk<kTcK, kTcV, true>(w, chains * w.slices, s);
+    if (e != cudaSuccess) return e;
+    return launch_ssm_tc_out(TcOutArgs{a, decay, reinterpret_cast<const uint8_t*>(w.local),
+                                       reinterpret_cast<const uint8_t*>(w.start), status, p.nc, p.nc / 2, p.segs,
+                                       p.per_seg, p.slices}, s);
+  }
+  ChunkDecay* decay = reinterpret_cast<ChunkDecay*>(ws + l.decay);
+  w.decay = decay;
+  w.wD = decay->wD;
+  w.wD_step = sizeof(ChunkDecay) / sizeof(float);
+  const cudaError_t e = launch_ssm_decay(a, decay, tot, p.nc, false, status, s);
   if (e != cudaSuccess) return e;
 #define M2RNN_SSM_CASE(KP, VS) \
   if (p.kp == KP && p.vs == VS) return run<KP, VS>(w, chains, s);

@@ -126,8 +126,9 @@ struct __align__(16) ChunkDecayGrad {
 };
 
 // Decays of every (chain, chunk) into `out` (ChunkDecay, or ChunkDecayGrad for
-// the backward), exp(l_63) into tot.
-cudaError_t launch_ssm_decay(const SsmArgs& a, void* out, float* tot, int nc, bool grad, cudaStream_t s);
+// the backward), exp(l_63) into tot; clears the status block.
+cudaError_t launch_ssm_decay(const SsmArgs& a, void* out, float* tot, int nc, bool grad, StatusBlock* status,
+                             cudaStream_t s);
 
 // exp(a) for a difference a of sums, by the hardware's 2^x.
 __device__ __forceinline__ float exp_fast(float a) { return ex2_fast(1.44269504f * a); }

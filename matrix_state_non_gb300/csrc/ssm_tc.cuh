@@ -1,0 +1,43 @@
+// The outputs of the selective state space scan on tcgen05 (ssm_tc.cu), in
+// tiles of 128 steps: two chunks, one state.
+#pragma once
+
+#include "ssm_mma.cuh"
+
+namespace m2rnn {
+
+// The decays of one chunk (64 steps) for the tiles: sums run within blocks of
+// 32 steps, the rows of one warp's share of a tile.
+struct __align__(16) TileDecay {
+  float rel[kChunk];   // l_i - l before i's block
+  float cf[kChunk];    // exp(l at the end of j's block - l_j) D_j
+  float D[kChunk];     // step sizes, 0 behind the sequence's end
+  float T[4];          // the two blocks' sums; the decay from the segment's start to the chunk's (the walk's); padding
+  float wD[kChunk];    // exp(l_63 - l_j) D_j, for the walk; not copied by the tiles
+};
+static_assert(sizeof(TileDecay) <= sizeof(ChunkDecay), "they share a scratch area");
+constexpr int kTileDecayCopied = (3 * kChunk + 4) * 4;  // bytes of it a tile reads
+
+constexpr int kTcK = 64, kTcV = 64;            // padded widths it is built for
+constexpr int kTcStateBytes = kTcK * kTcV * 2;  // a state as the B operand of Q S
+
+struct TcOutArgs {
+  SsmArgs a;
+  const TileDecay* decay;   // [B N][chunks]
+  const uint8_t* local;     // [B N][slices][tiles][kTcStateBytes]: the segment's own state before each tile
+  const uint8_t* start;     // [B N][slices][segs][kTcStateBytes]: the state before each segment
+  StatusBlock* status;
+  int nc, nt, segs, per_seg, slices;  // chunks (even), tiles, segments, chunks in each (even)
+};
+
+// Byte of state element (k, v) in such an operand: core matrices of 8 value
+// columns by 8 state rows, state rows contiguous.
+__host__ __device__ constexpr int tc_state_at(int k, int v) {
+  return (k / 8) * (kTcV * 16) + (v / 8) * 128 + (v % 8) * 16 + (k % 8) * 2;
+}
+
+cudaError_t launch_ssm_tile_decay(const SsmArgs& a, TileDecay* out, float* tot, int nc, StatusBlock* status,
+                                  cudaStream_t s);
+cudaError_t launch_ssm_tc_out(const TcOutArgs& w, cudaStream_t s);
+
+}  // namespace m2rnn

@@ -160,6 +160,31 @@ def test_ssm_scan(B, T, N, G, K, V, dtype, lengths, h0):
     close(r["H_T"], H, 1e-5, "H_T")
 
 
+# Enough heads and steps for the tcgen05 outputs (tiles of 128 steps).
+TILES = [(4, 1200, 8, 1, 64, 64, None), (5, 1300, 8, 2, 64, 64, (1300, 0, 1, 129, 640)), (4, 1281, 8, 8, 40, 56, None),
+         (3, 1100, 8, 4, 48, 96, (1100, 64, 1000)), (1, 5000, 8, 1, 64, 40, None), (40, 128, 8, 1, 64, 64, None)]
+
+
+@pytest.mark.parametrize("h0", [True, False])
+@pytest.mark.parametrize("B,T,N,G,K,V,lengths", TILES)
+def test_ssm_scan_in_tiles(B, T, N, G, K, V, lengths, h0):
+    from matrix_state_non_gb300 import binding as m
+    d = ssm_inputs(B, T, N, G, K, V, "bf16", seed=T + K + V, h0=h0)
+    g = ssm_dev(d, "bf16")
+    _spoil_ssm(g, lengths)
+    a, kw = _scan_args(g)
+    if not h0:
+        kw["w_r"] = None
+    r = m.ssm_scan(*a, lengths=ints(lengths), **kw)
+    assert m.sync_status(r["workspace"]) == (m.M2RNN_OK, 0)
+    ra, rkw = _scan_args(d)
+    if not h0:
+        rkw["w_r"] = None
+    y, H = o.ssm_scan(*ra, lengths=lengths, **rkw)
+    close(r["y"], y, TOL["bf16"], "y")
+    close(r["H_T"], H, 1e-5, "H_T")
+
+
 @pytest.mark.parametrize("h0", [True, False])
 @pytest.mark.parametrize("B,T,N,G,K,V,dtype,lengths", SSM)
 def test_ssm_scan_backward(B, T, N, G, K, V, dtype, lengths, h0):
