@@ -1,10 +1,13 @@
 // Backward of the selective state space scan on tensor cores (bf16 inputs; the
 // mathematics in ssm.cu), in chunks of 64 steps, every chunk on its own:
 //   1. decays of every chunk;
-//   2. every chunk's sums sum_j last_j D_j k_j v_j^T and sum_i first_i q_i u_i^T;
-//   3. a scan over the chunks turns them into the state S before each chunk and
-//      the state gradient R behind it;
-//   4. the chunk's gradients from q, k, v, u = dy, S and R;
+//   2. the state S before each chunk and the state gradient R behind it: a
+//      sequence is cut into segments, enough of them to fill the GPU, and a
+//      block walks a segment's chunks with the state in its warps' accumulators,
+//      adding sum_j last_j D_j k_j v_j^T (for R, from the last chunk to the
+//      first, sum_i first_i q_i u_i^T);
+//   3. a scan over the segments: what each of them is handed;
+//   4. the chunk's gradients from q, k, v, u = dy, S and R, all chunks at once;
 //   5. sums over the chunks (dA, ddt_bias, dw_r) and over the heads that share
 //      q and k.
 // The gradients are fp32 and good to that: q, k, v and u are exact bf16
@@ -27,36 +30,42 @@ struct GradArgs {
   SsmGradOut o;
   const ChunkDecayGrad* decay;  // [B N][chunks]
   const float* tot;             // [B N][chunks]
-  float* sums[2];               // [B N][chunks][K][V]: of S, of R
-  uint16_t* planes[2];          // [B N][chunks][3][K][V]: S, R in three bf16 parts
-  int nc;
-  bool vq, vk, vv, vu;          // rows that asynchronous copies can take
+  // Of S and of R (walked from the sequence's end):
+  float* local[2];  // [B N][chunks][K][V]: what the segment's own steps put into S before a chunk, R behind it
+  float* since[2];  // [B N][chunks]: the decay between there and the segment's start (R: end)
+  float* ends[2];   // [B N][segs][K][V]: what a segment hands on
+  float* start[2];  // [B N][segs][K][V]: what it is handed
+  float* seg_tot;   // [B N][segs]
+  int nc, segs, per_seg;
+  bool vq, vk, vv, vu;  // rows that asynchronous copies can take
 };
 
 template <int KP, int VS>
-struct SumShape {
+struct WalkShape {
   static constexpr int kMw = KP >= 64 ? 4 : KP / 16, kNw = 4 / kMw;
   static constexpr int kMt = KP / 16 / kMw, kNt = VS / 8 / kNw;
   static_assert(kNt % 2 == 0, "value tiles are loaded in pairs");
-  static constexpr int kK = Tile<KP>::kBytes(kChunk), kV = Tile<VS>::kBytes(kChunk), kBytes = kK + kV + kChunk * 4;
+  static constexpr int kK = Tile<KP>::kBytes(kChunk), kV = Tile<VS>::kBytes(kChunk), kStage = kK + kV + kChunk * 4;
+  static constexpr int kBytes = 2 * kStage;
+  static constexpr int kBlocks = KP * VS > 4096 ? 2 : 3;  // per SM (registers)
 };
 
-// Phase 2: block (S or R, value slice, chain, chunk); rows of the sum along K.
+// Phase 2: block (chain and segment, S or R and value slice); the state's rows along K.
 template <int KP, int VS>
-__global__ void __launch_bounds__(kThreads) ssm_grad_sum_kernel(GradArgs W, int slices) {
-  using Sh = SumShape<KP, VS>;
+__global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_grad_walk_kernel(GradArgs W, int slices) {
+  using Sh = WalkShape<KP, VS>;
   extern __shared__ __align__(16) uint8_t smem[];
   const SsmArgs& A = W.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
   const int mw = warp % Sh::kMw, nw = warp / Sh::kMw;
   const bool rev = blockIdx.y >= static_cast<unsigned>(slices);
-  const int v0 = (blockIdx.y - (rev ? slices : 0)) * VS, bn = blockIdx.x / W.nc, c = blockIdx.x - bn * W.nc;
-  const int b = bn / A.N, n = bn - b * A.N, gq = n / (A.N / A.G), K = A.K, V = A.V, len = ssm_len(A, b), t0 = c * kChunk;
+  const int slice = blockIdx.y - (rev ? slices : 0), v0 = slice * VS;
+  const int bn = blockIdx.x / W.segs, seg = blockIdx.x - bn * W.segs;
+  const int b = bn / A.N, n = bn - b * A.N, gq = n / (A.N / A.G), K = A.K, V = A.V, len = ssm_len(A, b);
   const int width = min(VS, V - v0);
-  const int64_t row = static_cast<int64_t>(b) * A.T;
-  const uint32_t sK = smem_u32(smem), sV = sK + Sh::kK;
-  const float* w = reinterpret_cast<const float*>(smem + Sh::kK + Sh::kV);
-  const ChunkDecayGrad* d = W.decay + blockIdx.x;
+  const int c0 = seg * W.per_seg, live = min(min(W.nc, c0 + W.per_seg), (len + kChunk - 1) / kChunk);
+  const int64_t row = static_cast<int64_t>(b) * A.T, KV = static_cast<int64_t>(K) * V;
+  const uint32_t base = smem_u32(smem);
   const TileLoader<KP, kThreads> lk =
       rev ? TileLoader<KP, kThreads>{static_cast<const uint16_t*>(A.q) + row * A.q_stride + static_cast<int64_t>(gq) * K,
                                      A.q_stride, K, W.vq}
@@ -67,112 +76,141 @@ __global__ void __launch_bounds__(kThreads) ssm_grad_sum_kernel(GradArgs W, int 
                                      static_cast<int64_t>(A.N) * V, width, W.vu}
           : TileLoader<VS, kThreads>{static_cast<const uint16_t*>(A.v) + row * A.v_stride + static_cast<int64_t>(n) * V + v0,
                                      A.v_stride, width, W.vv};
-  if (tid < kChunk / 4) cp_async_16(sV + Sh::kV + tid * 16, (rev ? d->d.first : d->d.wD) + tid * 4, true);
-  lk.load(sK, t0, len);
-  lv.load(sV, t0, len);
-  cp_async_commit();
-  cp_async_wait<0>();
-  __syncthreads();
-  // The small parts on their own: four adds, not twelve, at the sum's full size are truncated.
-  float U[Sh::kMt][Sh::kNt][4] = {}, low[Sh::kMt][Sh::kNt][4] = {};
+  const ChunkDecayGrad* pd = W.decay + static_cast<int64_t>(bn) * W.nc;
+  const float* ptot = W.tot + static_cast<int64_t>(bn) * W.nc;
+  auto load_chunk = [&](int c, int stage) {
+    const uint32_t st = base + stage * Sh::kStage;
+    lk.load(st, c * kChunk, len);
+    lv.load(st + Sh::kK, c * kChunk, len);
+    if (tid < kChunk / 4) cp_async_16(st + Sh::kK + Sh::kV + tid * 16, (rev ? pd[c].d.first : pd[c].d.wD) + tid * 4, true);
+    cp_async_commit();
+  };
+  float S[Sh::kMt][Sh::kNt][4];
+  // Pairs of columns of the accumulators: f(row, column, x, y).
+  auto each = [&](auto f) {
 #pragma unroll
-  for (int jt = 0; jt < 4; ++jt) {
-    constexpr int kPairs = Sh::kNt / 2;
-    uint32_t vf[kPairs][4];
+    for (int mt = 0; mt < Sh::kMt; ++mt)
 #pragma unroll
-    for (int np = 0; np < kPairs; ++np)
-      ldmatrix_x4_trans(vf[np], at_rows<VS>(sV, 16 * jt, nw * Sh::kNt * 8 + 16 * np, lane));
-    const int j = 16 * jt + 2 * q4;
-    const float2 wa = *reinterpret_cast<const float2*>(&w[j]), wb = *reinterpret_cast<const float2*>(&w[j + 8]);
+      for (int nt = 0; nt < Sh::kNt; ++nt)
 #pragma unroll
-    for (int mt = 0; mt < Sh::kMt; ++mt) {
-      uint32_t kf[4], p[3][4];
-      ldmatrix_x4_trans(kf, at_cols<KP>(sK, 16 * jt, (mw * Sh::kMt + mt) * 16, lane));
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float2 x = r < 2 ? wa : wb;
-        split3_weighted(kf[r], x.x, x.y, p[2][r], p[1][r], p[0][r]);
-      }
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
-#pragma unroll
-        for (int nt = 0; nt < Sh::kNt; ++nt)
-          mma_bf16_16816(i < 2 ? low[mt][nt] : U[mt][nt], p[i], vf[nt / 2][2 * (nt & 1)], vf[nt / 2][2 * (nt & 1) + 1]);
-    }
-  }
-  float* out = W.sums[rev] + static_cast<int64_t>(blockIdx.x) * K * V + v0;
-#pragma unroll
-  for (int mt = 0; mt < Sh::kMt; ++mt)
-#pragma unroll
-    for (int nt = 0; nt < Sh::kNt; ++nt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = (mw * Sh::kMt + mt) * 16 + g + 8 * h, col = (nw * Sh::kNt + nt) * 8 + 2 * q4;
-        if (r >= K || col >= width) continue;
-        float* at = out + r * V + col;
-        const float x = U[mt][nt][2 * h] + low[mt][nt][2 * h], y = U[mt][nt][2 * h + 1] + low[mt][nt][2 * h + 1];
-        if (V % 2 == 0) {
-          *reinterpret_cast<float2*>(at) = make_float2(x, y);
-        } else {
-          at[0] = x;
-          if (col + 1 < width) at[1] = y;
+        for (int h = 0; h < 2; ++h) {
+          const int r = (mw * Sh::kMt + mt) * 16 + g + 8 * h, col = (nw * Sh::kNt + nt) * 8 + 2 * q4;
+          f(r, col, S[mt][nt][2 * h], S[mt][nt][2 * h + 1]);
         }
+  };
+  auto store = [&](float* state) {
+    each([&](int r, int col, float& x, float& y) {
+      if (r >= K || col >= width) return;
+      float* at = state + r * V + v0 + col;
+      if (V % 2 == 0) {
+        *reinterpret_cast<float2*>(at) = make_float2(x, y);
+      } else {
+        at[0] = x;
+        if (col + 1 < width) at[1] = y;
       }
+    });
+  };
+  const float* given = seg == (rev ? W.segs - 1 : 0) ? (rev ? A.dH_T : A.H_0) : nullptr;
+  each([&](int r, int col, float& x, float& y) {
+    const float* at = given + bn * KV + r * V + v0 + col;
+    x = given != nullptr && r < K && col < width ? at[0] : 0.f;
+    y = given != nullptr && r < K && col + 1 < width ? at[1] : 0.f;
+  });
+
+  const int step = rev ? -1 : 1, count = live - c0;
+  int c = rev ? live - 1 : c0;
+  float tot = 0.f, decay = 1.f;  // of a chunk; of the chunks so far
+  if (count > 0) {
+    load_chunk(c, 0);
+    tot = ptot[c];
+  }
+  for (int i = 0; i < count; ++i, c += step) {
+    cp_async_wait<0>();
+    __syncthreads();
+    const float tot_c = tot;
+    if (i + 1 < count) {
+      load_chunk(c + step, (i + 1) & 1);
+      tot = ptot[c + step];
+    }
+    const int64_t id = static_cast<int64_t>(bn) * W.nc + c;
+    if (slice == 0 && tid == 0) W.since[rev][id] = decay;
+    decay *= tot_c;
+    store(W.local[rev] + id * KV);
+    const int stage = (i & 1) * Sh::kStage;
+    const uint32_t sK = base + stage, sV = sK + Sh::kK;
+    const float* w = reinterpret_cast<const float*>(smem + stage + Sh::kK + Sh::kV);
+    // The small parts on their own: four adds, not twelve, at the sum's full size are truncated.
+    float U[Sh::kMt][Sh::kNt][4] = {}, low[Sh::kMt][Sh::kNt][4] = {};
+#pragma unroll
+    for (int jt = 0; jt < 4; ++jt) {
+      constexpr int kPairs = Sh::kNt / 2;
+      uint32_t vf[kPairs][4];
+#pragma unroll
+      for (int np = 0; np < kPairs; ++np)
+        ldmatrix_x4_trans(vf[np], at_rows<VS>(sV, 16 * jt, nw * Sh::kNt * 8 + 16 * np, lane));
+      const int j = 16 * jt + 2 * q4;
+      const float2 wa = *reinterpret_cast<const float2*>(&w[j]), wb = *reinterpret_cast<const float2*>(&w[j + 8]);
+#pragma unroll
+      for (int mt = 0; mt < Sh::kMt; ++mt) {
+        uint32_t kf[4], p[3][4];
+        ldmatrix_x4_trans(kf, at_cols<KP>(sK, 16 * jt, (mw * Sh::kMt + mt) * 16, lane));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float2 x = r < 2 ? wa : wb;
+          split3_weighted(kf[r], x.x, x.y, p[2][r], p[1][r], p[0][r]);
+        }
+#pragma unroll
+        for (int part = 0; part < 3; ++part)
+#pragma unroll
+          for (int nt = 0; nt < Sh::kNt; ++nt)
+            mma_bf16_16816(part < 2 ? low[mt][nt] : U[mt][nt], p[part], vf[nt / 2][2 * (nt & 1)],
+                           vf[nt / 2][2 * (nt & 1) + 1]);
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < Sh::kMt; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < Sh::kNt; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[mt][nt][e] = fmaf(tot_c, S[mt][nt][e], U[mt][nt][e] + low[mt][nt][e]);
+  }
+  if (W.segs > 1) {
+    store(W.ends[rev] + (static_cast<int64_t>(bn) * W.segs + seg) * KV);
+    if (!rev && slice == 0 && tid == 0) W.seg_tot[static_cast<int64_t>(bn) * W.segs + seg] = decay;
+  } else if (rev && A.dH_0 != nullptr) {
+    store(A.dH_0 + bn * KV);
+  }
 }
 
-// Phase 3: block (chain, 256 kVec elements of a state, S or R).
-template <int kVec>
-__global__ void __launch_bounds__(256) ssm_grad_scan_kernel(GradArgs W) {
-  constexpr int kAhead = 4;
+// Phase 3: block (chain, 256 elements of a state, S or R).
+__global__ void __launch_bounds__(256) ssm_grad_segments_kernel(GradArgs W) {
+  constexpr int kAhead = 8;
   const SsmArgs& A = W.a;
-  const int KV = A.K * A.V, e = (blockIdx.y * 256 + threadIdx.x) * kVec;
+  const int64_t KV = static_cast<int64_t>(A.K) * A.V, bn = blockIdx.x;
+  const int e = blockIdx.y * 256 + threadIdx.x;
   const bool rev = blockIdx.z == 1;
-  const int64_t bn = blockIdx.x;
   if (e >= KV) return;
-  const float* sums = W.sums[rev] + bn * W.nc * KV + e;
-  uint16_t* planes = W.planes[rev] + bn * W.nc * 3 * KV + e;
-  const float* tot = W.tot + bn * W.nc;
-  const float* from = rev ? A.dH_T : A.H_0;
-  float s[kVec];
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) s[i] = from ? from[bn * KV + e + i] : 0.f;
-  for (int i0 = 0; i0 < W.nc; i0 += kAhead) {
-    float u[kAhead][kVec], a[kAhead];
+  const float* ends = W.ends[rev] + bn * W.segs * KV + e;
+  float* start = W.start[rev] + bn * W.segs * KV + e;
+  const float* tot = W.seg_tot + bn * W.segs;
+  float s = 0.f;
+  for (int i0 = 0; i0 < W.segs; i0 += kAhead) {
+    float u[kAhead], a[kAhead];
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      if (i0 + j >= W.nc) continue;
-      const int c = rev ? W.nc - 1 - i0 - j : i0 + j;
-      if constexpr (kVec == 4)
-        *reinterpret_cast<float4*>(u[j]) = *reinterpret_cast<const float4*>(sums + static_cast<int64_t>(c) * KV);
-      else
-        u[j][0] = sums[static_cast<int64_t>(c) * KV];
+      if (i0 + j >= W.segs) continue;
+      const int c = rev ? W.segs - 1 - i0 - j : i0 + j;
+      u[j] = ends[c * KV];
       a[j] = tot[c];
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
-      if (i0 + j >= W.nc) continue;
-      const int c = rev ? W.nc - 1 - i0 - j : i0 + j;
-      uint16_t* out = planes + static_cast<int64_t>(c) * 3 * KV;
-      if constexpr (kVec == 4) {
-        uint32_t p[3][2];
-        split3(s[0], s[1], p[0][0], p[1][0], p[2][0]);
-        split3(s[2], s[3], p[0][1], p[1][1], p[2][1]);
-#pragma unroll
-        for (int x = 0; x < 3; ++x) *reinterpret_cast<uint2*>(out + x * KV) = make_uint2(p[x][0], p[x][1]);
-      } else {
-        uint32_t p[3];
-        split3(s[0], 0.f, p[0], p[1], p[2]);
-#pragma unroll
-        for (int x = 0; x < 3; ++x) out[x * KV] = static_cast<uint16_t>(p[x]);
-      }
-#pragma unroll
-      for (int x = 0; x < kVec; ++x) s[x] = fmaf(a[j], s[x], u[j][x]);
+      if (i0 + j >= W.segs) continue;
+      start[(rev ? W.segs - 1 - i0 - j : i0 + j) * KV] = s;
+      s = fmaf(a[j], s, u[j]);
     }
   }
-  if (rev && A.dH_0 != nullptr) {
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) A.dH_0[bn * KV + e + i] = s[i];
-  }
+  if (rev && A.dH_0 != nullptr) A.dH_0[bn * KV + e] = s;
 }
 
 template <int KP, int VP>
@@ -255,31 +293,56 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
     for (int e = tid; e < static_cast<int>(sizeof(ChunkDecayGrad)) / 16; e += kThreads)
       cp_async_16(sP + 3 * Sh::kP + e * 16, src + e * 16, true);
   }
-  const uint16_t* gS = W.planes[0] + static_cast<int64_t>(blockIdx.x) * 3 * KV;
-  const uint16_t* gR = W.planes[1] + static_cast<int64_t>(blockIdx.x) * 3 * KV;
-  // Element pieces of the planes: 8 columns of a row, or single elements where rows are not whole pieces.
-  const bool vec = V % 8 == 0;
-  auto load_planes = [&](const uint16_t* src) {
-#pragma unroll
-    for (int p = 0; p < 3; ++p) {
-      if (vec) {
-#pragma unroll 4
-        for (int e = tid; e < KP * (VP / 8); e += kThreads) {
-          const int r = e / (VP / 8), col = (e % (VP / 8)) * 8;
-          const bool ok = r < K && col < V;
-          cp_async_16(sP + p * Sh::kP + r * Tile<VP>::kPitch + col * 2, ok ? src + p * KV + r * V + col : src, ok);
-        }
-      } else {
-        for (int e = tid; e < KP * VP; e += kThreads) {
-          const int r = e / VP, col = e % VP;
-          const uint16_t x = r < K && col < V ? src[p * KV + r * V + col] : uint16_t(0);
-          asm volatile("st.shared.u16 [%0], %1;" ::"r"(sP + p * Sh::kP + r * Tile<VP>::kPitch + col * 2), "h"(x) : "memory");
-        }
-      }
-    }
-    cp_async_commit();
+  cp_async_commit();
+  // S and R, four columns of a row at a time: the segment's own and, behind the segment that S (R) comes into first,
+  // what the segment was handed.
+  constexpr int kPieces = KP * VP / 4 / kThreads, kBatch = kPieces < 4 ? kPieces : 4;
+  const int seg = c / W.per_seg;
+  struct State {
+    const float *own, *start;
+    float since;
   };
-  load_planes(gS);
+  const int64_t at_seg = (static_cast<int64_t>(bn) * W.segs + seg) * KV;
+  const State gS{W.local[0] + blockIdx.x * KV, seg > 0 ? W.start[0] + at_seg : nullptr, W.since[0][blockIdx.x]};
+  const State gR{W.local[1] + blockIdx.x * KV, seg < W.segs - 1 ? W.start[1] + at_seg : nullptr, W.since[1][blockIdx.x]};
+  auto piece_row = [&](int i) { return (i * kThreads + tid) / (VP / 4); };
+  auto piece_col = [&](int i) { return (i * kThreads + tid) % (VP / 4) * 4; };
+  auto fetch = [&](const float* p, int i) {
+    const int r = piece_row(i), col = piece_col(i);
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p == nullptr || r >= K || col >= V) return x;
+    const float* at = p + r * V + col;
+    if (V % 4 == 0) return *reinterpret_cast<const float4*>(at);
+    x.x = at[0];
+    if (col + 1 < V) x.y = at[1];
+    if (col + 2 < V) x.z = at[2];
+    if (col + 3 < V) x.w = at[3];
+    return x;
+  };
+  auto joined = [](const float4& own, const float4& start, float since) {
+    return make_float4(fmaf(since, start.x, own.x), fmaf(since, start.y, own.y), fmaf(since, start.z, own.z),
+                       fmaf(since, start.w, own.w));
+  };
+  auto put = [&](const float4& x, int i) {  // as three bf16 parts
+    uint32_t p[3][2];
+    split3(x.x, x.y, p[0][0], p[1][0], p[2][0]);
+    split3(x.z, x.w, p[0][1], p[1][1], p[2][1]);
+    const uint32_t at = sP + piece_row(i) * Tile<VP>::kPitch + piece_col(i) * 2;
+#pragma unroll
+    for (int part = 0; part < 3; ++part)
+      asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at + part * Sh::kP), "r"(p[part][0]), "r"(p[part][1])
+                   : "memory");
+  };
+#pragma unroll 1
+  for (int i0 = 0; i0 < kPieces; i0 += kBatch) {
+    float4 own[kBatch], start[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) own[i] = fetch(gS.own, i0 + i);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) start[i] = fetch(gS.start, i0 + i);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) put(joined(own[i], start[i], gS.since), i0 + i);
+  }
   cp_async_wait<0>();
   __syncthreads();
 
@@ -404,8 +467,11 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
     }
   }
 
-  __syncthreads();
-  load_planes(gR);  // in S's place, behind the first half of dk
+  // R's first pieces, behind the first half of dk.
+  constexpr int kHold = kPieces < 8 ? kPieces : 8, kDot = kHold < 4 ? kHold : 4;
+  float4 held[kHold];
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) held[i] = fetch(gR.own, i);
 
   const float l0 = dg.last[m0], l1 = dg.last[m1], D0 = d.D[m0], D1 = d.D[m1];
   // Rows j of the transposed scores: factors exp(l_i - l_j), columns i of block it.
@@ -426,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
       }
   };
 
+  float rs = 0.f;  // <R, S>
   {  // zk_j = last_j R v_j + sum_i E_ij (u_i . v_j) q_i
     float x[KP / 8][4] = {};
     uint32_t vf[kVt][4];
@@ -452,7 +519,27 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
         add_split(x[2 * kt + 1], p, f[2], f[3]);
       }
     }
-    cp_async_wait<0>();
+    __syncthreads();  // S has been read
+    auto place = [&](const float4& own, const float4& start, const float4& s_own, const float4& s_start, int i) {
+      const float4 r = joined(own, start, gR.since), s = joined(s_own, s_start, gS.since);
+      rs = fmaf(r.x, s.x, fmaf(r.y, s.y, fmaf(r.z, s.z, fmaf(r.w, s.w, rs))));
+      put(r, i);
+    };
+#pragma unroll
+    for (int i0 = 0; i0 < kHold; i0 += kDot) {
+      float4 start[kDot], s_own[kDot], s_start[kDot];
+#pragma unroll
+      for (int i = 0; i < kDot; ++i) {
+        start[i] = fetch(gR.start, i0 + i);
+        s_own[i] = fetch(gS.own, i0 + i);
+        s_start[i] = fetch(gS.start, i0 + i);
+      }
+#pragma unroll
+      for (int i = 0; i < kDot; ++i) place(held[i0 + i], start[i], s_own[i], s_start[i], i0 + i);
+    }
+#pragma unroll 2
+    for (int i = kHold; i < kPieces; ++i)
+      place(fetch(gR.own, i), fetch(gR.start, i), fetch(gS.own, i), fetch(gS.start, i), i);
     __syncthreads();
     float z[KP / 8][4] = {};
 #pragma unroll
@@ -477,23 +564,6 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
     row_dots(sK, x, ck);
 #pragma unroll
     for (int nt = 0; nt < KP / 8; ++nt) store_rows(dk, qk_stride, K, x[nt], nt, D0, D1);
-  }
-
-  // <R, S>: the thread's pieces of S are loaded here and used behind dv, with
-  // R from shared memory (the two larger parts of both: what the third adds to
-  // a sum over K V elements is far below fp32).
-  constexpr int kDot = KP * VP / 8 / kThreads < 4 ? KP * VP / 8 / kThreads : 4;
-  uint4 s_hi[kDot], s_mid[kDot];
-  if (vec) {
-#pragma unroll
-    for (int i = 0; i < kDot; ++i) {
-      const int e = i * kThreads + tid, r = e / (VP / 8), col = (e % (VP / 8)) * 8;
-      s_hi[i] = s_mid[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < K && col < V) {
-        s_hi[i] = *reinterpret_cast<const uint4*>(gS + r * V + col);
-        s_mid[i] = *reinterpret_cast<const uint4*>(gS + KV + r * V + col);
-      }
-    }
   }
 
   {  // zv_j = last_j R^T k_j + sum_i E_ij (q_i . k_j) u_i
@@ -560,42 +630,6 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
       store_rows(dv, v_stride, V, x[nt], nt, 1.f, 1.f);
     }
   }
-  float rs = 0.f;
-  auto dot_piece = [&](const uint4& hi, const uint4& mid, int r, int col) {
-    const uint4 b0 = ld_shared_v4(sP + r * Tile<VP>::kPitch + col * 2);
-    const uint4 b1 = ld_shared_v4(sP + Sh::kP + r * Tile<VP>::kPitch + col * 2);
-    const uint32_t x0[4] = {hi.x, hi.y, hi.z, hi.w}, x1[4] = {mid.x, mid.y, mid.z, mid.w};
-    const uint32_t y0[4] = {b0.x, b0.y, b0.z, b0.w}, y1[4] = {b1.x, b1.y, b1.z, b1.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      rs = fmaf(bf16lo(x0[i]) + bf16lo(x1[i]), bf16lo(y0[i]) + bf16lo(y1[i]), rs);
-      rs = fmaf(bf16hi(x0[i]) + bf16hi(x1[i]), bf16hi(y0[i]) + bf16hi(y1[i]), rs);
-    }
-  };
-  if (vec) {
-#pragma unroll
-    for (int i = 0; i < kDot; ++i) {
-      const int e = i * kThreads + tid;
-      dot_piece(s_hi[i], s_mid[i], e / (VP / 8), (e % (VP / 8)) * 8);  // zeros where there is no S
-    }
-    for (int e = kDot * kThreads + tid; e < K * (VP / 8); e += kThreads) {
-      const int r = e / (VP / 8), col = (e % (VP / 8)) * 8;
-      if (col < V)
-        dot_piece(*reinterpret_cast<const uint4*>(gS + r * V + col),
-                  *reinterpret_cast<const uint4*>(gS + KV + r * V + col), r, col);
-    }
-  } else {
-    for (int e = tid; e < K * V; e += kThreads) {
-      const int r = e / V, col = e % V;
-      float x = 0.f, y = 0.f;
-#pragma unroll
-      for (int p = 1; p >= 0; --p) {
-        x += bf16_bits_to_f32(static_cast<uint16_t>(ld_shared_u16(sP + p * Sh::kP + r * Tile<VP>::kPitch + col * 2)));
-        y += bf16_bits_to_f32(gS[p * KV + e]);
-      }
-      rs = fmaf(x, y, rs);
-    }
-  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) rs += __shfl_xor_sync(0xffffffffu, rs, o);
   if (lane == 0) red[warp] = rs;
@@ -633,11 +667,32 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
 
 int padded(int64_t x) { return x <= 32 ? 32 : x <= 64 ? 64 : 128; }
 
-struct Layout {
-  size_t decay, tot, sums[2], planes[2], ab, wr, dq, dk, total;
+int slice_cols(int vp) { return vp < 64 ? vp : 64; }
+
+struct Plan {
+  int kp, vp, slices, nc, segs, per_seg;
 };
 
-Layout make_layout(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V) {
+// Segments: as many as the GPU holds walking blocks at once, half of them for S.
+Plan make_plan(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
+  Plan p{};
+  p.kp = padded(K);
+  p.vp = padded(V);
+  const int vs = slice_cols(p.vp);
+  p.slices = static_cast<int>((V + vs - 1) / vs);
+  p.nc = static_cast<int>((T + kChunk - 1) / kChunk);
+  const int64_t room = 152 * (p.kp * vs > 4096 ? 2 : 3) / (2 * B * N * p.slices);
+  const int64_t segs = room < 1 ? 1 : room > p.nc ? p.nc : room;
+  p.per_seg = static_cast<int>((p.nc + segs - 1) / segs);
+  p.segs = (p.nc + p.per_seg - 1) / p.per_seg;
+  return p;
+}
+
+struct Layout {
+  size_t decay, tot, local[2], since[2], ends[2], start[2], seg_tot, ab, wr, dq, dk, total;
+};
+
+Layout make_layout(const Plan& p, int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V) {
   Layout l{};
   l.total = sizeof(StatusBlock);
   auto take = [&](size_t bytes) {
@@ -645,13 +700,17 @@ Layout make_layout(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_
     l.total += (bytes + 15) / 16 * 16;
     return at;
   };
-  const size_t chunks = static_cast<size_t>(B) * N * ((T + kChunk - 1) / kChunk), KV = static_cast<size_t>(K) * V;
+  const size_t chains = static_cast<size_t>(B) * N, chunks = chains * p.nc, KV = static_cast<size_t>(K) * V;
   l.decay = take(chunks * sizeof(ChunkDecayGrad));
   l.tot = take(chunks * 4);
   for (int i = 0; i < 2; ++i) {
-    l.sums[i] = take(chunks * KV * 4);
-    l.planes[i] = take(chunks * KV * 6);
+    l.local[i] = take(chunks * KV * 4);
+    l.since[i] = take(chunks * 4);
+    if (p.segs == 1) continue;
+    l.ends[i] = take(chains * p.segs * KV * 4);
+    l.start[i] = take(chains * p.segs * KV * 4);
   }
+  if (p.segs > 1) l.seg_tot = take(chains * p.segs * 4);
   l.ab = take(chunks * 8);
   l.wr = take(chunks * V * 4);
   if (G != N) {
@@ -662,21 +721,19 @@ Layout make_layout(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_
 }
 
 template <int KP, int VP>
-cudaError_t run(const GradArgs& w, cudaStream_t s) {
+cudaError_t run(const GradArgs& w, int slices, cudaStream_t s) {
   constexpr int VS = VP < 64 ? VP : 64;
-  using Sum = SumShape<KP, VS>;
+  using Walk = WalkShape<KP, VS>;
   using Gr = GradShape<KP, VP>;
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_grad_kernel<KP, VP>), Gr::kBytes, done);
+  static std::atomic<uint64_t> done{0}, done_walk{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_grad_kernel<KP, VP>), Gr::kBytes, done);
+  if (e == cudaSuccess)
+    e = allow_smem(reinterpret_cast<const void*>(ssm_grad_walk_kernel<KP, VS>), Walk::kBytes, done_walk);
   if (e != cudaSuccess) return e;
   const SsmArgs& a = w.a;
-  const unsigned blocks = static_cast<unsigned>(static_cast<int64_t>(a.B) * a.N * w.nc);
-  const int slices = (a.V + VS - 1) / VS, KV = a.K * a.V;
-  ssm_grad_sum_kernel<KP, VS><<<dim3(blocks, 2 * slices), kThreads, Sum::kBytes, s>>>(w, slices);
-  if (KV % 4 == 0)
-    ssm_grad_scan_kernel<4><<<dim3(a.B * a.N, (KV / 4 + 255) / 256, 2), 256, 0, s>>>(w);
-  else
-    ssm_grad_scan_kernel<1><<<dim3(a.B * a.N, (KV + 255) / 256, 2), 256, 0, s>>>(w);
+  const unsigned chains = static_cast<unsigned>(a.B) * a.N, blocks = chains * w.nc;
+  ssm_grad_walk_kernel<KP, VS><<<dim3(chains * w.segs, 2 * slices), kThreads, Walk::kBytes, s>>>(w, slices);
+  if (w.segs > 1) ssm_grad_segments_kernel<<<dim3(chains, (a.K * a.V + 255) / 256, 2), 256, 0, s>>>(w);
   ssm_grad_kernel<KP, VP><<<blocks, kThreads, Gr::kBytes, s>>>(w);
   return cudaGetLastError();
 }
@@ -684,21 +741,27 @@ cudaError_t run(const GradArgs& w, cudaStream_t s) {
 }  // namespace
 
 size_t ssm_mma_backward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V) {
-  return make_layout(B, T, N, G, K, V).total;
+  return make_layout(make_plan(B, T, N, K, V), B, T, N, G, K, V).total;
 }
 
 cudaError_t launch_ssm_mma_backward(const SsmArgs& a, cudaStream_t s) {
-  const Layout l = make_layout(a.B, a.T, a.N, a.G, a.K, a.V);
+  const Plan p = make_plan(a.B, a.T, a.N, a.K, a.V);
+  const Layout l = make_layout(p, a.B, a.T, a.N, a.G, a.K, a.V);
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   GradArgs w{};
   w.a = a;
-  w.nc = (a.T + kChunk - 1) / kChunk;
+  w.nc = p.nc;
+  w.segs = p.segs;
+  w.per_seg = p.per_seg;
   w.decay = reinterpret_cast<const ChunkDecayGrad*>(ws + l.decay);
   w.tot = reinterpret_cast<const float*>(ws + l.tot);
   for (int i = 0; i < 2; ++i) {
-    w.sums[i] = reinterpret_cast<float*>(ws + l.sums[i]);
-    w.planes[i] = reinterpret_cast<uint16_t*>(ws + l.planes[i]);
+    w.local[i] = reinterpret_cast<float*>(ws + l.local[i]);
+    w.since[i] = reinterpret_cast<float*>(ws + l.since[i]);
+    w.ends[i] = reinterpret_cast<float*>(ws + l.ends[i]);
+    w.start[i] = reinterpret_cast<float*>(ws + l.start[i]);
   }
+  w.seg_tot = reinterpret_cast<float*>(ws + l.seg_tot);
   w.o = SsmGradOut{a.dq, a.dk, a.dw_r ? reinterpret_cast<float*>(ws + l.wr) : nullptr,
                    reinterpret_cast<float2*>(ws + l.ab), a.N};
   if (a.G != a.N) {
@@ -715,10 +778,9 @@ cudaError_t launch_ssm_mma_backward(const SsmArgs& a, cudaStream_t s) {
   cudaError_t e = launch_ssm_decay(a, ws + l.decay, reinterpret_cast<float*>(ws + l.tot), w.nc, true,
                                   reinterpret_cast<StatusBlock*>(ws), s);
   if (e != cudaSuccess) return e;
-  const int kp = padded(a.K), vp = padded(a.V);
   e = cudaErrorInvalidValue;
 #define M2RNN_SSM_CASE(KP, VP) \
-  if (kp == KP && vp == VP) e = run<KP, VP>(w, s);
+  if (p.kp == KP && p.vp == VP) e = run<KP, VP>(w, p.slices, s);
   M2RNN_SSM_CASE(32, 32)
   M2RNN_SSM_CASE(32, 64)
   M2RNN_SSM_CASE(32, 128)
