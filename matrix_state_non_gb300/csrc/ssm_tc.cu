@@ -20,6 +20,7 @@
 #include <cstdint>
 
 #include "gate.cuh"
+#include "mma_common.cuh"
 #include "ssm_tc.cuh"
 
 namespace m2rnn {
@@ -87,7 +88,8 @@ static_assert(kSmem <= 227 * 1024, "shared memory");
 // Tensor-memory columns of a slot.
 constexpr uint32_t kColP = 0, kColPV = 64, kColS = 128, kColS0 = 192, kSlot = 256;
 
-constexpr uint32_t kWhereFull = 401, kWhereP = 402, kWhereScores = 403, kWhereOut = 404, kWhereEmpty = 405;
+constexpr uint32_t kWhereFull = 401, kWhereP = 402, kWhereScores = 403, kWhereOut = 404, kWhereEmpty = 405,
+                   kWhereDrain = 406;
 
 // A bounded wait of a whole warp: all lanes go on, or all give up.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, StatusBlock* status,
@@ -95,27 +97,57 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, where));
 }
 
+// The tiles of a block in order: tile tt of (chain, slice) `head`, every gridDim.x-th of them, heads side by side.
+// Stepping and `live` go without divisions where there are no lengths: the warps ask for every tile of the block.
+struct TileWalk {
+  const TcOutArgs& W;
+  unsigned id, tt, head, heads, tiles, rows, rest;
+  __device__ __forceinline__ TileWalk(const TcOutArgs& w, unsigned heads, unsigned tiles)
+      : W(w), id(blockIdx.x), heads(heads), tiles(tiles) {
+    tt = id / heads;
+    head = id - tt * heads;
+    rows = gridDim.x / heads;
+    rest = gridDim.x - rows * heads;
+  }
+  __device__ __forceinline__ bool there() const { return id < tiles; }
+  __device__ __forceinline__ void next() {
+    id += gridDim.x;
+    tt += rows;
+    head += rest;
+    if (head >= heads) {
+      head -= heads;
+      ++tt;
+    }
+  }
+  __device__ __forceinline__ bool live() const {  // steps of the sequence in it
+    const int len = W.a.lengths ? ssm_len(W.a, head / (W.slices * W.a.N)) : W.a.T;
+    return static_cast<int>(tt) * kTile < len;
+  }
+  __device__ __forceinline__ bool handed() const {  // a segment before it
+    return 2 * static_cast<int>(tt) >= W.per_seg;
+  }
+};
+
 struct TilePlace {
   int b, n, gq, v0, width, len, t0, seg;
   int64_t chain, head;
-  bool live;
 };
 
-__device__ __forceinline__ TilePlace tile_place(const TcOutArgs& W, unsigned id, unsigned heads) {
+__device__ __forceinline__ TilePlace tile_place(const TileWalk& at) {
+  const TcOutArgs& W = at.W;
   const SsmArgs& A = W.a;
   TilePlace p;
-  const unsigned tt = id / heads, head = id - tt * heads, bn = head / W.slices, slice = head - bn * W.slices;
-  p.head = head;
+  const unsigned bn = W.slices == 1 ? at.head : at.head / W.slices, slice = at.head - bn * W.slices;
+  p.head = at.head;
   p.chain = bn;
   p.b = bn / A.N;
   p.n = bn - p.b * A.N;
-  p.gq = p.n / (A.N / A.G);
+  p.gq = A.G == 1 ? 0 : p.n / (A.N / A.G);
   p.v0 = slice * kTcV;
   p.width = min(kTcV, A.V - p.v0);
   p.len = ssm_len(A, p.b);
-  p.t0 = tt * kTile;
-  p.seg = 2 * static_cast<int>(tt) / W.per_seg;
-  p.live = p.t0 < p.len;
+  p.t0 = at.tt * kTile;
+  p.seg = 2 * static_cast<int>(at.tt) / W.per_seg;
   return p;
 }
 
@@ -179,11 +211,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&map_v);
     }
     int u = 0;  // live tiles of this block
-    for (unsigned id = blockIdx.x; id < tiles; id += gridDim.x) {
-      const TilePlace t = tile_place(W, id, heads);
-      if (!t.live) continue;
+    bool ok = true;
+    for (TileWalk at(W, heads, tiles); at.there(); at.next()) {
+      if (!at.live()) continue;
+      const TilePlace t = tile_place(at);
       const int s = u % kStages;
-      if (u >= kStages && !warp_wait(empty(s), (u / kStages - 1) & 1, abort_flag, W.status, kWhereEmpty)) break;
+      if (u >= kStages && !warp_wait(empty(s), (u / kStages - 1) & 1, abort_flag, W.status, kWhereEmpty)) {
+        ok = false;
+        break;
+      }
       const uint32_t st = base + s * kStage, bar = full(s);
       const bool whole = t.t0 + kTile <= t.len;
       if (p == 0) {
@@ -224,6 +260,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_arrive(bar);
       ++u;
     }
+    if (!ok)  // the copies in flight land before the block ends
+      for (int x = max(0, u - kStages); x < u; ++x)
+        mbar_wait_timed(full(x % kStages), (x / kStages) & 1, nullptr, kWhereDrain);
   } else if (warp == kMmaWarp) {
     // ---------------- products ----------------
     constexpr uint32_t kIdQK = idesc_bf16_f32(128, kTile, false, false), kIdS = idesc_bf16_f32(128, kTcV, false, false),
@@ -231,22 +270,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Live tiles in order: `s` is the next whose scores are issued (its segment's place known), `o` the next
     // for P V.  Whichever has its operands is issued; neither waits behind the other.
     int s = 0, o = 0;
-    unsigned id = blockIdx.x;
-    bool more = false, left;
-    auto advance = [&] {  // the next live tile
-      for (left = false; id < tiles; id += gridDim.x) {
-        const TilePlace t = tile_place(W, id, heads);
-        if (t.live) {
-          more = t.seg > 0;
-          left = true;
-          id += gridDim.x;
-          break;
-        }
-      }
+    TileWalk at(W, heads, tiles);
+    auto find = [&] {  // the next live tile
+      while (at.there() && !at.live()) at.next();
     };
-    advance();
+    find();
     uint64_t since = global_timer_ns();
-    for (uint32_t spins = 0; left || o < s;) {
+    for (uint32_t spins = 0; at.there() || o < s;) {
       bool moved = false;
       if (o < s && __all_sync(0xffffffffu, mbar_test_wait(pready(o & 1), (o >> 1) & 1))) {
         if (elect_one()) {
@@ -261,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++o;
         moved = true;
       }
-      if (left && s - o < 2 && __all_sync(0xffffffffu, mbar_test_wait(full(s % kStages), (s / kStages) & 1)) &&
+      if (at.there() && s - o < 2 && __all_sync(0xffffffffu, mbar_test_wait(full(s % kStages), (s / kStages) & 1)) &&
           (s < 2 || __all_sync(0xffffffffu, mbar_test_wait(tfree(s & 1), ((s >> 1) - 1) & 1)))) {
         if (elect_one()) {
           tc_fence_after_sync();
@@ -273,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < kTcK / 16; ++kk)
             tc_mma_f16_ss(tm + kColS, desc_sw128(sq + kk * 32), desc_state(sq + kOffS + kk * 2 * kTcV * 16), kIdS,
                           kk > 0);
-          if (more) {
+          if (at.handed()) {
 #pragma unroll
             for (int kk = 0; kk < kTcK / 16; ++kk)
               tc_mma_f16_ss(tm + kColS0, desc_sw128(sq + kk * 32), desc_state(sq + kOffS0 + kk * 2 * kTcV * 16), kIdS,
@@ -283,7 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         ++s;
-        advance();
+        at.next();
+        find();
         moved = true;
       }
       if (moved) {
@@ -299,26 +330,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (__any_sync(0xffffffffu, stop)) break;
       }
     }
+    if (at.there() || o < s) {  // given up: the products in flight end before their memory is freed
+      for (int x = max(0, s - 2); x < s; ++x) mbar_wait_timed(scores(x & 1), (x >> 1) & 1, nullptr, kWhereDrain);
+      for (int x = max(0, o - 2); x < o; ++x) mbar_wait_timed(ofull(x & 1), (x >> 1) & 1, nullptr, kWhereDrain);
+    }
   } else {
     // ---------------- outputs: thread = row of the tile ----------------
     const int group = warp >> 2, w = warp & 3, i = 32 * w + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * w) << 16;
     int u = 0;
-    for (unsigned id = blockIdx.x; id < tiles; id += gridDim.x) {
-      const TilePlace t = tile_place(W, id, heads);
+    for (TileWalk at(W, heads, tiles); at.there(); at.next()) {
+      const bool live = at.live();
+      const int v = u;
+      u += live;
+      if (live ? (v & 1) != group : group != 0) continue;
+      const TilePlace t = tile_place(at);
       uint16_t* y = static_cast<uint16_t*>(A.y) + ((static_cast<int64_t>(t.b) * A.T + t.t0) * A.N + t.n) * A.V + t.v0;
       const int64_t stride = static_cast<int64_t>(A.N) * A.V;
       const int rows = min(kTile, A.T - t.t0);
-      if (!t.live) {  // behind the sequence's end
-        if (group == 0)
-          for (int e = tid; e < rows * (t.width / 8); e += kEpi / 2) {
-            const int per = t.width / 8;
-            *reinterpret_cast<uint4*>(y + (e / per) * stride + (e % per) * 8) = make_uint4(0u, 0u, 0u, 0u);
-          }
+      if (!live) {  // behind the sequence's end
+        for (int e = tid; e < rows * (t.width / 8); e += kEpi / 2) {
+          const int per = t.width / 8;
+          *reinterpret_cast<uint4*>(y + (e / per) * stride + (e % per) * 8) = make_uint4(0u, 0u, 0u, 0u);
+        }
         continue;
       }
-      const int v = u++;
-      if ((v & 1) != group) continue;
       const int s = v % kStages, slot = v & 1;
       const uint32_t tm = tmem + slot * kSlot + lanes, st = base + s * kStage;
       const uint8_t* stp = smem + s * kStage;
@@ -456,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (r < rows && c < t.width)
           *reinterpret_cast<uint4*>(y + r * stride + c) = ld_shared_v4(st + r * kYPitch + c * 2);
       }
+      fence_proxy_async_smem();  // TMA writes there next
       mbar_arrive(empty(s));
     }
   }
