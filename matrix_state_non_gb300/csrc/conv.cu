@@ -323,6 +323,7 @@ template <typename T, int kVec, int kW>
 __global__ void __launch_bounds__(32 * kBwdWarps, kW == 4 ? kBwdBlocks : 2)
     conv_backward_kernel(ConvArgs A, int blocks_c, int blocks_t) {
   __shared__ float red[kBwdWarps][kW + 1][32 * kVec];
+  let_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int bc = blockIdx.x % blocks_c, bt = blockIdx.x / blocks_c;
   const int b = bt / blocks_t, c = (bc * 32 + lane) * kVec;
@@ -365,6 +366,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, kW == 4 ? kBwdBlocks : 2)
 __global__ void __launch_bounds__(256) conv_sum_parts_kernel(const float* part, float* dw, float* db, int parts, int C,
                                                              int W) {
   __shared__ float red[8][32];
+  wait_previous();
   const int lane = threadIdx.x & 31, v = threadIdx.x >> 5, c = blockIdx.x * 32 + lane, j = blockIdx.y;
   float t = 0.f;
   if (c < C) {
@@ -493,9 +495,8 @@ cudaError_t launch_conv_backward(const ConvArgs& a, cudaStream_t s) {
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  conv_sum_parts_kernel<<<dim3((a.C + 31) / 32, a.W + 1), 256, 0, s>>>(a.part, a.dw, a.db,
-                                                                      conv_backward_parts(a.B, a.T), a.C, a.W);
-  return cudaGetLastError();
+  return launch_next(conv_sum_parts_kernel, dim3((a.C + 31) / 32, a.W + 1), 256, 0, s, a.part, a.dw, a.db,
+                     conv_backward_parts(a.B, a.T), a.C, a.W);
 }
 
 cudaError_t launch_conv_step(void* state, const ConvArgs& a, cudaStream_t s) {

@@ -96,6 +96,7 @@ __device__ __forceinline__ double warp_sum(double v) {
 
 __global__ void __launch_bounds__(kThreads, kPerSm) grad_sum_kernel(const GradChunk* plan, int64_t pieces, ClipScratch* sc) {
   __shared__ double red[kWarps];
+  let_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   double acc = 0.;
   for (int64_t i = blockIdx.x; i < pieces; i += gridDim.x) {
@@ -121,6 +122,7 @@ __device__ __forceinline__ float total_norm(const ClipScratch* sc, int parts, in
 }
 
 __global__ void __launch_bounds__(32) grad_norm_kernel(const ClipScratch* sc, int parts, float* norm) {
+  wait_previous();
   const float t = total_norm(sc, parts, threadIdx.x);
   if (threadIdx.x == 0) *norm = t;
 }
@@ -160,6 +162,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_scale_kernel(const Grad
                                                                  const ClipScratch* sc, int parts, float max_norm,
                                                                  float* norm) {
   __shared__ float coef;
+  wait_previous();
   const int lane = threadIdx.x & 31;
   if (threadIdx.x < 32) {
     const float t = total_norm(sc, parts, lane);
@@ -190,11 +193,13 @@ cudaError_t launch_grad_clip(const GradChunk* plan, int64_t chunks, float max_no
   ClipScratch* sc = static_cast<ClipScratch*>(ws);
   const int grid = chunks < 1 ? 1 : static_cast<int>(chunks < kBlocks ? chunks : kBlocks);
   grad_sum_kernel<<<grid, kThreads, 0, s>>>(plan, chunks, sc);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   if (!clip || chunks < 1)
-    grad_norm_kernel<<<1, 32, 0, s>>>(sc, grid, norm);
+    e = launch_next(grad_norm_kernel, 1, 32, 0, s, sc, grid, norm);
   else
-    grad_scale_kernel<<<grid, kThreads, 0, s>>>(plan, chunks, sc, grid, max_norm, norm);
-  return cudaGetLastError();
+    e = launch_next(grad_scale_kernel, grid, kThreads, 0, s, plan, chunks, sc, grid, max_norm, norm);
+  return e;
 }
 
 }  // namespace m2rnn

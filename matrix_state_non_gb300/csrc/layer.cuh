@@ -41,6 +41,30 @@ inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_
   return e;
 }
 
+// Launches of one call that follow one another: a kernel that has begun lets
+// the next one's blocks come to the SMs (let_next, by every block, first
+// thing), where they wait for its end and its writes (wait_previous, before
+// they touch anything that an earlier launch of the call writes).  The first
+// launch of a call is an ordinary one, so that inputs are there before any of
+// them starts.
+__device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P, typename... V>
+cudaError_t launch_next(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, V... args) {
+  cudaLaunchAttribute behind{};
+  behind.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  behind.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t at{};
+  at.gridDim = grid;
+  at.blockDim = dim3(threads);
+  at.dynamicSmemBytes = smem;
+  at.stream = s;
+  at.attrs = &behind;
+  at.numAttrs = 1;
+  return cudaLaunchKernelEx(&at, kernel, static_cast<P>(args)...);
+}
+
 // 2^x and 1 / x by the hardware's approximations (a few units of fp32).
 __device__ __forceinline__ float ex2_fast(float x) {
   float y;

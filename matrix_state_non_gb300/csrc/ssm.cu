@@ -43,6 +43,8 @@ __global__ void __launch_bounds__(kSumThreads) ssm_grad_sums_kernel(const float2
                                                                     int V) {
   __shared__ double2 red[kSumThreads / 32];
   __shared__ float col[kSumThreads / 32][32];
+  let_next();
+  wait_previous();
   const int n = blockIdx.x, lane = threadIdx.x & 31, w = threadIdx.x >> 5, chunks = B * nc;
   auto at = [&](int i) { return (static_cast<int64_t>(i / nc) * N + n) * nc + i % nc; };
   if (blockIdx.y == 0) {
@@ -85,6 +87,7 @@ __global__ void __launch_bounds__(kSumThreads) ssm_grad_sums_kernel(const float2
 __global__ void __launch_bounds__(kThreads) ssm_sum_heads_kernel(const float* dqh, const float* dkh, float* dq,
                                                                  float* dk, int64_t n, int N, int G, int K) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  wait_previous();
   if (i >= n) return;
   const int kk = static_cast<int>(i % K), g = static_cast<int>((i / K) % G), r = N / G;
   const int64_t bt = i / (static_cast<int64_t>(K) * G), at = (bt * N + static_cast<int64_t>(g) * r) * K + kk;
@@ -177,14 +180,12 @@ inline size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 }  // namespace
 
 cudaError_t launch_ssm_grad_sums(const SsmArgs& a, const SsmGradOut& o, int nc, cudaStream_t s) {
-  ssm_grad_sums_kernel<<<dim3(a.N, a.dw_r != nullptr ? 1 + (a.V + 31) / 32 : 1), kSumThreads, 0, s>>>(
-      o.ab_part, o.wr_part, a.dA, a.ddt_bias, a.dw_r, a.B, a.N, nc, a.V);
-  if (a.G != a.N) {
-    const int64_t n = static_cast<int64_t>(a.B) * a.T * a.G * a.K;
-    ssm_sum_heads_kernel<<<static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(
-        o.dq, o.dk, a.dq, a.dk, n, a.N, a.G, a.K);
-  }
-  return cudaGetLastError();
+  const cudaError_t e = launch_next(ssm_grad_sums_kernel, dim3(a.N, a.dw_r != nullptr ? 1 + (a.V + 31) / 32 : 1),
+                                    kSumThreads, 0, s, o.ab_part, o.wr_part, a.dA, a.ddt_bias, a.dw_r, a.B, a.N, nc, a.V);
+  if (e != cudaSuccess || a.G == a.N) return e;
+  const int64_t n = static_cast<int64_t>(a.B) * a.T * a.G * a.K;
+  return launch_next(ssm_sum_heads_kernel, static_cast<unsigned>((n + kThreads - 1) / kThreads), kThreads, 0, s, o.dq,
+                     o.dk, a.dq, a.dk, n, a.N, a.G, a.K);
 }
 
 size_t ssm_forward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V, bool bf16) {

@@ -55,6 +55,8 @@ template <int KP, int VS>
 __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_grad_walk_kernel(GradArgs W, int slices) {
   using Sh = WalkShape<KP, VS>;
   extern __shared__ __align__(16) uint8_t smem[];
+  let_next();
+  wait_previous();
   const SsmArgs& A = W.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
   const int mw = warp % Sh::kMw, nw = warp / Sh::kMw;
@@ -185,6 +187,8 @@ __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_grad
 // Phase 3: block (chain, 256 elements of a state, S or R).
 __global__ void __launch_bounds__(256) ssm_grad_segments_kernel(GradArgs W) {
   constexpr int kAhead = 8;
+  let_next();
+  wait_previous();
   const SsmArgs& A = W.a;
   const int64_t KV = static_cast<int64_t>(A.K) * A.V, bn = blockIdx.x;
   const int e = blockIdx.y * 256 + threadIdx.x;
@@ -250,6 +254,8 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
   constexpr int kKt = KP / 16, kVt = VP / 16;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float qd[kChunk], ck[kChunk], ci[kChunk], red[4];
+  let_next();
+  wait_previous();
   const SsmArgs& A = W.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
   const int bn = blockIdx.x / W.nc, c = blockIdx.x - bn * W.nc, b = bn / A.N, n = bn - b * A.N, gq = n / (A.N / A.G);
@@ -732,10 +738,11 @@ cudaError_t run(const GradArgs& w, int slices, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const SsmArgs& a = w.a;
   const unsigned chains = static_cast<unsigned>(a.B) * a.N, blocks = chains * w.nc;
-  ssm_grad_walk_kernel<KP, VS><<<dim3(chains * w.segs, 2 * slices), kThreads, Walk::kBytes, s>>>(w, slices);
-  if (w.segs > 1) ssm_grad_segments_kernel<<<dim3(chains, (a.K * a.V + 255) / 256, 2), 256, 0, s>>>(w);
-  ssm_grad_kernel<KP, VP><<<blocks, kThreads, Gr::kBytes, s>>>(w);
-  return cudaGetLastError();
+  e = launch_next(ssm_grad_walk_kernel<KP, VS>, dim3(chains * w.segs, 2 * slices), kThreads, Walk::kBytes, s, w, slices);
+  if (e == cudaSuccess && w.segs > 1)
+    e = launch_next(ssm_grad_segments_kernel, dim3(chains, (a.K * a.V + 255) / 256, 2), 256, 0, s, w);
+  if (e != cudaSuccess) return e;
+  return launch_next(ssm_grad_kernel<KP, VP>, blocks, kThreads, Gr::kBytes, s, w);
 }
 
 }  // namespace

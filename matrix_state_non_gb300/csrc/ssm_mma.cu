@@ -39,6 +39,7 @@ constexpr int kThreads = 128;  // four warps
 template <bool kGrad>
 __global__ void __launch_bounds__(256) ssm_decay_kernel(SsmArgs A, void* out, float* tot, int nc,
                                                         StatusBlock* status) {
+  let_next();
   if (blockIdx.x == 0 && threadIdx.x < sizeof(StatusBlock) / 4) reinterpret_cast<unsigned*>(status)[threadIdx.x] = 0u;
   const int lane = threadIdx.x & 31, heads = (A.N + 7) / 8, own = lane >> 3;
   const unsigned bc = blockIdx.x / heads;
@@ -147,6 +148,8 @@ __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk
   using Sh = WalkShape<KP, VS>;
   using Fr = Frag<KP, VS>;
   extern __shared__ __align__(16) uint8_t smem[];
+  let_next();
+  wait_previous();
   const SsmArgs& A = W.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
   const int nw = warp % Sh::kNw, mw = warp / Sh::kNw;
@@ -311,6 +314,8 @@ template <int KP, int VS, bool kTile>
 __global__ void __launch_bounds__(256) ssm_segment_scan_kernel(ScanArgs W) {
   using Fr = Frag<KP, VS>;
   constexpr int kAhead = 8, kN = 2 * Fr::kCount;
+  let_next();
+  wait_previous();
   const SsmArgs& A = W.a;
   const int e = blockIdx.y * 256 + threadIdx.x;
   if (e >= kN) return;
@@ -371,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, OutShape<KP, VS>::kBlocks) ssm_out_k
   static_assert(VS <= KP, "outputs pass through the q tile");
   constexpr int kKt = KP / 16;
   extern __shared__ __align__(16) uint8_t smem[];
+  wait_previous();
   const SsmArgs& A = W.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
   const unsigned head = blockIdx.x / W.nc;  // (chain, slice)
@@ -591,13 +597,12 @@ template <int KP, int VS, bool kTile>
 cudaError_t walk(const ScanArgs& w, int64_t heads, cudaStream_t s) {
   using Walk = WalkShape<KP, VS>;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_walk_kernel<KP, VS, kTile>), Walk::kBytes, done);
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_walk_kernel<KP, VS, kTile>), Walk::kBytes, done);
   if (e != cudaSuccess) return e;
-  ssm_walk_kernel<KP, VS, kTile><<<static_cast<unsigned>(heads * w.segs), kThreads, Walk::kBytes, s>>>(w);
-  if (w.segs > 1)
-    ssm_segment_scan_kernel<KP, VS, kTile>
-        <<<dim3(static_cast<unsigned>(heads), (2 * Frag<KP, VS>::kCount + 255) / 256), 256, 0, s>>>(w);
-  return cudaGetLastError();
+  e = launch_next(ssm_walk_kernel<KP, VS, kTile>, static_cast<unsigned>(heads * w.segs), kThreads, Walk::kBytes, s, w);
+  if (e != cudaSuccess || w.segs == 1) return e;
+  return launch_next(ssm_segment_scan_kernel<KP, VS, kTile>,
+                     dim3(static_cast<unsigned>(heads), (2 * Frag<KP, VS>::kCount + 255) / 256), 256, 0, s, w);
 }
 
 template <int KP, int VS>
@@ -609,8 +614,7 @@ cudaError_t run(const ScanArgs& w, int64_t chains, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   e = allow_smem(reinterpret_cast<const void*>(ssm_out_kernel<KP, VS>), Out::kBytes, done);
   if (e != cudaSuccess) return e;
-  ssm_out_kernel<KP, VS><<<static_cast<unsigned>(heads * w.nc), kThreads, Out::kBytes, s>>>(w);
-  return cudaGetLastError();
+  return launch_next(ssm_out_kernel<KP, VS>, static_cast<unsigned>(heads * w.nc), kThreads, Out::kBytes, s, w);
 }
 
 }  // namespace

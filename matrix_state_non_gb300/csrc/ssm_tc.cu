@@ -29,6 +29,7 @@ namespace {
 // One warp per (chain, chunk), two steps a lane, eight heads a block.
 __global__ void __launch_bounds__(256) ssm_tile_decay_kernel(SsmArgs A, TileDecay* out, float* tot, int nc,
                                                              StatusBlock* status) {
+  let_next();
   if (blockIdx.x == 0 && threadIdx.x < sizeof(StatusBlock) / 4) reinterpret_cast<unsigned*>(status)[threadIdx.x] = 0u;
   const int lane = threadIdx.x & 31, heads = (A.N + 7) / 8, own = lane >> 4, in = lane & 15;
   const unsigned bc = blockIdx.x / heads;
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  wait_previous();
 
   if (warp > kMmaWarp) {
     // ---------------- producers ----------------
@@ -523,8 +525,7 @@ cudaError_t launch_ssm_tc_out(const TcOutArgs& w, cudaStream_t s) {
     return cudaErrorInvalidValue;
   const unsigned heads = static_cast<unsigned>(static_cast<int64_t>(a.B) * a.N * w.slices);
   const unsigned tiles = heads * static_cast<unsigned>(w.nt);
-  ssm_tc_out_kernel<<<tiles < 152 ? tiles : 152, kThreads, kSmem, s>>>(q, k, v, w, heads, tiles);
-  return cudaGetLastError();
+  return launch_next(ssm_tc_out_kernel, tiles < 152 ? tiles : 152, kThreads, kSmem, s, q, k, v, w, heads, tiles);
 }
 
 }  // namespace m2rnn
