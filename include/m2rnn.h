@@ -320,8 +320,10 @@ int m2rnn_decode_step(float* H, const void* q, const void* k, const void* v,
  * (rows on 16-byte boundaries take the vector path).  `lengths` [B] int32
  * (NULL = all T) cuts each sequence to its first lengths[b] steps, clamped to
  * [0, T]: steps behind it are not read, their outputs and gradients are 0, and
- * the final state is the one at lengths[b].  None of these calls uses a
- * status block.
+ * the final state is the one at lengths[b].
+ *
+ * The scan's workspaces begin with a status block (see m2rnn_sync_status)
+ * that each call clears; the other calls here have none.
  * ------------------------------------------------------------------------- */
 
 /*
@@ -372,7 +374,8 @@ int m2rnn_causal_conv_step(void* state, const void* x, int64_t x_stride, const v
  *   NULL); H_0 [B,N,K,V] fp32 (may be NULL = zero); K, V in [1, 128].
  *   out: y [B,T,N,V] in `dtype`; H_T [B,N,K,V] fp32 (may be NULL; may be H_0).
  * A step whose v is not finite may also leave non-finite y at earlier steps
- * of the same 64-step chunk.
+ * of the same 64 steps (128 where tiles of 128 are used: bf16, 32 < K <= 64,
+ * V > 32, long sequences), counted from the sequence's start.
  */
 size_t m2rnn_ssm_workspace_size(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V,
                                 m2rnn_dtype dtype);

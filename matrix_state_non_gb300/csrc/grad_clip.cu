@@ -6,7 +6,9 @@
 // side (a piece per warp instead is 13 % slower on 1.6 GB: too many fronts in
 // memory).  Two passes over the data, both bound by HBM: the sums, then the
 // scaling, which takes the pieces from the back, so that what the first pass
-// left in L2 is read from there.
+// left in L2 is read from there.  1.65 GB of fp32 gradients (of a 410M model):
+// 767 us, 6.4 TB/s over the three passes that the data makes; 32 MB of one
+// layer's: 20 us (the second pass from L2; two launches).
 //
 // A thread sums the squares of its 32 elements of a piece in fp32, then pieces,
 // threads, warps and blocks in fp64, all in a fixed order: results are bitwise

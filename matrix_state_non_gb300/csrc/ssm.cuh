@@ -20,6 +20,32 @@ __device__ __forceinline__ int ssm_len(const SsmArgs& A, int b) {
   return A.lengths ? min(max(A.lengths[b], 0), A.T) : A.T;
 }
 
+// A running sum as hi + lo, good to about twice fp32.  (Adding in fp64 would do as well; its unit is slow here.)
+struct Sum2 {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float x) {  // two-sum: the rounding of hi + x goes into lo
+    const float s = hi + x, w = s - hi;
+    lo += (hi - (s - w)) + (x - w);
+    hi = s;
+  }
+  __device__ __forceinline__ void add(const Sum2& x) {
+    add(x.hi);
+    lo += x.lo;
+  }
+  __device__ __forceinline__ void subtract(const Sum2& x) {
+    add(-x.hi);
+    lo -= x.lo;
+  }
+  __device__ __forceinline__ Sum2 across(int mask) const {
+    return Sum2{__shfl_xor_sync(0xffffffffu, hi, mask), __shfl_xor_sync(0xffffffffu, lo, mask)};
+  }
+  __device__ __forceinline__ Sum2 after(int n) const {  // of the lane n further; zero behind the last
+    const Sum2 x{__shfl_down_sync(0xffffffffu, hi, n), __shfl_down_sync(0xffffffffu, lo, n)};
+    return static_cast<int>(threadIdx.x & 31) + n < 32 ? x : Sum2{};
+  }
+  __device__ __forceinline__ float value() const { return hi + lo; }
+};
+
 // The CUDA-core kernels (fp32 inputs).
 size_t ssm_f32_forward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V);
 size_t ssm_f32_backward_scratch_bytes(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V);

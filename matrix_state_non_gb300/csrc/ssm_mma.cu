@@ -10,12 +10,20 @@
 //        y_i = first_i (S^T q_i + (decay since the segment's start) S0^T q_i)
 //              + sum_j P_ij v_j + w_r (*) v_i,
 //      S the segment's own state before the chunk, S0 the state before the
-//      segment, P the decayed scores.
+//      segment, P the decayed scores.  (64 x 64 states with tiles enough:
+//      128 steps at a time on tcgen05, ssm_tc.cu.)
 // S, S0 and P take one rounding to bf16 each, as y does.  The states
 // themselves stay good to fp32: k_j exp(l_63 - l_j) D_j is split into three
 // bf16 parts (v is exact), their products are summed from the smallest part
 // up, and the chunk's sum is added to the state by an fp32 FMA, so that the
 // tensor core's truncating adds never see the running state.
+//
+// B=2 heads=16 T=16384 64x64, shared q and k: 106 us, of which decays 5, walk
+// 46, segments 5, outputs 52 (on tcgen05; 128 in all with ssm_out_kernel).
+// The walk is bound by the latency of its MMAs and of the operand split, 12
+// warps to an SM, the tensor pipe 46 % busy; a walk with the outputs in the
+// same kernel (no states through memory) took 136 us, a block per chain and
+// chunk with a scan over the chunks' sums 52 us for this phase alone.
 //
 // The state is held transposed, V rows by K columns: an accumulator fragment
 // of it, packed to bf16, is as it stands the B operand of Q S, so states go
@@ -535,7 +543,10 @@ __global__ void __launch_bounds__(kThreads, OutShape<KP, VS>::kBlocks) ssm_out_k
   }
 }
 
-constexpr int64_t kMinTiles = 2 * 152;
+// The tcgen05 outputs are built for 64 x 64 states.  They have one block per SM and want a tile for nearly each of
+// them.  Measured, a whole call with them / with ssm_out_kernel (four small blocks to an SM), us: 64 tiles 14.4 / 13.7,
+// 128 tiles 16.0 / 16.7, 256 20.0 / 20.2, 512 27.7 / 31.5, 1024 40 / 45, 2048 61 / 71, 4096 106 / 128.
+constexpr int64_t kMinTiles = 128;
 
 int padded_rows(int64_t K) { return K <= 32 ? 32 : K <= 64 ? 64 : 128; }
 int slice_cols(int64_t K, int64_t V) { return V <= 16 ? 16 : V <= 32 || K <= 32 ? 32 : 64; }
@@ -553,8 +564,6 @@ Plan make_plan(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
   p.slices = static_cast<int>((V + p.vs - 1) / p.vs);
   p.nc = static_cast<int>((T + kChunk - 1) / kChunk);
   const int64_t chains = B * N * p.slices, room = 152 * (p.kp * p.vs > 4096 ? 2 : 3);
-  // The tcgen05 outputs are built for 64 x 64 states and want a few tiles for each SM: below that the
-  // blocks of ssm_out_kernel, four to an SM, are done sooner.
   p.tile = p.kp == kTcK && p.vs == kTcV && chains * ((p.nc + 1) / 2) >= kMinTiles;
   const int unit = p.tile ? 2 : 1;
   if (p.tile) p.nc = (p.nc + 1) / 2 * 2;

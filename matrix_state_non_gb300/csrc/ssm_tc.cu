@@ -15,6 +15,12 @@
 // 256 columns and two tiles are in work at once.  The factor of row i and an
 // earlier block of 32 steps is one exponential per row and block times a
 // tabled factor per step, so a tile takes some 40 exponentials a row, not 128.
+//
+// B=2 heads=16 T=16384 64x64, shared q and k: 52 us (whole scan 106), 345 MB
+// through L2 at 6.6 TB/s; a tile takes 3900 cycles of an SM, of which the
+// rows' work (decay, P, y) is 3100 for each of two tiles at a time.  The same
+// outputs on mma.sync, four blocks of 64 steps to an SM: 72 us.  y by a TMA
+// store and S, S0 as one operand of 128 columns: no gain, left out.
 #include <cuda_runtime.h>
 
 #include <cstdint>
