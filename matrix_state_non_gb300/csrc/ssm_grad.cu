@@ -750,7 +750,7 @@ struct Plan {
 Plan make_plan(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
   Plan p{};
   p.kp = padded(K);
-  p.vp = padded(V);
+  p.vp = p.kp > 32 && V <= 16 ? 16 : padded(V);
   const int vs = slice_cols(p.vp);
   p.slices = static_cast<int>((V + vs - 1) / vs);
   p.nc = static_cast<int>((T + kChunk - 1) / kChunk);
@@ -858,9 +858,11 @@ cudaError_t launch_ssm_mma_backward(const SsmArgs& a, cudaStream_t s) {
   M2RNN_SSM_CASE(32, 32)
   M2RNN_SSM_CASE(32, 64)
   M2RNN_SSM_CASE(32, 128)
+  M2RNN_SSM_CASE(64, 16)
   M2RNN_SSM_CASE(64, 32)
   M2RNN_SSM_CASE(64, 64)
   M2RNN_SSM_CASE(64, 128)
+  M2RNN_SSM_CASE(128, 16)
   M2RNN_SSM_CASE(128, 32)
   M2RNN_SSM_CASE(128, 64)
   M2RNN_SSM_CASE(128, 128)

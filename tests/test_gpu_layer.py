@@ -133,7 +133,9 @@ SSM = [(1, 1, 1, 1, 16, 16, "bf16", None), (2, 63, 2, 2, 64, 64, "bf16", None), 
        (2, 100, 2, 2, 80, 48, "bf16", (31, 100)), (1, 77, 2, 1, 33, 17, "bf16", None),
        (2, 70, 2, 1, 16, 16, "bf16", (2, 69)), (1, 90, 2, 2, 5, 100, "bf16", None), (1, 33, 1, 1, 1, 1, "bf16", None),
        (1, 1, 2, 1, 8, 8, "f32", None), (2, 33, 2, 1, 16, 24, "f32", (33, 5)), (1, 100, 3, 3, 33, 17, "f32", None),
-       (2, 64, 2, 2, 64, 64, "f32", (0, 64)), (1, 40, 1, 1, 128, 128, "f32", None), (1, 31, 1, 1, 1, 3, "f32", None)]
+       (2, 64, 2, 2, 64, 64, "f32", (0, 64)), (1, 40, 1, 1, 128, 128, "f32", None), (1, 31, 1, 1, 1, 3, "f32", None),
+       (2, 130, 2, 1, 64, 16, "bf16", (130, 7)), (1, 100, 4, 2, 100, 12, "bf16", None),
+       (1, 700, 2, 1, 128, 16, "bf16", None), (1, 66, 1, 1, 40, 1, "bf16", None)]
 
 
 def _scan_args(g):
@@ -344,6 +346,38 @@ def test_ssm_scan_large_and_small_steps(dtype):
     r = m.ssm_scan(*a, **kw)
     close(r["y"], y, TOL[dtype], "y")
     close(r["H_T"], H, 1e-5, "H_T")
+
+
+@pytest.mark.parametrize("decay", [0.0, -1e-3, -300.0])
+def test_ssm_scan_in_tiles_extreme_decays(decay):
+    from matrix_state_non_gb300 import binding as m
+    d = ssm_inputs(2, 1160, 8, 2, 64, 64, "bf16", seed=9, decay=decay)
+    d["dt"][:, 5::41] = 60.0
+    g = ssm_dev(d, "bf16")
+    a, kw = _scan_args(g)
+    ra, rkw = _scan_args(d)
+    r = m.ssm_scan(*a, **kw)
+    y, H = o.ssm_scan(*ra, **rkw)
+    close(r["y"], y, TOL["bf16"], "y")
+    close(r["H_T"], H, 1e-5, "H_T")
+    assert m.sync_status(r["workspace"]) == (m.M2RNN_OK, 0)
+
+
+def test_ssm_sums_over_all_steps_are_not_lost_to_cancellation():
+    """dA and ddt_bias are sums of per-step gradients of both signs.  Every
+    term's own error is a few times 2^-24 of it; errors of a sum of n of them
+    stay below 2^-21 of the terms' root sum of squares times a few, here 16."""
+    from matrix_state_non_gb300 import binding as m
+    for dtype in ("bf16", "f32"):
+        d = ssm_inputs(2, 500, 6, 2, 64, 48, dtype, seed=19)
+        g = ssm_dev(d, dtype)
+        a, kw = _scan_args(g)
+        ra, rkw = _scan_args(d)
+        r = m.ssm_scan_backward(*a, g["dy"], dH_T=g["dH_T"], want_dH0=True, **kw)
+        ref = o.ssm_scan_backward(*ra, d["dy"], dH_T=d["dH_T"], **rkw)
+        size = np.sqrt((ref["ddt"] ** 2).sum((0, 1)))
+        err = np.abs(r["ddt_bias"].double().cpu().numpy() - ref["ddt_bias"])
+        assert (err <= 16 * 2.0 ** -21 * size).all(), (dtype, err / size)
 
 
 def test_ssm_scan_on_column_slices_another_stream_and_without_options():
