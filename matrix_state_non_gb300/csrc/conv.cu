@@ -28,7 +28,7 @@ struct Row {
     if constexpr (sizeof(T) * kVec == 16) {
       *reinterpret_cast<uint4*>(e) = *reinterpret_cast<const uint4*>(p);
     } else if constexpr (sizeof(T) * kVec == 8) {
-      *reinterpret_cast<uint2*>(e) = *reinterpret_cast<const uint2*>(p);
+      *reinterpret_cast<uint2*>(e) = __ldcs(reinterpret_cast<const uint2*>(p));
     } else if constexpr (sizeof(T) * kVec == 4) {
       *reinterpret_cast<uint32_t*>(e) = *reinterpret_cast<const uint32_t*>(p);
     } else {
@@ -40,7 +40,7 @@ struct Row {
     if constexpr (sizeof(T) * kVec == 16) {
       *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(e);
     } else if constexpr (sizeof(T) * kVec == 8) {
-      *reinterpret_cast<uint2*>(p) = *reinterpret_cast<const uint2*>(e);
+      __stcs(reinterpret_cast<uint2*>(p), *reinterpret_cast<const uint2*>(e));
     } else if constexpr (sizeof(T) * kVec == 4) {
       *reinterpret_cast<uint32_t*>(p) = *reinterpret_cast<const uint32_t*>(e);
     } else {
@@ -214,21 +214,36 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocks)
     forward_strip<T, kVec, kW, true>(A, src, y, c, t0, t1, len);
 }
 
-// Backward.  A warp takes 32 kVec channels of a strip of kStrip steps: it
-// walks the steps with the last kW - 1 inputs and gradients g in registers,
-// so that dxs comes out kW - 1 steps behind; the strip's last gradients are
-// those of the kW - 1 steps behind it.  The block's warps are consecutive
-// strips; their sums of dw, db are added in warp order through shared memory
-// into one partial per block.  Bound by HBM (10 bytes per bf16 element) and
-// nearly as much by instructions: B=4 T=4096 C=1536 W=4 bf16: 64 us with the
-// partials' sum, 3.9 TB/s.  Two channels a thread: their products pair into
-// one fp32 instruction, and four blocks' registers fit an SM; four channels a
-// thread halve the warps and lose.
-constexpr int kBwdWarps = 8, kStrip = 64, kBwdAhead = 4, kBwdBlocks = 4;
+// Backward.  A warp takes 32 kVec channels of a strip of `strip` steps (a
+// multiple of kBwdAhead): it walks the steps with the last kW - 1 inputs and
+// gradients g in registers, so that dxs comes out kW - 1 steps behind; the
+// strip's last gradients are those of the kW - 1 steps behind it.  The block's
+// warps are consecutive strips; their sums of dw, db are added in warp order
+// through shared memory into one partial per block.  Bound by HBM (10 bytes per
+// bf16 element) and nearly as much by instructions: B=4 T=4096 C=1536 W=4
+// bf16 56 us with the partials' sum, 4.5 TB/s.  Two channels a thread, whose
+// products pair into one fp32 instruction (four: 69 us); strips as long as one
+// wave of blocks wants them (a fixed 64 steps, blocks of 8 warps: 61, 4 of
+// those to an SM 64; 32 steps 68); gradients pass the caches by (2 us).
+constexpr int kBwdWarps = 4, kBwdAhead = 4, kBwdBlocks = 7;
+
+// Blocks of kBwdWarps strips along a sequence, and a strip's steps.
+struct BwdCut {
+  int blocks, strip;
+};
+
+BwdCut backward_cut(int64_t B, int64_t T, int64_t C) {
+  const int64_t per_strip = B * ((C + 63) / 64), room = 152 * kBwdBlocks;
+  int64_t blocks = room / per_strip < 1 ? 1 : room / per_strip;
+  int64_t strip = (T + blocks * kBwdWarps - 1) / (blocks * kBwdWarps);
+  strip = strip < 16 ? 16 : strip > 128 ? 128 : (strip + kBwdAhead - 1) / kBwdAhead * kBwdAhead;
+  blocks = (T + strip * kBwdWarps - 1) / (strip * kBwdWarps);
+  return {static_cast<int>(blocks), static_cast<int>(strip)};
+}
 
 // kEdge: the strip is its sequence's first or reaches its end.
 template <typename T, int kVec, int kW, bool kEdge>
-__device__ __forceinline__ void backward_strip(const ConvArgs& A, int b, int c, int t0, int t1, int len,
+__device__ __forceinline__ void backward_strip(const ConvArgs& A, int b, int c, int t0, int t1, int strip, int len,
                                                float (&dw)[kW][kVec], float (&db)[kVec]) {
   const Source<T, kVec> src = source<T, kVec>(A, b, c);
   float w[kW][kVec], bias[kVec], h[kW][kVec], g[kW][kVec];
@@ -244,7 +259,7 @@ __device__ __forceinline__ void backward_strip(const ConvArgs& A, int b, int c, 
     for (int e = 0; e < kVec; ++e) g[j][e] = 0.f;  // gradients before the strip belong to the strip before
   }
   load_weights<T, kVec, kW>(A, c, w, bias);
-  const int end = t0 + kStrip + kW - 1;  // g is wanted up to the last input's kW - 1 steps later
+  const int end = t0 + strip + kW - 1;  // g is wanted up to the last input's kW - 1 steps later
   // One group of kBwdAhead steps; kMine: all of them belong to the strip.
   auto group = [&](int t, auto mine_tag) {
     constexpr bool kMine = decltype(mine_tag)::value;
@@ -322,19 +337,19 @@ __device__ __forceinline__ void backward_strip(const ConvArgs& A, int b, int c, 
   };
   int t = t0;
   if (!kEdge)
-    for (; t < t0 + kStrip; t += kBwdAhead) group(t, Yes{});
+    for (; t < t0 + strip; t += kBwdAhead) group(t, Yes{});
   for (; t < end; t += kBwdAhead) group(t, No{});
 }
 
 template <typename T, int kVec, int kW>
-__global__ void __launch_bounds__(32 * kBwdWarps, kW == 4 ? kBwdBlocks : 2)
-    conv_backward_kernel(ConvArgs A, int blocks_c, int blocks_t) {
+__global__ void __launch_bounds__(32 * kBwdWarps, kW == 4 ? kBwdBlocks : 4)
+    conv_backward_kernel(ConvArgs A, int blocks_c, int blocks_t, int strip) {
   __shared__ float red[kBwdWarps][kW + 1][32 * kVec];
   let_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int bc = blockIdx.x % blocks_c, bt = blockIdx.x / blocks_c;
   const int b = bt / blocks_t, c = (bc * 32 + lane) * kVec;
-  const int t0 = ((bt % blocks_t) * kBwdWarps + warp) * kStrip, t1 = min(A.T, t0 + kStrip);
+  const int t0 = ((bt % blocks_t) * kBwdWarps + warp) * strip, t1 = min(A.T, t0 + strip);
   const int len = seq_len(A, b);
   float dw[kW][kVec], db[kVec];
 #pragma unroll
@@ -345,10 +360,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps, kW == 4 ? kBwdBlocks : 2)
   }
   if (c < A.C && t0 < A.T) {
     // The last kW steps of a sequence may take dx_T in.
-    if (t0 > 0 && t0 + kStrip + kW - 1 <= len - kW)
-      backward_strip<T, kVec, kW, false>(A, b, c, t0, t1, len, dw, db);
+    if (t0 > 0 && t0 + strip + kW - 1 <= len - kW)
+      backward_strip<T, kVec, kW, false>(A, b, c, t0, t1, strip, len, dw, db);
     else
-      backward_strip<T, kVec, kW, true>(A, b, c, t0, t1, len, dw, db);
+      backward_strip<T, kVec, kW, true>(A, b, c, t0, t1, strip, len, dw, db);
   }
 #pragma unroll
   for (int e = 0; e < kVec; ++e) {
@@ -447,9 +462,10 @@ void forward(const ConvArgs& a, cudaStream_t s) {
 
 template <typename T, int kVec, int kW>
 void backward(const ConvArgs& a, cudaStream_t s) {
-  const int blocks_c = (a.C + 32 * kVec - 1) / (32 * kVec), blocks_t = conv_backward_parts(1, a.T);
+  const BwdCut cut = backward_cut(a.B, a.T, a.C);
+  const int blocks_c = (a.C + 32 * kVec - 1) / (32 * kVec), blocks_t = cut.blocks;
   conv_backward_kernel<T, kVec, kW><<<static_cast<unsigned>(static_cast<int64_t>(blocks_c) * blocks_t * a.B),
-                                      32 * kBwdWarps, 0, s>>>(a, blocks_c, blocks_t);
+                                      32 * kBwdWarps, 0, s>>>(a, blocks_c, blocks_t, cut.strip);
 }
 
 template <typename T, int kVec, int kW>
@@ -470,8 +486,8 @@ void step(const ConvArgs& a, void* state, cudaStream_t s) {
 
 }  // namespace
 
-int conv_backward_parts(int64_t B, int64_t T) {
-  return static_cast<int>(B * ((T + kBwdWarps * kStrip - 1) / (kBwdWarps * kStrip)));
+int conv_backward_parts(int64_t B, int64_t T, int64_t C) {
+  return static_cast<int>(B * backward_cut(B, T, C).blocks);
 }
 
 cudaError_t launch_conv_forward(const ConvArgs& a, cudaStream_t s) {
@@ -504,7 +520,7 @@ cudaError_t launch_conv_backward(const ConvArgs& a, cudaStream_t s) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_next(conv_sum_parts_kernel, dim3((a.C + 31) / 32, a.W + 1), 256, 0, s, a.part, a.dw, a.db,
-                     conv_backward_parts(a.B, a.T), a.C, a.W);
+                     conv_backward_parts(a.B, a.T, a.C), a.C, a.W);
 }
 
 cudaError_t launch_conv_step(void* state, const ConvArgs& a, cudaStream_t s) {

@@ -113,7 +113,7 @@ int m2rnn_causal_conv(const void* x, int64_t x_stride, const void* w, const void
 
 size_t m2rnn_causal_conv_backward_workspace_size(int64_t B, int64_t T, int64_t C, int64_t W) {
   if (conv_dims(B, T, C, W, M2RNN_F32) != M2RNN_OK) return 0;
-  return sizeof(float) * static_cast<size_t>(conv_backward_parts(B, T)) * (W + 1) * C;
+  return sizeof(float) * static_cast<size_t>(conv_backward_parts(B, T, C)) * (W + 1) * C;
 }
 
 int m2rnn_causal_conv_backward(const void* x, int64_t x_stride, const void* w, const void* bias, const void* x0,
