@@ -1,4 +1,6 @@
-"""GB300 (sm_103a) M2RNN forward/backward scans behind a C ABI (libm2rnn.so).
+"""GB300 (sm_103a) M2RNN forward/backward scans behind a C ABI (libm2rnn.so),
+with the operators of the layer around them: the short causal convolution, a
+selective state space scan, gradient clipping.
 
 ``binding`` holds the ctypes wrappers of the C ABI and the torch helpers;
 ``inputs`` holds the seeded synthetic input generator.  The library is loaded

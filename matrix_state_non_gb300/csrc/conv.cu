@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocks)
 // warps are consecutive strips; their sums of dw, db are added in warp order
 // through shared memory into one partial per block.  Bound by HBM (10 bytes per
 // bf16 element) and nearly as much by instructions: B=4 T=4096 C=1536 W=4
-// bf16 56 us with the partials' sum, 4.5 TB/s.  Two channels a thread, whose
+// bf16 54.5 us with the partials' sum, 4.6 TB/s.  Two channels a thread, whose
 // products pair into one fp32 instruction (four: 69 us); strips as long as one
 // wave of blocks wants them (a fixed 64 steps, blocks of 8 warps: 61, 4 of
 // those to an SM 64; 32 steps 68); gradients pass the caches by (2 us).

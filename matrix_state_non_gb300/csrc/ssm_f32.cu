@@ -6,7 +6,7 @@
 // traffic counts, and 32 backward, where shared memory holds twice as much.
 // Bound by shared-memory loads and FMAs: B=4 heads=8 T=4096 64x64 forward
 // 228 us (19 TFLOP/s of chunk products; one result to a thread took 821),
-// T=2048 backward 390 us (685).
+// T=2048 backward 403 us (685; the sums of W, see ssm.cu, are 8 of them).
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -15,11 +15,13 @@
 // weighted rows) is split into three bf16 parts, whose products are summed
 // from the smallest part up.
 //
-// B=4 heads=8 T=4096 64x64: 163 us, of which decays 4, walk 30, segments 5,
-// gradients 115, sums 5.  The gradients' kernel is bound by latency: 12 warps
+// B=4 heads=8 T=4096 64x64: 172 us, of which decays 4, walk 32, segments 5,
+// gradients 123, sums 5.  The gradients' kernel is bound by latency: 12 warps
 // to an SM (168 registers, 67 KB a block), the tensor pipe 24 % and HBM 22 %
-// busy, one instruction in three cycles issued.  Sums of single chunks and a
-// scan over all of them, with the states' three parts in memory, took 180 us.
+// busy, one instruction in three cycles issued; larger batches of loads or
+// rolled loops change nothing.  The sums of W (ssm.cu) are 9 us of it.  Sums of
+// single chunks and a scan over all of them in the walk's place, with the
+// states' three parts in memory, cost 14 us more.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -241,9 +243,10 @@ __device__ __forceinline__ void split_scores(const float (&s)[2][4], uint32_t (&
 }
 
 // x += P f, P in three parts: the products are summed on their own, from the
-// smallest part up, and added in fp32.  The tensor core truncates its adds;
-// on the running sum itself that is a bias which dA and ddt_bias, differences
-// of sums over all steps, cannot take.
+// smallest part up, and added in fp32.  The tensor core truncates its adds,
+// which on the running sum itself is a bias (dq 1.9e-7 of the float64 value
+// instead of 1.3e-7); the eight chains of three also hide each other's
+// latency better than one of twelve, so it costs no time.
 __device__ __forceinline__ void add_split(float (&x)[4], const uint32_t (&p)[3][4], uint32_t f0, uint32_t f1) {
   float t[4];
   mma_bf16_16816_zc(t, p[0], f0, f1);
