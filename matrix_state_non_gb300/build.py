@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libm2rnn.so")
 SOURCES = ["api.cu", "simt.cu", "tc_forward.cu", "tc_backward.cu", "tc_backward128.cu", "mma_forward.cu",
            "mma_backward.cu", "host_util.cu", "noalloc.cu", "decode.cu",
            "mv_forward.cu", "mv_backward.cu", "mv_backward_pipe.cu", "mv_forward_pipe.cu", "gate_norm.cu",
-           "layer_api.cu", "conv.cu", "ssm.cu", "ssm_f32.cu", "ssm_mma.cu", "ssm_tc.cu",
+           "layer_api.cu", "conv.cu", "ssm.cu", "ssm_f32.cu", "ssm_mma.cu", "ssm_tc.cu", "ssm_tc_walk.cu",
            "ssm_grad.cu", "grad_clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

@@ -10,20 +10,21 @@
 //        y_i = first_i (S^T q_i + (decay since the segment's start) S0^T q_i)
 //              + sum_j P_ij v_j + w_r (*) v_i,
 //      S the segment's own state before the chunk, S0 the state before the
-//      segment, P the decayed scores.  (64 x 64 states with tiles enough:
-//      128 steps at a time on tcgen05, ssm_tc.cu.)
+//      segment, P the decayed scores.
+// 64 x 64 states with tiles enough take phases 2 and 4 on tcgen05, 128 steps at
+// a time (ssm_tc_walk.cu, ssm_tc.cu).
 // S, S0 and P take one rounding to bf16 each, as y does.  The states
 // themselves stay good to fp32: k_j exp(l_63 - l_j) D_j is split into three
 // bf16 parts (v is exact), their products are summed from the smallest part
 // up, and the chunk's sum is added to the state by an fp32 FMA, so that the
 // tensor core's truncating adds never see the running state.
 //
-// B=2 heads=16 T=16384 64x64, shared q and k: 106 us, of which decays 5, walk
-// 46, segments 5, outputs 52 (on tcgen05; 128 in all with ssm_out_kernel).
-// The walk is bound by the latency of its MMAs and of the operand split, 12
-// warps to an SM, the tensor pipe 46 % busy; a walk with the outputs in the
-// same kernel (no states through memory) took 136 us, a block per chain and
-// chunk with a scan over the chunks' sums 52 us for this phase alone.
+// B=2 heads=16 T=16384 64x64, shared q and k: 128 us, of which decays 5, walk
+// 46, segments 5, outputs 72 (96 us with tcgen05).  The walk is bound by the
+// latency of its MMAs and of the operand split, 12 warps to an SM, the tensor
+// pipe 46 % busy; a walk with the outputs in the same kernel (no states through
+// memory) took 136 us, a block per chain and chunk with a scan over the chunks'
+// sums 52 us for this phase alone.  B=8 heads=16 T=4096 128x128: 450 us.
 //
 // The state is held transposed, V rows by K columns: an accumulator fragment
 // of it, packed to bf16, is as it stands the B operand of Q S, so states go
@@ -117,16 +118,13 @@ __global__ void __launch_bounds__(256) ssm_decay_kernel(SsmArgs A, void* out, fl
 struct ScanArgs {
   SsmArgs a;
   const ChunkDecay* decay;  // [B N][chunks]
-  const float* wD;          // of the first chunk: exp(l_63 - l_j) D_j; a chunk's wD_step floats apart
-  int64_t wD_step;
   const float* tot;         // [B N][chunks]: exp(l_63)
-  float* since;             // of the first chunk: decay from the segment's start to the chunk's; since_step apart
-  int64_t since_step;
-  uint4* local;             // [B N][slices][chunks][fragments]: a segment's own state before each chunk (kTile:
-                            // of every second chunk, in the order of tc_state_at)
+  float* since;             // [B N][chunks]: decay from the segment's start to the chunk's
+  uint4* local;             // [B N][slices][chunks][fragments]: a segment's own state before each chunk
   float4* sums;             // [B N][slices][segs][2 x fragments]: the state each segment leaves
   float* seg_tot;           // [B N][segs]
-  uint4* start;             // [B N][slices][segs][fragments]: the state before each segment (kTile: likewise)
+  uint4* start;             // [B N][slices][segs][fragments]: the state before each segment (kTile, for the tiles of
+                            // ssm_tc.cu: in the order of tc_state_at)
   int nc, segs, per_seg, slices;
   bool vq, vk, vv;          // rows that asynchronous copies can take
 };
@@ -150,8 +148,8 @@ struct WalkShape {
   static constexpr int kBlocks = KP * VS > 4096 ? 2 : 3;  // per SM (registers)
 };
 
-// Phase 2.  kTile: states for the tiles of ssm_tc.cu.
-template <int KP, int VS, bool kTile>
+// Phase 2.
+template <int KP, int VS>
 __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk_kernel(ScanArgs W) {
   using Sh = WalkShape<KP, VS>;
   using Fr = Frag<KP, VS>;
@@ -175,13 +173,13 @@ __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk
                                     A.k_stride, K, W.vk};
   const TileLoader<VS, kThreads> lv{
       static_cast<const uint16_t*>(A.v) + row * A.v_stride + static_cast<int64_t>(n) * V + v0, A.v_stride, width, W.vv};
-  const float* pw = W.wD + static_cast<int64_t>(bn) * W.nc * W.wD_step;
+  const ChunkDecay* pd = W.decay + static_cast<int64_t>(bn) * W.nc;
   const float* ptot = W.tot + static_cast<int64_t>(bn) * W.nc;
   auto load_chunk = [&](int c) {
     const uint32_t st = base + (c & 1) * Sh::kStage;
     lk.load(st, c * kChunk, len);
     lv.load(st + Sh::kK, c * kChunk, len);
-    if (tid < kChunk / 4) cp_async_16(st + Sh::kK + Sh::kV + tid * 16, pw + c * W.wD_step + tid * 4, true);
+    if (tid < kChunk / 4) cp_async_16(st + Sh::kK + Sh::kV + tid * 16, pd[c].wD + tid * 4, true);
     cp_async_commit();
   };
 
@@ -206,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk
   each([&](float& s, int k, int v, bool ok) { s = from != nullptr && ok ? from[k * V + v0 + v] : 0.f; });
 
   float tot = 0.f, decay = 1.f;  // of a chunk; since the segment's start
-  uint4* local = W.local + (static_cast<int64_t>(head) * (kTile ? W.nc / 2 : W.nc) + (kTile ? c0 / 2 : c0)) * Fr::kCount;
+  uint4* local = W.local + (static_cast<int64_t>(head) * W.nc + c0) * Fr::kCount;
   if (c0 < live) {
     load_chunk(c0);
     tot = ptot[c0];
@@ -219,40 +217,22 @@ __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk
       load_chunk(c + 1);
       tot = ptot[c + 1];
     }
-    if (slice == 0 && tid == 0) W.since[(static_cast<int64_t>(bn) * W.nc + c) * W.since_step] = decay;
+    if (slice == 0 && tid == 0) W.since[static_cast<int64_t>(bn) * W.nc + c] = decay;
     decay *= tot_c;
     const int stage = (c & 1) * Sh::kStage;
     const uint32_t sK = base + stage, sV = sK + Sh::kK;
     const float* wD = reinterpret_cast<const float*>(smem + stage + Sh::kK + Sh::kV);
     if (busy) {
-      if constexpr (kTile) {
-        if ((c & 1) == 0) {
-          uint8_t* out = reinterpret_cast<uint8_t*>(local);
 #pragma unroll
-          for (int vt = 0; vt < Sh::kVt; ++vt)
+      for (int vt = 0; vt < Sh::kVt; ++vt)
 #pragma unroll
-            for (int kt = 0; kt < Sh::kKt; ++kt)
-#pragma unroll
-              for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int e = 0; e < 2; ++e)  // a core matrix of 128 bytes to a store
-                  *reinterpret_cast<uint32_t*>(out + tc_state_at(16 * (nw * Sh::kKt + kt) + 8 * h + 2 * q4,
-                                                                 16 * (mw * Sh::kVt + vt) + 8 * e + g)) =
-                      pack_bf16x2(S[vt][kt][h][2 * e], S[vt][kt][h][2 * e + 1]);
-          local += Fr::kCount;
+        for (int kt = 0; kt < Sh::kKt; ++kt) {
+          const auto& s = S[vt][kt];
+          local[Fr::at(nw * Sh::kKt + kt, mw * Sh::kVt + vt, lane)] =
+              make_uint4(pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[0][2], s[0][3]),
+                         pack_bf16x2(s[1][2], s[1][3]));
         }
-      } else {
-#pragma unroll
-        for (int vt = 0; vt < Sh::kVt; ++vt)
-#pragma unroll
-          for (int kt = 0; kt < Sh::kKt; ++kt) {
-            const auto& s = S[vt][kt];
-            local[Fr::at(nw * Sh::kKt + kt, mw * Sh::kVt + vt, lane)] =
-                make_uint4(pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[0][2], s[0][3]),
-                           pack_bf16x2(s[1][2], s[1][3]));
-          }
-        local += Fr::kCount;
-      }
+      local += Fr::kCount;
       float U[Sh::kVt][Sh::kKt][2][4] = {};
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
@@ -543,17 +523,17 @@ __global__ void __launch_bounds__(kThreads, OutShape<KP, VS>::kBlocks) ssm_out_k
   }
 }
 
-// The tcgen05 outputs are built for 64 x 64 states.  They have one block per SM and want a tile for nearly each of
-// them.  Measured, a whole call with them / with ssm_out_kernel (four small blocks to an SM), us: 64 tiles 14.4 / 13.7,
-// 128 tiles 16.0 / 16.7, 256 20.0 / 20.2, 512 27.7 / 31.5, 1024 40 / 45, 2048 61 / 71, 4096 106 / 128.
-constexpr int64_t kMinTiles = 128;
+// The tcgen05 walk and outputs are built for 64 x 64 states, have one block per SM and want a tile or two for each
+// of them.  Measured, a whole call with them / with the walk and the outputs of this file, us: 64 tiles 15.1 / 13.7,
+// 128 tiles 17.0 / 16.7, 256 19.5 / 20.2, 512 25.6 / 31.5, 1024 31.8 / 44.8, 2048 54 / 71, 4096 96 / 128.
+constexpr int64_t kMinTiles = 256;
 
 int padded_rows(int64_t K) { return K <= 32 ? 32 : K <= 64 ? 64 : 128; }
 int slice_cols(int64_t K, int64_t V) { return V <= 16 ? 16 : V <= 32 || K <= 32 ? 32 : 64; }
 
 struct Plan {
   int kp, vs, slices, segs, per_seg, nc;
-  bool tile;  // outputs on tcgen05 (ssm_tc.cu)
+  bool tile;  // walk and outputs on tcgen05 (ssm_tc_walk.cu, ssm_tc.cu)
 };
 
 // Segments: as many as the GPU holds walking blocks at once.
@@ -563,10 +543,11 @@ Plan make_plan(int64_t B, int64_t T, int64_t N, int64_t K, int64_t V) {
   p.vs = slice_cols(K, V);
   p.slices = static_cast<int>((V + p.vs - 1) / p.vs);
   p.nc = static_cast<int>((T + kChunk - 1) / kChunk);
-  const int64_t chains = B * N * p.slices, room = 152 * (p.kp * p.vs > 4096 ? 2 : 3);
+  const int64_t chains = B * N * p.slices;
   p.tile = p.kp == kTcK && p.vs == kTcV && chains * ((p.nc + 1) / 2) >= kMinTiles;
   const int unit = p.tile ? 2 : 1;
   if (p.tile) p.nc = (p.nc + 1) / 2 * 2;
+  const int64_t room = 152 * (p.tile ? 1 : p.kp * p.vs > 4096 ? 2 : 3);
   int64_t segs = room / chains;
   segs = segs < 1 ? 1 : segs > p.nc / unit ? p.nc / unit : segs;
   p.per_seg = static_cast<int>((p.nc / unit + segs - 1) / segs) * unit;
@@ -603,25 +584,23 @@ Layout make_layout(const Plan& p, int64_t chains) {
 }
 
 template <int KP, int VS, bool kTile>
-cudaError_t walk(const ScanArgs& w, int64_t heads, cudaStream_t s) {
-  using Walk = WalkShape<KP, VS>;
-  static std::atomic<uint64_t> done{0};
-  cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_walk_kernel<KP, VS, kTile>), Walk::kBytes, done);
-  if (e != cudaSuccess) return e;
-  e = launch_next(ssm_walk_kernel<KP, VS, kTile>, static_cast<unsigned>(heads * w.segs), kThreads, Walk::kBytes, s, w);
-  if (e != cudaSuccess || w.segs == 1) return e;
+cudaError_t join_segments(const ScanArgs& w, int64_t heads, cudaStream_t s) {
+  if (w.segs == 1) return cudaSuccess;
   return launch_next(ssm_segment_scan_kernel<KP, VS, kTile>,
                      dim3(static_cast<unsigned>(heads), (2 * Frag<KP, VS>::kCount + 255) / 256), 256, 0, s, w);
 }
 
 template <int KP, int VS>
 cudaError_t run(const ScanArgs& w, int64_t chains, cudaStream_t s) {
+  using Walk = WalkShape<KP, VS>;
   using Out = OutShape<KP, VS>;
   const int64_t heads = chains * w.slices;
-  cudaError_t e = walk<KP, VS, false>(w, heads, s);
-  if (e != cudaSuccess) return e;
-  static std::atomic<uint64_t> done{0};
-  e = allow_smem(reinterpret_cast<const void*>(ssm_out_kernel<KP, VS>), Out::kBytes, done);
+  static std::atomic<uint64_t> done_walk{0}, done{0};
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_walk_kernel<KP, VS>), Walk::kBytes, done_walk);
+  if (e == cudaSuccess) e = allow_smem(reinterpret_cast<const void*>(ssm_out_kernel<KP, VS>), Out::kBytes, done);
+  if (e == cudaSuccess)
+    e = launch_next(ssm_walk_kernel<KP, VS>, static_cast<unsigned>(heads * w.segs), kThreads, Walk::kBytes, s, w);
+  if (e == cudaSuccess) e = join_segments<KP, VS, false>(w, heads, s);
   if (e != cudaSuccess) return e;
   return launch_next(ssm_out_kernel<KP, VS>, static_cast<unsigned>(heads * w.nc), kThreads, Out::kBytes, s, w);
 }
@@ -655,7 +634,6 @@ cudaError_t launch_ssm_mma_forward(const SsmArgs& a, cudaStream_t s) {
   w.a = a;
   w.tot = reinterpret_cast<float*>(ws + l.tot);
   w.since = reinterpret_cast<float*>(ws + l.since);
-  w.since_step = 1;
   w.local = reinterpret_cast<uint4*>(ws + l.local);
   w.sums = reinterpret_cast<float4*>(ws + l.sums);
   w.seg_tot = reinterpret_cast<float*>(ws + l.seg_tot);
@@ -673,20 +651,18 @@ cudaError_t launch_ssm_mma_forward(const SsmArgs& a, cudaStream_t s) {
                                                  : (a.k_stride > a.v_stride ? a.k_stride : a.v_stride);
   if (p.tile && w.vq && w.vk && w.vv && widest * a.T < (int64_t{1} << 39)) {
     TileDecay* decay = reinterpret_cast<TileDecay*>(ws + l.decay);
-    w.wD = decay->wD;
-    w.since = &decay->T[2];
-    w.wD_step = w.since_step = sizeof(TileDecay) / sizeof(float);
+    uint8_t* local = reinterpret_cast<uint8_t*>(w.local);
     cudaError_t e = launch_ssm_tile_decay(a, decay, tot, p.nc, status, s);
-    if (e == cudaSuccess) e = walk<kTcK, kTcV, true>(w, chains * w.slices, s);
+    if (e == cudaSuccess)
+      e = launch_ssm_tc_walk(TcWalkArgs{a, decay, tot, local, w.sums, w.seg_tot, status, p.nc, p.nc / 2, p.segs,
+                                        p.per_seg, p.slices}, s);
+    if (e == cudaSuccess) e = join_segments<kTcK, kTcV, true>(w, chains * w.slices, s);
     if (e != cudaSuccess) return e;
-    return launch_ssm_tc_out(TcOutArgs{a, decay, reinterpret_cast<const uint8_t*>(w.local),
-                                       reinterpret_cast<const uint8_t*>(w.start), status, p.nc, p.nc / 2, p.segs,
+    return launch_ssm_tc_out(TcOutArgs{a, decay, local, reinterpret_cast<const uint8_t*>(w.start), status, p.nc, p.nc / 2, p.segs,
                                        p.per_seg, p.slices}, s);
   }
   ChunkDecay* decay = reinterpret_cast<ChunkDecay*>(ws + l.decay);
   w.decay = decay;
-  w.wD = decay->wD;
-  w.wD_step = sizeof(ChunkDecay) / sizeof(float);
   const cudaError_t e = launch_ssm_decay(a, decay, tot, p.nc, false, status, s);
   if (e != cudaSuccess) return e;
 #define M2RNN_SSM_CASE(KP, VS) \

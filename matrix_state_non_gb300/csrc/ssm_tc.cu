@@ -1,6 +1,6 @@
 // Outputs of the selective state space scan on the 5th-generation tensor
 // cores, for tiles of 128 steps of one head and up to 64 state rows and value
-// columns (the mathematics in ssm.cu, the phases before in ssm_mma.cu):
+// columns (the mathematics in ssm.cu, the phases in ssm_mma.cu):
 //     y_i = first_i (S^T q_i + since S0^T q_i) + sum_j P_ij v_j + w_r (*) v_i,
 //     P_ij = exp(l_i - l_j) D_j (q_i . k_j) for j <= i.
 // One persistent block per SM:
@@ -16,7 +16,7 @@
 // earlier block of 32 steps is one exponential per row and block times a
 // tabled factor per step, so a tile takes some 40 exponentials a row, not 128.
 //
-// B=2 heads=16 T=16384 64x64, shared q and k: 52 us (whole scan 106), 345 MB
+// B=2 heads=16 T=16384 64x64, shared q and k: 52 us (whole scan 96), 345 MB
 // through L2 at 6.6 TB/s; a tile takes 3900 cycles of an SM, of which the
 // rows' work (decay, P, y) is 3100 for each of two tiles at a time.  The same
 // outputs on mma.sync, four blocks of 64 steps to an SM: 72 us.  y by a TMA
@@ -26,7 +26,6 @@
 #include <cstdint>
 
 #include "gate.cuh"
-#include "mma_common.cuh"
 #include "ssm_tc.cuh"
 
 namespace m2rnn {
@@ -75,14 +74,12 @@ __global__ void __launch_bounds__(256) ssm_tile_decay_kernel(SsmArgs A, TileDeca
   }
 }
 
-constexpr int kTile = 2 * kChunk;
 constexpr int kEpi = 256, kMmaWarp = 8, kProd = 96, kThreads = kEpi + 32 + kProd;  // 12 warps: 168 registers
 constexpr int kStages = 3;
 
 // Shared memory of a stage.  Q, K, V: 128 rows of 128 bytes, 16-byte pieces
 // XOR-swizzled by (row mod 8), 1 KB aligned, as TMA writes and the products'
 // descriptors read them; the states as tc_state_at orders them.
-constexpr int kOp = kTile * 128;
 constexpr int kOffK = kOp, kOffV = 2 * kOp, kOffS = 3 * kOp, kOffS0 = kOffS + kTcStateBytes,
               kOffD = kOffS0 + kTcStateBytes, kOffWr = kOffD + 2 * kTileDecayCopied,
               kStage = (kOffWr + kTcV * 2 + 1023) / 1024 * 1024;
@@ -97,12 +94,6 @@ constexpr uint32_t kColP = 0, kColPV = 64, kColS = 128, kColS0 = 192, kSlot = 25
 
 constexpr uint32_t kWhereFull = 401, kWhereP = 402, kWhereScores = 403, kWhereOut = 404, kWhereEmpty = 405,
                    kWhereDrain = 406;
-
-// A bounded wait of a whole warp: all lanes go on, or all give up.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, StatusBlock* status,
-                                          uint32_t where) {
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, where));
-}
 
 // The tiles of a block in order: tile tt of (chain, slice) `head`, every gridDim.x-th of them, heads side by side.
 // Stepping and `live` go without divisions where there are no lengths: the warps ask for every tile of the block.
@@ -158,14 +149,7 @@ __device__ __forceinline__ TilePlace tile_place(const TileWalk& at) {
   return p;
 }
 
-// Descriptor of a 128-byte swizzled operand: 8-row groups 1 KB apart.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr) {
-  return smem_desc_noswizzle(addr, 16, 1024) | (static_cast<uint64_t>(2) << 61);
-}
 __device__ __forceinline__ uint64_t desc_state(uint32_t addr) { return smem_desc_noswizzle(addr, kTcV * 16, 128); }
-
-// Byte of 16-byte piece c of row r in a swizzled operand.
-__device__ __forceinline__ uint32_t piece_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 
 __global__ void __launch_bounds__(kThreads, 1) 
     ssm_tc_out_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,

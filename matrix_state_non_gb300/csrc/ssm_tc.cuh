@@ -2,6 +2,7 @@
 // tiles of 128 steps: two chunks, one state.
 #pragma once
 
+#include "mma_common.cuh"
 #include "ssm_mma.cuh"
 
 namespace m2rnn {
@@ -19,6 +20,8 @@ static_assert(sizeof(TileDecay) <= sizeof(ChunkDecay), "they share a scratch are
 constexpr int kTileDecayCopied = (3 * kChunk + 4) * 4;  // bytes of it a tile reads
 
 constexpr int kTcK = 64, kTcV = 64;            // padded widths it is built for
+constexpr int kTile = 2 * kChunk;               // steps
+constexpr int kOp = kTile * 128;                // bytes of an operand of 128 rows of 64 columns
 constexpr int kTcStateBytes = kTcK * kTcV * 2;  // a state as the B operand of Q S
 
 struct TcOutArgs {
@@ -36,6 +39,32 @@ __host__ __device__ constexpr int tc_state_at(int k, int v) {
   return (k / 8) * (kTcV * 16) + (v / 8) * 128 + (v % 8) * 16 + (k % 8) * 2;
 }
 
+// A bounded wait of a whole warp: all lanes go on, or all give up.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, StatusBlock* status,
+                                          uint32_t where) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, status, where));
+}
+
+// Descriptor of a 128-byte swizzled operand: 8-row groups 1 KB apart; an operand wider than 64 columns goes on in
+// another such tile, `next` bytes behind.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t next = 16) {
+  return smem_desc_noswizzle(addr, next, 1024) | (static_cast<uint64_t>(2) << 61);
+}
+// Byte of 16-byte piece c of row r in a swizzled operand.
+__device__ __forceinline__ uint32_t piece_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+struct TcWalkArgs {
+  SsmArgs a;
+  TileDecay* decay;    // [B N][chunks]; the walk writes T[2] of every second
+  const float* tot;    // [B N][chunks]: a chunk's whole decay
+  uint8_t* local;      // [B N][slices][tiles][kTcStateBytes]
+  float4* sums;        // [B N][slices][segs][1024]: the state each segment leaves, in the order of Frag (ssm_mma.cu)
+  float* seg_tot;      // [B N][segs]
+  StatusBlock* status;
+  int nc, nt, segs, per_seg, slices;
+};
+
+cudaError_t launch_ssm_tc_walk(const TcWalkArgs& w, cudaStream_t s);
 cudaError_t launch_ssm_tile_decay(const SsmArgs& a, TileDecay* out, float* tot, int nc, StatusBlock* status,
                                   cudaStream_t s);
 cudaError_t launch_ssm_tc_out(const TcOutArgs& w, cudaStream_t s);
