@@ -345,7 +345,6 @@ template <typename T, int kVec, int kW>
 __global__ void __launch_bounds__(32 * kBwdWarps, kW == 4 ? kBwdBlocks : 4)
     conv_backward_kernel(ConvArgs A, int blocks_c, int blocks_t, int strip) {
   __shared__ float red[kBwdWarps][kW + 1][32 * kVec];
-  let_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int bc = blockIdx.x % blocks_c, bt = blockIdx.x / blocks_c;
   const int b = bt / blocks_t, c = (bc * 32 + lane) * kVec;
@@ -372,6 +371,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps, kW == 4 ? kBwdBlocks : 4)
     red[warp][kW][lane * kVec + e] = db[e];
   }
   __syncthreads();
+  let_next();
   // Partials are [block of steps][A.W taps, then the bias][C].
   for (int i = threadIdx.x; i < (kW + 1) * 32 * kVec; i += 32 * kBwdWarps) {
     const int j = i / (32 * kVec) - (kW - A.W), x = i % (32 * kVec), cc = bc * 32 * kVec + x;

@@ -98,7 +98,6 @@ __device__ __forceinline__ double warp_sum(double v) {
 
 __global__ void __launch_bounds__(kThreads, kPerSm) grad_sum_kernel(const GradChunk* plan, int64_t pieces, ClipScratch* sc) {
   __shared__ double red[kWarps];
-  let_next();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   double acc = 0.;
   for (int64_t i = blockIdx.x; i < pieces; i += gridDim.x) {
@@ -106,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) grad_sum_kernel(const GradCh
     acc += c.bf16 ? square_sum(static_cast<const uint16_t*>(c.in), c.count)
                   : square_sum(static_cast<const float*>(c.in), c.count);
   }
+  let_next();
   acc = warp_sum(acc);
   if (lane == 0) red[warp] = acc;
   __syncthreads();

@@ -41,12 +41,13 @@ inline cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_
   return e;
 }
 
-// Launches of one call that follow one another: a kernel that has begun lets
-// the next one's blocks come to the SMs (let_next, by every block, first
-// thing), where they wait for its end and its writes (wait_previous, before
-// they touch anything that an earlier launch of the call writes).  The first
-// launch of a call is an ordinary one, so that inputs are there before any of
-// them starts.
+// Launches of one call that follow one another: when every block of a kernel
+// has called let_next (or ended), the next one's blocks come to the SMs, where
+// wait_previous holds them until its end and its writes (before they touch
+// anything that an earlier launch of the call writes).  Mostly called behind a
+// kernel's main loop: earlier, blocks that only wait cost a small call 1 to 2
+// us of the 2 to 4 that this saves.  The first launch of a call is an ordinary
+// one, so that inputs are there before any of them starts.
 __device__ __forceinline__ void let_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

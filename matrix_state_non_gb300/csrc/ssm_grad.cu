@@ -63,7 +63,6 @@ template <int KP, int VS>
 __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_grad_walk_kernel(GradArgs W, int slices) {
   using Sh = WalkShape<KP, VS>;
   extern __shared__ __align__(16) uint8_t smem[];
-  let_next();
   wait_previous();
   const SsmArgs& A = W.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
@@ -184,6 +183,7 @@ __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_grad
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[mt][nt][e] = fmaf(tot_c, S[mt][nt][e], U[mt][nt][e] + low[mt][nt][e]);
   }
+  let_next();
   if (W.segs > 1) {
     store(W.ends[rev] + (static_cast<int64_t>(bn) * W.segs + seg) * KV);
     if (!rev && slice == 0 && tid == 0) W.seg_tot[static_cast<int64_t>(bn) * W.segs + seg] = decay;

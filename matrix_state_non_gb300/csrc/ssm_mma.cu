@@ -48,7 +48,6 @@ constexpr int kThreads = 128;  // four warps
 template <bool kGrad>
 __global__ void __launch_bounds__(256) ssm_decay_kernel(SsmArgs A, void* out, float* tot, int nc,
                                                         StatusBlock* status) {
-  let_next();
   if (blockIdx.x == 0 && threadIdx.x < sizeof(StatusBlock) / 4) reinterpret_cast<unsigned*>(status)[threadIdx.x] = 0u;
   const int lane = threadIdx.x & 31, heads = (A.N + 7) / 8, own = lane >> 3;
   const unsigned bc = blockIdx.x / heads;
@@ -87,6 +86,7 @@ __global__ void __launch_bounds__(256) ssm_decay_kernel(SsmArgs A, void* out, fl
   for (int i = 0; i < 4; ++i) T[i] = __shfl_sync(0xffffffffu, up, 8 * i + 7);
   const float base = own == 0 ? 0.f : own == 1 ? T[0] : own == 2 ? T[0] + T[1] : T[0] + T[1] + T[2];
   const float rest = own == 3 ? 0.f : own == 2 ? T[3] : own == 1 ? T[3] + T[2] : T[3] + T[2] + T[1];
+  let_next();
   ChunkDecay& d = kGrad ? static_cast<ChunkDecayGrad*>(out)[id].d : static_cast<ChunkDecay*>(out)[id];
   const int i = 2 * lane;
   auto put = [&](float* at, float x, float y) { *reinterpret_cast<float2*>(at + i) = make_float2(x, y); };
@@ -154,7 +154,6 @@ __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk
   using Sh = WalkShape<KP, VS>;
   using Fr = Frag<KP, VS>;
   extern __shared__ __align__(16) uint8_t smem[];
-  let_next();
   wait_previous();
   const SsmArgs& A = W.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
@@ -275,6 +274,7 @@ __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk
             for (int e = 0; e < 4; ++e) S[vt][kt][h][e] = fmaf(tot_c, S[vt][kt][h][e], U[vt][kt][h][e]);
     }
   }
+  let_next();
   if (W.segs == 1) {
     if (A.H_T != nullptr)
       each([&](float& s, int k, int v, bool ok) {
@@ -302,7 +302,7 @@ template <int KP, int VS, bool kTile>
 __global__ void __launch_bounds__(256) ssm_segment_scan_kernel(ScanArgs W) {
   using Fr = Frag<KP, VS>;
   constexpr int kAhead = 8, kN = 2 * Fr::kCount;
-  let_next();
+  if (kTile) let_next();  // a persistent kernel, which has barriers and tensor memory to set up meanwhile
   wait_previous();
   const SsmArgs& A = W.a;
   const int e = blockIdx.y * 256 + threadIdx.x;
@@ -339,6 +339,7 @@ __global__ void __launch_bounds__(256) ssm_segment_scan_kernel(ScanArgs W) {
                       fmaf(a[j], s.w, u[j].w));
     }
   }
+  if (!kTile) let_next();
   if (A.H_T == nullptr || slice * VS + v >= A.V) return;
   float* H = A.H_T + bn * A.K * A.V + slice * VS + v;
   const float x[4] = {s.x, s.y, s.z, s.w};

@@ -70,7 +70,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     ssm_tc_walk_kernel(const __grid_constant__ CUtensorMap map_v, TcWalkArgs W, unsigned items) {
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  let_next();
   const SsmArgs& A = W.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = smem_u32(smem), bars = base + kOffBar;
@@ -317,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (tid == 0 && at.slice == 0) W.seg_tot[at.chain * W.segs + at.seg] = decay;
     }
   }
+  let_next();
   cp_async_wait<0>();
   tc_fence_before_sync();
   __syncthreads();
