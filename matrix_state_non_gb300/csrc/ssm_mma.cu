@@ -524,10 +524,10 @@ __global__ void __launch_bounds__(kThreads, OutShape<KP, VS>::kBlocks) ssm_out_k
   }
 }
 
-// The tcgen05 walk and outputs are built for 64 x 64 states, have one block per SM and want a tile or two for each
-// of them.  Measured, a whole call with them / with the walk and the outputs of this file, us: 64 tiles 15.1 / 13.7,
-// 128 tiles 17.0 / 16.7, 256 19.5 / 20.2, 512 25.6 / 31.5, 1024 31.8 / 44.8, 2048 54 / 71, 4096 96 / 128.
-constexpr int64_t kMinTiles = 256;
+// The tcgen05 walk and outputs are built for 64 x 64 states, have one block per SM and want two tiles for each of
+// them.  Measured, a whole call with them / with the walk and the outputs of this file, us: 64 tiles 13.1 / 12.6,
+// 128 tiles 17.1 / 15.7, 256 18.5 / 17.0, 512 23.7 / 27.3, 1024 31.6 / 43.1, 2048 54 / 70, 4096 96 / 127.
+constexpr int64_t kMinTiles = 2 * 152;
 
 int padded_rows(int64_t K) { return K <= 32 ? 32 : K <= 64 ? 64 : 128; }
 int slice_cols(int64_t K, int64_t V) { return V <= 16 ? 16 : V <= 32 || K <= 32 ? 32 : 64; }

@@ -351,7 +351,7 @@ def test_ssm_scan_large_and_small_steps(dtype):
 @pytest.mark.parametrize("decay", [0.0, -1e-3, -300.0])
 def test_ssm_scan_in_tiles_extreme_decays(decay):
     from matrix_state_non_gb300 import binding as m
-    d = ssm_inputs(2, 1160, 8, 2, 64, 64, "bf16", seed=9, decay=decay)
+    d = ssm_inputs(4, 1160, 8, 2, 64, 64, "bf16", seed=9, decay=decay)
     d["dt"][:, 5::41] = 60.0
     g = ssm_dev(d, "bf16")
     a, kw = _scan_args(g)
