@@ -220,23 +220,27 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocks)
 // strip's last gradients are those of the kW - 1 steps behind it.  The block's
 // warps are consecutive strips; their sums of dw, db are added in warp order
 // through shared memory into one partial per block.  Bound by HBM (10 bytes per
-// bf16 element) and nearly as much by instructions: B=4 T=4096 C=1536 W=4
-// bf16 54.5 us with the partials' sum, 4.6 TB/s.  Two channels a thread, whose
-// products pair into one fp32 instruction (four: 69 us); strips as long as one
-// wave of blocks wants them (a fixed 64 steps, blocks of 8 warps: 61, 4 of
-// those to an SM 64; 32 steps 68); gradients pass the caches by (2 us).
-constexpr int kBwdWarps = 4, kBwdAhead = 4, kBwdBlocks = 7;
+// bf16 element): B=4 T=4096 C=1536 W=4 bf16 49 us with the partials' sum,
+// 5.2 TB/s, three quarters of a plain copy's rate.  Two channels a thread,
+// whose products pair into one fp32 instruction; the next rows in flight while
+// it computes (without, and a block more per SM, 54); strips as long as one
+// wave of blocks wants them (a fixed 64 steps then took 59); gradients pass the
+// caches by (2 us).
+constexpr int kBwdWarps = 4, kBwdAhead = 4;
+
+// Blocks to an SM, by the registers they take (fp32 at 6: 67 us for 57).
+constexpr int backward_blocks(bool bf16, bool wide) { return wide ? 4 : bf16 ? 6 : 5; }
 
 // Blocks of kBwdWarps strips along a sequence, and a strip's steps.
 struct BwdCut {
   int blocks, strip;
 };
 
-BwdCut backward_cut(int64_t B, int64_t T, int64_t C) {
-  const int64_t per_strip = B * ((C + 63) / 64), room = 152 * kBwdBlocks;
+BwdCut backward_cut(int64_t B, int64_t T, int64_t C, int per_sm) {
+  const int64_t per_strip = B * ((C + 63) / 64), room = 152 * per_sm;
   int64_t blocks = room / per_strip < 1 ? 1 : room / per_strip;
   int64_t strip = (T + blocks * kBwdWarps - 1) / (blocks * kBwdWarps);
-  strip = strip < 16 ? 16 : strip > 128 ? 128 : (strip + kBwdAhead - 1) / kBwdAhead * kBwdAhead;
+  strip = strip < 16 ? 16 : strip > 256 ? 256 : (strip + kBwdAhead - 1) / kBwdAhead * kBwdAhead;
   blocks = (T + strip * kBwdWarps - 1) / (strip * kBwdWarps);
   return {static_cast<int>(blocks), static_cast<int>(strip)};
 }
@@ -260,21 +264,35 @@ __device__ __forceinline__ void backward_strip(const ConvArgs& A, int b, int c, 
   }
   load_weights<T, kVec, kW>(A, c, w, bias);
   const int end = t0 + strip + kW - 1;  // g is wanted up to the last input's kW - 1 steps later
-  // One group of kBwdAhead steps; kMine: all of them belong to the strip.
+  const int lim = kEdge ? min(len, end) : end;
+  Row<T, kVec> next_in[kBwdAhead];
+  Row<float, kVec> next_up[kBwdAhead];
+  auto load = [&](int t) {
+#pragma unroll
+    for (int u = 0; u < kBwdAhead; ++u) {
+      if (t + u < lim) {
+        next_in[u].load(px + u * src.stride);
+        next_up[u].load(pu + static_cast<int64_t>(u) * A.C);
+      } else {
+        next_in[u].zero();
+        next_up[u].zero();
+      }
+    }
+    px += kBwdAhead * src.stride;
+    pu += static_cast<int64_t>(kBwdAhead) * A.C;
+  };
+  load(t0);
+  // One group of kBwdAhead steps, the next one's rows on their way; kMine: all of them belong to the strip.
   auto group = [&](int t, auto mine_tag) {
     constexpr bool kMine = decltype(mine_tag)::value;
     Row<T, kVec> in[kBwdAhead];
     Row<float, kVec> up[kBwdAhead];
 #pragma unroll
     for (int u = 0; u < kBwdAhead; ++u) {
-      if ((!kEdge && kMine) || t + u < (kEdge ? min(len, end) : end)) {
-        in[u].load(px + u * src.stride);
-        up[u].load(pu + static_cast<int64_t>(u) * A.C);
-      } else {
-        in[u].zero();
-        up[u].zero();
-      }
+      in[u] = next_in[u];
+      up[u] = next_up[u];
     }
+    load(t + kBwdAhead);
 #pragma unroll
     for (int u = 0; u < kBwdAhead; ++u) {
       float p[kVec], x[kVec], r[kVec];
@@ -331,8 +349,6 @@ __device__ __forceinline__ void backward_strip(const ConvArgs& A, int b, int c, 
           out.store(A.dx0 + (static_cast<int64_t>(b) * (A.W - 1) + s + A.W - 1) * A.C + c);
       }
     }
-    px += kBwdAhead * src.stride;
-    pu += static_cast<int64_t>(kBwdAhead) * A.C;
     pd += static_cast<int64_t>(kBwdAhead) * A.C;
   };
   int t = t0;
@@ -342,7 +358,7 @@ __device__ __forceinline__ void backward_strip(const ConvArgs& A, int b, int c, 
 }
 
 template <typename T, int kVec, int kW>
-__global__ void __launch_bounds__(32 * kBwdWarps, kW == 4 ? kBwdBlocks : 4)
+__global__ void __launch_bounds__(32 * kBwdWarps, backward_blocks(sizeof(T) == 2, kW == 8))
     conv_backward_kernel(ConvArgs A, int blocks_c, int blocks_t, int strip) {
   __shared__ float red[kBwdWarps][kW + 1][32 * kVec];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -462,7 +478,7 @@ void forward(const ConvArgs& a, cudaStream_t s) {
 
 template <typename T, int kVec, int kW>
 void backward(const ConvArgs& a, cudaStream_t s) {
-  const BwdCut cut = backward_cut(a.B, a.T, a.C);
+  const BwdCut cut = backward_cut(a.B, a.T, a.C, backward_blocks(a.bf16, a.W > 4));
   const int blocks_c = (a.C + 32 * kVec - 1) / (32 * kVec), blocks_t = cut.blocks;
   conv_backward_kernel<T, kVec, kW><<<static_cast<unsigned>(static_cast<int64_t>(blocks_c) * blocks_t * a.B),
                                       32 * kBwdWarps, 0, s>>>(a, blocks_c, blocks_t, cut.strip);
@@ -487,7 +503,12 @@ void step(const ConvArgs& a, void* state, cudaStream_t s) {
 }  // namespace
 
 int conv_backward_parts(int64_t B, int64_t T, int64_t C) {
-  return static_cast<int>(B * backward_cut(B, T, C).blocks);
+  int most = 0;
+  for (int per_sm = 4; per_sm <= 6; ++per_sm) {
+    const int blocks = backward_cut(B, T, C, per_sm).blocks;
+    most = blocks > most ? blocks : most;
+  }
+  return static_cast<int>(B * most);
 }
 
 cudaError_t launch_conv_forward(const ConvArgs& a, cudaStream_t s) {
@@ -520,7 +541,7 @@ cudaError_t launch_conv_backward(const ConvArgs& a, cudaStream_t s) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_next(conv_sum_parts_kernel, dim3((a.C + 31) / 32, a.W + 1), 256, 0, s, a.part, a.dw, a.db,
-                     conv_backward_parts(a.B, a.T, a.C), a.C, a.W);
+                     a.B * backward_cut(a.B, a.T, a.C, backward_blocks(a.bf16, a.W > 4)).blocks, a.C, a.W);
 }
 
 cudaError_t launch_conv_step(void* state, const ConvArgs& a, cudaStream_t s) {

@@ -138,7 +138,7 @@ struct ConvArgs {
   bool silu, bf16;
 };
 
-int conv_backward_parts(int64_t B, int64_t T, int64_t C);
+int conv_backward_parts(int64_t B, int64_t T, int64_t C);  // the most that any type and width takes
 cudaError_t launch_conv_forward(const ConvArgs& a, cudaStream_t s);
 cudaError_t launch_conv_backward(const ConvArgs& a, cudaStream_t s);
 // One token: state [B,W-1,C] in place; a.x, a.y [B,C].
