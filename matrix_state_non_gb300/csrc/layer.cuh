@@ -105,6 +105,11 @@ __device__ __forceinline__ void sub2(float& d0, float& d1, float b0, float b1) {
       : "+f"(d0), "+f"(d1)
       : "f"(b0), "f"(b1));
 }
+// What the rounding of s = a + b left out, exactly (two-sum).
+__device__ __forceinline__ float two_sum_low(float a, float b, float s) {
+  const float w = s - a;
+  return (a - (s - w)) + (b - w);
+}
 // d += a * b over kN elements, in pairs.
 template <int kN>
 __device__ __forceinline__ void fma_row(float (&d)[kN], const float (&a)[kN], const float (&b)[kN]) {

@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, GradShape<KP, VP>::kBlocks) ssm_grad
   const int m0 = 16 * warp + g, m1 = m0 + 8;  // the warp's rows of every product
   // exp(l_i - l_j) for rows i of block bi > bj and columns j, or within a block (i >= j, else 0).
   auto diag = [&](int i, int j) {
-    return i >= j ? exp_fast((d.rel[i] - d.rel[j]) + (dg.rel_lo[i] - dg.rel_lo[j])) : 0.f;
+    return i >= j ? exp_fast((d.rel[i] - d.rel[j]) + (d.rel_lo[i] - d.rel_lo[j])) : 0.f;
   };
   // Dot product of the warp's rows of a bf16 tile with accumulators, over the quad's lanes.
   auto row_dots = [&](uint32_t tile, const float (&x)[KP / 8][4], float* out) {

@@ -4,27 +4,30 @@
 //   1. decays of every chunk;
 //   2. a block per (head, value slice, segment) walks the segment's chunks
 //      with the state in its warps' accumulators, from zero (the first segment
-//      from H_0), and leaves the state before each chunk as bf16 operands;
+//      from H_0), and leaves the state before each chunk, in fp32;
 //   3. a scan over the segments: the state before each, and H_T;
 //   4. a block per (head, value slice, chunk), all independent: the outputs
-//        y_i = first_i (S^T q_i + (decay since the segment's start) S0^T q_i)
+//        y_i = first_i (S + (decay since the segment's start) S0)^T q_i
 //              + sum_j P_ij v_j + w_r (*) v_i,
 //      S the segment's own state before the chunk, S0 the state before the
 //      segment, P the decayed scores.
 // 64 x 64 states with tiles enough take phases 2 and 4 on tcgen05, 128 steps at
 // a time (ssm_tc_walk.cu, ssm_tc.cu).
-// S, S0 and P take one rounding to bf16 each, as y does.  The states
-// themselves stay good to fp32: k_j exp(l_63 - l_j) D_j is split into three
-// bf16 parts (v is exact), their products are summed from the smallest part
-// up, and the chunk's sum is added to the state by an fp32 FMA, so that the
-// tensor core's truncating adds never see the running state.
+// y is the fp32 result rounded once: the joined state and P enter their
+// products as two bf16 parts each, good to 2^-16, 1/256 of y's own rounding
+// (one part each made y's error a fifth larger than its rounding, for 24 us less
+// at B=2 heads=16 T=16384 64x64 on tcgen05, 97 and 121), and differences of
+// sums of log decays keep their low parts.  The states themselves stay good to
+// fp32: k_j exp(l_63 - l_j) D_j is split into three bf16 parts (v is exact),
+// their products are summed from the smallest part up, and the chunk's sum is
+// added to the state by an fp32 FMA, so that the tensor core's truncating adds
+// never see the running state.
 //
-// B=2 heads=16 T=16384 64x64, shared q and k: 128 us, of which decays 5, walk
-// 46, segments 5, outputs 72 (96 us with tcgen05).  The walk is bound by the
-// latency of its MMAs and of the operand split, 12 warps to an SM, the tensor
-// pipe 46 % busy; a walk with the outputs in the same kernel (no states through
-// memory) took 136 us, a block per chain and chunk with a scan over the chunks'
-// sums 52 us for this phase alone.  B=8 heads=16 T=4096 128x128: 450 us.
+// B=4 heads=16 T=4096 64x64, shared q and k: 88 us (65 with tcgen05).  B=8
+// heads=16 T=4096 128x128: 597 us, of which decays 7, walk 234, outputs 358:
+// the walk is bound by the latency of its MMAs and of the operand split (8
+// warps to an SM, by registers), the outputs by the states that they read (537
+// MB in all) with as few warps, by shared memory.
 //
 // The state is held transposed, V rows by K columns: an accumulator fragment
 // of it, packed to bf16, is as it stands the B operand of Q S, so states go
@@ -59,25 +62,22 @@ __global__ void __launch_bounds__(256) ssm_decay_kernel(SsmArgs A, void* out, fl
   const float bias = A.dt_bias ? A.dt_bias[n] : 0.f, An = A.A[n];
   const float x0 = t < len ? to_f32(p[0]) + bias : 0.f, x1 = t + 1 < len ? to_f32(p[A.dt_stride]) + bias : 0.f;
   const float D0 = t < len ? softplus_f(x0) : 0.f, D1 = t + 1 < len ? softplus_f(x1) : 0.f;
-  const float a0 = D0 * An, a1 = D1 * An;
+  const float a0 = log_decay(D0, An), a1 = log_decay(D1, An);
   // Within the block of 16 steps: the sum up to a step, and the sum behind it.
-  float up = a0 + a1, down = up, low = kGrad ? (a0 - up) + a1 : 0.f;
+  float up = a0 + a1, down = up, low = two_sum_low(a0, a1, up);
 #pragma unroll
   for (int o = 1; o < 8; o <<= 1) {
     const float x = __shfl_up_sync(0xffffffffu, up, o, 8), y = __shfl_down_sync(0xffffffffu, down, o, 8);
-    const float z = kGrad ? __shfl_up_sync(0xffffffffu, low, o, 8) : 0.f;
+    const float z = __shfl_up_sync(0xffffffffu, low, o, 8);
     if ((lane & 7) >= o) {
       const float s = up + x;
-      if (kGrad) {  // the rounding of this sum, kept
-        const float w = s - up;
-        low += z + ((up - (s - w)) + (x - w));
-      }
+      low += z + two_sum_low(up, x, s);
       up = s;
     }
     if ((lane & 7) + o < 8) down += y;
   }
   float before = __shfl_up_sync(0xffffffffu, up, 1, 8), behind = __shfl_down_sync(0xffffffffu, down, 1, 8);
-  float before_low = kGrad ? __shfl_up_sync(0xffffffffu, low, 1, 8) : 0.f;
+  float before_low = __shfl_up_sync(0xffffffffu, low, 1, 8);
   if ((lane & 7) == 0) before = before_low = 0.f;
   if ((lane & 7) == 7) behind = 0.f;
   const float r0 = before + a0, r1 = up, s0 = behind + a1, s1 = behind;
@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(256) ssm_decay_kernel(SsmArgs A, void* out, fl
   const float e0 = expf(s0 + rest), e1 = expf(s1 + rest);
   put(d.D, D0, D1);
   put(d.rel, r0, r1);
+  put(d.rel_lo, before_low + two_sum_low(before, a0, r0), low);
   put(d.row, expf(r0), expf(r1));
   put(d.first, expf(base + r0), expf(base + r1));
   put(d.wD, e0 * D0, e1 * D1);
@@ -107,9 +108,7 @@ __global__ void __launch_bounds__(256) ssm_decay_kernel(SsmArgs A, void* out, fl
   }
   if (kGrad) {
     ChunkDecayGrad& dg = static_cast<ChunkDecayGrad*>(out)[id];
-    const float w = r0 - before;
     put(dg.last, e0, e1);
-    put(dg.rel_lo, before_low + ((before - (r0 - w)) + (a0 - w)), low);
     put(dg.sg, 1.f / (1.f + expf(-x0)), 1.f / (1.f + expf(-x1)));
   }
   if (lane == 0) tot[id] = expf(T[0] + T[1] + T[2] + T[3]);
@@ -120,21 +119,22 @@ struct ScanArgs {
   const ChunkDecay* decay;  // [B N][chunks]
   const float* tot;         // [B N][chunks]: exp(l_63)
   float* since;             // [B N][chunks]: decay from the segment's start to the chunk's
-  uint4* local;             // [B N][slices][chunks][fragments]: a segment's own state before each chunk
+  float4* local;            // [B N][slices][chunks][2 x fragments]: a segment's own state before each chunk
   float4* sums;             // [B N][slices][segs][2 x fragments]: the state each segment leaves
   float* seg_tot;           // [B N][segs]
-  uint4* start;             // [B N][slices][segs][fragments]: the state before each segment (kTile, for the tiles of
-                            // ssm_tc.cu: in the order of tc_state_at)
+  float4* start;            // [B N][slices][segs][2 x fragments]: the state before each segment (kTile, for the tiles
+                            // of ssm_tc.cu: in the order of tc_piece_at)
   int nc, segs, per_seg, slices;
   bool vq, vk, vv;          // rows that asynchronous copies can take
 };
 
 // A fragment: 16 state rows kt by 16 value columns vt, 32 lanes of 8 values
 // (k, v) = (16 kt + 8 b + 2 (lane % 4) + e, 16 vt + 8 h + lane / 4), in order
-// h, b, e: as bf16 pairs the B operands of value tiles 2 vt and 2 vt + 1.
+// h, b, e: as bf16 pairs the B operands of value tiles 2 vt and 2 vt + 1.  In
+// fp32 two float4 (h), in one bf16 part a uint4.
 template <int KP, int VS>
 struct Frag {
-  static constexpr int kVt = VS / 16, kCount = (KP / 16) * kVt * 32;  // uint4 per state of a slice
+  static constexpr int kVt = VS / 16, kCount = (KP / 16) * kVt * 32;  // per state of a slice
   static __device__ __forceinline__ int at(int kt, int vt, int lane) { return (kt * kVt + vt) * 32 + lane; }
 };
 
@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk
   each([&](float& s, int k, int v, bool ok) { s = from != nullptr && ok ? from[k * V + v0 + v] : 0.f; });
 
   float tot = 0.f, decay = 1.f;  // of a chunk; since the segment's start
-  uint4* local = W.local + (static_cast<int64_t>(head) * W.nc + c0) * Fr::kCount;
+  float4* local = W.local + (static_cast<int64_t>(head) * W.nc + c0) * (2 * Fr::kCount);
   if (c0 < live) {
     load_chunk(c0);
     tot = ptot[c0];
@@ -227,11 +227,11 @@ __global__ void __launch_bounds__(kThreads, WalkShape<KP, VS>::kBlocks) ssm_walk
 #pragma unroll
         for (int kt = 0; kt < Sh::kKt; ++kt) {
           const auto& s = S[vt][kt];
-          local[Fr::at(nw * Sh::kKt + kt, mw * Sh::kVt + vt, lane)] =
-              make_uint4(pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[0][2], s[0][3]),
-                         pack_bf16x2(s[1][2], s[1][3]));
+          float4* to = local + 2 * Fr::at(nw * Sh::kKt + kt, mw * Sh::kVt + vt, lane);
+          to[0] = make_float4(s[0][0], s[0][1], s[1][0], s[1][1]);
+          to[1] = make_float4(s[0][2], s[0][3], s[1][2], s[1][3]);
         }
-      local += Fr::kCount;
+      local += 2 * Fr::kCount;
       float U[Sh::kVt][Sh::kKt][2][4] = {};
 #pragma unroll
       for (int jt = 0; jt < 4; ++jt) {
@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(256) ssm_segment_scan_kernel(ScanArgs W) {
   const int lane = (e >> 1) & 31, tile = e >> 6, vt = tile % Fr::kVt, kt = tile / Fr::kVt;
   const int v = 16 * vt + 8 * (e & 1) + (lane >> 2), k = 16 * kt + 2 * (lane & 3);  // (and k + 1, k + 8, k + 9)
   const float4* sums = W.sums + static_cast<int64_t>(blockIdx.x) * W.segs * kN + e;
-  uint2* start = reinterpret_cast<uint2*>(W.start) + static_cast<int64_t>(blockIdx.x) * W.segs * kN + e;
+  float4* start = W.start + static_cast<int64_t>(blockIdx.x) * W.segs * kN;
   const float* tot = W.seg_tot + bn * W.segs;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = 0; i < W.segs; i += kAhead) {
@@ -328,12 +328,11 @@ __global__ void __launch_bounds__(256) ssm_segment_scan_kernel(ScanArgs W) {
     for (int j = 0; j < kAhead; ++j) {
       if (i + j >= W.segs) continue;
       if constexpr (kTile) {
-        uint8_t* out = reinterpret_cast<uint8_t*>(W.start) +
-                       (static_cast<int64_t>(blockIdx.x) * W.segs + i + j) * (Fr::kCount * 16) + tc_state_at(k, v);
-        *reinterpret_cast<uint32_t*>(out) = pack_bf16x2(s.x, s.y);
-        *reinterpret_cast<uint32_t*>(out + tc_state_at(8, 0)) = pack_bf16x2(s.z, s.w);
+        float* out = reinterpret_cast<float*>(start + static_cast<int64_t>(i + j) * kN);
+        *reinterpret_cast<float2*>(out + 4 * tc_piece_at(k, v) + (k & 3)) = make_float2(s.x, s.y);
+        *reinterpret_cast<float2*>(out + 4 * tc_piece_at(k + 8, v) + (k & 3)) = make_float2(s.z, s.w);
       } else {
-        start[static_cast<int64_t>(i + j) * kN] = make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+        start[static_cast<int64_t>(i + j) * kN + e] = s;
       }
       s = make_float4(fmaf(a[j], s.x, u[j].x), fmaf(a[j], s.y, u[j].y), fmaf(a[j], s.z, u[j].z),
                       fmaf(a[j], s.w, u[j].w));
@@ -353,7 +352,7 @@ __global__ void __launch_bounds__(256) ssm_segment_scan_kernel(ScanArgs W) {
 template <int KP, int VS>
 struct OutShape {
   static constexpr int kQ = Tile<KP>::kBytes(kChunk), kV = Tile<VS>::kBytes(kChunk), kS = Frag<KP, VS>::kCount * 16;
-  static constexpr int kBytes = 2 * kQ + kV + static_cast<int>(sizeof(ChunkDecay)) + 2 * kS + VS * 4;
+  static constexpr int kBytes = 2 * kQ + kV + kChunkDecayCopied + 2 * kS + VS * 4;
   static constexpr int kBlocks = KP * VS > 4096 ? 2 : 4;
 };
 
@@ -379,11 +378,10 @@ __global__ void __launch_bounds__(kThreads, OutShape<KP, VS>::kBlocks) ssm_out_k
     for (int e = tid; e < min(kChunk, A.T - t0) * width; e += kThreads) y[(e / width) * y_stride + e % width] = 0;
     return;
   }
-  const uint32_t sQ = smem_u32(smem), sK = sQ + Sh::kQ, sV = sK + Sh::kQ, sD = sV + Sh::kV,
-                 sS = sD + static_cast<uint32_t>(sizeof(ChunkDecay));
-  const ChunkDecay& d = *reinterpret_cast<const ChunkDecay*>(smem + 2 * Sh::kQ + Sh::kV);
-  const uint4* fS = reinterpret_cast<const uint4*>(smem + 2 * Sh::kQ + Sh::kV + sizeof(ChunkDecay));
-  float* s_wr = reinterpret_cast<float*>(smem + 2 * Sh::kQ + Sh::kV + sizeof(ChunkDecay) + 2 * Sh::kS);
+  const uint32_t sQ = smem_u32(smem), sK = sQ + Sh::kQ, sV = sK + Sh::kQ, sD = sV + Sh::kV;
+  const ChunkDecay& d = *reinterpret_cast<const ChunkDecay*>(smem + 2 * Sh::kQ + Sh::kV);  // without wD
+  uint4* fS = reinterpret_cast<uint4*>(smem + 2 * Sh::kQ + Sh::kV + kChunkDecayCopied);  // hi, then lo
+  float* s_wr = reinterpret_cast<float*>(smem + 2 * Sh::kQ + Sh::kV + kChunkDecayCopied + 2 * Sh::kS);
   const TileLoader<KP, kThreads> lq{static_cast<const uint16_t*>(A.q) + row * A.q_stride + static_cast<int64_t>(gq) * K,
                                     A.q_stride, K, W.vq};
   const TileLoader<KP, kThreads> lk{static_cast<const uint16_t*>(A.k) + row * A.k_stride + static_cast<int64_t>(gq) * K,
@@ -394,84 +392,67 @@ __global__ void __launch_bounds__(kThreads, OutShape<KP, VS>::kBlocks) ssm_out_k
   lq.load(sQ, t0, len);
   lk.load(sK, t0, len);
   const int64_t at = static_cast<int64_t>(bn) * W.nc + c;
+  static_assert(kChunkDecayCopied == 16 * kThreads, "a copy a thread");
   cp_async_16(sD + tid * 16, reinterpret_cast<const uint8_t*>(W.decay + at) + tid * 16, true);
-  cp_async_commit();
-  {
-    const uint4* l = W.local + ((static_cast<int64_t>(bn) * W.slices + slice) * W.nc + c) * Fr::kCount;
-    const uint4* s = W.start + ((static_cast<int64_t>(bn) * W.slices + slice) * W.segs + seg) * Fr::kCount;
-#pragma unroll
-    for (int e = tid; e < Fr::kCount; e += kThreads) cp_async_16(sS + e * 16, l + e, true);
-    if (more) {
-#pragma unroll
-      for (int e = tid; e < Fr::kCount; e += kThreads) cp_async_16(sS + Sh::kS + e * 16, s + e, true);
-    }
-  }
   lv.load(sV, t0, len);
   cp_async_commit();
-  const float since = more ? W.since[at] : 0.f;
+  {  // The state before the chunk, joined and in two parts.
+    const float4* l = W.local + ((static_cast<int64_t>(bn) * W.slices + slice) * W.nc + c) * (2 * Fr::kCount);
+    const float4* s = W.start + ((static_cast<int64_t>(bn) * W.slices + slice) * W.segs + seg) * (2 * Fr::kCount);
+    const float since = more ? W.since[at] : 0.f;
+    auto part = [&](const float4& own, const float4& before, uint32_t* hi, uint32_t* lo) {
+      split2(fmaf(since, before.x, own.x), fmaf(since, before.y, own.y), hi[0], lo[0]);
+      split2(fmaf(since, before.z, own.z), fmaf(since, before.w, own.w), hi[1], lo[1]);
+    };
+    constexpr int kPer = (Fr::kCount + kThreads - 1) / kThreads, kMost = Sh::kBlocks == 2 ? 8 : 4,
+                  kBatch = kPer < kMost ? kPer : kMost;
+#pragma unroll
+    for (int i0 = 0; i0 < kPer; i0 += kBatch) {
+      float4 own[kBatch][2], before[kBatch][2];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int e = (i0 + i) * kThreads + tid;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          own[i][h] = before[i][h] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (e >= Fr::kCount) continue;
+          own[i][h] = l[2 * e + h];
+          if (more) before[i][h] = s[2 * e + h];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int e = (i0 + i) * kThreads + tid;
+        if (e >= Fr::kCount) continue;
+        uint32_t hi[4], lo[4];
+        part(own[i][0], before[i][0], hi, lo);
+        part(own[i][1], before[i][1], hi + 2, lo + 2);
+        fS[e] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        fS[Fr::kCount + e] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
+  }
   for (int e = tid; e < VS; e += kThreads)
     s_wr[e] = A.w_r != nullptr && e < width ? to_f32(static_cast<const uint16_t*>(A.w_r)[n * V + v0 + e]) : 0.f;
-  cp_async_wait<1>();
+  cp_async_wait<0>();
   __syncthreads();
 
-  uint32_t qf[kKt][4], P[4][4];  // q; decayed scores as A operands, per 16 steps j
+  uint32_t qf[kKt][4];
 #pragma unroll
   for (int kt = 0; kt < kKt; ++kt) ldmatrix_x4(qf[kt], at_rows<KP>(sQ, 16 * warp, 16 * kt, lane));
   const int i0 = 16 * warp + g, i1 = i0 + 8;
-  {
-    const float r0 = d.row[i0], r1 = d.row[i1], l0 = d.rel[i0], l1 = d.rel[i1];
-#pragma unroll
-    for (int jt = 0; jt < 4; ++jt) {
-      if (jt > warp) continue;
-      float s[2][4] = {};
-#pragma unroll
-      for (int kt = 0; kt < kKt; ++kt) {
-        uint32_t kf[4];
-        ldmatrix_x4(kf, at_cols<KP>(sK, 16 * jt, 16 * kt, lane));
-        mma_bf16_16816(s[0], qf[kt], kf[0], kf[1]);
-        mma_bf16_16816(s[1], qf[kt], kf[2], kf[3]);
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int j = 16 * jt + 8 * h + 2 * q4;
-        if (jt < warp) {
-          const float2 cf = *reinterpret_cast<const float2*>(&d.col[warp - 1][j]);
-          P[jt][2 * h] = pack_bf16x2(s[h][0] * (r0 * cf.x), s[h][1] * (r0 * cf.y));
-          P[jt][2 * h + 1] = pack_bf16x2(s[h][2] * (r1 * cf.x), s[h][3] * (r1 * cf.y));
-        } else {
-          const float2 D = *reinterpret_cast<const float2*>(&d.D[j]);
-          const float2 lj = *reinterpret_cast<const float2*>(&d.rel[j]);
-          const float p0 = j <= i0 ? s[h][0] * (exp_fast(l0 - lj.x) * D.x) : 0.f;
-          const float p1 = j + 1 <= i0 ? s[h][1] * (exp_fast(l0 - lj.y) * D.y) : 0.f;
-          const float p2 = j <= i1 ? s[h][2] * (exp_fast(l1 - lj.x) * D.x) : 0.f;
-          const float p3 = j + 1 <= i1 ? s[h][3] * (exp_fast(l1 - lj.y) * D.y) : 0.f;
-          P[jt][2 * h] = pack_bf16x2(p0, p1);
-          P[jt][2 * h + 1] = pack_bf16x2(p2, p3);
-        }
-      }
-    }
-  }
-  cp_async_wait<0>();
-  __syncthreads();
+  // The state's part, from its small part up.
   float O[VS / 8][4] = {};
-  auto add_state = [&](const uint4* f) {
+#pragma unroll
+  for (int part = 1; part >= 0; --part)
 #pragma unroll
     for (int kt = 0; kt < kKt; ++kt)
 #pragma unroll
       for (int vt = 0; vt < VS / 16; ++vt) {
-        const uint4 s = f[Fr::at(kt, vt, lane)];
+        const uint4 s = fS[part * Fr::kCount + Fr::at(kt, vt, lane)];
         mma_bf16_16816(O[2 * vt], qf[kt], s.x, s.y);
         mma_bf16_16816(O[2 * vt + 1], qf[kt], s.z, s.w);
       }
-  };
-  if (more) {
-    add_state(fS + Fr::kCount);
-#pragma unroll
-    for (int nt = 0; nt < VS / 8; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) O[nt][e] *= since;
-  }
-  add_state(fS);
   const float e0 = d.first[i0], e1 = d.first[i1];
 #pragma unroll
   for (int nt = 0; nt < VS / 8; ++nt) {
@@ -480,15 +461,45 @@ __global__ void __launch_bounds__(kThreads, OutShape<KP, VS>::kBlocks) ssm_out_k
     O[nt][2] *= e1;
     O[nt][3] *= e1;
   }
+  // Blocks of 16 steps: scores, their decays, in two parts times v.
+  const float r0 = d.row[i0], r1 = d.row[i1], l0 = d.rel[i0], l1 = d.rel[i1], m0 = d.rel_lo[i0], m1 = d.rel_lo[i1];
+#pragma unroll 1
+  for (int jt = 0; jt <= warp; ++jt) {
+    float s[2][4] = {};
 #pragma unroll
-  for (int jt = 0; jt < 4; ++jt) {
-    if (jt > warp) continue;
+    for (int kt = 0; kt < kKt; ++kt) {
+      uint32_t kf[4];
+      ldmatrix_x4(kf, at_cols<KP>(sK, 16 * jt, 16 * kt, lane));
+      mma_bf16_16816(s[0], qf[kt], kf[0], kf[1]);
+      mma_bf16_16816(s[1], qf[kt], kf[2], kf[3]);
+    }
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = 16 * jt + 8 * h + 2 * q4;
+      if (jt < warp) {
+        const float2 cf = *reinterpret_cast<const float2*>(&d.col[warp - 1][j]);
+        split2(s[h][0] * (r0 * cf.x), s[h][1] * (r0 * cf.y), hi[2 * h], lo[2 * h]);
+        split2(s[h][2] * (r1 * cf.x), s[h][3] * (r1 * cf.y), hi[2 * h + 1], lo[2 * h + 1]);
+      } else {
+        const float2 D = *reinterpret_cast<const float2*>(&d.D[j]);
+        const float2 lj = *reinterpret_cast<const float2*>(&d.rel[j]), mj = *reinterpret_cast<const float2*>(&d.rel_lo[j]);
+        const float p0 = j <= i0 ? s[h][0] * (exp_fast((l0 - lj.x) + (m0 - mj.x)) * D.x) : 0.f;
+        const float p1 = j + 1 <= i0 ? s[h][1] * (exp_fast((l0 - lj.y) + (m0 - mj.y)) * D.y) : 0.f;
+        const float p2 = j <= i1 ? s[h][2] * (exp_fast((l1 - lj.x) + (m1 - mj.x)) * D.x) : 0.f;
+        const float p3 = j + 1 <= i1 ? s[h][3] * (exp_fast((l1 - lj.y) + (m1 - mj.y)) * D.y) : 0.f;
+        split2(p0, p1, hi[2 * h], lo[2 * h]);
+        split2(p2, p3, hi[2 * h + 1], lo[2 * h + 1]);
+      }
+    }
 #pragma unroll
     for (int vt = 0; vt < VS / 16; ++vt) {
       uint32_t vf[4];
       ldmatrix_x4_trans(vf, at_rows<VS>(sV, 16 * jt, 16 * vt, lane));
-      mma_bf16_16816(O[2 * vt], P[jt], vf[0], vf[1]);
-      mma_bf16_16816(O[2 * vt + 1], P[jt], vf[2], vf[3]);
+      mma_bf16_16816(O[2 * vt], lo, vf[0], vf[1]);
+      mma_bf16_16816(O[2 * vt + 1], lo, vf[2], vf[3]);
+      mma_bf16_16816(O[2 * vt], hi, vf[0], vf[1]);
+      mma_bf16_16816(O[2 * vt + 1], hi, vf[2], vf[3]);
     }
   }
   // y = O + w_r v, rounded to bf16, by way of the warp's own rows of the q tile.
@@ -525,8 +536,8 @@ __global__ void __launch_bounds__(kThreads, OutShape<KP, VS>::kBlocks) ssm_out_k
 }
 
 // The tcgen05 walk and outputs are built for 64 x 64 states, have one block per SM and want two tiles for each of
-// them.  Measured, a whole call with them / with the walk and the outputs of this file, us: 64 tiles 13.1 / 12.6,
-// 128 tiles 17.1 / 15.7, 256 18.5 / 17.0, 512 23.7 / 27.3, 1024 31.6 / 43.1, 2048 54 / 70, 4096 96 / 127.
+// them.  Measured, a whole call with them / with the walk and the outputs of this file, us: 64 tiles 14.4 / 13.9,
+// 128 tiles 19.9 / 17.4, 256 20.8 / 19.8, 512 26.4 / 32.5, 1024 35.8 / 52.7, 2048 65 / 88.
 constexpr int64_t kMinTiles = 2 * 152;
 
 int padded_rows(int64_t K) { return K <= 32 ? 32 : K <= 64 ? 64 : 128; }
@@ -575,11 +586,11 @@ Layout make_layout(const Plan& p, int64_t chains) {
   // cannot take fall back on the larger)
   l.tot = take(chunks * 4);
   l.since = take(chunks * 4);
-  l.local = take(chunks * p.slices * state * 2);
+  l.local = take(chunks * p.slices * state * 4);
   if (p.segs > 1) {
     l.sums = take(segs * p.slices * state * 4);
     l.seg_tot = take(segs * 4);
-    l.start = take(segs * p.slices * state * 2);
+    l.start = take(segs * p.slices * state * 4);
   }
   return l;
 }
@@ -635,10 +646,10 @@ cudaError_t launch_ssm_mma_forward(const SsmArgs& a, cudaStream_t s) {
   w.a = a;
   w.tot = reinterpret_cast<float*>(ws + l.tot);
   w.since = reinterpret_cast<float*>(ws + l.since);
-  w.local = reinterpret_cast<uint4*>(ws + l.local);
+  w.local = reinterpret_cast<float4*>(ws + l.local);
   w.sums = reinterpret_cast<float4*>(ws + l.sums);
   w.seg_tot = reinterpret_cast<float*>(ws + l.seg_tot);
-  w.start = reinterpret_cast<uint4*>(ws + l.start);
+  w.start = reinterpret_cast<float4*>(ws + l.start);
   w.nc = p.nc;
   w.segs = p.segs;
   w.per_seg = p.per_seg;
@@ -652,14 +663,13 @@ cudaError_t launch_ssm_mma_forward(const SsmArgs& a, cudaStream_t s) {
                                                  : (a.k_stride > a.v_stride ? a.k_stride : a.v_stride);
   if (p.tile && w.vq && w.vk && w.vv && widest * a.T < (int64_t{1} << 39)) {
     TileDecay* decay = reinterpret_cast<TileDecay*>(ws + l.decay);
-    uint8_t* local = reinterpret_cast<uint8_t*>(w.local);
     cudaError_t e = launch_ssm_tile_decay(a, decay, tot, p.nc, status, s);
     if (e == cudaSuccess)
-      e = launch_ssm_tc_walk(TcWalkArgs{a, decay, tot, local, w.sums, w.seg_tot, status, p.nc, p.nc / 2, p.segs,
+      e = launch_ssm_tc_walk(TcWalkArgs{a, decay, tot, w.local, w.sums, w.seg_tot, status, p.nc, p.nc / 2, p.segs,
                                         p.per_seg, p.slices}, s);
     if (e == cudaSuccess) e = join_segments<kTcK, kTcV, true>(w, chains * w.slices, s);
     if (e != cudaSuccess) return e;
-    return launch_ssm_tc_out(TcOutArgs{a, decay, local, reinterpret_cast<const uint8_t*>(w.start), status, p.nc, p.nc / 2, p.segs,
+    return launch_ssm_tc_out(TcOutArgs{a, decay, w.local, w.start, status, p.nc, p.nc / 2, p.segs,
                                        p.per_seg, p.slices}, s);
   }
   ChunkDecay* decay = reinterpret_cast<ChunkDecay*>(ws + l.decay);

@@ -94,7 +94,14 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t& hi, uint32_t&
   lo = pack_bf16x2(x, y);
 }
 
-// The same of two bf16 values times two weights.
+// As two, whose sum is good to 2^-16.
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf16x2(x, y);
+  sub2(x, y, bf16lo(hi), bf16hi(hi));
+  lo = pack_bf16x2(x, y);
+}
+
+// The same of two bf16 values times two weights, as three.
 __device__ __forceinline__ void split3_weighted(uint32_t k, float w0, float w1, uint32_t& hi, uint32_t& mid,
                                                 uint32_t& lo) {
   float x, y;
@@ -108,22 +115,31 @@ __device__ __forceinline__ void split3_weighted(uint32_t k, float w0, float w1, 
 // chunk takes a few hundred exponentials and not 64 x 64.  Made once per call
 // for every (chain, chunk) and read by the chunk's blocks.
 struct __align__(16) ChunkDecay {
-  float wD[kChunk];      // exp(l_63 - l_j) D_j
   float first[kChunk];   // exp(l_i)
   float row[kChunk];     // exp(l_i - l before i's block)
-  float rel[kChunk];     // l_i - l before i's block
+  float rel[kChunk];     // l_i - l before i's block,
+  float rel_lo[kChunk];  // and the part of it that rel leaves out: differences of long sums keep their bits
   float D[kChunk];       // step sizes, 0 behind the sequence's end
   float col[3][kChunk];  // exp(l before block ib - l_j) for j < 16 ib, ib = 1 .. 3 (else 0); the forward's times D_j
+  float wD[kChunk];      // exp(l_63 - l_j) D_j, for the walks; the forward's outputs leave it out
 };
-static_assert(sizeof(ChunkDecay) == 2048, "128 copies of 16 bytes");
+constexpr int kChunkDecayCopied = 8 * kChunk * 4;
+static_assert(kChunkDecayCopied == 2048 && sizeof(ChunkDecay) == kChunkDecayCopied + kChunk * 4,
+              "128 copies of 16 bytes for the outputs");
 
 // What the backward reads besides.
 struct __align__(16) ChunkDecayGrad {
   ChunkDecay d;
   float last[kChunk];    // exp(l_63 - l_j)
-  float rel_lo[kChunk];  // the part of the sum that rel leaves out
   float sg[kChunk];      // sigmoid(dt + dt_bias)
 };
+
+// log a = D A, kept finite where it runs out of fp32 below (a is 0 all the same): sums of it and their differences
+// stay numbers.
+__device__ __forceinline__ float log_decay(float D, float A) {
+  const float x = D * A;
+  return x < -1e30f ? -1e30f : x;
+}
 
 // Decays of every (chain, chunk) into `out` (ChunkDecay, or ChunkDecayGrad for
 // the backward), exp(l_63) into tot; clears the status block.

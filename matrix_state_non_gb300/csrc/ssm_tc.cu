@@ -1,26 +1,29 @@
 // Outputs of the selective state space scan on the 5th-generation tensor
 // cores, for tiles of 128 steps of one head and up to 64 state rows and value
 // columns (the mathematics in ssm.cu, the phases in ssm_mma.cu):
-//     y_i = first_i (S^T q_i + since S0^T q_i) + sum_j P_ij v_j + w_r (*) v_i,
+//     y_i = first_i (S + since S0)^T q_i + sum_j P_ij v_j + w_r (*) v_i,
 //     P_ij = exp(l_i - l_j) D_j (q_i . k_j) for j <= i.
 // One persistent block per SM:
-//   warps 9-11  producers: q, k, v by TMA (128-byte swizzle), the states and the
-//               decays by bulk copies, into a ring of three stages; a sequence's
-//               last tile row by row, with zeros behind its end;
-//   warp 8      issues the products: Q K^T, Q S, Q S0 (M = 128) into one of two
-//               tensor-memory slots, then P V, with P taken from tensor memory;
+//   warps 9-11  producers: q, k, v by TMA (128-byte swizzle), the decays by bulk
+//               copies, into a ring of three stages; a sequence's last tile row by
+//               row, with zeros behind its end; the state, S and S0 joined in fp32,
+//               by way of registers as two bf16 operands;
+//   warp 8      issues the products: Q K^T and Q times the state's two parts
+//               (M = 128) into one of two tensor-memory slots, then P V, with P's
+//               two parts taken from tensor memory;
 //   warps 0-3, 4-7  take the slots in turn, a thread a row: decay the scores,
-//               round P to bf16 and write it back over them; then y.
-// P takes its place in the scores' first half and P V the second, so a slot is
-// 256 columns and two tiles are in work at once.  The factor of row i and an
+//               split P into two bf16 parts and write them back; then y.
+// P's large part takes its place in the scores' first half and P V the second,
+// so with the state's product and P's small part a slot is 256 columns and two
+// tiles are in work at once.  The factor of row i and an
 // earlier block of 32 steps is one exponential per row and block times a
 // tabled factor per step, so a tile takes some 40 exponentials a row, not 128.
 //
-// B=2 heads=16 T=16384 64x64, shared q and k: 52 us (whole scan 96), 345 MB
-// through L2 at 6.6 TB/s; a tile takes 3900 cycles of an SM, of which the
-// rows' work (decay, P, y) is 3100 for each of two tiles at a time.  The same
-// outputs on mma.sync, four blocks of 64 steps to an SM: 72 us.  y by a TMA
-// store and S, S0 as one operand of 128 columns: no gain, left out.
+// B=2 heads=16 T=16384 64x64, shared q and k: 73 us (whole scan 121), 412 MB
+// through L2; without the states' 134 MB, which go through L2 in fp32, and
+// their split it would be 57.  (Operands in one bf16 part each, rounded by the
+// walk: 52 us, and y's error a fifth above its rounding.)  y by a TMA store: no
+// gain, left out.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -46,17 +49,23 @@ __global__ void __launch_bounds__(256) ssm_tile_decay_kernel(SsmArgs A, TileDeca
   const float bias = A.dt_bias ? A.dt_bias[n] : 0.f, An = A.A[n];
   const float D0 = t < len ? softplus_f(to_f32(p[0]) + bias) : 0.f;
   const float D1 = t + 1 < len ? softplus_f(to_f32(p[A.dt_stride]) + bias) : 0.f;
-  const float a0 = D0 * An, a1 = D1 * An;
+  const float a0 = log_decay(D0, An), a1 = log_decay(D1, An);
   // Within the block of 32 steps: the sum up to a step, and the sum behind it.
-  float up = a0 + a1, down = up;
+  float up = a0 + a1, down = up, low = two_sum_low(a0, a1, up);
 #pragma unroll
   for (int o = 1; o < 16; o <<= 1) {
     const float x = __shfl_up_sync(0xffffffffu, up, o, 16), y = __shfl_down_sync(0xffffffffu, down, o, 16);
-    if (in >= o) up += x;
+    const float z = __shfl_up_sync(0xffffffffu, low, o, 16);
+    if (in >= o) {
+      const float s = up + x;
+      low += z + two_sum_low(up, x, s);
+      up = s;
+    }
     if (in + o < 16) down += y;
   }
   float before = __shfl_up_sync(0xffffffffu, up, 1, 16), behind = __shfl_down_sync(0xffffffffu, down, 1, 16);
-  if (in == 0) before = 0.f;
+  float before_low = __shfl_up_sync(0xffffffffu, low, 1, 16);
+  if (in == 0) before = before_low = 0.f;
   if (in == 15) behind = 0.f;
   const float s0 = behind + a1, s1 = behind;
   const float T0 = __shfl_sync(0xffffffffu, up, 15), T1 = __shfl_sync(0xffffffffu, up, 31);
@@ -64,7 +73,9 @@ __global__ void __launch_bounds__(256) ssm_tile_decay_kernel(SsmArgs A, TileDeca
   TileDecay& d = out[id];
   const int i = 2 * lane;
   auto put = [&](float* at, float x, float y) { *reinterpret_cast<float2*>(at + i) = make_float2(x, y); };
-  put(d.rel, before + a0, up);
+  const float r0 = before + a0;
+  put(d.rel, r0, up);
+  put(d.lo, before_low + two_sum_low(before, a0, r0), low);
   put(d.cf, expf(s0) * D0, expf(s1) * D1);
   put(d.D, D0, D1);
   put(d.wD, expf(s0 + rest) * D0, expf(s1 + rest) * D1);
@@ -80,8 +91,8 @@ constexpr int kStages = 3;
 // Shared memory of a stage.  Q, K, V: 128 rows of 128 bytes, 16-byte pieces
 // XOR-swizzled by (row mod 8), 1 KB aligned, as TMA writes and the products'
 // descriptors read them; the states as tc_state_at orders them.
-constexpr int kOffK = kOp, kOffV = 2 * kOp, kOffS = 3 * kOp, kOffS0 = kOffS + kTcStateBytes,
-              kOffD = kOffS0 + kTcStateBytes, kOffWr = kOffD + 2 * kTileDecayCopied,
+constexpr int kOffK = kOp, kOffV = 2 * kOp, kOffS = 3 * kOp, kOffSLo = kOffS + kTcStateBytes,
+              kOffD = kOffSLo + kTcStateBytes, kOffWr = kOffD + 2 * kTileDecayCopied,
               kStage = (kOffWr + kTcV * 2 + 1023) / 1024 * 1024;
 constexpr int kOffBar = kStages * kStage;  // barriers, then the tensor-memory address and the abort flag
 constexpr int kSmem = kOffBar + 256 + 1024;  // 1024: alignment
@@ -90,7 +101,7 @@ static_assert(kTile * kYPitch <= 2 * kOp, "y fits over Q and K");
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 // Tensor-memory columns of a slot.
-constexpr uint32_t kColP = 0, kColPV = 64, kColS = 128, kColS0 = 192, kSlot = 256;
+constexpr uint32_t kColP = 0, kColPV = 64, kColS = 128, kColPLo = 192, kSlot = 256;
 
 constexpr uint32_t kWhereFull = 401, kWhereP = 402, kWhereScores = 403, kWhereOut = 404, kWhereEmpty = 405,
                    kWhereDrain = 406;
@@ -120,9 +131,6 @@ struct TileWalk {
   __device__ __forceinline__ bool live() const {  // steps of the sequence in it
     const int len = W.a.lengths ? ssm_len(W.a, head / (W.slices * W.a.N)) : W.a.T;
     return static_cast<int>(tt) * kTile < len;
-  }
-  __device__ __forceinline__ bool handed() const {  // a segment before it
-    return 2 * static_cast<int>(tt) >= W.per_seg;
   }
 };
 
@@ -208,6 +216,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!at.live()) continue;
       const TilePlace t = tile_place(at);
       const int s = u % kStages;
+      // The state before the tile, eight state rows of a value column at a time: on its way before the stage is free.
+      constexpr int kPieces = kTcState / 2, kPer = (kPieces + kProd - 1) / kProd;
+      float4 own[kPer][2], before[kPer][2];
+      const float4* l = W.local + (t.head * W.nt + t.t0 / kTile) * kTcState;
+      const float4* z = W.start + (t.head * W.segs + t.seg) * kTcState;
+      const TileDecay* d = W.decay + t.chain * W.nc + t.t0 / kChunk;
+      const float since = t.seg > 0 ? d->T[2] : 0.f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int e = p + i * kProd, x = tc_piece_at(e / kTcV * 8, e % kTcV);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          own[i][h] = before[i][h] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (e >= kPieces) continue;
+          own[i][h] = l[x + h * kTcV];
+          if (t.seg > 0) before[i][h] = z[x + h * kTcV];
+        }
+      }
       if (u >= kStages && !warp_wait(empty(s), (u / kStages - 1) & 1, abort_flag, W.status, kWhereEmpty)) {
         ok = false;
         break;
@@ -216,15 +242,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool whole = t.t0 + kTile <= t.len;
       if (p == 0) {
         const uint32_t wr_bytes = A.w_r != nullptr ? 2 * t.width : 0;
-        mbar_expect_tx(bar, kTcStateBytes * (t.seg > 0 ? 2 : 1) + 2 * kTileDecayCopied + wr_bytes + (whole ? 3 * kOp : 0));
+        mbar_expect_tx(bar, 2 * kTileDecayCopied + wr_bytes + (whole ? 3 * kOp : 0));
         if (whole) {
           tma_load_4d(st, &map_q, bar, 0, t.gq, t.t0, t.b);
           tma_load_4d(st + kOffK, &map_k, bar, 0, t.gq, t.t0, t.b);
           tma_load_4d(st + kOffV, &map_v, bar, t.v0, t.n, t.t0, t.b);
         }
-        bulk_load(st + kOffS, W.local + (t.head * W.nt + t.t0 / kTile) * kTcStateBytes, kTcStateBytes, bar);
-        if (t.seg > 0) bulk_load(st + kOffS0, W.start + (t.head * W.segs + t.seg) * kTcStateBytes, kTcStateBytes, bar);
-        const TileDecay* d = W.decay + t.chain * W.nc + t.t0 / kChunk;
         bulk_load(st + kOffD, d, kTileDecayCopied, bar);
         bulk_load(st + kOffD + kTileDecayCopied, d + 1, kTileDecayCopied, bar);
         if (wr_bytes != 0)
@@ -246,9 +269,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           cp_async_16(st + op * kOp + piece_at(r, piece), in ? src + r * stride + piece * 8 : src, in);
         }
         cp_async_commit();
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
       }
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int e = p + i * kProd;
+        if (e >= kPieces) continue;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float4 &a = own[i][h], &b = before[i][h];
+          split2(fmaf(since, b.x, a.x), fmaf(since, b.y, a.y), hi[2 * h], lo[2 * h]);
+          split2(fmaf(since, b.z, a.z), fmaf(since, b.w, a.w), hi[2 * h + 1], lo[2 * h + 1]);
+        }
+        const uint32_t to = st + kOffS + tc_state_at(e / kTcV * 8, e % kTcV);
+        st_shared_v4(to, hi);
+        st_shared_v4(to + kTcStateBytes, lo);
+      }
+      if (!whole) cp_async_wait<0>();
+      fence_proxy_async_smem();
       mbar_arrive(bar);
       ++u;
     }
@@ -276,7 +314,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t tm = tmem + (o & 1) * kSlot, sv = base + (o % kStages) * kStage + kOffV;
 #pragma unroll
           for (int kk = 0; kk < kTile / 16; ++kk)
-            tc_mma_f16_ts(tm + kColPV, tm + kColP + 8 * kk, desc_sw128(sv + kk * 2048), kIdPV, kk > 0);
+            tc_mma_f16_ts(tm + kColPV, tm + kColPLo + 8 * kk, desc_sw128(sv + kk * 2048), kIdPV, kk > 0);
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            tc_mma_f16_ts(tm + kColPV, tm + kColP + 8 * kk, desc_sw128(sv + kk * 2048), kIdPV, true);
           tc_commit(ofull(o & 1));
         }
         __syncwarp();
@@ -293,14 +334,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_mma_f16_ss(tm, desc_sw128(sq + kk * 32), desc_sw128(sq + kOffK + kk * 32), kIdQK, kk > 0);
 #pragma unroll
           for (int kk = 0; kk < kTcK / 16; ++kk)
-            tc_mma_f16_ss(tm + kColS, desc_sw128(sq + kk * 32), desc_state(sq + kOffS + kk * 2 * kTcV * 16), kIdS,
+            tc_mma_f16_ss(tm + kColS, desc_sw128(sq + kk * 32), desc_state(sq + kOffSLo + kk * 2 * kTcV * 16), kIdS,
                           kk > 0);
-          if (at.handed()) {
 #pragma unroll
-            for (int kk = 0; kk < kTcK / 16; ++kk)
-              tc_mma_f16_ss(tm + kColS0, desc_sw128(sq + kk * 32), desc_state(sq + kOffS0 + kk * 2 * kTcV * 16), kIdS,
-                            kk > 0);
-          }
+          for (int kk = 0; kk < kTcK / 16; ++kk)
+            tc_mma_f16_ss(tm + kColS, desc_sw128(sq + kk * 32), desc_state(sq + kOffS + kk * 2 * kTcV * 16), kIdS,
+                          true);
           tc_commit(scores(s & 1));
         }
         __syncwarp();
@@ -354,27 +393,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!warp_wait(full(s), (v / kStages) & 1, abort_flag, W.status, kWhereFull)) break;
       const float* dec = reinterpret_cast<const float*>(stp + kOffD);
       constexpr int kHalf = kTileDecayCopied / 4;
-      auto decays = [&](int block) { return dec + (block >> 1) * kHalf + (block & 1) * 32; };  // rel; cf 64, D 128 behind
-      const float rel = decays(w)[lane];
+      auto decays = [&](int block) { return dec + (block >> 1) * kHalf + (block & 1) * 32; };  // rel; cf 64, D 128, lo 192 behind
+      const float rel = decays(w)[lane], low = decays(w)[3 * kChunk + lane];
       float T[4];
 #pragma unroll
-      for (int x = 0; x < 4; ++x) T[x] = dec[(x >> 1) * kHalf + 3 * kChunk + (x & 1)];
-      const float since = dec[3 * kChunk + 2];
+      for (int x = 0; x < 4; ++x) T[x] = dec[(x >> 1) * kHalf + 4 * kChunk + (x & 1)];
       if (!warp_wait(scores(slot), (v >> 1) & 1, abort_flag, W.status, kWhereScores)) break;
       tc_fence_after_sync();
       // Blocks of 32 steps before the warp's own, the next block's scores on their way.  (A loop, not unrolled: the
       // warps are in different phases, and their code has to fit the instruction cache together.)
       uint32_t sc[32];
       tmem_ld_32x32b<32>(tm, sc);
-      float mid = 0.f;  // the blocks between
-#pragma unroll
-      for (int x = 1; x < 3; ++x) mid += x < w ? T[x] : 0.f;
+      float mid = w < 2 ? 0.f : w == 2 ? T[1] : T[1] + T[2];  // the blocks between
 #pragma unroll 1
       for (int jb = 0; jb < w; ++jb) {
         const float4* f = reinterpret_cast<const float4*>(decays(jb) + kChunk);
         const float rf = exp_fast(rel + mid);
-        mid -= jb == 0 ? (w > 1 ? T[1] : 0.f) : jb == 1 ? (w > 2 ? T[2] : 0.f) : 0.f;
-        uint32_t pr[16];
+        mid = jb == 0 && w == 3 ? T[2] : 0.f;
+        uint32_t hi[16], lo[16];
         tmem_ld_wait();
         tmem_ld_fence_regs(sc);
 #pragma unroll
@@ -385,32 +421,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           mul2(d, e, c.z, c.w, rf, rf);
           mul2(a, b, a, b, __uint_as_float(sc[x]), __uint_as_float(sc[x + 1]));
           mul2(d, e, d, e, __uint_as_float(sc[x + 2]), __uint_as_float(sc[x + 3]));
-          pr[x / 2] = pack_bf16x2(a, b);
-          pr[x / 2 + 1] = pack_bf16x2(d, e);
+          split2(a, b, hi[x / 2], lo[x / 2]);
+          split2(d, e, hi[x / 2 + 1], lo[x / 2 + 1]);
         }
         tmem_ld_32x32b<32>(tm + 32 * (jb + 1), sc);
-        tmem_st_32x32b_x16(tm + kColP + 16 * jb, pr);
+        tmem_st_32x32b_x16(tm + kColP + 16 * jb, hi);
+        tmem_st_32x32b_x16(tm + kColPLo + 16 * jb, lo);
       }
       {
         const float4* dr = reinterpret_cast<const float4*>(decays(w));
-        uint32_t pr[16];
+        uint32_t hi[16], lo[16];
         tmem_ld_wait();
         tmem_ld_fence_regs(sc);
 #pragma unroll
         for (int x = 0; x < 32; x += 4) {
-          const float4 r = dr[x / 4], D = dr[(2 * kChunk + x) / 4];
-          const float a = x <= lane ? __uint_as_float(sc[x]) * (exp_fast(rel - r.x) * D.x) : 0.f;
-          const float b = x + 1 <= lane ? __uint_as_float(sc[x + 1]) * (exp_fast(rel - r.y) * D.y) : 0.f;
-          const float c = x + 2 <= lane ? __uint_as_float(sc[x + 2]) * (exp_fast(rel - r.z) * D.z) : 0.f;
-          const float e = x + 3 <= lane ? __uint_as_float(sc[x + 3]) * (exp_fast(rel - r.w) * D.w) : 0.f;
-          pr[x / 2] = pack_bf16x2(a, b);
-          pr[x / 2 + 1] = pack_bf16x2(c, e);
+          const float4 r = dr[x / 4], D = dr[(2 * kChunk + x) / 4], m = dr[(3 * kChunk + x) / 4];
+          const float a = x <= lane ? __uint_as_float(sc[x]) * (exp_fast((rel - r.x) + (low - m.x)) * D.x) : 0.f;
+          const float b = x + 1 <= lane ? __uint_as_float(sc[x + 1]) * (exp_fast((rel - r.y) + (low - m.y)) * D.y) : 0.f;
+          const float c = x + 2 <= lane ? __uint_as_float(sc[x + 2]) * (exp_fast((rel - r.z) + (low - m.z)) * D.z) : 0.f;
+          const float e = x + 3 <= lane ? __uint_as_float(sc[x + 3]) * (exp_fast((rel - r.w) + (low - m.w)) * D.w) : 0.f;
+          split2(a, b, hi[x / 2], lo[x / 2]);
+          split2(c, e, hi[x / 2 + 1], lo[x / 2 + 1]);
         }
-        tmem_st_32x32b_x16(tm + kColP + 16 * w, pr);
+        tmem_st_32x32b_x16(tm + kColP + 16 * w, hi);
+        tmem_st_32x32b_x16(tm + kColPLo + 16 * w, lo);
 #pragma unroll
-        for (int x = 0; x < 16; ++x) pr[x] = 0u;
+        for (int x = 0; x < 16; ++x) hi[x] = 0u;
 #pragma unroll 1
-        for (int jb = w + 1; jb < 4; ++jb) tmem_st_32x32b_x16(tm + kColP + 16 * jb, pr);
+        for (int jb = w + 1; jb < 4; ++jb) {
+          tmem_st_32x32b_x16(tm + kColP + 16 * jb, hi);
+          tmem_st_32x32b_x16(tm + kColPLo + 16 * jb, hi);
+        }
       }
       tmem_st_wait();
       tc_fence_before_sync();
@@ -423,27 +464,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       first = exp_fast(first);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t a[32], b[32];
+        uint32_t a[32];
         tmem_ld_32x32b<32>(tm + kColS + 32 * h, a);
-        if (t.seg > 0) tmem_ld_32x32b<32>(tm + kColS0 + 32 * h, b);
         tmem_ld_wait();
         tmem_ld_fence_regs(a);
-        tmem_ld_fence_regs(b);
-        if (t.seg > 0) {
-          const float f0 = first * since;
 #pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            float p0 = 0.f, p1 = 0.f;
-            fma2(p0, p1, __uint_as_float(b[x]), __uint_as_float(b[x + 1]), f0, f0);
-            fma2(p0, p1, __uint_as_float(a[x]), __uint_as_float(a[x + 1]), first, first);
-            out[32 * h + x] = p0;
-            out[32 * h + x + 1] = p1;
-          }
-        } else {
-#pragma unroll
-          for (int x = 0; x < 32; x += 2)
-            mul2(out[32 * h + x], out[32 * h + x + 1], __uint_as_float(a[x]), __uint_as_float(a[x + 1]), first, first);
-        }
+        for (int x = 0; x < 32; x += 2)
+          mul2(out[32 * h + x], out[32 * h + x + 1], __uint_as_float(a[x]), __uint_as_float(a[x + 1]), first, first);
       }
 #pragma unroll
       for (int c = 0; c < kTcV / 8; ++c) {

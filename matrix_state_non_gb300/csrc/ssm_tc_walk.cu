@@ -3,12 +3,11 @@
 //     S' = tot S + sum_j (w_j k_j) v_j^T,  w_j = exp(l_end - l_j) D_j,
 // held transposed: D = v^T (w k) has value columns as rows and state rows as
 // columns, so a thread of the accumulator's 64 lanes has a value column's whole
-// row and writes it as the operand of the outputs, 16 bytes at a time.
+// row and leaves it in fp32, 16 bytes at a time, side by side with its neighbours.
 // v is exact in bf16; w k is split into three bf16 parts, side by side one
 // operand of 192 columns with an accumulator each, so that eight truncating
 // adds see a sum's full size.  The state itself is fp32 in registers.
-// B=2 heads=16 T=16384 64x64, shared q and k: 35 us (46 on mma.sync; whole scan
-// 96 and 106).  A tile takes 1900 cycles, in which the products (64 KB of
+// B=2 heads=16 T=16384 64x64, shared q and k: 38 us (46 on mma.sync).  A tile takes 1900 cycles, in which the products (64 KB of
 // operands) and the split (48 KB written) share the bandwidth of shared memory:
 // k through shared memory as well, 24 products of 64 columns in the place of 8,
 // or two groups of split warps on tiles in turn are 4 to 7 us slower each.
@@ -260,8 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < kTcK; ++k)
         S[k] = at.seg == 0 && A.H_0 != nullptr && in && k < A.K ? A.H_0[state + static_cast<int64_t>(k) * A.V] : 0.f;
       float decay = 1.f;  // since the segment's start
-      uint8_t* to = W.local + (at.head * W.nt + at.t0) * kTcStateBytes + tc_state_at(0, v);
-      for (int tt = at.t0; tt < at.t1; ++tt, ++u, to += kTcStateBytes) {
+      float4* to = W.local + (at.head * W.nt + at.t0) * kTcState + tc_piece_at(0, v);
+      for (int tt = at.t0; tt < at.t1; ++tt, ++u, to += kTcState) {
         const int slot = u & 1;
         const float* tot = W.tot + at.chain * W.nc + 2 * tt;
         const float t = tot[0] * tot[1];
@@ -269,10 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         decay *= t;
         if (own) {
 #pragma unroll
-          for (int k = 0; k < kTcK; k += 8)
-            *reinterpret_cast<uint4*>(to + tc_state_at(k, 0)) =
-                make_uint4(pack_bf16x2(S[k], S[k + 1]), pack_bf16x2(S[k + 2], S[k + 3]), pack_bf16x2(S[k + 4], S[k + 5]),
-                           pack_bf16x2(S[k + 6], S[k + 7]));
+          for (int k = 0; k < kTcK; k += 4) to[tc_piece_at(k, 0)] = make_float4(S[k], S[k + 1], S[k + 2], S[k + 3]);
         }
         ok = warp_wait(done(slot), (u >> 1) & 1, abort_flag, W.status, kWhereDone);
         if (!ok) break;
