@@ -90,14 +90,14 @@ __device__ __forceinline__ Source<T, kVec> source(const ConvArgs& A, int b, int 
           A.W};
 }
 
-// The channels' weights, right-aligned to kW taps (zero in front).  With W =
-// kW they are consecutive and come as a few 16-byte loads: 40 single loads
-// per thread cost as much as the strip's own rows.
+// The channels' weights.  They are consecutive and come as a few 16-byte loads
+// where they fill them: 40 single loads per thread cost as much as the strip's
+// own rows.
 template <typename T, int kVec, int kW>
 __device__ __forceinline__ void load_weights(const ConvArgs& A, int c, float (&w)[kW][kVec], float (&bias)[kVec]) {
-  const T* p = static_cast<const T*>(A.w) + static_cast<int64_t>(c) * A.W;
+  const T* p = static_cast<const T*>(A.w) + static_cast<int64_t>(c) * kW;
   constexpr int kPer = 16 / sizeof(T);
-  if (kVec * kW % kPer == 0 && A.W == kW) {
+  if constexpr (kVec * kW % kPer == 0) {
 #pragma unroll
     for (int i = 0; i < kVec * kW / kPer; ++i) {
       Row<T, kPer> r;
@@ -109,10 +109,7 @@ __device__ __forceinline__ void load_weights(const ConvArgs& A, int c, float (&w
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
 #pragma unroll
-      for (int j = 0; j < kW; ++j) {
-        const int k = j - (kW - A.W);
-        w[j][i] = k >= 0 ? to_f32(p[i * A.W + k]) : 0.f;
-      }
+      for (int j = 0; j < kW; ++j) w[j][i] = to_f32(p[i * kW + j]);
     }
   }
   Row<T, kVec> r;
@@ -358,7 +355,7 @@ __device__ __forceinline__ void backward_strip(const ConvArgs& A, int b, int c, 
 }
 
 template <typename T, int kVec, int kW>
-__global__ void __launch_bounds__(32 * kBwdWarps, backward_blocks(sizeof(T) == 2, kW == 8))
+__global__ void __launch_bounds__(32 * kBwdWarps, backward_blocks(sizeof(T) == 2, kW > 4))
     conv_backward_kernel(ConvArgs A, int blocks_c, int blocks_t, int strip) {
   __shared__ float red[kBwdWarps][kW + 1][32 * kVec];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -388,14 +385,14 @@ __global__ void __launch_bounds__(32 * kBwdWarps, backward_blocks(sizeof(T) == 2
   }
   __syncthreads();
   let_next();
-  // Partials are [block of steps][A.W taps, then the bias][C].
+  // Partials are [block of steps][kW taps, then the bias][C].
   for (int i = threadIdx.x; i < (kW + 1) * 32 * kVec; i += 32 * kBwdWarps) {
-    const int j = i / (32 * kVec) - (kW - A.W), x = i % (32 * kVec), cc = bc * 32 * kVec + x;
-    if (j < 0 || cc >= A.C) continue;
+    const int j = i / (32 * kVec), x = i % (32 * kVec), cc = bc * 32 * kVec + x;
+    if (cc >= A.C) continue;
     float s = 0.f;
 #pragma unroll
-    for (int v = 0; v < kBwdWarps; ++v) s += red[v][i / (32 * kVec)][x];
-    A.part[(static_cast<int64_t>(bt) * (A.W + 1) + j) * A.C + cc] = s;
+    for (int v = 0; v < kBwdWarps; ++v) s += red[v][j][x];
+    A.part[(static_cast<int64_t>(bt) * (kW + 1) + j) * A.C + cc] = s;
   }
 }
 
@@ -423,31 +420,22 @@ __global__ void __launch_bounds__(256) conv_sum_parts_kernel(const float* part, 
 }
 
 // One token: a thread takes kVec channels of one sequence.  A latency: 32
-// sequences of 1536 channels 2.4 us in a graph.
+// sequences of 1536 channels 2.1 us in a graph.
 template <typename T, int kVec, int kW>
 __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs A, T* state) {
   const int groups = A.C / kVec;
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
   if (i >= static_cast<int64_t>(A.B) * groups) return;
-  const int c = static_cast<int>(i % groups) * kVec, b = static_cast<int>(i / groups), W = A.W;
-  T* st = state + static_cast<int64_t>(b) * (W - 1) * A.C + c;
+  const int c = static_cast<int>(i % groups) * kVec, b = static_cast<int>(i / groups);
+  T* st = state + static_cast<int64_t>(b) * (kW - 1) * A.C + c;
   Row<T, kVec> r[kW], out;
   r[kW - 1].load(static_cast<const T*>(A.x) + b * A.x_stride + c);
 #pragma unroll
-  for (int j = 0; j < kW - 1; ++j) {
-    const int k = j - (kW - W);
-    if (k >= 0)
-      r[j].load(st + static_cast<int64_t>(k) * A.C);
-    else
-      r[j].zero();
-  }
+  for (int j = 0; j < kW - 1; ++j) r[j].load(st + static_cast<int64_t>(j) * A.C);
   float w[kW][kVec], bias[kVec];
   load_weights<T, kVec, kW>(A, c, w, bias);
 #pragma unroll
-  for (int j = 1; j < kW; ++j) {
-    const int k = j - 1 - (kW - W);
-    if (k >= 0) r[j].store(st + static_cast<int64_t>(k) * A.C);
-  }
+  for (int j = 1; j < kW; ++j) r[j].store(st + static_cast<int64_t>(j - 1) * A.C);
 #pragma unroll
   for (int e = 0; e < kVec; ++e) {
     float p = bias[e];
@@ -490,15 +478,21 @@ void step(const ConvArgs& a, void* state, cudaStream_t s) {
   conv_step_kernel<T, kVec, kW><<<static_cast<unsigned>((n + 127) / 128), 128, 0, s>>>(a, static_cast<T*>(state));
 }
 
-// Widths 1-4 run as 4 taps, 5-8 as 8 (those with fewer channels a thread: 8
-// taps of 8 channels spill).
-#define M2RNN_CONV(CALL, T, VEC, VEC8, ...) \
-  do {                                      \
-    if (a.W <= 4)                           \
-      CALL<T, VEC, 4>(__VA_ARGS__);         \
-    else                                    \
-      CALL<T, VEC8, 8>(__VA_ARGS__);        \
-  } while (0)
+// Every width has its own kernels: taps that are not there would be products
+// of zero with inputs outside the window, NaN where those are not finite.
+// Widths above 4 with fewer channels a thread (8 taps of 8 channels spill).
+#define M2RNN_CONV(CALL, T, VEC, VEC8, ...)                 \
+  switch (a.W) {                                            \
+    case 1: CALL<T, VEC, 1>(__VA_ARGS__); break;            \
+    case 2: CALL<T, VEC, 2>(__VA_ARGS__); break;            \
+    case 3: CALL<T, VEC, 3>(__VA_ARGS__); break;            \
+    case 4: CALL<T, VEC, 4>(__VA_ARGS__); break;            \
+    case 5: CALL<T, VEC8, 5>(__VA_ARGS__); break;           \
+    case 6: CALL<T, VEC8, 6>(__VA_ARGS__); break;           \
+    case 7: CALL<T, VEC8, 7>(__VA_ARGS__); break;           \
+    case 8: CALL<T, VEC8, 8>(__VA_ARGS__); break;           \
+    default: return cudaErrorInvalidValue;                  \
+  }
 
 }  // namespace
 
@@ -513,30 +507,34 @@ int conv_backward_parts(int64_t B, int64_t T, int64_t C) {
 
 cudaError_t launch_conv_forward(const ConvArgs& a, cudaStream_t s) {
   if (a.bf16) {
-    if (rows_of(a, 8))
-      M2RNN_CONV(forward, uint16_t, 8, 4, a, s);
-    else
-      M2RNN_CONV(forward, uint16_t, 1, 1, a, s);
+    if (rows_of(a, 8)) {
+      M2RNN_CONV(forward, uint16_t, 8, 4, a, s)
+    } else {
+      M2RNN_CONV(forward, uint16_t, 1, 1, a, s)
+    }
   } else {
-    if (rows_of(a, 4))
-      M2RNN_CONV(forward, float, 4, 4, a, s);
-    else
-      M2RNN_CONV(forward, float, 1, 1, a, s);
+    if (rows_of(a, 4)) {
+      M2RNN_CONV(forward, float, 4, 4, a, s)
+    } else {
+      M2RNN_CONV(forward, float, 1, 1, a, s)
+    }
   }
   return cudaGetLastError();
 }
 
 cudaError_t launch_conv_backward(const ConvArgs& a, cudaStream_t s) {
   if (a.bf16) {
-    if (rows_of(a, 2))
-      M2RNN_CONV(backward, uint16_t, 2, 1, a, s);
-    else
-      M2RNN_CONV(backward, uint16_t, 1, 1, a, s);
+    if (rows_of(a, 2)) {
+      M2RNN_CONV(backward, uint16_t, 2, 1, a, s)
+    } else {
+      M2RNN_CONV(backward, uint16_t, 1, 1, a, s)
+    }
   } else {
-    if (rows_of(a, 2))
-      M2RNN_CONV(backward, float, 2, 1, a, s);
-    else
-      M2RNN_CONV(backward, float, 1, 1, a, s);
+    if (rows_of(a, 2)) {
+      M2RNN_CONV(backward, float, 2, 1, a, s)
+    } else {
+      M2RNN_CONV(backward, float, 1, 1, a, s)
+    }
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -546,15 +544,17 @@ cudaError_t launch_conv_backward(const ConvArgs& a, cudaStream_t s) {
 
 cudaError_t launch_conv_step(void* state, const ConvArgs& a, cudaStream_t s) {
   if (a.bf16) {
-    if (rows_of(a, 8))
-      M2RNN_CONV(step, uint16_t, 8, 4, a, state, s);
-    else
-      M2RNN_CONV(step, uint16_t, 1, 1, a, state, s);
+    if (rows_of(a, 8)) {
+      M2RNN_CONV(step, uint16_t, 8, 4, a, state, s)
+    } else {
+      M2RNN_CONV(step, uint16_t, 1, 1, a, state, s)
+    }
   } else {
-    if (rows_of(a, 4))
-      M2RNN_CONV(step, float, 4, 4, a, state, s);
-    else
-      M2RNN_CONV(step, float, 1, 1, a, state, s);
+    if (rows_of(a, 4)) {
+      M2RNN_CONV(step, float, 4, 4, a, state, s)
+    } else {
+      M2RNN_CONV(step, float, 1, 1, a, state, s)
+    }
   }
   return cudaGetLastError();
 }
