@@ -642,9 +642,19 @@ def _rows(t, name: str, shape, inner: int, width: int, dtype, gpu: int):
 
 
 def _gpu(t) -> int:
+    """The tensor's GPU, which has to be the current one: the library's launches
+    go there."""
     gpu = t.get_device()
     if gpu < 0:
         raise ValueError(f"expected CUDA tensors, got one on {t.device}")
+    return _current(gpu)
+
+
+def _current(gpu: int) -> int:
+    import torch
+    if gpu != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{gpu}, the current device is cuda:{torch.cuda.current_device()}: "
+                         f"call under torch.cuda.device({gpu})")
     return gpu
 
 
@@ -873,6 +883,7 @@ def grad_plan(grads, out=None) -> GradPlan:
 def grad_norm(plan: GradPlan, *, norm=None, stream=None):
     """Global norm of the plan's tensors: a 0-dim fp32 tensor on the device."""
     import torch
+    _current(plan.gpu)
     if norm is None:
         norm = _alloc(plan.table, (), torch.float32, stream)
     st = load().m2rnn_grad_norm(plan.table.data_ptr(), plan.table.numel(), norm.data_ptr(), plan.workspace.data_ptr(),
@@ -885,6 +896,7 @@ def grad_clip(plan: GradPlan, max_norm: float, *, norm=None, stream=None):
     """Scales the plan's tensors by min(1, max_norm / (norm + 1e-6)) into its
     outputs.  Returns the norm before clipping, a 0-dim fp32 tensor."""
     import torch
+    _current(plan.gpu)
     if norm is None:
         norm = _alloc(plan.table, (), torch.float32, stream)
     st = load().m2rnn_grad_clip(plan.table.data_ptr(), plan.table.numel(), float(max_norm), norm.data_ptr(),
