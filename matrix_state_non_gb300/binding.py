@@ -687,9 +687,11 @@ def _scratch(workspace, nbytes: int, like, stream, what: str):
     import torch
     if nbytes == 0:
         raise M2RNNError(M2RNN_ERR_UNSUPPORTED, what)
-    if workspace is None or workspace.numel() < nbytes:
+    if workspace is None:
         return _alloc(like, (nbytes,), torch.uint8, stream)
-    return workspace
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on cuda:{like.get_device()}, is on {workspace.device}")
+    return workspace if workspace.numel() >= nbytes else _alloc(like, (nbytes,), torch.uint8, stream)
 
 
 def causal_conv(x, w, bias=None, *, x0=None, lengths=None, silu: bool = True, want_state: bool = False,
@@ -880,12 +882,21 @@ def grad_plan(grads, out=None) -> GradPlan:
     return GradPlan(grads, out)
 
 
+def _norm(plan, norm, stream):
+    """The one fp32 number that the calls write."""
+    import torch
+    if norm is None:
+        return _alloc(plan.table, (), torch.float32, stream)
+    if norm.dtype is not torch.float32 or norm.numel() != 1 or norm.get_device() != plan.gpu:
+        raise ValueError(f"norm: expected one torch.float32 on cuda:{plan.gpu}, got {norm.numel()} {norm.dtype} on "
+                         f"{norm.device}")
+    return norm
+
+
 def grad_norm(plan: GradPlan, *, norm=None, stream=None):
     """Global norm of the plan's tensors: a 0-dim fp32 tensor on the device."""
-    import torch
     _current(plan.gpu)
-    if norm is None:
-        norm = _alloc(plan.table, (), torch.float32, stream)
+    norm = _norm(plan, norm, stream)
     st = load().m2rnn_grad_norm(plan.table.data_ptr(), plan.table.numel(), norm.data_ptr(), plan.workspace.data_ptr(),
                                 plan.workspace.numel(), _on(plan.gpu, stream))
     _check(st, "m2rnn_grad_norm")
@@ -895,10 +906,8 @@ def grad_norm(plan: GradPlan, *, norm=None, stream=None):
 def grad_clip(plan: GradPlan, max_norm: float, *, norm=None, stream=None):
     """Scales the plan's tensors by min(1, max_norm / (norm + 1e-6)) into its
     outputs.  Returns the norm before clipping, a 0-dim fp32 tensor."""
-    import torch
     _current(plan.gpu)
-    if norm is None:
-        norm = _alloc(plan.table, (), torch.float32, stream)
+    norm = _norm(plan, norm, stream)
     st = load().m2rnn_grad_clip(plan.table.data_ptr(), plan.table.numel(), float(max_norm), norm.data_ptr(),
                                 plan.workspace.data_ptr(), plan.workspace.numel(), _on(plan.gpu, stream))
     _check(st, "m2rnn_grad_clip")

@@ -54,3 +54,40 @@ def test_tensors_of_another_than_the_current_gpu_are_refused(current):
                  lambda: m.grad_plan([x]), lambda: m.grad_norm(plan), lambda: m.grad_clip(plan, 1.0)):
         with pytest.raises(ValueError, match="current device is cuda:0"):
             call()
+
+
+@pytest.mark.parametrize("norm", [On((), gpu=-1), On((), torch.float64), On((), torch.bfloat16), On((0,)), On((2,)),
+                                  On((), gpu=1)])
+def test_norm_is_checked(current, norm):
+    plan = m.GradPlan.__new__(m.GradPlan)
+    plan.gpu, plan.table, plan.workspace, plan.stream = 0, On((64,), torch.uint8), On((8192,), torch.uint8), 0
+    for call in (lambda: m.grad_norm(plan, norm=norm), lambda: m.grad_clip(plan, 1.0, norm=norm)):
+        with pytest.raises(ValueError, match="norm"):
+            call()
+
+
+def test_workspaces_are_checked(monkeypatch):
+    """One on the host, on another GPU, or in pieces; one that is too small is replaced."""
+    b, made = torch.bfloat16, []
+    lib = type("Lib", (), dict(m2rnn_ssm_workspace_size=lambda *a: 1000, m2rnn_ssm_backward_workspace_size=lambda *a: 1000,
+                               m2rnn_causal_conv_backward_workspace_size=lambda *a: 1000))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(m, "load", lambda: lib)
+
+    def alloc(like, shape, dtype, stream):
+        made.append(On(shape if isinstance(shape, tuple) else (), dtype))
+        return made[-1]
+
+    monkeypatch.setattr(m, "_alloc", alloc)
+    q, v, dt, A = On((2, 9, 1, 8), b), On((2, 9, 2, 8), b), On((2, 9, 2), b), On((2,))
+    pieces = On((2000,), torch.uint8)
+    pieces.is_contiguous = lambda: False
+    for ws in (On((2000,), torch.uint8, -1), On((2000,), torch.uint8, 1), pieces):
+        for call in (lambda: m.ssm_scan(q, q, v, dt, A, workspace=ws),
+                     lambda: m.ssm_scan_backward(q, q, v, dt, A, v, workspace=ws),
+                     lambda: m.causal_conv_backward(On((2, 9, 8), b), On((8, 4), b), None, On((2, 9, 8)), workspace=ws)):
+            with pytest.raises(ValueError, match="workspace"):
+                call()
+    good = On((1000,), torch.uint8)
+    assert m._scratch(good, 1000, v, None, "") is good
+    assert m._scratch(On((999,), torch.uint8), 1000, v, None, "") is made[-1] and made[-1].shape == (1000,)
