@@ -871,6 +871,7 @@ class GradPlan:
         size = m2rnn_grad_plan_size(n, counts)
         host = torch.empty(size, dtype=torch.uint8)
         _check(m2rnn_grad_plan_build(n, ptrs, optrs, counts, codes, host.data_ptr(), size), "m2rnn_grad_plan_build")
+        self.stream = _on(self.gpu, None)
         self.table = host.to(grads[0].device)
         self.workspace = self.table.new_empty(m2rnn_grad_workspace_size())
         self.grads, self.outs = grads, outs
@@ -880,6 +881,16 @@ def grad_plan(grads, out=None) -> GradPlan:
     """Lists gradient tensors (contiguous, bf16 or fp32) for ``grad_clip``;
     ``out``: where the clipped ones go (None = in place)."""
     return GradPlan(grads, out)
+
+
+def _keep(plan, stream, handle):
+    """Tells the allocator that another stream than the plan's own uses its
+    buffers, which the caller does not see."""
+    import torch
+    if handle != plan.stream:
+        used = stream if stream is not None else torch.cuda.current_stream(plan.gpu)
+        plan.table.record_stream(used)
+        plan.workspace.record_stream(used)
 
 
 def _norm(plan, norm, stream):
@@ -897,9 +908,11 @@ def grad_norm(plan: GradPlan, *, norm=None, stream=None):
     """Global norm of the plan's tensors: a 0-dim fp32 tensor on the device."""
     _current(plan.gpu)
     norm = _norm(plan, norm, stream)
+    handle = _on(plan.gpu, stream)
     st = load().m2rnn_grad_norm(plan.table.data_ptr(), plan.table.numel(), norm.data_ptr(), plan.workspace.data_ptr(),
-                                plan.workspace.numel(), _on(plan.gpu, stream))
+                                plan.workspace.numel(), handle)
     _check(st, "m2rnn_grad_norm")
+    _keep(plan, stream, handle)
     return norm
 
 
@@ -908,7 +921,9 @@ def grad_clip(plan: GradPlan, max_norm: float, *, norm=None, stream=None):
     outputs.  Returns the norm before clipping, a 0-dim fp32 tensor."""
     _current(plan.gpu)
     norm = _norm(plan, norm, stream)
+    handle = _on(plan.gpu, stream)
     st = load().m2rnn_grad_clip(plan.table.data_ptr(), plan.table.numel(), float(max_norm), norm.data_ptr(),
-                                plan.workspace.data_ptr(), plan.workspace.numel(), _on(plan.gpu, stream))
+                                plan.workspace.data_ptr(), plan.workspace.numel(), handle)
     _check(st, "m2rnn_grad_clip")
+    _keep(plan, stream, handle)
     return norm

@@ -91,3 +91,57 @@ def test_workspaces_are_checked(monkeypatch):
     good = On((1000,), torch.uint8)
     assert m._scratch(good, 1000, v, None, "") is good
     assert m._scratch(On((999,), torch.uint8), 1000, v, None, "") is made[-1] and made[-1].shape == (1000,)
+
+
+class Stream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+@pytest.mark.parametrize("call", [m.grad_norm, lambda plan, **kw: m.grad_clip(plan, 1.0, **kw)])
+def test_a_plan_used_on_another_stream_stays_until_that_stream_is_done(monkeypatch, call):
+    """The table and the workspace belong to the stream that the plan was made
+    on; where another stream uses them, the allocator is told."""
+    lib = type("Lib", (), dict(m2rnn_grad_norm=lambda *a: 0, m2rnn_grad_clip=lambda *a: 0))
+    here = [Stream(7)]
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: here[0])
+    monkeypatch.setattr(m, "load", lambda: lib)
+    monkeypatch.setattr(m, "_on", lambda gpu, stream: (stream or here[0]).cuda_stream)
+
+    def plan():
+        p = m.GradPlan.__new__(m.GradPlan)
+        p.gpu, p.table, p.workspace, p.stream = 0, On((64,), torch.uint8), On((8192,), torch.uint8), 7
+        return p
+
+    norm, p = On(()), plan()
+    call(p, norm=norm)
+    call(p, norm=norm, stream=here[0])
+    assert p.table.streams == [] and p.workspace.streams == []
+    side = Stream(9)
+    call(p, norm=norm, stream=side)
+    assert p.table.streams == [side] and p.workspace.streams == [side]
+    p, here[0] = plan(), side
+    call(p, norm=norm)
+    assert p.table.streams == [side] and p.workspace.streams == [side]
+
+
+@pytest.mark.gpu
+def test_a_dropped_plan_is_not_handed_out_while_a_side_stream_reads_it():
+    grads = [torch.randn(70001, device="cuda"), torch.randn(30000, device="cuda").bfloat16()]
+    want = float(m.grad_norm(m.grad_plan(grads)))
+    side = torch.cuda.Stream()
+    for use in (lambda p: m.grad_norm(p, stream=side), lambda p: m.grad_clip(p, 1e9, stream=side)):
+        plan = m.grad_plan(grads)
+        size, at = plan.table.numel(), {plan.table.data_ptr(), plan.workspace.data_ptr()}
+        work = plan.workspace.numel()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)  # about a tenth of a second
+        norm = use(plan)
+        del plan
+        other = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in (size, work) for _ in range(4)]
+        busy = not side.query()
+        assert not busy or not at & {t.data_ptr() for t in other}
+        side.synchronize()
+        assert float(norm) == want
