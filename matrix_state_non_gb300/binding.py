@@ -282,7 +282,12 @@ def m2rnn_sync_status(workspace, stream):
 # torch conveniences
 # ---------------------------------------------------------------------------
 def _ptr(t) -> Optional[int]:
-    return None if t is None else t.data_ptr()
+    """Address of a dense tensor (the library takes no strides here)."""
+    if t is None:
+        return None
+    if not t.is_contiguous():
+        raise ValueError(f"expected a contiguous tensor, got strides {t.stride()} for {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _dtype_code(t) -> int:
