@@ -167,6 +167,23 @@ def test_dA_is_not_lost_to_cancellation(dtype):
     assert bool((err <= 16 * 2.0 ** -21 * size).all()), float((err / size).max())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_dA_needs_its_running_sums_in_two_floats(dtype):
+    """At 6000 steps a head.  A term D_t g_t is off by the roundings of the row
+    products in it, 64 of 2^-24 that add up as their square root: 2^-21 of its
+    size; independent over the terms, so dA is off by 2^-21 of the terms' root
+    sum of squares, in the mean over the heads; 4 of it are allowed.  (Running
+    sums over a chunk in single floats leave 6 to 8.)"""
+    from matrix_state_non_gb300 import binding as m
+    d = ssm_inputs(4, 1500, 8, 8, 64, 64, dtype, seed=3, h0=False)
+    g = ssm_dev(d, dtype)
+    a, kw = args(g)
+    r = m.ssm_scan_backward(*a, g["dy"], **kw)
+    want = ref.scan(g)
+    off = (r["dA"].double() - want["dA"]) / want["g"].square().sum((0, 1)).sqrt()
+    assert float(off.square().mean().sqrt()) <= 4 * 2.0 ** -21, float(off.square().mean().sqrt()) * 2 ** 21
+
+
 def test_nan_stays_behind_its_step_in_tiles():
     """A NaN in q touches its own step, one in k or dt the steps from its own
     on; other heads and sequences, and the steps before, stay as they were."""
