@@ -19,6 +19,28 @@ namespace {
 struct Yes { static constexpr bool value = true; };
 struct No { static constexpr bool value = false; };
 
+// s = 1 / (1 + e^-x) by the hardware's 2^x and reciprocal, and tail = 1 - s.
+// The rounding of the exponent -x log2 e counts x times: 2^-18 of the result at
+// |x| = 80.  bf16 outputs are 2^9 times coarser; for fp32 the rounding and the
+// rest of log2 e go into the power's first-order term, which leaves a few units
+// at every x (the exact functions cost a quarter of the forward's time), and
+// the tail of a large x is e^-x s, not what 1 - s leaves of it.
+template <typename T>
+__device__ __forceinline__ float sigmoid(float x, float* tail = nullptr) {
+  if constexpr (sizeof(T) == 2) {
+    const float s = sigmoid_fast(x);
+    if (tail != nullptr) *tail = 1.f - s;
+    return s;
+  } else {
+    constexpr float kHi = -1.44269504f, kLo = -1.44269504088896341 - static_cast<double>(kHi);  // -log2 e
+    const float c = fminf(fmaxf(x, -88.f), 88.f);  // behind them s is 0 and 1, and nothing below leaves the fp32 range
+    const float t = c * kHi, r = fmaf(c, kLo, fmaf(c, kHi, -t)), p = ex2_fast(t);
+    const float e = fmaf(p, 0.693147181f * r, p), s = rcp_fast(1.f + e);
+    if (tail != nullptr) *tail = x > 0.f ? e * s : 1.f - s;
+    return s;
+  }
+}
+
 // kVec consecutive elements of a row: one load or store of kVec elements
 // (16 or 8 bytes on the vector paths).
 template <typename T, int kVec>
@@ -176,7 +198,7 @@ __device__ __forceinline__ void forward_strip(const ConvArgs& A, const Source<T,
       fma_row<kVec>(p, w[kW - 1], h[kW - 1]);
       if (A.silu) {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) p[e] *= sigmoid_fast(p[e]);
+        for (int e = 0; e < kVec; ++e) p[e] *= sigmoid<T>(p[e]);
       }
       out.set(p);
       if (kEdge && t + u >= len) out.zero();
@@ -313,8 +335,9 @@ __device__ __forceinline__ void backward_strip(const ConvArgs& A, int b, int c, 
       if (A.silu) {
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-          const float sg = sigmoid_fast(p[e]);
-          x[e] *= fmaf(p[e] * sg, 1.f - sg, sg);
+          float tail;
+          const float sg = sigmoid<T>(p[e], &tail);
+          x[e] *= fmaf(p[e] * sg, tail, sg);
         }
       }
 #pragma unroll
@@ -441,7 +464,7 @@ __global__ void __launch_bounds__(128) conv_step_kernel(ConvArgs A, T* state) {
     float p = bias[e];
 #pragma unroll
     for (int j = 0; j < kW; ++j) p = fmaf(w[j][e], to_f32(r[j].e[e]), p);
-    out.e[e] = from_f32<T>(A.silu ? p * sigmoid_fast(p) : p);
+    out.e[e] = from_f32<T>(A.silu ? p * sigmoid<T>(p) : p);
   }
   out.store(static_cast<T*>(A.y) + static_cast<int64_t>(b) * A.C + c);
 }
