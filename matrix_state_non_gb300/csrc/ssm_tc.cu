@@ -103,9 +103,6 @@ static_assert(kSmem <= 227 * 1024, "shared memory");
 // Tensor-memory columns of a slot.
 constexpr uint32_t kColP = 0, kColPV = 64, kColS = 128, kColPLo = 192, kSlot = 256;
 
-constexpr uint32_t kWhereFull = 401, kWhereP = 402, kWhereScores = 403, kWhereOut = 404, kWhereEmpty = 405,
-                   kWhereDrain = 406;
-
 // The tiles of a block in order: tile tt of (chain, slice) `head`, every gridDim.x-th of them, heads side by side.
 // Stepping and `live` go without divisions where there are no lengths: the warps ask for every tile of the block.
 struct TileWalk {
@@ -234,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t.seg > 0) before[i][h] = z[x + h * kTcV];
         }
       }
-      if (u >= kStages && !warp_wait(empty(s), (u / kStages - 1) & 1, abort_flag, W.status, kWhereEmpty)) {
+      if (u >= kStages && !warp_wait(empty(s), (u / kStages - 1) & 1, abort_flag, W.status, kWhereOutEmpty)) {
         ok = false;
         break;
       }
@@ -292,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok)  // the copies in flight land before the block ends
       for (int x = max(0, u - kStages); x < u; ++x)
-        mbar_wait_timed(full(x % kStages), (x / kStages) & 1, nullptr, kWhereDrain);
+        mbar_wait_timed(full(x % kStages), (x / kStages) & 1, nullptr, kWhereOutDrain);
   } else if (warp == kMmaWarp) {
     // ---------------- products ----------------
     constexpr uint32_t kIdQK = idesc_bf16_f32(128, kTile, false, false), kIdS = idesc_bf16_f32(128, kTcV, false, false),
@@ -354,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if ((++spins & 255u) == 0u) {  // bounded, as every wait
         bool stop = *abort_flag != 0;
         if (!stop && global_timer_ns() - since > kWaitLimitNs) {
-          if (lane == 0) report_device_error(W.status, kStatusTimeout, kWhereP);
+          if (lane == 0) report_device_error(W.status, kStatusTimeout, kWhereOutP);
           *abort_flag = 1;
           stop = true;
         }
@@ -362,8 +359,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (at.there() || o < s) {  // given up: the products in flight end before their memory is freed
-      for (int x = max(0, s - 2); x < s; ++x) mbar_wait_timed(scores(x & 1), (x >> 1) & 1, nullptr, kWhereDrain);
-      for (int x = max(0, o - 2); x < o; ++x) mbar_wait_timed(ofull(x & 1), (x >> 1) & 1, nullptr, kWhereDrain);
+      for (int x = max(0, s - 2); x < s; ++x) mbar_wait_timed(scores(x & 1), (x >> 1) & 1, nullptr, kWhereOutDrain);
+      for (int x = max(0, o - 2); x < o; ++x) mbar_wait_timed(ofull(x & 1), (x >> 1) & 1, nullptr, kWhereOutDrain);
     }
   } else {
     // ---------------- outputs: thread = row of the tile ----------------
@@ -390,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tm = tmem + slot * kSlot + lanes, st = base + s * kStage;
       const uint8_t* stp = smem + s * kStage;
       // The stage (decays, v) and then the scores.
-      if (!warp_wait(full(s), (v / kStages) & 1, abort_flag, W.status, kWhereFull)) break;
+      if (!warp_wait(full(s), (v / kStages) & 1, abort_flag, W.status, kWhereOutFull)) break;
       const float* dec = reinterpret_cast<const float*>(stp + kOffD);
       constexpr int kHalf = kTileDecayCopied / 4;
       auto decays = [&](int block) { return dec + (block >> 1) * kHalf + (block & 1) * 32; };  // rel; cf 64, D 128, lo 192 behind
@@ -398,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float T[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) T[x] = dec[(x >> 1) * kHalf + 4 * kChunk + (x & 1)];
-      if (!warp_wait(scores(slot), (v >> 1) & 1, abort_flag, W.status, kWhereScores)) break;
+      if (!warp_wait(scores(slot), (v >> 1) & 1, abort_flag, W.status, kWhereOutScores)) break;
       tc_fence_after_sync();
       // Blocks of 32 steps before the warp's own, the next block's scores on their way.  (A loop, not unrolled: the
       // warps are in different phases, and their code has to fit the instruction cache together.)
@@ -480,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int e = 0; e < 4; ++e)
           fma2(out[8 * c + 2 * e], out[8 * c + 2 * e + 1], bf16lo(x[e]), bf16hi(x[e]), bf16lo(z[e]), bf16hi(z[e]));
       }
-      if (!warp_wait(ofull(slot), (v >> 1) & 1, abort_flag, W.status, kWhereOut)) break;
+      if (!warp_wait(ofull(slot), (v >> 1) & 1, abort_flag, W.status, kWhereOutDone)) break;
       tc_fence_after_sync();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {

@@ -37,9 +37,6 @@ constexpr int kSmem = kOffBar + 256 + 1024;  // 1024: alignment
 static_assert(kSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t kSlot = 3 * kTcK;  // tensor-memory columns: an accumulator for each part
 
-constexpr uint32_t kWhereFull = 411, kWhereSplit = 412, kWhereDone = 413, kWhereEmpty = 414, kWhereFree = 415,
-                   kWhereDrain = 416;
-
 // Item `id`: a (chain, slice) head's segment and its tiles with steps in them.
 struct WalkPlace {
   int b, n, gq, slice, v0, width, len, seg, t0, t1;
@@ -112,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const WalkPlace at = walk_place(W, id);
       for (int tt = at.t0; tt < at.t1; ++tt, ++u) {
         const int s = u % kStages, t0 = tt * kTile;
-        if (u >= kStages && !warp_wait(empty(s), (u / kStages - 1) & 1, abort_flag, W.status, kWhereEmpty)) {
+        if (u >= kStages && !warp_wait(empty(s), (u / kStages - 1) & 1, abort_flag, W.status, kWhereWalkEmpty)) {
           ok = false;
           break;
         }
@@ -139,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok)  // the copies in flight land before the block ends
       for (int x = max(0, u - kStages); x < u; ++x)
-        mbar_wait_timed(full(x % kStages), (x / kStages) & 1, nullptr, kWhereDrain);
+        mbar_wait_timed(full(x % kStages), (x / kStages) & 1, nullptr, kWhereWalkDrain);
   } else if (warp == kMmaWarp) {
     // ---------------- products ----------------
     constexpr uint32_t kId = idesc_bf16_f32(64, 3 * kTcK, true, true);
@@ -149,9 +146,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const WalkPlace at = walk_place(W, id);
       for (int tt = at.t0; tt < at.t1; ++tt, ++u) {
         const int s = u % kStages, slot = u & 1;
-        ok = warp_wait(full(s), (u / kStages) & 1, abort_flag, W.status, kWhereFull) &&
-             (u < 2 || warp_wait(tfree(slot), ((u >> 1) - 1) & 1, abort_flag, W.status, kWhereFree)) &&
-             warp_wait(split(s), (u / kStages) & 1, abort_flag, W.status, kWhereSplit);
+        ok = warp_wait(full(s), (u / kStages) & 1, abort_flag, W.status, kWhereWalkFull) &&
+             (u < 2 || warp_wait(tfree(slot), ((u >> 1) - 1) & 1, abort_flag, W.status, kWhereWalkFree)) &&
+             warp_wait(split(s), (u / kStages) & 1, abort_flag, W.status, kWhereWalkSplit);
         if (!ok) break;
         if (elect_one()) {
           tc_fence_after_sync();
@@ -166,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok)  // the products in flight end before their memory is freed
-      for (int x = max(0, u - 2); x < u; ++x) mbar_wait_timed(done(x & 1), (x >> 1) & 1, nullptr, kWhereDrain);
+      for (int x = max(0, u - 2); x < u; ++x) mbar_wait_timed(done(x & 1), (x >> 1) & 1, nullptr, kWhereWalkDrain);
   } else if (warp >= kState / 32) {
     // ---------------- split ----------------
     const int q = tid - kState, piece = q & 7;
@@ -225,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       there = find();
       if (there) load();
-      if (u >= kStages && !warp_wait(empty(s), (u / kStages - 1) & 1, abort_flag, W.status, kWhereEmpty)) break;
+      if (u >= kStages && !warp_wait(empty(s), (u / kStages - 1) & 1, abort_flag, W.status, kWhereWalkEmpty)) break;
       const uint32_t sk = base + s * kStage + kOffK;
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
@@ -270,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < kTcK; k += 4) to[tc_piece_at(k, 0)] = make_float4(S[k], S[k + 1], S[k + 2], S[k + 3]);
         }
-        ok = warp_wait(done(slot), (u >> 1) & 1, abort_flag, W.status, kWhereDone);
+        ok = warp_wait(done(slot), (u >> 1) & 1, abort_flag, W.status, kWhereWalkDone);
         if (!ok) break;
         tc_fence_after_sync();
         const uint32_t tm = tmem + slot * kSlot + lanes;

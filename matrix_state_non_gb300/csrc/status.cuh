@@ -32,6 +32,11 @@ constexpr uint32_t kWhereWRange = 301;
 // takes q as an fp16 operand (the V = 64 and V = 16 warp-MMA forwards with
 // readout warps).
 constexpr uint32_t kWhereQRange = 302;
+// The selective state space scan on tcgen05: its outputs, its walk over the states.
+constexpr uint32_t kWhereOutFull = 401, kWhereOutP = 402, kWhereOutScores = 403, kWhereOutDone = 404,
+                   kWhereOutEmpty = 405, kWhereOutDrain = 406;
+constexpr uint32_t kWhereWalkFull = 411, kWhereWalkSplit = 412, kWhereWalkDone = 413, kWhereWalkEmpty = 414,
+                   kWhereWalkFree = 415, kWhereWalkDrain = 416;
 
 __device__ __forceinline__ void report_device_error(StatusBlock* s, unsigned int code,
                                                     uint32_t where) {
