@@ -373,9 +373,9 @@ int m2rnn_causal_conv_step(void* state, const void* x, int64_t x_stride, const v
  *   A [N] fp32 (negative for a decaying state); dt_bias [N] fp32 (may be
  *   NULL); H_0 [B,N,K,V] fp32 (may be NULL = zero); K, V in [1, 128].
  *   out: y [B,T,N,V] in `dtype`; H_T [B,N,K,V] fp32 (may be NULL; may be H_0).
- * A step whose v is not finite may also leave non-finite y at earlier steps
- * of the same 64 steps (128 where tiles of 128 are used: bf16, 32 < K <= 64,
- * V > 32, long sequences), counted from the sequence's start.
+ * A value that is not finite reaches y from its own step on and no earlier
+ * one; one of v stays in its own column.  y is the fp32 result rounded once to
+ * `dtype`.
  */
 size_t m2rnn_ssm_workspace_size(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V,
                                 m2rnn_dtype dtype);
@@ -391,7 +391,10 @@ int m2rnn_ssm_scan(const void* q, int64_t q_stride, const void* k, int64_t k_str
  *   out, all fp32: dq, dk [B,T,G,K] (summed over the heads that share them),
  *   dv [B,T,N,V], ddt [B,T,N], dA [N], ddt_bias [N] (may be NULL), dw_r [N,V]
  *   (may be NULL), dH_0 [B,N,K,V] (may be NULL; may be dH_T).
- * Sums in a fixed order: results are bitwise reproducible.
+ * Sums in a fixed order: results are bitwise reproducible.  A value of an input
+ * that is not finite may also leave gradients that are not finite at other steps
+ * of its own 64 (fp32: 32), counted from the sequence's start, than those that
+ * depend on it.
  */
 size_t m2rnn_ssm_backward_workspace_size(int64_t B, int64_t T, int64_t N, int64_t G, int64_t K, int64_t V,
                                          m2rnn_dtype dtype);

@@ -141,6 +141,9 @@ __device__ __forceinline__ void st_shared_b32(uint32_t addr, uint32_t v) {
 // Explicit shared-space loads and stores for the step loops (the inputs sit
 // in shared memory behind computed offsets; these keep every access a plain
 // shared-memory instruction).
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
+  asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
   unsigned short v;
   asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");

@@ -84,13 +84,18 @@ __device__ __forceinline__ float decay(const Decays<L>& d, int i, int j) {
   return expf((d.hi[i] - d.hi[j]) + (d.lo[i] - d.lo[j]));
 }
 
-// Rows of a head into a tile, zero behind `live` rows and in the padding.
-__device__ void load_rows(const float* x, int64_t stride, int width, int rows, int live, float* dst) {
+// Rows of a head into a tile, zero behind `live` rows and in the padding.  True where the thread met a value that is
+// not finite.
+__device__ bool load_rows(const float* x, int64_t stride, int width, int rows, int live, float* dst) {
   const int ld = pitch(width);
+  bool bad = false;
   for (int e = threadIdx.x; e < rows * ld; e += kThreads) {
     const int i = e / ld, j = e - i * ld;
-    dst[e] = i < live && j < width ? x[i * stride + j] : 0.f;
+    const float v = i < live && j < width ? x[i * stride + j] : 0.f;
+    bad |= !isfinite(v);
+    dst[e] = v;
   }
+  return bad;
 }
 
 __device__ __forceinline__ float4 ld4(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -290,6 +295,7 @@ __global__ void __launch_bounds__(kThreads) ssm_chunk_out_kernel(SsmArgs A, cons
   constexpr int L = kFwd;
   extern __shared__ __align__(16) float sm[];
   __shared__ Decays<L> dc;
+  __shared__ int s_from[128];  // the first step at which a value column is not finite
   const Place p = place<L>(A, nc);
   const int K = A.K, V = A.V, lk = pitch(K), lv = pitch(V);
   float *sq = sm, *sk = sq + L * lk, *sv = sk + L * lk, *P = sv + L * lv, *sS = P + L * pitch(L);
@@ -302,9 +308,23 @@ __global__ void __launch_bounds__(kThreads) ssm_chunk_out_kernel(SsmArgs A, cons
   load_decays<L>(A, p.b, p.n, p.t0, p.len, dc);
   load_rows(q_rows(A, p), A.q_stride, K, L, p.live, sq);
   load_rows(k_rows(A, p), A.k_stride, K, L, p.live, sk);
-  load_rows(v_rows(A, p), A.v_stride, V, L, p.live, sv);
+  const bool bad = load_rows(v_rows(A, p), A.v_stride, V, L, p.live, sv);
   load_rows(states + static_cast<int64_t>(blockIdx.x) * K * V, V, V, (K + 3) / 4 * 4, K, sS);
-  __syncthreads();
+  // Values that are not finite make their column NaN from their step on; the product with the scores, in which a later
+  // step's zero score would make NaN of them for the steps before, takes zeros in their place.
+  const bool spoilt = __syncthreads_or(bad);
+  if (spoilt) {
+    for (int c = threadIdx.x; c < V; c += kThreads) {
+      int from = L;
+      for (int j = L - 1; j >= 0; --j) {
+        if (isfinite(sv[j * lv + c])) continue;
+        from = j;
+        sv[j * lv + c] = 0.f;
+      }
+      s_from[c] = from;
+    }
+    __syncthreads();
+  }
   scores<L>(sq, sk, lk, K, P, [&](int i, int j) { return decay(dc, i, j) * dc.D[j]; });
   __syncthreads();
   // The rows of y twice: q S, kept in the q tile's place by the same thread, then the scores times v.
@@ -324,6 +344,7 @@ __global__ void __launch_bounds__(kThreads) ssm_chunk_out_kernel(SsmArgs A, cons
       const int c = col_nn(c0, cg, e);
       r[e] = x[e] + oo[e];
       if (wr && c < V) r[e] = fmaf(wr[c], vv[e], r[e]);
+      if (spoilt && c < V && i >= s_from[c]) r[e] = __int_as_float(0x7FFFFFFF);
       if (i >= p.live) r[e] = 0.f;
     }
     float* at = y + i * stride + 4 * c0;

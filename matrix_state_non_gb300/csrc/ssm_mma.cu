@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(kThreads, OutShape<KP, VS>::kBlocks) ssm_out_k
   static_assert(VS <= KP, "outputs pass through the q tile");
   constexpr int kKt = KP / 16;
   extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int s_from[VS];  // the first step at which a value column is not finite
   wait_previous();
   const SsmArgs& A = W.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
@@ -435,7 +436,22 @@ __global__ void __launch_bounds__(kThreads, OutShape<KP, VS>::kBlocks) ssm_out_k
   for (int e = tid; e < VS; e += kThreads)
     s_wr[e] = A.w_r != nullptr && e < width ? to_f32(static_cast<const uint16_t*>(A.w_r)[n * V + v0 + e]) : 0.f;
   cp_async_wait<0>();
-  __syncthreads();
+  // Values that are not finite make their column NaN from their step on; the products, in which a later step's zero
+  // score would make NaN of them for the steps before, take zeros in their place.
+  const bool spoilt = __syncthreads_or(lv.copied_not_finite(sV));
+  if (spoilt) {
+    for (int col = tid; col < VS; col += kThreads) {
+      int from = kChunk;
+      for (int j = kChunk - 1; j >= 0; --j) {
+        const uint32_t at = sV + j * Tile<VS>::kPitch + col * 2;
+        if ((not_finite(ld_shared_u16(at)) & kNotFinite) == 0u) continue;
+        from = j;
+        st_shared_u16(at, 0);
+      }
+      s_from[col] = from;
+    }
+    __syncthreads();
+  }
 
   uint32_t qf[kKt][4];
 #pragma unroll
@@ -512,8 +528,12 @@ __global__ void __launch_bounds__(kThreads, OutShape<KP, VS>::kBlocks) ssm_out_k
       const int col = 8 * nt + 2 * q4;
       const uint32_t vv = ld_shared_b32(sV + i * Tile<VS>::kPitch + col * 2);
       const float2 wr = *reinterpret_cast<const float2*>(&s_wr[col]);
-      st_shared_b32(sQ + i * Tile<KP>::kPitch + col * 2,
-                    pack_bf16x2(fmaf(wr.x, bf16lo(vv), O[nt][2 * h]), fmaf(wr.y, bf16hi(vv), O[nt][2 * h + 1])));
+      float y0 = fmaf(wr.x, bf16lo(vv), O[nt][2 * h]), y1 = fmaf(wr.y, bf16hi(vv), O[nt][2 * h + 1]);
+      if (spoilt) {
+        if (i >= s_from[col]) y0 = __int_as_float(0x7FFFFFFF);
+        if (i >= s_from[col + 1]) y1 = __int_as_float(0x7FFFFFFF);
+      }
+      st_shared_b32(sQ + i * Tile<KP>::kPitch + col * 2, pack_bf16x2(y0, y1));
     }
   }
   __syncwarp();

@@ -28,6 +28,10 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
+// Whether a pair of bf16 values holds one that is not finite: bit 15 or 31 of the result, OR-ed over many.
+constexpr uint32_t kNotFinite = 0x80008000u;
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) { return (x & 0x7F807F80u) + 0x00800080u; }
+
 // Copies the 64 rows of a chunk of one head into a tile, chunk after chunk:
 // `width` columns are there, steps behind `len` and columns behind `width`
 // become zero.  vec: rows on 16-byte boundaries and width a multiple of 8
@@ -63,9 +67,27 @@ struct TileLoader {
       for (int e = threadIdx.x; e < kChunk * kCols; e += kThreads) {
         const int r = e / kCols, c = e % kCols;
         const uint16_t x = t0 + r < len && c < width ? p[static_cast<int64_t>(t0 + r) * stride + c] : uint16_t(0);
-        asm volatile("st.shared.u16 [%0], %1;" ::"r"(tile + r * Tile<kCols>::kPitch + c * 2), "h"(x) : "memory");
+        st_shared_u16(tile + r * Tile<kCols>::kPitch + c * 2, x);
       }
     }
+  }
+
+  // Whether one of the values that this thread has copied (and waited for) is not finite.
+  __device__ __forceinline__ bool copied_not_finite(uint32_t tile) const {
+    uint32_t any = 0u;
+    if (vec) {
+      const uint32_t at = tile + threadIdx.x / kPer * Tile<kCols>::kPitch + threadIdx.x % kPer * 16;
+#pragma unroll
+      for (int i = 0; i < kChunk / kStep; ++i) {
+        const uint4 x = ld_shared_v4(at + i * kStep * Tile<kCols>::kPitch);
+        any |= not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w);
+      }
+    } else {
+#pragma unroll 4
+      for (int e = threadIdx.x; e < kChunk * kCols; e += kThreads)
+        any |= not_finite(ld_shared_u16(tile + e / kCols * Tile<kCols>::kPitch + e % kCols * 2));
+    }
+    return (any & kNotFinite) != 0u;
   }
 };
 

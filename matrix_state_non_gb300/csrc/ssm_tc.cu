@@ -154,6 +154,40 @@ __device__ __forceinline__ TilePlace tile_place(const TileWalk& at) {
   return p;
 }
 
+// A value of v that is not finite times the zero scores of the steps before it is NaN: those rows of P V are summed
+// again, over their own steps alone, column by column.  For the rows of one warp (row i of the tile at yr, its
+// tensor-memory lanes at tm), whose y has been staged; rows that are not finite by themselves come out as they were.
+// (A tile whose state is not finite already is not summed again: nothing would come of it.)
+__device__ __noinline__ void mend_columns(uint32_t st, uint32_t yr, uint32_t tm, int w, int i, bool in, float first) {
+  for (int c = 0; c < kTcV; ++c) {
+    bool hit = in && (not_finite(ld_shared_u16(yr + 2 * c)) & kNotFinite) != 0u;
+    if (!__any_sync(0xffffffffu, hit)) continue;
+    uint32_t s[2];
+    tmem_ld_32x32b<2>(tm + kColS + (c & ~1), s);
+    tmem_ld_wait();
+    tmem_ld_fence_regs(s);
+    auto v = [&](int j) { return bf16_bits_to_f32(ld_shared_u16(st + kOffV + piece_at(j, c >> 3) + (c & 7) * 2)); };
+    float y = fmaf(bf16_bits_to_f32(ld_shared_u16(st + kOffWr + c * 2)), v(i), first * __uint_as_float(s[c & 1]));
+    hit = hit && isfinite(y);
+    if (!__any_sync(0xffffffffu, hit)) continue;
+    for (int jb = 0; jb <= w; ++jb) {
+      uint32_t hi[16], lo[16];
+      tmem_ld_32x32b<16>(tm + kColP + 16 * jb, hi);
+      tmem_ld_32x32b<16>(tm + kColPLo + 16 * jb, lo);
+      tmem_ld_wait();
+      tmem_ld_fence_regs(hi);
+      tmem_ld_fence_regs(lo);
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const int j = 32 * jb + 2 * x;
+        if (j <= i) y = fmaf(bf16lo(hi[x]) + bf16lo(lo[x]), v(j), y);
+        if (j + 1 <= i) y = fmaf(bf16hi(hi[x]) + bf16hi(lo[x]), v(j + 1), y);
+      }
+    }
+    if (hit) st_shared_u16(yr + 2 * c, static_cast<uint16_t>(pack_bf16x2(y, 0.f) & 0xFFFFu));
+  }
+}
+
 __device__ __forceinline__ uint64_t desc_state(uint32_t addr) { return smem_desc_noswizzle(addr, kTcV * 16, 128); }
 
 __global__ void __launch_bounds__(kThreads, 1) 
@@ -488,11 +522,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int x = 0; x < 32; ++x) out[32 * h + x] += __uint_as_float(a[x]);
       }
-      tc_fence_before_sync();
-      mbar_arrive(tfree(slot));
+      const bool in = t.t0 + i < t.len;
+      float zero[2] = {0.f, 0.f};  // NaN where one of the row's values is not finite
+#pragma unroll
+      for (int x = 0; x < kTcV; x += 2) fma2(zero[0], zero[1], out[x], out[x + 1], 0.f, 0.f);
+      const bool spoilt = __any_sync(0xffffffffu, in && !(zero[0] + zero[1] == 0.f));
+      if (!spoilt) {
+        tc_fence_before_sync();
+        mbar_arrive(tfree(slot));
+      }
       // Rows to shared memory (over Q and K, which the products are done with), then out in whole lines.
       const uint32_t yr = st + i * kYPitch;
-      const bool in = t.t0 + i < t.len;
 #pragma unroll
       for (int c = 0; c < kTcV / 8; ++c) {
         const uint32_t x0 = pack_bf16x2(out[8 * c], out[8 * c + 1]), x1 = pack_bf16x2(out[8 * c + 2], out[8 * c + 3]),
@@ -500,6 +540,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(yr + 16 * c), "r"(in ? x0 : 0u), "r"(in ? x1 : 0u),
                      "r"(in ? x2 : 0u), "r"(in ? x3 : 0u)
                      : "memory");
+      }
+      if (spoilt) {
+        mend_columns(st, yr, tm, w, i, in, first);
+        tc_fence_before_sync();
+        mbar_arrive(tfree(slot));
       }
       __syncwarp();
 #pragma unroll
