@@ -149,10 +149,12 @@ __device__ __forceinline__ int seq_len(const ConvArgs& A, int b) {
 // multiple of kAhead) and keeps the last kW - 1 inputs in registers, so every
 // input is loaded once but for the W - 1 rows before each strip; the next
 // kAhead rows are in flight while it computes on the last.  kEdge: the strip
-// may reach behind its sequence's end.  Bound by HBM: B=4 T=4096 C=1536 W=4
-// bf16, x a slice of a wider tensor: 21.7 us, 4.6 TB/s (two thirds of a plain
-// copy's rate: one wave of blocks, whose start and end show at 20 us; 3 blocks
-// per SM spill, strips of a fixed 64 steps leave SMs idle, 25 us).
+// may reach behind its sequence's end.  B=4 T=4096 C=1536 W=4 bf16, x a slice
+// of a wider tensor: 21.5 us, 4.7 TB/s, 69 % of a plain copy's rate; fp32 41.2
+// us, 72 %.  Neither DRAM (37 % busy over the launch) nor issue (48 %) is the
+// limit but what a launch of one wave has in flight: 16 warps to an SM at 128
+// registers, four rows each, and the wave's start and end (3 blocks per SM spill,
+// strips of a fixed 64 steps leave SMs idle, 25 us).
 constexpr int kFwdThreads = 256, kFwdBlocks = 2, kAhead = 4;
 
 template <typename T, int kVec, int kW, bool kEdge>
@@ -238,9 +240,11 @@ __global__ void __launch_bounds__(kFwdThreads, kFwdBlocks)
 // gradients g in registers, so that dxs comes out kW - 1 steps behind; the
 // strip's last gradients are those of the kW - 1 steps behind it.  The block's
 // warps are consecutive strips; their sums of dw, db are added in warp order
-// through shared memory into one partial per block.  Bound by HBM (10 bytes per
-// bf16 element): B=4 T=4096 C=1536 W=4 bf16 49 us with the partials' sum,
-// 5.2 TB/s, three quarters of a plain copy's rate.  Two channels a thread,
+// through shared memory into one partial per block.  B=4 T=4096 C=1536 W=4 bf16
+// (10 bytes an element) 49 us with the partials' sum, 5.2 TB/s, three quarters of
+// a plain copy's rate; fp32 57 us, 78 %.  DRAM 57 % and issue 51 % busy over the
+// launch: loads in flight and the instructions between them, in one wave.  Two
+// channels a thread,
 // whose products pair into one fp32 instruction; the next rows in flight while
 // it computes (without, and a block more per SM, 54); strips as long as one
 // wave of blocks wants them (a fixed 64 steps then took 59); gradients pass the

@@ -5,7 +5,7 @@
 // 16-byte loads for 64 FMAs.  Chunks have 64 steps forward, where the states'
 // traffic counts, and 32 backward, where shared memory holds twice as much.
 // Bound by shared-memory loads and FMAs: B=4 heads=8 T=4096 64x64 forward
-// 228 us (19 TFLOP/s of chunk products; one result to a thread took 821),
+// 231 us (19 TFLOP/s of chunk products; one result to a thread took 821),
 // T=2048 backward 403 us (685; the sums of W, see ssm.cu, are 8 of them).
 #include <cuda_runtime.h>
 

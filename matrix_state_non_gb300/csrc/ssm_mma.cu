@@ -16,7 +16,7 @@
 // y is the fp32 result rounded once: the joined state and P enter their
 // products as two bf16 parts each, good to 2^-16, 1/256 of y's own rounding
 // (one part each made y's error a fifth larger than its rounding, for 24 us less
-// at B=2 heads=16 T=16384 64x64 on tcgen05, 97 and 121), and differences of
+// at B=2 heads=16 T=16384 64x64 on tcgen05, 96 and 120), and differences of
 // sums of log decays keep their low parts.  The states themselves stay good to
 // fp32: k_j exp(l_63 - l_j) D_j is split into three bf16 parts (v is exact),
 // their products are summed from the smallest part up, and the chunk's sum is
@@ -24,7 +24,7 @@
 // never see the running state.
 //
 // B=4 heads=16 T=4096 64x64, shared q and k: 88 us (65 with tcgen05).  B=8
-// heads=16 T=4096 128x128: 597 us, of which decays 7, walk 234, outputs 358:
+// heads=16 T=4096 128x128: 609 us, of which decays 7, walk 234, outputs 368:
 // the walk is bound by the latency of its MMAs and of the operand split (8
 // warps to an SM, by registers), the outputs by the states that they read (537
 // MB in all) with as few warps, by shared memory.

@@ -19,7 +19,7 @@
 // earlier block of 32 steps is one exponential per row and block times a
 // tabled factor per step, so a tile takes some 40 exponentials a row, not 128.
 //
-// B=2 heads=16 T=16384 64x64, shared q and k: 73 us (whole scan 121), 412 MB
+// B=2 heads=16 T=16384 64x64, shared q and k: 73 us (whole scan 120), 412 MB
 // through L2; without the states' 134 MB, which go through L2 in fp32, and
 // their split it would be 57.  (Operands in one bf16 part each, rounded by the
 // walk: 52 us, and y's error a fifth above its rounding.)  y by a TMA store: no
