@@ -20,6 +20,14 @@ __device__ __forceinline__ int ssm_len(const SsmArgs& A, int b) {
   return A.lengths ? min(max(A.lengths[b], 0), A.T) : A.T;
 }
 
+// log a = D A.  From -1e4 down, where a is 0 many times over, the same: sums of it stay finite, and what small steps
+// add to them is not lost beside a huge one.
+template <typename T>
+__device__ __forceinline__ T log_decay(T D, T A) {
+  const T x = D * A;
+  return x < T(-1e4) ? T(-1e4) : x;
+}
+
 // A running sum as hi + lo, good to about twice fp32.  (Adding in fp64 would do as well; its unit is slow here.)
 struct Sum2 {
   float hi = 0.f, lo = 0.f;

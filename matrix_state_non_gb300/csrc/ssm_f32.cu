@@ -55,7 +55,7 @@ __device__ void load_decays(const SsmArgs& A, int b, int n, int t0, int len, Dec
     }
     d.D[i] = D;
     d.sg[i] = sg;
-    sum += static_cast<double>(D) * An;
+    sum += log_decay<double>(D, An);
     l[e] = sum;
   }
   double up = sum;

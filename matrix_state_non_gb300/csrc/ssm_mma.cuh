@@ -156,13 +156,6 @@ struct __align__(16) ChunkDecayGrad {
   float sg[kChunk];      // sigmoid(dt + dt_bias)
 };
 
-// log a = D A, kept finite where it runs out of fp32 below (a is 0 all the same): sums of it and their differences
-// stay numbers.
-__device__ __forceinline__ float log_decay(float D, float A) {
-  const float x = D * A;
-  return x < -1e30f ? -1e30f : x;
-}
-
 // Decays of every (chain, chunk) into `out` (ChunkDecay, or ChunkDecayGrad for
 // the backward), exp(l_63) into tot; clears the status block.
 cudaError_t launch_ssm_decay(const SsmArgs& a, void* out, float* tot, int nc, bool grad, StatusBlock* status,

@@ -44,3 +44,26 @@ def test_y_is_rounded_once(B, T, N, G, K, V, lengths, decay, spike, h0):
     want, size = ref.scan(g, lengths)["y"], ref.sizes(g, lengths)["y"]
     err = (r["y"].double() - want).abs() - half_unit(want)
     assert bool((err <= 2.0 ** -15 * size).all()), float((err / size.clamp_min(1e-30)).max() * 2 ** 15)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,N,G,K,V", [(2, 200, 2, 1, 32, 32), (4, 1200, 8, 2, 64, 64)])
+def test_log_decays_beyond_the_fp32_range(B, T, N, G, K, V, dtype):
+    """Steps so long that D A leaves the fp32 range (D k does not) forget
+    everything before them; what they put into the state decays by the small
+    steps after them, 1e6 x 2e-9 each."""
+    from matrix_state_non_gb300 import binding as m
+    d = ssm_inputs(B, T, N, G, K, V, dtype, seed=5, decay=-1e6)
+    d.pop("dy"), d.pop("dH_T")
+    g = ssm_dev(d, dtype)
+    g["dt_bias"] -= 20.0
+    g["dt"][:, 3::97] = 1e34
+    r = m.ssm_scan(*(g[n] for n in SSM_IN), **{n: g[n] for n in SSM_OPT})
+    want = ref.scan(g)
+    assert bool(want["y"].abs().max() < 1e38)
+    tol = 4e-3 if dtype == "bf16" else 1e-5
+    for t0 in range(3, T, 97):  # each step's reign on its own: the first steps after it, while its state lasts
+        got, w = r["y"][:, t0:t0 + 8].double(), want["y"][:, t0:t0 + 8]
+        assert float((got - w).norm() / w.norm()) <= tol, t0
+    got, w = r["H_T"].double(), want["H_T"]
+    assert bool(got.isfinite().all()) and float((got - w).norm() / w.norm()) <= 1e-5
