@@ -67,7 +67,8 @@ typedef enum {
   M2RNN_ERR_DEVICE = -6       /* device: an internal check failed           */
 } m2rnn_status;
 
-typedef enum { M2RNN_F32 = 0, M2RNN_BF16 = 1 } m2rnn_dtype;
+/* M2RNN_E4M3: an output type of m2rnn_residual_norm only. */
+typedef enum { M2RNN_F32 = 0, M2RNN_BF16 = 1, M2RNN_E4M3 = 2 } m2rnn_dtype;
 
 /* Library version, as MAJOR*10000 + MINOR*100 + PATCH. */
 int m2rnn_version(void);
@@ -442,6 +443,107 @@ int m2rnn_grad_norm(const void* plan, size_t plan_bytes, float* norm, void* work
                     void* cuda_stream);
 int m2rnn_grad_clip(const void* plan, size_t plan_bytes, float max_norm, float* norm, void* workspace,
                     size_t workspace_bytes, void* cuda_stream);
+
+/* ---------------------------------------------------------------------------
+ * Around the layers: the norm of the residual stream in front of each, a gated
+ * linear recurrence on a vector state, and the orthogonalised update of a
+ * weight matrix.  Types, strides and `lengths` as in the section above.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Root-mean-square norm of the residual stream, with the branch's addition
+ * (the pre-norm of a residual layer), per row:
+ *     h = x + residual,   s = (sum_j h_j^2 / D + eps)^(-1/2),
+ *     y = w (*) h s.
+ *   x [rows,D] in `x_dtype` (rows x_stride elements apart); residual [rows,D]
+ *   in `h_dtype` (may be NULL = zero: the stream's start); w [D] fp32;
+ *   eps >= 0;  1 <= D <= 16384.
+ *   out: h [rows,D] in `h_dtype`, rounded once (may be NULL; may be residual;
+ *   NULL where residual is NULL); y [rows,D] in `y_dtype`, the fp32 result for
+ *   the sum before it was rounded to h, rounded once.
+ *   y_dtype M2RNN_E4M3: 8-bit values (4 exponent bits, 3 of mantissa) with a
+ *   scale for each 128 values of a row, scale [rows,ceil(D/128)] fp32 (NULL
+ *   for the other types): scale = max(max |y| / 448, 2^-126), and what is
+ *   stored is y / scale, to the nearest; y = stored * scale.
+ * Outputs must not overlap inputs but for h = residual.  Rows with |h| above
+ * 1e18 leave the range of the fp32 sum of squares.
+ */
+int m2rnn_residual_norm(const void* x, int64_t x_stride, const void* residual, const float* w, float eps, void* h, void* y,
+                        float* scale, int64_t rows, int64_t D, m2rnn_dtype x_dtype, m2rnn_dtype h_dtype,
+                        m2rnn_dtype y_dtype, void* cuda_stream);
+
+/* Bytes of device workspace m2rnn_residual_norm_backward needs, 0 for an
+ * unsupported shape. */
+size_t m2rnn_residual_norm_backward_workspace_size(int64_t rows, int64_t D);
+
+/*
+ * Backward of m2rnn_residual_norm: with p = w (*) dy, r = sum_j p_j h_j,
+ *     dx = s p - r s^3 h / D + dh,   dw = sum over rows of dy (*) h s
+ * (fixed order).  h [rows,D] in `h_dtype` (what the forward left); dy [rows,D]
+ * in `dy_dtype`; dh [rows,D] fp32 (may be NULL = zero): what comes back along
+ * the stream;  out, fp32: dx [rows,D] (may be dh), the gradient of x and of
+ * residual alike; dw [D].
+ */
+int m2rnn_residual_norm_backward(const void* h, const float* w, const void* dy, const float* dh, float eps, float* dx,
+                                 float* dw, int64_t rows, int64_t D, m2rnn_dtype h_dtype, m2rnn_dtype dy_dtype,
+                                 void* workspace, size_t workspace_bytes, void* cuda_stream);
+
+/*
+ * Gated linear recurrence on a vector state (no counterpart in the paper: the
+ * gate of its Eq. 13 for every channel, without the transform), per batch
+ * element and channel, from H_0:
+ *     f_t = exp(-alpha softplus(a_t + beta)),
+ *     h_t = f_t h_{t-1} + (1 - f_t) x_t,   y_t = h_t.
+ *   x, a [B,T,C] in `dtype`, column slices of wider tensors or not; alpha [C],
+ *   beta [C] fp32 (beta may be NULL = zero), alpha >= 0 for a state that does
+ *   not grow; H_0 [B,C] fp32 (may be NULL = zero); lengths as above.
+ *   out: y [B,T,C] in `dtype`, the fp32 state rounded once; H_T [B,C] fp32
+ *   (may be NULL; may be H_0).
+ * A value that is not finite reaches no step before its own.
+ */
+int m2rnn_linear_scan(const void* x, int64_t x_stride, const void* a, int64_t a_stride, const float* alpha,
+                      const float* beta, const float* H_0, const int32_t* lengths, void* y, float* H_T, int64_t B,
+                      int64_t T, int64_t C, m2rnn_dtype dtype, void* cuda_stream);
+
+/* Bytes of device workspace m2rnn_linear_scan_backward needs, 0 for an
+ * unsupported shape. */
+size_t m2rnn_linear_backward_workspace_size(int64_t B, int64_t T, int64_t C);
+
+/*
+ * Backward of m2rnn_linear_scan for L = sum(dy * y) + <dH_T, H_T>.
+ *   dy [B,T,C] in `dtype`; dH_T [B,C] fp32 (may be NULL = zero).
+ *   out, all fp32: dx, da [B,T,C], dalpha [C], dbeta [C] (may be NULL),
+ *   dH_0 [B,C] (may be NULL; may be dH_T).
+ * Sums in a fixed order: results are bitwise reproducible.
+ */
+int m2rnn_linear_scan_backward(const void* x, int64_t x_stride, const void* a, int64_t a_stride, const float* alpha,
+                               const float* beta, const float* H_0, const int32_t* lengths, const void* dy,
+                               const float* dH_T, float* dx, float* da, float* dalpha, float* dbeta, float* dH_0,
+                               int64_t B, int64_t T, int64_t C, m2rnn_dtype dtype, void* workspace,
+                               size_t workspace_bytes, void* cuda_stream);
+
+/* One token: H [B,C] fp32 advances in place; x, a, y [B,C]; strides lie between
+ * sequences.  No workspace. */
+int m2rnn_linear_step(float* H, const void* x, int64_t x_stride, const void* a, int64_t a_stride, const float* alpha,
+                      const float* beta, void* y, int64_t B, int64_t C, m2rnn_dtype dtype, void* cuda_stream);
+
+/*
+ * Orthogonalised update (as the Muon optimiser takes the step of a weight
+ * matrix), for each of n matrices: Newton-Schulz steps that bring the singular
+ * values of G near 1 (within about 0.7 to 1.2 after five, where they were not
+ * below 1e-2 of the norm) and leave its singular vectors,
+ *     X = G / (|G| + eps)                 (Frobenius norm),
+ *     `steps` times:  A = X X^T,  X <- a X + (b A + c A A) X,
+ *     a = 3.4445, b = -4.7750, c = 2.0315.
+ *   g [n,rows,cols] in `dtype`; out [n,rows,cols] bf16 (may be g, where that
+ *   is bf16);  rows, cols in [1, 16384], n <= 65535, 1 <= steps <= 32,
+ *   eps >= 0.
+ * The workspace (m2rnn_orthogonalize_workspace_size bytes, 0 for an unsupported
+ * shape) begins with a status block (see m2rnn_sync_status) that the call clears.
+ */
+size_t m2rnn_orthogonalize_workspace_size(int64_t n, int64_t rows, int64_t cols);
+int m2rnn_orthogonalize(const void* g, void* out, int64_t n, int64_t rows, int64_t cols, int steps, float eps,
+                        m2rnn_dtype dtype, void* workspace, size_t workspace_bytes, void* cuda_stream);
 
 /*
  * Synchronises `cuda_stream`, then reads and clears the workspace status

@@ -26,6 +26,7 @@ M2RNN_ERR_TIMEOUT = -5
 M2RNN_ERR_DEVICE = -6
 M2RNN_F32 = 0
 M2RNN_BF16 = 1
+M2RNN_E4M3 = 2
 M2RNN_OPT_KERNEL_FAMILY = 0
 M2RNN_OPT_TEST_STALL_TILE = 1
 # Kernel family codes (as m2rnn_path returns them); -1 = automatic choice.
@@ -44,6 +45,9 @@ EXPORTS = (
     "m2rnn_ssm_backward_workspace_size", "m2rnn_ssm_scan_backward", "m2rnn_ssm_step",
     "m2rnn_grad_plan_size", "m2rnn_grad_plan_build", "m2rnn_grad_workspace_size", "m2rnn_grad_norm",
     "m2rnn_grad_clip",
+    "m2rnn_residual_norm", "m2rnn_residual_norm_backward_workspace_size", "m2rnn_residual_norm_backward",
+    "m2rnn_linear_scan", "m2rnn_linear_backward_workspace_size", "m2rnn_linear_scan_backward", "m2rnn_linear_step",
+    "m2rnn_orthogonalize_workspace_size", "m2rnn_orthogonalize",
 )
 
 _lib = None
@@ -136,6 +140,24 @@ def load() -> ctypes.CDLL:
     lib.m2rnn_grad_norm.argtypes = [vp, sz, vp, vp, sz, vp]
     lib.m2rnn_grad_clip.restype = ci
     lib.m2rnn_grad_clip.argtypes = [vp, sz, fl, vp, vp, sz, vp]
+    lib.m2rnn_residual_norm.restype = ci
+    lib.m2rnn_residual_norm.argtypes = [vp, i64, vp, vp, fl, vp, vp, vp, i64, i64, ci, ci, ci, vp]
+    lib.m2rnn_residual_norm_backward_workspace_size.restype = sz
+    lib.m2rnn_residual_norm_backward_workspace_size.argtypes = [i64] * 2
+    lib.m2rnn_residual_norm_backward.restype = ci
+    lib.m2rnn_residual_norm_backward.argtypes = [vp] * 4 + [fl, vp, vp, i64, i64, ci, ci, vp, sz, vp]
+    lib.m2rnn_linear_scan.restype = ci
+    lib.m2rnn_linear_scan.argtypes = [vp, i64] * 2 + [vp] * 6 + [i64] * 3 + [ci, vp]
+    lib.m2rnn_linear_backward_workspace_size.restype = sz
+    lib.m2rnn_linear_backward_workspace_size.argtypes = [i64] * 3
+    lib.m2rnn_linear_scan_backward.restype = ci
+    lib.m2rnn_linear_scan_backward.argtypes = [vp, i64] * 2 + [vp] * 11 + [i64] * 3 + [ci, vp, sz, vp]
+    lib.m2rnn_linear_step.restype = ci
+    lib.m2rnn_linear_step.argtypes = [vp] + [vp, i64] * 2 + [vp] * 3 + [i64] * 2 + [ci, vp]
+    lib.m2rnn_orthogonalize_workspace_size.restype = sz
+    lib.m2rnn_orthogonalize_workspace_size.argtypes = [i64] * 3
+    lib.m2rnn_orthogonalize.restype = ci
+    lib.m2rnn_orthogonalize.argtypes = [vp, vp, i64, i64, i64, ci, fl, ci, vp, sz, vp]
     _lib = lib
     return lib
 
@@ -932,3 +954,218 @@ def grad_clip(plan: GradPlan, max_norm: float, *, norm=None, stream=None):
     _check(st, "m2rnn_grad_clip")
     _keep(plan, stream, handle)
     return norm
+
+
+# ---------------------------------------------------------------------------
+# Around the layers: residual norm, gated linear recurrence, orthogonalised
+# update (raw wrappers, then torch conveniences)
+# ---------------------------------------------------------------------------
+def m2rnn_residual_norm(*args) -> int:
+    return load().m2rnn_residual_norm(*args)
+
+
+def m2rnn_residual_norm_backward_workspace_size(rows, D) -> int:
+    return load().m2rnn_residual_norm_backward_workspace_size(rows, D)
+
+
+def m2rnn_residual_norm_backward(*args) -> int:
+    return load().m2rnn_residual_norm_backward(*args)
+
+
+def m2rnn_linear_scan(*args) -> int:
+    return load().m2rnn_linear_scan(*args)
+
+
+def m2rnn_linear_backward_workspace_size(B, T, C) -> int:
+    return load().m2rnn_linear_backward_workspace_size(B, T, C)
+
+
+def m2rnn_linear_scan_backward(*args) -> int:
+    return load().m2rnn_linear_scan_backward(*args)
+
+
+def m2rnn_linear_step(*args) -> int:
+    return load().m2rnn_linear_step(*args)
+
+
+def m2rnn_orthogonalize_workspace_size(n, rows, cols) -> int:
+    return load().m2rnn_orthogonalize_workspace_size(n, rows, cols)
+
+
+def m2rnn_orthogonalize(*args) -> int:
+    return load().m2rnn_orthogonalize(*args)
+
+
+SCALE_BLOCK = 128  # 8-bit values of a row that share a scale
+
+
+def _flat_rows(t, name: str, dtype, gpu: int):
+    """Address and row stride of [...,D] rows that may be a column slice of a
+    wider tensor, evenly spaced through all leading dimensions."""
+    D = t.shape[-1]
+    if t.get_device() != gpu or t.dtype is not dtype:
+        _refuse(t, name, t.shape, dtype, gpu)
+    if t.is_contiguous():
+        return t.data_ptr(), D
+    shape, stride = t.shape, t.stride()
+    if D != 1 and stride[-1] != 1:
+        raise ValueError(f"{name}: the values of one row must be dense")
+    step = apart = None
+    for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            step = apart = s
+        elif s != step:
+            raise ValueError(f"{name}: rows must lie evenly spaced")
+        step *= n
+    return t.data_ptr(), D if apart is None else apart
+
+
+def residual_norm(x, w, residual=None, *, eps: float = 1e-6, dtype=None, out=None, stream=None):
+    """Root-mean-square norm of the residual stream with the branch's addition
+    (see m2rnn_residual_norm): ``x`` [...,D] (may be a column slice of a wider
+    tensor), ``residual`` [...,D] of its own type, ``w`` [D] fp32.  Returns
+    dict(y[, h][, scale]): h = x + residual in the residual's type (with a
+    residual); y of type ``dtype`` (torch.bfloat16, torch.float32 or
+    torch.float8_e4m3fn; None = x's), with scale [...,ceil(D/128)] fp32 for the
+    8-bit type.  ``out`` may hold preallocated y / h / scale; its h may be the
+    residual itself."""
+    import torch
+    shape, D, gpu, f32 = x.shape, x.shape[-1], _gpu(x), torch.float32
+    ty = x.dtype if dtype is None else dtype
+    eight = ty is torch.float8_e4m3fn
+    if not eight and ty is not torch.bfloat16 and ty is not f32:
+        raise TypeError(f"unsupported output dtype {ty}")
+    code = _dtype_code(x)
+    rows = x.numel() // D if D else 0
+    xp, xs = _flat_rows(x, "x", x.dtype, gpu)
+    res = {}
+    hcode = code
+    if residual is not None:
+        hcode = _dtype_code(residual)
+        res["h"] = _out(out, "h", x, shape, residual.dtype, stream)
+    res["y"] = y = _out(out, "y", x, shape, ty, stream)
+    if eight:
+        res["scale"] = _out(out, "scale", x, shape[:-1] + (-(-D // SCALE_BLOCK),), f32, stream)
+    st = load().m2rnn_residual_norm(
+        xp, xs, None if residual is None else _need(residual, "residual", shape, residual.dtype, gpu),
+        _need(w, "w", (D,), f32, gpu), float(eps), _ptr(res.get("h")), y.data_ptr(), _ptr(res.get("scale")), rows, D,
+        code, hcode, M2RNN_E4M3 if eight else _dtype_code(y), _on(gpu, stream))
+    _check(st, "m2rnn_residual_norm")
+    return res
+
+
+def residual_norm_backward(h, w, dy, *, dh=None, eps: float = 1e-6, out=None, workspace=None, stream=None):
+    """Backward of ``residual_norm``: ``h`` [...,D] as the forward left it (x
+    itself where there was no residual), ``dy`` [...,D] bf16 or fp32, ``dh``
+    [...,D] fp32 what comes back along the stream.  Returns dict(dx, dw,
+    workspace), fp32; dx [...,D] is the gradient of x and of the residual
+    alike.  ``out`` may hold preallocated dx / dw; its dx may be dh."""
+    import torch
+    shape, D, gpu, f32 = h.shape, h.shape[-1], _gpu(h), torch.float32
+    hcode, dcode = _dtype_code(h), _dtype_code(dy)
+    rows = h.numel() // D if D else 0
+    dx, dw = _out(out, "dx", h, shape, f32, stream), _out(out, "dw", h, (D,), f32, stream)
+    ws = _scratch(workspace, m2rnn_residual_norm_backward_workspace_size(rows, D), h, stream,
+                  "m2rnn_residual_norm_backward_workspace_size")
+    st = load().m2rnn_residual_norm_backward(
+        _need(h, "h", shape, h.dtype, gpu), _need(w, "w", (D,), f32, gpu), _need(dy, "dy", shape, dy.dtype, gpu),
+        _need(dh, "dh", shape, f32, gpu), float(eps), dx.data_ptr(), dw.data_ptr(), rows, D, hcode, dcode,
+        ws.data_ptr(), ws.numel(), _on(gpu, stream))
+    _check(st, "m2rnn_residual_norm_backward")
+    return dict(dx=dx, dw=dw, workspace=ws)
+
+
+def linear_scan(x, a, alpha, beta=None, *, H_0=None, lengths=None, want_state: bool = True, out=None, stream=None):
+    """Gated linear recurrence on a vector state (see m2rnn_linear_scan): ``x``,
+    ``a`` [B,T,C] (column slices of wider tensors are fine), ``alpha``,
+    ``beta`` [C] fp32, ``H_0`` [B,C] fp32, ``lengths`` [B] int32.  Returns
+    dict(y[, H_T]): y in the inputs' type, H_T fp32.  ``out`` may hold
+    preallocated y / H_T."""
+    import torch
+    B, T, C = x.shape
+    gpu, ty, f32 = _gpu(x), x.dtype, torch.float32
+    code = _dtype_code(x)
+    xp, xs = _rows(x, "x", (B, T, C), 1, C, ty, gpu)
+    ap, as_ = _rows(a, "a", (B, T, C), 1, C, ty, gpu)
+    y = _out(out, "y", x, (B, T, C), ty, stream)
+    H_T = _out(out, "H_T", x, (B, C), f32, stream) if want_state else None
+    st = load().m2rnn_linear_scan(xp, xs, ap, as_, _need(alpha, "alpha", (C,), f32, gpu),
+                                  _need(beta, "beta", (C,), f32, gpu), _need(H_0, "H_0", (B, C), f32, gpu),
+                                  _need(lengths, "lengths", (B,), torch.int32, gpu), y.data_ptr(), _ptr(H_T), B, T, C,
+                                  code, _on(gpu, stream))
+    _check(st, "m2rnn_linear_scan")
+    return dict(y=y) if H_T is None else dict(y=y, H_T=H_T)
+
+
+def linear_scan_backward(x, a, alpha, beta, dy, *, H_0=None, dH_T=None, lengths=None, want_dH0: bool = False, out=None,
+                         workspace=None, stream=None):
+    """Backward of ``linear_scan``: ``dy`` [B,T,C] in the inputs' type, ``dH_T``
+    [B,C] fp32.  Returns dict(dx, da, dalpha[, dbeta][, dH_0], workspace), all
+    fp32 (dbeta when there is a beta)."""
+    import torch
+    B, T, C = x.shape
+    gpu, ty, f32 = _gpu(x), x.dtype, torch.float32
+    code = _dtype_code(x)
+    xp, xs = _rows(x, "x", (B, T, C), 1, C, ty, gpu)
+    ap, as_ = _rows(a, "a", (B, T, C), 1, C, ty, gpu)
+    shapes = dict(dx=(B, T, C), da=(B, T, C), dalpha=(C,))
+    if beta is not None:
+        shapes["dbeta"] = (C,)
+    if want_dH0:
+        shapes["dH_0"] = (B, C)
+    res = {n: _out(out, n, x, sh, f32, stream) for n, sh in shapes.items()}
+    ws = _scratch(workspace, m2rnn_linear_backward_workspace_size(B, T, C), x, stream,
+                  "m2rnn_linear_backward_workspace_size")
+    st = load().m2rnn_linear_scan_backward(
+        xp, xs, ap, as_, _need(alpha, "alpha", (C,), f32, gpu), _need(beta, "beta", (C,), f32, gpu),
+        _need(H_0, "H_0", (B, C), f32, gpu), _need(lengths, "lengths", (B,), torch.int32, gpu),
+        _need(dy, "dy", (B, T, C), ty, gpu), _need(dH_T, "dH_T", (B, C), f32, gpu),
+        *(_ptr(res.get(n)) for n in ("dx", "da", "dalpha", "dbeta", "dH_0")), B, T, C, code, ws.data_ptr(), ws.numel(),
+        _on(gpu, stream))
+    _check(st, "m2rnn_linear_scan_backward")
+    res["workspace"] = ws
+    return res
+
+
+def linear_step(H, x, a, alpha, beta=None, *, y=None, stream=None):
+    """One token of ``linear_scan``: ``H`` [B,C] fp32 advances in place; x, a
+    [B,C].  Returns y [B,C]."""
+    import torch
+    B, C = x.shape
+    gpu, ty, f32 = _gpu(x), x.dtype, torch.float32
+    code = _dtype_code(x)
+    xp, xs = _rows(x, "x", (B, C), 1, C, ty, gpu)
+    ap, as_ = _rows(a, "a", (B, C), 1, C, ty, gpu)
+    if y is None:
+        y = _alloc(x, (B, C), ty, stream)
+    st = load().m2rnn_linear_step(_need(H, "H", (B, C), f32, gpu), xp, xs, ap, as_,
+                                  _need(alpha, "alpha", (C,), f32, gpu), _need(beta, "beta", (C,), f32, gpu),
+                                  _need(y, "y", (B, C), ty, gpu), B, C, code, _on(gpu, stream))
+    _check(st, "m2rnn_linear_step")
+    return y
+
+
+def orthogonalize(g, *, steps: int = 5, eps: float = 1e-7, out=None, workspace=None, stream=None):
+    """Orthogonalised update of a weight matrix or a stack of them (see
+    m2rnn_orthogonalize): ``g`` [...,rows,cols] bf16 or fp32, contiguous (a
+    gradient or its momentum).  Returns bf16 [...,rows,cols], ``out`` if given
+    (which may be a bf16 ``g``).  ``workspace``: scratch to use if it is large
+    enough; calls that overlap need one each."""
+    import torch
+    gpu, shape = _gpu(g), g.shape
+    code = _dtype_code(g)
+    if len(shape) < 2:
+        raise ValueError(f"expected matrices, got {tuple(shape)}")
+    rows, cols = shape[-2:]
+    n = g.numel() // (rows * cols) if rows and cols else 0
+    gp = _need(g, "g", shape, g.dtype, gpu)
+    if out is None:
+        out = _alloc(g, shape, torch.bfloat16, stream)
+    ws = _scratch(workspace, m2rnn_orthogonalize_workspace_size(n, rows, cols), g, stream,
+                  "m2rnn_orthogonalize_workspace_size")
+    st = load().m2rnn_orthogonalize(gp, _need(out, "out", shape, torch.bfloat16, gpu), n, rows, cols, int(steps),
+                                    float(eps), code, ws.data_ptr(), ws.numel(), _on(gpu, stream))
+    _check(st, "m2rnn_orthogonalize")
+    return out

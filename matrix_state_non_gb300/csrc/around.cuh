@@ -1,0 +1,94 @@
+// Shared by the operators around the scans' layer: the residual norm, the gated
+// linear recurrence and the orthogonalised update.  Argument blocks that the
+// C-ABI layer fills, and the launchers.
+#pragma once
+
+#include "layer.cuh"
+
+namespace m2rnn {
+
+// out[j] = sum over p of part[p][j], in a fixed order; with `two`, rows are 2 D
+// wide and columns from D on are out2's (which may be null).
+cudaError_t launch_sum_parts(const float* part, float* out, float* out2, bool two, int parts, int64_t D,
+                             cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Residual norm
+// ---------------------------------------------------------------------------
+constexpr int kNormMaxWidth = 16384;
+constexpr int kScaleBlock = 128;  // values of a row that share a scale
+
+struct NormRowsArgs {
+  const void* x;         // [rows, D], rows x_stride elements apart
+  const void* residual;  // [rows, D] or null
+  const float* w;        // [D]
+  void* h;               // [rows, D]: forward: out or null; backward: in
+  void* y;               // [rows, D]
+  float* scale;          // [rows, ceil(D / 128)], for e4m3
+  const void* dy;        // backward: [rows, D]
+  const float* dh;       // backward: [rows, D] or null
+  float* dx;             // backward: [rows, D]
+  float* dw;             // backward: [D]
+  float* part;           // backward: [parts][D]
+  int64_t rows, x_stride;
+  int D;
+  float eps;
+  bool x_bf16, h_bf16, dy_bf16;
+  int y_type;
+};
+
+int norm_rows_parts(int64_t rows, int64_t D);
+cudaError_t launch_residual_norm(const NormRowsArgs& a, cudaStream_t s);
+cudaError_t launch_residual_norm_backward(const NormRowsArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Gated linear recurrence
+// ---------------------------------------------------------------------------
+struct LinearArgs {
+  const void* x;       // [B,T,C], rows x_stride elements apart
+  const void* a;       // [B,T,C], rows a_stride elements apart
+  const float* alpha;  // [C]
+  const float* beta;   // [C] or null
+  const float* H_0;    // [B,C] or null
+  const int* lengths;  // [B] or null
+  void* y;             // forward: [B,T,C]
+  float* H_T;          // forward: [B,C] or null
+  const void* dy;      // backward: [B,T,C]
+  const float* dH_T;   // backward: [B,C] or null
+  float* dx;           // backward: [B,T,C]
+  float* da;           // backward: [B,T,C]
+  float* dalpha;       // backward: [C]
+  float* dbeta;        // backward: [C] or null
+  float* dH_0;         // backward: [B,C] or null
+  void* ws;            // backward
+  int64_t x_stride, a_stride;
+  int B, T, C;
+  bool bf16;
+};
+
+size_t linear_backward_scratch_bytes(int64_t B, int64_t T, int64_t C);
+cudaError_t launch_linear_forward(const LinearArgs& a, cudaStream_t s);
+cudaError_t launch_linear_backward(const LinearArgs& a, cudaStream_t s);
+// One token: H [B,C] in place; a.x, a.a, a.y [B,C].
+cudaError_t launch_linear_step(float* H, const LinearArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// Orthogonalised update
+// ---------------------------------------------------------------------------
+constexpr int kOrthoMaxDim = 16384, kOrthoMaxSteps = 32;
+
+struct OrthoArgs {
+  const void* g;  // [n, rows, cols]
+  uint16_t* out;  // [n, rows, cols] bf16
+  void* ws;       // scratch behind the status block
+  StatusBlock* status;
+  int64_t n;
+  int rows, cols, steps;
+  float eps;
+  bool bf16;
+};
+
+size_t ortho_scratch_bytes(int64_t n, int64_t rows, int64_t cols);
+cudaError_t launch_orthogonalize(const OrthoArgs& a, cudaStream_t s);
+
+}  // namespace m2rnn
