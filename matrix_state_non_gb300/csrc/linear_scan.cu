@@ -70,16 +70,31 @@ struct Raw2<float> {
   float2 v;
   __device__ __forceinline__ float2 f() const { return v; }
 };
+// `other`: from the lane's first to its second channel (not kPair).
 template <bool kPair>
-__device__ __forceinline__ Raw2<uint16_t> load_2(const uint16_t* p, bool in0, bool in1) {
-  if constexpr (kPair) return {in0 ? *reinterpret_cast<const uint32_t*>(p) : 0u};
-  const uint32_t lo = in0 ? p[0] : 0u, hi = in1 ? p[32] : 0u;
-  return {lo | hi << 16};
+__device__ __forceinline__ Raw2<uint16_t> load_2(const uint16_t* p, int other) {
+  if constexpr (kPair) return {*reinterpret_cast<const uint32_t*>(p)};
+  return {static_cast<uint32_t>(p[0]) | static_cast<uint32_t>(p[other]) << 16};
 }
 template <bool kPair>
-__device__ __forceinline__ Raw2<float> load_2(const float* p, bool in0, bool in1) {
-  if constexpr (kPair) return {in0 ? *reinterpret_cast<const float2*>(p) : make_float2(0.f, 0.f)};
-  return {make_float2(in0 ? p[0] : 0.f, in1 ? p[32] : 0.f)};
+__device__ __forceinline__ Raw2<float> load_2(const float* p, int other) {
+  if constexpr (kPair) return {*reinterpret_cast<const float2*>(p)};
+  return {make_float2(p[0], p[other])};
+}
+// kL rows from row t0 on; those at or behind `len` are zero.
+template <bool kPair, int kL, typename E>
+__device__ __forceinline__ void load_rows(Raw2<E> (&r)[kL], const E* p, int64_t stride, int other, int t0, int len) {
+  p += t0 * stride;
+  if (t0 + kL <= len) {
+#pragma unroll
+    for (int i = 0; i < kL; ++i, p += stride) r[i] = load_2<kPair>(p, other);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kL; ++i, p += stride) {
+      r[i] = Raw2<E>{};
+      if (t0 + i < len) r[i] = load_2<kPair>(p, other);
+    }
+  }
 }
 template <bool kPair>
 __device__ __forceinline__ void store_2(uint16_t* p, float2 v, bool in0, bool in1) {
@@ -100,18 +115,21 @@ __device__ __forceinline__ void store_2(float* p, float2 v, bool in0, bool in1) 
   }
 }
 
-// A lane's two channels: c and c + 1, or c and c + 32.
+// A lane's two channels: c and c + 1, or c and c + 32.  Lanes without a channel
+// read the last one's (`from`, and `other` further on) and write nothing.
 template <bool kPair>
 struct Lane {
-  int c;
+  int c, from, other;
   bool in0, in1;
   __device__ __forceinline__ Lane(int group, int C) {
     c = group * kChan + (threadIdx.x & 31) * (kPair ? 2 : 1);
     in0 = c < C;
     in1 = c + (kPair ? 1 : 32) < C;
+    from = in0 ? c : C - (kPair ? 2 : 1);
+    other = in1 ? (kPair ? 1 : 32) : 0;
   }
-  __device__ __forceinline__ float2 get(const float* p, float other) const {
-    return make_float2(p != nullptr && in0 ? p[c] : other, p != nullptr && in1 ? p[c + (kPair ? 1 : 32)] : other);
+  __device__ __forceinline__ float2 get(const float* p) const {
+    return p != nullptr ? make_float2(p[from], p[from + other]) : make_float2(0.f, 0.f);
   }
   __device__ __forceinline__ void put(float* p, float2 v) const {
     if (in0) p[c] = v.x;
@@ -128,13 +146,16 @@ struct Gate2 {
 
 // All to a few units of fp32.  softplus(z) = max(z, 0) + log(1 + t), t = exp(-|z|),
 // and log(1 + t) = 2 atanh(v), v = t / (2 + t) <= 1/3: a polynomial in v^2 of
-// degree 4 (minimax, 4e-9).  1 - f = u P(u), u = alpha softplus, for small u (minimax
-// on [-1/8, 0.7], 3e-8), so that it keeps its digits where f is near 1, and f is
-// what is left; beyond, f = 2^(-u log2 e).
+// degree 4 (minimax, 4e-9).  1 - f = u P(u), u = alpha softplus, for |u| <= 0.7
+// (minimax, 3e-8), so that it keeps its digits where f is near 1, and f is what
+// is left; beyond, f = 2^(-u log2 e).  kSmall: f keeps its digits where it is
+// near 0 too, which only gradients show.
+template <bool kSmall>
 __device__ __forceinline__ Gate2 gate_of(float2 z, float2 alpha) {
   constexpr float kLog2e = 1.44269504f;
   Gate2 g;
-  g.t = make_float2(ex2_fast(fabsf(z.x) * -kLog2e), ex2_fast(fabsf(z.y) * -kLog2e));
+  const float2 y = mul_2(z, two(kLog2e));
+  g.t = make_float2(ex2_fast(-fabsf(y.x)), ex2_fast(-fabsf(y.y)));
   const float2 w = add_2(g.t, two(2.f));
   const float2 v = mul_2(g.t, make_float2(rcp_fast(w.x), rcp_fast(w.y)));
   const float2 s = mul_2(v, v);
@@ -144,16 +165,18 @@ __device__ __forceinline__ Gate2 gate_of(float2 z, float2 alpha) {
   p = fma_2(s, p, two(2.f));
   g.soft = fma_2(v, p, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
   const float2 u = mul_2(alpha, g.soft);
-  p = fma_2(u, two(-0.00108651957f), two(0.00816469174f));
-  p = fma_2(u, p, two(-0.04163466394f));
-  p = fma_2(u, p, two(0.16666769981f));
-  p = fma_2(u, p, two(-0.50000053644f));
+  p = fma_2(u, two(0.00019840967f), two(-0.00141012867f));
+  p = fma_2(u, p, two(0.00833449047f));
+  p = fma_2(u, p, two(-0.04166151583f));
+  p = fma_2(u, p, two(0.16666638851f));
+  p = fma_2(u, p, two(-0.50000029802f));
   p = fma_2(u, p, two(1.f));
-  const float2 e = mul_2(u, p);
-  const float f0 = ex2_fast(u.x * -kLog2e), f1 = ex2_fast(u.y * -kLog2e);
-  const bool small0 = u.x <= 0.7f && u.x >= -0.125f, small1 = u.y <= 0.7f && u.y >= -0.125f;
-  g.e = make_float2(small0 ? e.x : 1.f - f0, small1 ? e.y : 1.f - f1);
-  g.f = make_float2(small0 ? 1.f - e.x : f0, small1 ? 1.f - e.y : f1);
+  const float2 e = mul_2(u, p), x = mul_2(u, two(-kLog2e));
+  const float2 f = make_float2(ex2_fast(x.x), ex2_fast(x.y)), far = fma_2(f, two(-1.f), two(1.f));
+  const bool near0 = fabsf(u.x) <= 0.7f, near1 = fabsf(u.y) <= 0.7f;
+  g.e = make_float2(near0 ? e.x : far.x, near1 ? e.y : far.y);
+  g.f = fma_2(g.e, two(-1.f), two(1.f));
+  if constexpr (kSmall) g.f = make_float2(near0 ? g.f.x : f.x, near1 ? g.f.y : f.y);
   return g;
 }
 
@@ -161,12 +184,31 @@ __device__ __forceinline__ Gate2 gate_of(float2 z, float2 alpha) {
 // The exchange
 // ---------------------------------------------------------------------------
 struct Exchange {
-  float4 warp[2][kWarps][32];       // F, U of the block's segments
+  float4 warp[2][kWarps][32];        // F, U of the block's segments
   float4 block[2][kMaxCluster][32];  // of the cluster's tiles
+  alignas(8) uint64_t arrived[2];    // a phase for each second round: every tile's F and U are there
+  int abort_flag;
 };
+
+__device__ __forceinline__ void open_exchange(Exchange& x, int blocks) {
+  if (blocks == 1) return;
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&x.arrived[0]), 1);
+    mbar_init(smem_u32(&x.arrived[1]), 1);
+    x.abort_flag = 0;
+    fence_mbar_init_cluster();
+  }
+  cluster_sync_all();
+}
 
 // The state before the warp's segment, from `carry`, the state before the
 // round; carry goes on to the next round.  Every thread of the cluster calls it.
+// A block hands its F and U to every block of the cluster by stores that count
+// on the receiver's mbarrier: a cluster barrier's release would wait for the
+// outputs stored before it.  Buffers of two rounds serve: nobody sends for round
+// i + 2 before it has what this block sent for round i + 1, after this block was
+// done with round i; and nobody ends before all that is sent to it has come.  A
+// wait that gives up (seconds) spoils the state with NaN.
 __device__ __forceinline__ float2 state_before(Exchange& x, int round, float2 F, float2 U, float2& carry, int rank, int blocks) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, buf = round & 1;
   x.warp[buf][warp][lane] = make_float4(F.x, F.y, U.x, U.y);
@@ -187,12 +229,15 @@ __device__ __forceinline__ float2 state_before(Exchange& x, int round, float2 F,
   if (blocks == 1) {
     carry = fma_2(tF, carry, tU);
   } else {
+    const uint32_t bar = smem_u32(&x.arrived[buf]);
     if (warp < blocks) {
-      const uint32_t to = mapa_shared(smem_u32(&x.block[buf][rank][lane]), warp);
-      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(to), "f"(tF.x), "f"(tF.y), "f"(tU.x), "f"(tU.y)
+      const uint32_t to = mapa_shared(smem_u32(&x.block[buf][rank][lane]), warp), at = mapa_shared(bar, warp);
+      asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
+                   "f"(tF.x), "f"(tF.y), "f"(tU.x), "f"(tU.y), "r"(at)
                    : "memory");
     }
-    cluster_sync_all();
+    if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, blocks * 32 * 16);
+    if (!mbar_wait<true>(bar, (round >> 1) & 1, &x.abort_flag, nullptr, 0)) carry = two(__int_as_float(0x7fc00000));
     for (int r = 0; r < blocks; ++r) {
       if (r == rank) mine = carry;
       const float4 s = x.block[buf][r][lane];
@@ -218,33 +263,26 @@ __global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs 
   const Lane<kPair> me(group, A.C);
   const int len = length_of(A, b);
   const int64_t first = static_cast<int64_t>(b) * A.T;
-  const E* px = static_cast<const E*>(A.x) + first * A.x_stride + me.c;
-  const E* pa = static_cast<const E*>(A.a) + first * A.a_stride + me.c;
+  const E* px = static_cast<const E*>(A.x) + first * A.x_stride + me.from;
+  const E* pa = static_cast<const E*>(A.a) + first * A.a_stride + me.from;
   E* py = static_cast<E*>(A.y) + first * A.C + me.c;
-  const float2 alpha = me.get(A.alpha, 0.f), beta = me.get(A.beta, 0.f);
-  float2 carry = A.H_0 != nullptr ? me.get(A.H_0 + static_cast<int64_t>(b) * A.C, 0.f) : two(0.f);
+  const float2 alpha = me.get(A.alpha), beta = me.get(A.beta);
+  float2 carry = me.get(A.H_0 != nullptr ? A.H_0 + static_cast<int64_t>(b) * A.C : nullptr);
   const int rounds = (len + kTile * blocks - 1) / (kTile * blocks);
 
   Raw2<E> ra[kL], rx[kL];
   auto load = [&](int t0) {
-    const E* p = pa + static_cast<int64_t>(t0) * A.a_stride;
-    const E* q = px + static_cast<int64_t>(t0) * A.x_stride;
-#pragma unroll
-    for (int i = 0; i < kL; ++i) {
-      const bool live = t0 + i < len;
-      ra[i] = load_2<kPair>(p, live && me.in0, live && me.in1);
-      rx[i] = load_2<kPair>(q, live && me.in0, live && me.in1);
-      p += A.a_stride;
-      q += A.x_stride;
-    }
+    load_rows<kPair>(ra, pa, A.a_stride, me.other, t0, len);
+    load_rows<kPair>(rx, px, A.x_stride, me.other, t0, len);
   };
+  open_exchange(xch, blocks);
   int t0 = rank * kTile + warp * kL;
   if (rounds > 0) load(t0);
   for (int it = 0; it < rounds; ++it) {
     float2 f[kL], in[kL], F = two(1.f), U = two(0.f);
 #pragma unroll
     for (int i = 0; i < kL; ++i) {
-      const Gate2 g = gate_of(add_2(ra[i].f(), beta), alpha);
+      const Gate2 g = gate_of<false>(add_2(ra[i].f(), beta), alpha);
       f[i] = g.f;
       in[i] = mul_2(g.e, rx[i].f());
     }
@@ -274,12 +312,18 @@ __global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs 
       }
     } else {
       E* p = py + static_cast<int64_t>(now) * A.C;
+      if (now + kL <= len) {
 #pragma unroll
-      for (int i = 0; i < kL; ++i) {
-        h = fma_2(f[i], h, in[i]);
-        const int t = now + i;
-        if (t < A.T) store_2<kPair>(p, t < len ? h : two(0.f), me.in0, me.in1);
-        p += A.C;
+        for (int i = 0; i < kL; ++i, p += A.C) {
+          h = fma_2(f[i], h, in[i]);
+          store_2<kPair>(p, h, me.in0, me.in1);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < kL; ++i, p += A.C) {
+          h = fma_2(f[i], h, in[i]);
+          if (now + i < A.T) store_2<kPair>(p, now + i < len ? h : two(0.f), me.in0, me.in1);
+        }
       }
     }
   }
@@ -304,14 +348,14 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs
   const Lane<kPair> me(group, A.C);
   const int len = length_of(A, b);
   const int64_t first = static_cast<int64_t>(b) * A.T;
-  const E* px = static_cast<const E*>(A.x) + first * A.x_stride + me.c;
-  const E* pa = static_cast<const E*>(A.a) + first * A.a_stride + me.c;
-  const E* pd = static_cast<const E*>(A.dy) + first * A.C + me.c;
+  const E* px = static_cast<const E*>(A.x) + first * A.x_stride + me.from;
+  const E* pa = static_cast<const E*>(A.a) + first * A.a_stride + me.from;
+  const E* pd = static_cast<const E*>(A.dy) + first * A.C + me.from;
   float *pdx = A.dx + first * A.C + me.c, *pda = A.da + first * A.C + me.c;
   const float* ph = states + static_cast<int64_t>(b) * ((A.T + kL - 1) / kL) * A.C;
-  const float2 alpha = me.get(A.alpha, 0.f), beta = me.get(A.beta, 0.f);
+  const float2 alpha = me.get(A.alpha), beta = me.get(A.beta);
   const float2 minus_alpha = make_float2(-alpha.x, -alpha.y);
-  float2 carry = A.dH_T != nullptr ? me.get(A.dH_T + static_cast<int64_t>(b) * A.C, 0.f) : two(0.f);
+  float2 carry = me.get(A.dH_T != nullptr ? A.dH_T + static_cast<int64_t>(b) * A.C : nullptr);
   float2 sa = two(0.f), sb = two(0.f);
   const int tiles = (len + kTile - 1) / kTile, rounds = (tiles + blocks - 1) / blocks;
 
@@ -319,25 +363,16 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs
   int t0 = ((tiles - 1 - rank) * kWarps + kWarps - 1 - warp) * kL;
   Raw2<E> ra[kL], rx[kL], rd[kL];
   float2 hs = two(0.f);
-  auto load = [&](int t0) {
-    const bool any = t0 >= 0;
-    const E* p = pa + static_cast<int64_t>(t0) * A.a_stride;
-    const E* q = px + static_cast<int64_t>(t0) * A.x_stride;
-    const E* d = pd + static_cast<int64_t>(t0) * A.C;
-#pragma unroll
-    for (int i = 0; i < kL; ++i) {
-      const bool live = any && t0 + i < len;
-      ra[i] = load_2<kPair>(p, live && me.in0, live && me.in1);
-      rx[i] = load_2<kPair>(q, live && me.in0, live && me.in1);
-      rd[i] = load_2<kPair>(d, live && me.in0, live && me.in1);
-      p += A.a_stride;
-      q += A.x_stride;
-      d += A.C;
-    }
+  auto load = [&](int t0) {  // (before the sequence as behind it: zeros)
+    const int from = t0 < 0 ? len : t0;
+    load_rows<kPair>(ra, pa, A.a_stride, me.other, from, len);
+    load_rows<kPair>(rx, px, A.x_stride, me.other, from, len);
+    load_rows<kPair>(rd, pd, A.C, me.other, from, len);
   };
   auto load_state = [&](int t0) {
-    if (t0 >= 0 && t0 < len) hs = me.get(ph + static_cast<int64_t>(t0 / kL) * A.C, 0.f);
+    if (t0 >= 0 && t0 < len) hs = me.get(ph + static_cast<int64_t>(t0 / kL) * A.C);
   };
+  open_exchange(xch, blocks);
   if (rounds > 0) load(t0);
   wait_previous();
   if (rounds > 0) load_state(t0);
@@ -347,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs
 #pragma unroll
     for (int i = 0; i < kL; ++i) {
       const float2 z = add_2(ra[i].f(), beta), x = rx[i].f();
-      const Gate2 g = gate_of(z, alpha);
+      const Gate2 g = gate_of<true>(z, alpha);
       f[i] = g.f;
       e[i] = g.e;
       const float2 w = add_2(g.t, two(1.f));
@@ -428,11 +463,11 @@ __global__ void __launch_bounds__(128) linear_step_kernel(float* H, LinearArgs A
   const int b = static_cast<int>(id / groups);
   if (b >= A.B) return;
   const Lane<kPair> me(static_cast<int>(id - static_cast<int64_t>(b) * groups), A.C);
-  const Raw2<E> a = load_2<kPair>(static_cast<const E*>(A.a) + b * A.a_stride + me.c, me.in0, me.in1);
-  const Raw2<E> x = load_2<kPair>(static_cast<const E*>(A.x) + b * A.x_stride + me.c, me.in0, me.in1);
+  const Raw2<E> a = load_2<kPair>(static_cast<const E*>(A.a) + b * A.a_stride + me.from, me.other);
+  const Raw2<E> x = load_2<kPair>(static_cast<const E*>(A.x) + b * A.x_stride + me.from, me.other);
   const int64_t at = static_cast<int64_t>(b) * A.C;
-  const Gate2 g = gate_of(add_2(a.f(), me.get(A.beta, 0.f)), me.get(A.alpha, 0.f));
-  const float2 h = fma_2(g.f, me.get(H + at, 0.f), mul_2(g.e, x.f()));
+  const Gate2 g = gate_of<false>(add_2(a.f(), me.get(A.beta)), me.get(A.alpha));
+  const float2 h = fma_2(g.f, me.get(H + at), mul_2(g.e, x.f()));
   me.put(H + at, h);
   store_2<kPair>(static_cast<E*>(A.y) + at + me.c, h, me.in0, me.in1);
 }
