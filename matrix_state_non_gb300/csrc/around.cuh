@@ -7,6 +7,11 @@
 
 namespace m2rnn {
 
+// A tiled tensor map of up to 5 dimensions, innermost first (strides in bytes,
+// from the second dimension on); what lies outside reads as zero.
+bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
+                     const uint64_t* strides, const uint32_t* box, bool swizzle128);
+
 // out[j] = sum over p of part[p][j], in a fixed order; with `two`, rows are 2 D
 // wide and columns from D on are out2's (which may be null).
 cudaError_t launch_sum_parts(const float* part, float* out, float* out2, bool two, int parts, int64_t D,

@@ -16,8 +16,9 @@
 // consecutive segments, the blocks of a cluster consecutive tiles, and the
 // cluster marches through the sequence in rounds: F and U of the warps go
 // through shared memory, those of the blocks through the cluster's, and every
-// thread composes what lies before it.  The next round's inputs are loaded
-// before the exchange.  The backward marches the other way; the states before
+// thread composes what lies before it.  Inputs come a few rounds ahead, by TMA
+// into a ring of tiles in shared memory (kTma, where rows lie on 16 bytes), else
+// a round ahead into registers.  The backward marches the other way; the states before
 // its segments are left by the forward's kernel, without y, in one launch
 // before it.
 #include <cuda_runtime.h>
@@ -25,6 +26,7 @@
 #include <cstdint>
 
 #include "around.cuh"
+#include "mma_common.cuh"
 
 namespace m2rnn {
 namespace {
@@ -115,6 +117,41 @@ __device__ __forceinline__ void store_2(float* p, float2 v, bool in0, bool in1) 
   }
 }
 
+// A ring of tiles in shared memory: kN inputs of kRows steps of 64 channels, by
+// TMA.  One thread fills, everybody waits.
+template <typename E, int kN, int kRows>
+struct Ring {
+  static constexpr int kStages = 3, kTileBytes = kRows * kChan * static_cast<int>(sizeof(E));
+  static constexpr int kBytes = kStages * kN * kTileBytes;
+  uint8_t* tiles;  // on 128 bytes
+  uint64_t* full;  // [kStages]
+  __device__ __forceinline__ const E* row(int stage, int input, int r) const {
+    return reinterpret_cast<const E*>(tiles + (stage * kN + input) * kTileBytes) + r * kChan + 2 * (threadIdx.x & 31);
+  }
+  __device__ __forceinline__ void fill(int stage, const CUtensorMap* const (&maps)[kN], int c, int t, int b) const {
+    const uint32_t bar = smem_u32(full + stage);
+    mbar_arrive_expect_tx(bar, kN * kTileBytes);
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      asm volatile(
+          "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+              smem_u32(tiles + (stage * kN + i) * kTileBytes)),
+          "l"(reinterpret_cast<uint64_t>(maps[i])), "r"(bar), "r"(c), "r"(t), "r"(b)
+          : "memory");
+  }
+};
+// A block that gave up waits for what is still on its way to its ring, of
+// `fills` tiles in all.
+template <typename Tiles>
+__device__ __forceinline__ void drain(const Tiles& ring, int fills) {
+  for (int i = max(0, fills - Tiles::kStages); i < fills; ++i)
+    mbar_wait_timed(smem_u32(ring.full + i % Tiles::kStages), (i / Tiles::kStages) & 1, nullptr, 0);
+}
+template <int kN>
+struct Maps {
+  CUtensorMap m[kN];
+};
+
 // A lane's two channels: c and c + 1, or c and c + 32.  Lanes without a channel
 // read the last one's (`from`, and `other` further on) and write nothing.
 template <bool kPair>
@@ -187,19 +224,24 @@ struct Exchange {
   float4 warp[2][kWarps][32];        // F, U of the block's segments
   float4 block[2][kMaxCluster][32];  // of the cluster's tiles
   alignas(8) uint64_t arrived[2];    // a phase for each second round: every tile's F and U are there
+  alignas(8) uint64_t full[3];       // the ring's
   int abort_flag;
 };
 
 __device__ __forceinline__ void open_exchange(Exchange& x, int blocks) {
-  if (blocks == 1) return;
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(&x.arrived[0]), 1);
-    mbar_init(smem_u32(&x.arrived[1]), 1);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&x.arrived[i]), 1);
+    for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&x.full[i]), 1);
     x.abort_flag = 0;
     fence_mbar_init_cluster();
   }
-  cluster_sync_all();
+  if (blocks > 1)
+    cluster_sync_all();
+  else
+    __syncthreads();
 }
+
+constexpr float kSpoilt = __builtin_nanf("");
 
 // The state before the warp's segment, from `carry`, the state before the
 // round; carry goes on to the next round.  Every thread of the cluster calls it.
@@ -237,7 +279,7 @@ __device__ __forceinline__ float2 state_before(Exchange& x, int round, float2 F,
                    : "memory");
     }
     if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, blocks * 32 * 16);
-    if (!mbar_wait<true>(bar, (round >> 1) & 1, &x.abort_flag, nullptr, 0)) carry = two(__int_as_float(0x7fc00000));
+    if (!mbar_wait<true>(bar, (round >> 1) & 1, &x.abort_flag, nullptr, 0)) carry = two(kSpoilt);
     for (int r = 0; r < blocks; ++r) {
       if (r == rank) mine = carry;
       const float4 s = x.block[buf][r][lane];
@@ -247,6 +289,10 @@ __device__ __forceinline__ float2 state_before(Exchange& x, int round, float2 F,
   return fma_2(pF, mine, pU);
 }
 
+__device__ __forceinline__ uint8_t* align_smem(uint8_t* p) {
+  return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 127) & ~static_cast<uintptr_t>(127));
+}
+
 __device__ __forceinline__ int length_of(const LinearArgs& A, int b) {
   return A.lengths != nullptr ? min(max(A.lengths[b], 0), A.T) : A.T;
 }
@@ -254,9 +300,11 @@ __device__ __forceinline__ int length_of(const LinearArgs& A, int b) {
 // ---------------------------------------------------------------------------
 // Forward: y, H_T; or (kStates) the state before each kEvery steps
 // ---------------------------------------------------------------------------
-template <typename E, bool kPair, bool kStates, int kL, int kEvery>
-__global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs A, float* states, int blocks, int groups) {
+template <typename E, bool kPair, bool kTma, bool kStates, int kL, int kEvery>
+__global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs A, float* states, int blocks, int groups,
+                                                                     const __grid_constant__ Maps<2> maps) {
   __shared__ Exchange xch;
+  extern __shared__ uint8_t raw[];
   constexpr int kTile = kWarps * kL;
   const int chain = blockIdx.x / blocks, rank = blockIdx.x - chain * blocks;
   const int b = chain / groups, group = chain - b * groups, warp = threadIdx.x >> 5;
@@ -270,21 +318,35 @@ __global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs 
   float2 carry = me.get(A.H_0 != nullptr ? A.H_0 + static_cast<int64_t>(b) * A.C : nullptr);
   const int rounds = (len + kTile * blocks - 1) / (kTile * blocks);
 
-  Raw2<E> ra[kL], rx[kL];
-  auto load = [&](int t0) {
-    load_rows<kPair>(ra, pa, A.a_stride, me.other, t0, len);
-    load_rows<kPair>(rx, px, A.x_stride, me.other, t0, len);
-  };
+  using Tiles = Ring<E, 2, kTile>;
+  const Tiles ring{align_smem(raw), xch.full};
+  const CUtensorMap* const from[2] = {&maps.m[0], &maps.m[1]};
+  Raw2<E> ra[kTma ? 1 : kL], rx[kTma ? 1 : kL];
   open_exchange(xch, blocks);
   int t0 = rank * kTile + warp * kL;
-  if (rounds > 0) load(t0);
+  auto load = [&](int round) {  // the tile of a round, if it has steps
+    if constexpr (kTma) {
+      const int t = (round * blocks + rank) * kTile;
+      if (threadIdx.x == 0 && t < len) ring.fill(round % Tiles::kStages, from, group * kChan, t, b);
+    } else if (round < rounds) {
+      load_rows<kPair>(ra, pa, A.a_stride, me.other, (round * blocks + rank) * kTile + warp * kL, len);
+      load_rows<kPair>(rx, px, A.x_stride, me.other, (round * blocks + rank) * kTile + warp * kL, len);
+    }
+  };
+  for (int i = 0; i < (kTma ? Tiles::kStages : 1); ++i) load(i);
   for (int it = 0; it < rounds; ++it) {
+    const int stage = it % Tiles::kStages;
+    if (kTma && (it * blocks + rank) * kTile < len &&
+        !mbar_wait(smem_u32(ring.full + stage), (it / Tiles::kStages) & 1, &xch.abort_flag, nullptr, 0))
+      carry = two(kSpoilt);
     float2 f[kL], in[kL], F = two(1.f), U = two(0.f);
 #pragma unroll
     for (int i = 0; i < kL; ++i) {
-      const Gate2 g = gate_of<false>(add_2(ra[i].f(), beta), alpha);
+      const Raw2<E> a = kTma ? load_2<true>(ring.row(stage, 0, warp * kL + i), 0) : ra[kTma ? 0 : i];
+      const Raw2<E> x = kTma ? load_2<true>(ring.row(stage, 1, warp * kL + i), 0) : rx[kTma ? 0 : i];
+      const Gate2 g = gate_of<false>(add_2(a.f(), beta), alpha);
       f[i] = g.f;
-      in[i] = mul_2(g.e, rx[i].f());
+      in[i] = mul_2(g.e, x.f());
     }
     if (t0 + kL > len) {  // steps behind the end leave the state as it is
 #pragma unroll
@@ -301,8 +363,9 @@ __global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs 
     }
     const int now = t0;
     t0 += kTile * blocks;
-    if (it + 1 < rounds) load(t0);
+    if (!kTma) load(it + 1);
     float2 h = state_before(xch, it, F, U, carry, rank, blocks);
+    if (kTma) load(it + Tiles::kStages);  // the block is done with this round's tile
     if constexpr (kStates) {
       float* p = states + (static_cast<int64_t>(b) * ((A.T + kEvery - 1) / kEvery) + now / kEvery) * A.C;
 #pragma unroll
@@ -328,6 +391,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs 
     }
   }
   let_next();
+  if (kTma && xch.abort_flag) drain(ring, (len - rank * kTile + kTile * blocks - 1) / (kTile * blocks));
   if constexpr (!kStates) {
     for (int t = rounds * kTile * blocks + rank * kWarps + warp; t < A.T; t += blocks * kWarps)
       store_2<kPair>(py + static_cast<int64_t>(t) * A.C, two(0.f), me.in0, me.in1);
@@ -338,10 +402,11 @@ __global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs 
 // ---------------------------------------------------------------------------
 // Backward
 // ---------------------------------------------------------------------------
-template <typename E, bool kPair, int kL>
+template <typename E, bool kPair, bool kTma, int kL>
 __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs A, const float* states, float* part, int blocks,
-                                                                      int groups) {
+                                                                      int groups, const __grid_constant__ Maps<3> maps) {
   __shared__ Exchange xch;
+  extern __shared__ uint8_t raw[];
   constexpr int kTile = kWarps * kL;
   const int chain = blockIdx.x / blocks, rank = blockIdx.x - chain * blocks;
   const int b = chain / groups, group = chain - b * groups, warp = threadIdx.x >> 5;
@@ -361,27 +426,42 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs
 
   // Rounds go from the end: block 0 has the last tile, warp 0 the last segment of it.
   int t0 = ((tiles - 1 - rank) * kWarps + kWarps - 1 - warp) * kL;
-  Raw2<E> ra[kL], rx[kL], rd[kL];
+  using Tiles = Ring<E, 3, kTile>;
+  const Tiles ring{align_smem(raw), xch.full};
+  const CUtensorMap* const from[3] = {&maps.m[0], &maps.m[1], &maps.m[2]};
+  Raw2<E> ra[kTma ? 1 : kL], rx[kTma ? 1 : kL], rd[kTma ? 1 : kL];
   float2 hs = two(0.f);
-  auto load = [&](int t0) {  // (before the sequence as behind it: zeros)
-    const int from = t0 < 0 ? len : t0;
-    load_rows<kPair>(ra, pa, A.a_stride, me.other, from, len);
-    load_rows<kPair>(rx, px, A.x_stride, me.other, from, len);
-    load_rows<kPair>(rd, pd, A.C, me.other, from, len);
+  auto load = [&](int round) {  // the tile of a round; before the sequence as behind it: zeros
+    const int tile = tiles - 1 - (round * blocks + rank);
+    if constexpr (kTma) {
+      if (threadIdx.x == 0 && tile >= 0) ring.fill(round % Tiles::kStages, from, group * kChan, tile * kTile, b);
+    } else if (round < rounds) {
+      const int t = tile < 0 ? len : tile * kTile + (kWarps - 1 - warp) * kL;
+      load_rows<kPair>(ra, pa, A.a_stride, me.other, t, len);
+      load_rows<kPair>(rx, px, A.x_stride, me.other, t, len);
+      load_rows<kPair>(rd, pd, A.C, me.other, t, len);
+    }
   };
   auto load_state = [&](int t0) {
     if (t0 >= 0 && t0 < len) hs = me.get(ph + static_cast<int64_t>(t0 / kL) * A.C);
   };
   open_exchange(xch, blocks);
-  if (rounds > 0) load(t0);
+  for (int i = 0; i < (kTma ? Tiles::kStages : 1); ++i) load(i);
   wait_previous();
   if (rounds > 0) load_state(t0);
   for (int it = 0; it < rounds; ++it) {
+    const int stage = it % Tiles::kStages, r0 = (kWarps - 1 - warp) * kL;
+    if (kTma && tiles - 1 - (it * blocks + rank) >= 0 &&
+        !mbar_wait(smem_u32(ring.full + stage), (it / Tiles::kStages) & 1, &xch.abort_flag, nullptr, 0))
+      carry = two(kSpoilt);
     float2 f[kL], e[kL], ma[kL], ms[kL], dy[kL], F = two(1.f), U = two(0.f);
     float2 h = hs;
 #pragma unroll
     for (int i = 0; i < kL; ++i) {
-      const float2 z = add_2(ra[i].f(), beta), x = rx[i].f();
+      const Raw2<E> qa = kTma ? load_2<true>(ring.row(stage, 0, r0 + i), 0) : ra[kTma ? 0 : i];
+      const Raw2<E> qx = kTma ? load_2<true>(ring.row(stage, 1, r0 + i), 0) : rx[kTma ? 0 : i];
+      const Raw2<E> qd = kTma ? load_2<true>(ring.row(stage, 2, r0 + i), 0) : rd[kTma ? 0 : i];
+      const float2 z = add_2(qa.f(), beta), x = qx.f();
       const Gate2 g = gate_of<true>(z, alpha);
       f[i] = g.f;
       e[i] = g.e;
@@ -391,14 +471,14 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs
       ma[i] = mul_2(away, mul_2(minus_alpha, sig));
       ms[i] = mul_2(away, make_float2(-g.soft.x, -g.soft.y));
       h = fma_2(g.f, h, mul_2(g.e, x));
-      dy[i] = rd[i].f();
+      dy[i] = qd.f();
     }
     if (t0 < 0 || t0 + kL > len) {  // steps that are not there hand the gradient on
 #pragma unroll
       for (int i = 0; i < kL; ++i)
         if (t0 < 0 || t0 + i >= len) {
           f[i] = two(1.f);
-          ma[i] = ms[i] = two(0.f);
+          ma[i] = ms[i] = dy[i] = two(0.f);
         }
     }
 #pragma unroll
@@ -408,11 +488,10 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs
     }
     const int now = t0;
     t0 -= kTile * blocks;
-    if (it + 1 < rounds) {
-      load(t0);
-      load_state(t0);
-    }
+    if (!kTma) load(it + 1);
+    if (it + 1 < rounds) load_state(t0);
     float2 c = state_before(xch, it, F, U, carry, rank, blocks);
+    if (kTma) load(it + Tiles::kStages);
     if (now >= 0) {
 #pragma unroll
       for (int i = kL - 1; i >= 0; --i) {
@@ -431,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs
     }
   }
   let_next();
+  if (kTma && xch.abort_flag) drain(ring, (tiles - rank + blocks - 1) / blocks);
   for (int t = tiles * kTile + rank * kWarps + warp; t < A.T; t += blocks * kWarps) {
     store_2<kPair>(pdx + static_cast<int64_t>(t) * A.C, two(0.f), me.in0, me.in1);
     store_2<kPair>(pda + static_cast<int64_t>(t) * A.C, two(0.f), me.in0, me.in1);
@@ -472,28 +552,31 @@ __global__ void __launch_bounds__(128) linear_step_kernel(float* H, LinearArgs A
   store_2<kPair>(static_cast<E*>(A.y) + at + me.c, h, me.in0, me.in1);
 }
 
-// Sums over parts: eight warps of a block take every eighth part each of 32
-// columns, then add up in order.
-__global__ void __launch_bounds__(256) sum_parts_kernel(const float* part, float* out, float* out2, int parts, int64_t D,
-                                                        int64_t width) {
-  __shared__ float red[8][32];
+// Sums over parts: the warps of a block take parts in turn, each of 32 columns,
+// then add up in order.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(32 * kSumWarps) sum_parts_kernel(const float* part, float* out, float* out2, int parts,
+                                                                   int64_t D, int64_t width) {
+  __shared__ float red[kSumWarps][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   wait_previous();
   float t = 0.f;
   if (j < width) {
-#pragma unroll 4
-    for (int p = warp; p < parts; p += 8) t += part[p * width + j];
+#pragma unroll 8
+    for (int p = warp; p < parts; p += kSumWarps) t += part[p * width + j];
   }
   red[warp][lane] = t;
   __syncthreads();
-  if (warp != 0 || j >= width) return;
+  // lane w of warp c has what warp w found of columns c, so that the tree's order is fixed
+  for (int c = warp; c < 32; c += kSumWarps) {
+    float v = red[lane][c];
 #pragma unroll
-  for (int w = 1; w < 8; ++w) t += red[w][lane];
-  if (j < D)
-    out[j] = t;
-  else if (out2 != nullptr)
-    out2[j - D] = t;
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int64_t k = static_cast<int64_t>(blockIdx.x) * 32 + c;
+    if (lane == 0 && k < D) out[k] = v;
+    if (lane == 0 && k >= D && k < width && out2 != nullptr) out2[k - D] = v;
+  }
 }
 
 constexpr int kEveryBf16 = 8, kEveryF32 = 4;  // steps of a segment of the backward
@@ -508,7 +591,7 @@ int cluster_blocks(const LinearArgs& a, int tile) {
 }
 
 template <typename... P, typename... V>
-cudaError_t launch_cluster(void (*kernel)(P...), int64_t grid, int blocks, bool behind, cudaStream_t s, V... args) {
+cudaError_t launch_cluster(void (*kernel)(P...), int64_t grid, int blocks, int smem, bool behind, cudaStream_t s, V... args) {
   cudaLaunchAttribute at[2] = {};
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = blocks;
@@ -518,38 +601,71 @@ cudaError_t launch_cluster(void (*kernel)(P...), int64_t grid, int blocks, bool 
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(static_cast<unsigned>(grid));
   c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = smem;
   c.stream = s;
   c.attrs = at;
   c.numAttrs = behind ? 2 : 1;
   return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
 }
 
-// Whether rows can be read and written two channels at a time.
-bool paired(const LinearArgs& a) {
-  const uintptr_t two = a.bf16 ? 3 : 7;
-  return a.C % 2 == 0 && a.x_stride % 2 == 0 && a.a_stride % 2 == 0 &&
-         ((reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.a)) & two) == 0;
+// How rows can be read: value by value, two channels at a time, or by TMA.
+enum class Access { kSingle, kPair, kTma };
+Access access_of(const LinearArgs& a) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.a);
+  const int e = a.bf16 ? 2 : 4;
+  auto all = [&](int bytes) {
+    return a.C * e % bytes == 0 && a.x_stride * e % bytes == 0 && a.a_stride * e % bytes == 0 && at % bytes == 0;
+  };
+  return all(16) ? Access::kTma : all(2 * e) ? Access::kPair : Access::kSingle;
 }
 
-template <typename E, bool kPair, int kL, int kEvery>
-cudaError_t forward(const LinearArgs& a, cudaStream_t s) {
-  const int groups = (a.C + kChan - 1) / kChan, blocks = cluster_blocks(a, kWarps * kL);
-  return launch_cluster(linear_forward_kernel<E, kPair, false, kL, kEvery>, static_cast<int64_t>(a.B) * groups * blocks,
-                        blocks, false, s, a, nullptr, blocks, groups);
+// Tiles of `rows` steps of 64 channels of [B,T,C].
+bool map_rows(CUtensorMap* m, const LinearArgs& a, const void* p, int64_t stride, int rows) {
+  const uint64_t e = a.bf16 ? 2 : 4;
+  const uint64_t dims[3] = {static_cast<uint64_t>(a.C), static_cast<uint64_t>(a.T), static_cast<uint64_t>(a.B)};
+  const uint64_t strides[2] = {stride * e, stride * e * a.T};
+  const uint32_t box[3] = {kChan, static_cast<uint32_t>(rows), 1};
+  return make_tensor_map(m, a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p, 3, dims, strides,
+                         box, false);
 }
 
-template <typename E, bool kPair, int kL, int kEvery>
+template <typename E, bool kPair, bool kTma, bool kStates, int kL, int kEvery>
+cudaError_t forward(const LinearArgs& a, float* states, cudaStream_t s) {
+  constexpr int kTile = kWarps * kL, kSmem = kTma ? Ring<E, 2, kTile>::kBytes + 128 : 0;
+  static std::atomic<uint64_t> ready{0};
+  const auto kernel = linear_forward_kernel<E, kPair, kTma, kStates, kL, kEvery>;
+  Maps<2> maps{};
+  if constexpr (kTma) {
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kSmem, ready);
+    if (e != cudaSuccess) return e;
+    if (!map_rows(&maps.m[0], a, a.a, a.a_stride, kTile) || !map_rows(&maps.m[1], a, a.x, a.x_stride, kTile))
+      return cudaErrorInvalidValue;
+  }
+  const int groups = (a.C + kChan - 1) / kChan, blocks = cluster_blocks(a, kTile);
+  return launch_cluster(kernel, static_cast<int64_t>(a.B) * groups * blocks, blocks, kSmem, false, s, a, states, blocks, groups,
+                        maps);
+}
+
+template <typename E, bool kPair, bool kTma, int kL, int kEvery>
 cudaError_t backward(const LinearArgs& a, cudaStream_t s) {
-  const int groups = (a.C + kChan - 1) / kChan;
-  const int64_t chains = static_cast<int64_t>(a.B) * groups;
+  constexpr int kTile = kWarps * kEvery, kSmem = kTma ? Ring<E, 3, kTile>::kBytes + 128 : 0;
   float* part = static_cast<float*>(a.ws);
   float* states = part + static_cast<int64_t>(a.B) * kMaxCluster * 2 * a.C;
-  const int before = cluster_blocks(a, kWarps * kL), blocks = cluster_blocks(a, kWarps * kEvery);
-  cudaError_t e = launch_cluster(linear_forward_kernel<E, kPair, true, kL, kEvery>, chains * before, before, false, s, a,
-                                 states, before, groups);
+  cudaError_t e = forward<E, kPair, kTma, true, kL, kEvery>(a, states, s);
   if (e != cudaSuccess) return e;
-  e = launch_cluster(linear_backward_kernel<E, kPair, kEvery>, chains * blocks, blocks, true, s, a, states, part, blocks,
-                     groups);
+  static std::atomic<uint64_t> ready{0};
+  const auto kernel = linear_backward_kernel<E, kPair, kTma, kEvery>;
+  Maps<3> maps{};
+  if constexpr (kTma) {
+    e = allow_smem(reinterpret_cast<const void*>(kernel), kSmem, ready);
+    if (e != cudaSuccess) return e;
+    if (!map_rows(&maps.m[0], a, a.a, a.a_stride, kTile) || !map_rows(&maps.m[1], a, a.x, a.x_stride, kTile) ||
+        !map_rows(&maps.m[2], a, a.dy, a.C, kTile))
+      return cudaErrorInvalidValue;
+  }
+  const int groups = (a.C + kChan - 1) / kChan, blocks = cluster_blocks(a, kTile);
+  e = launch_cluster(kernel, static_cast<int64_t>(a.B) * groups * blocks, blocks, kSmem, true, s, a, states, part, blocks, groups,
+                     maps);
   if (e != cudaSuccess) return e;
   return launch_sum_parts(part, a.dalpha, a.dbeta, true, a.B * blocks, a.C, s);
 }
@@ -562,25 +678,40 @@ size_t linear_backward_scratch_bytes(int64_t B, int64_t T, int64_t C) {
 
 cudaError_t launch_sum_parts(const float* part, float* out, float* out2, bool two, int parts, int64_t D, cudaStream_t s) {
   const int64_t width = two ? 2 * D : D;
-  return launch_next(sum_parts_kernel, static_cast<unsigned>((width + 31) / 32), 256, 0, s, part, out, out2, parts, D, width);
+  return launch_next(sum_parts_kernel, static_cast<unsigned>((width + 31) / 32), 32 * kSumWarps, 0, s, part, out, out2, parts, D, width);
 }
 
+// Steps of a segment: 16 in bf16, 8 in fp32 (registers); of the backward's, kEvery.
 cudaError_t launch_linear_forward(const LinearArgs& a, cudaStream_t s) {
-  if (paired(a))
-    return a.bf16 ? forward<uint16_t, true, 16, kEveryBf16>(a, s) : forward<float, true, 8, kEveryF32>(a, s);
-  return a.bf16 ? forward<uint16_t, false, 16, kEveryBf16>(a, s) : forward<float, false, 8, kEveryF32>(a, s);
+  switch (access_of(a)) {
+    case Access::kTma:
+      return a.bf16 ? forward<uint16_t, true, true, false, 16, kEveryBf16>(a, nullptr, s)
+                    : forward<float, true, true, false, 8, kEveryF32>(a, nullptr, s);
+    case Access::kPair:
+      return a.bf16 ? forward<uint16_t, true, false, false, 16, kEveryBf16>(a, nullptr, s)
+                    : forward<float, true, false, false, 8, kEveryF32>(a, nullptr, s);
+    default:
+      return a.bf16 ? forward<uint16_t, false, false, false, 16, kEveryBf16>(a, nullptr, s)
+                    : forward<float, false, false, false, 8, kEveryF32>(a, nullptr, s);
+  }
 }
 
 cudaError_t launch_linear_backward(const LinearArgs& a, cudaStream_t s) {
-  if (paired(a))
-    return a.bf16 ? backward<uint16_t, true, 16, kEveryBf16>(a, s) : backward<float, true, 8, kEveryF32>(a, s);
-  return a.bf16 ? backward<uint16_t, false, 16, kEveryBf16>(a, s) : backward<float, false, 8, kEveryF32>(a, s);
+  switch (access_of(a)) {
+    case Access::kTma:
+      return a.bf16 ? backward<uint16_t, true, true, 16, kEveryBf16>(a, s) : backward<float, true, true, 8, kEveryF32>(a, s);
+    case Access::kPair:
+      return a.bf16 ? backward<uint16_t, true, false, 16, kEveryBf16>(a, s) : backward<float, true, false, 8, kEveryF32>(a, s);
+    default:
+      return a.bf16 ? backward<uint16_t, false, false, 16, kEveryBf16>(a, s)
+                    : backward<float, false, false, 8, kEveryF32>(a, s);
+  }
 }
 
 cudaError_t launch_linear_step(float* H, const LinearArgs& a, cudaStream_t s) {
   const int groups = (a.C + kChan - 1) / kChan;
   const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(a.B) * groups + 3) / 4);
-  if (paired(a)) {
+  if (access_of(a) != Access::kSingle) {
     if (a.bf16)
       linear_step_kernel<uint16_t, true><<<grid, 128, 0, s>>>(H, a, groups);
     else

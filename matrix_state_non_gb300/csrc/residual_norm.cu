@@ -5,10 +5,10 @@
 //     dx = s p - r s^3 h / D + dh,   dw = sum over rows of dy (*) h s.
 //
 // Bound by HBM: a team of 1 to 16 warps has a row in registers, reads and
-// writes it once, and goes from row to row with w in registers.  A lane holds
-// groups of 8 neighbouring values (kVec: 16-byte accesses, where every row lies
-// on 16 bytes), or values 32 apart; either way 128 values that share a scale are
-// in one warp.  Sums run in a fixed order.
+// writes it once, and goes from row to row with w in registers, the next row's
+// inputs on their way.  A lane holds groups of 8 neighbouring values (kVec:
+// 16-byte accesses, where every row lies on 16 bytes), or values 32 apart; either
+// way 128 values that share a scale are in one warp.  Sums run in a fixed order.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -25,22 +25,34 @@ __device__ __forceinline__ float sum_lanes(float v) {
   return v;
 }
 
-// The sum over a team of kTeam warps (a block, where that is more than one).
+// Teams of kTeam warps: a block of eight warps has one or several, one of
+// sixteen is a block.
 template <int kTeam>
-__device__ __forceinline__ float2 sum_team(float a, float b, float2 (&red)[2][kTeam], int turn) {
+struct Team {
+  static constexpr int kWarps = kTeam > 8 ? kTeam : 8, kTeams = kWarps / kTeam, kThreads = 32 * kWarps;
+  float2 red[2][kWarps];
+};
+
+// The sums over a team, in every thread.
+template <int kTeam>
+__device__ __forceinline__ float2 sum_team(float a, float b, Team<kTeam>& t, int turn) {
   a = sum_lanes(a);
   b = sum_lanes(b);
   if constexpr (kTeam == 1) return make_float2(a, b);
-  float2* r = red[turn & 1];  // two in turn: one barrier is enough
-  if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = make_float2(a, b);
-  __syncthreads();
-  float2 t = r[0];
+  const int warp = threadIdx.x >> 5, team = warp / kTeam;
+  float2* r = t.red[turn & 1] + team * kTeam;  // two in turn: one barrier is enough
+  if ((threadIdx.x & 31) == 0) r[warp - team * kTeam] = make_float2(a, b);
+  if constexpr (Team<kTeam>::kTeams == 1)
+    __syncthreads();
+  else
+    named_bar_sync(1 + team, 32 * kTeam);
+  float2 s = r[0];
 #pragma unroll
   for (int w = 1; w < kTeam; ++w) {
-    t.x += r[w].x;
-    t.y += r[w].y;
+    s.x += r[w].x;
+    s.y += r[w].y;
   }
-  return t;
+  return s;
 }
 
 // A thread's share of a row of up to 256 kPer kTeam values: kPer groups of 8.
@@ -48,7 +60,7 @@ __device__ __forceinline__ float2 sum_team(float a, float b, float2 (&red)[2][kT
 template <int kTeam, int kPer, bool kVec>
 struct Share {
   int lane, warp;
-  __device__ __forceinline__ Share() : lane(threadIdx.x & 31), warp(kTeam == 1 ? 0 : threadIdx.x >> 5) {}
+  __device__ __forceinline__ Share() : lane(threadIdx.x & 31), warp((threadIdx.x >> 5) % kTeam) {}
   __device__ __forceinline__ int at(int i, int e) const {
     return kVec ? 8 * (lane + 32 * (warp * kPer + i)) + e : lane + 32 * (e + 8 * (warp * kPer + i));
   }
@@ -107,60 +119,52 @@ __device__ __forceinline__ uint32_t e4m3_2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
-constexpr int kRowsPerBlock = 8;  // teams of one warp
-template <int kTeam>
-constexpr int kThreadsOf = kTeam == 1 ? 32 * kRowsPerBlock : 32 * kTeam;
+// Blocks per SM: registers, by the groups of a lane.
+template <int kTeam, int kPer>
+constexpr int kBlocksPerSm = kTeam > 8 ? 1 : kPer == 1 ? 4 : kPer == 2 ? 3 : 2;
 
 template <typename X, typename H, int kTeam, int kPer, bool kVec>
-__global__ void __launch_bounds__(kThreadsOf<kTeam>) residual_norm_kernel(NormRowsArgs A) {
-  __shared__ float2 red[2][kTeam];
+__global__ void __launch_bounds__(Team<kTeam>::kThreads, kBlocksPerSm<kTeam, kPer>) residual_norm_kernel(NormRowsArgs A) {
+  __shared__ Team<kTeam> team;
   using S = Share<kTeam, kPer, kVec>;
+  constexpr int kTeams = Team<kTeam>::kTeams;
   const S me;
   const int D = A.D, blocks = (D + kScaleBlock - 1) / kScaleBlock;
-  const int64_t teams = kTeam == 1 ? gridDim.x * static_cast<int64_t>(kRowsPerBlock) : gridDim.x;
-  const int64_t team = kTeam == 1 ? blockIdx.x * static_cast<int64_t>(kRowsPerBlock) + (threadIdx.x >> 5) : blockIdx.x;
-  typename S::template Raw<float> w;
-  // w is allocated to 16 bytes; its end is guarded by value
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kTeams + (threadIdx.x >> 5) / kTeam;
+  float w[kPer][8];
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      float e[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) e[k] = me.at(i, 4 * q + k) < D ? A.w[me.at(i, 4 * q + k)] : 0.f;
-      w.v[i][q] = make_uint4(__float_as_uint(e[0]), __float_as_uint(e[1]), __float_as_uint(e[2]), __float_as_uint(e[3]));
-    }
-  int turn = 0;
-  for (int64_t row = team; row < A.rows; row += teams, ++turn) {
+    for (int e = 0; e < 8; ++e) w[i][e] = me.at(i, e) < D ? A.w[me.at(i, e)] : 0.f;
+  typename S::template Raw<X> x;
+  typename S::template Raw<H> r;
+  const bool added = A.residual != nullptr;
+  auto load = [&](int64_t at) {
+    me.load(x, static_cast<const X*>(A.x) + at * A.x_stride, D);
+    if (added) me.load(r, static_cast<const H*>(A.residual) + at * D, D);
+  };
+  constexpr bool kAhead = kPer == 1;  // registers for the next row's inputs
+  if (kAhead && row < A.rows) load(row);
+  for (int turn = 0; row < A.rows; row += step, ++turn) {
+    if (!kAhead) load(row);
     float h[kPer][8], ss = 0.f;
-    {
-      typename S::template Raw<X> x;
-      me.load(x, static_cast<const X*>(A.x) + row * A.x_stride, D);
-      if (A.residual != nullptr) {
-        typename S::template Raw<H> r;
-        me.load(r, static_cast<const H*>(A.residual) + row * D, D);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
+    for (int i = 0; i < kPer; ++i)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) h[i][e] = me.get(x, i, e) + me.get(r, i, e);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) h[i][e] = me.get(x, i, e);
-      }
-    }
+      for (int e = 0; e < 8; ++e) h[i][e] = me.get(x, i, e) + (added ? me.get(r, i, e) : 0.f);
+    if (kAhead && row + step < A.rows) load(row + step);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(h[i][e], h[i][e], ss);
       if (A.h != nullptr) me.store(static_cast<H*>(A.h) + row * D, i, h[i], D);
     }
-    const float s = rsqrtf(sum_team<kTeam>(ss, 0.f, red, turn).x / static_cast<float>(D) + A.eps);
+    const float s = rsqrtf(sum_team<kTeam>(ss, 0.f, team, turn).x / static_cast<float>(D) + A.eps);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] * s * me.get(w, i, e);
+      for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] * s * w[i][e];
       if (A.y_type == M2RNN_BF16) me.store(static_cast<uint16_t*>(A.y) + row * D, i, h[i], D);
       if (A.y_type == M2RNN_F32) me.store(static_cast<float*>(A.y) + row * D, i, h[i], D);
     }
@@ -205,15 +209,17 @@ __global__ void __launch_bounds__(kThreadsOf<kTeam>) residual_norm_kernel(NormRo
 }
 
 template <typename H, typename G, int kTeam, int kPer, bool kVec>
-__global__ void __launch_bounds__(kThreadsOf<kTeam>) residual_norm_backward_kernel(NormRowsArgs A) {
-  __shared__ float2 red[2][kTeam];
-  __shared__ float dws[kTeam == 1 ? kRowsPerBlock : 1][kTeam == 1 ? 256 * kPer : 1];
+__global__ void __launch_bounds__(Team<kTeam>::kThreads, kPer == 1 ? 3 : 1) residual_norm_backward_kernel(NormRowsArgs A) {
+  __shared__ Team<kTeam> team;
   using S = Share<kTeam, kPer, kVec>;
+  constexpr int kTeams = Team<kTeam>::kTeams, kWidth = 256 * kPer * kTeam;
+  __shared__ float dws[kTeams > 1 ? kTeams : 1][kTeams > 1 ? kWidth : 1];
   const S me;
   const int D = A.D;
   const float inv = 1.f / static_cast<float>(D);
-  const int64_t teams = kTeam == 1 ? gridDim.x * static_cast<int64_t>(kRowsPerBlock) : gridDim.x;
-  const int64_t team = kTeam == 1 ? blockIdx.x * static_cast<int64_t>(kRowsPerBlock) + (threadIdx.x >> 5) : blockIdx.x;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kTeams;
+  const int mine = (threadIdx.x >> 5) / kTeam;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * kTeams + mine;
   float w[kPer][8], dw[kPer][8];
 #pragma unroll
   for (int i = 0; i < kPer; ++i)
@@ -222,12 +228,23 @@ __global__ void __launch_bounds__(kThreadsOf<kTeam>) residual_norm_backward_kern
       w[i][e] = me.at(i, e) < D ? A.w[me.at(i, e)] : 0.f;
       dw[i][e] = 0.f;
     }
-  int turn = 0;
-  for (int64_t row = team; row < A.rows; row += teams, ++turn) {
-    typename S::template Raw<H> h;
-    typename S::template Raw<G> g;
-    me.load(h, static_cast<const H*>(A.h) + row * D, D);
-    me.load(g, static_cast<const G*>(A.dy) + row * D, D);
+  typename S::template Raw<H> nh;
+  typename S::template Raw<G> ng;
+  typename S::template Raw<float> nu;
+  const bool added = A.dh != nullptr;
+  auto load = [&](int64_t at) {
+    me.load(nh, static_cast<const H*>(A.h) + at * D, D);
+    me.load(ng, static_cast<const G*>(A.dy) + at * D, D);
+    if (added) me.load(nu, A.dh + at * D, D);
+  };
+  constexpr bool kAhead = kPer == 1;
+  if (kAhead && row < A.rows) load(row);
+  for (int turn = 0; row < A.rows; row += step, ++turn) {
+    if (!kAhead) load(row);
+    const typename S::template Raw<H> h = nh;
+    const typename S::template Raw<G> g = ng;
+    const typename S::template Raw<float> up = nu;
+    if (kAhead && row + step < A.rows) load(row + step);
     float ss = 0.f, rr = 0.f;
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
@@ -237,48 +254,32 @@ __global__ void __launch_bounds__(kThreadsOf<kTeam>) residual_norm_backward_kern
         ss = fmaf(v, v, ss);
         rr = fmaf(v, me.get(g, i, e) * w[i][e], rr);
       }
-    const float2 t = sum_team<kTeam>(ss, rr, red, turn);
+    const float2 t = sum_team<kTeam>(ss, rr, team, turn);
     const float s = rsqrtf(t.x * inv + A.eps), c = t.y * s * s * s * inv;
-    const float* up = A.dh != nullptr ? A.dh + row * D : nullptr;
-    float* out = A.dx + row * D;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       float d[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) d[e] = 0.f;
-      if (up != nullptr) {
-        if constexpr (kVec) {
-          if (me.at(i, 0) < D) {
-            const float4 a = *reinterpret_cast<const float4*>(up + me.at(i, 0)), b = *reinterpret_cast<const float4*>(up + me.at(i, 4));
-            d[0] = a.x, d[1] = a.y, d[2] = a.z, d[3] = a.w, d[4] = b.x, d[5] = b.y, d[6] = b.z, d[7] = b.w;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (me.at(i, e) < D) d[e] = up[me.at(i, e)];
-        }
-      }
-#pragma unroll
       for (int e = 0; e < 8; ++e) {
         const float v = me.get(h, i, e), p = me.get(g, i, e);
-        d[e] += s * (p * w[i][e]) - c * v;
+        d[e] = s * (p * w[i][e]) - c * v + (added ? me.get(up, i, e) : 0.f);
         dw[i][e] = fmaf(p, v * s, dw[i][e]);
       }
-      me.store(out, i, d, D);
+      me.store(A.dx + row * D, i, d, D);
     }
   }
   let_next();
   float* part = A.part + static_cast<int64_t>(blockIdx.x) * D;
-  if constexpr (kTeam == 1) {  // the block's eight warps, in order
+  if constexpr (kTeams > 1) {  // the block's teams, in order
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) dws[threadIdx.x >> 5][me.at(i, e)] = dw[i][e];
+      for (int e = 0; e < 8; ++e) dws[mine][me.at(i, e)] = dw[i][e];
     __syncthreads();
-    for (int j = threadIdx.x; j < D; j += 32 * kRowsPerBlock) {
+    for (int j = threadIdx.x; j < D; j += Team<kTeam>::kThreads) {
       float t = dws[0][j];
 #pragma unroll
-      for (int k = 1; k < kRowsPerBlock; ++k) t += dws[k][j];
+      for (int k = 1; k < kTeams; ++k) t += dws[k][j];
       part[j] = t;
     }
   } else {
@@ -294,38 +295,34 @@ __global__ void __launch_bounds__(kThreadsOf<kTeam>) residual_norm_backward_kern
 struct NormShape {
   int team, per;
 };
-NormShape norm_shape(int D) {
+NormShape norm_shape(int64_t D) {
   if (D <= 256) return {1, 1};
-  if (D <= 512) return {1, 2};
-  if (D <= 1024) return {1, 4};
-  if (D <= 2048) return {2, 4};
-  if (D <= 4096) return {4, 4};
-  if (D <= 8192) return {8, 4};
+  if (D <= 512) return {2, 1};
+  if (D <= 1024) return {4, 1};
+  if (D <= 2048) return {8, 1};
+  if (D <= 4096) return {8, 2};
+  if (D <= 8192) return {16, 2};
   return {16, 4};
 }
 
-constexpr int kSms = 152;
-
-int forward_grid(int64_t rows, const NormShape& sh) {
-  const int64_t blocks = sh.team == 1 ? (rows + kRowsPerBlock - 1) / kRowsPerBlock : rows;
-  const int64_t most = sh.team == 1 ? 4 * kSms : kSms * (32 / sh.team);
+// As many blocks as run at once, or as there are rows for.
+int norm_grid(int64_t rows, const NormShape& sh, int per_sm) {
+  const int teams = sh.team >= 8 ? 1 : 8 / sh.team;
+  const int64_t blocks = (rows + teams - 1) / teams, most = 152 * per_sm;
   return static_cast<int>(blocks < most ? blocks : most);
 }
+
+#define M2RNN_NORM_SHAPES(CASE) \
+  CASE(1, 1) CASE(2, 1) CASE(4, 1) CASE(8, 1) CASE(8, 2) CASE(16, 2) CASE(16, 4)
 
 template <typename X, typename H, bool kVec>
 cudaError_t forward(const NormRowsArgs& a, cudaStream_t s) {
   const NormShape sh = norm_shape(a.D);
-  const int grid = forward_grid(a.rows, sh);
-#define M2RNN_NORM_CASE(TEAM, PER)                                                          \
-  if (sh.team == TEAM && sh.per == PER)                                                     \
-  residual_norm_kernel<X, H, TEAM, PER, kVec><<<grid, kThreadsOf<TEAM>, 0, s>>>(a)
-  M2RNN_NORM_CASE(1, 1);
-  M2RNN_NORM_CASE(1, 2);
-  M2RNN_NORM_CASE(1, 4);
-  M2RNN_NORM_CASE(2, 4);
-  M2RNN_NORM_CASE(4, 4);
-  M2RNN_NORM_CASE(8, 4);
-  M2RNN_NORM_CASE(16, 4);
+#define M2RNN_NORM_CASE(TEAM, PER)                                                                       \
+  if (sh.team == TEAM && sh.per == PER)                                                                  \
+    residual_norm_kernel<X, H, TEAM, PER, kVec>                                                          \
+        <<<norm_grid(a.rows, sh, kBlocksPerSm<TEAM, PER>), Team<TEAM>::kThreads, 0, s>>>(a);
+  M2RNN_NORM_SHAPES(M2RNN_NORM_CASE)
 #undef M2RNN_NORM_CASE
   return cudaGetLastError();
 }
@@ -333,16 +330,10 @@ cudaError_t forward(const NormRowsArgs& a, cudaStream_t s) {
 template <typename H, typename G, bool kVec>
 cudaError_t backward(const NormRowsArgs& a, int grid, cudaStream_t s) {
   const NormShape sh = norm_shape(a.D);
-#define M2RNN_NORM_CASE(TEAM, PER)                                                          \
-  if (sh.team == TEAM && sh.per == PER)                                                     \
-  residual_norm_backward_kernel<H, G, TEAM, PER, kVec><<<grid, kThreadsOf<TEAM>, 0, s>>>(a)
-  M2RNN_NORM_CASE(1, 1);
-  M2RNN_NORM_CASE(1, 2);
-  M2RNN_NORM_CASE(1, 4);
-  M2RNN_NORM_CASE(2, 4);
-  M2RNN_NORM_CASE(4, 4);
-  M2RNN_NORM_CASE(8, 4);
-  M2RNN_NORM_CASE(16, 4);
+#define M2RNN_NORM_CASE(TEAM, PER)      \
+  if (sh.team == TEAM && sh.per == PER) \
+    residual_norm_backward_kernel<H, G, TEAM, PER, kVec><<<grid, Team<TEAM>::kThreads, 0, s>>>(a);
+  M2RNN_NORM_SHAPES(M2RNN_NORM_CASE)
 #undef M2RNN_NORM_CASE
   return cudaGetLastError();
 }
@@ -350,10 +341,8 @@ cudaError_t backward(const NormRowsArgs& a, int grid, cudaStream_t s) {
 }  // namespace
 
 int norm_rows_parts(int64_t rows, int64_t D) {
-  const NormShape sh = norm_shape(static_cast<int>(D));
-  const int64_t blocks = sh.team == 1 ? (rows + kRowsPerBlock - 1) / kRowsPerBlock : rows;
-  const int64_t most = sh.team == 1 ? 2 * kSms : kSms * (16 / sh.team);
-  return static_cast<int>(blocks < most ? blocks : most);
+  const NormShape sh = norm_shape(D);
+  return norm_grid(rows, sh, sh.per == 1 ? 3 : sh.team == 8 ? 2 : 1);
 }
 
 cudaError_t launch_residual_norm(const NormRowsArgs& a, cudaStream_t s) {
