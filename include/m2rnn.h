@@ -536,7 +536,8 @@ int m2rnn_linear_step(float* H, const void* x, int64_t x_stride, const void* a, 
  *     `steps` times:  A = X X^T,  X <- a X + (b A + c A A) X,
  *     a = 3.4445, b = -4.7750, c = 2.0315.
  *   g [n,rows,cols] in `dtype`; out [n,rows,cols] bf16 (may be g, where that
- *   is bf16);  rows, cols in [1, 16384], n <= 65535, 1 <= steps <= 32,
+ *   is bf16);  rows, cols in [1, 16384], n <= 65535 (2^38 values in all),
+ *   1 <= steps <= 32,
  *   eps >= 0.
  * The workspace (m2rnn_orthogonalize_workspace_size bytes, 0 for an unsupported
  * shape) begins with a status block (see m2rnn_sync_status) that the call clears.

@@ -91,7 +91,7 @@ bool linear_inputs_ok(const LinearArgs& a) {
 
 int ortho_dims(int64_t n, int64_t rows, int64_t cols) {
   if (n < 1 || rows < 1 || cols < 1) return M2RNN_ERR_INVALID_ARG;
-  if (n > 65535 || rows > kOrthoMaxDim || cols > kOrthoMaxDim) return M2RNN_ERR_UNSUPPORTED;
+  if (n > 65535 || rows > kOrthoMaxDim || cols > kOrthoMaxDim || n * rows * cols > (1ll << 38)) return M2RNN_ERR_UNSUPPORTED;
   return M2RNN_OK;
 }
 

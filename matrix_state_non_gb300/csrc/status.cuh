@@ -37,6 +37,9 @@ constexpr uint32_t kWhereOutFull = 401, kWhereOutP = 402, kWhereOutScores = 403,
                    kWhereOutEmpty = 405, kWhereOutDrain = 406;
 constexpr uint32_t kWhereWalkFull = 411, kWhereWalkSplit = 412, kWhereWalkDone = 413, kWhereWalkEmpty = 414,
                    kWhereWalkFree = 415, kWhereWalkDrain = 416;
+// The orthogonalised update's products.
+constexpr uint32_t kWhereOrthoFull = 421, kWhereOrthoEmpty = 422, kWhereOrthoDone = 423, kWhereOrthoFree = 424,
+                   kWhereOrthoDrain = 425;
 
 __device__ __forceinline__ void report_device_error(StatusBlock* s, unsigned int code,
                                                     uint32_t where) {
