@@ -10,7 +10,7 @@ namespace m2rnn {
 // A tiled tensor map of up to 5 dimensions, innermost first (strides in bytes,
 // from the second dimension on); what lies outside reads as zero.
 bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
-                     const uint64_t* strides, const uint32_t* box, bool swizzle128);
+                     const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
 
 // out[j] = sum over p of part[p][j], in a fixed order; with `two`, rows are 2 D
 // wide and columns from D on are out2's (which may be null).

@@ -63,7 +63,7 @@ bool make_tensor_map_rows(CUtensorMap* m, const void* base, int X, int heads, in
 }
 
 bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
-                     const uint64_t* strides, const uint32_t* box, bool swizzle128) {
+                     const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle) {
   auto enc = encode_fn();
   if (enc == nullptr) return false;
   cuuint64_t d[5], st[4];
@@ -74,7 +74,7 @@ bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, i
     if (i > 0) st[i - 1] = strides[i - 1];
   }
   return enc(m, dt, rank, const_cast<void*>(base), d, st, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

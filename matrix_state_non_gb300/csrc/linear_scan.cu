@@ -626,7 +626,7 @@ bool map_rows(CUtensorMap* m, const LinearArgs& a, const void* p, int64_t stride
   const uint64_t strides[2] = {stride * e, stride * e * a.T};
   const uint32_t box[3] = {kChan, static_cast<uint32_t>(rows), 1};
   return make_tensor_map(m, a.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, p, 3, dims, strides,
-                         box, false);
+                         box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 template <typename E, bool kPair, bool kTma, bool kStates, int kL, int kEvery>

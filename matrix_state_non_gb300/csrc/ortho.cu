@@ -41,26 +41,54 @@ __host__ __device__ constexpr int64_t round_up(int64_t v, int64_t to) { return (
 constexpr int kSumThreads = 256, kSumParts = 64;  // blocks of a matrix, at most
 constexpr int kSumCount = 16384;                  // values for a block, at least
 
-// The thread's share of a sum of squares over a block's piece.  Squares that
-// leave the fp32 range are caught as in grad_clip.cu: next to x^2 it sums
-// (x 2^90)^2, for where the first may have lost bits, and a sum that is not
-// finite is taken again in fp64.
+// Eight values from p on (on 16 bytes).
+__device__ __forceinline__ void load_8(const uint16_t* p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load_8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// The thread's share of a sum of squares over a block's piece, a multiple of 8
+// values if `vec`.  Squares that leave the fp32 range are caught as in
+// grad_clip.cu: next to x^2 it sums (x 2^90)^2, for where the first may have lost
+// bits, and a sum that is not finite is taken again in fp64.
 template <typename E>
-__device__ double square_sum(const E* g, int64_t from, int64_t to) {
+__device__ double square_sum(const E* g, int64_t from, int64_t to, bool vec) {
   float s = 0.f, up = 0.f;
-#pragma unroll 8
-  for (int64_t i = from + threadIdx.x; i < to; i += kSumThreads) {
-    const float x = to_f32(g[i]), y = x * 0x1p90f;
+  auto add = [&](float x) {
+    const float y = x * 0x1p90f;
     s = fmaf(x, x, s);
     up = fmaf(y, y, up);
+  };
+  if (vec) {
+#pragma unroll 4
+    for (int64_t i = from + 8 * threadIdx.x; i < to; i += 8 * kSumThreads) {
+      float v[8];
+      load_8(g + i, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) add(v[e]);
+    }
+  } else {
+#pragma unroll 8
+    for (int64_t i = from + threadIdx.x; i < to; i += kSumThreads) add(to_f32(g[i]));
   }
   if (s < 0x1p-60f) return static_cast<double>(up) * 0x1p-180;
   if (s <= 3.4e38f) return s;
   double w = 0.;
-  for (int64_t i = from + threadIdx.x; i < to; i += kSumThreads) {
-    const double x = to_f32(g[i]);
-    w += x * x;
-  }
+  const int64_t step = vec ? 8 * kSumThreads : kSumThreads, run = vec ? 8 : 1;
+  for (int64_t i = from + run * threadIdx.x; i < to; i += step)
+    for (int64_t j = i; j < i + run; ++j) {
+      const double x = to_f32(g[j]);
+      w += x * x;
+    }
   return w;
 }
 
@@ -69,8 +97,8 @@ __global__ void __launch_bounds__(kSumThreads) ortho_sum_kernel(const E* g, int6
   __shared__ double red[kSumThreads / 32];
   const int64_t mat = blockIdx.x / parts;
   const int p = static_cast<int>(blockIdx.x - mat * parts);
-  const int64_t per = (size + parts - 1) / parts;
-  double acc = square_sum(g + mat * size, p * per, min(size, (p + 1) * per));
+  const int64_t per = round_up((size + parts - 1) / parts, 8);
+  double acc = square_sum(g + mat * size, p * per, min(size, (p + 1) * per), size % 8 == 0);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = acc;
@@ -82,55 +110,101 @@ __global__ void __launch_bounds__(kSumThreads) ortho_sum_kernel(const E* g, int6
   }
 }
 
-__device__ __forceinline__ void split_half(float v, __half& hi, __half& lo) {
-  hi = __float2half_rn(v);
-  lo = __float2half_rn(v - __half2float(hi));
-}
-
-// X [m][pitch] in two parts from G [rows][cols], a tile of 32 x 64 of X at a
-// time; tall: G is [k][m] and goes through shared memory.
-constexpr int kLoadRows = 32, kLoadCols = 64;
-template <typename E>
-__global__ void __launch_bounds__(256) ortho_load_kernel(const E* g, const double* part, int parts, float eps, __half* hi,
-                                                         __half* lo, int m, int k, int pitch, bool tall, int tiles_m,
-                                                         int tiles_k) {
-  __shared__ float t[kLoadRows][kLoadCols + 1];
-  __shared__ float factor;
-  wait_previous();
-  const int64_t tiles = static_cast<int64_t>(tiles_m) * tiles_k, mat = blockIdx.x / tiles;
-  const int tile = static_cast<int>(blockIdx.x - mat * tiles);
-  const int r0 = tile / tiles_k * kLoadRows, c0 = tile % tiles_k * kLoadCols;
+// In every thread of a block: what the matrix's entries are multiplied with.
+__device__ __forceinline__ float first_factor(const double* part, int parts, float eps, float* shared) {
   if (threadIdx.x < 32) {
     double acc = 0.;
-    for (int i = threadIdx.x; i < parts; i += 32) acc += part[mat * parts + i];
+    for (int i = threadIdx.x; i < parts; i += 32) acc += part[i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (threadIdx.x == 0) factor = static_cast<float>(1. / (sqrt(acc) + eps));
-  }
-  const E* p = g + mat * m * k;
-  if (tall) {
-    for (int i = threadIdx.x; i < kLoadRows * kLoadCols; i += 256) {
-      const int r = i % kLoadRows, c = i / kLoadRows;
-      t[r][c] = r0 + r < m && c0 + c < k ? to_f32(p[static_cast<int64_t>(c0 + c) * m + r0 + r]) : 0.f;
-    }
-  } else {
-    for (int i = threadIdx.x; i < kLoadRows * kLoadCols; i += 256) {
-      const int r = i / kLoadCols, c = i % kLoadCols;
-      t[r][c] = r0 + r < m && c0 + c < k ? to_f32(p[static_cast<int64_t>(r0 + r) * k + c0 + c]) : 0.f;
-    }
+    if (threadIdx.x == 0) *shared = static_cast<float>(1. / (sqrt(acc) + eps));
   }
   __syncthreads();
-  let_next();
-  for (int i = threadIdx.x; i < kLoadRows * kLoadCols / 2; i += 256) {
-    const int r = i / (kLoadCols / 2), c = i % (kLoadCols / 2) * 2;
-    if (r0 + r >= m || c0 + c >= pitch) continue;
-    __half2 h, l;
-    split_half(t[r][c] * factor * kScaleX, h.x, l.x);
-    split_half(t[r][c + 1] * factor * kScaleX, h.y, l.y);
-    const int64_t at = (mat * m + r0 + r) * pitch + c0 + c;
-    *reinterpret_cast<__half2*>(hi + at) = h;
-    *reinterpret_cast<__half2*>(lo + at) = l;
+  return *shared;
+}
+
+union Eight {
+  uint4 v;
+  __half2 h[4];
+};
+
+__device__ __forceinline__ void split_8(const float (&v)[8], Eight& hi, Eight& lo) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    hi.h[e] = __floats2half2_rn(v[2 * e], v[2 * e + 1]);
+    lo.h[e] = __floats2half2_rn(v[2 * e] - __half2float(hi.h[e].x), v[2 * e + 1] - __half2float(hi.h[e].y));
   }
+}
+
+// X [m][pitch] in two parts from G [m][k]: eight values of a row to a thread, a
+// block takes kLoadRun of its turns.
+constexpr int kLoadRun = 4;
+template <typename E>
+__global__ void __launch_bounds__(256) ortho_load_kernel(const E* g, const double* part, int parts, float eps, __half* hi,
+                                                         __half* lo, int m, int k, int pitch, int blocks) {
+  __shared__ float shared;
+  const int64_t mat = blockIdx.x / blocks;
+  const int block = static_cast<int>(blockIdx.x - mat * blocks), per_row = pitch / 8;
+  const E* p = g + mat * m * k;
+  wait_previous();
+  const float f = first_factor(part + mat * parts, parts, eps, &shared);
+  const int64_t size = static_cast<int64_t>(m) * per_row;
+#pragma unroll
+  for (int u = 0; u < kLoadRun; ++u) {
+    const int64_t i = (static_cast<int64_t>(block) * kLoadRun + u) * 256 + threadIdx.x;
+    if (i >= size) break;
+    const int64_t r = i / per_row;
+    const int c = static_cast<int>(i - r * per_row) * 8;
+    float v[8];
+    if (k % 8 == 0) {
+      load_8(p + r * k + c, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = c + e < k ? to_f32(p[r * k + c + e]) : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = v[e] * f * kScaleX;
+    Eight h, l;
+    split_8(v, h, l);
+    const int64_t at = mat * m * pitch + i * 8;
+    *reinterpret_cast<uint4*>(hi + at) = h.v;
+    *reinterpret_cast<uint4*>(lo + at) = l.v;
+  }
+  let_next();
+}
+
+// The same from G [k][m] (tall), tiles of 64 x 64 through shared memory.
+constexpr int kTurn = 64;
+template <typename E>
+__global__ void __launch_bounds__(256) ortho_load_tall_kernel(const E* g, const double* part, int parts, float eps, __half* hi,
+                                                              __half* lo, int m, int k, int pitch, int tiles_m, int tiles) {
+  __shared__ float t[kTurn][kTurn + 1];
+  __shared__ float shared;
+  const int64_t mat = blockIdx.x / tiles;
+  const int tile = static_cast<int>(blockIdx.x - mat * tiles);
+  const int r0 = tile % tiles_m * kTurn, c0 = tile / tiles_m * kTurn;
+  const E* p = g + mat * m * k;
+#pragma unroll 8
+  for (int i = threadIdx.x; i < kTurn * kTurn; i += 256) {
+    const int r = i % kTurn, c = i / kTurn;
+    t[r][c] = r0 + r < m && c0 + c < k ? to_f32(p[static_cast<int64_t>(c0 + c) * m + r0 + r]) : 0.f;
+  }
+  wait_previous();
+  const float f = first_factor(part + mat * parts, parts, eps, &shared);
+#pragma unroll
+  for (int i = threadIdx.x; i < kTurn * kTurn / 8; i += 256) {
+    const int r = i / (kTurn / 8), c = i % (kTurn / 8) * 8;
+    if (r0 + r >= m || c0 + c >= pitch) continue;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = t[r][c + e] * f * kScaleX;
+    Eight h, l;
+    split_8(v, h, l);
+    const int64_t at = (mat * m + r0 + r) * pitch + c0 + c;
+    *reinterpret_cast<uint4*>(hi + at) = h.v;
+    *reinterpret_cast<uint4*>(lo + at) = l.v;
+  }
+  let_next();
 }
 
 // ---------------------------------------------------------------------------
@@ -141,12 +215,10 @@ enum { kGram = 0, kPoly = 1, kUpdate = 2 };
 struct ProductArgs {
   const __half* in;      // kPoly: A; kUpdate: X's upper part
   const __half* in_low;  // kUpdate: X's lower part
-  __half* out;           // A; P; X'
-  __half* out_low;       // kUpdate
   uint16_t* last;        // kUpdate of the last step: the result in bf16, [m][k] or (tall) [k][m]
   StatusBlock* status;
   int m, k;              // X is m x k
-  int pitch;             // of in, out
+  int pitch;             // of in
   int inner;             // of the product
   int tiles_m, tiles_n, tiles;  // of one matrix; those that are computed
   int64_t items;
@@ -154,6 +226,7 @@ struct ProductArgs {
 };
 
 constexpr int kRows = 128, kDepth = 64;  // a tile's rows, the inner dimension of a stage
+constexpr int kBlockBytes = 32 * 32 * 2;   // what an epilogue warp stores at once
 constexpr int kEpilogueWarps = 8, kFirstEpilogue = 2, kProductThreads = 32 * (kFirstEpilogue + kEpilogueWarps);
 
 template <int kMode, int kN, bool kLow>
@@ -161,8 +234,10 @@ struct Shape {
   static constexpr int kLeft = kRows * kDepth * 2, kRight = kN * kDepth * 2;
   static constexpr int kStage = kLeft + kRight * (kLow ? 2 : 1);
   static constexpr int kStages = 196608 / kStage;
-  static constexpr int kOffBar = kStages * kStage;
+  static constexpr int kOffOut = kStages * kStage;  // two 32 x 32 blocks for each epilogue warp
+  static constexpr int kOffBar = kOffOut + kEpilogueWarps * 2 * kBlockBytes;
   static constexpr int kSmem = kOffBar + 256 + 1024;  // 1024: alignment
+  static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
 struct Item {
@@ -198,15 +273,18 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-union Eight {
-  uint4 v;
-  __half2 h[4];
-};
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t from, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(from), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
 
 template <int kMode, int kN, bool kLow>
 __global__ void __launch_bounds__(kProductThreads, 1)
     ortho_product_kernel(const __grid_constant__ CUtensorMap left, const __grid_constant__ CUtensorMap right,
-                         const __grid_constant__ CUtensorMap right_low, ProductArgs A) {
+                         const __grid_constant__ CUtensorMap right_low, const __grid_constant__ CUtensorMap out,
+                         const __grid_constant__ CUtensorMap out_low, ProductArgs A) {
   using S = Shape<kMode, kN, kLow>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -316,54 +394,72 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         mbar_wait_timed(empty(x % S::kStages), (x / S::kStages) & 1, nullptr, kWhereOrthoDrain);
   } else {
     // ---------------- epilogue: a thread has a row, its warp 32 columns at a time ----------------
+    // What the epilogue reads is on its way a block ahead; what it writes goes through shared memory, 64-byte rows
+    // with their 16-byte pieces swizzled, to TMA.
     const int quarter = warp & 3, half = (warp - kFirstEpilogue) >> 2;
+    const int cols = kMode == kUpdate ? A.k : A.m;
+    const uint32_t block = base + S::kOffOut + (warp - kFirstEpilogue) * 2 * kBlockBytes;
+    const uint32_t line = block + lane * 64, swz = (lane >> 1) & 3;
+    Eight up[4], low[4];
+    auto read = [&](int64_t mat, int r, int c0) {
+      const int64_t row = (mat * A.m + r) * A.pitch + c0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        up[q].v = low[q].v = make_uint4(0u, 0u, 0u, 0u);
+        if (r < A.m && c0 + 8 * q < A.pitch) {
+          up[q].v = *reinterpret_cast<const uint4*>(A.in + row + 8 * q);
+          if (kMode == kUpdate) low[q].v = *reinterpret_cast<const uint4*>(A.in_low + row + 8 * q);
+        }
+      }
+    };
+    auto used = [&](int r0, int c0) { return r0 < A.m && c0 < cols && (kMode == kUpdate || c0 >= r0); };
     int n = 0;
     for (int64_t id = blockIdx.x; id < A.items; id += gridDim.x, ++n) {
       const Item t = item_at<kMode, kN>(A, id);
-      const int slot = n & 1;
+      const int slot = n & 1, mat = static_cast<int>(t.mat);
+      const int r0 = t.i * kRows + quarter * 32, r = r0 + lane;
+      const int x0 = half * (kN / 2);
+      if (kMode != kGram && used(r0, t.j * kN + x0)) read(t.mat, r, t.j * kN + x0);
       if (!warp_wait(done(slot), (n >> 1) & 1, abort_flag, A.status, kWhereOrthoDone)) break;
       tc_fence_after_sync();
-      const int r0 = t.i * kRows + quarter * 32, r = r0 + lane;
       const uint32_t tm = tmem + slot * kN + (static_cast<uint32_t>(32 * quarter) << 16);
-      const int cols = kMode == kUpdate ? A.k : A.m;
-      const int64_t row = (t.mat * A.m + r) * A.pitch, turned = t.mat * A.m * static_cast<int64_t>(A.pitch);
 #pragma unroll 1
-      for (int x = half * (kN / 2); x < (half + 1) * (kN / 2); x += 32) {
+      for (int x = x0; x < x0 + kN / 2; x += 32) {
         const int c0 = t.j * kN + x;
-        if (r0 >= A.m || c0 >= cols || (kMode != kUpdate && c0 < r0)) continue;
-        Eight up[4], low[4];
-        if constexpr (kMode != kGram) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            up[q].v = low[q].v = make_uint4(0u, 0u, 0u, 0u);
-            if (r < A.m && c0 + 8 * q < A.pitch) {
-              up[q].v = *reinterpret_cast<const uint4*>(A.in + row + c0 + 8 * q);
-              if (kMode == kUpdate) low[q].v = *reinterpret_cast<const uint4*>(A.in_low + row + c0 + 8 * q);
-            }
-          }
+        const bool ahead = kMode != kGram && x + 32 < x0 + kN / 2 && used(r0, c0 + 32);
+        if (!used(r0, c0)) {
+          if (ahead) read(t.mat, r, c0 + 32);
+          continue;
         }
         uint32_t acc[32];
         tmem_ld_32x32b<32>(tm + x, acc);
+        float s[32];
+        if constexpr (kMode != kGram) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const __half2 u2 = up[e / 8].h[e % 8 / 2], l2 = low[e / 8].h[e % 8 / 2];
+            s[e] = __half2float(e % 2 == 0 ? u2.x : u2.y);
+            if (kMode == kUpdate) s[e] += __half2float(e % 2 == 0 ? l2.x : l2.y);
+          }
+        }
+        if (ahead) read(t.mat, r, c0 + 32);
         tmem_ld_wait();
         tmem_ld_fence_regs(acc);
-        float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const float p = __uint_as_float(acc[e]);
-          const __half2 u2 = up[e / 8].h[e % 8 / 2], l2 = low[e / 8].h[e % 8 / 2];
-          const float u1 = __half2float(e % 2 == 0 ? u2.x : u2.y), l1 = __half2float(e % 2 == 0 ? l2.x : l2.y);
-          if constexpr (kMode == kGram) v[e] = p * 0x1p-14f;
-          if constexpr (kMode == kPoly) v[e] = fmaf(kC * 0x1p-15f, p, kB * 0.5f * u1);
-          if constexpr (kMode == kUpdate) v[e] = fmaf(p, 0x1p-13f, kA * (u1 + l1));
+          if constexpr (kMode == kGram) s[e] = p * 0x1p-14f;
+          if constexpr (kMode == kPoly) s[e] = fmaf(kC * 0x1p-15f, p, kB * 0.5f * s[e]);
+          if constexpr (kMode == kUpdate) s[e] = fmaf(p, 0x1p-13f, kA * s[e]);
         }
         if (kMode == kUpdate && A.last != nullptr) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] *= 1.f / kScaleX;
+          for (int e = 0; e < 32; ++e) s[e] *= 1.f / kScaleX;
           if (A.tall) {
             uint16_t* to = A.last + (t.mat * A.k + c0) * A.m + r;
 #pragma unroll
             for (int e = 0; e < 32; ++e, to += A.m)
-              if (r < A.m && c0 + e < A.k) *to = from_f32<uint16_t>(v[e]);
+              if (r < A.m && c0 + e < A.k) *to = from_f32<uint16_t>(s[e]);
           } else if (r < A.m) {
             uint16_t* to = A.last + (t.mat * A.m + r) * A.k + c0;
             if (A.k % 8 == 0) {
@@ -371,40 +467,52 @@ __global__ void __launch_bounds__(kProductThreads, 1)
               for (int q = 0; q < 4; ++q)
                 if (c0 + 8 * q < A.k)
                   *reinterpret_cast<uint4*>(to + 8 * q) =
-                      make_uint4(pack_bf16x2(v[8 * q], v[8 * q + 1]), pack_bf16x2(v[8 * q + 2], v[8 * q + 3]),
-                                 pack_bf16x2(v[8 * q + 4], v[8 * q + 5]), pack_bf16x2(v[8 * q + 6], v[8 * q + 7]));
+                      make_uint4(pack_bf16x2(s[8 * q], s[8 * q + 1]), pack_bf16x2(s[8 * q + 2], s[8 * q + 3]),
+                                 pack_bf16x2(s[8 * q + 4], s[8 * q + 5]), pack_bf16x2(s[8 * q + 6], s[8 * q + 7]));
             } else {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (c0 + e < A.k) to[e] = from_f32<uint16_t>(v[e]);
+                if (c0 + e < A.k) to[e] = from_f32<uint16_t>(s[e]);
             }
           }
           continue;
         }
+        // the blocks of the last turn have left shared memory
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+        __syncwarp();
+        const bool mirror = kMode != kUpdate && c0 != r0;  // the diagonal's own blocks are whole
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+          float v[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float a = v[8 * q + 2 * e], b = v[8 * q + 2 * e + 1];
-            up[q].h[e] = __floats2half2_rn(a, b);
-            if constexpr (kMode == kUpdate)
-              low[q].h[e] = __floats2half2_rn(a - __half2float(up[q].h[e].x), b - __half2float(up[q].h[e].y));
-          }
-          if (r < A.m && c0 + 8 * q < A.pitch) {
-            *reinterpret_cast<uint4*>(A.out + row + c0 + 8 * q) = up[q].v;
-            if (kMode == kUpdate) *reinterpret_cast<uint4*>(A.out_low + row + c0 + 8 * q) = low[q].v;
+          for (int e = 0; e < 8; ++e) v[e] = s[8 * q + e];
+          Eight h, l;
+          split_8(v, h, l);
+          st_shared_v4(line + ((q ^ swz) << 4), {h.v.x, h.v.y, h.v.z, h.v.w});
+          if (kMode == kUpdate) st_shared_v4(line + kBlockBytes + ((q ^ swz) << 4), {l.v.x, l.v.y, l.v.z, l.v.w});
+          if (mirror) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {  // row 8 q + e of the other side's block, column `lane`
+              const int row = 8 * q + e;
+              const uint32_t at = block + kBlockBytes + row * 64 + ((((lane >> 3) ^ (row >> 1)) & 3) << 4) + (lane & 7) * 2;
+              const __half2 pair = h.h[e / 2];
+              asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(__half_as_ushort(e % 2 == 0 ? pair.x : pair.y)) : "memory");
+            }
           }
         }
-        if (kMode != kUpdate && c0 != r0 && r < A.m) {  // the other side of the diagonal (whose 32 x 32 blocks are whole)
-          __half* to = A.out + turned + static_cast<int64_t>(c0) * A.pitch + r;
-#pragma unroll
-          for (int e = 0; e < 32; ++e, to += A.pitch)
-            if (c0 + e < A.m) *to = e % 2 == 0 ? up[e / 8].h[e % 8 / 2].x : up[e / 8].h[e % 8 / 2].y;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&out, block, c0, r0, mat);
+          if (kMode == kUpdate) tma_store_3d(&out_low, block + kBlockBytes, c0, r0, mat);
+          if (mirror) tma_store_3d(&out, block + kBlockBytes, r0, c0, mat);
+          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
       }
       tc_fence_before_sync();
       mbar_arrive(tfree(slot));
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   let_next();
   tc_fence_before_sync();
@@ -412,17 +520,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-// Rows of a stack of matrices [n][rows][pitch], boxes of `depth` rows of 64 columns.
-bool map_matrix(CUtensorMap* map, const __half* p, int64_t n, int rows, int cols, int pitch, int depth) {
+// Rows of a stack of matrices [n][rows][pitch]: boxes of `depth` rows of 64 columns to load, 32 x 32 to store.
+bool map_matrix(CUtensorMap* map, const __half* p, int64_t n, int rows, int cols, int pitch, int depth, bool store = false) {
   const uint64_t dims[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), static_cast<uint64_t>(n)};
   const uint64_t strides[2] = {static_cast<uint64_t>(pitch) * 2, static_cast<uint64_t>(pitch) * 2 * rows};
-  const uint32_t box[3] = {64, static_cast<uint32_t>(depth), 1};
-  return make_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p, 3, dims, strides, box, true);
+  const uint32_t box[3] = {store ? 32u : 64u, static_cast<uint32_t>(store ? 32 : depth), 1};
+  return make_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p, 3, dims, strides, box,
+                         store ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <int kMode, int kN, bool kLow>
-cudaError_t product(const CUtensorMap& l, const CUtensorMap& r, const CUtensorMap& low, ProductArgs a, int64_t n,
-                    cudaStream_t s) {
+cudaError_t product(const CUtensorMap& l, const CUtensorMap& r, const CUtensorMap& low, const CUtensorMap& out,
+                    const CUtensorMap& out_low, ProductArgs a, int64_t n, cudaStream_t s) {
   using S = Shape<kMode, kN, kLow>;
   static std::atomic<uint64_t> ready{0};
   const auto kernel = ortho_product_kernel<kMode, kN, kLow>;
@@ -433,7 +542,8 @@ cudaError_t product(const CUtensorMap& l, const CUtensorMap& r, const CUtensorMa
   a.tiles = 0;
   for (int i = 0; i < a.tiles_m; ++i) a.tiles += a.tiles_n - (kMode == kUpdate ? 0 : i * kRows / kN);
   a.items = n * a.tiles;
-  return launch_next(kernel, static_cast<unsigned>(a.items < 152 ? a.items : 152), kProductThreads, S::kSmem, s, l, r, low, a);
+  return launch_next(kernel, static_cast<unsigned>(a.items < 152 ? a.items : 152), kProductThreads, S::kSmem, s, l, r, low, out,
+                     out_low, a);
 }
 
 struct Scratch {
@@ -468,13 +578,19 @@ struct Scratch {
 template <typename E>
 cudaError_t load_first(const OrthoArgs& A, const Scratch& w, int m, int k, bool tall, cudaStream_t s) {
   const E* g = static_cast<const E*>(A.g);
-  const int tiles_m = (m + kLoadRows - 1) / kLoadRows, tiles_k = (k + kLoadCols - 1) / kLoadCols;
   ortho_sum_kernel<E><<<static_cast<unsigned>(A.n * w.parts), kSumThreads, 0, s>>>(g, static_cast<int64_t>(m) * k, w.parts,
                                                                                    w.part);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_next(ortho_load_kernel<E>, static_cast<unsigned>(A.n * tiles_m * tiles_k), 256, 0, s, g, w.part, w.parts, A.eps,
-                     w.x[0], w.low[0], m, k, w.pitch, tall, tiles_m, tiles_k);
+  if (tall) {
+    const int tiles_m = (m + kTurn - 1) / kTurn, tiles = tiles_m * ((k + kTurn - 1) / kTurn);
+    return launch_next(ortho_load_tall_kernel<E>, static_cast<unsigned>(A.n * tiles), 256, 0, s, g, w.part, w.parts, A.eps,
+                       w.x[0], w.low[0], m, k, w.pitch, tiles_m, tiles);
+  }
+  const int64_t eights = static_cast<int64_t>(m) * (w.pitch / 8);
+  const int blocks = static_cast<int>((eights + 256 * kLoadRun - 1) / (256 * kLoadRun));
+  return launch_next(ortho_load_kernel<E>, static_cast<unsigned>(A.n * blocks), 256, 0, s, g, w.part, w.parts, A.eps, w.x[0],
+                     w.low[0], m, k, w.pitch, blocks);
 }
 
 }  // namespace
@@ -486,27 +602,34 @@ cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
   const int m = tall ? A.cols : A.rows, k = tall ? A.rows : A.cols;
   const Scratch w(A.ws, A.n, A.rows, A.cols);
   cudaError_t e = A.bf16 ? load_first<uint16_t>(A, w, m, k, tall, s) : load_first<float>(A, w, m, k, tall, s);
-  CUtensorMap rows[2], cols[2], cols_low[2], gram, poly;
+  if (e != cudaSuccess) return e;
+  CUtensorMap rows[2], cols[2], cols_low[2], x_out[2], low_out[2], gram, poly, gram_out, poly_out;
+  bool made = true;
   for (int i = 0; i < 2; ++i)
-    if (!map_matrix(&rows[i], w.x[i], A.n, m, k, w.pitch, kRows) || !map_matrix(&cols[i], w.x[i], A.n, m, k, w.pitch, kDepth) ||
-        !map_matrix(&cols_low[i], w.low[i], A.n, m, k, w.pitch, kDepth))
-      return cudaErrorInvalidValue;
-  if (!map_matrix(&gram, w.gram, A.n, m, m, w.square, kRows) || !map_matrix(&poly, w.poly, A.n, m, m, w.square, kRows))
-    return cudaErrorInvalidValue;
+    made = made && map_matrix(&rows[i], w.x[i], A.n, m, k, w.pitch, kRows) &&
+           map_matrix(&cols[i], w.x[i], A.n, m, k, w.pitch, kDepth) &&
+           map_matrix(&cols_low[i], w.low[i], A.n, m, k, w.pitch, kDepth) &&
+           map_matrix(&x_out[i], w.x[i], A.n, m, k, w.pitch, 0, true) &&
+           map_matrix(&low_out[i], w.low[i], A.n, m, k, w.pitch, 0, true);
+  made = made && map_matrix(&gram, w.gram, A.n, m, m, w.square, kRows) &&
+         map_matrix(&poly, w.poly, A.n, m, m, w.square, kRows) &&
+         map_matrix(&gram_out, w.gram, A.n, m, m, w.square, 0, true) &&
+         map_matrix(&poly_out, w.poly, A.n, m, m, w.square, 0, true);
+  if (!made) return cudaErrorInvalidValue;
   ProductArgs a{};
   a.status = A.status; a.m = m; a.k = k; a.tall = tall;
   for (int i = 0; i < A.steps && e == cudaSuccess; ++i) {
     const int from = i & 1, to = from ^ 1;
-    a.in = nullptr; a.out = w.gram; a.pitch = w.square; a.inner = k;
-    e = product<kGram, 128, false>(rows[from], rows[from], rows[from], a, A.n, s);
+    a.in = nullptr; a.pitch = w.square; a.inner = k;
+    e = product<kGram, 128, false>(rows[from], rows[from], rows[from], gram_out, gram_out, a, A.n, s);
     if (e != cudaSuccess) break;
-    a.in = w.gram; a.out = w.poly; a.inner = m;
-    e = product<kPoly, 128, false>(gram, gram, gram, a, A.n, s);
+    a.in = w.gram; a.inner = m;
+    e = product<kPoly, 128, false>(gram, gram, gram, poly_out, poly_out, a, A.n, s);
     if (e != cudaSuccess) break;
-    a.in = w.x[from]; a.in_low = w.low[from]; a.out = w.x[to]; a.out_low = w.low[to]; a.pitch = w.pitch;
+    a.in = w.x[from]; a.in_low = w.low[from]; a.pitch = w.pitch;
     a.last = i == A.steps - 1 ? A.out : nullptr;
-    e = m < 512 ? product<kUpdate, 128, true>(poly, cols[from], cols_low[from], a, A.n, s)
-                : product<kUpdate, 256, false>(poly, cols[from], cols_low[from], a, A.n, s);
+    e = m < 512 ? product<kUpdate, 128, true>(poly, cols[from], cols_low[from], x_out[to], low_out[to], a, A.n, s)
+                : product<kUpdate, 256, false>(poly, cols[from], cols_low[from], x_out[to], low_out[to], a, A.n, s);
   }
   return e;
 }
