@@ -12,6 +12,26 @@ namespace m2rnn {
 bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const uint64_t* dims,
                      const uint64_t* strides, const uint32_t* box, CUtensorMapSwizzle swizzle);
 
+// A launch in clusters of `blocks` blocks; behind: as launch_next.
+template <typename... P, typename... V>
+cudaError_t launch_cluster(void (*kernel)(P...), int64_t grid, int blocks, int threads, int smem, bool behind, cudaStream_t s,
+                           V... args) {
+  cudaLaunchAttribute at[2] = {};
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = blocks;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(static_cast<unsigned>(grid));
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = at;
+  c.numAttrs = behind ? 2 : 1;
+  return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+
 // out[j] = sum over p of part[p][j], in a fixed order; with `two`, rows are 2 D
 // wide and columns from D on are out2's (which may be null).
 cudaError_t launch_sum_parts(const float* part, float* out, float* out2, bool two, int parts, int64_t D,

@@ -590,24 +590,6 @@ int cluster_blocks(const LinearArgs& a, int tile) {
   return r;
 }
 
-template <typename... P, typename... V>
-cudaError_t launch_cluster(void (*kernel)(P...), int64_t grid, int blocks, int smem, bool behind, cudaStream_t s, V... args) {
-  cudaLaunchAttribute at[2] = {};
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = blocks;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t c{};
-  c.gridDim = dim3(static_cast<unsigned>(grid));
-  c.blockDim = dim3(kThreads);
-  c.dynamicSmemBytes = smem;
-  c.stream = s;
-  c.attrs = at;
-  c.numAttrs = behind ? 2 : 1;
-  return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
-}
-
 // How rows can be read: value by value, two channels at a time, or by TMA.
 enum class Access { kSingle, kPair, kTma };
 Access access_of(const LinearArgs& a) {
@@ -642,7 +624,7 @@ cudaError_t forward(const LinearArgs& a, float* states, cudaStream_t s) {
       return cudaErrorInvalidValue;
   }
   const int groups = (a.C + kChan - 1) / kChan, blocks = cluster_blocks(a, kTile);
-  return launch_cluster(kernel, static_cast<int64_t>(a.B) * groups * blocks, blocks, kSmem, false, s, a, states, blocks, groups,
+  return launch_cluster(kernel, static_cast<int64_t>(a.B) * groups * blocks, blocks, kThreads, kSmem, false, s, a, states, blocks, groups,
                         maps);
 }
 
@@ -664,7 +646,7 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t s) {
       return cudaErrorInvalidValue;
   }
   const int groups = (a.C + kChan - 1) / kChan, blocks = cluster_blocks(a, kTile);
-  e = launch_cluster(kernel, static_cast<int64_t>(a.B) * groups * blocks, blocks, kSmem, true, s, a, states, part, blocks, groups,
+  e = launch_cluster(kernel, static_cast<int64_t>(a.B) * groups * blocks, blocks, kThreads, kSmem, true, s, a, states, part, blocks, groups,
                      maps);
   if (e != cudaSuccess) return e;
   return launch_sum_parts(part, a.dalpha, a.dbeta, true, a.B * blocks, a.C, s);

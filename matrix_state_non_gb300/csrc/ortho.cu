@@ -229,15 +229,19 @@ constexpr int kRows = 128, kDepth = 64;  // a tile's rows, the inner dimension o
 constexpr int kBlockBytes = 32 * 32 * 2;   // what an epilogue warp stores at once
 constexpr int kEpilogueWarps = 8, kFirstEpilogue = 2, kProductThreads = 32 * (kFirstEpilogue + kEpilogueWarps);
 
-template <int kMode, int kN, bool kLow>
+// kPair: two blocks of a cluster on two SMs share a tile of 256 rows, each with
+// half of its rows, the accumulators of those, and half of its columns' operand.
+template <int kMode, int kN, bool kLow, bool kPair>
 struct Shape {
-  static constexpr int kLeft = kRows * kDepth * 2, kRight = kN * kDepth * 2;
+  static constexpr int kTileRows = kPair ? 2 * kRows : kRows, kOwnN = kPair ? kN / 2 : kN;
+  static constexpr int kLeft = kRows * kDepth * 2, kRight = kOwnN * kDepth * 2;
   static constexpr int kStage = kLeft + kRight * (kLow ? 2 : 1);
-  static constexpr int kStages = 196608 / kStage;
+  static constexpr int kStages = 196608 / kStage > 8 ? 8 : 196608 / kStage;
   static constexpr int kOffOut = kStages * kStage;  // two 32 x 32 blocks for each epilogue warp
   static constexpr int kOffBar = kOffOut + kEpilogueWarps * 2 * kBlockBytes;
   static constexpr int kSmem = kOffBar + 256 + 1024;  // 1024: alignment
   static_assert(kSmem <= 227 * 1024, "shared memory");
+  static_assert(2 * kN <= 512, "tensor memory");
 };
 
 struct Item {
@@ -245,7 +249,7 @@ struct Item {
   int i, j;  // tile's row and column
 };
 // Symmetric products: of row i the tiles with a column at or right of the diagonal.
-template <int kMode, int kN>
+template <int kMode, int kN, int kTileRows>
 __device__ __forceinline__ Item item_at(const ProductArgs& A, int64_t id) {
   Item t;
   t.mat = id / A.tiles;
@@ -259,20 +263,71 @@ __device__ __forceinline__ Item item_at(const ProductArgs& A, int64_t id) {
     while (left >= A.tiles_n - first) {
       left -= A.tiles_n - first;
       ++t.i;
-      first = t.i * kRows / kN;
+      first = t.i * kTileRows / kN;
     }
     t.j = first + left;
   }
   return t;
 }
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
+// Tensor memory, products and their completion for one block or a pair (the pair's products are issued by its first
+// block; both hear of their completion, on barriers at the same place).
+template <bool kPair>
+__device__ __forceinline__ void acquire_tmem(uint32_t slot) {
+  if constexpr (kPair) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(slot) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    tmem_alloc(slot, 512);
+    tmem_relinquish();
+  }
+}
+template <bool kPair>
+__device__ __forceinline__ void release_tmem(uint32_t tmem) {
+  if constexpr (kPair)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  else
+    tmem_dealloc(tmem, 512);
+}
+template <bool kPair>
+__device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    tc_mma_f16_ss(d, a, b, idesc, accumulate);
+}
+template <bool kPair>
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (kPair)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+  else
+    tc_commit(bar);
 }
 
+// `bar` may be the other block's of a pair.
+template <bool kPair>
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2) {
+  if constexpr (kPair)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t from, int c0, int c1, int c2) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
@@ -280,12 +335,13 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t fr
                : "memory");
 }
 
-template <int kMode, int kN, bool kLow>
+template <int kMode, int kN, bool kLow, bool kPair>
 __global__ void __launch_bounds__(kProductThreads, 1)
     ortho_product_kernel(const __grid_constant__ CUtensorMap left, const __grid_constant__ CUtensorMap right,
                          const __grid_constant__ CUtensorMap right_low, const __grid_constant__ CUtensorMap out,
                          const __grid_constant__ CUtensorMap out_low, ProductArgs A) {
-  using S = Shape<kMode, kN, kLow>;
+  using S = Shape<kMode, kN, kLow, kPair>;
+  constexpr int kBlocks = kPair ? 2 : 1;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -297,6 +353,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffBar + 160);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffBar + 164);
   static_assert(S::kStages <= 8, "barriers");
+  const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t first = blockIdx.x / kBlocks, step = gridDim.x / kBlocks;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(full(s), 1);
@@ -304,17 +362,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(done(s), 1);
-      mbar_init(tfree(s), 32 * kEpilogueWarps);
+      mbar_init(tfree(s), 32 * kEpilogueWarps * kBlocks);
     }
     *abort_flag = 0;
     fence_mbar_init_cluster();
   }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
-  }
+  if (warp == 1) acquire_tmem<kPair>(smem_u32(tmem_slot));
   tc_fence_before_sync();
-  __syncthreads();
+  __syncwarp();
+  if constexpr (kPair)
+    cluster_sync_all();
+  else
+    __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   wait_previous();
@@ -326,8 +385,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       asm volatile("fence.proxy.async;" ::: "memory");  // what earlier launches stored, before TMA reads it
       int u = 0;  // stages filled
       bool ok = true;
-      for (int64_t id = blockIdx.x; ok && id < A.items; id += gridDim.x) {
-        const Item t = item_at<kMode, kN>(A, id);
+      for (int64_t id = first; ok && id < A.items; id += step) {
+        const Item t = item_at<kMode, kN, S::kTileRows>(A, id);
         const int mat = static_cast<int>(t.mat);
         for (int d = 0; d < depth; ++d, ++u) {
           const int s = u % S::kStages;
@@ -335,32 +394,34 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t to = base + s * S::kStage, bar = full(s);
-          mbar_arrive_expect_tx(bar, S::kStage);
-          tma_load_3d(to, &left, bar, d * kDepth, t.i * kRows, mat);
+          const uint32_t to = base + s * S::kStage, bar = kPair ? mapa_shared(full(s), 0) : full(s);
+          if (rank == 0) mbar_arrive_expect_tx(full(s), S::kStage * kBlocks);
+          tma_load_3d<kPair>(to, &left, bar, d * kDepth, t.i * S::kTileRows + rank * kRows, mat);
+          const int n0 = t.j * kN + rank * S::kOwnN;
           if constexpr (kMode == kUpdate) {  // 64 columns of 64 rows at a time
 #pragma unroll
-            for (int c = 0; c < kN; c += 64) {
-              tma_load_3d(to + S::kLeft + c * kDepth * 2, &right, bar, t.j * kN + c, d * kDepth, mat);
-              if (kLow) tma_load_3d(to + S::kLeft + S::kRight + c * kDepth * 2, &right_low, bar, t.j * kN + c, d * kDepth, mat);
+            for (int c = 0; c < S::kOwnN; c += 64) {
+              tma_load_3d<kPair>(to + S::kLeft + c * kDepth * 2, &right, bar, n0 + c, d * kDepth, mat);
+              if (kLow) tma_load_3d<kPair>(to + S::kLeft + S::kRight + c * kDepth * 2, &right_low, bar, n0 + c, d * kDepth, mat);
             }
           } else {
 #pragma unroll
-            for (int r = 0; r < kN; r += kRows)
-              tma_load_3d(to + S::kLeft + r * kDepth * 2, &right, bar, d * kDepth, t.j * kN + r, mat);
+            for (int r = 0; r < S::kOwnN; r += kRows)
+              tma_load_3d<kPair>(to + S::kLeft + r * kDepth * 2, &right, bar, d * kDepth, n0 + r, mat);
           }
         }
       }
-      if (!ok)  // the copies in flight land before the block ends
+      if (!ok && rank == 0)  // the copies in flight land before the block ends (a pair's: before it has met)
         for (int x = max(0, u - S::kStages); x < u; ++x)
           mbar_wait_timed(full(x % S::kStages), (x / S::kStages) & 1, nullptr, kWhereOrthoDrain);
     }
   } else if (warp == 1) {
     // ---------------- products ----------------
-    constexpr uint32_t kId = idesc_f16_f32(kRows, kN, false, kMode == kUpdate);
+    if (rank == 0) {
+    constexpr uint32_t kId = idesc_f16_f32(S::kTileRows, kN, false, kMode == kUpdate);
     int u = 0, n = 0;  // stages, tiles
     bool ok = true;
-    for (int64_t id = blockIdx.x; ok && id < A.items; id += gridDim.x, ++n) {
+    for (int64_t id = first; ok && id < A.items; id += step, ++n) {
       const int slot = n & 1;
       if (n >= 2 && !warp_wait(tfree(slot), ((n >> 1) - 1) & 1, abort_flag, A.status, kWhereOrthoFree)) break;
       tc_fence_after_sync();
@@ -376,15 +437,15 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < kDepth / 16; ++kk) {
             if constexpr (kMode == kUpdate) {
-              tc_mma_f16_ss(tm, desc_sw128(l + kk * 32), desc_sw128(r + kk * 2048, kDepth * 128), kId, d > 0 || kk > 0);
+              multiply<kPair>(tm, desc_sw128(l + kk * 32), desc_sw128(r + kk * 2048, kDepth * 128), kId, d > 0 || kk > 0);
               if (kLow)
-                tc_mma_f16_ss(tm, desc_sw128(l + kk * 32), desc_sw128(r + S::kRight + kk * 2048, kDepth * 128), kId, 1);
+                multiply<kPair>(tm, desc_sw128(l + kk * 32), desc_sw128(r + S::kRight + kk * 2048, kDepth * 128), kId, 1);
             } else {
-              tc_mma_f16_ss(tm, desc_sw128(l + kk * 32), desc_sw128(r + kk * 32), kId, d > 0 || kk > 0);
+              multiply<kPair>(tm, desc_sw128(l + kk * 32), desc_sw128(r + kk * 32), kId, d > 0 || kk > 0);
             }
           }
-          tc_commit(empty(s));
-          if (d == depth - 1) tc_commit(done(slot));
+          commit<kPair>(empty(s));
+          if (d == depth - 1) commit<kPair>(done(slot));
         }
         __syncwarp();
       }
@@ -392,6 +453,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     if (*abort_flag)  // the products in flight end before their memory is freed
       for (int x = max(0, u - S::kStages); x < u; ++x)
         mbar_wait_timed(empty(x % S::kStages), (x / S::kStages) & 1, nullptr, kWhereOrthoDrain);
+    }
   } else {
     // ---------------- epilogue: a thread has a row, its warp 32 columns at a time ----------------
     // What the epilogue reads is on its way a block ahead; what it writes goes through shared memory, 64-byte rows
@@ -414,10 +476,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     };
     auto used = [&](int r0, int c0) { return r0 < A.m && c0 < cols && (kMode == kUpdate || c0 >= r0); };
     int n = 0;
-    for (int64_t id = blockIdx.x; id < A.items; id += gridDim.x, ++n) {
-      const Item t = item_at<kMode, kN>(A, id);
+    for (int64_t id = first; id < A.items; id += step, ++n) {
+      const Item t = item_at<kMode, kN, S::kTileRows>(A, id);
       const int slot = n & 1, mat = static_cast<int>(t.mat);
-      const int r0 = t.i * kRows + quarter * 32, r = r0 + lane;
+      const int r0 = t.i * S::kTileRows + rank * kRows + quarter * 32, r = r0 + lane;
       const int x0 = half * (kN / 2);
       if (kMode != kGram && used(r0, t.j * kN + x0)) read(t.mat, r, t.j * kN + x0);
       if (!warp_wait(done(slot), (n >> 1) & 1, abort_flag, A.status, kWhereOrthoDone)) break;
@@ -510,14 +572,21 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
       }
       tc_fence_before_sync();
-      mbar_arrive(tfree(slot));
+      if (rank == 0)
+        mbar_arrive(tfree(slot));
+      else
+        mbar_arrive_cluster(mapa_shared(tfree(slot), 0));
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   let_next();
   tc_fence_before_sync();
-  __syncthreads();
-  if (warp == 1) tmem_dealloc(tmem, 512);
+  __syncwarp();
+  if constexpr (kPair)
+    cluster_sync_all();  // no block ends while the other's products read it or its epilogue signals to it
+  else
+    __syncthreads();
+  if (warp == 1) release_tmem<kPair>(tmem);
 }
 
 // Rows of a stack of matrices [n][rows][pitch]: boxes of `depth` rows of 64 columns to load, 32 x 32 to store.
@@ -529,21 +598,26 @@ bool map_matrix(CUtensorMap* map, const __half* p, int64_t n, int rows, int cols
                          store ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <int kMode, int kN, bool kLow>
-cudaError_t product(const CUtensorMap& l, const CUtensorMap& r, const CUtensorMap& low, const CUtensorMap& out,
-                    const CUtensorMap& out_low, ProductArgs a, int64_t n, cudaStream_t s) {
-  using S = Shape<kMode, kN, kLow>;
+struct Operands {
+  const CUtensorMap &left, &right, &right_low, &out, &out_low;
+};
+
+template <int kMode, int kN, bool kLow, bool kPair>
+cudaError_t product(const Operands& o, ProductArgs a, int64_t n, cudaStream_t s) {
+  using S = Shape<kMode, kN, kLow, kPair>;
+  constexpr int kBlocks = kPair ? 2 : 1;
   static std::atomic<uint64_t> ready{0};
-  const auto kernel = ortho_product_kernel<kMode, kN, kLow>;
+  const auto kernel = ortho_product_kernel<kMode, kN, kLow, kPair>;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem, ready);
   if (e != cudaSuccess) return e;
-  a.tiles_m = (a.m + kRows - 1) / kRows;
+  a.tiles_m = (a.m + S::kTileRows - 1) / S::kTileRows;
   a.tiles_n = ((kMode == kUpdate ? a.k : a.m) + kN - 1) / kN;
   a.tiles = 0;
-  for (int i = 0; i < a.tiles_m; ++i) a.tiles += a.tiles_n - (kMode == kUpdate ? 0 : i * kRows / kN);
+  for (int i = 0; i < a.tiles_m; ++i) a.tiles += a.tiles_n - (kMode == kUpdate ? 0 : i * S::kTileRows / kN);
   a.items = n * a.tiles;
-  return launch_next(kernel, static_cast<unsigned>(a.items < 152 ? a.items : 152), kProductThreads, S::kSmem, s, l, r, low, out,
-                     out_low, a);
+  const int64_t most = 152 / kBlocks;
+  return launch_cluster(kernel, (a.items < most ? a.items : most) * kBlocks, kBlocks, kProductThreads, S::kSmem, true, s, o.left,
+                        o.right, o.right_low, o.out, o.out_low, a);
 }
 
 struct Scratch {
@@ -616,20 +690,25 @@ cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
          map_matrix(&gram_out, w.gram, A.n, m, m, w.square, 0, true) &&
          map_matrix(&poly_out, w.poly, A.n, m, m, w.square, 0, true);
   if (!made) return cudaErrorInvalidValue;
+  // pairs where their tiles fill the GPU
+  const int64_t edge = (m + 255) / 256;
+  const bool pair = m >= 512 && A.n * edge * (edge + 1) / 2 >= 76;
   ProductArgs a{};
   a.status = A.status; a.m = m; a.k = k; a.tall = tall;
   for (int i = 0; i < A.steps && e == cudaSuccess; ++i) {
     const int from = i & 1, to = from ^ 1;
     a.in = nullptr; a.pitch = w.square; a.inner = k;
-    e = product<kGram, 128, false>(rows[from], rows[from], rows[from], gram_out, gram_out, a, A.n, s);
+    const Operands to_gram{rows[from], rows[from], rows[from], gram_out, gram_out};
+    e = pair ? product<kGram, 256, false, true>(to_gram, a, A.n, s) : product<kGram, 128, false, false>(to_gram, a, A.n, s);
     if (e != cudaSuccess) break;
     a.in = w.gram; a.inner = m;
-    e = product<kPoly, 128, false>(gram, gram, gram, poly_out, poly_out, a, A.n, s);
+    const Operands to_poly{gram, gram, gram, poly_out, poly_out};
+    e = pair ? product<kPoly, 256, false, true>(to_poly, a, A.n, s) : product<kPoly, 128, false, false>(to_poly, a, A.n, s);
     if (e != cudaSuccess) break;
     a.in = w.x[from]; a.in_low = w.low[from]; a.pitch = w.pitch;
     a.last = i == A.steps - 1 ? A.out : nullptr;
-    e = m < 512 ? product<kUpdate, 128, true>(poly, cols[from], cols_low[from], x_out[to], low_out[to], a, A.n, s)
-                : product<kUpdate, 256, false>(poly, cols[from], cols_low[from], x_out[to], low_out[to], a, A.n, s);
+    const Operands to_x{poly, cols[from], cols_low[from], x_out[to], low_out[to]};
+    e = pair ? product<kUpdate, 256, false, true>(to_x, a, A.n, s) : product<kUpdate, 128, true, false>(to_x, a, A.n, s);
   }
   return e;
 }

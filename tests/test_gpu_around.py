@@ -382,6 +382,25 @@ def test_orthogonalize(n, rows, cols, kind):
             close(got[i], ref[i], ORTHO_TOL, (dtype, i))
 
 
+@pytest.mark.parametrize("n,rows,cols", [(27, 512, 520), (8, 1000, 1025), (13, 1030, 777), (76, 513, 512)])
+def test_orthogonalize_stacks(n, rows, cols):
+    """Stacks that fill the GPU, whose matrices share tiles of 256 x 256."""
+    import torch
+    from matrix_state_non_gb300 import binding as m
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    g = torch.randn((n, rows, cols), generator=gen, device="cuda")
+    got = m.orthogonalize(g)
+    a, b, c = o.COEFFICIENTS
+    for i in (0, 1, n // 2, n - 1):
+        x = g[i].double()
+        x = x / (x.norm() + 1e-7)
+        for _ in range(5):
+            gram = x @ x.mT
+            x = a * x + (b * gram + c * gram @ gram) @ x
+        assert float((got[i].double() - x).norm() / x.norm()) <= ORTHO_TOL, i
+    assert torch.equal(got, m.orthogonalize(g))
+
+
 @pytest.mark.parametrize("rows,cols", [(48, 64), (200, 136)])
 @pytest.mark.parametrize("steps", [1, 2, 3, 8])
 def test_orthogonalize_steps(rows, cols, steps):
