@@ -213,16 +213,19 @@ __global__ void __launch_bounds__(256) ortho_load_tall_kernel(const E* g, const 
 enum { kGram = 0, kPoly = 1, kUpdate = 2 };
 
 struct ProductArgs {
-  const __half* in;      // kPoly: A; kUpdate: X's upper part
-  const __half* in_low;  // kUpdate: X's lower part
-  uint16_t* last;        // kUpdate of the last step: the result in bf16, [m][k] or (tall) [k][m]
+  uint16_t* last;  // kUpdate of the last step: the result in bf16, [m][k] or (tall) [k][m]
   StatusBlock* status;
-  int m, k;              // X is m x k
-  int pitch;             // of in
-  int inner;             // of the product
+  int m, k;   // X is m x k
+  int inner;  // of the product
   int tiles_m, tiles_n, tiles;  // of one matrix; those that are computed
   int64_t items;
   bool tall;
+  bool direct;  // last: rows that TMA cannot store (not on 16 bytes)
+};
+
+// By TMA: the operands; `in`: kPoly: A; kUpdate: X, its lower part in_low; `out`: A, P or X' (out_low), or the result.
+struct Operands {
+  CUtensorMap left, right, right_low, in, in_low, out, out_low;
 };
 
 constexpr int kRows = 128, kDepth = 64;  // a tile's rows, the inner dimension of a stage
@@ -236,10 +239,12 @@ struct Shape {
   static constexpr int kTileRows = kPair ? 2 * kRows : kRows, kOwnN = kPair ? kN / 2 : kN;
   static constexpr int kLeft = kRows * kDepth * 2, kRight = kOwnN * kDepth * 2;
   static constexpr int kStage = kLeft + kRight * (kLow ? 2 : 1);
-  static constexpr int kStages = 196608 / kStage > 8 ? 8 : 196608 / kStage;
-  static constexpr int kOffOut = kStages * kStage;  // two 32 x 32 blocks for each epilogue warp
-  static constexpr int kOffBar = kOffOut + kEpilogueWarps * 2 * kBlockBytes;
-  static constexpr int kSmem = kOffBar + 256 + 1024;  // 1024: alignment
+  // An epilogue warp's ring of what it reads and writes: two 32 x 32 blocks a turn.
+  static constexpr int kTurns = kLow ? 2 : 3, kTurn = 2 * kBlockBytes;
+  static constexpr int kStages = kLow ? 3 : 4;
+  static constexpr int kOffRing = kStages * kStage;
+  static constexpr int kOffBar = kOffRing + kEpilogueWarps * kTurns * kTurn;
+  static constexpr int kSmem = kOffBar + 512 + 1024;  // 1024: alignment
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(2 * kN <= 512, "tensor memory");
 };
@@ -335,11 +340,15 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t fr
                : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
 template <int kMode, int kN, bool kLow, bool kPair>
 __global__ void __launch_bounds__(kProductThreads, 1)
-    ortho_product_kernel(const __grid_constant__ CUtensorMap left, const __grid_constant__ CUtensorMap right,
-                         const __grid_constant__ CUtensorMap right_low, const __grid_constant__ CUtensorMap out,
-                         const __grid_constant__ CUtensorMap out_low, ProductArgs A) {
+    ortho_product_kernel(const __grid_constant__ Operands O, ProductArgs A) {
   using S = Shape<kMode, kN, kLow, kPair>;
   constexpr int kBlocks = kPair ? 2 : 1;
   extern __shared__ uint8_t raw[];
@@ -350,6 +359,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   auto empty = [&](int s) { return bars + 64 + 8 * s; };   // [stages] products -> TMA
   auto done = [&](int s) { return bars + 128 + 8 * s; };   // [2] products -> epilogue
   auto tfree = [&](int s) { return bars + 144 + 8 * s; };  // [2] epilogue -> products
+  auto there = [&](int w, int s) { return bars + 192 + 8 * (w * S::kTurns + s); };  // [warps][turns] TMA -> epilogue
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffBar + 160);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffBar + 164);
   static_assert(S::kStages <= 8, "barriers");
@@ -364,6 +374,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       mbar_init(done(s), 1);
       mbar_init(tfree(s), 32 * kEpilogueWarps * kBlocks);
     }
+    for (int s = 0; s < kEpilogueWarps * S::kTurns; ++s) mbar_init(there(0, s), 1);
     *abort_flag = 0;
     fence_mbar_init_cluster();
   }
@@ -396,18 +407,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           }
           const uint32_t to = base + s * S::kStage, bar = kPair ? mapa_shared(full(s), 0) : full(s);
           if (rank == 0) mbar_arrive_expect_tx(full(s), S::kStage * kBlocks);
-          tma_load_3d<kPair>(to, &left, bar, d * kDepth, t.i * S::kTileRows + rank * kRows, mat);
+          tma_load_3d<kPair>(to, &O.left, bar, d * kDepth, t.i * S::kTileRows + rank * kRows, mat);
           const int n0 = t.j * kN + rank * S::kOwnN;
           if constexpr (kMode == kUpdate) {  // 64 columns of 64 rows at a time
 #pragma unroll
             for (int c = 0; c < S::kOwnN; c += 64) {
-              tma_load_3d<kPair>(to + S::kLeft + c * kDepth * 2, &right, bar, n0 + c, d * kDepth, mat);
-              if (kLow) tma_load_3d<kPair>(to + S::kLeft + S::kRight + c * kDepth * 2, &right_low, bar, n0 + c, d * kDepth, mat);
+              tma_load_3d<kPair>(to + S::kLeft + c * kDepth * 2, &O.right, bar, n0 + c, d * kDepth, mat);
+              if (kLow) tma_load_3d<kPair>(to + S::kLeft + S::kRight + c * kDepth * 2, &O.right_low, bar, n0 + c, d * kDepth, mat);
             }
           } else {
 #pragma unroll
             for (int r = 0; r < S::kOwnN; r += kRows)
-              tma_load_3d<kPair>(to + S::kLeft + r * kDepth * 2, &right, bar, d * kDepth, n0 + r, mat);
+              tma_load_3d<kPair>(to + S::kLeft + r * kDepth * 2, &O.right, bar, d * kDepth, n0 + r, mat);
           }
         }
       }
@@ -456,102 +467,109 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
   } else {
     // ---------------- epilogue: a thread has a row, its warp 32 columns at a time ----------------
-    // What the epilogue reads is on its way a block ahead; what it writes goes through shared memory, 64-byte rows
-    // with their 16-byte pieces swizzled, to TMA.
-    const int quarter = warp & 3, half = (warp - kFirstEpilogue) >> 2;
+    // What it reads comes by TMA, a turn or two ahead, and what it writes takes its place and goes by TMA: 64-byte
+    // rows with their 16-byte pieces swizzled.
+    const int me = warp - kFirstEpilogue, quarter = warp & 3, half = me >> 2;
     const int cols = kMode == kUpdate ? A.k : A.m;
-    const uint32_t block = base + S::kOffOut + (warp - kFirstEpilogue) * 2 * kBlockBytes;
-    const uint32_t line = block + lane * 64, swz = (lane >> 1) & 3;
-    Eight up[4], low[4];
-    auto read = [&](int64_t mat, int r, int c0) {
-      const int64_t row = (mat * A.m + r) * A.pitch + c0;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        up[q].v = low[q].v = make_uint4(0u, 0u, 0u, 0u);
-        if (r < A.m && c0 + 8 * q < A.pitch) {
-          up[q].v = *reinterpret_cast<const uint4*>(A.in + row + 8 * q);
-          if (kMode == kUpdate) low[q].v = *reinterpret_cast<const uint4*>(A.in_low + row + 8 * q);
-        }
-      }
+    constexpr int kPerTile = kN / 64;  // turns of a tile
+    const uint32_t ring = base + S::kOffRing + me * S::kTurns * S::kTurn, swz = (lane >> 1) & 3;
+    const int64_t tiles = first < A.items ? (A.items - 1 - first) / step + 1 : 0;
+    const int64_t turns = tiles * kPerTile;
+    auto place = [&](int64_t u, int& r0, int& c0) {
+      const Item t = item_at<kMode, kN, S::kTileRows>(A, first + u / kPerTile * step);
+      r0 = t.i * S::kTileRows + rank * kRows + quarter * 32;
+      c0 = t.j * kN + half * (kN / 2) + static_cast<int>(u % kPerTile) * 32;
+      return static_cast<int>(t.mat);
     };
-    auto used = [&](int r0, int c0) { return r0 < A.m && c0 < cols && (kMode == kUpdate || c0 >= r0); };
-    int n = 0;
-    for (int64_t id = first; id < A.items; id += step, ++n) {
-      const Item t = item_at<kMode, kN, S::kTileRows>(A, id);
-      const int slot = n & 1, mat = static_cast<int>(t.mat);
-      const int r0 = t.i * S::kTileRows + rank * kRows + quarter * 32, r = r0 + lane;
-      const int x0 = half * (kN / 2);
-      if (kMode != kGram && used(r0, t.j * kN + x0)) read(t.mat, r, t.j * kN + x0);
-      if (!warp_wait(done(slot), (n >> 1) & 1, abort_flag, A.status, kWhereOrthoDone)) break;
+    auto read = [&](int64_t u) {  // by one lane
+      if (kMode == kGram || u >= turns) return;
+      int r0, c0;
+      const int mat = place(u, r0, c0), s = static_cast<int>(u % S::kTurns);
+      mbar_arrive_expect_tx(there(me, s), kMode == kUpdate ? S::kTurn : kBlockBytes);
+      tma_load_3d<false>(ring + s * S::kTurn, &O.in, there(me, s), c0, r0, mat);
+      if (kMode == kUpdate) tma_load_3d<false>(ring + s * S::kTurn + kBlockBytes, &O.in_low, there(me, s), c0, r0, mat);
+    };
+    if (lane == 0) {
+      asm volatile("fence.proxy.async;" ::: "memory");
+      for (int u = 0; u < S::kTurns - 1; ++u) read(u);
+    }
+    int64_t u = 0;
+    bool ok = true;
+    for (int n = 0; ok && n < tiles; ++n) {
+      const int slot = n & 1;
+      ok = warp_wait(done(slot), (n >> 1) & 1, abort_flag, A.status, kWhereOrthoDone);
       tc_fence_after_sync();
-      const uint32_t tm = tmem + slot * kN + (static_cast<uint32_t>(32 * quarter) << 16);
+      const uint32_t tm = tmem + slot * kN + half * (kN / 2) + (static_cast<uint32_t>(32 * quarter) << 16);
 #pragma unroll 1
-      for (int x = x0; x < x0 + kN / 2; x += 32) {
-        const int c0 = t.j * kN + x;
-        const bool ahead = kMode != kGram && x + 32 < x0 + kN / 2 && used(r0, c0 + 32);
-        if (!used(r0, c0)) {
-          if (ahead) read(t.mat, r, c0 + 32);
-          continue;
+      for (int x = 0; ok && x < kPerTile; ++x, ++u) {
+        int r0, c0;
+        const int mat = place(u, r0, c0), s = static_cast<int>(u % S::kTurns);
+        const bool used = r0 < A.m && c0 < cols && (kMode == kUpdate || c0 >= r0);
+        const uint32_t block = ring + s * S::kTurn, line = block + lane * 64;
+        float v[32];
+        if (kMode != kGram) {
+          ok = warp_wait(there(me, s), static_cast<uint32_t>(u / S::kTurns) & 1, abort_flag, A.status, kWhereOrthoIn);
+          if (!ok) break;
         }
-        uint32_t acc[32];
-        tmem_ld_32x32b<32>(tm + x, acc);
-        float s[32];
-        if constexpr (kMode != kGram) {
+        if (used) {
+          uint32_t acc[32];
+          tmem_ld_32x32b<32>(tm + 32 * x, acc);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const __half2 u2 = up[e / 8].h[e % 8 / 2], l2 = low[e / 8].h[e % 8 / 2];
-            s[e] = __half2float(e % 2 == 0 ? u2.x : u2.y);
-            if (kMode == kUpdate) s[e] += __half2float(e % 2 == 0 ? l2.x : l2.y);
-          }
-        }
-        if (ahead) read(t.mat, r, c0 + 32);
-        tmem_ld_wait();
-        tmem_ld_fence_regs(acc);
+          for (int q = 0; q < 4; ++q) {
+            Eight h, l;
+            if constexpr (kMode != kGram) h.v = ld_shared_v4(line + ((q ^ swz) << 4));
+            if constexpr (kMode == kUpdate) l.v = ld_shared_v4(line + kBlockBytes + ((q ^ swz) << 4));
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          const float p = __uint_as_float(acc[e]);
-          if constexpr (kMode == kGram) s[e] = p * 0x1p-14f;
-          if constexpr (kMode == kPoly) s[e] = fmaf(kC * 0x1p-15f, p, kB * 0.5f * s[e]);
-          if constexpr (kMode == kUpdate) s[e] = fmaf(p, 0x1p-13f, kA * s[e]);
-        }
-        if (kMode == kUpdate && A.last != nullptr) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) s[e] *= 1.f / kScaleX;
-          if (A.tall) {
-            uint16_t* to = A.last + (t.mat * A.k + c0) * A.m + r;
-#pragma unroll
-            for (int e = 0; e < 32; ++e, to += A.m)
-              if (r < A.m && c0 + e < A.k) *to = from_f32<uint16_t>(s[e]);
-          } else if (r < A.m) {
-            uint16_t* to = A.last + (t.mat * A.m + r) * A.k + c0;
-            if (A.k % 8 == 0) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                if (c0 + 8 * q < A.k)
-                  *reinterpret_cast<uint4*>(to + 8 * q) =
-                      make_uint4(pack_bf16x2(s[8 * q], s[8 * q + 1]), pack_bf16x2(s[8 * q + 2], s[8 * q + 3]),
-                                 pack_bf16x2(s[8 * q + 4], s[8 * q + 5]), pack_bf16x2(s[8 * q + 6], s[8 * q + 7]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (c0 + e < A.k) to[e] = from_f32<uint16_t>(s[e]);
+            for (int e = 0; e < 8; ++e) {
+              if constexpr (kMode != kGram) v[8 * q + e] = __half2float(e % 2 == 0 ? h.h[e / 2].x : h.h[e / 2].y);
+              if constexpr (kMode == kUpdate) v[8 * q + e] += __half2float(e % 2 == 0 ? l.h[e / 2].x : l.h[e / 2].y);
             }
           }
+          tmem_ld_wait();
+          tmem_ld_fence_regs(acc);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const float p = __uint_as_float(acc[e]);
+            if constexpr (kMode == kGram) v[e] = p * 0x1p-14f;
+            if constexpr (kMode == kPoly) v[e] = fmaf(kC * 0x1p-15f, p, kB * 0.5f * v[e]);
+            if constexpr (kMode == kUpdate) v[e] = fmaf(p, 0x1p-13f, kA * v[e]);
+          }
+        }
+        __syncwarp();
+        if (lane == 0) {  // the turn before has left shared memory: its place is free
+          asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+          read(u + S::kTurns - 1);
+        }
+        if (!used) continue;
+        const bool last = kMode == kUpdate && A.last != nullptr;
+        const bool mirror = (kMode != kUpdate && c0 != r0) || (last && A.tall);  // the diagonal's own blocks are whole
+        if (last && A.direct) {
+          const int r = r0 + lane;
+          const int64_t right = A.tall ? A.m : 1, down = A.tall ? 1 : A.k;
+          uint16_t* to = A.last + (static_cast<int64_t>(mat) * A.m * A.k + r * down + c0 * right);
+          if (r < A.m) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c0 + e < A.k) to[e * right] = from_f32<uint16_t>(v[e] * (1.f / kScaleX));
+          }
           continue;
         }
-        // the blocks of the last turn have left shared memory
-        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         __syncwarp();
-        const bool mirror = kMode != kUpdate && c0 != r0;  // the diagonal's own blocks are whole
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          float v[8];
+          float w[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = s[8 * q + e];
+          for (int e = 0; e < 8; ++e) w[e] = v[8 * q + e];
           Eight h, l;
-          split_8(v, h, l);
+          if (last) {
+            constexpr float f = 1.f / kScaleX;
+            h.v = make_uint4(pack_bf16x2(w[0] * f, w[1] * f), pack_bf16x2(w[2] * f, w[3] * f), pack_bf16x2(w[4] * f, w[5] * f),
+                             pack_bf16x2(w[6] * f, w[7] * f));
+          } else {
+            split_8(w, h, l);
+          }
           st_shared_v4(line + ((q ^ swz) << 4), {h.v.x, h.v.y, h.v.z, h.v.w});
-          if (kMode == kUpdate) st_shared_v4(line + kBlockBytes + ((q ^ swz) << 4), {l.v.x, l.v.y, l.v.z, l.v.w});
+          if (kMode == kUpdate && !last) st_shared_v4(line + kBlockBytes + ((q ^ swz) << 4), {l.v.x, l.v.y, l.v.z, l.v.w});
           if (mirror) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {  // row 8 q + e of the other side's block, column `lane`
@@ -565,19 +583,26 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_3d(&out, block, c0, r0, mat);
-          if (kMode == kUpdate) tma_store_3d(&out_low, block + kBlockBytes, c0, r0, mat);
-          if (mirror) tma_store_3d(&out, block + kBlockBytes, r0, c0, mat);
+          if (!(last && A.tall)) tma_store_3d(&O.out, block, c0, r0, mat);
+          if (kMode == kUpdate && !last) tma_store_3d(&O.out_low, block + kBlockBytes, c0, r0, mat);
+          if (mirror) tma_store_3d(&O.out, block + kBlockBytes, r0, c0, mat);
           asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
       }
+      if (!ok) break;
       tc_fence_before_sync();
       if (rank == 0)
         mbar_arrive(tfree(slot));
       else
         mbar_arrive_cluster(mapa_shared(tfree(slot), 0));
     }
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    if (lane == 0) {
+      if (!ok && kMode != kGram)  // what is on its way lands before the block ends
+        for (int64_t x = u; x < u + S::kTurns && x < turns; ++x)
+          mbar_wait_timed(there(me, static_cast<int>(x % S::kTurns)), static_cast<uint32_t>(x / S::kTurns) & 1, nullptr,
+                          kWhereOrthoDrain);
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
   }
   let_next();
   tc_fence_before_sync();
@@ -589,18 +614,17 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   if (warp == 1) release_tmem<kPair>(tmem);
 }
 
-// Rows of a stack of matrices [n][rows][pitch]: boxes of `depth` rows of 64 columns to load, 32 x 32 to store.
-bool map_matrix(CUtensorMap* map, const __half* p, int64_t n, int rows, int cols, int pitch, int depth, bool store = false) {
+// A stack of matrices [n][rows][pitch] as TMA sees it: boxes of `depth` rows of 64 columns for the products' operands
+// (128-byte swizzle), of 32 x 32 for the epilogue (64-byte swizzle).
+constexpr int kEpilogueBox = 0;
+bool map_matrix(CUtensorMap* map, const void* p, int64_t n, int rows, int cols, int pitch, int depth,
+                CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_FLOAT16) {
   const uint64_t dims[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), static_cast<uint64_t>(n)};
   const uint64_t strides[2] = {static_cast<uint64_t>(pitch) * 2, static_cast<uint64_t>(pitch) * 2 * rows};
-  const uint32_t box[3] = {store ? 32u : 64u, static_cast<uint32_t>(store ? 32 : depth), 1};
-  return make_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, p, 3, dims, strides, box,
-                         store ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+  const bool small = depth == kEpilogueBox;
+  const uint32_t box[3] = {small ? 32u : 64u, small ? 32u : static_cast<uint32_t>(depth), 1};
+  return make_tensor_map(map, type, p, 3, dims, strides, box, small ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
-
-struct Operands {
-  const CUtensorMap &left, &right, &right_low, &out, &out_low;
-};
 
 template <int kMode, int kN, bool kLow, bool kPair>
 cudaError_t product(const Operands& o, ProductArgs a, int64_t n, cudaStream_t s) {
@@ -616,8 +640,7 @@ cudaError_t product(const Operands& o, ProductArgs a, int64_t n, cudaStream_t s)
   for (int i = 0; i < a.tiles_m; ++i) a.tiles += a.tiles_n - (kMode == kUpdate ? 0 : i * S::kTileRows / kN);
   a.items = n * a.tiles;
   const int64_t most = 152 / kBlocks;
-  return launch_cluster(kernel, (a.items < most ? a.items : most) * kBlocks, kBlocks, kProductThreads, S::kSmem, true, s, o.left,
-                        o.right, o.right_low, o.out, o.out_low, a);
+  return launch_cluster(kernel, (a.items < most ? a.items : most) * kBlocks, kBlocks, kProductThreads, S::kSmem, true, s, o, a);
 }
 
 struct Scratch {
@@ -677,38 +700,47 @@ cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
   const Scratch w(A.ws, A.n, A.rows, A.cols);
   cudaError_t e = A.bf16 ? load_first<uint16_t>(A, w, m, k, tall, s) : load_first<float>(A, w, m, k, tall, s);
   if (e != cudaSuccess) return e;
-  CUtensorMap rows[2], cols[2], cols_low[2], x_out[2], low_out[2], gram, poly, gram_out, poly_out;
-  bool made = true;
-  for (int i = 0; i < 2; ++i)
-    made = made && map_matrix(&rows[i], w.x[i], A.n, m, k, w.pitch, kRows) &&
-           map_matrix(&cols[i], w.x[i], A.n, m, k, w.pitch, kDepth) &&
-           map_matrix(&cols_low[i], w.low[i], A.n, m, k, w.pitch, kDepth) &&
-           map_matrix(&x_out[i], w.x[i], A.n, m, k, w.pitch, 0, true) &&
-           map_matrix(&low_out[i], w.low[i], A.n, m, k, w.pitch, 0, true);
-  made = made && map_matrix(&gram, w.gram, A.n, m, m, w.square, kRows) &&
-         map_matrix(&poly, w.poly, A.n, m, m, w.square, kRows) &&
-         map_matrix(&gram_out, w.gram, A.n, m, m, w.square, 0, true) &&
-         map_matrix(&poly_out, w.poly, A.n, m, m, w.square, 0, true);
-  if (!made) return cudaErrorInvalidValue;
   // pairs where their tiles fill the GPU
   const int64_t edge = (m + 255) / 256;
   const bool pair = m >= 512 && A.n * edge * (edge + 1) / 2 >= 76;
   ProductArgs a{};
   a.status = A.status; a.m = m; a.k = k; a.tall = tall;
+  a.direct = A.cols % 8 != 0;
+  Operands to_gram[2], to_poly, to_x[2], to_last;
+  bool made = map_matrix(&to_poly.left, w.gram, A.n, m, m, w.square, kRows) &&
+              map_matrix(&to_poly.in, w.gram, A.n, m, m, w.square, kEpilogueBox) &&
+              map_matrix(&to_poly.out, w.poly, A.n, m, m, w.square, kEpilogueBox);
+  to_poly.right = to_poly.right_low = to_poly.left;
+  to_poly.in_low = to_poly.out_low = to_poly.out;
+  for (int i = 0; i < 2; ++i) {
+    Operands &g = to_gram[i], &x = to_x[i];
+    made = made && map_matrix(&g.left, w.x[i], A.n, m, k, w.pitch, kRows) && map_matrix(&x.left, w.poly, A.n, m, m, w.square, kRows) &&
+           map_matrix(&x.right, w.x[i], A.n, m, k, w.pitch, kDepth) && map_matrix(&x.right_low, w.low[i], A.n, m, k, w.pitch, kDepth) &&
+           map_matrix(&x.in, w.x[i], A.n, m, k, w.pitch, kEpilogueBox) &&
+           map_matrix(&x.in_low, w.low[i], A.n, m, k, w.pitch, kEpilogueBox);
+    g.right = g.right_low = g.left;
+    g.out = g.out_low = g.in = g.in_low = to_poly.in;
+  }
+  for (int i = 0; i < 2; ++i) {
+    to_x[i].out = to_x[i ^ 1].in;
+    to_x[i].out_low = to_x[i ^ 1].in_low;
+  }
+  to_last = to_x[(A.steps - 1) & 1];
+  if (!a.direct)
+    made = made && map_matrix(&to_last.out, A.out, A.n, A.rows, A.cols, A.cols, kEpilogueBox, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+  if (!made) return cudaErrorInvalidValue;
   for (int i = 0; i < A.steps && e == cudaSuccess; ++i) {
-    const int from = i & 1, to = from ^ 1;
-    a.in = nullptr; a.pitch = w.square; a.inner = k;
-    const Operands to_gram{rows[from], rows[from], rows[from], gram_out, gram_out};
-    e = pair ? product<kGram, 256, false, true>(to_gram, a, A.n, s) : product<kGram, 128, false, false>(to_gram, a, A.n, s);
+    const int at = i & 1;
+    const bool last = i == A.steps - 1;
+    a.inner = k;
+    e = pair ? product<kGram, 256, false, true>(to_gram[at], a, A.n, s) : product<kGram, 128, false, false>(to_gram[at], a, A.n, s);
     if (e != cudaSuccess) break;
-    a.in = w.gram; a.inner = m;
-    const Operands to_poly{gram, gram, gram, poly_out, poly_out};
+    a.inner = m;
     e = pair ? product<kPoly, 256, false, true>(to_poly, a, A.n, s) : product<kPoly, 128, false, false>(to_poly, a, A.n, s);
     if (e != cudaSuccess) break;
-    a.in = w.x[from]; a.in_low = w.low[from]; a.pitch = w.pitch;
-    a.last = i == A.steps - 1 ? A.out : nullptr;
-    const Operands to_x{poly, cols[from], cols_low[from], x_out[to], low_out[to]};
-    e = pair ? product<kUpdate, 256, false, true>(to_x, a, A.n, s) : product<kUpdate, 128, true, false>(to_x, a, A.n, s);
+    a.last = last ? A.out : nullptr;
+    const Operands& o = last ? to_last : to_x[at];
+    e = pair ? product<kUpdate, 256, false, true>(o, a, A.n, s) : product<kUpdate, 128, true, false>(o, a, A.n, s);
   }
   return e;
 }

@@ -39,7 +39,7 @@ constexpr uint32_t kWhereWalkFull = 411, kWhereWalkSplit = 412, kWhereWalkDone =
                    kWhereWalkFree = 415, kWhereWalkDrain = 416;
 // The orthogonalised update's products.
 constexpr uint32_t kWhereOrthoFull = 421, kWhereOrthoEmpty = 422, kWhereOrthoDone = 423, kWhereOrthoFree = 424,
-                   kWhereOrthoDrain = 425;
+                   kWhereOrthoDrain = 425, kWhereOrthoIn = 426;
 
 __device__ __forceinline__ void report_device_error(StatusBlock* s, unsigned int code,
                                                     uint32_t where) {
