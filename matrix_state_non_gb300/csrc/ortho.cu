@@ -240,8 +240,8 @@ struct Shape {
   static constexpr int kLeft = kRows * kDepth * 2, kRight = kOwnN * kDepth * 2;
   static constexpr int kStage = kLeft + kRight * (kLow ? 2 : 1);
   // An epilogue warp's ring of what it reads and writes: two 32 x 32 blocks a turn.
-  static constexpr int kTurns = kLow ? 2 : 3, kTurn = 2 * kBlockBytes;
-  static constexpr int kStages = kLow ? 3 : 4;
+  static constexpr int kTurns = kMode == kGram ? 1 : kMode == kPoly || kLow ? 2 : 3, kTurn = 2 * kBlockBytes;
+  static constexpr int kStages = kMode == kGram ? 6 : kMode == kPoly ? 5 : kLow ? 3 : 4;
   static constexpr int kOffRing = kStages * kStage;
   static constexpr int kOffBar = kOffRing + kEpilogueWarps * kTurns * kTurn;
   static constexpr int kSmem = kOffBar + 512 + 1024;  // 1024: alignment
@@ -344,6 +344,82 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
+}
+
+// A row's 32 columns of the result from the accumulators and what the turn's place holds: v.
+template <int kMode>
+__device__ __forceinline__ void combine(float (&v)[32], const uint32_t (&acc)[32], uint32_t line, uint32_t swz) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    Eight h, l;
+    if constexpr (kMode != kGram) h.v = ld_shared_v4(line + ((q ^ swz) << 4));
+    if constexpr (kMode == kUpdate) l.v = ld_shared_v4(line + kBlockBytes + ((q ^ swz) << 4));
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float p = __uint_as_float(acc[8 * q + e]);
+      float x = 0.f;
+      if constexpr (kMode != kGram) x = __half2float(e % 2 == 0 ? h.h[e / 2].x : h.h[e / 2].y);
+      if constexpr (kMode == kUpdate) x += __half2float(e % 2 == 0 ? l.h[e / 2].x : l.h[e / 2].y);
+      if constexpr (kMode == kGram) v[8 * q + e] = p * 0x1p-14f;
+      if constexpr (kMode == kPoly) v[8 * q + e] = fmaf(kC * 0x1p-15f, p, kB * 0.5f * x);
+      if constexpr (kMode == kUpdate) v[8 * q + e] = fmaf(p, 0x1p-13f, kA * x);
+    }
+  }
+}
+
+// The warp's 32 x 32 block of the result from row r0 and column c0 on, to where it belongs: through the place `block`
+// to TMA, which one lane commits; rows that TMA cannot store, directly.
+template <int kMode>
+__device__ __forceinline__ void emit(const Operands& O, const ProductArgs& A, const float (&v)[32], uint32_t block, int r0, int c0,
+                                     int mat, int lane) {
+  const uint32_t line = block + lane * 64, swz = (lane >> 1) & 3;
+  const bool last = kMode == kUpdate && A.last != nullptr;
+  const bool mirror = (kMode != kUpdate && c0 != r0) || (last && A.tall);  // the diagonal's own blocks are whole
+  if (last && A.direct) {
+    const int r = r0 + lane;
+    const int64_t right = A.tall ? A.m : 1, down = A.tall ? 1 : A.k;
+    uint16_t* to = A.last + (static_cast<int64_t>(mat) * A.m * A.k + r * down + c0 * right);
+    if (r < A.m) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (c0 + e < A.k) to[e * right] = from_f32<uint16_t>(v[e] * (1.f / kScaleX));
+    }
+    return;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = v[8 * q + e];
+    Eight h, l;
+    if (last) {
+      constexpr float f = 1.f / kScaleX;
+      h.v = make_uint4(pack_bf16x2(w[0] * f, w[1] * f), pack_bf16x2(w[2] * f, w[3] * f), pack_bf16x2(w[4] * f, w[5] * f),
+                       pack_bf16x2(w[6] * f, w[7] * f));
+    } else {
+      split_8(w, h, l);
+    }
+    st_shared_v4(line + ((q ^ swz) << 4), {h.v.x, h.v.y, h.v.z, h.v.w});
+    if (kMode == kUpdate && !last) st_shared_v4(line + kBlockBytes + ((q ^ swz) << 4), {l.v.x, l.v.y, l.v.z, l.v.w});
+    if (mirror) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {  // row 8 q + e of the other side's block, column `lane`
+        const int row = 8 * q + e;
+        const uint32_t at = block + kBlockBytes + row * 64 + ((((lane >> 3) ^ (row >> 1)) & 3) << 4) + (lane & 7) * 2;
+        const __half2 pair = h.h[e / 2];
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(__half_as_ushort(e % 2 == 0 ? pair.x : pair.y)) : "memory");
+      }
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (!(last && A.tall)) tma_store_3d(&O.out, block, c0, r0, mat);
+    if (kMode == kUpdate && !last) tma_store_3d(&O.out_low, block + kBlockBytes, c0, r0, mat);
+    if (mirror) tma_store_3d(&O.out, block + kBlockBytes, r0, c0, mat);
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
 }
 
 template <int kMode, int kN, bool kLow, bool kPair>
@@ -514,80 +590,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         if (used) {
           uint32_t acc[32];
           tmem_ld_32x32b<32>(tm + 32 * x, acc);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            Eight h, l;
-            if constexpr (kMode != kGram) h.v = ld_shared_v4(line + ((q ^ swz) << 4));
-            if constexpr (kMode == kUpdate) l.v = ld_shared_v4(line + kBlockBytes + ((q ^ swz) << 4));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if constexpr (kMode != kGram) v[8 * q + e] = __half2float(e % 2 == 0 ? h.h[e / 2].x : h.h[e / 2].y);
-              if constexpr (kMode == kUpdate) v[8 * q + e] += __half2float(e % 2 == 0 ? l.h[e / 2].x : l.h[e / 2].y);
-            }
-          }
           tmem_ld_wait();
           tmem_ld_fence_regs(acc);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float p = __uint_as_float(acc[e]);
-            if constexpr (kMode == kGram) v[e] = p * 0x1p-14f;
-            if constexpr (kMode == kPoly) v[e] = fmaf(kC * 0x1p-15f, p, kB * 0.5f * v[e]);
-            if constexpr (kMode == kUpdate) v[e] = fmaf(p, 0x1p-13f, kA * v[e]);
-          }
+          combine<kMode>(v, acc, line, swz);
         }
         __syncwarp();
         if (lane == 0) {  // the turn before has left shared memory: its place is free
           asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
           read(u + S::kTurns - 1);
         }
-        if (!used) continue;
-        const bool last = kMode == kUpdate && A.last != nullptr;
-        const bool mirror = (kMode != kUpdate && c0 != r0) || (last && A.tall);  // the diagonal's own blocks are whole
-        if (last && A.direct) {
-          const int r = r0 + lane;
-          const int64_t right = A.tall ? A.m : 1, down = A.tall ? 1 : A.k;
-          uint16_t* to = A.last + (static_cast<int64_t>(mat) * A.m * A.k + r * down + c0 * right);
-          if (r < A.m) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c0 + e < A.k) to[e * right] = from_f32<uint16_t>(v[e] * (1.f / kScaleX));
-          }
-          continue;
-        }
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float w[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = v[8 * q + e];
-          Eight h, l;
-          if (last) {
-            constexpr float f = 1.f / kScaleX;
-            h.v = make_uint4(pack_bf16x2(w[0] * f, w[1] * f), pack_bf16x2(w[2] * f, w[3] * f), pack_bf16x2(w[4] * f, w[5] * f),
-                             pack_bf16x2(w[6] * f, w[7] * f));
-          } else {
-            split_8(w, h, l);
-          }
-          st_shared_v4(line + ((q ^ swz) << 4), {h.v.x, h.v.y, h.v.z, h.v.w});
-          if (kMode == kUpdate && !last) st_shared_v4(line + kBlockBytes + ((q ^ swz) << 4), {l.v.x, l.v.y, l.v.z, l.v.w});
-          if (mirror) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {  // row 8 q + e of the other side's block, column `lane`
-              const int row = 8 * q + e;
-              const uint32_t at = block + kBlockBytes + row * 64 + ((((lane >> 3) ^ (row >> 1)) & 3) << 4) + (lane & 7) * 2;
-              const __half2 pair = h.h[e / 2];
-              asm volatile("st.shared.b16 [%0], %1;" ::"r"(at), "h"(__half_as_ushort(e % 2 == 0 ? pair.x : pair.y)) : "memory");
-            }
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (!(last && A.tall)) tma_store_3d(&O.out, block, c0, r0, mat);
-          if (kMode == kUpdate && !last) tma_store_3d(&O.out_low, block + kBlockBytes, c0, r0, mat);
-          if (mirror) tma_store_3d(&O.out, block + kBlockBytes, r0, c0, mat);
-          asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-        }
+        if (used) emit<kMode>(O, A, v, block, r0, c0, mat, lane);
       }
       if (!ok) break;
       tc_fence_before_sync();
@@ -612,6 +624,189 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   else
     __syncthreads();
   if (warp == 1) release_tmem<kPair>(tmem);
+}
+
+// ---------------------------------------------------------------------------
+// The same products where there are few tiles: the `split` blocks of a cluster
+// share a tile's inner dimension, leave their accumulators in shared memory, and
+// each finishes its share of the tile's columns from everybody's.  A tile to a
+// cluster, so that the time is that of a few stages.  1024 x 1024, one matrix:
+// ===
+// ---------------------------------------------------------------------------
+template <bool kLow>
+struct SplitShape {
+  static constexpr int kN = 128, kStages = kLow ? 3 : 4;
+  static constexpr int kLeft = kRows * kDepth * 2, kRight = kN * kDepth * 2, kStage = kLeft + kRight * (kLow ? 2 : 1);
+  static constexpr int kOffRing = kStages * kStage, kOffBar = kOffRing + kEpilogueWarps * 2 * 2 * kBlockBytes;
+  static constexpr int kSmem = kOffBar + 512 + 1024;
+  static_assert(kOffRing >= kRows * kN * 4, "the accumulators take the stages' place");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+template <int kMode, bool kLow>
+__global__ void __launch_bounds__(kProductThreads, 1)
+    ortho_split_kernel(const __grid_constant__ Operands O, ProductArgs A, int split) {
+  using S = SplitShape<kLow>;
+  constexpr int kN = S::kN;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t base = smem_u32(smem), bars = base + S::kOffBar;
+  auto full = [&](int s) { return bars + 8 * s; };
+  auto empty = [&](int s) { return bars + 64 + 8 * s; };
+  const uint32_t done = bars + 128;
+  auto there = [&](int w, int x) { return bars + 192 + 8 * (2 * w + x); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffBar + 160);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffBar + 164);
+  const int rank = split == 1 ? 0 : static_cast<int>(cluster_ctarank());
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    mbar_init(done, 1);
+    for (int s = 0; s < 2 * kEpilogueWarps; ++s) mbar_init(there(0, s), 1);
+    *abort_flag = 0;
+    fence_mbar_init_cluster();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), kN);
+    tmem_relinquish();
+  }
+  tc_fence_before_sync();
+  __syncwarp();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const Item t = item_at<kMode, kN, kRows>(A, blockIdx.x / split);
+  const int mat = static_cast<int>(t.mat);
+  const int depth = (A.inner + kDepth - 1) / kDepth, d0 = depth * rank / split, d1 = depth * (rank + 1) / split;
+  // a warp's blocks: 32 rows, of the block's own columns (kN / split: 128, 64 or 32) every second 32
+  const int me = warp - kFirstEpilogue, quarter = warp & 3, half = me >> 2;
+  const int own = kN / split, r0 = t.i * kRows + quarter * 32, blocks = (own / 32 + 1 - half) / 2;
+  auto column = [&](int x) { return rank * own + 32 * (half + 2 * x); };  // in the tile
+  const uint32_t ring = base + S::kOffRing + me * 2 * 2 * kBlockBytes;
+  wait_previous();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      asm volatile("fence.proxy.async;" ::: "memory");
+      bool ok = true;
+      int u = 0;
+      for (int d = d0; d < d1; ++d, ++u) {
+        const int s = u % S::kStages;
+        if (u >= S::kStages && !mbar_wait(empty(s), (u / S::kStages - 1) & 1, abort_flag, A.status, kWhereOrthoEmpty)) {
+          ok = false;
+          break;
+        }
+        const uint32_t to = base + s * S::kStage, bar = full(s);
+        mbar_arrive_expect_tx(bar, S::kStage);
+        tma_load_3d<false>(to, &O.left, bar, d * kDepth, t.i * kRows, mat);
+        if constexpr (kMode == kUpdate) {
+#pragma unroll
+          for (int c = 0; c < kN; c += 64) {
+            tma_load_3d<false>(to + S::kLeft + c * kDepth * 2, &O.right, bar, t.j * kN + c, d * kDepth, mat);
+            if (kLow) tma_load_3d<false>(to + S::kLeft + S::kRight + c * kDepth * 2, &O.right_low, bar, t.j * kN + c, d * kDepth, mat);
+          }
+        } else {
+          tma_load_3d<false>(to + S::kLeft, &O.right, bar, d * kDepth, t.j * kN, mat);
+        }
+      }
+      if (!ok)
+        for (int x = max(0, u - S::kStages); x < u; ++x)
+          mbar_wait_timed(full(x % S::kStages), (x / S::kStages) & 1, nullptr, kWhereOrthoDrain);
+    }
+  } else if (warp == 1) {
+    constexpr uint32_t kId = idesc_f16_f32(kRows, kN, false, kMode == kUpdate);
+    int u = 0;
+    for (int d = d0; d < d1; ++d, ++u) {
+      const int s = u % S::kStages;
+      if (!warp_wait(full(s), (u / S::kStages) & 1, abort_flag, A.status, kWhereOrthoFull)) break;
+      if (elect_one()) {
+        tc_fence_after_sync();
+        const uint32_t l = base + s * S::kStage, r = l + S::kLeft;
+#pragma unroll
+        for (int kk = 0; kk < kDepth / 16; ++kk) {
+          if constexpr (kMode == kUpdate) {
+            tc_mma_f16_ss(tmem, desc_sw128(l + kk * 32), desc_sw128(r + kk * 2048, kDepth * 128), kId, u > 0 || kk > 0);
+            if (kLow) tc_mma_f16_ss(tmem, desc_sw128(l + kk * 32), desc_sw128(r + S::kRight + kk * 2048, kDepth * 128), kId, 1);
+          } else {
+            tc_mma_f16_ss(tmem, desc_sw128(l + kk * 32), desc_sw128(r + kk * 32), kId, u > 0 || kk > 0);
+          }
+        }
+        tc_commit(empty(s));
+        if (d == d1 - 1) tc_commit(done);
+      }
+      __syncwarp();
+    }
+    if (*abort_flag)
+      for (int x = max(0, u - S::kStages); x < u; ++x)
+        mbar_wait_timed(empty(x % S::kStages), (x / S::kStages) & 1, nullptr, kWhereOrthoDrain);
+  } else {
+    if (kMode != kGram && lane == 0) {
+      asm volatile("fence.proxy.async;" ::: "memory");
+      for (int x = 0; x < blocks; ++x) {
+        const uint32_t to = ring + x * 2 * kBlockBytes;
+        mbar_arrive_expect_tx(there(me, x), kMode == kUpdate ? 2 * kBlockBytes : kBlockBytes);
+        tma_load_3d<false>(to, &O.in, there(me, x), t.j * kN + column(x), r0, mat);
+        if (kMode == kUpdate) tma_load_3d<false>(to + kBlockBytes, &O.in_low, there(me, x), t.j * kN + column(x), r0, mat);
+      }
+    }
+    warp_wait(done, 0, abort_flag, A.status, kWhereOrthoDone);
+    tc_fence_after_sync();
+    if (split > 1) {  // the accumulators, a column after another
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int c = 64 * half + 32 * x;
+        uint32_t acc[32];
+        tmem_ld_32x32b<32>(tmem + c + (static_cast<uint32_t>(32 * quarter) << 16), acc);
+        tmem_ld_wait();
+        tmem_ld_fence_regs(acc);
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+          asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + ((c + e) * kRows + quarter * 32 + lane) * 4), "r"(acc[e]) : "memory");
+      }
+    }
+  }
+  __syncwarp();
+  if (split > 1) cluster_sync_all();
+  if (warp >= kFirstEpilogue) {
+    const int cols = kMode == kUpdate ? A.k : A.m;
+    for (int x = 0; x < blocks; ++x) {
+      const int c = column(x), c0 = t.j * kN + c;
+      const uint32_t block = ring + x * 2 * kBlockBytes;
+      if (kMode != kGram) warp_wait(there(me, x), 0, abort_flag, A.status, kWhereOrthoIn);
+      if (r0 >= A.m || c0 >= cols || (kMode != kUpdate && c0 < r0)) continue;
+      uint32_t acc[32];
+      if (split == 1) {
+        tmem_ld_32x32b<32>(tmem + c + (static_cast<uint32_t>(32 * quarter) << 16), acc);
+        tmem_ld_wait();
+        tmem_ld_fence_regs(acc);
+      } else {
+        const uint32_t from = base + (c * kRows + quarter * 32 + lane) * 4;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) acc[e] = 0u;
+        for (int r = 0; r < split; ++r) {
+          const uint32_t there_ = mapa_shared(from, r);
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            acc[e] = __float_as_uint(__uint_as_float(acc[e]) + ld_shared_cluster_f32(there_ + e * kRows * 4));
+        }
+      }
+      float v[32];
+      combine<kMode>(v, acc, block + lane * 64, (lane >> 1) & 3);
+      emit<kMode>(O, A, v, block, r0, c0, mat, lane);
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+  let_next();
+  tc_fence_before_sync();
+  __syncwarp();
+  if (split > 1)
+    cluster_sync_all();  // no block ends while another reads from it
+  else
+    __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, kN);
 }
 
 // A stack of matrices [n][rows][pitch] as TMA sees it: boxes of `depth` rows of 64 columns for the products' operands
@@ -641,6 +836,29 @@ cudaError_t product(const Operands& o, ProductArgs a, int64_t n, cudaStream_t s)
   a.items = n * a.tiles;
   const int64_t most = 152 / kBlocks;
   return launch_cluster(kernel, (a.items < most ? a.items : most) * kBlocks, kBlocks, kProductThreads, S::kSmem, true, s, o, a);
+}
+
+template <int kMode, bool kLow>
+cudaError_t split_product(const Operands& o, ProductArgs a, int64_t n, cudaStream_t s) {
+  using S = SplitShape<kLow>;
+  static std::atomic<uint64_t> ready{0};
+  const auto kernel = ortho_split_kernel<kMode, kLow>;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem, ready);
+  if (e != cudaSuccess) return e;
+  const int stages = (a.inner + kDepth - 1) / kDepth;
+  int split = 1;
+  while (split < 4 && 2 * split * a.items <= 152 && 2 * split <= stages) split *= 2;
+  return launch_cluster(kernel, a.items * split, split, kProductThreads, S::kSmem, true, s, o, a, split);
+}
+
+// The tiles of 128 x 128 of n matrices.
+template <int kMode>
+ProductArgs small_tiles(ProductArgs a, int64_t n) {
+  a.tiles_m = (a.m + kRows - 1) / kRows;
+  a.tiles_n = ((kMode == kUpdate ? a.k : a.m) + 127) / 128;
+  a.tiles = kMode == kUpdate ? a.tiles_m * a.tiles_n : a.tiles_m * (a.tiles_m + 1) / 2;
+  a.items = n * a.tiles;
+  return a;
 }
 
 struct Scratch {
@@ -733,14 +951,23 @@ cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
     const int at = i & 1;
     const bool last = i == A.steps - 1;
     a.inner = k;
-    e = pair ? product<kGram, 256, false, true>(to_gram[at], a, A.n, s) : product<kGram, 128, false, false>(to_gram[at], a, A.n, s);
+    const ProductArgs tg = small_tiles<kGram>(a, A.n);
+    e = pair                 ? product<kGram, 256, false, true>(to_gram[at], a, A.n, s)
+        : tg.items * 2 <= 152 ? split_product<kGram, false>(to_gram[at], tg, A.n, s)
+                              : product<kGram, 128, false, false>(to_gram[at], a, A.n, s);
     if (e != cudaSuccess) break;
     a.inner = m;
-    e = pair ? product<kPoly, 256, false, true>(to_poly, a, A.n, s) : product<kPoly, 128, false, false>(to_poly, a, A.n, s);
+    const ProductArgs tp = small_tiles<kPoly>(a, A.n);
+    e = pair                 ? product<kPoly, 256, false, true>(to_poly, a, A.n, s)
+        : tp.items * 2 <= 152 ? split_product<kPoly, false>(to_poly, tp, A.n, s)
+                              : product<kPoly, 128, false, false>(to_poly, a, A.n, s);
     if (e != cudaSuccess) break;
     a.last = last ? A.out : nullptr;
     const Operands& o = last ? to_last : to_x[at];
-    e = pair ? product<kUpdate, 256, false, true>(o, a, A.n, s) : product<kUpdate, 128, true, false>(o, a, A.n, s);
+    const ProductArgs tu = small_tiles<kUpdate>(a, A.n);
+    e = pair                 ? product<kUpdate, 256, false, true>(o, a, A.n, s)
+        : tu.items * 2 <= 152 ? split_product<kUpdate, true>(o, tu, A.n, s)
+                              : product<kUpdate, 128, true, false>(o, a, A.n, s);
   }
   return e;
 }
