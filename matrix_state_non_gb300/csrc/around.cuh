@@ -115,5 +115,8 @@ struct OrthoArgs {
 
 size_t ortho_scratch_bytes(int64_t n, int64_t rows, int64_t cols);
 cudaError_t launch_orthogonalize(const OrthoArgs& a, cudaStream_t s);
+// Matrices that a block has in shared memory (no scratch).
+bool ortho_small(int64_t rows, int64_t cols);
+cudaError_t launch_ortho_small(const OrthoArgs& a, cudaStream_t s);
 
 }  // namespace m2rnn

@@ -340,12 +340,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t fr
                : "memory");
 }
 
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-
 // A row's 32 columns of the result from the accumulators and what the turn's place holds: v.
 template <int kMode>
 __device__ __forceinline__ void combine(float (&v)[32], const uint32_t (&acc)[32], uint32_t line, uint32_t swz) {
@@ -910,9 +904,12 @@ cudaError_t load_first(const OrthoArgs& A, const Scratch& w, int m, int k, bool 
 
 }  // namespace
 
-size_t ortho_scratch_bytes(int64_t n, int64_t rows, int64_t cols) { return Scratch(nullptr, n, rows, cols).bytes; }
+size_t ortho_scratch_bytes(int64_t n, int64_t rows, int64_t cols) {
+  return ortho_small(rows, cols) ? 0 : Scratch(nullptr, n, rows, cols).bytes;
+}
 
 cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
+  if (ortho_small(A.rows, A.cols)) return launch_ortho_small(A, s);
   const bool tall = A.rows > A.cols;
   const int m = tall ? A.cols : A.rows, k = tall ? A.rows : A.cols;
   const Scratch w(A.ws, A.n, A.rows, A.cols);

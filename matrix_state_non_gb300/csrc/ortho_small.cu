@@ -1,0 +1,211 @@
+// The orthogonalised update (ortho.cu) of small matrices, up to 64 x 256 or 256 x
+// 64: a block per matrix, everything in shared memory from the norm to the last
+// step, one launch.  The three products of a step run on warp MMA with fp16
+// operands in two parts each, three products of parts for one of values (22
+// bits; what is left out is 2^-22 of it), scaled as in ortho.cu; so the result is
+// the fp32 one to its rounding to bf16.  Eight warps: a quarter of the rows and
+// half of the columns each.
+// ===
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "around.cuh"
+#include "mma_common.cuh"
+
+namespace m2rnn {
+namespace {
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f, kScaleX = 0x1p14f;
+constexpr int kRows = 64, kThreads = 256, kSquare = kRows + 8;  // a row's pitch: 8 more, for the banks
+
+// v0, v1 in two fp16 parts each.
+__device__ __forceinline__ void split_pair(float v0, float v1, uint32_t& hi, uint32_t& lo) {
+  hi = pack2_f16(v0, v1);
+  lo = pack2_f16(v0 - f16lo(hi), v1 - f16hi(hi));
+}
+
+// d += a b over 16 x (8 kTiles) x depth; a: rows of 16, b: [n][depth] (kTurned: [depth][n]), in two parts of `a_part`,
+// `b_part` bytes.
+template <int kTiles, bool kTurned>
+__device__ __forceinline__ void multiply(float (&d)[kTiles][4], uint32_t a, int a_pitch, uint32_t a_part, uint32_t b, int b_pitch,
+                                         uint32_t b_part, int depth, int lane) {
+  const uint32_t pa = a + ((lane & 15) * a_pitch + (lane >> 4) * 8) * 2;
+  const uint32_t pb = kTurned ? b + ((lane & 15) * b_pitch + (lane >> 4) * 8) * 2
+                              : b + (((lane & 7) + ((lane >> 4) << 3)) * b_pitch + ((lane >> 3) & 1) * 8) * 2;
+#pragma unroll 2
+  for (int k = 0; k < depth; k += 16) {
+    uint32_t ah[4], al[4];
+    ldmatrix_x4(ah, pa + k * 2);
+    ldmatrix_x4(al, pa + a_part + k * 2);
+#pragma unroll
+    for (int t = 0; t < kTiles; t += 2) {
+      uint32_t bh[4], bl[4];
+      const uint32_t at = kTurned ? pb + (k * b_pitch + t * 8) * 2 : pb + (t * 8 * b_pitch + k) * 2;
+      if constexpr (kTurned) {
+        ldmatrix_x4_trans(bh, at);
+        ldmatrix_x4_trans(bl, at + b_part);
+      } else {
+        ldmatrix_x4(bh, at);
+        ldmatrix_x4(bl, at + b_part);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mma_f16_16816(d[t + h], ah, bh[2 * h], bh[2 * h + 1]);
+        mma_f16_16816(d[t + h], ah, bl[2 * h], bl[2 * h + 1]);
+        mma_f16_16816(d[t + h], al, bh[2 * h], bh[2 * h + 1]);
+      }
+    }
+  }
+}
+
+template <typename E, int kCols>
+__global__ void __launch_bounds__(kThreads, kCols > 128 ? 2 : 3) ortho_small_kernel(const E* g, uint16_t* out, int m, int k,
+                                                                                   bool tall, int steps, float eps) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  constexpr int kPitch = kCols + 8;
+  constexpr uint32_t kXPart = kRows * kPitch * 2, kSPart = kRows * kSquare * 2;
+  __shared__ double red[kThreads / 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = lane & 3, row = 16 * (warp & 3) + (lane >> 2);
+  const uint32_t x = smem_u32(raw), s = x + 2 * kXPart, p = s + 2 * kSPart;
+  const int size = m * k, line = tall ? m : k;  // a line of G
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * size;
+
+  // ---- the norm; X ----
+  float v[kCols / 4];
+  float sum = 0.f, up = 0.f;
+#pragma unroll
+  for (int j = 0; j < kCols / 4; ++j) {
+    const int i = threadIdx.x + kThreads * j;
+    v[j] = i < size ? to_f32(g[at + i]) : 0.f;
+  }
+  for (uint32_t o = threadIdx.x * 16; o < 2 * kXPart; o += kThreads * 16) st_shared_f32x4(x + o, make_float4(0.f, 0.f, 0.f, 0.f));
+#pragma unroll
+  for (int j = 0; j < kCols / 4; ++j) {
+    const float y = v[j] * 0x1p90f;
+    sum = fmaf(v[j], v[j], sum);
+    up = fmaf(y, y, up);
+  }
+  double acc = sum;  // squares that leave the fp32 range, as in ortho.cu
+  if (sum < 0x1p-60f) acc = static_cast<double>(up) * 0x1p-180;
+  if (!(sum <= 3.4e38f)) {
+    acc = 0.;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < size; i += kThreads) {
+      const double w = to_f32(g[at + i]);
+      acc += w * w;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
+  if (lane == 0) red[warp] = acc;
+  __syncthreads();
+  acc = red[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 32; ++w) acc += red[w];
+  const float f = static_cast<float>(1. / (sqrt(acc) + eps));
+#pragma unroll
+  for (int j = 0; j < kCols / 4; ++j) {
+    const int i = threadIdx.x + kThreads * j, a = i / line, c = i - a * line;
+    if (i < size) {
+      const float w = v[j] * f * kScaleX;
+      const __half hi = __float2half_rn(w), lo = __float2half_rn(w - __half2float(hi));
+      const uint32_t to = x + ((tall ? c : a) * kPitch + (tall ? a : c)) * 2;
+      st_shared_u16(to, __half_as_ushort(hi));
+      st_shared_u16(to + kXPart, __half_as_ushort(lo));
+    }
+  }
+  __syncthreads();
+
+  // ---- the steps ----
+  const int c0 = 32 * (warp >> 2);             // the warp's columns of A, P
+  const int k0 = (kCols / 2) * (warp >> 2);    // and of X
+  const uint32_t rows_x = x + 16 * (warp & 3) * kPitch * 2, rows_s = s + 16 * (warp & 3) * kSquare * 2,
+                 rows_p = p + 16 * (warp & 3) * kSquare * 2;
+  auto put = [&](uint32_t to, int pitch, uint32_t part, int r, int c, float v0, float v1) {
+    uint32_t hi, lo;
+    split_pair(v0, v1, hi, lo);
+    st_shared_b32(to + (r * pitch + c) * 2, hi);
+    st_shared_b32(to + (r * pitch + c) * 2 + part, lo);
+  };
+  for (int i = 0; i < steps; ++i) {
+    float a[4][4] = {};
+    multiply<4, false>(a, rows_x, kPitch, kXPart, x + c0 * kPitch * 2, kPitch, kXPart, kCols, lane);
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        a[t][e] *= 0x1p-14f;
+        a[t][e + 1] *= 0x1p-14f;
+        put(s, kSquare, kSPart, row + 4 * e, c0 + 8 * t + 2 * q, a[t][e], a[t][e + 1]);
+      }
+    __syncthreads();
+    float b[4][4] = {};
+    multiply<4, false>(b, rows_s, kSquare, kSPart, s + c0 * kSquare * 2, kSquare, kSPart, kRows, lane);
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2)
+        put(p, kSquare, kSPart, row + 4 * e, c0 + 8 * t + 2 * q, fmaf(kC * 0x1p-15f, b[t][e], kB * 0.5f * a[t][e]),
+            fmaf(kC * 0x1p-15f, b[t][e + 1], kB * 0.5f * a[t][e + 1]));
+    __syncthreads();
+    constexpr int kTiles = kCols / 16;
+    float d[kTiles][4] = {};
+    multiply<kTiles, true>(d, rows_p, kSquare, kSPart, x + k0 * 2, kPitch, kXPart, kRows, lane);
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const uint32_t from = x + ((row + 4 * e) * kPitch + k0 + 8 * t + 2 * q) * 2;
+        const uint32_t hi = ld_shared_b32(from), lo = ld_shared_b32(from + kXPart);
+        d[t][e] = fmaf(d[t][e], 0x1p-13f, kA * (f16lo(hi) + f16lo(lo)));
+        d[t][e + 1] = fmaf(d[t][e + 1], 0x1p-13f, kA * (f16hi(hi) + f16hi(lo)));
+      }
+    __syncthreads();
+    const bool last = i == steps - 1;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        const int r = row + 4 * e, c = k0 + 8 * t + 2 * q;
+        if (last)  // the result takes X's upper part's place
+          st_shared_b32(x + (r * kPitch + c) * 2, pack_bf16x2(d[t][e] * (1.f / kScaleX), d[t][e + 1] * (1.f / kScaleX)));
+        else
+          put(x, kPitch, kXPart, r, c, d[t][e], d[t][e + 1]);
+      }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < size; i += kThreads) {
+    const int a = i / line, c = i - a * line;
+    out[at + i] = static_cast<uint16_t>(ld_shared_u16(x + ((tall ? c : a) * kPitch + (tall ? a : c)) * 2));
+  }
+}
+
+template <typename E, int kCols>
+cudaError_t launch(const OrthoArgs& A, int m, int k, cudaStream_t s) {
+  constexpr int kSmem = 4 * kRows * (kCols + 8) + 8 * kRows * kSquare;
+  static std::atomic<uint64_t> ready{0};
+  const auto kernel = ortho_small_kernel<E, kCols>;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kSmem, ready);
+  if (e != cudaSuccess) return e;
+  kernel<<<static_cast<unsigned>(A.n), kThreads, kSmem, s>>>(static_cast<const E*>(A.g), A.out, m, k, A.rows > A.cols, A.steps,
+                                                             A.eps);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool ortho_small(int64_t rows, int64_t cols) {
+  const int64_t m = rows < cols ? rows : cols, k = rows < cols ? cols : rows;
+  return m <= kRows && k <= 256;
+}
+
+cudaError_t launch_ortho_small(const OrthoArgs& A, cudaStream_t s) {
+  const int m = A.rows < A.cols ? A.rows : A.cols, k = A.rows < A.cols ? A.cols : A.rows;
+  if (A.bf16)
+    return k <= 64 ? launch<uint16_t, 64>(A, m, k, s) : k <= 128 ? launch<uint16_t, 128>(A, m, k, s) : launch<uint16_t, 256>(A, m, k, s);
+  return k <= 64 ? launch<float, 64>(A, m, k, s) : k <= 128 ? launch<float, 128>(A, m, k, s) : launch<float, 256>(A, m, k, s);
+}
+
+}  // namespace m2rnn
