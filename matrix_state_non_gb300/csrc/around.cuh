@@ -113,6 +113,16 @@ struct OrthoArgs {
   bool bf16;
 };
 
+// 1 / (sqrt(sum) + eps) with few fp64 operations (slow here): the root of the sum times an even power of two.
+__device__ __forceinline__ float inverse_norm(double sum, float eps) {
+  float norm = static_cast<float>(sum);  // 0, an infinity or NaN
+  if (sum > 0. && sum < 1.7e308) {
+    const int half = ((__double2hiint(sum) >> 20) - 1023) >> 1;
+    norm = scalbnf(sqrtf(static_cast<float>(sum * __hiloint2double((1023 - 2 * half) << 20, 0))), half);
+  }
+  return 1.f / (norm + eps);
+}
+
 size_t ortho_scratch_bytes(int64_t n, int64_t rows, int64_t cols);
 cudaError_t launch_orthogonalize(const OrthoArgs& a, cudaStream_t s);
 // Matrices that a block has in shared memory (no scratch).

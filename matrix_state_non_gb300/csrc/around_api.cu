@@ -228,9 +228,7 @@ int m2rnn_orthogonalize(const void* g, void* out, int64_t n, int64_t rows, int64
   a.ws = static_cast<char*>(workspace) + sizeof(StatusBlock);
   a.n = n; a.rows = static_cast<int>(rows); a.cols = static_cast<int>(cols); a.steps = steps; a.eps = eps;
   a.bf16 = dtype == M2RNN_BF16;
-  const cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  if (cudaMemsetAsync(workspace, 0, sizeof(StatusBlock), s) != cudaSuccess) return M2RNN_ERR_CUDA;
-  return cuda_status(launch_orthogonalize(a, s));
+  return cuda_status(launch_orthogonalize(a, static_cast<cudaStream_t>(cuda_stream)));  // (clears the status block)
 }
 
 }  // extern "C"

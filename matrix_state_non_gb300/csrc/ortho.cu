@@ -93,7 +93,9 @@ __device__ double square_sum(const E* g, int64_t from, int64_t to, bool vec) {
 }
 
 template <typename E>
-__global__ void __launch_bounds__(kSumThreads) ortho_sum_kernel(const E* g, int64_t size, int parts, double* part) {
+__global__ void __launch_bounds__(kSumThreads) ortho_sum_kernel(const E* g, int64_t size, int parts, double* part,
+                                                                StatusBlock* status) {
+  if (blockIdx.x == 0 && threadIdx.x < sizeof(StatusBlock) / 4) reinterpret_cast<uint32_t*>(status)[threadIdx.x] = 0u;
   __shared__ double red[kSumThreads / 32];
   const int64_t mat = blockIdx.x / parts;
   const int p = static_cast<int>(blockIdx.x - mat * parts);
@@ -117,7 +119,7 @@ __device__ __forceinline__ float first_factor(const double* part, int parts, flo
     for (int i = threadIdx.x; i < parts; i += 32) acc += part[i];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (threadIdx.x == 0) *shared = static_cast<float>(1. / (sqrt(acc) + eps));
+    if (threadIdx.x == 0) *shared = inverse_norm(acc, eps);
   }
   __syncthreads();
   return *shared;
@@ -888,7 +890,7 @@ template <typename E>
 cudaError_t load_first(const OrthoArgs& A, const Scratch& w, int m, int k, bool tall, cudaStream_t s) {
   const E* g = static_cast<const E*>(A.g);
   ortho_sum_kernel<E><<<static_cast<unsigned>(A.n * w.parts), kSumThreads, 0, s>>>(g, static_cast<int64_t>(m) * k, w.parts,
-                                                                                   w.part);
+                                                                                   w.part, A.status);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (tall) {
