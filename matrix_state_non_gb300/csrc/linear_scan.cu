@@ -177,40 +177,43 @@ struct Lane {
 // ---------------------------------------------------------------------------
 // The gate, for two channels
 // ---------------------------------------------------------------------------
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+
 struct Gate2 {
-  float2 f, e, soft, t;  // e = 1 - f; t = exp(-|z|)
+  float2 f, e, soft, t;  // e = 1 - f; soft = softplus(z) log2 e; t = exp(-|z|)
 };
 
-// All to a few units of fp32.  softplus(z) = max(z, 0) + log(1 + t), t = exp(-|z|),
-// and log(1 + t) = 2 atanh(v), v = t / (2 + t) <= 1/3: a polynomial in v^2 of
-// degree 4 (minimax, 4e-9).  1 - f = u P(u), u = alpha softplus, for |u| <= 0.7
-// (minimax, 3e-8), so that it keeps its digits where f is near 1, and f is what
-// is left; beyond, f = 2^(-u log2 e).  kSmall: f keeps its digits where it is
-// near 0 too, which only gradients show.
+// All to a few units of fp32, from y = z log2 e.  With t = 2^-|y|,
+//     softplus(z) log2 e = max(y, 0) + log2(1 + t),
+// and log2(1 + t) = 2 log2 e atanh(v), v = t / (2 + t) <= 1/3: a polynomial in v^2
+// of degree 4 (minimax, 4e-9).  f = 2^-w, w = alpha softplus(z) log2 e; 1 - f is
+// w P(w) for |w| <= 0.7 (minimax, 8e-8), so that it keeps its digits where f is
+// near 1, and f is what is left; beyond, f is the hardware's power.  kSmall: f
+// keeps its digits where it is near 0 too, which only gradients show.
+// Multiply-adds bound the kernels (two channels to an instruction, two cycles
+// each): log2(1 + t) by a polynomial in t, one reciprocal less and three of them
+// more, is 7 % slower.
 template <bool kSmall>
-__device__ __forceinline__ Gate2 gate_of(float2 z, float2 alpha) {
-  constexpr float kLog2e = 1.44269504f;
+__device__ __forceinline__ Gate2 gate_of(float2 y, float2 alpha) {
   Gate2 g;
-  const float2 y = mul_2(z, two(kLog2e));
   g.t = make_float2(ex2_fast(-fabsf(y.x)), ex2_fast(-fabsf(y.y)));
-  const float2 w = add_2(g.t, two(2.f));
-  const float2 v = mul_2(g.t, make_float2(rcp_fast(w.x), rcp_fast(w.y)));
+  const float2 d = add_2(g.t, two(2.f));
+  const float2 v = mul_2(g.t, make_float2(rcp_fast(d.x), rcp_fast(d.y)));
   const float2 s = mul_2(v, v);
-  float2 p = fma_2(s, two(0.28178346157f), two(0.27960598469f));
-  p = fma_2(s, p, two(0.40024909377f));
-  p = fma_2(s, p, two(0.66666316986f));
-  p = fma_2(s, p, two(2.f));
-  g.soft = fma_2(v, p, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
-  const float2 u = mul_2(alpha, g.soft);
-  p = fma_2(u, two(0.00019840967f), two(-0.00141012867f));
-  p = fma_2(u, p, two(0.00833449047f));
-  p = fma_2(u, p, two(-0.04166151583f));
-  p = fma_2(u, p, two(0.16666638851f));
-  p = fma_2(u, p, two(-0.50000029802f));
-  p = fma_2(u, p, two(1.f));
-  const float2 e = mul_2(u, p), x = mul_2(u, two(-kLog2e));
-  const float2 f = make_float2(ex2_fast(x.x), ex2_fast(x.y)), far = fma_2(f, two(-1.f), two(1.f));
-  const bool near0 = fabsf(u.x) <= 0.7f, near1 = fabsf(u.y) <= 0.7f;
+  float2 p = fma_2(s, two(0.40652760863f), two(0.40338617563f));
+  p = fma_2(s, p, two(0.57743740082f));
+  p = fma_2(s, p, two(0.96179163456f));
+  p = fma_2(s, p, two(2.88539004326f));
+  g.soft = fma_2(v, p, make_float2(fmaxf(y.x, 0.f), fmaxf(y.y, 0.f)));
+  const float2 w = mul_2(alpha, g.soft);
+  p = fma_2(w, two(-0.00015403463f), two(0.00134455867f));
+  p = fma_2(w, p, two(-0.00961854495f));
+  p = fma_2(w, p, two(0.05550206453f));
+  p = fma_2(w, p, two(-0.24022643268f));
+  p = fma_2(w, p, two(0.69314724207f));
+  const float2 e = mul_2(w, p);
+  const float2 f = make_float2(ex2_fast(-w.x), ex2_fast(-w.y)), far = fma_2(f, two(-1.f), two(1.f));
+  const bool near0 = fabsf(w.x) <= 0.7f, near1 = fabsf(w.y) <= 0.7f;
   g.e = make_float2(near0 ? e.x : far.x, near1 ? e.y : far.y);
   g.f = fma_2(g.e, two(-1.f), two(1.f));
   if constexpr (kSmall) g.f = make_float2(near0 ? g.f.x : f.x, near1 ? g.f.y : f.y);
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs 
   const E* px = static_cast<const E*>(A.x) + first * A.x_stride + me.from;
   const E* pa = static_cast<const E*>(A.a) + first * A.a_stride + me.from;
   E* py = static_cast<E*>(A.y) + first * A.C + me.c;
-  const float2 alpha = me.get(A.alpha), beta = me.get(A.beta);
+  const float2 alpha = me.get(A.alpha), beta = mul_2(me.get(A.beta), two(kLog2e));
   float2 carry = me.get(A.H_0 != nullptr ? A.H_0 + static_cast<int64_t>(b) * A.C : nullptr);
   const int rounds = (len + kTile * blocks - 1) / (kTile * blocks);
 
@@ -344,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs 
     for (int i = 0; i < kL; ++i) {
       const Raw2<E> a = kTma ? load_2<true>(ring.row(stage, 0, warp * kL + i), 0) : ra[kTma ? 0 : i];
       const Raw2<E> x = kTma ? load_2<true>(ring.row(stage, 1, warp * kL + i), 0) : rx[kTma ? 0 : i];
-      const Gate2 g = gate_of<false>(add_2(a.f(), beta), alpha);
+      const Gate2 g = gate_of<false>(fma_2(a.f(), two(kLog2e), beta), alpha);
       f[i] = g.f;
       in[i] = mul_2(g.e, x.f());
     }
@@ -418,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs
   const E* pd = static_cast<const E*>(A.dy) + first * A.C + me.from;
   float *pdx = A.dx + first * A.C + me.c, *pda = A.da + first * A.C + me.c;
   const float* ph = states + static_cast<int64_t>(b) * ((A.T + kL - 1) / kL) * A.C;
-  const float2 alpha = me.get(A.alpha), beta = me.get(A.beta);
+  const float2 alpha = me.get(A.alpha), beta = mul_2(me.get(A.beta), two(kLog2e));
   const float2 minus_alpha = make_float2(-alpha.x, -alpha.y);
   float2 carry = me.get(A.dH_T != nullptr ? A.dH_T + static_cast<int64_t>(b) * A.C : nullptr);
   float2 sa = two(0.f), sb = two(0.f);
@@ -461,12 +464,12 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs
       const Raw2<E> qa = kTma ? load_2<true>(ring.row(stage, 0, r0 + i), 0) : ra[kTma ? 0 : i];
       const Raw2<E> qx = kTma ? load_2<true>(ring.row(stage, 1, r0 + i), 0) : rx[kTma ? 0 : i];
       const Raw2<E> qd = kTma ? load_2<true>(ring.row(stage, 2, r0 + i), 0) : rd[kTma ? 0 : i];
-      const float2 z = add_2(qa.f(), beta), x = qx.f();
-      const Gate2 g = gate_of<true>(z, alpha);
+      const float2 y = fma_2(qa.f(), two(kLog2e), beta), x = qx.f();
+      const Gate2 g = gate_of<true>(y, alpha);
       f[i] = g.f;
       e[i] = g.e;
       const float2 w = add_2(g.t, two(1.f));
-      const float2 sig = make_float2((z.x >= 0.f ? 1.f : g.t.x) * rcp_fast(w.x), (z.y >= 0.f ? 1.f : g.t.y) * rcp_fast(w.y));
+      const float2 sig = make_float2((y.x >= 0.f ? 1.f : g.t.x) * rcp_fast(w.x), (y.y >= 0.f ? 1.f : g.t.y) * rcp_fast(w.y));
       const float2 away = mul_2(g.f, make_float2(h.x - x.x, h.y - x.y));
       ma[i] = mul_2(away, mul_2(minus_alpha, sig));
       ms[i] = mul_2(away, make_float2(-g.soft.x, -g.soft.y));
@@ -529,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs
       t.w += s.w;
     }
     float* p = part + (static_cast<int64_t>(b) * blocks + rank) * 2 * A.C;
-    me.put(p, make_float2(t.x, t.y));
+    me.put(p, make_float2(t.x * kLn2, t.y * kLn2));  // (softplus in units of log2)
     me.put(p + A.C, make_float2(t.z, t.w));
   }
 }
@@ -546,37 +549,37 @@ __global__ void __launch_bounds__(128) linear_step_kernel(float* H, LinearArgs A
   const Raw2<E> a = load_2<kPair>(static_cast<const E*>(A.a) + b * A.a_stride + me.from, me.other);
   const Raw2<E> x = load_2<kPair>(static_cast<const E*>(A.x) + b * A.x_stride + me.from, me.other);
   const int64_t at = static_cast<int64_t>(b) * A.C;
-  const Gate2 g = gate_of<false>(add_2(a.f(), me.get(A.beta)), me.get(A.alpha));
+  const Gate2 g = gate_of<false>(mul_2(add_2(a.f(), me.get(A.beta)), two(kLog2e)), me.get(A.alpha));
   const float2 h = fma_2(g.f, me.get(H + at), mul_2(g.e, x.f()));
   me.put(H + at, h);
   store_2<kPair>(static_cast<E*>(A.y) + at + me.c, h, me.in0, me.in1);
 }
 
-// Sums over parts: the warps of a block take parts in turn, each of 32 columns,
-// then add up in order.
-constexpr int kSumWarps = 32;
-__global__ void __launch_bounds__(32 * kSumWarps) sum_parts_kernel(const float* part, float* out, float* out2, int parts,
-                                                                   int64_t D, int64_t width) {
-  __shared__ float red[kSumWarps][33];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t j = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+// Sums over parts: a block has 8 columns, its threads take parts in turn, then
+// add up as a tree.
+constexpr int kSumThreads = 1024, kSumCols = 8, kSumRows = kSumThreads / kSumCols;
+__global__ void __launch_bounds__(kSumThreads) sum_parts_kernel(const float* part, float* out, float* out2, int parts,
+                                                                int64_t D, int64_t width) {
+  __shared__ float red[kSumRows][kSumCols + 1];
+  const int col = threadIdx.x % kSumCols, row = threadIdx.x / kSumCols, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t j = static_cast<int64_t>(blockIdx.x) * kSumCols + col;
   wait_previous();
   float t = 0.f;
   if (j < width) {
-#pragma unroll 8
-    for (int p = warp; p < parts; p += kSumWarps) t += part[p * width + j];
+#pragma unroll 4
+    for (int p = row; p < parts; p += kSumRows) t += part[p * width + j];
   }
-  red[warp][lane] = t;
+  red[row][col] = t;
   __syncthreads();
-  // lane w of warp c has what warp w found of columns c, so that the tree's order is fixed
-  for (int c = warp; c < 32; c += kSumWarps) {
-    float v = red[lane][c];
+  if (warp >= kSumCols) return;
+  float v = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const int64_t k = static_cast<int64_t>(blockIdx.x) * 32 + c;
-    if (lane == 0 && k < D) out[k] = v;
-    if (lane == 0 && k >= D && k < width && out2 != nullptr) out2[k - D] = v;
-  }
+  for (int r = 0; r < kSumRows; r += 32) v += red[r + lane][warp];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int64_t k = static_cast<int64_t>(blockIdx.x) * kSumCols + warp;
+  if (lane == 0 && k < D) out[k] = v;
+  if (lane == 0 && k >= D && k < width && out2 != nullptr) out2[k - D] = v;
 }
 
 constexpr int kEveryBf16 = 8, kEveryF32 = 4;  // steps of a segment of the backward
@@ -660,7 +663,7 @@ size_t linear_backward_scratch_bytes(int64_t B, int64_t T, int64_t C) {
 
 cudaError_t launch_sum_parts(const float* part, float* out, float* out2, bool two, int parts, int64_t D, cudaStream_t s) {
   const int64_t width = two ? 2 * D : D;
-  return launch_next(sum_parts_kernel, static_cast<unsigned>((width + 31) / 32), 32 * kSumWarps, 0, s, part, out, out2, parts, D, width);
+  return launch_next(sum_parts_kernel, static_cast<unsigned>((width + kSumCols - 1) / kSumCols), kSumThreads, 0, s, part, out, out2, parts, D, width);
 }
 
 // Steps of a segment: 16 in bf16, 8 in fp32 (registers); of the backward's, kEvery.
