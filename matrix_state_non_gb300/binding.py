@@ -1032,26 +1032,31 @@ def residual_norm(x, w, residual=None, *, eps: float = 1e-6, dtype=None, out=Non
     8-bit type.  ``out`` may hold preallocated y / h / scale; its h may be the
     residual itself."""
     import torch
-    shape, D, gpu, f32 = x.shape, x.shape[-1], _gpu(x), torch.float32
+    shape, gpu, f32 = x.shape, _gpu(x), torch.float32
+    D = shape[-1]
+    code = _dtype_code(x)
     ty = x.dtype if dtype is None else dtype
     eight = ty is torch.float8_e4m3fn
-    if not eight and ty is not torch.bfloat16 and ty is not f32:
+    if eight:
+        ycode = M2RNN_E4M3
+    elif ty is torch.bfloat16 or ty is f32:
+        ycode = M2RNN_BF16 if ty is torch.bfloat16 else M2RNN_F32
+    else:
         raise TypeError(f"unsupported output dtype {ty}")
-    code = _dtype_code(x)
     rows = x.numel() // D if D else 0
     xp, xs = _flat_rows(x, "x", x.dtype, gpu)
-    res = {}
-    hcode = code
+    res, hcode, rp, hp, sp = {}, code, None, None, None
     if residual is not None:
         hcode = _dtype_code(residual)
-        res["h"] = _out(out, "h", x, shape, residual.dtype, stream)
+        rp = _need(residual, "residual", shape, residual.dtype, gpu)
+        res["h"] = h = _out(out, "h", x, shape, residual.dtype, stream)
+        hp = h.data_ptr()
     res["y"] = y = _out(out, "y", x, shape, ty, stream)
     if eight:
-        res["scale"] = _out(out, "scale", x, shape[:-1] + (-(-D // SCALE_BLOCK),), f32, stream)
-    st = load().m2rnn_residual_norm(
-        xp, xs, None if residual is None else _need(residual, "residual", shape, residual.dtype, gpu),
-        _need(w, "w", (D,), f32, gpu), float(eps), _ptr(res.get("h")), y.data_ptr(), _ptr(res.get("scale")), rows, D,
-        code, hcode, M2RNN_E4M3 if eight else _dtype_code(y), _on(gpu, stream))
+        res["scale"] = scale = _out(out, "scale", x, shape[:-1] + (-(-D // SCALE_BLOCK),), f32, stream)
+        sp = scale.data_ptr()
+    st = load().m2rnn_residual_norm(xp, xs, rp, _need(w, "w", (D,), f32, gpu), eps, hp, y.data_ptr(), sp, rows, D, code,
+                                    hcode, ycode, _on(gpu, stream))
     _check(st, "m2rnn_residual_norm")
     return res
 

@@ -42,6 +42,9 @@ __device__ __forceinline__ float2 fma_2(float2 a, float2 b, float2 c) {
   fma2(c.x, c.y, a.x, a.y, b.x, b.y);
   return c;
 }
+__device__ __forceinline__ float2 fma_1(float2 a, float2 b, float2 c) {  // an instruction each
+  return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
+}
 __device__ __forceinline__ float2 mul_2(float2 a, float2 b) {
   float2 d;
   mul2(d.x, d.y, a.x, a.y, b.x, b.y);
@@ -190,9 +193,11 @@ struct Gate2 {
 // w P(w) for |w| <= 0.7 (minimax, 8e-8), so that it keeps its digits where f is
 // near 1, and f is what is left; beyond, f is the hardware's power.  kSmall: f
 // keeps its digits where it is near 0 too, which only gradients show.
-// Multiply-adds bound the kernels (two channels to an instruction, two cycles
-// each): log2(1 + t) by a polynomial in t, one reciprocal less and three of them
-// more, is 7 % slower.
+// Multiply-adds bound the kernels.  Two channels to an instruction take two
+// cycles of one of the two pipes, so some (here and in the scan itself) are left
+// single for the other: B=2 T=16384 C=1024 bf16 takes 56.7 us so, 62 with all in
+// pairs, 65 with none.  log2(1 + t) by a polynomial in t, one reciprocal less and
+// three multiply-adds more, is 7 % slower.
 template <bool kSmall>
 __device__ __forceinline__ Gate2 gate_of(float2 y, float2 alpha) {
   Gate2 g;
@@ -208,10 +213,10 @@ __device__ __forceinline__ Gate2 gate_of(float2 y, float2 alpha) {
   const float2 w = mul_2(alpha, g.soft);
   p = fma_2(w, two(-0.00015403463f), two(0.00134455867f));
   p = fma_2(w, p, two(-0.00961854495f));
-  p = fma_2(w, p, two(0.05550206453f));
-  p = fma_2(w, p, two(-0.24022643268f));
-  p = fma_2(w, p, two(0.69314724207f));
-  const float2 e = mul_2(w, p);
+  p = fma_1(w, p, two(0.05550206453f));
+  p = fma_1(w, p, two(-0.24022643268f));
+  p = fma_1(w, p, two(0.69314724207f));
+  const float2 e = make_float2(w.x * p.x, w.y * p.y);
   const float2 f = make_float2(ex2_fast(-w.x), ex2_fast(-w.y)), far = fma_2(f, two(-1.f), two(1.f));
   const bool near0 = fabsf(w.x) <= 0.7f, near1 = fabsf(w.y) <= 0.7f;
   g.e = make_float2(near0 ? e.x : far.x, near1 ? e.y : far.y);
@@ -361,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs 
     }
 #pragma unroll
     for (int i = 0; i < kL; ++i) {
-      U = fma_2(f[i], U, in[i]);
-      F = mul_2(f[i], F);
+      U = fma_1(f[i], U, in[i]);
+      F = make_float2(f[i].x * F.x, f[i].y * F.y);
     }
     const int now = t0;
     t0 += kTile * blocks;
@@ -381,13 +386,13 @@ __global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs 
       if (now + kL <= len) {
 #pragma unroll
         for (int i = 0; i < kL; ++i, p += A.C) {
-          h = fma_2(f[i], h, in[i]);
+          h = fma_1(f[i], h, in[i]);
           store_2<kPair>(p, h, me.in0, me.in1);
         }
       } else {
 #pragma unroll
         for (int i = 0; i < kL; ++i, p += A.C) {
-          h = fma_2(f[i], h, in[i]);
+          h = fma_1(f[i], h, in[i]);
           if (now + i < A.T) store_2<kPair>(p, now + i < len ? h : two(0.f), me.in0, me.in1);
         }
       }
