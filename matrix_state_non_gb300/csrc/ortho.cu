@@ -231,6 +231,7 @@ struct Operands {
 };
 
 constexpr int kRows = 128, kDepth = 64;  // a tile's rows, the inner dimension of a stage
+constexpr int kBoxRows = 32;            // of the right operand's loads, K-major
 constexpr int kBlockBytes = 32 * 32 * 2;   // what an epilogue warp stores at once
 constexpr int kEpilogueWarps = 8, kFirstEpilogue = 2, kProductThreads = 32 * (kFirstEpilogue + kEpilogueWarps);
 
@@ -490,7 +491,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           } else {
 #pragma unroll
             for (int r = 0; r < S::kOwnN; r += kRows)
-              tma_load_3d<kPair>(to + S::kLeft + r * kDepth * 2, &O.right, bar, d * kDepth, n0 + r, mat);
+              tma_load_3d<kPair>(to + S::kLeft + r * kDepth * 2, &O.left, bar, d * kDepth, n0 + r, mat);
           }
         }
       }
@@ -623,27 +624,26 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 }
 
 // ---------------------------------------------------------------------------
-// The same products where there are few tiles: the `split` blocks of a cluster
-// share a tile's inner dimension, leave their accumulators in shared memory, and
-// each finishes its share of the tile's columns from everybody's.  A tile to a
-// cluster, so that the time is that of a few stages.  1024 x 1024, one matrix:
+// The same products where there are few tiles: a narrow tile (kN columns) to a
+// block, so that there are enough of them, and nothing that a block does twice.
+// The time is that of a launch behind another (2 us) and of a tile's operands on
+// their way to one SM.
 // ===
 // ---------------------------------------------------------------------------
-template <bool kLow>
-struct SplitShape {
-  static constexpr int kN = 128, kStages = kLow ? 3 : 4;
+template <int kN, bool kLow>
+struct NarrowShape {
   static constexpr int kLeft = kRows * kDepth * 2, kRight = kN * kDepth * 2, kStage = kLeft + kRight * (kLow ? 2 : 1);
-  static constexpr int kOffRing = kStages * kStage, kOffBar = kOffRing + kEpilogueWarps * 2 * 2 * kBlockBytes;
-  static constexpr int kSmem = kOffBar + 512 + 1024;
-  static_assert(kOffRing >= kRows * kN * 4, "the accumulators take the stages' place");
-  static_assert(kSmem <= 227 * 1024, "shared memory");
+  static constexpr int kStages = 98304 / kStage;
+  // Once the products are done the stages hold the epilogue's blocks, kBlocks to a warp.
+  static constexpr int kTurn = 2 * kBlockBytes, kBlocks = kN > 64 ? kN / 64 : 1;
+  static constexpr int kOffBar = kStages * kStage, kSmem = kOffBar + 512 + 1024;
+  static_assert(kStages <= 8 && kOffBar >= kEpilogueWarps * kBlocks * kTurn, "the stages' place");
+  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "the next launch's blocks come to the same SMs");
 };
 
-template <int kMode, bool kLow>
-__global__ void __launch_bounds__(kProductThreads, 1)
-    ortho_split_kernel(const __grid_constant__ Operands O, ProductArgs A, int split) {
-  using S = SplitShape<kLow>;
-  constexpr int kN = S::kN;
+template <int kMode, int kN, bool kLow>
+__global__ void __launch_bounds__(kProductThreads, 2) ortho_narrow_kernel(const __grid_constant__ Operands O, ProductArgs A) {
+  using S = NarrowShape<kN, kLow>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -651,19 +651,25 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   auto full = [&](int s) { return bars + 8 * s; };
   auto empty = [&](int s) { return bars + 64 + 8 * s; };
   const uint32_t done = bars + 128;
-  auto there = [&](int w, int x) { return bars + 192 + 8 * (2 * w + x); };
+  auto there = [&](int w) { return bars + 192 + 8 * w; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffBar + 160);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffBar + 164);
-  const int rank = split == 1 ? 0 : static_cast<int>(cluster_ctarank());
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(full(s), 1);
       mbar_init(empty(s), 1);
     }
     mbar_init(done, 1);
-    for (int s = 0; s < 2 * kEpilogueWarps; ++s) mbar_init(there(0, s), 1);
+    for (int s = 0; s < kEpilogueWarps; ++s) mbar_init(there(s), 1);
     *abort_flag = 0;
     fence_mbar_init_cluster();
+  }
+  if (warp == 0 && lane == 1) {
+    tma_prefetch_desc(&O.left);
+    tma_prefetch_desc(&O.right);
+    if (kLow) tma_prefetch_desc(&O.right_low);
+    if (kMode != kGram) tma_prefetch_desc(&O.in);
+    tma_prefetch_desc(&O.out);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), kN);
@@ -674,14 +680,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  const Item t = item_at<kMode, kN, kRows>(A, blockIdx.x / split);
-  const int mat = static_cast<int>(t.mat);
-  const int depth = (A.inner + kDepth - 1) / kDepth, d0 = depth * rank / split, d1 = depth * (rank + 1) / split;
-  // a warp's blocks: 32 rows, of the block's own columns (kN / split: 128, 64 or 32) every second 32
+  const Item t = item_at<kMode, kN, kRows>(A, blockIdx.x);
+  const int mat = static_cast<int>(t.mat), depth = (A.inner + kDepth - 1) / kDepth;
+  // a warp's blocks: 32 rows, every second 32 of the columns
   const int me = warp - kFirstEpilogue, quarter = warp & 3, half = me >> 2;
-  const int own = kN / split, r0 = t.i * kRows + quarter * 32, blocks = (own / 32 + 1 - half) / 2;
-  auto column = [&](int x) { return rank * own + 32 * (half + 2 * x); };  // in the tile
-  const uint32_t ring = base + S::kOffRing + me * 2 * 2 * kBlockBytes;
+  const int r0 = t.i * kRows + quarter * 32, blocks = (kN / 32 + 1 - half) / 2;
+  auto column = [&](int x) { return 32 * (half + 2 * x); };  // in the tile
+  const uint32_t ring = base + me * S::kBlocks * S::kTurn;
   wait_previous();
 
   if (warp == 0) {
@@ -689,7 +694,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       asm volatile("fence.proxy.async;" ::: "memory");
       bool ok = true;
       int u = 0;
-      for (int d = d0; d < d1; ++d, ++u) {
+      for (; u < depth; ++u) {
         const int s = u % S::kStages;
         if (u >= S::kStages && !mbar_wait(empty(s), (u / S::kStages - 1) & 1, abort_flag, A.status, kWhereOrthoEmpty)) {
           ok = false;
@@ -697,15 +702,17 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
         const uint32_t to = base + s * S::kStage, bar = full(s);
         mbar_arrive_expect_tx(bar, S::kStage);
-        tma_load_3d<false>(to, &O.left, bar, d * kDepth, t.i * kRows, mat);
+        tma_load_3d<false>(to, &O.left, bar, u * kDepth, t.i * kRows, mat);
         if constexpr (kMode == kUpdate) {
 #pragma unroll
           for (int c = 0; c < kN; c += 64) {
-            tma_load_3d<false>(to + S::kLeft + c * kDepth * 2, &O.right, bar, t.j * kN + c, d * kDepth, mat);
-            if (kLow) tma_load_3d<false>(to + S::kLeft + S::kRight + c * kDepth * 2, &O.right_low, bar, t.j * kN + c, d * kDepth, mat);
+            tma_load_3d<false>(to + S::kLeft + c * kDepth * 2, &O.right, bar, t.j * kN + c, u * kDepth, mat);
+            if (kLow) tma_load_3d<false>(to + S::kLeft + S::kRight + c * kDepth * 2, &O.right_low, bar, t.j * kN + c, u * kDepth, mat);
           }
         } else {
-          tma_load_3d<false>(to + S::kLeft, &O.right, bar, d * kDepth, t.j * kN, mat);
+#pragma unroll
+          for (int r = 0; r < kN; r += kBoxRows)
+            tma_load_3d<false>(to + S::kLeft + r * kDepth * 2, &O.right, bar, u * kDepth, t.j * kN + r, mat);
         }
       }
       if (!ok)
@@ -715,7 +722,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   } else if (warp == 1) {
     constexpr uint32_t kId = idesc_f16_f32(kRows, kN, false, kMode == kUpdate);
     int u = 0;
-    for (int d = d0; d < d1; ++d, ++u) {
+    for (; u < depth; ++u) {
       const int s = u % S::kStages;
       if (!warp_wait(full(s), (u / S::kStages) & 1, abort_flag, A.status, kWhereOrthoFull)) break;
       if (elect_one()) {
@@ -731,64 +738,37 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           }
         }
         tc_commit(empty(s));
-        if (d == d1 - 1) tc_commit(done);
+        if (u == depth - 1) tc_commit(done);
       }
       __syncwarp();
     }
     if (*abort_flag)
       for (int x = max(0, u - S::kStages); x < u; ++x)
         mbar_wait_timed(empty(x % S::kStages), (x / S::kStages) & 1, nullptr, kWhereOrthoDrain);
-  } else {
-    if (kMode != kGram && lane == 0) {
-      asm volatile("fence.proxy.async;" ::: "memory");
-      for (int x = 0; x < blocks; ++x) {
-        const uint32_t to = ring + x * 2 * kBlockBytes;
-        mbar_arrive_expect_tx(there(me, x), kMode == kUpdate ? 2 * kBlockBytes : kBlockBytes);
-        tma_load_3d<false>(to, &O.in, there(me, x), t.j * kN + column(x), r0, mat);
-        if (kMode == kUpdate) tma_load_3d<false>(to + kBlockBytes, &O.in_low, there(me, x), t.j * kN + column(x), r0, mat);
-      }
-    }
-    warp_wait(done, 0, abort_flag, A.status, kWhereOrthoDone);
-    tc_fence_after_sync();
-    if (split > 1) {  // the accumulators, a column after another
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int c = 64 * half + 32 * x;
-        uint32_t acc[32];
-        tmem_ld_32x32b<32>(tmem + c + (static_cast<uint32_t>(32 * quarter) << 16), acc);
-        tmem_ld_wait();
-        tmem_ld_fence_regs(acc);
-#pragma unroll
-        for (int e = 0; e < 32; ++e)
-          asm volatile("st.shared.b32 [%0], %1;" ::"r"(base + ((c + e) * kRows + quarter * 32 + lane) * 4), "r"(acc[e]) : "memory");
-      }
-    }
-  }
-  __syncwarp();
-  if (split > 1) cluster_sync_all();
-  if (warp >= kFirstEpilogue) {
+  } else if (warp_wait(done, 0, abort_flag, A.status, kWhereOrthoDone) && blocks > 0) {
+    // ---------------- epilogue, in the stages' place ----------------
     const int cols = kMode == kUpdate ? A.k : A.m;
-    for (int x = 0; x < blocks; ++x) {
-      const int c = column(x), c0 = t.j * kN + c;
-      const uint32_t block = ring + x * 2 * kBlockBytes;
-      if (kMode != kGram) warp_wait(there(me, x), 0, abort_flag, A.status, kWhereOrthoIn);
-      if (r0 >= A.m || c0 >= cols || (kMode != kUpdate && c0 < r0)) continue;
-      uint32_t acc[32];
-      if (split == 1) {
-        tmem_ld_32x32b<32>(tmem + c + (static_cast<uint32_t>(32 * quarter) << 16), acc);
-        tmem_ld_wait();
-        tmem_ld_fence_regs(acc);
-      } else {
-        const uint32_t from = base + (c * kRows + quarter * 32 + lane) * 4;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) acc[e] = 0u;
-        for (int r = 0; r < split; ++r) {
-          const uint32_t there_ = mapa_shared(from, r);
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            acc[e] = __float_as_uint(__uint_as_float(acc[e]) + ld_shared_cluster_f32(there_ + e * kRows * 4));
+    if (kMode != kGram) {
+      if (lane == 0) {
+        asm volatile("fence.proxy.async;" ::: "memory");
+        mbar_arrive_expect_tx(there(me), blocks * (kMode == kUpdate ? S::kTurn : kBlockBytes));
+        for (int x = 0; x < blocks; ++x) {
+          const uint32_t to = ring + x * S::kTurn;
+          tma_load_3d<false>(to, &O.in, there(me), t.j * kN + column(x), r0, mat);
+          if (kMode == kUpdate) tma_load_3d<false>(to + kBlockBytes, &O.in_low, there(me), t.j * kN + column(x), r0, mat);
         }
       }
+      warp_wait(there(me), 0, abort_flag, A.status, kWhereOrthoIn);
+    }
+    tc_fence_after_sync();
+    for (int x = 0; x < blocks; ++x) {
+      const int c = column(x), c0 = t.j * kN + c;
+      const uint32_t block = ring + x * S::kTurn;
+      if (r0 >= A.m || c0 >= cols || (kMode != kUpdate && c0 < r0)) continue;
+      uint32_t acc[32];
+      tmem_ld_32x32b<32>(tmem + c + (static_cast<uint32_t>(32 * quarter) << 16), acc);
+      tmem_ld_wait();
+      tmem_ld_fence_regs(acc);
       float v[32];
       combine<kMode>(v, acc, block + lane * 64, (lane >> 1) & 3);
       emit<kMode>(O, A, v, block, r0, c0, mat, lane);
@@ -798,10 +778,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   let_next();
   tc_fence_before_sync();
   __syncwarp();
-  if (split > 1)
-    cluster_sync_all();  // no block ends while another reads from it
-  else
-    __syncthreads();
+  __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, kN);
 }
 
@@ -834,27 +811,43 @@ cudaError_t product(const Operands& o, ProductArgs a, int64_t n, cudaStream_t s)
   return launch_cluster(kernel, (a.items < most ? a.items : most) * kBlocks, kBlocks, kProductThreads, S::kSmem, true, s, o, a);
 }
 
-template <int kMode, bool kLow>
-cudaError_t split_product(const Operands& o, ProductArgs a, int64_t n, cudaStream_t s) {
-  using S = SplitShape<kLow>;
-  static std::atomic<uint64_t> ready{0};
-  const auto kernel = ortho_split_kernel<kMode, kLow>;
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem, ready);
-  if (e != cudaSuccess) return e;
-  const int stages = (a.inner + kDepth - 1) / kDepth;
-  int split = 1;
-  while (split < 4 && 2 * split * a.items <= 152 && 2 * split <= stages) split *= 2;
-  return launch_cluster(kernel, a.items * split, split, kProductThreads, S::kSmem, true, s, o, a, split);
-}
-
-// The tiles of 128 x 128 of n matrices.
-template <int kMode>
+// The tiles of 128 x kN of n matrices.
+template <int kMode, int kN>
 ProductArgs small_tiles(ProductArgs a, int64_t n) {
   a.tiles_m = (a.m + kRows - 1) / kRows;
-  a.tiles_n = ((kMode == kUpdate ? a.k : a.m) + 127) / 128;
-  a.tiles = kMode == kUpdate ? a.tiles_m * a.tiles_n : a.tiles_m * (a.tiles_m + 1) / 2;
+  a.tiles_n = ((kMode == kUpdate ? a.k : a.m) + kN - 1) / kN;
+  a.tiles = 0;
+  for (int i = 0; i < a.tiles_m; ++i) a.tiles += a.tiles_n - (kMode == kUpdate ? 0 : i * kRows / kN);
   a.items = n * a.tiles;
   return a;
+}
+
+template <int kMode, int kN, bool kLow>
+cudaError_t narrow_product(const Operands& o, const ProductArgs& a, cudaStream_t s) {
+  using S = NarrowShape<kN, kLow>;
+  static std::atomic<uint64_t> ready{0};
+  const auto kernel = ortho_narrow_kernel<kMode, kN, kLow>;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), S::kSmem, ready);
+  return e != cudaSuccess ? e : launch_next(kernel, static_cast<unsigned>(a.items), kProductThreads, S::kSmem, s, o, a);
+}
+
+// One product: by pairs of SMs (tiles of 256 x 256); where there are few tiles, by a block to each of the narrowest
+// that do not exceed the SMs; else by persistent blocks.  X's lower part enters P X where m is below 512.
+template <int kMode>
+cudaError_t run_product(const Operands& o, const ProductArgs& a, int64_t n, bool pair, cudaStream_t s) {
+  if (pair) return product<kMode, 256, false, true>(o, a, n, s);
+  if constexpr (kMode == kUpdate) {
+    const ProductArgs t = small_tiles<kMode, 64>(a, n);
+    if (a.m < 512) return t.items <= 152 ? narrow_product<kMode, 64, true>(o, t, s) : product<kMode, 128, true, false>(o, a, n, s);
+    if (t.items <= 152) return narrow_product<kMode, 64, false>(o, t, s);
+  } else {
+    ProductArgs t = small_tiles<kMode, 32>(a, n);
+    if (t.items <= 152) return narrow_product<kMode, 32, false>(o, t, s);
+    t = small_tiles<kMode, 64>(a, n);
+    if (t.items <= 152) return narrow_product<kMode, 64, false>(o, t, s);
+  }
+  const ProductArgs t = small_tiles<kMode, 128>(a, n);
+  return t.items <= 152 ? narrow_product<kMode, 128, false>(o, t, s) : product<kMode, 128, false, false>(o, a, n, s);
 }
 
 struct Scratch {
@@ -927,7 +920,8 @@ cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
   bool made = map_matrix(&to_poly.left, w.gram, A.n, m, m, w.square, kRows) &&
               map_matrix(&to_poly.in, w.gram, A.n, m, m, w.square, kEpilogueBox) &&
               map_matrix(&to_poly.out, w.poly, A.n, m, m, w.square, kEpilogueBox);
-  to_poly.right = to_poly.right_low = to_poly.left;
+  made = made && map_matrix(&to_poly.right, w.gram, A.n, m, m, w.square, kBoxRows);
+  to_poly.right_low = to_poly.right;
   to_poly.in_low = to_poly.out_low = to_poly.out;
   for (int i = 0; i < 2; ++i) {
     Operands &g = to_gram[i], &x = to_x[i];
@@ -935,7 +929,8 @@ cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
            map_matrix(&x.right, w.x[i], A.n, m, k, w.pitch, kDepth) && map_matrix(&x.right_low, w.low[i], A.n, m, k, w.pitch, kDepth) &&
            map_matrix(&x.in, w.x[i], A.n, m, k, w.pitch, kEpilogueBox) &&
            map_matrix(&x.in_low, w.low[i], A.n, m, k, w.pitch, kEpilogueBox);
-    g.right = g.right_low = g.left;
+    made = made && map_matrix(&g.right, w.x[i], A.n, m, k, w.pitch, kBoxRows);
+    g.right_low = g.right;
     g.out = g.out_low = g.in = g.in_low = to_poly.in;
   }
   for (int i = 0; i < 2; ++i) {
@@ -950,23 +945,13 @@ cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
     const int at = i & 1;
     const bool last = i == A.steps - 1;
     a.inner = k;
-    const ProductArgs tg = small_tiles<kGram>(a, A.n);
-    e = pair                 ? product<kGram, 256, false, true>(to_gram[at], a, A.n, s)
-        : tg.items * 2 <= 152 ? split_product<kGram, false>(to_gram[at], tg, A.n, s)
-                              : product<kGram, 128, false, false>(to_gram[at], a, A.n, s);
+    e = run_product<kGram>(to_gram[at], a, A.n, pair, s);
     if (e != cudaSuccess) break;
     a.inner = m;
-    const ProductArgs tp = small_tiles<kPoly>(a, A.n);
-    e = pair                 ? product<kPoly, 256, false, true>(to_poly, a, A.n, s)
-        : tp.items * 2 <= 152 ? split_product<kPoly, false>(to_poly, tp, A.n, s)
-                              : product<kPoly, 128, false, false>(to_poly, a, A.n, s);
+    e = run_product<kPoly>(to_poly, a, A.n, pair, s);
     if (e != cudaSuccess) break;
     a.last = last ? A.out : nullptr;
-    const Operands& o = last ? to_last : to_x[at];
-    const ProductArgs tu = small_tiles<kUpdate>(a, A.n);
-    e = pair                 ? product<kUpdate, 256, false, true>(o, a, A.n, s)
-        : tu.items * 2 <= 152 ? split_product<kUpdate, true>(o, tu, A.n, s)
-                              : product<kUpdate, 128, true, false>(o, a, A.n, s);
+    e = run_product<kUpdate>(last ? to_last : to_x[at], a, A.n, pair, s);
   }
   return e;
 }
