@@ -1,6 +1,7 @@
 """GB300 (sm_103a) M2RNN forward/backward scans behind a C ABI (libm2rnn.so),
 with the operators of the layer around them: the short causal convolution, a
-selective state space scan, gradient clipping.
+selective state space scan, gradient clipping; and around the layers the
+residual norm, a gated linear recurrence and the orthogonalised update.
 
 ``binding`` holds the ctypes wrappers of the C ABI and the torch helpers;
 ``inputs`` holds the seeded synthetic input generator.  The library is loaded

@@ -633,16 +633,16 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 template <int kN, bool kLow>
 struct NarrowShape {
   static constexpr int kLeft = kRows * kDepth * 2, kRight = kN * kDepth * 2, kStage = kLeft + kRight * (kLow ? 2 : 1);
-  static constexpr int kStages = 98304 / kStage;
+  static constexpr int kStages = 196608 / kStage > 8 ? 8 : 196608 / kStage;
   // Once the products are done the stages hold the epilogue's blocks, kBlocks to a warp.
   static constexpr int kTurn = 2 * kBlockBytes, kBlocks = kN > 64 ? kN / 64 : 1;
   static constexpr int kOffBar = kStages * kStage, kSmem = kOffBar + 512 + 1024;
   static_assert(kStages <= 8 && kOffBar >= kEpilogueWarps * kBlocks * kTurn, "the stages' place");
-  static_assert(2 * (kSmem + 1024) <= 228 * 1024, "the next launch's blocks come to the same SMs");
+  static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
 template <int kMode, int kN, bool kLow>
-__global__ void __launch_bounds__(kProductThreads, 2) ortho_narrow_kernel(const __grid_constant__ Operands O, ProductArgs A) {
+__global__ void __launch_bounds__(kProductThreads, 1) ortho_narrow_kernel(const __grid_constant__ Operands O, ProductArgs A) {
   using S = NarrowShape<kN, kLow>;
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
