@@ -695,9 +695,9 @@ def _on(gpu: int, stream) -> int:
 
 def _alloc(like, shape, dtype, stream):
     """A new tensor that belongs to the stream it is used on."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
     import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=like.device)
 

@@ -21,6 +21,10 @@
 // a round ahead into registers.  The backward marches the other way; the states before
 // its segments are left by the forward's kernel, without y, in one launch
 // before it.
+//
+// Bound by instructions, most of them the gate's multiply-adds, and by the
+// exchange's latency (0.9 us a round, partly behind the other block of an SM).  B=2
+// T=16384 C=1024 bf16: 57 us, 3.5 TB/s; backward B=4 T=4096: 27 + 52 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -589,16 +593,19 @@ __global__ void __launch_bounds__(kSumThreads) sum_parts_kernel(const float* par
 
 constexpr int kEveryBf16 = 8, kEveryF32 = 4;  // steps of a segment of the backward
 
-// Blocks to a cluster: more until two per SM are there, as long as each has a
-// tile of its own.
+// Blocks to a cluster: twice as many until 240 and more are there (two to an SM,
+// for most SMs), as long as each has a tile of its own.  More, in several waves,
+// lose: B=8 T=2048 C=1024 bf16 takes 27.6 us with 2 (one wave), 35.8 with 8; B=8
+// T=4096 C=640 42 and 49.
 int cluster_blocks(const LinearArgs& a, int tile) {
   const int64_t chains = static_cast<int64_t>(a.B) * ((a.C + kChan - 1) / kChan);
   int r = 1;
-  while (r < kMaxCluster && chains * r < 2 * 152 - 64 && r * tile < a.T) r *= 2;
+  while (r < kMaxCluster && chains * r < 240 && r * tile < a.T) r *= 2;
   return r;
 }
 
-// How rows can be read: value by value, two channels at a time, or by TMA.
+// How rows can be read: value by value, two channels at a time, or (on 16 bytes)
+// by TMA, which took B=2 T=16384 C=1024 bf16 from 79 to 67 us.
 enum class Access { kSingle, kPair, kTma };
 Access access_of(const LinearArgs& a) {
   const uintptr_t at = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.a);

@@ -18,7 +18,11 @@
 // grow: P X stays in the row space of X.  What they leave is 1.0e-3 to 1.9e-3 of
 // the result (1.3e-3 at 1024 x 1024 of random entries), the output's rounding to
 // bf16 1.7e-3.  With X's lower part in P X as well (kLow) it is 1.0e-3 to
-// 1.5e-3, which matrices too small to fill the GPU get for nothing.
+// 1.5e-3; matrices of fewer than 512 rows, where errors average least, get that.
+//
+// 24 of 1024 x 4096 bf16, 5 steps: 1.73 ms, of which A 5 x 90 us (1.4 PFLOP/s, 3.2
+// waves of tiles), P 5 x 36 (its epilogue), X' 5 x 185 (HBM, 5.4 TB/s: X read and
+// written in two parts), the norm and the first X 130.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -627,8 +631,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 // The same products where there are few tiles: a narrow tile (kN columns) to a
 // block, so that there are enough of them, and nothing that a block does twice.
 // The time is that of a launch behind another (2 us) and of a tile's operands on
-// their way to one SM.
-// ===
+// their way to one SM.  1024 x 1024, one matrix, 5 steps: 117 us; 2 of 1000 x 333:
+// 96 us (163 and 140 by persistent blocks with tiles of 128 x 128; 131 and 113 with
+// clusters of four that share a tile's inner dimension; 142 and 120 in one
+// cooperative launch with barriers across the grid).
 // ---------------------------------------------------------------------------
 template <int kN, bool kLow>
 struct NarrowShape {
@@ -910,9 +916,11 @@ cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
   const Scratch w(A.ws, A.n, A.rows, A.cols);
   cudaError_t e = A.bf16 ? load_first<uint16_t>(A, w, m, k, tall, s) : load_first<float>(A, w, m, k, tall, s);
   if (e != cudaSuccess) return e;
-  // pairs where their tiles fill the GPU
+  // Pairs where there are tiles of 256 x 256 for all of them and few of their rows are empty or short of work: 16 of
+  // 1024 x 1024 take 489 us by pairs and 518 without, 8 of 2048 x 2048 1198 and 1590, 24 of 512 x 4096 718 and 766;
+  // but 60 of 512 x 512 394 and 355, 60 of 600 x 700 916 and 883.
   const int64_t edge = (m + 255) / 256;
-  const bool pair = m >= 512 && A.n * edge * (edge + 1) / 2 >= 76;
+  const bool pair = A.n * edge * (edge + 1) / 2 >= 76 && (m > 768 || (m >= 512 && k >= 4096));
   ProductArgs a{};
   a.status = A.status; a.m = m; a.k = k; a.tall = tall;
   a.direct = A.cols % 8 != 0;
