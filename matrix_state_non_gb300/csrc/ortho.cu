@@ -224,7 +224,7 @@ struct ProductArgs {
   int m, k;   // X is m x k
   int inner;  // of the product
   int tiles_m, tiles_n, tiles;  // of one matrix; those that are computed
-  int64_t items;
+  int items;  // of all matrices
   bool tall;
   bool direct;  // last: rows that TMA cannot store (not on 16 bytes)
 };
@@ -257,18 +257,17 @@ struct Shape {
 };
 
 struct Item {
-  int64_t mat;
-  int i, j;  // tile's row and column
+  int mat, i, j;  // (a tile's row and column)
 };
 // Symmetric products: of row i the tiles with a column at or right of the diagonal.
 template <int kMode, int kN, int kTileRows>
-__device__ __forceinline__ Item item_at(const ProductArgs& A, int64_t id) {
+__device__ __forceinline__ Item item_at(const ProductArgs& A, int id) {
   Item t;
-  t.mat = id / A.tiles;
-  int left = static_cast<int>(id - t.mat * A.tiles);
+  t.mat = static_cast<unsigned>(id) / static_cast<unsigned>(A.tiles);
+  int left = id - t.mat * A.tiles;
   if constexpr (kMode == kUpdate) {
-    t.i = left % A.tiles_m;  // neighbours share the columns of X
-    t.j = left / A.tiles_m;
+    t.j = static_cast<unsigned>(left) / static_cast<unsigned>(A.tiles_m);
+    t.i = left - t.j * A.tiles_m;  // neighbours share the columns of X
   } else {
     t.i = 0;
     int first = 0;
@@ -441,7 +440,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::kOffBar + 164);
   static_assert(S::kStages <= 8, "barriers");
   const int rank = kPair ? static_cast<int>(cluster_ctarank()) : 0;
-  const int64_t first = blockIdx.x / kBlocks, step = gridDim.x / kBlocks;
+  const int first = blockIdx.x / kBlocks, step = gridDim.x / kBlocks;
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
       mbar_init(full(s), 1);
@@ -473,9 +472,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       asm volatile("fence.proxy.async;" ::: "memory");  // what earlier launches stored, before TMA reads it
       int u = 0;  // stages filled
       bool ok = true;
-      for (int64_t id = first; ok && id < A.items; id += step) {
+      for (int id = first; ok && id < A.items; id += step) {
         const Item t = item_at<kMode, kN, S::kTileRows>(A, id);
-        const int mat = static_cast<int>(t.mat);
+        const int mat = t.mat;
         for (int d = 0; d < depth; ++d, ++u) {
           const int s = u % S::kStages;
           if (u >= S::kStages && !mbar_wait(empty(s), (u / S::kStages - 1) & 1, abort_flag, A.status, kWhereOrthoEmpty)) {
@@ -509,7 +508,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     constexpr uint32_t kId = idesc_f16_f32(S::kTileRows, kN, false, kMode == kUpdate);
     int u = 0, n = 0;  // stages, tiles
     bool ok = true;
-    for (int64_t id = first; ok && id < A.items; id += step, ++n) {
+    for (int id = first; ok && id < A.items; id += step, ++n) {
       const int slot = n & 1;
       if (n >= 2 && !warp_wait(tfree(slot), ((n >> 1) - 1) & 1, abort_flag, A.status, kWhereOrthoFree)) break;
       tc_fence_after_sync();
@@ -550,42 +549,43 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const int cols = kMode == kUpdate ? A.k : A.m;
     constexpr int kPerTile = kN / 64;  // turns of a tile
     const uint32_t ring = base + S::kOffRing + me * S::kTurns * S::kTurn, swz = (lane >> 1) & 3;
-    const int64_t tiles = first < A.items ? (A.items - 1 - first) / step + 1 : 0;
-    const int64_t turns = tiles * kPerTile;
-    auto place = [&](int64_t u, int& r0, int& c0) {
-      const Item t = item_at<kMode, kN, S::kTileRows>(A, first + u / kPerTile * step);
-      r0 = t.i * S::kTileRows + rank * kRows + quarter * 32;
-      c0 = t.j * kN + half * (kN / 2) + static_cast<int>(u % kPerTile) * 32;
-      return static_cast<int>(t.mat);
-    };
-    auto read = [&](int64_t u) {  // by one lane
-      if (kMode == kGram || u >= turns) return;
-      int r0, c0;
-      const int mat = place(u, r0, c0), s = static_cast<int>(u % S::kTurns);
+    const int row = rank * kRows + quarter * 32, column = half * (kN / 2);  // in a tile
+    // One lane reads ahead: the next block to read is number `next` of tile `coming`.
+    int coming = first, next = 0, reads = 0;
+    Item ahead = item_at<kMode, kN, S::kTileRows>(A, first);
+    auto read = [&] {
+      if (kMode == kGram || coming >= A.items) return;
+      const int s = reads++ % S::kTurns;
+      const int r0 = ahead.i * S::kTileRows + row, c0 = ahead.j * kN + column + 32 * next;
       mbar_arrive_expect_tx(there(me, s), kMode == kUpdate ? S::kTurn : kBlockBytes);
-      tma_load_3d<false>(ring + s * S::kTurn, &O.in, there(me, s), c0, r0, mat);
-      if (kMode == kUpdate) tma_load_3d<false>(ring + s * S::kTurn + kBlockBytes, &O.in_low, there(me, s), c0, r0, mat);
+      tma_load_3d<false>(ring + s * S::kTurn, &O.in, there(me, s), c0, r0, ahead.mat);
+      if (kMode == kUpdate) tma_load_3d<false>(ring + s * S::kTurn + kBlockBytes, &O.in_low, there(me, s), c0, r0, ahead.mat);
+      if (++next == kPerTile) {
+        next = 0;
+        coming += step;
+        if (coming < A.items) ahead = item_at<kMode, kN, S::kTileRows>(A, coming);
+      }
     };
     if (lane == 0) {
       asm volatile("fence.proxy.async;" ::: "memory");
-      for (int u = 0; u < S::kTurns - 1; ++u) read(u);
+      for (int u = 0; u < S::kTurns - 1; ++u) read();
     }
-    int64_t u = 0;
+    int u = 0, n = 0;
     bool ok = true;
-    for (int n = 0; ok && n < tiles; ++n) {
-      const int slot = n & 1;
+    for (int id = first; ok && id < A.items; id += step, ++n) {
+      const Item t = item_at<kMode, kN, S::kTileRows>(A, id);
+      const int slot = n & 1, r0 = t.i * S::kTileRows + row;
       ok = warp_wait(done(slot), (n >> 1) & 1, abort_flag, A.status, kWhereOrthoDone);
       tc_fence_after_sync();
       const uint32_t tm = tmem + slot * kN + half * (kN / 2) + (static_cast<uint32_t>(32 * quarter) << 16);
 #pragma unroll 1
       for (int x = 0; ok && x < kPerTile; ++x, ++u) {
-        int r0, c0;
-        const int mat = place(u, r0, c0), s = static_cast<int>(u % S::kTurns);
+        const int c0 = t.j * kN + column + 32 * x, s = u % S::kTurns;
         const bool used = r0 < A.m && c0 < cols && (kMode == kUpdate || c0 >= r0);
         const uint32_t block = ring + s * S::kTurn, line = block + lane * 64;
         float v[32];
         if (kMode != kGram) {
-          ok = warp_wait(there(me, s), static_cast<uint32_t>(u / S::kTurns) & 1, abort_flag, A.status, kWhereOrthoIn);
+          ok = warp_wait(there(me, s), (u / S::kTurns) & 1, abort_flag, A.status, kWhereOrthoIn);
           if (!ok) break;
         }
         if (used) {
@@ -598,9 +598,9 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         __syncwarp();
         if (lane == 0) {  // the turn before has left shared memory: its place is free
           asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-          read(u + S::kTurns - 1);
+          read();
         }
-        if (used) emit<kMode>(O, A, v, block, r0, c0, mat, lane);
+        if (used) emit<kMode>(O, A, v, block, r0, c0, t.mat, lane);
       }
       if (!ok) break;
       tc_fence_before_sync();
@@ -611,9 +611,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     if (lane == 0) {
       if (!ok && kMode != kGram)  // what is on its way lands before the block ends
-        for (int64_t x = u; x < u + S::kTurns && x < turns; ++x)
-          mbar_wait_timed(there(me, static_cast<int>(x % S::kTurns)), static_cast<uint32_t>(x / S::kTurns) & 1, nullptr,
-                          kWhereOrthoDrain);
+        for (int x = u; x < reads; ++x) mbar_wait_timed(there(me, x % S::kTurns), (x / S::kTurns) & 1, nullptr, kWhereOrthoDrain);
       asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
   }
@@ -687,7 +685,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) ortho_narrow_kernel(const 
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   const Item t = item_at<kMode, kN, kRows>(A, blockIdx.x);
-  const int mat = static_cast<int>(t.mat), depth = (A.inner + kDepth - 1) / kDepth;
+  const int mat = t.mat, depth = (A.inner + kDepth - 1) / kDepth;
   // a warp's blocks: 32 rows, every second 32 of the columns
   const int me = warp - kFirstEpilogue, quarter = warp & 3, half = me >> 2;
   const int r0 = t.i * kRows + quarter * 32, blocks = (kN / 32 + 1 - half) / 2;
@@ -812,8 +810,8 @@ cudaError_t product(const Operands& o, ProductArgs a, int64_t n, cudaStream_t s)
   a.tiles_n = ((kMode == kUpdate ? a.k : a.m) + kN - 1) / kN;
   a.tiles = 0;
   for (int i = 0; i < a.tiles_m; ++i) a.tiles += a.tiles_n - (kMode == kUpdate ? 0 : i * S::kTileRows / kN);
-  a.items = n * a.tiles;
-  const int64_t most = 152 / kBlocks;
+  a.items = static_cast<int>(n * a.tiles);
+  const int most = 152 / kBlocks;
   return launch_cluster(kernel, (a.items < most ? a.items : most) * kBlocks, kBlocks, kProductThreads, S::kSmem, true, s, o, a);
 }
 
@@ -824,7 +822,7 @@ ProductArgs small_tiles(ProductArgs a, int64_t n) {
   a.tiles_n = ((kMode == kUpdate ? a.k : a.m) + kN - 1) / kN;
   a.tiles = 0;
   for (int i = 0; i < a.tiles_m; ++i) a.tiles += a.tiles_n - (kMode == kUpdate ? 0 : i * kRows / kN);
-  a.items = n * a.tiles;
+  a.items = static_cast<int>(n * a.tiles);
   return a;
 }
 
