@@ -128,5 +128,12 @@ cudaError_t launch_orthogonalize(const OrthoArgs& a, cudaStream_t s);
 // Matrices that a block has in shared memory (no scratch).
 bool ortho_small(int64_t rows, int64_t cols);
 cudaError_t launch_ortho_small(const OrthoArgs& a, cudaStream_t s);
+// Long matrices with a side of up to 64.
+bool ortho_thin(int64_t rows, int64_t cols);
+size_t ortho_thin_scratch_bytes(int64_t n, int64_t rows, int64_t cols);
+cudaError_t launch_ortho_thin(const OrthoArgs& a, cudaStream_t s);
+// Clears the status block and sums the squares of every matrix: part [n][parts].
+int ortho_sum_parts(int64_t size);
+cudaError_t launch_ortho_sum(const OrthoArgs& a, int parts, double* part, cudaStream_t s);
 
 }  // namespace m2rnn

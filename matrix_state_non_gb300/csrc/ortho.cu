@@ -11,7 +11,8 @@
 //
 // Precision.  Operands are fp16 (11 bits, rounded to nearest) with fixed powers
 // of two in front: the polynomial maps [0, 1.2025] into itself, so that no entry
-// of X exceeds 1.2025, of A 1.4461, of P 2.81.  X is kept in two fp16 parts (22
+// of X exceeds 1.2025, of A 1.4461, of P 2.81.  Matrices with a side of up to 64 are
+// taken by ortho_small.cu and ortho_thin.cu.  X is kept in two fp16 parts (22
 // bits) between steps: small singular values grow 480-fold in five steps, and
 // the rounding noise of X in one part would grow with them (for a matrix of
 // rank 1 the result would be 0.15 off; it is 3e-4).  Noise of A and P does not
@@ -864,8 +865,7 @@ struct Scratch {
     const int64_t m = rows < cols ? rows : cols, k = rows < cols ? cols : rows;
     pitch = static_cast<int>(round_up(k, 8));
     square = static_cast<int>(round_up(m, 8));
-    const int64_t want = (m * k + kSumCount - 1) / kSumCount;
-    parts = static_cast<int>(want < kSumParts ? want : kSumParts);
+    parts = ortho_sum_parts(m * k);
     uint8_t* at = static_cast<uint8_t*>(ws);
     bytes = 0;
     auto take = [&](int64_t size) {
@@ -886,9 +886,7 @@ struct Scratch {
 template <typename E>
 cudaError_t load_first(const OrthoArgs& A, const Scratch& w, int m, int k, bool tall, cudaStream_t s) {
   const E* g = static_cast<const E*>(A.g);
-  ortho_sum_kernel<E><<<static_cast<unsigned>(A.n * w.parts), kSumThreads, 0, s>>>(g, static_cast<int64_t>(m) * k, w.parts,
-                                                                                   w.part, A.status);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_ortho_sum(A, w.parts, w.part, s);
   if (e != cudaSuccess) return e;
   if (tall) {
     const int tiles_m = (m + kTurn - 1) / kTurn, tiles = tiles_m * ((k + kTurn - 1) / kTurn);
@@ -903,12 +901,29 @@ cudaError_t load_first(const OrthoArgs& A, const Scratch& w, int m, int k, bool 
 
 }  // namespace
 
+int ortho_sum_parts(int64_t size) {
+  const int64_t want = (size + kSumCount - 1) / kSumCount;
+  return static_cast<int>(want < kSumParts ? want : kSumParts);
+}
+
+cudaError_t launch_ortho_sum(const OrthoArgs& A, int parts, double* part, cudaStream_t s) {
+  const unsigned grid = static_cast<unsigned>(A.n * parts);
+  const int64_t size = static_cast<int64_t>(A.rows) * A.cols;
+  if (A.bf16)
+    ortho_sum_kernel<uint16_t><<<grid, kSumThreads, 0, s>>>(static_cast<const uint16_t*>(A.g), size, parts, part, A.status);
+  else
+    ortho_sum_kernel<float><<<grid, kSumThreads, 0, s>>>(static_cast<const float*>(A.g), size, parts, part, A.status);
+  return cudaGetLastError();
+}
+
 size_t ortho_scratch_bytes(int64_t n, int64_t rows, int64_t cols) {
-  return ortho_small(rows, cols) ? 0 : Scratch(nullptr, n, rows, cols).bytes;
+  if (ortho_small(rows, cols)) return 0;
+  return ortho_thin(rows, cols) ? ortho_thin_scratch_bytes(n, rows, cols) : Scratch(nullptr, n, rows, cols).bytes;
 }
 
 cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
   if (ortho_small(A.rows, A.cols)) return launch_ortho_small(A, s);
+  if (ortho_thin(A.rows, A.cols)) return launch_ortho_thin(A, s);
   const bool tall = A.rows > A.cols;
   const int m = tall ? A.cols : A.rows, k = tall ? A.rows : A.cols;
   const Scratch w(A.ws, A.n, A.rows, A.cols);

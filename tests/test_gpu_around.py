@@ -382,6 +382,40 @@ def test_orthogonalize(n, rows, cols, kind):
             close(got[i], ref[i], ORTHO_TOL, (dtype, i))
 
 
+@pytest.mark.parametrize("kind", ["gauss", "decay", "floor", "rank1"])
+@pytest.mark.parametrize("n,rows,cols", [(1, 1, 300), (2, 3, 1000), (1, 700, 17), (3, 40, 257), (2, 64, 513), (1, 2100, 64), (2, 33, 4099),
+                                         (1, 9000, 5), (1, 65, 300), (2, 257, 65)])
+def test_orthogonalize_thin(n, rows, cols, kind):
+    """One side short, the other long; few rows average least over the errors of an entry."""
+    from matrix_state_non_gb300 import binding as m
+    g = np.stack([spectrum(rows, cols, kind, 7 * rows + cols + i) for i in range(n)])
+    for dtype in ("bf16", "f32"):
+        x = round_to(g, dtype)
+        got = m.orthogonalize(dev(x, dtype))
+        ref = o.orthogonalize(x)
+        for i in range(n):
+            close(got[i], ref[i], ORTHO_TOL, (dtype, i))
+
+
+@pytest.mark.parametrize("kind", ["gauss", "floor"])
+@pytest.mark.parametrize("steps", [1, 2, 6, 11, 32])
+@pytest.mark.parametrize("rows,cols", [(24, 32), (20, 300), (400, 48), (100, 130)])
+def test_orthogonalize_few_and_many_steps(rows, cols, steps, kind):
+    """The polynomial maps [0.67, 1.21] into itself, where its slope of up to 4
+    makes the places of singular values unpredictable after many steps; but there
+    they stay, and after eleven all of these are there."""
+    import torch
+    from matrix_state_non_gb300 import binding as m
+    x = round_to(spectrum(rows, cols, kind, 5), "f32")
+    got = m.orthogonalize(dev(x), steps=steps)
+    if steps <= 2:
+        close(got, o.orthogonalize(x, steps), ORTHO_TOL, steps)
+        return
+    s = torch.linalg.svdvals(got.double())
+    assert float(s.max()) <= 1.25, s
+    assert steps < 11 or float(s.min()) >= 0.6, s
+
+
 @pytest.mark.parametrize("n,rows,cols", [(27, 512, 520), (8, 1000, 1025), (13, 1030, 777), (76, 513, 512)])
 def test_orthogonalize_stacks(n, rows, cols):
     """Stacks that fill the GPU, whose matrices share tiles of 256 x 256."""
