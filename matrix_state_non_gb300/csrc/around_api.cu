@@ -134,12 +134,12 @@ int m2rnn_residual_norm_backward(const void* h, const float* w, const void* dy, 
   if (!dtype_ok(h_dtype) || !dtype_ok(dy_dtype) || !eps_ok(eps) || !given16(h) || !given16(w) || !given16(dy) ||
       !opt16(dh) || !given16(dx) || !given16(dw))
     return M2RNN_ERR_INVALID_ARG;
+  const size_t need = m2rnn_residual_norm_backward_workspace_size(rows, D);
+  if (!given16(workspace) || workspace_bytes < need) return M2RNN_ERR_WORKSPACE;
   const uint64_t n = static_cast<uint64_t>(rows) * D;
-  const Span outs[] = {{dx, n * 4}, {dw, static_cast<uint64_t>(D) * 4}};
+  const Span outs[] = {{dx, n * 4}, {dw, static_cast<uint64_t>(D) * 4}, {workspace, need}};
   const Span ins[] = {{dh, n * 4}, {h, n * elem(h_dtype)}, {w, static_cast<uint64_t>(D) * 4}, {dy, n * elem(dy_dtype)}};
   if (clobbers(outs, ins, true)) return M2RNN_ERR_INVALID_ARG;
-  if (!given16(workspace) || workspace_bytes < m2rnn_residual_norm_backward_workspace_size(rows, D))
-    return M2RNN_ERR_WORKSPACE;
   NormRowsArgs a{};
   a.h = const_cast<void*>(h); a.w = w; a.dy = dy; a.dh = dh; a.dx = dx; a.dw = dw; a.part = static_cast<float*>(workspace);
   a.rows = rows; a.D = static_cast<int>(D); a.eps = eps;
@@ -179,14 +179,14 @@ int m2rnn_linear_scan_backward(const void* x, int64_t x_stride, const void* a, i
   if (!linear_inputs_ok(r) || !given16(dy) || !opt16(dH_T) || !given16(dx) || !given16(da) || !given16(dalpha) ||
       !opt16(dbeta) || !opt16(dH_0))
     return M2RNN_ERR_INVALID_ARG;
-  const size_t e = elem(dtype);
+  const size_t e = elem(dtype), need = m2rnn_linear_backward_workspace_size(B, T, C);
+  if (!given16(workspace) || workspace_bytes < need) return M2RNN_ERR_WORKSPACE;
   const uint64_t n = static_cast<uint64_t>(B) * T * C, state = static_cast<uint64_t>(B) * C * 4,
                  chan = static_cast<uint64_t>(C) * 4;
-  const Span outs[] = {{dH_0, state}, {dx, n * 4}, {da, n * 4}, {dalpha, chan}, {dbeta, chan}};
+  const Span outs[] = {{dH_0, state}, {dx, n * 4}, {da, n * 4}, {dalpha, chan}, {dbeta, chan}, {workspace, need}};
   const Span ins[] = {{dH_T, state}, {x, span(B * T, x_stride, C, e)}, {a, span(B * T, a_stride, C, e)}, {alpha, chan},
                       {beta, chan}, {H_0, state}, {lengths, static_cast<uint64_t>(B) * 4}, {dy, n * e}};
   if (clobbers(outs, ins, true)) return M2RNN_ERR_INVALID_ARG;
-  if (!given16(workspace) || workspace_bytes < m2rnn_linear_backward_workspace_size(B, T, C)) return M2RNN_ERR_WORKSPACE;
   r.dy = dy; r.dH_T = dH_T; r.dx = dx; r.da = da; r.dalpha = dalpha; r.dbeta = dbeta; r.dH_0 = dH_0; r.ws = workspace;
   return cuda_status(launch_linear_backward(r, static_cast<cudaStream_t>(cuda_stream)));
 }

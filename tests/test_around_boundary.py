@@ -50,7 +50,8 @@ def test_norm_limits():
 @pytest.mark.parametrize("kw", [
     dict(h=None), dict(h=P + 8), dict(w=None), dict(dy=None), dict(dy=3 * P + 2), dict(dh=4 * P + 4), dict(dx=None),
     dict(dx=Q + 4), dict(dw=None), dict(dw=R + 8), dict(rows=0), dict(D=0), dict(ht=E4), dict(dt=E4), dict(eps=nan),
-    dict(dx=P), dict(dx=3 * P), dict(dx=4 * P + 16), dict(dw=Q), dict(dw=2 * P), dict(dh=P, dx=P)])
+    dict(dx=P), dict(dx=3 * P), dict(dx=4 * P + 16), dict(dw=Q), dict(dw=2 * P), dict(dh=P, dx=P), dict(ws=P), dict(ws=3 * P),
+    dict(ws=4 * P), dict(ws=Q), dict(ws=R)])
 def test_norm_backward_refuses(kw):
     assert call(m.m2rnn_residual_norm_backward, NORM_BWD, **kw) == BAD
 
@@ -75,7 +76,8 @@ def test_linear_scan_refuses(kw):
 @pytest.mark.parametrize("kw", ROWS_BAD + [
     dict(T=0), dict(dy=None), dict(dy=4 * P + 8), dict(dx=None), dict(da=Q + 4), dict(dalpha=None), dict(dbeta=R + 4),
     dict(dH_0=S + 4), dict(dH_T=S + 8), dict(dx=P), dict(da=4 * P), dict(da=Q), dict(dbeta=R), dict(dH_0=3 * P),
-    dict(dH_T=S, dH_0=S + 16), dict(H_0=S, dH_0=S)])
+    dict(dH_T=S, dH_0=S + 16), dict(H_0=S, dH_0=S), dict(ws=P),
+    dict(ws=4 * P), dict(ws=Q), dict(ws=R), dict(dbeta=S), dict(dH_0=S)])
 def test_linear_scan_backward_refuses(kw):
     assert call(m.m2rnn_linear_scan_backward, SCAN_BWD, **kw) == BAD
 
