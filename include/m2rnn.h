@@ -466,7 +466,7 @@ int m2rnn_grad_clip(const void* plan, size_t plan_bytes, float max_norm, float* 
  *   for the other types): scale = max(max |y| / 448, 2^-126), and what is
  *   stored is y / scale, to the nearest; y = stored * scale.
  * Outputs must not overlap inputs but for h = residual.  Rows with |h| above
- * 1e18 leave the range of the fp32 sum of squares.
+ * 1e18, or with eps = 0 below 1e-18, leave the range of the fp32 sum of squares.
  */
 int m2rnn_residual_norm(const void* x, int64_t x_stride, const void* residual, const float* w, float eps, void* h, void* y,
                         float* scale, int64_t rows, int64_t D, m2rnn_dtype x_dtype, m2rnn_dtype h_dtype,
@@ -499,7 +499,8 @@ int m2rnn_residual_norm_backward(const void* h, const float* w, const void* dy, 
  *   not grow; H_0 [B,C] fp32 (may be NULL = zero); lengths as above.
  *   out: y [B,T,C] in `dtype`, the fp32 state rounded once; H_T [B,C] fp32
  *   (may be NULL; may be H_0).
- * A value that is not finite reaches no step before its own.
+ * A value that is not finite reaches no step before its own; a of -infinity
+ * and, where alpha > 0, of +infinity are gates: f = 1 and f = 0.
  */
 int m2rnn_linear_scan(const void* x, int64_t x_stride, const void* a, int64_t a_stride, const float* alpha,
                       const float* beta, const float* H_0, const int32_t* lengths, void* y, float* H_T, int64_t B,

@@ -325,6 +325,44 @@ def test_extreme_gates():
         assert abs(host(bwd["dH_0"])[0, c] - ref["dH_0"][0, c]) <= 1e-4 * abs(ref["dH_0"][0, c]) + 1e-37
 
 
+@pytest.mark.parametrize("dtype,C", [("f32", 12), ("bf16", 64), ("bf16", 9)])
+def test_gates_at_the_ends_of_their_type(dtype, C):
+    """a of the type's largest and lowest value and of either infinity: the state is x, or stays (alpha of 0: stays)."""
+    import torch
+    from matrix_state_non_gb300 import binding as m
+    T = 300
+    d = scan_inputs(2, T, C, dtype, 11, True)
+    limit = torch.finfo(torch.float32 if dtype == "f32" else torch.bfloat16)
+    opened, shut = (40, 133, 134, 299), (0, 77, 78, 200)
+    ref_a = np.array(d["a"])
+    for n in (opened, shut):
+        ref_a[:, list(n)] = 1e30 if n is opened else -1e30  # (f is 0 or 1, softplus finite)
+    alpha = np.array(d["alpha"])
+    alpha[1] = 0.0
+    ref_y, ref_H = o.linear_scan(d["x"], ref_a, alpha, d["beta"], d["H_0"])
+    dy = round_to(np.random.default_rng(12).normal(size=(2, T, C)), dtype)
+    ref = o.linear_scan_backward(d["x"], ref_a, alpha, d["beta"], dy, d["H_0"])
+    live = np.arange(C) != 1  # (where alpha is 0, dalpha is as large as softplus)
+    some = torch.from_numpy(live).cuda()
+    for high, low in ((limit.max, limit.min), (float("inf"), float("-inf"))):
+        a = dev(d["a"], dtype)
+        a[:, list(opened)], a[:, list(shut)] = high, low
+        if high == float("inf"):  # (0 times infinity where alpha is 0)
+            a[:, list(opened), 1] = 1.0
+        args = (dev(d["x"], dtype), a, dev(alpha), dev(d["beta"]))
+        got = m.linear_scan(*args, H_0=dev(d["H_0"]))
+        close(got["H_T"], ref_H, TOL, "H_T")
+        near(got["y"], ref_y, (BF16_HALF if dtype == "bf16" else 0) + TOL, "y", TOL * np.abs(ref_y).max())
+        bwd = m.linear_scan_backward(*args, dev(dy, dtype), H_0=dev(d["H_0"]))
+        for k in ("dx", "da"):
+            close(bwd[k], ref[k], TOL, k)
+        for k in ("dalpha", "dbeta"):
+            close(bwd[k][some], ref[k][live], 4 * TOL, k)
+        H = dev(d["H_0"]).clone()
+        y = m.linear_step(H, args[0][:, 40].contiguous(), a[:, 40].contiguous(), args[2], args[3])
+        assert torch.equal(y[:, some], args[0][:, 40][:, some]) and torch.equal(H[:, 1], dev(d["H_0"])[:, 1])
+
+
 def test_scan_values_that_are_not_finite():
     """They reach their own channel from their own step on, and no other sequence."""
     import torch
@@ -484,6 +522,30 @@ def test_orthogonalize_in_place_and_workspace():
         assert m.orthogonalize(g, out=g) is g and torch.equal(g, want)
 
 
+@pytest.mark.parametrize("shape", [(20, 400), (700, 33), (2, 5, 300), (65, 70), (3, 128, 257)])
+def test_orthogonalize_in_place_elsewhere(shape):
+    import torch
+    from matrix_state_non_gb300 import binding as m
+    g = torch.randn(shape, device="cuda").bfloat16()
+    want = m.orthogonalize(g, steps=7)
+    assert m.orthogonalize(g, steps=7, out=g) is g and torch.equal(g, want)
+
+
+def test_orthogonalize_stacks_are_matrices_on_their_own():
+    """Each matrix of a stack gets what it would get in a stack of as many others."""
+    import torch
+    from matrix_state_non_gb300 import binding as m
+    for n, rows, cols in ((5, 40, 64), (4, 30, 900), (3, 200, 136), (30, 300, 300)):
+        g = torch.randn((n, rows, cols), device="cuda")
+        got = m.orthogonalize(g)
+        turned = m.orthogonalize(g.flip(0).contiguous()).flip(0)
+        assert torch.equal(got, turned)
+        zeros = torch.zeros_like(g)
+        zeros[n // 2] = g[n // 2]
+        alone = m.orthogonalize(zeros)
+        assert torch.equal(alone[n // 2], got[n // 2]) and int(alone[:n // 2].count_nonzero()) == 0
+
+
 # ---------------------------------------------------------------------------
 # Calls in graphs and on two streams
 # ---------------------------------------------------------------------------
@@ -498,7 +560,8 @@ def _all_calls(g):
     t = m.linear_step(H, y[:, 0].contiguous(), g["x"][:, 0].contiguous(), g["alpha"], g["beta"])
     d = m.linear_scan_backward(y, g["r"], g["alpha"], g["beta"], g["dy"], H_0=g["H_0"], dH_T=g["H_0"], want_dH0=True)
     small, large = m.orthogonalize(g["small"]), m.orthogonalize(g["large"])
-    return [f["y"].float(), f["scale"], f["h"], y, b["dx"], b["dw"], s["y"], s["H_T"], H, t, d["dx"], d["da"], d["dalpha"],
+    thin = m.orthogonalize(g["thin"])
+    return [thin, f["y"].float(), f["scale"], f["h"], y, b["dx"], b["dw"], s["y"], s["H_T"], H, t, d["dx"], d["da"], d["dalpha"],
             d["dbeta"], d["dH_0"], small, large]
 
 
@@ -508,7 +571,7 @@ def _graph_inputs(seed):
     r = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
     return dict(x=r(2, 700, 264).bfloat16(), r=r(2, 700, 264).bfloat16(), w=r(264), dy=r(2, 700, 264).bfloat16(),
                 dh=r(2, 700, 264), alpha=r(264).exp(), beta=r(264), H_0=r(2, 264), small=r(3, 40, 64),
-                large=r(2, 200, 136).bfloat16())
+                large=r(2, 200, 136).bfloat16(), thin=r(2, 30, 600))
 
 
 def test_calls_in_a_graph():
