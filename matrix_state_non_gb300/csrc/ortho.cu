@@ -20,10 +20,13 @@
 // the result (1.3e-3 at 1024 x 1024 of random entries), the output's rounding to
 // bf16 1.7e-3.  With X's lower part in P X as well (kLow) it is 1.0e-3 to
 // 1.5e-3; matrices of fewer than 512 rows, where errors average least, get that.
+// One part holds the first X where G is bf16, and, from 512 rows on, the last
+// step's, whose noise grows once (a matrix of rank 1 comes out 1e-3 off for it).
 //
-// 24 of 1024 x 4096 bf16, 5 steps: 1.73 ms, of which A 5 x 90 us (1.4 PFLOP/s, 3.2
-// waves of tiles), P 5 x 36 (its epilogue), X' 5 x 185 (HBM, 5.4 TB/s: X read and
-// written in two parts), the norm and the first X 130.
+// 24 of 1024 x 4096 bf16, 5 steps: 1.60 ms, of which A 5 x 90 us (1.4 PFLOP/s, 3.2
+// waves of tiles), P 5 x 36 (its epilogue), X' up to 185 (HBM, 5.4 TB/s, where X is
+// read and written in two parts), the norm and the first X 100.  With two parts in
+// all steps it is 1.71 ms.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -143,18 +146,41 @@ __device__ __forceinline__ void split_8(const float (&v)[8], Eight& hi, Eight& l
   }
 }
 
-// X [m][pitch] in two parts from G [m][k]: eight values of a row to a thread, a
-// block takes kLoadRun of its turns.
+// What the first X is made with.  fp32: the factor, and X is in two parts.  bf16:
+// the power of two below it, which leaves X in one part with all its digits; the
+// rest, in [1, 2), is a factor of the first step (`rest`, for each matrix).
+template <typename E>
+__device__ __forceinline__ float first_scale(float f, float* rest) {
+  if constexpr (sizeof(E) == 2) {
+    int e = 0;
+    const bool usual = f > 0.f && f <= 3.4e38f;
+    const float r = usual ? 2.f * frexpf(f, &e) : 1.f;
+    if (threadIdx.x == 0 && rest != nullptr) *rest = r;
+    return usual ? ldexpf(1.f, e - 1) : f;
+  }
+  return f;
+}
+__device__ __forceinline__ void store_first(float (&v)[8], float f, __half* hi, __half* lo, int64_t at) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = v[e] * f * kScaleX;
+  Eight h, l;
+  split_8(v, h, l);
+  *reinterpret_cast<uint4*>(hi + at) = h.v;
+  if (lo != nullptr) *reinterpret_cast<uint4*>(lo + at) = l.v;
+}
+
+// X [m][pitch] from G [m][k] (lo: null where one part is enough): eight values of a
+// row to a thread, a block takes kLoadRun of its turns.
 constexpr int kLoadRun = 4;
 template <typename E>
 __global__ void __launch_bounds__(256) ortho_load_kernel(const E* g, const double* part, int parts, float eps, __half* hi,
-                                                         __half* lo, int m, int k, int pitch, int blocks) {
+                                                         __half* lo, float* rest, int m, int k, int pitch, int blocks) {
   __shared__ float shared;
   const int64_t mat = blockIdx.x / blocks;
   const int block = static_cast<int>(blockIdx.x - mat * blocks), per_row = pitch / 8;
   const E* p = g + mat * m * k;
   wait_previous();
-  const float f = first_factor(part + mat * parts, parts, eps, &shared);
+  const float f = first_scale<E>(first_factor(part + mat * parts, parts, eps, &shared), block == 0 ? rest + mat : nullptr);
   const int64_t size = static_cast<int64_t>(m) * per_row;
 #pragma unroll
   for (int u = 0; u < kLoadRun; ++u) {
@@ -169,13 +195,7 @@ __global__ void __launch_bounds__(256) ortho_load_kernel(const E* g, const doubl
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = c + e < k ? to_f32(p[r * k + c + e]) : 0.f;
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = v[e] * f * kScaleX;
-    Eight h, l;
-    split_8(v, h, l);
-    const int64_t at = mat * m * pitch + i * 8;
-    *reinterpret_cast<uint4*>(hi + at) = h.v;
-    *reinterpret_cast<uint4*>(lo + at) = l.v;
+    store_first(v, f, hi, lo, mat * m * pitch + i * 8);
   }
   let_next();
 }
@@ -184,7 +204,8 @@ __global__ void __launch_bounds__(256) ortho_load_kernel(const E* g, const doubl
 constexpr int kTurn = 64;
 template <typename E>
 __global__ void __launch_bounds__(256) ortho_load_tall_kernel(const E* g, const double* part, int parts, float eps, __half* hi,
-                                                              __half* lo, int m, int k, int pitch, int tiles_m, int tiles) {
+                                                              __half* lo, float* rest, int m, int k, int pitch, int tiles_m,
+                                                              int tiles) {
   __shared__ float t[kTurn][kTurn + 1];
   __shared__ float shared;
   const int64_t mat = blockIdx.x / tiles;
@@ -197,19 +218,15 @@ __global__ void __launch_bounds__(256) ortho_load_tall_kernel(const E* g, const 
     t[r][c] = r0 + r < m && c0 + c < k ? to_f32(p[static_cast<int64_t>(c0 + c) * m + r0 + r]) : 0.f;
   }
   wait_previous();
-  const float f = first_factor(part + mat * parts, parts, eps, &shared);
+  const float f = first_scale<E>(first_factor(part + mat * parts, parts, eps, &shared), tile == 0 ? rest + mat : nullptr);
 #pragma unroll
   for (int i = threadIdx.x; i < kTurn * kTurn / 8; i += 256) {
     const int r = i / (kTurn / 8), c = i % (kTurn / 8) * 8;
     if (r0 + r >= m || c0 + c >= pitch) continue;
     float v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = t[r][c + e] * f * kScaleX;
-    Eight h, l;
-    split_8(v, h, l);
-    const int64_t at = (mat * m + r0 + r) * pitch + c0 + c;
-    *reinterpret_cast<uint4*>(hi + at) = h.v;
-    *reinterpret_cast<uint4*>(lo + at) = l.v;
+    for (int e = 0; e < 8; ++e) v[e] = t[r][c + e];
+    store_first(v, f, hi, lo, (mat * m + r0 + r) * pitch + c0 + c);
   }
   let_next();
 }
@@ -221,6 +238,7 @@ enum { kGram = 0, kPoly = 1, kUpdate = 2 };
 
 struct ProductArgs {
   uint16_t* last;  // kUpdate of the last step: the result in bf16, [m][k] or (tall) [k][m]
+  const float* rest;  // [n], or null: X is that times what is stored
   StatusBlock* status;
   int m, k;   // X is m x k
   int inner;  // of the product
@@ -228,6 +246,7 @@ struct ProductArgs {
   int items;  // of all matrices
   bool tall;
   bool direct;  // last: rows that TMA cannot store (not on 16 bytes)
+  bool in_low, out_low;  // kUpdate: X and X' have a lower part
 };
 
 // By TMA: the operands; `in`: kPoly: A; kUpdate: X, its lower part in_low; `out`: A, P or X' (out_low), or the result.
@@ -347,23 +366,24 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t fr
                : "memory");
 }
 
-// A row's 32 columns of the result from the accumulators and what the turn's place holds: v.
+// A row's 32 columns of the result from the accumulators and what the turn's place holds: v.  f: what the stored X lacks.
 template <int kMode>
-__device__ __forceinline__ void combine(float (&v)[32], const uint32_t (&acc)[32], uint32_t line, uint32_t swz) {
+__device__ __forceinline__ void combine(float (&v)[32], const uint32_t (&acc)[32], uint32_t line, uint32_t swz, float f, bool in_low) {
+  const float by = kMode == kGram ? 0x1p-14f * f * f : 0x1p-13f * f, a = kA * f;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     Eight h, l;
     if constexpr (kMode != kGram) h.v = ld_shared_v4(line + ((q ^ swz) << 4));
-    if constexpr (kMode == kUpdate) l.v = ld_shared_v4(line + kBlockBytes + ((q ^ swz) << 4));
+    if (kMode == kUpdate) l.v = in_low ? ld_shared_v4(line + kBlockBytes + ((q ^ swz) << 4)) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float p = __uint_as_float(acc[8 * q + e]);
       float x = 0.f;
       if constexpr (kMode != kGram) x = __half2float(e % 2 == 0 ? h.h[e / 2].x : h.h[e / 2].y);
       if constexpr (kMode == kUpdate) x += __half2float(e % 2 == 0 ? l.h[e / 2].x : l.h[e / 2].y);
-      if constexpr (kMode == kGram) v[8 * q + e] = p * 0x1p-14f;
+      if constexpr (kMode == kGram) v[8 * q + e] = p * by;
       if constexpr (kMode == kPoly) v[8 * q + e] = fmaf(kC * 0x1p-15f, p, kB * 0.5f * x);
-      if constexpr (kMode == kUpdate) v[8 * q + e] = fmaf(p, 0x1p-13f, kA * x);
+      if constexpr (kMode == kUpdate) v[8 * q + e] = fmaf(p, by, a * x);
     }
   }
 }
@@ -402,7 +422,7 @@ __device__ __forceinline__ void emit(const Operands& O, const ProductArgs& A, co
       split_8(w, h, l);
     }
     st_shared_v4(line + ((q ^ swz) << 4), {h.v.x, h.v.y, h.v.z, h.v.w});
-    if (kMode == kUpdate && !last) st_shared_v4(line + kBlockBytes + ((q ^ swz) << 4), {l.v.x, l.v.y, l.v.z, l.v.w});
+    if (kMode == kUpdate && A.out_low) st_shared_v4(line + kBlockBytes + ((q ^ swz) << 4), {l.v.x, l.v.y, l.v.z, l.v.w});
     if (mirror) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {  // row 8 q + e of the other side's block, column `lane`
@@ -417,7 +437,7 @@ __device__ __forceinline__ void emit(const Operands& O, const ProductArgs& A, co
   __syncwarp();
   if (lane == 0) {
     if (!(last && A.tall)) tma_store_3d(&O.out, block, c0, r0, mat);
-    if (kMode == kUpdate && !last) tma_store_3d(&O.out_low, block + kBlockBytes, c0, r0, mat);
+    if (kMode == kUpdate && A.out_low) tma_store_3d(&O.out_low, block + kBlockBytes, c0, r0, mat);
     if (mirror) tma_store_3d(&O.out, block + kBlockBytes, r0, c0, mat);
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
@@ -558,9 +578,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       if (kMode == kGram || coming >= A.items) return;
       const int s = reads++ % S::kTurns;
       const int r0 = ahead.i * S::kTileRows + row, c0 = ahead.j * kN + column + 32 * next;
-      mbar_arrive_expect_tx(there(me, s), kMode == kUpdate ? S::kTurn : kBlockBytes);
+      const bool low = kMode == kUpdate && A.in_low;
+      mbar_arrive_expect_tx(there(me, s), low ? S::kTurn : kBlockBytes);
       tma_load_3d<false>(ring + s * S::kTurn, &O.in, there(me, s), c0, r0, ahead.mat);
-      if (kMode == kUpdate) tma_load_3d<false>(ring + s * S::kTurn + kBlockBytes, &O.in_low, there(me, s), c0, r0, ahead.mat);
+      if (low) tma_load_3d<false>(ring + s * S::kTurn + kBlockBytes, &O.in_low, there(me, s), c0, r0, ahead.mat);
       if (++next == kPerTile) {
         next = 0;
         coming += step;
@@ -576,6 +597,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     for (int id = first; ok && id < A.items; id += step, ++n) {
       const Item t = item_at<kMode, kN, S::kTileRows>(A, id);
       const int slot = n & 1, r0 = t.i * S::kTileRows + row;
+      const float f = A.rest != nullptr ? A.rest[t.mat] : 1.f;
       ok = warp_wait(done(slot), (n >> 1) & 1, abort_flag, A.status, kWhereOrthoDone);
       tc_fence_after_sync();
       const uint32_t tm = tmem + slot * kN + half * (kN / 2) + (static_cast<uint32_t>(32 * quarter) << 16);
@@ -594,7 +616,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           tmem_ld_32x32b<32>(tm + 32 * x, acc);
           tmem_ld_wait();
           tmem_ld_fence_regs(acc);
-          combine<kMode>(v, acc, line, swz);
+          combine<kMode>(v, acc, line, swz, f, A.in_low);
         }
         __syncwarp();
         if (lane == 0) {  // the turn before has left shared memory: its place is free
@@ -756,16 +778,18 @@ __global__ void __launch_bounds__(kProductThreads, 1) ortho_narrow_kernel(const 
     if (kMode != kGram) {
       if (lane == 0) {
         asm volatile("fence.proxy.async;" ::: "memory");
-        mbar_arrive_expect_tx(there(me), blocks * (kMode == kUpdate ? S::kTurn : kBlockBytes));
+        const bool low = kMode == kUpdate && A.in_low;
+        mbar_arrive_expect_tx(there(me), blocks * (low ? S::kTurn : kBlockBytes));
         for (int x = 0; x < blocks; ++x) {
           const uint32_t to = ring + x * S::kTurn;
           tma_load_3d<false>(to, &O.in, there(me), t.j * kN + column(x), r0, mat);
-          if (kMode == kUpdate) tma_load_3d<false>(to + kBlockBytes, &O.in_low, there(me), t.j * kN + column(x), r0, mat);
+          if (low) tma_load_3d<false>(to + kBlockBytes, &O.in_low, there(me), t.j * kN + column(x), r0, mat);
         }
       }
       warp_wait(there(me), 0, abort_flag, A.status, kWhereOrthoIn);
     }
     tc_fence_after_sync();
+    const float f = A.rest != nullptr ? A.rest[mat] : 1.f;
     for (int x = 0; x < blocks; ++x) {
       const int c = column(x), c0 = t.j * kN + c;
       const uint32_t block = ring + x * S::kTurn;
@@ -775,7 +799,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) ortho_narrow_kernel(const 
       tmem_ld_wait();
       tmem_ld_fence_regs(acc);
       float v[32];
-      combine<kMode>(v, acc, block + lane * 64, (lane >> 1) & 3);
+      combine<kMode>(v, acc, block + lane * 64, (lane >> 1) & 3, f, A.in_low);
       emit<kMode>(O, A, v, block, r0, c0, mat, lane);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -837,13 +861,14 @@ cudaError_t narrow_product(const Operands& o, const ProductArgs& a, cudaStream_t
 }
 
 // One product: by pairs of SMs (tiles of 256 x 256); where there are few tiles, by a block to each of the narrowest
-// that do not exceed the SMs; else by persistent blocks.  X's lower part enters P X where m is below 512.
+// that do not exceed the SMs; else by persistent blocks.  X's lower part, if it has one, enters P X where m is below 512.
+constexpr int kOnePart = 512;
 template <int kMode>
 cudaError_t run_product(const Operands& o, const ProductArgs& a, int64_t n, bool pair, cudaStream_t s) {
   if (pair) return product<kMode, 256, false, true>(o, a, n, s);
   if constexpr (kMode == kUpdate) {
     const ProductArgs t = small_tiles<kMode, 64>(a, n);
-    if (a.m < 512) return t.items <= 152 ? narrow_product<kMode, 64, true>(o, t, s) : product<kMode, 128, true, false>(o, a, n, s);
+    if (a.m < kOnePart && a.in_low) return t.items <= 152 ? narrow_product<kMode, 64, true>(o, t, s) : product<kMode, 128, true, false>(o, a, n, s);
     if (t.items <= 152) return narrow_product<kMode, 64, false>(o, t, s);
   } else {
     ProductArgs t = small_tiles<kMode, 32>(a, n);
@@ -857,6 +882,7 @@ cudaError_t run_product(const Operands& o, const ProductArgs& a, int64_t n, bool
 
 struct Scratch {
   double* part;
+  float* rest;
   __half *x[2], *low[2], *gram, *poly;
   size_t bytes;
   int pitch, square;  // of X, of A and P
@@ -874,6 +900,7 @@ struct Scratch {
       return p;
     };
     part = reinterpret_cast<double*>(take(n * parts * 8));
+    rest = reinterpret_cast<float*>(take(n * 4));
     for (int i = 0; i < 2; ++i) {
       x[i] = reinterpret_cast<__half*>(take(n * m * pitch * 2));
       low[i] = reinterpret_cast<__half*>(take(n * m * pitch * 2));
@@ -886,17 +913,18 @@ struct Scratch {
 template <typename E>
 cudaError_t load_first(const OrthoArgs& A, const Scratch& w, int m, int k, bool tall, cudaStream_t s) {
   const E* g = static_cast<const E*>(A.g);
+  __half* low = sizeof(E) == 2 ? nullptr : w.low[0];
   const cudaError_t e = launch_ortho_sum(A, w.parts, w.part, s);
   if (e != cudaSuccess) return e;
   if (tall) {
     const int tiles_m = (m + kTurn - 1) / kTurn, tiles = tiles_m * ((k + kTurn - 1) / kTurn);
     return launch_next(ortho_load_tall_kernel<E>, static_cast<unsigned>(A.n * tiles), 256, 0, s, g, w.part, w.parts, A.eps,
-                       w.x[0], w.low[0], m, k, w.pitch, tiles_m, tiles);
+                       w.x[0], low, w.rest, m, k, w.pitch, tiles_m, tiles);
   }
   const int64_t eights = static_cast<int64_t>(m) * (w.pitch / 8);
   const int blocks = static_cast<int>((eights + 256 * kLoadRun - 1) / (256 * kLoadRun));
   return launch_next(ortho_load_kernel<E>, static_cast<unsigned>(A.n * blocks), 256, 0, s, g, w.part, w.parts, A.eps, w.x[0],
-                     w.low[0], m, k, w.pitch, blocks);
+                     low, w.rest, m, k, w.pitch, blocks);
 }
 
 }  // namespace
@@ -966,6 +994,11 @@ cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
     const int at = i & 1;
     const bool last = i == A.steps - 1;
     a.inner = k;
+    a.rest = i == 0 && A.bf16 ? w.rest : nullptr;
+    // X before the last step is in one part where m is not below kOnePart: what that leaves grows 3.4-fold once.
+    auto two_parts = [&](int step) { return step == 0 ? !A.bf16 : step < A.steps && (step < A.steps - 1 || m < kOnePart); };
+    a.in_low = two_parts(i);
+    a.out_low = two_parts(i + 1);
     e = run_product<kGram>(to_gram[at], a, A.n, pair, s);
     if (e != cudaSuccess) break;
     a.inner = m;

@@ -497,6 +497,48 @@ def test_orthogonalize_sizes_of_values(rows, cols):
     assert torch.equal(got[0], torch.zeros_like(got[0])) and torch.equal(got[1], m.orthogonalize(z[1]))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(40, 60), (30, 500), (140, 150), (150, 140), (520, 516)])
+def test_orthogonalize_sizes_at_the_ends(rows, cols, dtype):
+    """Powers of two leave the result as it is, up to norms whose inverse is no normal fp32 number; so does eps = 0."""
+    import torch
+    from matrix_state_non_gb300 import binding as m
+    x = dev(spectrum(rows, cols, "gauss", 6), dtype)
+    want = m.orthogonalize(x, eps=0.0)
+    close(want, o.orthogonalize(host(x).astype(np.float64), eps=0.0), ORTHO_TOL, "1")
+    up = 126 - int(np.floor(np.log2(float(x.double().norm()))))
+    for k in (-90, 60, up, up + 1):
+        y = x * 2.0 ** (k // 2) * 2.0 ** (k - k // 2)
+        assert bool(y.isfinite().all())
+        # factors of fp32 with and without all their bits: an operand's last place may differ
+        close(m.orthogonalize(y, eps=0.0), host(want).astype(np.float64), ORTHO_TOL, k)
+    z = torch.zeros_like(x)
+    assert torch.equal(m.orthogonalize(z), z.bfloat16())
+
+
+@pytest.mark.parametrize("kind", ["gauss", "decay", "floor", "rank1"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,rows,cols", [(1, 520, 700), (2, 1100, 600), (1, 800, 8200), (30, 515, 512), (20, 800, 800)])
+def test_orthogonalize_long_sides(n, rows, cols, dtype, kind):
+    """Matrices whose last step takes X in one part: 3.4445 2^-12 of it, 1.2 / 0.67 at most of the result's size: 1.5e-3."""
+    import torch
+    from matrix_state_non_gb300 import binding as m
+    x = torch.stack([dev(spectrum(rows, cols, kind, 3 * rows + i), dtype) for i in range(min(n, 2))])
+    x = x.repeat((n + 1) // 2, 1, 1)[:n].contiguous()
+    got = m.orthogonalize(x)
+    a, b, c = o.COEFFICIENTS
+    for i in {0, n - 1}:
+        v = x[i].double()
+        v = v if rows <= cols else v.mT
+        v = v / (v.norm() + 1e-7)
+        for _ in range(5):
+            gram = v @ v.mT
+            v = a * v + (b * gram + c * gram @ gram) @ v
+        v = v if rows <= cols else v.mT
+        off = float((got[i].double() - v).norm() / v.norm())
+        assert off <= ORTHO_TOL, (i, off)
+
+
 @pytest.mark.parametrize("rows,cols", [(64, 64), (150, 140)])
 def test_orthogonalize_not_finite(rows, cols):
     """A NaN spoils its own matrix and no other of the stack."""
