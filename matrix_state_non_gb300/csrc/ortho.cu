@@ -22,12 +22,15 @@
 // 1.5e-3; matrices of fewer than 512 rows, where errors average least, get that.
 // One part holds the first X where G is bf16, and, from 512 rows on, the last
 // step's, whose noise grows once (a matrix of rank 1 comes out 1e-3 off for it).
+// The steps between have a byte for the lower part there, 14 to 15 bits in all
+// (another 9e-4 for rank 1).
 //
-// 24 of 1024 x 4096 bf16, 5 steps: 1.60 ms, of which A 5 x 90 us (1.4 PFLOP/s, 3.2
-// waves of tiles), P 5 x 36 (its epilogue), X' up to 185 (HBM, 5.4 TB/s, where X is
-// read and written in two parts), the norm and the first X 100.  With two parts in
-// all steps it is 1.71 ms.
+// 24 of 1024 x 4096 bf16, 5 steps: 1.56 ms, of which A 5 x 88 us (1.5 PFLOP/s, 3.2
+// waves of tiles), P 5 x 34, X' 145 to 170 (12 TB/s between L2 and the SMs; 3.6 of
+// HBM), the norm and the first X 100.  With two fp16 parts in all steps X' was 185,
+// bound by HBM, and the whole 1.71 ms; with two but in the first and last 1.61.
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -235,6 +238,9 @@ __global__ void __launch_bounds__(256) ortho_load_tall_kernel(const E* g, const 
 // The products
 // ---------------------------------------------------------------------------
 enum { kGram = 0, kPoly = 1, kUpdate = 2 };
+// Lower parts: fp16; or the upper byte of an fp16 (2 bits of mantissa), times 2^12.
+enum { kNone = 0, kBytes = 1, kHalf = 2 };
+constexpr float kByteScale = 0x1p12f;
 
 struct ProductArgs {
   uint16_t* last;  // kUpdate of the last step: the result in bf16, [m][k] or (tall) [k][m]
@@ -246,7 +252,7 @@ struct ProductArgs {
   int items;  // of all matrices
   bool tall;
   bool direct;  // last: rows that TMA cannot store (not on 16 bytes)
-  bool in_low, out_low;  // kUpdate: X and X' have a lower part
+  int in_low, out_low;  // kUpdate: the lower parts of X and X', kNone, kBytes or kHalf
 };
 
 // By TMA: the operands; `in`: kPoly: A; kUpdate: X, its lower part in_low; `out`: A, P or X' (out_low), or the result.
@@ -257,6 +263,7 @@ struct Operands {
 constexpr int kRows = 128, kDepth = 64;  // a tile's rows, the inner dimension of a stage
 constexpr int kBoxRows = 32;            // of the right operand's loads, K-major
 constexpr int kBlockBytes = 32 * 32 * 2;   // what an epilogue warp stores at once
+__host__ __device__ constexpr int low_bytes(int low) { return low == kHalf ? kBlockBytes : low == kBytes ? kBlockBytes / 2 : 0; }
 constexpr int kEpilogueWarps = 8, kFirstEpilogue = 2, kProductThreads = 32 * (kFirstEpilogue + kEpilogueWarps);
 
 // kPair: two blocks of a cluster on two SMs share a tile of 256 rows, each with
@@ -366,21 +373,38 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t fr
                : "memory");
 }
 
+// A thread's 16 of 32 bytes in a block of lower parts that are bytes (rows of 32 bytes, swizzled).
+__device__ __forceinline__ uint32_t byte_line(uint32_t block, int lane, int half) {
+  return block + kBlockBytes + lane * 32 + ((half ^ (lane >> 2 & 1)) << 4);
+}
+
 // A row's 32 columns of the result from the accumulators and what the turn's place holds: v.  f: what the stored X lacks.
 template <int kMode>
-__device__ __forceinline__ void combine(float (&v)[32], const uint32_t (&acc)[32], uint32_t line, uint32_t swz, float f, bool in_low) {
+__device__ __forceinline__ void combine(float (&v)[32], const uint32_t (&acc)[32], uint32_t block, int lane, float f, int low) {
+  const uint32_t line = block + lane * 64, swz = (lane >> 1) & 3;
   const float by = kMode == kGram ? 0x1p-14f * f * f : 0x1p-13f * f, a = kA * f;
+  const float low_by = low == kBytes ? 1.f / kByteScale : 1.f;
+  uint4 bytes = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     Eight h, l;
     if constexpr (kMode != kGram) h.v = ld_shared_v4(line + ((q ^ swz) << 4));
-    if (kMode == kUpdate) l.v = in_low ? ld_shared_v4(line + kBlockBytes + ((q ^ swz) << 4)) : make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (kMode == kUpdate) {
+      l.v = make_uint4(0u, 0u, 0u, 0u);
+      if (low == kHalf) l.v = ld_shared_v4(line + kBlockBytes + ((q ^ swz) << 4));
+      if (low == kBytes) {
+        if (q % 2 == 0) bytes = ld_shared_v4(byte_line(block, lane, q / 2));
+        const uint32_t b0 = q % 2 == 0 ? bytes.x : bytes.z, b1 = q % 2 == 0 ? bytes.y : bytes.w;
+        l.v = make_uint4(__byte_perm(b0, 0u, 0x1404), __byte_perm(b0, 0u, 0x3424), __byte_perm(b1, 0u, 0x1404),
+                         __byte_perm(b1, 0u, 0x3424));
+      }
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float p = __uint_as_float(acc[8 * q + e]);
       float x = 0.f;
       if constexpr (kMode != kGram) x = __half2float(e % 2 == 0 ? h.h[e / 2].x : h.h[e / 2].y);
-      if constexpr (kMode == kUpdate) x += __half2float(e % 2 == 0 ? l.h[e / 2].x : l.h[e / 2].y);
+      if constexpr (kMode == kUpdate) x = fmaf(__half2float(e % 2 == 0 ? l.h[e / 2].x : l.h[e / 2].y), low_by, x);
       if constexpr (kMode == kGram) v[8 * q + e] = p * by;
       if constexpr (kMode == kPoly) v[8 * q + e] = fmaf(kC * 0x1p-15f, p, kB * 0.5f * x);
       if constexpr (kMode == kUpdate) v[8 * q + e] = fmaf(p, by, a * x);
@@ -407,22 +431,41 @@ __device__ __forceinline__ void emit(const Operands& O, const ProductArgs& A, co
     }
     return;
   }
+  uint32_t bytes[4];
   __syncwarp();
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     float w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) w[e] = v[8 * q + e];
-    Eight h, l;
+    Eight h;
     if (last) {
       constexpr float f = 1.f / kScaleX;
       h.v = make_uint4(pack_bf16x2(w[0] * f, w[1] * f), pack_bf16x2(w[2] * f, w[3] * f), pack_bf16x2(w[4] * f, w[5] * f),
                        pack_bf16x2(w[6] * f, w[7] * f));
     } else {
-      split_8(w, h, l);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h.h[e] = __floats2half2_rn(w[2 * e], w[2 * e + 1]);
     }
     st_shared_v4(line + ((q ^ swz) << 4), {h.v.x, h.v.y, h.v.z, h.v.w});
-    if (kMode == kUpdate && A.out_low) st_shared_v4(line + kBlockBytes + ((q ^ swz) << 4), {l.v.x, l.v.y, l.v.z, l.v.w});
+    if (kMode == kUpdate && A.out_low != kNone) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] -= __half2float(e % 2 == 0 ? h.h[e / 2].x : h.h[e / 2].y);
+      if (A.out_low == kHalf) {
+        Eight l;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) l.h[e] = __floats2half2_rn(w[2 * e], w[2 * e + 1]);
+        st_shared_v4(line + kBlockBytes + ((q ^ swz) << 4), {l.v.x, l.v.y, l.v.z, l.v.w});
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(w[e] * kByteScale, w[e + 1] * kByteScale), __NV_SATFINITE, __NV_E5M2);
+          const uint32_t up = __nv_cvt_float2_to_fp8x2(make_float2(w[e + 2] * kByteScale, w[e + 3] * kByteScale), __NV_SATFINITE, __NV_E5M2);
+          bytes[2 * (q & 1) + e / 4] = lo | up << 16;
+        }
+        if (q % 2 == 1) st_shared_v4(byte_line(block, lane, q / 2), {bytes[0], bytes[1], bytes[2], bytes[3]});
+      }
+    }
     if (mirror) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {  // row 8 q + e of the other side's block, column `lane`
@@ -437,7 +480,7 @@ __device__ __forceinline__ void emit(const Operands& O, const ProductArgs& A, co
   __syncwarp();
   if (lane == 0) {
     if (!(last && A.tall)) tma_store_3d(&O.out, block, c0, r0, mat);
-    if (kMode == kUpdate && A.out_low) tma_store_3d(&O.out_low, block + kBlockBytes, c0, r0, mat);
+    if (kMode == kUpdate && A.out_low != kNone) tma_store_3d(&O.out_low, block + kBlockBytes, c0, r0, mat);
     if (mirror) tma_store_3d(&O.out, block + kBlockBytes, r0, c0, mat);
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
@@ -569,7 +612,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const int me = warp - kFirstEpilogue, quarter = warp & 3, half = me >> 2;
     const int cols = kMode == kUpdate ? A.k : A.m;
     constexpr int kPerTile = kN / 64;  // turns of a tile
-    const uint32_t ring = base + S::kOffRing + me * S::kTurns * S::kTurn, swz = (lane >> 1) & 3;
+    const uint32_t ring = base + S::kOffRing + me * S::kTurns * S::kTurn;
     const int row = rank * kRows + quarter * 32, column = half * (kN / 2);  // in a tile
     // One lane reads ahead: the next block to read is number `next` of tile `coming`.
     int coming = first, next = 0, reads = 0;
@@ -578,10 +621,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       if (kMode == kGram || coming >= A.items) return;
       const int s = reads++ % S::kTurns;
       const int r0 = ahead.i * S::kTileRows + row, c0 = ahead.j * kN + column + 32 * next;
-      const bool low = kMode == kUpdate && A.in_low;
-      mbar_arrive_expect_tx(there(me, s), low ? S::kTurn : kBlockBytes);
+      const int low = kMode == kUpdate ? A.in_low : kNone;
+      mbar_arrive_expect_tx(there(me, s), kBlockBytes + low_bytes(low));
       tma_load_3d<false>(ring + s * S::kTurn, &O.in, there(me, s), c0, r0, ahead.mat);
-      if (low) tma_load_3d<false>(ring + s * S::kTurn + kBlockBytes, &O.in_low, there(me, s), c0, r0, ahead.mat);
+      if (low != kNone) tma_load_3d<false>(ring + s * S::kTurn + kBlockBytes, &O.in_low, there(me, s), c0, r0, ahead.mat);
       if (++next == kPerTile) {
         next = 0;
         coming += step;
@@ -605,7 +648,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       for (int x = 0; ok && x < kPerTile; ++x, ++u) {
         const int c0 = t.j * kN + column + 32 * x, s = u % S::kTurns;
         const bool used = r0 < A.m && c0 < cols && (kMode == kUpdate || c0 >= r0);
-        const uint32_t block = ring + s * S::kTurn, line = block + lane * 64;
+        const uint32_t block = ring + s * S::kTurn;
         float v[32];
         if (kMode != kGram) {
           ok = warp_wait(there(me, s), (u / S::kTurns) & 1, abort_flag, A.status, kWhereOrthoIn);
@@ -616,7 +659,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
           tmem_ld_32x32b<32>(tm + 32 * x, acc);
           tmem_ld_wait();
           tmem_ld_fence_regs(acc);
-          combine<kMode>(v, acc, line, swz, f, A.in_low);
+          combine<kMode>(v, acc, block, lane, f, A.in_low);
         }
         __syncwarp();
         if (lane == 0) {  // the turn before has left shared memory: its place is free
@@ -778,12 +821,12 @@ __global__ void __launch_bounds__(kProductThreads, 1) ortho_narrow_kernel(const 
     if (kMode != kGram) {
       if (lane == 0) {
         asm volatile("fence.proxy.async;" ::: "memory");
-        const bool low = kMode == kUpdate && A.in_low;
-        mbar_arrive_expect_tx(there(me), blocks * (low ? S::kTurn : kBlockBytes));
+        const int low = kMode == kUpdate ? A.in_low : kNone;
+        mbar_arrive_expect_tx(there(me), blocks * (kBlockBytes + low_bytes(low)));
         for (int x = 0; x < blocks; ++x) {
           const uint32_t to = ring + x * S::kTurn;
           tma_load_3d<false>(to, &O.in, there(me), t.j * kN + column(x), r0, mat);
-          if (low) tma_load_3d<false>(to + kBlockBytes, &O.in_low, there(me), t.j * kN + column(x), r0, mat);
+          if (low != kNone) tma_load_3d<false>(to + kBlockBytes, &O.in_low, there(me), t.j * kN + column(x), r0, mat);
         }
       }
       warp_wait(there(me), 0, abort_flag, A.status, kWhereOrthoIn);
@@ -799,7 +842,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) ortho_narrow_kernel(const 
       tmem_ld_wait();
       tmem_ld_fence_regs(acc);
       float v[32];
-      combine<kMode>(v, acc, block + lane * 64, (lane >> 1) & 3, f, A.in_low);
+      combine<kMode>(v, acc, block, lane, f, A.in_low);
       emit<kMode>(O, A, v, block, r0, c0, mat, lane);
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -814,6 +857,13 @@ __global__ void __launch_bounds__(kProductThreads, 1) ortho_narrow_kernel(const 
 // A stack of matrices [n][rows][pitch] as TMA sees it: boxes of `depth` rows of 64 columns for the products' operands
 // (128-byte swizzle), of 32 x 32 for the epilogue (64-byte swizzle).
 constexpr int kEpilogueBox = 0;
+// Lower parts that are bytes: boxes of 32 x 32 (32-byte swizzle).
+bool map_bytes(CUtensorMap* map, const void* p, int64_t n, int rows, int cols, int pitch) {
+  const uint64_t dims[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), static_cast<uint64_t>(n)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(pitch), static_cast<uint64_t>(pitch) * rows};
+  const uint32_t box[3] = {32, 32, 1};
+  return make_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, p, 3, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_32B);
+}
 bool map_matrix(CUtensorMap* map, const void* p, int64_t n, int rows, int cols, int pitch, int depth,
                 CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_FLOAT16) {
   const uint64_t dims[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows), static_cast<uint64_t>(n)};
@@ -868,7 +918,7 @@ cudaError_t run_product(const Operands& o, const ProductArgs& a, int64_t n, bool
   if (pair) return product<kMode, 256, false, true>(o, a, n, s);
   if constexpr (kMode == kUpdate) {
     const ProductArgs t = small_tiles<kMode, 64>(a, n);
-    if (a.m < kOnePart && a.in_low) return t.items <= 152 ? narrow_product<kMode, 64, true>(o, t, s) : product<kMode, 128, true, false>(o, a, n, s);
+    if (a.m < kOnePart && a.in_low == kHalf) return t.items <= 152 ? narrow_product<kMode, 64, true>(o, t, s) : product<kMode, 128, true, false>(o, a, n, s);
     if (t.items <= 152) return narrow_product<kMode, 64, false>(o, t, s);
   } else {
     ProductArgs t = small_tiles<kMode, 32>(a, n);
@@ -965,7 +1015,8 @@ cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
   ProductArgs a{};
   a.status = A.status; a.m = m; a.k = k; a.tall = tall;
   a.direct = A.cols % 8 != 0;
-  Operands to_gram[2], to_poly, to_x[2], to_last;
+  Operands to_gram[2], to_poly, to_x[2];
+  CUtensorMap halves[2], bytes[2], result;  // X's lower part, the result, for the epilogue
   bool made = map_matrix(&to_poly.left, w.gram, A.n, m, m, w.square, kRows) &&
               map_matrix(&to_poly.in, w.gram, A.n, m, m, w.square, kEpilogueBox) &&
               map_matrix(&to_poly.out, w.poly, A.n, m, m, w.square, kEpilogueBox);
@@ -977,35 +1028,40 @@ cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
     made = made && map_matrix(&g.left, w.x[i], A.n, m, k, w.pitch, kRows) && map_matrix(&x.left, w.poly, A.n, m, m, w.square, kRows) &&
            map_matrix(&x.right, w.x[i], A.n, m, k, w.pitch, kDepth) && map_matrix(&x.right_low, w.low[i], A.n, m, k, w.pitch, kDepth) &&
            map_matrix(&x.in, w.x[i], A.n, m, k, w.pitch, kEpilogueBox) &&
-           map_matrix(&x.in_low, w.low[i], A.n, m, k, w.pitch, kEpilogueBox);
+           map_matrix(&halves[i], w.low[i], A.n, m, k, w.pitch, kEpilogueBox) &&
+           map_bytes(&bytes[i], w.low[i], A.n, m, k, static_cast<int>(round_up(k, 16)));
     made = made && map_matrix(&g.right, w.x[i], A.n, m, k, w.pitch, kBoxRows);
     g.right_low = g.right;
     g.out = g.out_low = g.in = g.in_low = to_poly.in;
   }
-  for (int i = 0; i < 2; ++i) {
-    to_x[i].out = to_x[i ^ 1].in;
-    to_x[i].out_low = to_x[i ^ 1].in_low;
-  }
-  to_last = to_x[(A.steps - 1) & 1];
+  for (int i = 0; i < 2; ++i) to_x[i].out = to_x[i ^ 1].in;
   if (!a.direct)
-    made = made && map_matrix(&to_last.out, A.out, A.n, A.rows, A.cols, A.cols, kEpilogueBox, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
+    made = made && map_matrix(&result, A.out, A.n, A.rows, A.cols, A.cols, kEpilogueBox, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
   if (!made) return cudaErrorInvalidValue;
+  // The lower part of a step's X.  From kOnePart rows on, where it is no operand, a byte serves from the second step on
+  // (the first X's noise would grow 480-fold), and nothing in the last step.
+  auto low_part = [&](int step) {
+    if (step == 0) return A.bf16 ? kNone : kHalf;
+    return m < kOnePart ? step < A.steps ? kHalf : kNone : step < A.steps - 1 ? kBytes : kNone;
+  };
   for (int i = 0; i < A.steps && e == cudaSuccess; ++i) {
     const int at = i & 1;
     const bool last = i == A.steps - 1;
     a.inner = k;
     a.rest = i == 0 && A.bf16 ? w.rest : nullptr;
-    // X before the last step is in one part where m is not below kOnePart: what that leaves grows 3.4-fold once.
-    auto two_parts = [&](int step) { return step == 0 ? !A.bf16 : step < A.steps && (step < A.steps - 1 || m < kOnePart); };
-    a.in_low = two_parts(i);
-    a.out_low = two_parts(i + 1);
+    a.in_low = low_part(i);
+    a.out_low = low_part(i + 1);
     e = run_product<kGram>(to_gram[at], a, A.n, pair, s);
     if (e != cudaSuccess) break;
     a.inner = m;
     e = run_product<kPoly>(to_poly, a, A.n, pair, s);
     if (e != cudaSuccess) break;
     a.last = last ? A.out : nullptr;
-    e = run_product<kUpdate>(last ? to_last : to_x[at], a, A.n, pair, s);
+    Operands x = to_x[at];
+    x.in_low = a.in_low == kBytes ? bytes[at] : halves[at];
+    x.out_low = a.out_low == kBytes ? bytes[at ^ 1] : halves[at ^ 1];
+    if (last && !a.direct) x.out = result;
+    e = run_product<kUpdate>(x, a, A.n, pair, s);
   }
   return e;
 }
