@@ -238,9 +238,8 @@ __global__ void __launch_bounds__(256) ortho_load_tall_kernel(const E* g, const 
 // The products
 // ---------------------------------------------------------------------------
 enum { kGram = 0, kPoly = 1, kUpdate = 2 };
-// Lower parts: fp16; or the upper byte of an fp16 (2 bits of mantissa), times 2^12.
+// Lower parts: fp16; or the upper byte of an fp16 (2 bits of mantissa).
 enum { kNone = 0, kBytes = 1, kHalf = 2 };
-constexpr float kByteScale = 0x1p12f;
 
 struct ProductArgs {
   uint16_t* last;  // kUpdate of the last step: the result in bf16, [m][k] or (tall) [k][m]
@@ -378,93 +377,96 @@ __device__ __forceinline__ uint32_t byte_line(uint32_t block, int lane, int half
   return block + kBlockBytes + lane * 32 + ((half ^ (lane >> 2 & 1)) << 4);
 }
 
-// A row's 32 columns of the result from the accumulators and what the turn's place holds: v.  f: what the stored X lacks.
-template <int kMode>
-__device__ __forceinline__ void combine(float (&v)[32], const uint32_t (&acc)[32], uint32_t block, int lane, float f, int low) {
+// A row's 32 columns of the result from the accumulators and what the turn's place holds: v.  f: what the stored X
+// lacks.  Two values to an instruction where that can be: the epilogue's instructions are what is beside the products.
+template <int kMode, int kIn>
+__device__ __forceinline__ void combine_as(float (&v)[32], const uint32_t (&acc)[32], uint32_t block, int lane, float f) {
   const uint32_t line = block + lane * 64, swz = (lane >> 1) & 3;
-  const float by = kMode == kGram ? 0x1p-14f * f * f : 0x1p-13f * f, a = kA * f;
-  const float low_by = low == kBytes ? 1.f / kByteScale : 1.f;
-  uint4 bytes = make_uint4(0u, 0u, 0u, 0u);
+  const float by = kMode == kGram ? 0x1p-14f * f * f : kMode == kPoly ? kC * 0x1p-15f : 0x1p-13f * f;
+  const float a = kMode == kPoly ? kB * 0.5f : kA * f;
+  uint32_t bytes[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     Eight h, l;
     if constexpr (kMode != kGram) h.v = ld_shared_v4(line + ((q ^ swz) << 4));
-    if constexpr (kMode == kUpdate) {
-      l.v = make_uint4(0u, 0u, 0u, 0u);
-      if (low == kHalf) l.v = ld_shared_v4(line + kBlockBytes + ((q ^ swz) << 4));
-      if (low == kBytes) {
-        if (q % 2 == 0) bytes = ld_shared_v4(byte_line(block, lane, q / 2));
-        const uint32_t b0 = q % 2 == 0 ? bytes.x : bytes.z, b1 = q % 2 == 0 ? bytes.y : bytes.w;
-        l.v = make_uint4(__byte_perm(b0, 0u, 0x1404), __byte_perm(b0, 0u, 0x3424), __byte_perm(b1, 0u, 0x1404),
-                         __byte_perm(b1, 0u, 0x3424));
+    if constexpr (kIn == kHalf) l.v = ld_shared_v4(line + kBlockBytes + ((q ^ swz) << 4));
+    if constexpr (kIn == kBytes) {
+      if (q % 2 == 0) {
+        const uint4 u = ld_shared_v4(byte_line(block, lane, q / 2));
+        bytes[0] = u.x, bytes[1] = u.y, bytes[2] = u.z, bytes[3] = u.w;
       }
+      const uint32_t b0 = bytes[2 * (q % 2)], b1 = bytes[2 * (q % 2) + 1];
+      l.v = make_uint4(__byte_perm(b0, 0u, 0x1404), __byte_perm(b0, 0u, 0x3424), __byte_perm(b1, 0u, 0x1404),
+                       __byte_perm(b1, 0u, 0x3424));
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float p = __uint_as_float(acc[8 * q + e]);
-      float x = 0.f;
-      if constexpr (kMode != kGram) x = __half2float(e % 2 == 0 ? h.h[e / 2].x : h.h[e / 2].y);
-      if constexpr (kMode == kUpdate) x = fmaf(__half2float(e % 2 == 0 ? l.h[e / 2].x : l.h[e / 2].y), low_by, x);
-      if constexpr (kMode == kGram) v[8 * q + e] = p * by;
-      if constexpr (kMode == kPoly) v[8 * q + e] = fmaf(kC * 0x1p-15f, p, kB * 0.5f * x);
-      if constexpr (kMode == kUpdate) v[8 * q + e] = fmaf(p, by, a * x);
+    for (int e = 0; e < 4; ++e) {
+      float &v0 = v[8 * q + 2 * e], &v1 = v[8 * q + 2 * e + 1];
+      mul2(v0, v1, __uint_as_float(acc[8 * q + 2 * e]), __uint_as_float(acc[8 * q + 2 * e + 1]), by, by);
+      if constexpr (kMode != kGram) {
+        const float2 x = __half22float2(h.h[e]);
+        fma2(v0, v1, x.x, x.y, a, a);
+      }
+      if constexpr (kIn != kNone) {
+        const float2 x = __half22float2(l.h[e]);
+        fma2(v0, v1, x.x, x.y, a, a);
+      }
     }
   }
 }
+template <int kMode>
+__device__ __forceinline__ void combine(float (&v)[32], const uint32_t (&acc)[32], uint32_t block, int lane, float f, int low) {
+  if (kMode == kUpdate && low == kBytes)
+    combine_as<kMode, kBytes>(v, acc, block, lane, f);
+  else if (kMode == kUpdate && low == kHalf)
+    combine_as<kMode, kHalf>(v, acc, block, lane, f);
+  else
+    combine_as<kMode, kNone>(v, acc, block, lane, f);
+}
 
 // The warp's 32 x 32 block of the result from row r0 and column c0 on, to where it belongs: through the place `block`
-// to TMA, which one lane commits; rows that TMA cannot store, directly.
-template <int kMode>
-__device__ __forceinline__ void emit(const Operands& O, const ProductArgs& A, const float (&v)[32], uint32_t block, int r0, int c0,
-                                     int mat, int lane) {
+// to TMA, which one lane commits; rows that TMA cannot store, directly.  kLast: in bf16.
+template <int kMode, int kOut, bool kLast>
+__device__ __forceinline__ void emit_as(const Operands& O, const ProductArgs& A, const float (&v)[32], uint32_t block, int r0,
+                                        int c0, int mat, int lane) {
   const uint32_t line = block + lane * 64, swz = (lane >> 1) & 3;
-  const bool last = kMode == kUpdate && A.last != nullptr;
-  const bool mirror = (kMode != kUpdate && c0 != r0) || (last && A.tall);  // the diagonal's own blocks are whole
-  if (last && A.direct) {
-    const int r = r0 + lane;
-    const int64_t right = A.tall ? A.m : 1, down = A.tall ? 1 : A.k;
-    uint16_t* to = A.last + (static_cast<int64_t>(mat) * A.m * A.k + r * down + c0 * right);
-    if (r < A.m) {
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (c0 + e < A.k) to[e * right] = from_f32<uint16_t>(v[e] * (1.f / kScaleX));
-    }
-    return;
-  }
+  const bool mirror = (kMode != kUpdate && c0 != r0) || (kLast && A.tall);  // the diagonal's own blocks are whole
   uint32_t bytes[4];
   __syncwarp();
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     float w[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = v[8 * q + e];
+    for (int e = 0; e < 8; ++e) w[e] = v[8 * q + e] * (kLast ? 1.f / kScaleX : 1.f);
     Eight h;
-    if (last) {
-      constexpr float f = 1.f / kScaleX;
-      h.v = make_uint4(pack_bf16x2(w[0] * f, w[1] * f), pack_bf16x2(w[2] * f, w[3] * f), pack_bf16x2(w[4] * f, w[5] * f),
-                       pack_bf16x2(w[6] * f, w[7] * f));
+    if constexpr (kLast) {
+      h.v = make_uint4(pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7]));
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e) h.h[e] = __floats2half2_rn(w[2 * e], w[2 * e + 1]);
     }
     st_shared_v4(line + ((q ^ swz) << 4), {h.v.x, h.v.y, h.v.z, h.v.w});
-    if (kMode == kUpdate && A.out_low != kNone) {
+    if constexpr (kOut != kNone) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] -= __half2float(e % 2 == 0 ? h.h[e / 2].x : h.h[e / 2].y);
-      if (A.out_low == kHalf) {
-        Eight l;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) l.h[e] = __floats2half2_rn(w[2 * e], w[2 * e + 1]);
-        st_shared_v4(line + kBlockBytes + ((q ^ swz) << 4), {l.v.x, l.v.y, l.v.z, l.v.w});
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; e += 4) {
-          const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(w[e] * kByteScale, w[e + 1] * kByteScale), __NV_SATFINITE, __NV_E5M2);
-          const uint32_t up = __nv_cvt_float2_to_fp8x2(make_float2(w[e + 2] * kByteScale, w[e + 3] * kByteScale), __NV_SATFINITE, __NV_E5M2);
-          bytes[2 * (q & 1) + e / 4] = lo | up << 16;
-        }
-        if (q % 2 == 1) st_shared_v4(byte_line(block, lane, q / 2), {bytes[0], bytes[1], bytes[2], bytes[3]});
+      for (int e = 0; e < 4; ++e) {
+        const float2 x = __half22float2(h.h[e]);
+        fma2(w[2 * e], w[2 * e + 1], x.x, x.y, -1.f, -1.f);
       }
+    }
+    if constexpr (kOut == kHalf) {
+      Eight l;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) l.h[e] = __floats2half2_rn(w[2 * e], w[2 * e + 1]);
+      st_shared_v4(line + kBlockBytes + ((q ^ swz) << 4), {l.v.x, l.v.y, l.v.z, l.v.w});
+    }
+    if constexpr (kOut == kBytes) {
+#pragma unroll
+      for (int e = 0; e < 8; e += 4) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(w[e], w[e + 1]), __NV_SATFINITE, __NV_E5M2);
+        const uint32_t up = __nv_cvt_float2_to_fp8x2(make_float2(w[e + 2], w[e + 3]), __NV_SATFINITE, __NV_E5M2);
+        bytes[2 * (q % 2) + e / 4] = lo | up << 16;
+      }
+      if (q % 2 == 1) st_shared_v4(byte_line(block, lane, q / 2), {bytes[0], bytes[1], bytes[2], bytes[3]});
     }
     if (mirror) {
 #pragma unroll
@@ -479,10 +481,35 @@ __device__ __forceinline__ void emit(const Operands& O, const ProductArgs& A, co
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
-    if (!(last && A.tall)) tma_store_3d(&O.out, block, c0, r0, mat);
-    if (kMode == kUpdate && A.out_low != kNone) tma_store_3d(&O.out_low, block + kBlockBytes, c0, r0, mat);
+    if (!(kLast && A.tall)) tma_store_3d(&O.out, block, c0, r0, mat);
+    if (kOut != kNone) tma_store_3d(&O.out_low, block + kBlockBytes, c0, r0, mat);
     if (mirror) tma_store_3d(&O.out, block + kBlockBytes, r0, c0, mat);
     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+template <int kMode>
+__device__ __forceinline__ void emit(const Operands& O, const ProductArgs& A, const float (&v)[32], uint32_t block, int r0, int c0,
+                                     int mat, int lane) {
+  if constexpr (kMode != kUpdate) {
+    emit_as<kMode, kNone, false>(O, A, v, block, r0, c0, mat, lane);
+  } else if (A.last == nullptr) {
+    if (A.out_low == kBytes)
+      emit_as<kMode, kBytes, false>(O, A, v, block, r0, c0, mat, lane);
+    else if (A.out_low == kHalf)
+      emit_as<kMode, kHalf, false>(O, A, v, block, r0, c0, mat, lane);
+    else
+      emit_as<kMode, kNone, false>(O, A, v, block, r0, c0, mat, lane);
+  } else if (!A.direct) {
+    emit_as<kMode, kNone, true>(O, A, v, block, r0, c0, mat, lane);
+  } else {
+    const int r = r0 + lane;
+    const int64_t right = A.tall ? A.m : 1, down = A.tall ? 1 : A.k;
+    uint16_t* to = A.last + (static_cast<int64_t>(mat) * A.m * A.k + r * down + c0 * right);
+    if (r < A.m) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (c0 + e < A.k) to[e * right] = from_f32<uint16_t>(v[e] * (1.f / kScaleX));
+    }
   }
 }
 
