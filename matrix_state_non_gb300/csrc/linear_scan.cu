@@ -603,15 +603,59 @@ __global__ void __launch_bounds__(kSumThreads) sum_parts_kernel(const float* par
 
 constexpr int kEveryBf16 = 8, kEveryF32 = 4;  // steps of a segment of the backward
 
-// Blocks to a cluster: twice as many until 240 and more are there (two to an SM,
-// for most SMs), as long as each has a tile of its own.  More, in several waves,
-// lose: B=8 T=2048 C=1024 bf16 takes 27.6 us with 2 (one wave), 35.8 with 8; B=8
-// T=4096 C=640 42 and 49.
-int cluster_blocks(const LinearArgs& a, int tile) {
+// Clusters of 2 to 8 blocks that the GPU runs at once, as it answered before, or 0.
+struct Fit {
+  std::atomic<int> of[kMaxCluster + 1];
+  template <typename... P>
+  int get(void (*kernel)(P...), int smem, int r) {
+    int n = of[r].load();
+    if (n == 0) {
+      cudaLaunchAttribute at{};
+      at.id = cudaLaunchAttributeClusterDimension;
+      at.val.clusterDim.x = r;
+      at.val.clusterDim.y = at.val.clusterDim.z = 1;
+      cudaLaunchConfig_t c{};
+      c.gridDim = dim3(r);
+      c.blockDim = dim3(kThreads);
+      c.dynamicSmemBytes = smem;
+      c.attrs = &at;
+      c.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &c) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        n = 304 / r;
+      }
+      of[r].store(n);
+    }
+    return n;
+  }
+};
+
+// Blocks to a cluster, each with a tile at least: the shortest of the waves of all
+// clusters (152, 97, 74, 58, 46, 38, 36 of 2 to 8 blocks run at once, two blocks to
+// an SM).  A block of r takes 1 / r of the steps, and 0.06 for the exchange, which
+// grows with r; a last wave with one block to an SM takes 0.64.  44 chains of
+// T=4096 bf16 take 22.0 us so, 26.3 with the power of two that first makes 240
+// blocks, 90 take 38.8 and 42.7; 100 take 43.8 with 4 and 52.6 with 2 or 3.  With
+// more than 152 clusters the waves overlap: 2 where that is shorter (200: 79.6 us,
+// 90.9 with 1; 230: 96.8 and 91.3; more than 2 lose a third at T=512).
+template <typename... P>
+int cluster_blocks(void (*kernel)(P...), int smem, const LinearArgs& a, int tile, Fit& fit) {
   const int64_t chains = static_cast<int64_t>(a.B) * ((a.C + kChan - 1) / kChan);
-  int r = 1;
-  while (r < kMaxCluster && chains * r < 240 && r * tile < a.T) r *= 2;
-  return r;
+  const int tiles = (a.T + tile - 1) / tile;
+  if (chains > 152) return chains <= 216 && tiles > 1 ? 2 : 1;
+  int best = 1;
+  float least = 1.06f;
+  for (int r = 2; r <= kMaxCluster && r <= tiles; ++r) {
+    const int at_once = fit.get(kernel, smem, r), left = static_cast<int>(chains) % at_once;
+    const bool half = 2 * left <= at_once && chains > at_once;
+    const float waves = static_cast<float>(chains / at_once) + (left == 0 ? 0.f : half ? 0.64f : 1.f);
+    const float time = waves * (1.f / static_cast<float>(r) + 0.06f);
+    if (time < least) {
+      best = r;
+      least = time;
+    }
+  }
+  return best;
 }
 
 // How rows can be read: value by value, two channels at a time, or (on 16 bytes)
@@ -648,7 +692,8 @@ cudaError_t forward(const LinearArgs& a, float* states, cudaStream_t s) {
     if (!map_rows(&maps.m[0], a, a.a, a.a_stride, kTile) || !map_rows(&maps.m[1], a, a.x, a.x_stride, kTile))
       return cudaErrorInvalidValue;
   }
-  const int groups = (a.C + kChan - 1) / kChan, blocks = cluster_blocks(a, kTile);
+  static Fit fit;
+  const int groups = (a.C + kChan - 1) / kChan, blocks = cluster_blocks(kernel, kSmem, a, kTile, fit);
   return launch_cluster(kernel, static_cast<int64_t>(a.B) * groups * blocks, blocks, kThreads, kSmem, false, s, a, states, blocks, groups,
                         maps);
 }
@@ -670,7 +715,8 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t s) {
         !map_rows(&maps.m[2], a, a.dy, a.C, kTile))
       return cudaErrorInvalidValue;
   }
-  const int groups = (a.C + kChan - 1) / kChan, blocks = cluster_blocks(a, kTile);
+  static Fit fit;
+  const int groups = (a.C + kChan - 1) / kChan, blocks = cluster_blocks(kernel, kSmem, a, kTile, fit);
   e = launch_cluster(kernel, static_cast<int64_t>(a.B) * groups * blocks, blocks, kThreads, kSmem, true, s, a, states, part, blocks, groups,
                      maps);
   if (e != cudaSuccess) return e;

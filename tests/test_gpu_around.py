@@ -254,6 +254,27 @@ def test_linear_scan_backward(B, T, C, dtype, lengths, h0, wide):
             assert np.all(host(got["dx"])[b, e:] == 0.0) and np.all(host(got["da"])[b, e:] == 0.0)
 
 
+@pytest.mark.parametrize("B", [36, 37, 44, 56, 70, 90, 100, 150, 200, 230])
+@pytest.mark.parametrize("C,dtype", [(16, "bf16"), (9, "f32")])
+def test_linear_scan_of_many_sequences(B, C, dtype):
+    """One to eight blocks share a sequence, by the number of sequences."""
+    from matrix_state_non_gb300 import binding as m
+    T = 1030
+    d = scan_inputs(B, T, C, dtype, B, True)
+    lengths = [int(n) for n in np.random.default_rng(B).integers(-3, T + 5, B)]
+    lengths[:4] = [T, 0, 1, T - 1]
+    g = scan_dev(d, dtype, 0, lengths)
+    y, H = o.linear_scan(d["x"], d["a"], d["alpha"], d["beta"], d["H_0"], clamped(lengths, T))
+    r = m.linear_scan(g["x"], g["a"], g["alpha"], g["beta"], H_0=g["H_0"], lengths=ints(lengths))
+    close(r["H_T"], H, TOL, "H_T")
+    near(r["y"], y, (BF16_HALF if dtype == "bf16" else 0) + TOL, "y", TOL * np.abs(y).max())
+    ref = o.linear_scan_backward(d["x"], d["a"], d["alpha"], d["beta"], d["dy"], d["H_0"], d["dH_T"], clamped(lengths, T))
+    got = m.linear_scan_backward(g["x"], g["a"], g["alpha"], g["beta"], g["dy"], H_0=g["H_0"], dH_T=g["dH_T"],
+                                 lengths=ints(lengths), want_dH0=True)
+    for k in ref:
+        close(got[k], ref[k], 4 * TOL if k in ("dalpha", "dbeta") else TOL, k)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_linear_scan_without_beta(dtype):
     from matrix_state_non_gb300 import binding as m
