@@ -25,8 +25,8 @@
 // The steps between have a byte for the lower part there, 14 to 15 bits in all
 // (another 9e-4 for rank 1).
 //
-// 24 of 1024 x 4096 bf16, 5 steps: 1.56 ms, of which A 5 x 88 us (1.5 PFLOP/s, 3.2
-// waves of tiles), P 5 x 34, X' 145 to 170 (12 TB/s between L2 and the SMs; 3.6 of
+// 24 of 1024 x 4096 bf16, 5 steps: 1.57 ms, of which A 5 x 88 us (1.5 PFLOP/s, 3.2
+// waves of tiles), P 5 x 34, X' 146 to 166 (15 TB/s between L2 and the SMs, 3.6 of
 // HBM), the norm and the first X 100.  With two fp16 parts in all steps X' was 185,
 // bound by HBM, and the whole 1.71 ms; with two but in the first and last 1.61.
 #include <cuda_fp16.h>
@@ -722,8 +722,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 // The same products where there are few tiles: a narrow tile (kN columns) to a
 // block, so that there are enough of them, and nothing that a block does twice.
 // The time is that of a launch behind another (2 us) and of a tile's operands on
-// their way to one SM.  1024 x 1024, one matrix, 5 steps: 117 us; 2 of 1000 x 333:
-// 96 us (163 and 140 by persistent blocks with tiles of 128 x 128; 131 and 113 with
+// their way to one SM.  1024 x 1024, one matrix, 5 steps: 116 us; 2 of 1000 x 333:
+// 99 us (163 and 140 by persistent blocks with tiles of 128 x 128; 131 and 113 with
 // clusters of four that share a tile's inner dimension; 142 and 120 in one
 // cooperative launch with barriers across the grid).
 // ---------------------------------------------------------------------------
