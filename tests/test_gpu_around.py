@@ -502,6 +502,17 @@ def test_orthogonalize_steps(rows, cols, steps):
     close(m.orthogonalize(dev(x), steps=steps), o.orthogonalize(x, steps), ORTHO_TOL, steps)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(520, 516), (20, 700), (600, 904), (130, 200)])
+@pytest.mark.parametrize("steps", [1, 2, 3, 4])
+def test_orthogonalize_early_steps(rows, cols, steps, dtype):
+    """Whichever step is the last: what X is kept in depends on it."""
+    from matrix_state_non_gb300 import binding as m
+    for kind in ("gauss", "rank1"):
+        x = round_to(spectrum(rows, cols, kind, 13), dtype)
+        close(m.orthogonalize(dev(x, dtype), steps=steps), o.orthogonalize(x, steps), ORTHO_TOL, (steps, kind))
+
+
 @pytest.mark.parametrize("rows,cols", [(40, 60), (140, 150)])
 def test_orthogonalize_sizes_of_values(rows, cols):
     """The result does not depend on the size of G, over the fp32 range; eps counts where G is small; zeros stay zeros."""
@@ -539,7 +550,8 @@ def test_orthogonalize_sizes_at_the_ends(rows, cols, dtype):
 
 @pytest.mark.parametrize("kind", ["gauss", "decay", "floor", "rank1"])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("n,rows,cols", [(1, 520, 700), (2, 1100, 600), (1, 800, 8200), (30, 515, 512), (20, 800, 800)])
+@pytest.mark.parametrize("n,rows,cols", [(1, 520, 700), (2, 1100, 600), (1, 800, 8200), (30, 515, 512), (20, 800, 800),
+                                         (20, 904, 800)])
 def test_orthogonalize_long_sides(n, rows, cols, dtype, kind):
     """Matrices whose last step takes X in one part: 3.4445 2^-12 of it, 1.2 / 0.67 at most of the result's size: 1.5e-3."""
     import torch
