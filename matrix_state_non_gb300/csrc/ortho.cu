@@ -22,8 +22,9 @@
 // 1.5e-3; matrices of fewer than 512 rows, where errors average least, get that.
 // One part holds the first X where G is bf16, and, from 512 rows on, the last
 // step's, whose noise grows once (a matrix of rank 1 comes out 1e-3 off for it).
-// The steps between have a byte for the lower part there, 14 to 15 bits in all
-// (another 9e-4 for rank 1).
+// The three before it have a byte for the lower part there, 14 to 15 bits in all
+// (another 9e-4 for rank 1): noise grows 3.44-fold a step where X has nothing, and
+// with bytes before that seven steps left 1.8e-2 of a matrix of rank 1, eight 4e-2.
 //
 // 24 of 1024 x 4096 bf16, 5 steps: 1.57 ms, of which A 5 x 88 us (1.5 PFLOP/s, 3.2
 // waves of tiles), P 5 x 34, X' 146 to 166 (15 TB/s between L2 and the SMs, 3.6 of
@@ -1065,11 +1066,13 @@ cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
   if (!a.direct)
     made = made && map_matrix(&result, A.out, A.n, A.rows, A.cols, A.cols, kEpilogueBox, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16);
   if (!made) return cudaErrorInvalidValue;
-  // The lower part of a step's X.  From kOnePart rows on, where it is no operand, a byte serves from the second step on
-  // (the first X's noise would grow 480-fold), and nothing in the last step.
+  // The lower part of a step's X, by the steps still to come (its own among them), through which its noise grows: from
+  // kOnePart rows on, where it is no operand, nothing serves in the last step and a byte in the three before it.
   auto low_part = [&](int step) {
+    const int left = A.steps - step;
     if (step == 0) return A.bf16 ? kNone : kHalf;
-    return m < kOnePart ? step < A.steps ? kHalf : kNone : step < A.steps - 1 ? kBytes : kNone;
+    if (left < 1) return kNone;
+    return m < kOnePart || left > 4 ? kHalf : left > 1 ? kBytes : kNone;
   };
   for (int i = 0; i < A.steps && e == cudaSuccess; ++i) {
     const int at = i & 1;
