@@ -113,14 +113,22 @@ struct OrthoArgs {
   bool bf16;
 };
 
-// 1 / (sqrt(sum) + eps) with few fp64 operations (slow here): the root of the sum times an even power of two.
-__device__ __forceinline__ float inverse_norm(double sum, float eps) {
-  float norm = static_cast<float>(sum);  // 0, an infinity or NaN
+// 1 / (sqrt(sum) + eps) as a power of two times a factor: fp32 holds neither a norm beyond its largest value nor the
+// inverse of one below 2^-128, so the power takes 64 binary places of those.
+struct Inverse {
+  float power, factor;
+  __device__ __forceinline__ float of(float v) const { return v * power * factor; }
+};
+// With few fp64 operations (slow here): the root of the sum times an even power of two.
+__device__ __forceinline__ Inverse inverse_norm(double sum, float eps) {
+  float root = static_cast<float>(sum);  // 0, an infinity or NaN
+  int half = sum == 0. ? -1000 : 0;
   if (sum > 0. && sum < 1.7e308) {
-    const int half = ((__double2hiint(sum) >> 20) - 1023) >> 1;
-    norm = scalbnf(sqrtf(static_cast<float>(sum * __hiloint2double((1023 - 2 * half) << 20, 0))), half);
+    half = ((__double2hiint(sum) >> 20) - 1023) >> 1;
+    root = sqrtf(static_cast<float>(sum * __hiloint2double((1023 - 2 * half) << 20, 0)));  // in [1, 2)
   }
-  return 1.f / (norm + eps);
+  const int by = half > 100 ? -64 : half < -100 && eps < 0x1p-100f ? 64 : 0;
+  return {ldexpf(1.f, by), 1.f / (scalbnf(root, half + by) + ldexpf(eps, by))};
 }
 
 size_t ortho_scratch_bytes(int64_t n, int64_t rows, int64_t cols);

@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kSumThreads) ortho_sum_kernel(const E* g, int6
 }
 
 // In every thread of a block: what the matrix's entries are multiplied with.
-__device__ __forceinline__ float first_factor(const double* part, int parts, float eps, float* shared) {
+__device__ __forceinline__ Inverse first_factor(const double* part, int parts, float eps, Inverse* shared) {
   if (threadIdx.x < 32) {
     double acc = 0.;
     for (int i = threadIdx.x; i < parts; i += 32) acc += part[i];
@@ -154,19 +154,19 @@ __device__ __forceinline__ void split_8(const float (&v)[8], Eight& hi, Eight& l
 // the power of two below it, which leaves X in one part with all its digits; the
 // rest, in [1, 2), is a factor of the first step (`rest`, for each matrix).
 template <typename E>
-__device__ __forceinline__ float first_scale(float f, float* rest) {
+__device__ __forceinline__ Inverse first_scale(Inverse f, float* rest) {
   if constexpr (sizeof(E) == 2) {
     int e = 0;
-    const bool usual = f > 0.f && f <= 3.4e38f;
-    const float r = usual ? 2.f * frexpf(f, &e) : 1.f;
+    const bool usual = f.factor > 0.f && f.factor <= 3.4e38f;
+    const float r = usual ? 2.f * frexpf(f.factor, &e) : 1.f;
     if (threadIdx.x == 0 && rest != nullptr) *rest = r;
-    return usual ? ldexpf(1.f, e - 1) : f;
+    if (usual) f.factor = ldexpf(1.f, e - 1);
   }
   return f;
 }
-__device__ __forceinline__ void store_first(float (&v)[8], float f, __half* hi, __half* lo, int64_t at) {
+__device__ __forceinline__ void store_first(float (&v)[8], Inverse f, __half* hi, __half* lo, int64_t at) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = v[e] * f * kScaleX;
+  for (int e = 0; e < 8; ++e) v[e] = f.of(v[e]) * kScaleX;
   Eight h, l;
   split_8(v, h, l);
   *reinterpret_cast<uint4*>(hi + at) = h.v;
@@ -179,12 +179,12 @@ constexpr int kLoadRun = 4;
 template <typename E>
 __global__ void __launch_bounds__(256) ortho_load_kernel(const E* g, const double* part, int parts, float eps, __half* hi,
                                                          __half* lo, float* rest, int m, int k, int pitch, int blocks) {
-  __shared__ float shared;
+  __shared__ Inverse shared;
   const int64_t mat = blockIdx.x / blocks;
   const int block = static_cast<int>(blockIdx.x - mat * blocks), per_row = pitch / 8;
   const E* p = g + mat * m * k;
   wait_previous();
-  const float f = first_scale<E>(first_factor(part + mat * parts, parts, eps, &shared), block == 0 ? rest + mat : nullptr);
+  const Inverse f = first_scale<E>(first_factor(part + mat * parts, parts, eps, &shared), block == 0 ? rest + mat : nullptr);
   const int64_t size = static_cast<int64_t>(m) * per_row;
 #pragma unroll
   for (int u = 0; u < kLoadRun; ++u) {
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(256) ortho_load_tall_kernel(const E* g, const 
                                                               __half* lo, float* rest, int m, int k, int pitch, int tiles_m,
                                                               int tiles) {
   __shared__ float t[kTurn][kTurn + 1];
-  __shared__ float shared;
+  __shared__ Inverse shared;
   const int64_t mat = blockIdx.x / tiles;
   const int tile = static_cast<int>(blockIdx.x - mat * tiles);
   const int r0 = tile % tiles_m * kTurn, c0 = tile / tiles_m * kTurn;
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(256) ortho_load_tall_kernel(const E* g, const 
     t[r][c] = r0 + r < m && c0 + c < k ? to_f32(p[static_cast<int64_t>(c0 + c) * m + r0 + r]) : 0.f;
   }
   wait_previous();
-  const float f = first_scale<E>(first_factor(part + mat * parts, parts, eps, &shared), tile == 0 ? rest + mat : nullptr);
+  const Inverse f = first_scale<E>(first_factor(part + mat * parts, parts, eps, &shared), tile == 0 ? rest + mat : nullptr);
 #pragma unroll
   for (int i = threadIdx.x; i < kTurn * kTurn / 8; i += 256) {
     const int r = i / (kTurn / 8), c = i % (kTurn / 8) * 8;

@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kThreads, kCols > 128 ? 2 : 3) ortho_small_ker
   constexpr int kPitch = kCols + 8;
   constexpr uint32_t kXPart = kRows * kPitch * 2, kSPart = kRows * kSquare * 2;
   __shared__ double red[kThreads / 32];
-  __shared__ float factor;
+  __shared__ Inverse factor;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, q = lane & 3, row = 16 * (warp & 3) + (lane >> 2);
   const uint32_t x = smem_u32(raw), s = x + 2 * kXPart, p = s + (kAll ? 2 : 1) * kSPart;
   const int size = m * k, line = tall ? m : k;  // a line of G
@@ -117,12 +117,12 @@ __global__ void __launch_bounds__(kThreads, kCols > 128 ? 2 : 3) ortho_small_ker
     factor = inverse_norm(acc, eps);
   }
   __syncthreads();
-  const float f = factor;
+  const Inverse f = factor;
 #pragma unroll
   for (int j = 0; j < kCols * kRows / kThreads; ++j) {
     const int i = threadIdx.x + kThreads * j, a = i / line, c = i - a * line;
     if (i < size) {
-      const float w = v[j] * f * kScaleX;
+      const float w = f.of(v[j]) * kScaleX;
       const __half hi = __float2half_rn(w), lo = __float2half_rn(w - __half2float(hi));
       const uint32_t to = x + ((tall ? c : a) * kPitch + (tall ? a : c)) * 2;
       st_shared_u16(to, __half_as_ushort(hi));

@@ -43,11 +43,11 @@ __device__ __forceinline__ void put(float* to, const float (&v)[4][4], int tx, i
 
 // Value (r, c) of X_0 (m x k) times f; tall: it lies as [k][m].
 template <typename E>
-__device__ __forceinline__ float value(const E* g, int r, int c, int m, int k, bool tall, float f) {
-  return r < m && c < k ? to_f32(g[tall ? static_cast<int64_t>(c) * m + r : static_cast<int64_t>(r) * k + c]) * f : 0.f;
+__device__ __forceinline__ float value(const E* g, int r, int c, int m, int k, bool tall, Inverse f) {
+  return r < m && c < k ? f.of(to_f32(g[tall ? static_cast<int64_t>(c) * m + r : static_cast<int64_t>(r) * k + c])) : 0.f;
 }
 
-__device__ __forceinline__ float factor_of(const double* part, int parts, float eps, float* shared) {
+__device__ __forceinline__ Inverse factor_of(const double* part, int parts, float eps, Inverse* shared) {
   if (threadIdx.x < 32) {
     double acc = 0.;
     for (int i = threadIdx.x; i < parts; i += 32) acc += part[i];
@@ -64,12 +64,12 @@ template <typename E>
 __global__ void __launch_bounds__(kThreads) thin_gram_kernel(const E* g, const double* part, int parts, float eps, float* sums,
                                                              int m, int k, bool tall, int per, int pieces) {
   __shared__ __align__(16) float t[kSide * kPitch];  // [column][row]
-  __shared__ float shared;
+  __shared__ Inverse shared;
   const int mat = blockIdx.x / pieces, piece = blockIdx.x - mat * pieces;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const E* p = g + static_cast<int64_t>(mat) * m * k;
   wait_previous();
-  const float f = part != nullptr ? factor_of(part + static_cast<int64_t>(mat) * parts, parts, eps, &shared) : 1.f;
+  const Inverse f = part != nullptr ? factor_of(part + static_cast<int64_t>(mat) * parts, parts, eps, &shared) : Inverse{1.f, 1.f};
   float acc[4][4] = {};
   for (int c0 = piece * per; c0 < min(k, (piece + 1) * per); c0 += kSide) {
     __syncthreads();
@@ -141,12 +141,12 @@ __global__ void __launch_bounds__(kThreads) thin_apply_kernel(const E* g, const 
                                                               float* x, uint16_t* out, int m, int k, bool from_tall, bool tall,
                                                               int tiles) {
   __shared__ __align__(16) float t[kSide * kPitch], l[kSide * kPitch];
-  __shared__ float shared;
+  __shared__ Inverse shared;
   const int mat = blockIdx.x / tiles, c0 = (blockIdx.x - mat * tiles) * kSide;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int64_t base = static_cast<int64_t>(mat) * m * k;
   wait_previous();
-  const float f = part != nullptr ? factor_of(part + static_cast<int64_t>(mat) * parts, parts, eps, &shared) : 1.f;
+  const Inverse f = part != nullptr ? factor_of(part + static_cast<int64_t>(mat) * parts, parts, eps, &shared) : Inverse{1.f, 1.f};
 #pragma unroll 4
   for (int i = threadIdx.x; i < kSquare; i += kThreads) {
     const int fast = i % kSide, slow = i / kSide, r = from_tall ? fast : slow, c = from_tall ? slow : fast;
