@@ -195,12 +195,13 @@ struct Gate2 {
 // and log2(1 + t) = 2 log2 e atanh(v), v = t / (2 + t) <= 1/3: a polynomial in v^2
 // of degree 4 (minimax, 4e-9).  f = 2^-w, w = alpha softplus(z) log2 e; 1 - f is
 // w P(w) for |w| <= 0.7 (minimax, 8e-8), so that it keeps its digits where f is
-// near 1, and f is what is left; beyond, f is the hardware's power.  kSmall: f
-// keeps its digits where it is near 0 too, which only gradients show, and
-// softplus stops at fp32's largest value, so that no 0 times infinity is a
-// gradient where y overflows (it does for a of the type's largest value).  Without
-// that, only alpha = 0 would meet it: there shut() takes y to -infinity, where f
-// is 1, too.  (The bound took the forward from 57.8 to 59.3 us.)
+// near 1, and f is what is left; beyond, f is the hardware's power, whose digits a
+// state shows that decays far below what it was, and 1 - f what is left.
+// kGradient: softplus stops at fp32's largest value, so that no 0 times infinity
+// is a gradient where y overflows (it does for a of the type's largest value).
+// Without that, only alpha = 0 would meet it: there shut() takes y to -infinity,
+// where f is 1, too.  (The bound took the forward from 57.8 to 59.3 us; 1 - e for
+// 1 - w P in pairs, 58.0 to 62.4.)
 // Multiply-adds bound the kernels.  Two channels to an instruction take two
 // cycles of one of the two pipes, so some (here and in the scan itself) are left
 // single for the other: B=2 T=16384 C=1024 bf16 takes 56.7 us so, 62 with all in
@@ -209,7 +210,7 @@ struct Gate2 {
 __device__ __forceinline__ float2 shut(float2 beta, float2 alpha) {
   return make_float2(alpha.x == 0.f ? -INFINITY : beta.x, alpha.y == 0.f ? -INFINITY : beta.y);
 }
-template <bool kSmall>
+template <bool kGradient>
 __device__ __forceinline__ Gate2 gate_of(float2 y, float2 alpha) {
   Gate2 g;
   g.t = make_float2(ex2_fast(-fabsf(y.x)), ex2_fast(-fabsf(y.y)));
@@ -221,7 +222,7 @@ __device__ __forceinline__ Gate2 gate_of(float2 y, float2 alpha) {
   p = fma_2(s, p, two(0.96179163456f));
   p = fma_2(s, p, two(2.88539004326f));
   float2 above = make_float2(fmaxf(y.x, 0.f), fmaxf(y.y, 0.f));
-  if constexpr (kSmall) above = make_float2(fminf(above.x, kMost), fminf(above.y, kMost));
+  if constexpr (kGradient) above = make_float2(fminf(above.x, kMost), fminf(above.y, kMost));
   g.soft = fma_2(v, p, above);
   const float2 w = mul_2(alpha, g.soft);
   p = fma_2(w, two(-0.00015403463f), two(0.00134455867f));
@@ -233,8 +234,8 @@ __device__ __forceinline__ Gate2 gate_of(float2 y, float2 alpha) {
   const float2 f = make_float2(ex2_fast(-w.x), ex2_fast(-w.y)), far = fma_2(f, two(-1.f), two(1.f));
   const bool near0 = fabsf(w.x) <= 0.7f, near1 = fabsf(w.y) <= 0.7f;
   g.e = make_float2(near0 ? e.x : far.x, near1 ? e.y : far.y);
-  g.f = fma_2(g.e, two(-1.f), two(1.f));
-  if constexpr (kSmall) g.f = make_float2(near0 ? g.f.x : f.x, near1 ? g.f.y : f.y);
+  const float2 rest = make_float2(fmaf(-w.x, p.x, 1.f), fmaf(-w.y, p.y, 1.f));
+  g.f = make_float2(near0 ? rest.x : f.x, near1 ? rest.y : f.y);
   return g;
 }
 
