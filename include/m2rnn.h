@@ -501,6 +501,9 @@ int m2rnn_residual_norm_backward(const void* h, const float* w, const void* dy, 
  *   (may be NULL; may be H_0).
  * A value that is not finite reaches no step before its own; a of -infinity
  * and, where alpha > 0, of +infinity are gates: f = 1 and f = 0.
+ * There is no workspace and so no status: a device-side wait that gives up
+ * (seconds; an internal failure) leaves NaN in its channels of that sequence
+ * from there on, here and in the gradients.
  */
 int m2rnn_linear_scan(const void* x, int64_t x_stride, const void* a, int64_t a_stride, const float* alpha,
                       const float* beta, const float* H_0, const int32_t* lengths, void* y, float* H_T, int64_t B,
@@ -626,6 +629,8 @@ int m2rnn_path(int64_t K, int64_t V, m2rnn_dtype dtype);
  *     warp-MMA forward's input producer withhold input tile n of chains that
  *     run on one CTA (K = 16), so that the consumers' bounded waits expire
  *     and the status block reports M2RNN_ERR_TIMEOUT; -1 (the default) is off.
+ *     In the gated linear recurrence the first block withholds its tile of
+ *     round n.
  * Initial values come from the environment variables M2RNN_KERNEL (auto |
  * tcgen05 | mma | simt) and M2RNN_TEST_STALL_TILE, read once, at the first
  * call that needs them; later changes of the environment have no effect.

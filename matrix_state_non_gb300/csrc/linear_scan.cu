@@ -30,6 +30,7 @@
 #include <cstdint>
 
 #include "around.cuh"
+#include "internal.h"
 #include "mma_common.cuh"
 
 namespace m2rnn {
@@ -150,9 +151,9 @@ struct Ring {
 // A block that gave up waits for what is still on its way to its ring, of
 // `fills` tiles in all.
 template <typename Tiles>
-__device__ __forceinline__ void drain(const Tiles& ring, int fills) {
+__device__ __forceinline__ void drain(uint64_t* full, int fills) {
   for (int i = max(0, fills - Tiles::kStages); i < fills; ++i)
-    mbar_wait_timed(smem_u32(ring.full + i % Tiles::kStages), (i / Tiles::kStages) & 1, nullptr, 0);
+    mbar_wait_timed(smem_u32(full + i % Tiles::kStages), (i / Tiles::kStages) & 1, nullptr, 0);
 }
 template <int kN>
 struct Maps {
@@ -247,14 +248,19 @@ struct Exchange {
   float4 block[2][kMaxCluster][32];  // of the cluster's tiles
   alignas(8) uint64_t arrived[2];    // a phase for each second round: every tile's F and U are there
   alignas(8) uint64_t full[3];       // the ring's
-  int abort_flag;
+  int abort_flag;                    // a wait of the block gave up
+  int fills, rounds;                 // the ring's tiles that thread 0 asked for, the rounds
+  int failed, armed;                 // the round whose exchange thread 0 gave up (-1: none), and whether it had arrived
+  __device__ __forceinline__ bool alive() const { return *const_cast<const volatile int*>(&abort_flag) == 0; }
 };
 
-__device__ __forceinline__ void open_exchange(Exchange& x, int blocks) {
+__device__ __forceinline__ void open_exchange(Exchange& x, int rounds, int blocks) {
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&x.arrived[i]), 1);
     for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&x.full[i]), 1);
-    x.abort_flag = 0;
+    x.abort_flag = x.fills = x.armed = 0;
+    x.rounds = rounds;
+    x.failed = -1;
     fence_mbar_init_cluster();
   }
   if (blocks > 1)
@@ -264,6 +270,7 @@ __device__ __forceinline__ void open_exchange(Exchange& x, int blocks) {
 }
 
 constexpr float kSpoilt = __builtin_nanf("");
+constexpr int kRoundBytes = 32 * 16;  // of a block's F and U
 
 // The state before the warp's segment, from `carry`, the state before the
 // round; carry goes on to the next round.  Every thread of the cluster calls it.
@@ -271,8 +278,11 @@ constexpr float kSpoilt = __builtin_nanf("");
 // on the receiver's mbarrier: a cluster barrier's release would wait for the
 // outputs stored before it.  Buffers of two rounds serve: nobody sends for round
 // i + 2 before it has what this block sent for round i + 1, after this block was
-// done with round i; and nobody ends before all that is sent to it has come.  A
-// wait that gives up (seconds) spoils the state with NaN.
+// done with round i; and nobody ends before all that is sent to it has come.
+// A wait that gives up (seconds) spoils the state with NaN, and the block neither
+// waits, arrives nor sends any more: the others of its cluster, which miss what
+// it would have sent, give up in their turn, and nobody sends for a round that
+// the receiver has not got to (which would count in the wrong phase).
 __device__ __forceinline__ float2 state_before(Exchange& x, int round, float2 F, float2 U, float2& carry, int rank, int blocks) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, buf = round & 1;
   x.warp[buf][warp][lane] = make_float4(F.x, F.y, U.x, U.y);
@@ -294,14 +304,21 @@ __device__ __forceinline__ float2 state_before(Exchange& x, int round, float2 F,
     carry = fma_2(tF, carry, tU);
   } else {
     const uint32_t bar = smem_u32(&x.arrived[buf]);
-    if (warp < blocks) {
+    const bool alive = x.alive();
+    if (alive && warp < blocks) {
       const uint32_t to = mapa_shared(smem_u32(&x.block[buf][rank][lane]), warp), at = mapa_shared(bar, warp);
       asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(to),
                    "f"(tF.x), "f"(tF.y), "f"(tU.x), "f"(tU.y), "r"(at)
                    : "memory");
     }
-    if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, blocks * 32 * 16);
-    if (!mbar_wait<true>(bar, (round >> 1) & 1, &x.abort_flag, nullptr, 0)) carry = two(kSpoilt);
+    if (alive && threadIdx.x == 0) mbar_arrive_expect_tx(bar, blocks * kRoundBytes);
+    if (!alive || !mbar_wait<true>(bar, (round >> 1) & 1, &x.abort_flag, nullptr, 0)) {
+      carry = two(kSpoilt);
+      if (threadIdx.x == 0 && x.failed < 0) {
+        x.failed = round;
+        x.armed = alive;
+      }
+    }
     for (int r = 0; r < blocks; ++r) {
       if (r == rank) mine = carry;
       const float4 s = x.block[buf][r][lane];
@@ -309,6 +326,33 @@ __device__ __forceinline__ float2 state_before(Exchange& x, int round, float2 F,
     }
   }
   return fma_2(pF, mine, pU);
+}
+
+// Behind its rounds a block says that it sends no more, and it ends when all of
+// its cluster have said so: one that gave up may be far ahead of the others.
+// Without release: there is nothing to be seen but that.
+__device__ __forceinline__ void done_sending(int blocks) {
+  __syncwarp();
+  if (blocks > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+// The last that a block does.  If it gave up, what is still on its way to it lands
+// first: tiles of the ring, and what the others sent for rounds that it did not
+// take part in (its thread 0 does, here; not inlined, for registers).
+template <typename Tiles>
+__device__ __noinline__ void land(Exchange& x, int blocks) {
+  drain<Tiles>(x.full, x.fills);
+#pragma unroll 1
+  for (int r = x.failed; r >= 0 && r < x.rounds; ++r) {
+    const uint32_t bar = smem_u32(&x.arrived[r & 1]);
+    if (r > x.failed || !x.armed) mbar_arrive_expect_tx(bar, blocks * kRoundBytes);
+    if (!mbar_wait_timed<true>(bar, (r >> 1) & 1, nullptr, 0)) break;
+  }
+}
+template <typename Tiles>
+__device__ __forceinline__ void leave(Exchange& x, int blocks) {
+  __syncwarp();
+  if (blocks > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if (threadIdx.x == 0 && !x.alive()) land<Tiles>(x, blocks);
 }
 
 __device__ __forceinline__ uint8_t* align_smem(uint8_t* p) {
@@ -323,7 +367,7 @@ __device__ __forceinline__ int length_of(const LinearArgs& A, int b) {
 // Forward: y, H_T; or (kStates) the state before each kEvery steps
 // ---------------------------------------------------------------------------
 template <typename E, bool kPair, bool kTma, bool kStates, int kL, int kEvery>
-__global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs A, float* states, int blocks, int groups,
+__global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs A, float* states, int blocks, int groups, int stall,
                                                                      const __grid_constant__ Maps<2> maps) {
   __shared__ Exchange xch;
   extern __shared__ uint8_t raw[];
@@ -344,12 +388,15 @@ __global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs 
   const Tiles ring{align_smem(raw), xch.full};
   const CUtensorMap* const from[2] = {&maps.m[0], &maps.m[1]};
   Raw2<E> ra[kTma ? 1 : kL], rx[kTma ? 1 : kL];
-  open_exchange(xch, blocks);
+  open_exchange(xch, rounds, blocks);
   int t0 = rank * kTile + warp * kL;
   auto load = [&](int round) {  // the tile of a round, if it has steps
     if constexpr (kTma) {
       const int t = (round * blocks + rank) * kTile;
-      if (threadIdx.x == 0 && t < len) ring.fill(round % Tiles::kStages, from, group * kChan, t, b);
+      if (threadIdx.x == 0 && t < len && xch.alive()) {
+        xch.fills = round + 1;
+        if (round != stall || blockIdx.x != 0) ring.fill(round % Tiles::kStages, from, group * kChan, t, b);
+      }
     } else if (round < rounds) {
       load_rows<kPair>(ra, pa, A.a_stride, me.other, (round * blocks + rank) * kTile + warp * kL, len);
       load_rows<kPair>(rx, px, A.x_stride, me.other, (round * blocks + rank) * kTile + warp * kL, len);
@@ -412,13 +459,14 @@ __global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs 
       }
     }
   }
+  done_sending(blocks);
   let_next();
-  if (kTma && xch.abort_flag) drain(ring, (len - rank * kTile + kTile * blocks - 1) / (kTile * blocks));
   if constexpr (!kStates) {
     for (int t = rounds * kTile * blocks + rank * kWarps + warp; t < A.T; t += blocks * kWarps)
       store_2<kPair>(py + static_cast<int64_t>(t) * A.C, two(0.f), me.in0, me.in1);
     if (A.H_T != nullptr && rank == 0 && warp == 0) me.put(A.H_T + static_cast<int64_t>(b) * A.C, carry);
   }
+  leave<Tiles>(xch, blocks);
 }
 
 // ---------------------------------------------------------------------------
@@ -426,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_forward_kernel(LinearArgs 
 // ---------------------------------------------------------------------------
 template <typename E, bool kPair, bool kTma, int kL>
 __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs A, const float* states, float* part, int blocks,
-                                                                      int groups, const __grid_constant__ Maps<3> maps) {
+                                                                      int groups, int stall, const __grid_constant__ Maps<3> maps) {
   __shared__ Exchange xch;
   extern __shared__ uint8_t raw[];
   constexpr int kTile = kWarps * kL;
@@ -456,7 +504,10 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs
   auto load = [&](int round) {  // the tile of a round; before the sequence as behind it: zeros
     const int tile = tiles - 1 - (round * blocks + rank);
     if constexpr (kTma) {
-      if (threadIdx.x == 0 && tile >= 0) ring.fill(round % Tiles::kStages, from, group * kChan, tile * kTile, b);
+      if (threadIdx.x == 0 && tile >= 0 && xch.alive()) {
+        xch.fills = round + 1;
+        if (round != stall || blockIdx.x != 0) ring.fill(round % Tiles::kStages, from, group * kChan, tile * kTile, b);
+      }
     } else if (round < rounds) {
       const int t = tile < 0 ? len : tile * kTile + (kWarps - 1 - warp) * kL;
       load_rows<kPair>(ra, pa, A.a_stride, me.other, t, len);
@@ -467,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs
   auto load_state = [&](int t0) {
     if (t0 >= 0 && t0 < len) hs = me.get(ph + static_cast<int64_t>(t0 / kL) * A.C);
   };
-  open_exchange(xch, blocks);
+  open_exchange(xch, rounds, blocks);
   for (int i = 0; i < (kTma ? Tiles::kStages : 1); ++i) load(i);
   wait_previous();
   if (rounds > 0) load_state(t0);
@@ -532,7 +583,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs
     }
   }
   let_next();
-  if (kTma && xch.abort_flag) drain(ring, (tiles - rank + blocks - 1) / blocks);
+  if (kTma && xch.abort_flag) drain<Tiles>(xch.full, xch.fills);  // (registers: not in leave alone)
+  done_sending(blocks);
   for (int t = tiles * kTile + rank * kWarps + warp; t < A.T; t += blocks * kWarps) {
     store_2<kPair>(pdx + static_cast<int64_t>(t) * A.C, two(0.f), me.in0, me.in1);
     store_2<kPair>(pda + static_cast<int64_t>(t) * A.C, two(0.f), me.in0, me.in1);
@@ -554,6 +606,7 @@ __global__ void __launch_bounds__(kThreads, 2) linear_backward_kernel(LinearArgs
     me.put(p, make_float2(t.x * kLn2, t.y * kLn2));  // (softplus in units of log2)
     me.put(p + A.C, make_float2(t.z, t.w));
   }
+  leave<Tiles>(xch, blocks);
 }
 
 // ---------------------------------------------------------------------------
@@ -696,7 +749,7 @@ cudaError_t forward(const LinearArgs& a, float* states, cudaStream_t s) {
   static Fit fit;
   const int groups = (a.C + kChan - 1) / kChan, blocks = cluster_blocks(kernel, kSmem, a, kTile, fit);
   return launch_cluster(kernel, static_cast<int64_t>(a.B) * groups * blocks, blocks, kThreads, kSmem, false, s, a, states, blocks, groups,
-                        maps);
+                        option_test_stall_tile(), maps);
 }
 
 template <typename E, bool kPair, bool kTma, int kL, int kEvery>
@@ -719,7 +772,7 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t s) {
   static Fit fit;
   const int groups = (a.C + kChan - 1) / kChan, blocks = cluster_blocks(kernel, kSmem, a, kTile, fit);
   e = launch_cluster(kernel, static_cast<int64_t>(a.B) * groups * blocks, blocks, kThreads, kSmem, true, s, a, states, part, blocks, groups,
-                     maps);
+                     option_test_stall_tile(), maps);
   if (e != cudaSuccess) return e;
   return launch_sum_parts(part, a.dalpha, a.dbeta, true, a.B * blocks, a.C, s);
 }
