@@ -550,6 +550,8 @@ int m2rnn_linear_step(float* H, const void* x, int64_t x_stride, const void* a, 
  *   eps >= 0.
  * The workspace (m2rnn_orthogonalize_workspace_size bytes, 0 for an unsupported
  * shape) begins with a status block (see m2rnn_sync_status) that the call clears.
+ * If a device-side wait gave up (an internal failure, reported there), what it
+ * spoilt is NaN: the whole of `out`, or the tiles it kept from the last product.
  */
 size_t m2rnn_orthogonalize_workspace_size(int64_t n, int64_t rows, int64_t cols);
 int m2rnn_orthogonalize(const void* g, void* out, int64_t n, int64_t rows, int64_t cols, int steps, float eps,
@@ -630,7 +632,8 @@ int m2rnn_path(int64_t K, int64_t V, m2rnn_dtype dtype);
  *     run on one CTA (K = 16), so that the consumers' bounded waits expire
  *     and the status block reports M2RNN_ERR_TIMEOUT; -1 (the default) is off.
  *     In the gated linear recurrence the first block withholds its tile of
- *     round n.
+ *     round n; in the orthogonalised update the first block of its product n
+ *     (three a step) withholds its first stage.
  * Initial values come from the environment variables M2RNN_KERNEL (auto |
  * tcgen05 | mma | simt) and M2RNN_TEST_STALL_TILE, read once, at the first
  * call that needs them; later changes of the environment have no effect.

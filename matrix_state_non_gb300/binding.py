@@ -1157,7 +1157,9 @@ def orthogonalize(g, *, steps: int = 5, eps: float = 1e-7, out=None, workspace=N
     m2rnn_orthogonalize): ``g`` [...,rows,cols] bf16 or fp32, contiguous (a
     gradient or its momentum).  Returns bf16 [...,rows,cols], ``out`` if given
     (which may be a bf16 ``g``).  ``workspace``: scratch to use if it is large
-    enough; calls that overlap need one each."""
+    enough; calls that overlap need one each.  It holds the call's status
+    (``sync_status``); without it a device-side wait that gave up shows as NaN
+    in the result."""
     import torch
     gpu, shape = _gpu(g), g.shape
     code = _dtype_code(g)

@@ -37,6 +37,7 @@
 #include <cstdint>
 
 #include "around.cuh"
+#include "internal.h"
 #include "ssm_tc.cuh"
 
 namespace m2rnn {
@@ -253,6 +254,7 @@ struct ProductArgs {
   bool tall;
   bool direct;  // last: rows that TMA cannot store (not on 16 bytes)
   int in_low, out_low;  // kUpdate: the lower parts of X and X', kNone, kBytes or kHalf
+  int skip;  // test hook: stages of the first block that never fill, 0 or 1
 };
 
 // By TMA: the operands; `in`: kPoly: A; kUpdate: X, its lower part in_low; `out`: A, P or X' (out_low), or the result.
@@ -514,6 +516,18 @@ __device__ __forceinline__ void emit(const Operands& O, const ProductArgs& A, co
   }
 }
 
+// A wait that gives up leaves its block's tiles as they were.  The last step's blocks make that visible where nobody
+// looks at the status: NaN in their tiles, if a wait of theirs (abort) or of any launch before theirs gave up.
+template <int kMode>
+__device__ __forceinline__ bool failed(const ProductArgs& A, int abort) {
+  return kMode == kUpdate && A.last != nullptr && (abort != 0 || *const_cast<const volatile unsigned int*>(&A.status->code) != 0u);
+}
+__device__ __forceinline__ void spoil(const ProductArgs& A, int mat, int r, int c0, int width) {
+  const int64_t right = A.tall ? A.m : 1, down = A.tall ? 1 : A.k;
+  uint16_t* to = A.last + (static_cast<int64_t>(mat) * A.m * A.k + r * down);
+  for (int c = c0; r < A.m && c < min(c0 + width, A.k); ++c) to[c * right] = 0x7fc0;
+}
+
 template <int kMode, int kN, bool kLow, bool kPair>
 __global__ void __launch_bounds__(kProductThreads, 1)
     ortho_product_kernel(const __grid_constant__ Operands O, ProductArgs A) {
@@ -562,12 +576,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     // ---------------- loads ----------------
     if (lane == 0) {
       asm volatile("fence.proxy.async;" ::: "memory");  // what earlier launches stored, before TMA reads it
-      int u = 0;  // stages filled
+      int d0 = first == 0 ? A.skip : 0, u = d0;  // stages filled
       bool ok = true;
       for (int id = first; ok && id < A.items; id += step) {
         const Item t = item_at<kMode, kN, S::kTileRows>(A, id);
         const int mat = t.mat;
-        for (int d = 0; d < depth; ++d, ++u) {
+        for (int d = d0; d < depth; ++d, ++u) {
           const int s = u % S::kStages;
           if (u >= S::kStages && !mbar_wait(empty(s), (u / S::kStages - 1) & 1, abort_flag, A.status, kWhereOrthoEmpty)) {
             ok = false;
@@ -589,6 +603,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
               tma_load_3d<kPair>(to + S::kLeft + r * kDepth * 2, &O.left, bar, d * kDepth, n0 + r, mat);
           }
         }
+        d0 = 0;
       }
       if (!ok && rank == 0)  // the copies in flight land before the block ends (a pair's: before it has met)
         for (int x = max(0, u - S::kStages); x < u; ++x)
@@ -717,6 +732,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   else
     __syncthreads();
   if (warp == 1) release_tmem<kPair>(tmem);
+  if (warp >= kFirstEpilogue && failed<kMode>(A, *abort_flag)) {
+    const int quarter = warp & 3, half = (warp - kFirstEpilogue) >> 2;
+    for (int id = first; id < A.items; id += step) {
+      const Item t = item_at<kMode, kN, S::kTileRows>(A, id);
+      spoil(A, t.mat, t.i * S::kTileRows + rank * kRows + quarter * 32 + lane, t.j * kN + half * (kN / 2), kN / 2);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -791,7 +813,7 @@ __global__ void __launch_bounds__(kProductThreads, 1) ortho_narrow_kernel(const 
     if (lane == 0) {
       asm volatile("fence.proxy.async;" ::: "memory");
       bool ok = true;
-      int u = 0;
+      int u = blockIdx.x == 0 ? A.skip : 0;
       for (; u < depth; ++u) {
         const int s = u % S::kStages;
         if (u >= S::kStages && !mbar_wait(empty(s), (u / S::kStages - 1) & 1, abort_flag, A.status, kWhereOrthoEmpty)) {
@@ -857,7 +879,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) ortho_narrow_kernel(const 
           if (low != kNone) tma_load_3d<false>(to + kBlockBytes, &O.in_low, there(me), t.j * kN + column(x), r0, mat);
         }
       }
-      warp_wait(there(me), 0, abort_flag, A.status, kWhereOrthoIn);
+      if (!warp_wait(there(me), 0, abort_flag, A.status, kWhereOrthoIn) && lane == 0)
+        mbar_wait_timed(there(me), 0, nullptr, kWhereOrthoDrain);  // what is on its way lands
     }
     tc_fence_after_sync();
     const float f = A.rest != nullptr ? A.rest[mat] : 1.f;
@@ -880,6 +903,8 @@ __global__ void __launch_bounds__(kProductThreads, 1) ortho_narrow_kernel(const 
   __syncwarp();
   __syncthreads();
   if (warp == 1) tmem_dealloc(tmem, kN);
+  if (warp >= kFirstEpilogue && failed<kMode>(A, *abort_flag))
+    for (int x = 0; x < blocks; ++x) spoil(A, mat, r0 + lane, t.j * kN + column(x), 32);
 }
 
 // A stack of matrices [n][rows][pitch] as TMA sees it: boxes of `depth` rows of 64 columns for the products' operands
@@ -1074,6 +1099,7 @@ cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
     if (left < 1) return kNone;
     return m < kOnePart || left > 4 ? kHalf : left > 1 ? kBytes : kNone;
   };
+  const int stall = option_test_stall_tile();
   for (int i = 0; i < A.steps && e == cudaSuccess; ++i) {
     const int at = i & 1;
     const bool last = i == A.steps - 1;
@@ -1081,9 +1107,11 @@ cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
     a.rest = i == 0 && A.bf16 ? w.rest : nullptr;
     a.in_low = low_part(i);
     a.out_low = low_part(i + 1);
+    a.skip = stall == 3 * i;
     e = run_product<kGram>(to_gram[at], a, A.n, pair, s);
     if (e != cudaSuccess) break;
     a.inner = m;
+    a.skip = stall == 3 * i + 1;
     e = run_product<kPoly>(to_poly, a, A.n, pair, s);
     if (e != cudaSuccess) break;
     a.last = last ? A.out : nullptr;
@@ -1091,6 +1119,7 @@ cudaError_t launch_orthogonalize(const OrthoArgs& A, cudaStream_t s) {
     x.in_low = a.in_low == kBytes ? bytes[at] : halves[at];
     x.out_low = a.out_low == kBytes ? bytes[at ^ 1] : halves[at ^ 1];
     if (last && !a.direct) x.out = result;
+    a.skip = stall == 3 * i + 2;
     e = run_product<kUpdate>(x, a, A.n, pair, s);
   }
   return e;

@@ -75,3 +75,26 @@ def test_backward_that_misses_a_tile(dtype, tile):
     again = call()
     for k in names:
         assert same(again[k], want[k]), k
+
+
+@pytest.mark.parametrize("n,rows,cols,product", [(1, 300, 200, 0), (1, 300, 200, 14), (60, 512, 520, 4), (60, 512, 520, 14),
+                                                 (20, 800, 800, 0), (20, 800, 800, 14), (1, 65, 1001, 14)])
+def test_update_that_misses_operands(n, rows, cols, product):
+    """Narrow tiles, persistent blocks, pairs of SMs, rows that TMA does not store: a product of the first, second and last
+    step misses its first operands."""
+    from matrix_state_non_gb300 import binding as m
+    g = torch.randn((n, rows, cols), generator=torch.Generator(device="cuda").manual_seed(rows), device="cuda")
+    want = m.orthogonalize(g)
+    ws = torch.empty(m.m2rnn_orthogonalize_workspace_size(n, rows, cols), dtype=torch.uint8, device="cuda")
+    out = torch.zeros_like(want)
+    with m.stall_tile_hook(product):
+        m.orthogonalize(g, out=out, workspace=ws)
+        status, where = m.sync_status(ws)
+    assert status == m.M2RNN_ERR_TIMEOUT and where // 10 == 42, (status, where)
+    if product < 14:
+        assert bool(out.isnan().all())
+    else:  # what the block that missed them had to make is NaN, the rest is right
+        spoilt = out.isnan()
+        assert bool(spoilt[0].any()) and not bool(spoilt.all())
+        assert torch.equal(out[~spoilt], want[~spoilt])
+    assert same(m.orthogonalize(g, out=out, workspace=ws), want) and m.sync_status(ws)[0] == m.M2RNN_OK
