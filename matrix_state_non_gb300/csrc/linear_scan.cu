@@ -30,13 +30,14 @@
 #include <cstdint>
 
 #include "around.cuh"
+#include "cluster_fit.h"
 #include "internal.h"
 #include "mma_common.cuh"
 
 namespace m2rnn {
 namespace {
 
-constexpr int kWarps = 8, kThreads = 32 * kWarps, kChan = 64, kMaxCluster = 8;
+constexpr int kWarps = 8, kThreads = 32 * kWarps, kChan = 64;
 static_assert(kWarps >= kMaxCluster, "a warp hands the block's total to each block of the cluster");
 
 // ---------------------------------------------------------------------------
@@ -657,32 +658,27 @@ __global__ void __launch_bounds__(kSumThreads) sum_parts_kernel(const float* par
 
 constexpr int kEveryBf16 = 8, kEveryF32 = 4;  // steps of a segment of the backward
 
-// Clusters of 2 to 8 blocks that the GPU runs at once, as it answered before, or 0.
-struct Fit {
-  std::atomic<int> of[kMaxCluster + 1];
-  template <typename... P>
-  int get(void (*kernel)(P...), int smem, int r) {
-    int n = of[r].load();
-    if (n == 0) {
-      cudaLaunchAttribute at{};
-      at.id = cudaLaunchAttributeClusterDimension;
-      at.val.clusterDim.x = r;
-      at.val.clusterDim.y = at.val.clusterDim.z = 1;
-      cudaLaunchConfig_t c{};
-      c.gridDim = dim3(r);
-      c.blockDim = dim3(kThreads);
-      c.dynamicSmemBytes = smem;
-      c.attrs = &at;
-      c.numAttrs = 1;
-      if (cudaOccupancyMaxActiveClusters(&n, kernel, &c) != cudaSuccess || n < 1) {
-        (void)cudaGetLastError();
-        n = 304 / r;
-      }
-      of[r].store(n);
-    }
-    return n;
-  }
-};
+// Clusters of `size` blocks of the kernel that the current device, `device`, runs at
+// once (if it does not say: as many as two blocks to an SM would be).
+template <typename... P>
+int clusters_at_once(void (*kernel)(P...), int smem, int device, int size, ClusterFit& fit) {
+  return fit.get(device, size, 304 / size, [&] {
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = size;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(size);
+    c.blockDim = dim3(kThreads);
+    c.dynamicSmemBytes = smem;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &c) == cudaSuccess) return n;
+    (void)cudaGetLastError();
+    return 0;
+  });
+}
 
 // Blocks to a cluster, each with a tile at least: the shortest of the waves of all
 // clusters (152, 97, 74, 58, 46, 38, 36 of 2 to 8 blocks run at once, two blocks to
@@ -693,14 +689,15 @@ struct Fit {
 // more than 152 clusters the waves overlap: 2 where that is shorter (200: 79.6 us,
 // 90.9 with 1; 230: 96.8 and 91.3; more than 2 lose a third at T=512).
 template <typename... P>
-int cluster_blocks(void (*kernel)(P...), int smem, const LinearArgs& a, int tile, Fit& fit) {
+int cluster_blocks(void (*kernel)(P...), int smem, const LinearArgs& a, int tile, ClusterFit& fit) {
   const int64_t chains = static_cast<int64_t>(a.B) * ((a.C + kChan - 1) / kChan);
   const int tiles = (a.T + tile - 1) / tile;
   if (chains > 152) return chains <= 216 && tiles > 1 ? 2 : 1;
-  int best = 1;
+  int best = 1, device = -1;
+  if (tiles > 1 && cudaGetDevice(&device) != cudaSuccess) (void)cudaGetLastError();
   float least = 1.06f;
   for (int r = 2; r <= kMaxCluster && r <= tiles; ++r) {
-    const int at_once = fit.get(kernel, smem, r), left = static_cast<int>(chains) % at_once;
+    const int at_once = clusters_at_once(kernel, smem, device, r, fit), left = static_cast<int>(chains) % at_once;
     const bool half = 2 * left <= at_once && chains > at_once;
     const float waves = static_cast<float>(chains / at_once) + (left == 0 ? 0.f : half ? 0.64f : 1.f);
     const float time = waves * (1.f / static_cast<float>(r) + 0.06f);
@@ -746,7 +743,7 @@ cudaError_t forward(const LinearArgs& a, float* states, cudaStream_t s) {
     if (!map_rows(&maps.m[0], a, a.a, a.a_stride, kTile) || !map_rows(&maps.m[1], a, a.x, a.x_stride, kTile))
       return cudaErrorInvalidValue;
   }
-  static Fit fit;
+  static ClusterFit fit;
   const int groups = (a.C + kChan - 1) / kChan, blocks = cluster_blocks(kernel, kSmem, a, kTile, fit);
   return launch_cluster(kernel, static_cast<int64_t>(a.B) * groups * blocks, blocks, kThreads, kSmem, false, s, a, states, blocks, groups,
                         option_test_stall_tile(), maps);
@@ -769,7 +766,7 @@ cudaError_t backward(const LinearArgs& a, cudaStream_t s) {
         !map_rows(&maps.m[2], a, a.dy, a.C, kTile))
       return cudaErrorInvalidValue;
   }
-  static Fit fit;
+  static ClusterFit fit;
   const int groups = (a.C + kChan - 1) / kChan, blocks = cluster_blocks(kernel, kSmem, a, kTile, fit);
   e = launch_cluster(kernel, static_cast<int64_t>(a.B) * groups * blocks, blocks, kThreads, kSmem, true, s, a, states, part, blocks, groups,
                      option_test_stall_tile(), maps);
