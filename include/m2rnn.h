@@ -540,7 +540,8 @@ int m2rnn_linear_step(float* H, const void* x, int64_t x_stride, const void* a, 
  *     `steps` times:  A = X X^T,  X <- a X + (b A + c A A) X,
  *     a = 3.4445, b = -4.7750, c = 2.0315.
  * The result is within 5e-3 (Frobenius norm) of the formula's at up to six
- * steps.  Where G has no component X has rounding noise, 2^-22 of its norm, that
+ * steps, 1e-2 for matrices whose values are all of one size, whose rounding
+ * errors do not average.  Where G has no component X has rounding noise, 2^-22 of its norm, that
  * grows 3.4445-fold a step like small singular values: a matrix of exactly low
  * rank keeps that accuracy for 8 steps, 3e-2 (rank 1) or 6e-3 (rank 32) for 10,
  * and has a noise floor of the result's own size from 12 on, as it has in fp32.

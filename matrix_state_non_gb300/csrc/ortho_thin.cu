@@ -5,9 +5,12 @@
 //     Q = a + b A + c A A,  R <- Q R,  A <- Q A Q,   X = R X_0.
 // A is summed over blocks that share the long side, a block per matrix takes the
 // steps, and blocks along the long side apply R.  All in fp32 on CUDA cores: the
-// rounding noise of A grows 12-fold a step where A has nothing (2e4 in four steps,
-// 1e-3 of the result for matrices of low rank, 1e-6 for others), which 24 bits
-// bear for five steps and no more: after each five, X is made and A taken anew.
+// rounding noise of A grows 12-fold a step where A has nothing (2e4 in four steps),
+// which 24 bits bear for five steps and no more: after each five, X is made and A
+// taken anew.  Q stands on either side of A, as A is symmetric but for its noise: in
+// A Q Q, the same without any, noise between what A has and what it has not grows
+// 12-fold as well, not 2.4-fold, and left 1.4e-2 of a 64 x 513 matrix of ones (Q A Q:
+// 6e-4, others of low rank 3e-4).
 // 64 x 2000: 56 us, 38 of them the steps' eighteen products on one SM (90 by the
 // launches of ortho.cu); 64 x 16384: 75 (355); 200 of 64 x 1024: 192 (260).
 #include <cuda_runtime.h>
@@ -24,7 +27,7 @@ constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr int kSide = 64, kPitch = kSide + 4, kThreads = 256, kTogether = 5;  // steps between two sums
 constexpr int kSquare = kSide * kSide;
 
-// acc[i][j] += sum over kk < depth of l[kk][4 ty + i] r[kk][4 tx + j], rows of kPitch.
+// acc[i][j] += sum over kk < depth of l[kk][4 ty + i] r[kk][4 tx + j], rows of kPitch: l's transpose times r.
 __device__ __forceinline__ void multiply(float (&acc)[4][4], const float* l, const float* r, int depth, int tx, int ty) {
 #pragma unroll 8
   for (int kk = 0; kk < depth; ++kk) {
@@ -118,14 +121,14 @@ __global__ void __launch_bounds__(kThreads) thin_steps_kernel(const float* sums,
     __syncthreads();
     float r[4][4] = {}, w[4][4] = {};
     if (step > 0 && in) multiply(r, Q, R, m, tx, ty);
-    if (step < steps - 1 && in) multiply(w, Q, A, m, tx, ty);
+    if (step < steps - 1 && in) multiply(w, A, Q, m, tx, ty);
     __syncthreads();
     if (step > 0) put(R, r, tx, ty);
     put(T, w, tx, ty);
     __syncthreads();
     if (step < steps - 1) {
       float x[4][4] = {};
-      if (in) multiply(x, T, Q, m, tx, ty);
+      if (in) multiply(x, Q, T, m, tx, ty);
       put(A, x, tx, ty);  // (nobody reads A here)
     }
     __syncthreads();
