@@ -465,8 +465,9 @@ int m2rnn_grad_clip(const void* plan, size_t plan_bytes, float max_norm, float* 
  *   scale for each 128 values of a row, scale [rows,ceil(D/128)] fp32 (NULL
  *   for the other types): scale = max(max |y| / 448, 2^-126), and what is
  *   stored is y / scale, to the nearest; y = stored * scale.
- * Outputs must not overlap inputs but for h = residual.  Rows with |h| above
- * 1e18, or with eps = 0 below 1e-18, leave the range of the fp32 sum of squares.
+ * Outputs must not overlap inputs but for h = residual.  The sum of a row's
+ * squares is taken in fp32: rows of a norm above 1.8e19, or with eps = 0 of
+ * values below 1e-18, leave its range.
  */
 int m2rnn_residual_norm(const void* x, int64_t x_stride, const void* residual, const float* w, float eps, void* h, void* y,
                         float* scale, int64_t rows, int64_t D, m2rnn_dtype x_dtype, m2rnn_dtype h_dtype,

@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(Team<kTeam>::kThreads, backward_per_sm(kTeam, 
         rr = fmaf(v, me.get(g, i, e) * w[i][e], rr);
       }
     const float2 t = sum_team<kTeam>(ss, rr, team, turn);
-    const float s = rsqrtf(t.x * inv + A.eps), c = t.y * s * s * s * inv;
+    const float s = rsqrtf(t.x * inv + A.eps);
+    const float c = t.y * s * (s * inv) * s;  // (in this order nothing overflows for small rows)
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       float d[8];
