@@ -544,8 +544,8 @@ int m2rnn_linear_step(float* H, const void* x, int64_t x_stride, const void* a, 
  * steps, 1e-2 for matrices whose values are all of one size, whose rounding
  * errors do not average.  Where G has no component X has rounding noise, 2^-22 of its norm, that
  * grows 3.4445-fold a step like small singular values: a matrix of exactly low
- * rank keeps that accuracy for 8 steps, 3e-2 (rank 1) or 6e-3 (rank 32) for 10,
- * and has a noise floor of the result's own size from 12 on, as it has in fp32.
+ * rank keeps that accuracy for 8 steps, and is up to 4e-2 (rank 1) or 1.3e-2
+ * (rank 32) off after 10, as much as half its size after 12, as it is in fp32.
  *   g [n,rows,cols] in `dtype`; out [n,rows,cols] bf16 (may be g, where that
  *   is bf16);  rows, cols in [1, 16384], n <= 65535 (2^38 values in all),
  *   1 <= steps <= 32,

@@ -22,9 +22,10 @@
 // its segments are left by the forward's kernel, without y, in one launch
 // before it.
 //
-// Bound by instructions, most of them the gate's multiply-adds, and by the
-// exchange's latency (0.9 us a round, partly behind the other block of an SM).  B=2
-// T=16384 C=1024 bf16: 57 us, 3.5 TB/s; backward B=4 T=4096: 27 + 52 us.
+// Bound by no unit but by latency and load: 13 warps to an SM, of whose issue slots
+// 54 % are used (the busier multiply-add pipe 45 %, DRAM 35 %), 256 blocks on 152
+// SMs, and in each round an exchange of 0.9 us, partly behind the other block of an
+// SM.  B=2 T=16384 C=1024 bf16: 58 us, 3.5 TB/s; backward B=4 T=4096: 27 + 53 us.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -204,9 +205,9 @@ struct Gate2 {
 // Without that, only alpha = 0 would meet it: there shut() takes y to -infinity,
 // where f is 1, too.  (The bound took the forward from 57.8 to 59.3 us; 1 - e for
 // 1 - w P in pairs, 58.0 to 62.4.)
-// Multiply-adds bound the kernels.  Two channels to an instruction take two
+// Multiply-adds are most of the instructions.  Two channels to an instruction take two
 // cycles of one of the two pipes, so some (here and in the scan itself) are left
-// single for the other: B=2 T=16384 C=1024 bf16 takes 56.7 us so, 62 with all in
+// single for the other: B=2 T=16384 C=1024 bf16 takes 57 us so, 62 with all in
 // pairs, 65 with none.  log2(1 + t) by a polynomial in t, one reciprocal less and
 // three multiply-adds more, is 7 % slower.
 __device__ __forceinline__ float2 shut(float2 beta, float2 alpha) {

@@ -26,7 +26,7 @@
 // (another 9e-4 for rank 1): noise grows 3.44-fold a step where X has nothing, and
 // with bytes before that seven steps left 1.8e-2 of a matrix of rank 1, eight 4e-2.
 //
-// 24 of 1024 x 4096 bf16, 5 steps: 1.57 ms, of which A 5 x 88 us (1.5 PFLOP/s, 3.2
+// 24 of 1024 x 4096 bf16, 5 steps: 1.51 to 1.60 ms (seven: 2.27), fp32 1.66; of 1.57, A 5 x 88 us (1.5 PFLOP/s, 3.2
 // waves of tiles), P 5 x 34, X' 146 to 166 (15 TB/s between L2 and the SMs, 3.6 of
 // HBM), the norm and the first X 100.  With two fp16 parts in all steps X' was 185,
 // bound by HBM, and the whole 1.71 ms; with two but in the first and last 1.61.
@@ -745,8 +745,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 // The same products where there are few tiles: a narrow tile (kN columns) to a
 // block, so that there are enough of them, and nothing that a block does twice.
 // The time is that of a launch behind another (2 us) and of a tile's operands on
-// their way to one SM.  1024 x 1024, one matrix, 5 steps: 116 us; 2 of 1000 x 333:
-// 99 us (163 and 140 by persistent blocks with tiles of 128 x 128; 131 and 113 with
+// their way to one SM.  1024 x 1024, one matrix, 5 steps: 117 us; 2 of 1000 x 333:
+// 100 us (163 and 140 by persistent blocks with tiles of 128 x 128; 131 and 113 with
 // clusters of four that share a tile's inner dimension; 142 and 120 in one
 // cooperative launch with barriers across the grid).
 // ---------------------------------------------------------------------------
